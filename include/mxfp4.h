@@ -71,7 +71,9 @@ typedef enum {
     MXFP4_ERR_WORKSPACE = 4,          /* workspace missing or smaller than required */
     MXFP4_ERR_CUDA = 5,               /* a CUDA runtime call or launch failed       */
     MXFP4_ERR_TIMEOUT = 6,            /* a device-side wait gave up                 */
-    MXFP4_ERR_NO_DEVICE = 7           /* no usable sm_103 device is current         */
+    MXFP4_ERR_NO_DEVICE = 7,          /* no usable sm_103 device is current         */
+    MXFP4_ERR_INDEX = 8               /* a page, slot or position read on the device
+                                         was out of range (mxfp4_get_device_error)  */
 } mxfp4_status;
 
 typedef enum {
@@ -341,10 +343,142 @@ MXFP4_API mxfp4_status mxfp4_gemm_noalloc(const void* a_bf16_dev, int lda, const
 MXFP4_API size_t mxfp4_gemm_noalloc_max_scratch_bytes(void);
 
 /*
+ * Latent attention (MLA) over a paged latent cache: what lies between the
+ * absorbed K-up and V-up products of a16wfp4_bmm (PR #34317, Modifications),
+ * and what fills the cache they read.  The pages name these layers only; the
+ * operators follow the published definition of multi-head latent attention.
+ *
+ * The CACHE holds one row per position for all heads: the normalized latent
+ * (L bf16 values), then the rotated key (R values).  Rows of a page are
+ * contiguous; page i starts i * page_stride elements from cache_dev.  L is a
+ * multiple of 128, at most 512; R is 64; page_size is a multiple of 8;
+ * page_stride >= page_size * (L + R).
+ *
+ * Strides are in elements.  Every bf16 tensor's innermost dimension is
+ * contiguous; its data pointer and page strides are 16-byte aligned, so its
+ * strides are multiples of 8 (MISALIGNED otherwise); a stride of a dimension
+ * of more than one entry is positive (UNSUPPORTED_SHAPE otherwise).
+ *
+ * Indexes that live on the device (pages, slots, positions, lengths) cannot
+ * be checked before the launch.  The kernels check them: nothing is read or
+ * written out of range, the rows concerned are unspecified or left as they
+ * were, and mxfp4_get_device_error() reports MXFP4_ERR_INDEX.
+ *
+ * Softmax statistics and sums are fp32; the softmax weights are rounded to
+ * bf16 for the second product, and each output once to bf16.  Cache rows past
+ * a sequence's length are never used (they may hold anything, NaN included).
+ * Keys that are inside the sequence but hidden from a query by causality only
+ * must be finite, as for a product with a zero weight.
+ */
+
+/*
+ * What enters the cache, in one pass over T new tokens: the latent's RMSNorm,
+ * the rotation of the shared key, the write of both into the paged cache, and
+ * the rotation of each head's query:
+ *   cache[slot] = [ bf16_RNE(lat / sqrt(mean(lat^2) + eps) * gamma)
+ *                   | bf16_RNE(rot(kv[t][L .. L + R))) ]
+ *   q_out[t][h] = bf16_RNE(rot(q[t][h]))
+ * rot turns R / 2 pairs (x_a, x_b) -> (x_a cos - x_b sin, x_b cos + x_a sin)
+ * by the angles of the token's position; pair i is elements (2i, 2i + 1) when
+ * interleaved != 0 and (i, i + R / 2) otherwise.  fp32 throughout.
+ *
+ *   kv_dev         bf16 [T][ld_kv]: latent L, then key R (ld_kv >= L + R)
+ *   gamma_dev      bf16 [L]
+ *   q_dev          bf16 [T][H][R] (strides q_tok, q_head), or NULL with H = 0
+ *   q_out_dev      bf16 [T][H][R] (strides qo_tok, qo_head); may be q_dev
+ *                  itself with the same strides
+ *   cos_sin_dev    fp32 [max_pos][R]: R / 2 cosines, then R / 2 sines
+ *   positions_dev  int64 [T], in [0, max_pos); a token whose position is not
+ *                  is skipped (index error)
+ *   slots_dev      int64 [T]: page * page_size + row, or negative for a
+ *                  padding token, which leaves the cache alone.  No two
+ *                  tokens may share a slot.
+ * Rows whose mean square leaves the fp32 range are outside the supported
+ * range.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA.
+ */
+MXFP4_API mxfp4_status mxfp4_mla_store(const void* kv_dev, int64_t ld_kv, const void* gamma_dev, float eps,
+                                       const void* q_dev, int64_t q_tok, int64_t q_head,
+                                       void* q_out_dev, int64_t qo_tok, int64_t qo_head, int H,
+                                       const float* cos_sin_dev, int max_pos, const int64_t* positions_dev,
+                                       const int64_t* slots_dev, void* cache_dev, int64_t page_stride,
+                                       int page_size, int num_pages, int T, int L, int R, int interleaved,
+                                       void* stream);
+
+/* Workspace bytes mxfp4_mla_decode needs: the parts of sequences that are cut
+ * between thread blocks.  max_len = max_pages * page_size.  0 where no
+ * sequence can be cut (max_len <= 128) or an argument is not positive. */
+MXFP4_API size_t mxfp4_mla_decode_workspace_bytes(int S, int q_len, int H, int L, int64_t max_len);
+
+/*
+ * Absorbed latent attention of the q_len newest tokens of S sequences, whose
+ * cache rows have been stored.  For row (sequence s, token i, head h), with
+ * c_j the cache row of position j of sequence s:
+ *   x_j   = scale * (q_lat . c_j[0..L) + q_rope . c_j[L..L+R)),
+ *           j < seq_lens[s] - q_len + 1 + i
+ *   out   = bf16_RNE( sum_j softmax(x)_j c_j[0..L) ),  lse = log sum_j exp(x_j)
+ * A row that sees no position (length 0, or a length below q_len) gives zeros
+ * and lse -inf.
+ *
+ *   q_lat_dev, q_rope_dev  bf16 [S * q_len][H][L] and [..][R] by their strides:
+ *                          the K-up product [H][T][L] as it stands, and
+ *                          mxfp4_mla_store's q_out
+ *   page_table_dev  int32 [S][table_stride >= max_pages]; only the entries of
+ *                   positions below the length are read
+ *   seq_lens_dev    int32 [S], the q_len new tokens included; taken as 0 below
+ *                   0 and as max_pages * page_size above it
+ *   out_dev         bf16 [S * q_len][H][L] by its strides (head-major is the
+ *                   V-up product's input)
+ *   lse_dev         fp32 [S * q_len][H] contiguous, or NULL
+ *   workspace_dev   mxfp4_mla_decode_workspace_bytes() bytes, 16-byte aligned,
+ *                   clobbered; calls sharing one must be ordered on the GPU
+ * Deterministic: the same call gives the same bits.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE, CUDA.
+ */
+MXFP4_API mxfp4_status mxfp4_mla_decode(const void* q_lat_dev, int64_t ql_tok, int64_t ql_head,
+                                        const void* q_rope_dev, int64_t qr_tok, int64_t qr_head,
+                                        const void* cache_dev, int64_t page_stride, int page_size, int num_pages,
+                                        const int32_t* page_table_dev, int64_t table_stride, int max_pages,
+                                        const int32_t* seq_lens_dev, void* out_dev, int64_t o_tok, int64_t o_head,
+                                        float* lse_dev, int S, int q_len, int H, int L, int R, float scale,
+                                        void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/*
+ * Expanded latent attention of S ragged prompts or chunks: sequence s has
+ * queries cu_q[s] .. cu_q[s + 1) and keys cu_k[s] .. cu_k[s + 1).  Per head,
+ *   x_ij = scale * (q_nope_i . k_nope_j + q_rope_i . k_rope_j)
+ *   out_i = bf16_RNE( sum_j softmax(x_i)_j v_j ),  lse_i = log sum_j exp(x_ij)
+ * with the rotated key k_rope shared by all heads.  causal != 0: query i of
+ * q_n sees keys j <= i + k_n - q_n (the newest query sees every key).  A query
+ * that sees no key gives zeros and lse -inf.
+ *
+ *   q_nope_dev, q_rope_dev  bf16 [Tq][H][dn], [Tq][H][R] by their strides
+ *                           (views of one query projection, or mxfp4_mla_store's q_out)
+ *   k_nope_dev, v_dev       bf16 [Tk][H][dn], [Tk][H][dv] by their strides
+ *                           (views of one expanding projection [Tk][H][dn + dv])
+ *   k_rope_dev              bf16 [Tk][R], row stride kr_tok
+ *   cu_q_dev, cu_k_dev      int32 [S + 1], ascending from 0 to Tq and Tk
+ *   out_dev                 bf16 [Tq][H][dv] by its strides
+ *   lse_dev                 fp32 [Tq][H] contiguous, or NULL
+ * dn and dv are multiples of 8, dn at most 192, dv at most 256; R is 64; H at
+ * most 65535.  Deterministic.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
+ * MISALIGNED, CUDA.
+ */
+MXFP4_API mxfp4_status mxfp4_mla_prefill(const void* q_nope_dev, int64_t qn_tok, int64_t qn_head,
+                                         const void* q_rope_dev, int64_t qr_tok, int64_t qr_head,
+                                         const void* k_nope_dev, int64_t kn_tok, int64_t kn_head,
+                                         const void* k_rope_dev, int64_t kr_tok,
+                                         const void* v_dev, int64_t v_tok, int64_t v_head,
+                                         const int32_t* cu_q_dev, const int32_t* cu_k_dev, int S,
+                                         void* out_dev, int64_t o_tok, int64_t o_head, float* lse_dev,
+                                         int Tq, int Tk, int H, int dn, int R, int dv, float scale, int causal,
+                                         void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the library's device error
  * words on the current device.  Returns MXFP4_ERR_TIMEOUT if a kernel gave
- * up a bounded wait since the last call, MXFP4_OK otherwise (or
- * MXFP4_ERR_CUDA if the synchronisation itself failed).
+ * up a bounded wait since the last call, MXFP4_ERR_INDEX if a latent-attention
+ * kernel met an index out of range, MXFP4_OK otherwise (or MXFP4_ERR_CUDA if
+ * the synchronisation itself failed).
  */
 MXFP4_API mxfp4_status mxfp4_get_device_error(void* stream);
 

@@ -21,7 +21,8 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 INCLUDE_DIR = os.path.join(os.path.dirname(PKG_DIR), "include")
 LIB_NAME = "libmxfp4_gb300.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-SOURCES = ("quant.cu", "norm_quant.cu", "gemm.cu", "decode.cu", "bmm.cu", "capi.cu", "noalloc.cu", "tc_rate.cu")
+SOURCES = ("quant.cu", "norm_quant.cu", "gemm.cu", "decode.cu", "bmm.cu", "capi.cu", "noalloc.cu", "tc_rate.cu",
+           "mla_store.cu", "mla_decode.cu", "mla_prefill.cu")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -26,11 +26,11 @@ lib = ctypes.CDLL(_LIB_PATH)
 
 # status codes (mxfp4_status)
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED_SHAPE, ERR_MISALIGNED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, \
-    ERR_NO_DEVICE = range(8)
+    ERR_NO_DEVICE, ERR_INDEX = range(9)
 LAYOUT_ROWMAJOR, LAYOUT_TILED = 0, 1
 OUT_BMN, OUT_MBN = 0, 1
 
-_p, _i, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_p, _i, _sz, _l, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64, ctypes.c_float
 
 _SIGNATURES = {
     "mxfp4_abi_version": (_i, []),
@@ -47,6 +47,13 @@ _SIGNATURES = {
     "mxfp4_gemm_mxfp4_out": (_i, [_p, _i, _p, _p, _i, _p, _p, _p, _p, _i, _i, _i, _p, _sz, _p]),
     "mxfp4_gemm_split_cat": (_i, [_p, _i, _p, _p, _i, _p, _p, _i, _i, _i, _i, _i, _p, _i, _p, _p, _p, _sz, _p]),
     "a16wfp4_bmm": (_i, [_p, _p, _p, _i, _i, _i, _i, _i, _p]),
+    "mxfp4_mla_store": (_i, [_p, _l, _p, _f, _p, _l, _l, _p, _l, _l, _i, _p, _i, _p, _p, _p, _l, _i, _i, _i, _i, _i,
+                             _i, _p]),
+    "mxfp4_mla_decode_workspace_bytes": (_sz, [_i, _i, _i, _i, _l]),
+    "mxfp4_mla_decode": (_i, [_p, _l, _l, _p, _l, _l, _p, _l, _i, _i, _p, _l, _i, _p, _p, _l, _l, _p, _i, _i, _i, _i,
+                              _i, _f, _p, _sz, _p]),
+    "mxfp4_mla_prefill": (_i, [_p, _l, _l, _p, _l, _l, _p, _l, _l, _p, _l, _p, _l, _l, _p, _p, _i, _p, _l, _l, _p, _i,
+                               _i, _i, _i, _i, _i, _f, _i, _p]),
     "mxfp4_get_device_error": (_i, [_p]),
     "mxfp4_gemm_noalloc": (_i, [_p, _i, _p, _p, _p, _i, _i, _i, _i, _p]),
     "mxfp4_gemm_noalloc_max_scratch_bytes": (_sz, []),
@@ -177,6 +184,41 @@ def mxfp4_gemm_noalloc(a_bf16, lda: int, w_packed, bias, out, ldo: int, M: int, 
 
 def mxfp4_gemm_noalloc_max_scratch_bytes() -> int:
     return lib.mxfp4_gemm_noalloc_max_scratch_bytes()
+
+
+def mxfp4_mla_store(kv, ld_kv: int, gamma, eps: float, q, q_tok: int, q_head: int, q_out, qo_tok: int, qo_head: int,
+                    H: int, cos_sin, max_pos: int, positions, slots, cache, page_stride: int, page_size: int,
+                    num_pages: int, T: int, L: int, R: int, interleaved: bool, stream=None) -> None:
+    _check(lib.mxfp4_mla_store(_ptr(kv), ld_kv, _ptr(gamma), eps, _ptr(q), q_tok, q_head, _ptr(q_out), qo_tok,
+                               qo_head, H, _ptr(cos_sin), max_pos, _ptr(positions), _ptr(slots), _ptr(cache),
+                               page_stride, page_size, num_pages, T, L, R, 1 if interleaved else 0, _stream(stream)),
+           "mxfp4_mla_store")
+
+
+def mxfp4_mla_decode_workspace_bytes(S: int, q_len: int, H: int, L: int, max_len: int) -> int:
+    return lib.mxfp4_mla_decode_workspace_bytes(S, q_len, H, L, max_len)
+
+
+def mxfp4_mla_decode(q_lat, ql_tok: int, ql_head: int, q_rope, qr_tok: int, qr_head: int, cache, page_stride: int,
+                     page_size: int, num_pages: int, page_table, table_stride: int, max_pages: int, seq_lens, out,
+                     o_tok: int, o_head: int, lse, S: int, q_len: int, H: int, L: int, R: int, scale: float,
+                     workspace, workspace_bytes: int, stream=None) -> None:
+    _check(lib.mxfp4_mla_decode(_ptr(q_lat), ql_tok, ql_head, _ptr(q_rope), qr_tok, qr_head, _ptr(cache), page_stride,
+                                page_size, num_pages, _ptr(page_table), table_stride, max_pages, _ptr(seq_lens),
+                                _ptr(out), o_tok, o_head, _ptr(lse), S, q_len, H, L, R, scale, _ptr(workspace),
+                                workspace_bytes, _stream(stream)),
+           "mxfp4_mla_decode")
+
+
+def mxfp4_mla_prefill(q_nope, qn_tok: int, qn_head: int, q_rope, qr_tok: int, qr_head: int, k_nope, kn_tok: int,
+                      kn_head: int, k_rope, kr_tok: int, v, v_tok: int, v_head: int, cu_q, cu_k, S: int, out,
+                      o_tok: int, o_head: int, lse, Tq: int, Tk: int, H: int, dn: int, R: int, dv: int, scale: float,
+                      causal: bool, stream=None) -> None:
+    _check(lib.mxfp4_mla_prefill(_ptr(q_nope), qn_tok, qn_head, _ptr(q_rope), qr_tok, qr_head, _ptr(k_nope), kn_tok,
+                                 kn_head, _ptr(k_rope), kr_tok, _ptr(v), v_tok, v_head, _ptr(cu_q), _ptr(cu_k), S,
+                                 _ptr(out), o_tok, o_head, _ptr(lse), Tq, Tk, H, dn, R, dv, scale,
+                                 1 if causal else 0, _stream(stream)),
+           "mxfp4_mla_prefill")
 
 
 def mxfp4_get_device_error(stream=None) -> int:

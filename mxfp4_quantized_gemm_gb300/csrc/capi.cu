@@ -10,6 +10,7 @@
 #include "mxfp4.h"
 #include "mxfp4_diag.h"
 #include "internal.h"
+#include "mla.h"
 #include "norm_quant.h"
 
 namespace mx {
@@ -98,6 +99,7 @@ const char* mxfp4_status_string(mxfp4_status s) {
     case MXFP4_ERR_CUDA: return "MXFP4_ERR_CUDA";
     case MXFP4_ERR_TIMEOUT: return "MXFP4_ERR_TIMEOUT";
     case MXFP4_ERR_NO_DEVICE: return "MXFP4_ERR_NO_DEVICE";
+    case MXFP4_ERR_INDEX: return "MXFP4_ERR_INDEX";
   }
   return "MXFP4_ERR_UNKNOWN";
 }
@@ -367,6 +369,134 @@ mxfp4_status a16wfp4_bmm(const void* x, const void* w_packed, void* out, int B, 
                               out_layout == MXFP4_OUT_MBN, dev, static_cast<cudaStream_t>(stream)));
 }
 
+// Checks a [tokens][heads][n] bf16 tensor of the latent-attention calls and
+// replaces the stride of a dimension of one entry, which is never used, by one
+// that is always valid.
+static mxfp4_status check_tensor(MlaTensor* t, int64_t tokens, int64_t heads, int n) {
+  if (tokens > 1 && t->tok <= 0) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  if (heads > 1 && t->head <= 0) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  const int64_t filler = (n + 7) / 8 * 8;
+  if (tokens <= 1) t->tok = filler;
+  if (heads <= 1) t->head = filler;
+  // strides in bytes stay below 2^40, the tensor maps' limit
+  if (t->tok >= (int64_t{1} << 39) || t->head >= (int64_t{1} << 39)) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  return (aligned16(t->p) && t->tok % 8 == 0 && t->head % 8 == 0) ? MXFP4_OK : MXFP4_ERR_MISALIGNED;
+}
+
+static mxfp4_status check_cache(MlaCache* c, int L) {
+  if (c->p == nullptr || c->page_size <= 0 || c->num_pages <= 0) return MXFP4_ERR_INVALID_ARG;
+  const int64_t rows = static_cast<int64_t>(c->page_size) * (L + kMlaRope);
+  if (c->page_size % 8 != 0) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  if (c->num_pages == 1) c->page_stride = rows;
+  if (c->page_stride < rows || c->page_stride >= (int64_t{1} << 39)) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  return (aligned16(c->p) && c->page_stride % 8 == 0) ? MXFP4_OK : MXFP4_ERR_MISALIGNED;
+}
+
+static bool latent_supported(int L, int R) { return L % 128 == 0 && L <= kMlaMaxLatent && R == kMlaRope; }
+
+mxfp4_status mxfp4_mla_store(const void* kv, int64_t ld_kv, const void* gamma, float eps, const void* q, int64_t q_tok,
+                             int64_t q_head, void* q_out, int64_t qo_tok, int64_t qo_head, int H,
+                             const float* cos_sin, int max_pos, const int64_t* positions, const int64_t* slots,
+                             void* cache, int64_t page_stride, int page_size, int num_pages, int T, int L, int R,
+                             int interleaved, void* stream) {
+  if (kv == nullptr || gamma == nullptr || cos_sin == nullptr || positions == nullptr || slots == nullptr)
+    return MXFP4_ERR_INVALID_ARG;
+  if (T <= 0 || L <= 0 || R <= 0 || H < 0 || max_pos <= 0 || !(eps >= 0.f)) return MXFP4_ERR_INVALID_ARG;
+  if (H > 0 && (q == nullptr || q_out == nullptr)) return MXFP4_ERR_INVALID_ARG;
+  if (!latent_supported(L, R)) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  MlaStoreProblem p{kv,  ld_kv, gamma, eps, {q, q_tok, q_head}, {q_out, qo_tok, qo_head}, H, cos_sin, max_pos, positions,
+                    slots, {cache, page_stride, page_size, num_pages}, T, L, interleaved != 0};
+  mxfp4_status st = check_cache(&p.cache, L);
+  if (st != MXFP4_OK) return st;
+  MlaTensor rows{kv, ld_kv, 0};
+  if (T > 1 && ld_kv < L + R) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  if ((st = check_tensor(&rows, T, 1, L + R)) != MXFP4_OK) return st;
+  if (H > 0) {
+    if ((st = check_tensor(&p.q, T, H, R)) != MXFP4_OK) return st;
+    if ((st = check_tensor(&p.q_out, T, H, R)) != MXFP4_OK) return st;
+  }
+  if (!aligned16(gamma) || !aligned16(cos_sin) || (reinterpret_cast<uintptr_t>(positions) & 7) ||
+      (reinterpret_cast<uintptr_t>(slots) & 7))
+    return MXFP4_ERR_MISALIGNED;
+  DeviceInfo dev;
+  if ((st = device_ready(&dev)) != MXFP4_OK) return st;
+  return from_cuda(launch_mla_store(p, dev, static_cast<cudaStream_t>(stream)));
+}
+
+// SMs of the current device (the most the kernels use if none is usable).
+static int current_sm_count() {
+  DeviceInfo dev;
+  if (current_device_info(&dev) == cudaSuccess && dev.ok) return dev.sm_count;
+  cudaGetLastError();   // clear the error of a failed device query
+  return kMaxStreamKCtas;
+}
+
+size_t mxfp4_mla_decode_workspace_bytes(int S, int q_len, int H, int L, int64_t max_len) {
+  if (S <= 0 || q_len <= 0 || H <= 0 || L <= 0 || max_len <= 0) return 0;
+  return mla_decode_workspace(S, q_len, H, L, max_len, current_sm_count());
+}
+
+mxfp4_status mxfp4_mla_decode(const void* q_lat, int64_t ql_tok, int64_t ql_head, const void* q_rope, int64_t qr_tok,
+                              int64_t qr_head, const void* cache, int64_t page_stride, int page_size, int num_pages,
+                              const int32_t* page_table, int64_t table_stride, int max_pages, const int32_t* seq_lens,
+                              void* out, int64_t o_tok, int64_t o_head, float* lse, int S, int q_len, int H, int L,
+                              int R, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  if (q_lat == nullptr || q_rope == nullptr || page_table == nullptr || seq_lens == nullptr || out == nullptr)
+    return MXFP4_ERR_INVALID_ARG;
+  if (S <= 0 || q_len <= 0 || H <= 0 || L <= 0 || R <= 0 || max_pages <= 0) return MXFP4_ERR_INVALID_ARG;
+  if (!latent_supported(L, R)) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  const int64_t T = static_cast<int64_t>(S) * q_len;
+  if (T > 0x7FFFFFFF || (S > 1 && table_stride < max_pages)) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  MlaDecodeProblem p{{q_lat, ql_tok, ql_head}, {q_rope, qr_tok, qr_head}, {out, o_tok, o_head},
+                     {const_cast<void*>(cache), page_stride, page_size, num_pages}, page_table, table_stride, max_pages,
+                     seq_lens, lse, S, q_len, H, L, scale, workspace};
+  mxfp4_status st = check_cache(&p.cache, L);
+  if (st != MXFP4_OK) return st;
+  if ((st = check_tensor(&p.q_lat, T, H, L)) != MXFP4_OK) return st;
+  if ((st = check_tensor(&p.q_rope, T, H, R)) != MXFP4_OK) return st;
+  if ((st = check_tensor(&p.out, T, H, L)) != MXFP4_OK) return st;
+  if ((reinterpret_cast<uintptr_t>(page_table) & 3) || (reinterpret_cast<uintptr_t>(seq_lens) & 3) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3))
+    return MXFP4_ERR_MISALIGNED;
+  if (!mla_decode_fits(S, q_len, H)) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  const size_t need = mla_decode_workspace(S, q_len, H, L, static_cast<int64_t>(max_pages) * page_size, current_sm_count());
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return MXFP4_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return MXFP4_ERR_MISALIGNED;
+  DeviceInfo dev;
+  if ((st = device_ready(&dev)) != MXFP4_OK) return st;
+  return from_cuda(launch_mla_decode(p, dev, static_cast<cudaStream_t>(stream)));
+}
+
+mxfp4_status mxfp4_mla_prefill(const void* q_nope, int64_t qn_tok, int64_t qn_head, const void* q_rope, int64_t qr_tok,
+                               int64_t qr_head, const void* k_nope, int64_t kn_tok, int64_t kn_head,
+                               const void* k_rope, int64_t kr_tok, const void* v, int64_t v_tok, int64_t v_head,
+                               const int32_t* cu_q, const int32_t* cu_k, int S, void* out, int64_t o_tok,
+                               int64_t o_head, float* lse, int Tq, int Tk, int H, int dn, int R, int dv, float scale,
+                               int causal, void* stream) {
+  if (q_nope == nullptr || q_rope == nullptr || k_nope == nullptr || k_rope == nullptr || v == nullptr ||
+      cu_q == nullptr || cu_k == nullptr || out == nullptr)
+    return MXFP4_ERR_INVALID_ARG;
+  if (S <= 0 || Tq <= 0 || Tk <= 0 || H <= 0 || dn <= 0 || R <= 0 || dv <= 0) return MXFP4_ERR_INVALID_ARG;
+  if (dn % 8 != 0 || dn > 192 || dv % 8 != 0 || dv > 256 || R != kMlaRope || H > 65535)
+    return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  MlaPrefillProblem p{{q_nope, qn_tok, qn_head}, {q_rope, qr_tok, qr_head}, {k_nope, kn_tok, kn_head},
+                      {k_rope, kr_tok, 0}, {v, v_tok, v_head}, {out, o_tok, o_head}, cu_q, cu_k, lse, S, Tq, Tk, H, dn,
+                      dv, scale, causal != 0};
+  mxfp4_status st = check_tensor(&p.q_nope, Tq, H, dn);
+  if (st == MXFP4_OK) st = check_tensor(&p.q_rope, Tq, H, R);
+  if (st == MXFP4_OK) st = check_tensor(&p.k_nope, Tk, H, dn);
+  if (st == MXFP4_OK) st = check_tensor(&p.k_rope, Tk, 1, R);
+  if (st == MXFP4_OK) st = check_tensor(&p.v, Tk, H, dv);
+  if (st == MXFP4_OK) st = check_tensor(&p.out, Tq, H, dv);
+  if (st != MXFP4_OK) return st;
+  if ((reinterpret_cast<uintptr_t>(cu_q) & 3) || (reinterpret_cast<uintptr_t>(cu_k) & 3) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3))
+    return MXFP4_ERR_MISALIGNED;
+  DeviceInfo dev;
+  if ((st = device_ready(&dev)) != MXFP4_OK) return st;
+  return from_cuda(launch_mla_prefill(p, dev, static_cast<cudaStream_t>(stream)));
+}
+
 mxfp4_status mxfp4_diag_set_wait_cycles(long long cycles) {
   if (cycles < 0) return MXFP4_ERR_INVALID_ARG;
   set_norm_wait_cycles(cycles);
@@ -387,8 +517,10 @@ mxfp4_status mxfp4_get_device_error(void* stream) {
   if (st != MXFP4_OK) return st;
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MXFP4_ERR_CUDA;
   const uint32_t err = quant_read_clear_error() | gemm_read_clear_error() | decode_read_clear_error() |
-                       bmm_read_clear_error() | norm_read_clear_error();
-  return (err & kErrTimeout) ? MXFP4_ERR_TIMEOUT : MXFP4_OK;
+                       bmm_read_clear_error() | norm_read_clear_error() | mla_store_read_clear_error() |
+                       mla_decode_read_clear_error() | mla_prefill_read_clear_error();
+  if (err & kErrTimeout) return MXFP4_ERR_TIMEOUT;
+  return (err & kErrIndex) ? MXFP4_ERR_INDEX : MXFP4_OK;
 }
 
 }  // extern "C"

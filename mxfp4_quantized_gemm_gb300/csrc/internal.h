@@ -30,6 +30,7 @@ inline int64_t weight_packed_bytes(int64_t R, int64_t K) {
 
 // Error bits recorded in a translation unit's device error word.
 constexpr uint32_t kErrTimeout = 1u;
+constexpr uint32_t kErrIndex = 2u;     // a page, slot or position read on the device is out of range
 
 // Largest stream-K grid the decode GEMM uses; sizes its partial-sum slots.
 constexpr int kMaxStreamKCtas = 256;

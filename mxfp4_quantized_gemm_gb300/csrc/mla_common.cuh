@@ -1,0 +1,193 @@
+// Device and launch helpers shared by the latent-attention kernels.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "mla.h"
+#include "ptx.cuh"
+
+namespace mx {
+
+// One lane of the (converged) warp, chosen by the hardware.  MMAs issued
+// under this predicate keep their descriptors in uniform registers: a group
+// of four 128 x 64 x 16 MMAs with its wait and commit issues in 180 ns, and
+// in 241 ns when the loop runs in a branch taken by lane 0 alone.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// A bounded mbarrier wait by a whole converged warp, whose lanes go on (or
+// give up) together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, bool& abort) {
+  mbar_wait(bar, parity, abort);
+  abort = __any_sync(0xFFFFFFFFu, abort);
+  return !abort;
+}
+
+// After a wait that gave up, by a whole warp that issued MMAs: a bounded wait
+// for those in flight, before their TMEM is freed.
+__device__ __forceinline__ void drain_mmas(uint64_t* bar, bool abort) {
+  if (!abort) return;
+  if (elect_one()) mma_commit(bar);
+  __syncwarp();
+  bool late = false;
+  mbar_wait(bar, 0, late);
+  __syncwarp();
+}
+
+// One box of a 3-D tensor map -> shared memory, completion counted on `bar`.
+__device__ __forceinline__ void tma_box_3d(void* smem_dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                           uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Descriptor of an operand whose M or N elements are contiguous (64 of them
+// per 128-byte row, rows along K), with the 128-byte swizzle: 8-row atoms
+// every 1024 bytes along K, the next 64 elements of M or N `block` bytes on.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t block) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(block >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
+// Instruction-descriptor bits: the operand's M (A) or N (B) elements contiguous.
+constexpr uint32_t kIdescAMn = 1u << 15, kIdescBMn = 1u << 16;
+
+// tmem_wait_ld that the loaded registers depend on, so that nothing that
+// reads them moves ahead of it.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld_of(uint32_t (&r)[N]) {
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+// N consecutive columns (a multiple of 16) of the calling warp's lanes.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 16) tmem_ld16(taddr + i, *reinterpret_cast<uint32_t(*)[16]>(&r[i]));
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 16) tmem_st16(taddr + i, *reinterpret_cast<const uint32_t(*)[16]>(&r[i]));
+}
+
+// 2^x (two units in the last place of fp32; -inf gives 0).
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// log2(x); log2(0) = -inf.
+__device__ __forceinline__ float log2_fast(float x) { return __log2f(x); }
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// A row's running maximum is raised only when a score passes it by more than
+// this many powers of two: until then exp2(s - max) stays below 2^8, which
+// neither fp32 sums nor the bf16 weights (whose relative rounding does not
+// depend on their size) lose anything to.
+constexpr float kMaxSlack = 8.0f;
+
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// Barrier over `threads` threads that also ORs their predicate.
+__device__ __forceinline__ bool named_sync_or(int id, int threads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(pred))
+      : "memory");
+  return r != 0;
+}
+
+// Zeroes 16-byte chunks of rows [row0, row1) of a 128-byte-row tile, by one
+// warp (whole rows: the swizzle permutes chunks within a row).
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int row0, int row1, int lane) {
+  for (int i = row0 * 8 + lane; i < row1 * 8; i += 32) reinterpret_cast<uint4*>(tile)[i] = make_uint4(0, 0, 0, 0);
+}
+
+// ------------------------------------------------------------------ host
+// The calling host thread's device context, made current if the runtime has
+// not bound it yet (cuTensorMapEncodeTiled is a driver call).
+inline cudaError_t mla_bind_context() {
+  static thread_local bool bound = false;
+  if (bound) return cudaSuccess;
+  const cudaError_t e = cudaFree(nullptr);
+  if (e == cudaSuccess) bound = true;
+  return e;
+}
+
+inline PFN_cuTensorMapEncodeTiled_v12000 mla_tensor_map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    return nullptr;
+  }();
+  return fn;
+}
+
+// Tensor map of a bf16 tensor [d2][d1][d0] with strides (elements) s1, s2 of
+// its outer dimensions, read in boxes b0 x b1 x b2 with the 128-byte swizzle
+// and zero fill outside.
+inline cudaError_t mla_tensor_map(CUtensorMap* map, const void* p, int64_t d0, int64_t d1, int64_t d2, int64_t s1,
+                                  int64_t s2, int b0, int b1, int b2) {
+  auto encode = mla_tensor_map_encoder();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(d2)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(b0), static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Launch as a programmatic dependent of the kernel ahead on the stream.
+template <typename... Params, typename... Args>
+cudaError_t mla_launch(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+}
+
+// Reads and clears a translation unit's device error word.
+template <typename Word>
+uint32_t read_clear_word(Word& word) {
+  uint32_t v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, word, sizeof(v)) != cudaSuccess) return 0;
+  if (v != 0) cudaMemcpyToSymbol(word, &zero, sizeof(zero));
+  return v;
+}
+
+}  // namespace mx

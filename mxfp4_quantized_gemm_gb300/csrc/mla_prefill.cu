@@ -1,0 +1,473 @@
+// mxfp4_mla_prefill: expanded latent attention of ragged prompts.  Per head
+//   s[i][j] = scale * (q_nope_i . k_nope_j + q_rope_i . k_rope_j)
+//   out_i   = sum_j softmax_j(s_i)[j] v_j
+// with k_rope shared by all heads, j < k_len, and for causal calls
+// j <= i + k_len - q_len (the newest query sees every key).
+//
+// Bound by the tensor cores: 2 (dn + R + dv) flop a (query, key, head).  A
+// block takes 128 queries of one head and walks the keys in tiles of 128 with
+// tcgen05 MMAs: S = Q K^T into one of two TMEM score tiles (128 columns each),
+// then O += P V with the weights P as the A operand straight from TMEM (bf16,
+// written over the score tile they come from), O (128 x dv <= 256 columns)
+// staying in TMEM for the whole walk.  The two halves of q and k come through
+// tensor maps of their own, so that nothing is concatenated in memory, and
+// the value tile is read in place from the expanding projection's output
+// [token][head][dn + dv] (its rows are the MMA's K: N-contiguous operand).
+//
+// Roles: warp 0 copies, in 16 KB slots of one ring (64 values of 128 keys, or
+// all values of 32 keys); warp 1 issues the score products, warp 2 the
+// output products; warps 4..7 and 8..11 hold the softmax, thread = (query,
+// half of the tile's keys).  Each query's running maximum is raised only when
+// a score passes it by 2^8, decided per 32 queries by a barrier with an OR
+// over the two warps that hold them.
+//
+// Blocks are ordered head by head and, within a head, from the last queries
+// (most keys) to the first: blocks that run together share a head's keys and
+// values in L2, and the shortest run last.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <atomic>
+
+#include "mla.h"
+#include "mla_common.cuh"
+
+namespace mx {
+
+static __device__ uint32_t g_mla_prefill_error;
+
+constexpr int kPreThreads = 384;
+constexpr int kPreTile = 128;                 // queries, and keys per tile
+constexpr int kSlotBytes = 16384;             // 128 keys x 64 values, or 32 keys x 256 values
+constexpr int kVTok = 32;                     // keys per value slot
+constexpr int kPreMaxSlots = 12;
+constexpr int kPreSmem = 227 * 1024;
+constexpr int kPreScol = 256;                 // first TMEM column of the score tiles
+
+struct PrefillArgs {
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  __nv_bfloat16* out;
+  float* lse;
+  int64_t o_tok, o_head;
+  int S, H, Tq, Tk, dn, dv;
+  int nq;               // 64-value chunks of q and k (the last is the rotated one)
+  int nv;               // 64-value blocks of v
+  int slots;
+  float c;              // scale * log2(e)
+  bool causal;
+};
+
+// Query rows and keys of sequence s, kept inside the tensors.
+struct Extent {
+  int q0, qn, k0, kn;
+};
+__device__ __forceinline__ int clamp_to(int v, int hi) { return v < 0 ? 0 : (v > hi ? hi : v); }
+__device__ __forceinline__ Extent extent(const PrefillArgs& a, int s) {
+  Extent e;
+  e.q0 = clamp_to(__ldg(a.cu_q + s), a.Tq);
+  e.qn = max(0, clamp_to(__ldg(a.cu_q + s + 1), a.Tq) - e.q0);
+  e.k0 = clamp_to(__ldg(a.cu_k + s), a.Tk);
+  e.kn = max(0, clamp_to(__ldg(a.cu_k + s + 1), a.Tk) - e.k0);
+  return e;
+}
+
+__global__ void __launch_bounds__(kPreThreads, 1)
+    mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_constant__ CUtensorMap qr_map,
+                       const __grid_constant__ CUtensorMap kn_map, const __grid_constant__ CUtensorMap kr_map,
+                       const __grid_constant__ CUtensorMap v_map, const PrefillArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qsm = smem;                                // nq chunks of 128 queries x 64 values
+  uint8_t* ring = qsm + a.nq * kSlotBytes;
+
+  __shared__ __align__(8) uint64_t full[2][kPreMaxSlots], empty[kPreMaxSlots];
+  __shared__ __align__(8) uint64_t q_full, s_full[2], p_full[2], pv_done[2], drain[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int scan[kPreThreads / 32];
+  __shared__ int at_seq, at_tile;
+  __shared__ float xch[2][kPreTile];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  bool abort = false;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.slots; ++s) {
+      mbar_init(&full[0][s], 1);
+      mbar_init(&full[1][s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&q_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 256);
+      mbar_init(&pv_done[i], 1);
+      mbar_init(&drain[i], 1);
+    }
+    at_seq = -1;
+    fence_mbar_init();
+  }
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+
+  // ---- this block's sequence and query tile: tiles in reverse order
+  {
+    const int per = (a.S + kPreThreads - 1) / kPreThreads;
+    const int s0 = threadIdx.x * per, s1 = min(a.S, s0 + per);
+    int mine = 0;
+    for (int s = s0; s < s1; ++s) mine += (extent(a, s).qn + kPreTile - 1) / kPreTile;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int base = 0, total = 0;
+    for (int w = 0; w < kPreThreads / 32; ++w) {
+      if (w < warp) base += scan[w];
+      total += scan[w];
+    }
+    const int want = total - 1 - static_cast<int>(blockIdx.x);
+    int at = base + incl - mine;
+    if (want >= at && want < at + mine) {
+      for (int s = s0; s < s1; ++s) {
+        const int n = (extent(a, s).qn + kPreTile - 1) / kPreTile;
+        if (want < at + n) {
+          at_tile = want - at;
+          at_seq = s;
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+  }
+  if (at_seq < 0) return;                             // more blocks than tiles
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const Extent ex = extent(a, at_seq);
+  const int h = blockIdx.y;
+  const int qi0 = at_tile * kPreTile;                 // first query of the tile, within its sequence
+  const int rows = min(kPreTile, ex.qn - qi0);
+  // keys visible to the tile's first and last query
+  const int see0 = a.causal ? clamp_to(qi0 + 1 + ex.kn - ex.qn, ex.kn) : ex.kn;
+  const int see1 = a.causal ? clamp_to(qi0 + rows + ex.kn - ex.qn, ex.kn) : ex.kn;
+  const int tiles = (see1 + kPreTile - 1) / kPreTile;
+
+  if (warp == 0) {
+    // ---- copies.  A ring slot has two full barriers, for keys and for values:
+    // the issuer of either product sees only its own, and a barrier whose
+    // phases it skipped could be taken for complete a turn early.
+    int slot = 0;
+    uint32_t ph = 0;
+    uint32_t fills[2] = {0, 0}, turn[2] = {0, 0};   // per slot: filled at all; parity of the next fill
+    auto take = [&]() -> bool {
+      if (!warp_wait(&empty[slot], ph ^ 1u, abort)) return false;
+      return true;
+    };
+    auto step = [&](int use) {
+      fills[use] |= 1u << slot;
+      turn[use] ^= 1u << slot;
+      if (++slot == a.slots) {
+        slot = 0;
+        ph ^= 1u;
+      }
+    };
+    if (tiles > 0) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(a.nq * kSlotBytes));
+        for (int k = 0; k + 1 < a.nq; ++k) tma_box_3d(qsm + k * kSlotBytes, &qn_map, k * 64, h, ex.q0 + qi0, &q_full);
+        tma_box_3d(qsm + (a.nq - 1) * kSlotBytes, &qr_map, 0, h, ex.q0 + qi0, &q_full);
+      }
+      __syncwarp();
+      for (int t = 0; t <= tiles && !abort; ++t) {
+        if (t < tiles) {
+          const int tok = ex.k0 + t * kPreTile;
+          for (int k = 0; k < a.nq; ++k) {
+            if (!take()) break;
+            if (elect_one()) {
+              mbar_arrive_expect_tx(&full[0][slot], kSlotBytes);
+              if (k + 1 < a.nq)
+                tma_box_3d(ring + slot * kSlotBytes, &kn_map, k * 64, h, tok, &full[0][slot]);
+              else
+                tma_box_3d(ring + slot * kSlotBytes, &kr_map, 0, 0, tok, &full[0][slot]);
+            }
+            __syncwarp();
+            step(0);
+          }
+        }
+        if (t > 0 && !abort) {
+          const int tok = (t - 1) * kPreTile;
+          const int vs = (min(kPreTile, see1 - tok) + kVTok - 1) / kVTok;
+          for (int j = 0; j < vs; ++j) {
+            if (!take()) break;
+            if (elect_one()) {
+              mbar_arrive_expect_tx(&full[1][slot], static_cast<uint32_t>(a.nv * kVTok * 128));
+              for (int k = 0; k < a.nv; ++k)
+                tma_box_3d(ring + slot * kSlotBytes + k * kVTok * 128, &v_map, k * 64, h, ex.k0 + tok + j * kVTok,
+                           &full[1][slot]);
+            }
+            __syncwarp();
+            step(1);
+          }
+        }
+      }
+      if (abort) {
+        // give the copies in flight a bounded time to land
+        for (int s = 0; s < 2 * a.slots; ++s) {
+          const int u = s & 1, at = s >> 1;
+          bool late = false;
+          if ((fills[u] >> at) & 1u) mbar_wait(&full[u][at], ((turn[u] >> at) & 1u) ^ 1u, late);
+        }
+        bool late = false;
+        mbar_wait(&q_full, 0, late);
+      }
+    }
+  } else if (warp == 1) {
+    // ---- score products S = Q K^T
+    constexpr uint32_t idesc = idesc_bf16(128, 128);
+    const uint32_t q_a = smem_u32(qsm), ring_a = smem_u32(ring);
+    int slot = 0;
+    uint32_t turn = 0;                                // parity of each slot's next fill for this issuer
+    if (tiles > 0) warp_wait(&q_full, 0, abort);
+    for (int t = 0; t < tiles && !abort; ++t) {
+      const uint32_t d = tmem + kPreScol + static_cast<uint32_t>(t & 1) * 128u;
+      // tile t - 2's weights, which lie over its scores, have been multiplied
+      if (t >= 2 && !warp_wait(&pv_done[t & 1], static_cast<uint32_t>((t >> 1) + 1) & 1u, abort)) break;
+      for (int k = 0; k < a.nq; ++k) {
+        if (!warp_wait(&full[0][slot], (turn >> slot) & 1u, abort)) break;
+        turn ^= 1u << slot;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t sa = q_a + static_cast<uint32_t>(k) * kSlotBytes;
+          const uint32_t sb = ring_a + static_cast<uint32_t>(slot) * kSlotBytes;
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            mma_bf16(d, sdesc_sw128(sa + m * 32), sdesc_sw128(sb + m * 32), idesc, (k | m) != 0);
+          mma_commit(&empty[slot]);
+          if (k + 1 == a.nq) mma_commit(&s_full[t & 1]);
+        }
+        __syncwarp();
+        if (++slot == a.slots) slot = 0;
+      }
+      if (t > 0) {                                    // tile t - 1's values
+        slot += kPreTile / kVTok;
+        if (slot >= a.slots) slot -= a.slots;
+      }
+    }
+    drain_mmas(&drain[0], abort);
+  } else if (warp == 2) {
+    // ---- output products O += P V
+    const uint32_t idesc = idesc_bf16(128, (a.dv + 15) & ~15) | kIdescBMn;
+    const uint32_t ring_a = smem_u32(ring);
+    int slot = 0;
+    uint32_t turn = 0;                                // parity of each slot's next fill for this issuer
+    auto skip = [&](int n) {
+      slot += n;
+      if (slot >= a.slots) slot -= a.slots;
+    };
+    skip(a.nq);
+    for (int t = 0; t < tiles && !abort; ++t) {
+      if (t + 1 < tiles) skip(a.nq);
+      const int valid = min(kPreTile, see1 - t * kPreTile);
+      const int ks = (valid + 15) >> 4;
+      const uint32_t p = tmem + kPreScol + static_cast<uint32_t>(t & 1) * 128u;
+      if (!warp_wait(&p_full[t & 1], static_cast<uint32_t>(t >> 1) & 1u, abort)) break;
+      for (int j = 0; 2 * j < ks; ++j) {
+        if (!warp_wait(&full[1][slot], (turn >> slot) & 1u, abort)) break;
+        turn ^= 1u << slot;
+        const int z0 = valid - j * kVTok;
+        if (z0 < kVTok) {
+          // keys of this slot that no query of the tile sees may hold anything
+          // (0 x NaN): their weights are 0 and they are made 0 too
+          for (int k = 0; k < a.nv; ++k) zero_rows(ring + slot * kSlotBytes + k * kVTok * 128, z0, kVTok, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t bd = sdesc_mn_sw128(ring_a + static_cast<uint32_t>(slot) * kSlotBytes, kVTok * 128);
+          // the weights of keys 64.. start 64 columns on
+          const uint32_t pj = p + static_cast<uint32_t>((j >> 1) * 64 + (j & 1) * 16);
+          mma_bf16_ts(tmem, pj, bd, idesc, (t | j) != 0);
+          if (2 * j + 1 < ks) mma_bf16_ts(tmem, pj + 8, bd + 128u, idesc, 1u);
+          mma_commit(&empty[slot]);
+          if (2 * j + 2 >= ks) mma_commit(&pv_done[t & 1]);
+        }
+        __syncwarp();
+        skip(1);
+      }
+    }
+    drain_mmas(&drain[1], abort);
+  } else if (warp >= 4) {
+    // ---- softmax.  Warps w and w + 4 hold the same 32 queries and meet at
+    // named barriers, so they walk every tile even after a wait has given up.
+    const int q4 = warp & 3, g = (warp - 4) >> 2;
+    const int row = q4 * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
+    const int see = row < rows ? (a.causal ? clamp_to(qi0 + row + 1 + ex.kn - ex.qn, ex.kn) : ex.kn) : 0;
+    const int dvp = (a.dv + 31) & ~31;                // accumulator columns, in halves of 16
+    float m = 0.f, l = 0.f;
+    for (int t = 0; t < tiles; ++t) {
+      const uint32_t sb = tl + kPreScol + static_cast<uint32_t>((t & 1) * 128 + g * 64);
+      uint32_t r[64];
+      mbar_wait(&s_full[t & 1], static_cast<uint32_t>(t >> 1) & 1u, abort);
+      __syncwarp();
+      tc_fence_after();
+      tmem_ld_cols<64>(sb, r);
+      tmem_wait_ld_of(r);
+      float mx = -INFINITY;
+      const int j0 = t * kPreTile + g * 64;
+      if ((t + 1) * kPreTile > see0) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+          r[j] = j0 + j < see ? __float_as_uint(__uint_as_float(r[j]) * a.c) : 0xFF800000u;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * a.c);
+      }
+#pragma unroll
+      for (int j = 0; j < 64; ++j) mx = fmaxf(mx, __uint_as_float(r[j]));
+      if (t == 0 || named_sync_or(1 + q4, 64, mx - m > kMaxSlack)) {
+        xch[g][row] = mx;
+        named_sync(1 + q4, 64);
+        float mn = fmaxf(mx, xch[g ^ 1][row]);
+        if (t > 0) mn = fmaxf(mn, m);
+        if (mn == -INFINITY) mn = 0.f;                // a query that sees no key of the first tile sees none
+        if (t > 0) {
+          const float f = exp2_fast(m - mn);
+          l *= f;
+          mbar_wait(&pv_done[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1) & 1u, abort);
+          __syncwarp();
+          tc_fence_after();
+          for (int c = g * (dvp >> 1); c < (g + 1) * (dvp >> 1); c += 16) {
+            uint32_t o[16];
+            tmem_ld16(tl + c, o);
+            tmem_wait_ld_of(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(tl + c, o);
+          }
+          tmem_wait_st();
+        }
+        m = mn;
+        named_sync(1 + q4, 64);                       // xch is free again
+      }
+      // weights (rounded to bf16 for the MMA) and their fp32 sum (unrounded)
+      uint32_t p[32];
+      float ls = 0.f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const float p0 = exp2_fast(__uint_as_float(r[2 * j]) - m), p1 = exp2_fast(__uint_as_float(r[2 * j + 1]) - m);
+        ls += p0 + p1;
+        p[j] = pack_bf16x2(p0, p1);
+      }
+      l += ls;
+      tmem_st_cols<32>(sb, p);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[t & 1]);
+    }
+    // ---- output
+    xch[g][row] = l;
+    named_sync(1 + q4, 64);
+    l = xch[0][row] + xch[1][row];
+    if (tiles > 0) {
+      mbar_wait(&pv_done[(tiles - 1) & 1], static_cast<uint32_t>((tiles - 1) >> 1) & 1u, abort);
+      __syncwarp();
+      tc_fence_after();
+    }
+    const float f = l == 0.f ? 0.f : 1.0f / l;
+    const int64_t tok = static_cast<int64_t>(ex.q0) + qi0 + row;
+    __nv_bfloat16* dst = a.out + tok * a.o_tok + h * a.o_head;
+    for (int c = g * (dvp >> 1); c < (g + 1) * (dvp >> 1); c += 16) {
+      uint32_t o[16];
+      if (tiles > 0) {
+        tmem_ld16(tl + c, o);
+        tmem_wait_ld_of(o);
+      }
+      if (row < rows) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {
+          if (c + e >= a.dv) break;                   // dv is a multiple of 8
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            w[x] = l == 0.f ? 0u
+                            : pack_bf16x2(__uint_as_float(o[e + 2 * x]) * f, __uint_as_float(o[e + 2 * x + 1]) * f);
+          *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+    if (g == 0 && row < rows && a.lse != nullptr)
+      a.lse[tok * a.H + h] = l == 0.f ? -INFINITY : (m + log2_fast(l)) * kLn2;
+  }
+  if (abort) atomicOr(&g_mla_prefill_error, kErrTimeout);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ host
+static std::atomic<bool> g_prefill_attr[64];
+
+cudaError_t launch_mla_prefill(const MlaPrefillProblem& p, const DeviceInfo& dev, cudaStream_t s) {
+  if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
+  cudaError_t e = mla_bind_context();
+  if (e != cudaSuccess) return e;
+  if (!g_prefill_attr[dev.device].load(std::memory_order_acquire)) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, mla_prefill_kernel)) != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kPreSmem - static_cast<int>(fa.sharedSizeBytes));
+    if (e != cudaSuccess) return e;
+    g_prefill_attr[dev.device].store(true, std::memory_order_release);
+  }
+  PrefillArgs a{};
+  a.cu_q = p.cu_q;
+  a.cu_k = p.cu_k;
+  a.out = static_cast<__nv_bfloat16*>(const_cast<void*>(p.out.p));
+  a.lse = p.lse;
+  a.o_tok = p.out.tok;
+  a.o_head = p.out.head;
+  a.S = p.S;
+  a.H = p.H;
+  a.Tq = p.Tq;
+  a.Tk = p.Tk;
+  a.dn = p.dn;
+  a.dv = p.dv;
+  a.nq = static_cast<int>(ceil_div(p.dn, 64)) + 1;
+  a.nv = static_cast<int>(ceil_div(p.dv, 64));
+  a.c = p.scale * kLog2e;
+  a.causal = p.causal;
+  const int fixed = a.nq * kSlotBytes + 1024;
+  int slots = (kPreSmem - 2048 - fixed) / kSlotBytes;
+  a.slots = slots > kPreMaxSlots ? kPreMaxSlots : slots;
+
+  CUtensorMap m[5];
+  if ((e = mla_tensor_map(&m[0], p.q_nope.p, p.dn, p.H, p.Tq, p.q_nope.head, p.q_nope.tok, 64, 1, kPreTile)) !=
+          cudaSuccess ||
+      (e = mla_tensor_map(&m[1], p.q_rope.p, kMlaRope, p.H, p.Tq, p.q_rope.head, p.q_rope.tok, 64, 1, kPreTile)) !=
+          cudaSuccess ||
+      (e = mla_tensor_map(&m[2], p.k_nope.p, p.dn, p.H, p.Tk, p.k_nope.head, p.k_nope.tok, 64, 1, kPreTile)) !=
+          cudaSuccess ||
+      (e = mla_tensor_map(&m[3], p.k_rope.p, kMlaRope, 1, p.Tk, kMlaRope, p.k_rope.tok, 64, 1, kPreTile)) !=
+          cudaSuccess ||
+      (e = mla_tensor_map(&m[4], p.v.p, p.dv, p.H, p.Tk, p.v.head, p.v.tok, 64, 1, kVTok)) != cudaSuccess)
+    return e;
+  // at most one partly filled query tile per sequence
+  const unsigned tiles = static_cast<unsigned>(p.Tq / kPreTile + p.S);
+  return mla_launch(mla_prefill_kernel, dim3(tiles, static_cast<unsigned>(p.H)), kPreThreads,
+                    fixed + a.slots * kSlotBytes, s, m[0], m[1], m[2], m[3], m[4], a);
+}
+
+uint32_t mla_prefill_read_clear_error() { return read_clear_word(g_mla_prefill_error); }
+
+}  // namespace mx
