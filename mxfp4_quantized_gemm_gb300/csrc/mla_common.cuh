@@ -33,6 +33,33 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, bool& 
   return !abort;
 }
 
+// A place in a ring of n slots with a full and an empty barrier each: the slot
+// and the parity of the current turn round the ring.  One warp fills it and
+// one warp empties it (a warp that skipped another's phases could take a
+// barrier for complete a turn early).
+struct Ring {
+  int n;
+  int slot = 0;
+  uint32_t turn = 0;
+  int filled = 0;
+  __device__ __forceinline__ explicit Ring(int slots) : n(slots) {}
+  __device__ __forceinline__ void step() {
+    if (filled < n) ++filled;
+    if (++slot == n) {
+      slot = 0;
+      turn ^= 1u;
+    }
+  }
+  // For the filling warp, after a wait that gave up: a bounded wait for the
+  // copies in flight.
+  __device__ __forceinline__ void drain(uint64_t* full) const {
+    for (int s = 0; s < filled; ++s) {
+      bool late = false;
+      mbar_wait(&full[s], s < slot ? turn : turn ^ 1u, late);
+    }
+  }
+};
+
 // After a wait that gave up, by a whole warp that issued MMAs: a bounded wait
 // for those in flight, before their TMEM is freed.
 __device__ __forceinline__ void drain_mmas(uint64_t* bar, bool abort) {
@@ -85,6 +112,38 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)
   for (int i = 0; i < N; i += 16) tmem_st16(taddr + i, *reinterpret_cast<const uint32_t(*)[16]>(&r[i]));
 }
 
+// Pairs of fp32 values in one 64-bit register: an FMA or an addition of both
+// is one instruction.
+__device__ __forceinline__ uint64_t pair2(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
+}
+__device__ __forceinline__ uint64_t pair2f(float lo, float hi) {
+  return pair2(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ void split2(uint64_t v, float& lo, float& hi) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+  lo = __uint_as_float(a);
+  hi = __uint_as_float(b);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // 2^x (two units in the last place of fp32; -inf gives 0).
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -125,6 +184,14 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int row0, int row1, int
 }
 
 // ------------------------------------------------------------------ host
+// The factor from scores to powers of two.  Hidden scores are -inf and stay
+// so under any positive factor; 0 x -inf would not, so a scale of zero becomes
+// the least normal number, which leaves all finite scores equal just the same.
+inline float positive_scale(float scale) {
+  const float c = scale * kLog2e;
+  return c < 1.17549435e-38f ? 1.17549435e-38f : c;
+}
+
 // The calling host thread's device context, made current if the runtime has
 // not bound it yet (cuTensorMapEncodeTiled is a driver call).
 inline cudaError_t mla_bind_context() {

@@ -14,12 +14,17 @@
 // the value tile is read in place from the expanding projection's output
 // [token][head][dn + dv] (its rows are the MMA's K: N-contiguous operand).
 //
-// Roles: warp 0 copies, in 16 KB slots of one ring (64 values of 128 keys, or
-// all values of 32 keys); warp 1 issues the score products, warp 2 the
-// output products; warps 4..7 and 8..11 hold the softmax, thread = (query,
+// Roles: warp 0 copies keys and warp 3 values, each through a ring of 16 KB
+// slots of its own (64 values of 128 keys; all values of 32 keys); warp 1
+// issues the score products, warp 2 the output products; warps 4..7 and 8..11 hold the softmax, thread = (query,
 // half of the tile's keys).  Each query's running maximum is raised only when
 // a score passes it by 2^8, decided per 32 queries by a barrier with an OR
 // over the two warps that hold them.
+//
+// Two copying warps because one is too slow: a wait, an arrival and a tensor
+// copy take a warp about 430 cycles whatever the copy's size (16 more for each
+// further copy under the same wait), 38 bytes a cycle with 16 KB slots, and
+// the products use 62.  One warp for both: 2096 us at 8192 tokens x 64 heads.
 //
 // Blocks are ordered head by head and, within a head, from the last queries
 // (most keys) to the first: blocks that run together share a head's keys and
@@ -39,7 +44,7 @@ constexpr int kPreThreads = 384;
 constexpr int kPreTile = 128;                 // queries, and keys per tile
 constexpr int kSlotBytes = 16384;             // 128 keys x 64 values, or 32 keys x 256 values
 constexpr int kVTok = 32;                     // keys per value slot
-constexpr int kPreMaxSlots = 12;
+constexpr int kPreMaxSlots = 12;              // ring slots, keys' and values' together
 constexpr int kPreSmem = 227 * 1024;
 constexpr int kPreScol = 256;                 // first TMEM column of the score tiles
 
@@ -52,8 +57,9 @@ struct PrefillArgs {
   int S, H, Tq, Tk, dn, dv;
   int nq;               // 64-value chunks of q and k (the last is the rotated one)
   int nv;               // 64-value blocks of v
-  int slots;
-  float c;              // scale * log2(e)
+  int kslots, vslots;   // ring slots of the keys and of the values
+  float c;              // |scale| * log2(e)
+  bool flip;            // scale < 0: the scores change sign first
   bool causal;
 };
 
@@ -78,9 +84,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qsm = smem;                                // nq chunks of 128 queries x 64 values
-  uint8_t* ring = qsm + a.nq * kSlotBytes;
+  uint8_t* kring = qsm + a.nq * kSlotBytes;
+  uint8_t* vring = kring + a.kslots * kSlotBytes;
 
-  __shared__ __align__(8) uint64_t full[2][kPreMaxSlots], empty[kPreMaxSlots];
+  __shared__ __align__(8) uint64_t kfull[kPreMaxSlots], kempty[kPreMaxSlots], vfull[kPreMaxSlots], vempty[kPreMaxSlots];
   __shared__ __align__(8) uint64_t q_full, s_full[2], p_full[2], pv_done[2], drain[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int scan[kPreThreads / 32];
@@ -90,10 +97,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   bool abort = false;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < a.slots; ++s) {
-      mbar_init(&full[0][s], 1);
-      mbar_init(&full[1][s], 1);
-      mbar_init(&empty[s], 1);
+    for (int s = 0; s < kPreMaxSlots; ++s) {
+      mbar_init(&kfull[s], 1);
+      mbar_init(&kempty[s], 1);
+      mbar_init(&vfull[s], 1);
+      mbar_init(&vempty[s], 1);
     }
     mbar_init(&q_full, 1);
     for (int i = 0; i < 2; ++i) {
@@ -161,147 +169,113 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   const int tiles = (see1 + kPreTile - 1) / kPreTile;
 
   if (warp == 0) {
-    // ---- copies.  A ring slot has two full barriers, for keys and for values:
-    // the issuer of either product sees only its own, and a barrier whose
-    // phases it skipped could be taken for complete a turn early.
-    int slot = 0;
-    uint32_t ph = 0;
-    uint32_t fills[2] = {0, 0}, turn[2] = {0, 0};   // per slot: filled at all; parity of the next fill
-    auto take = [&]() -> bool {
-      if (!warp_wait(&empty[slot], ph ^ 1u, abort)) return false;
-      return true;
-    };
-    auto step = [&](int use) {
-      fills[use] |= 1u << slot;
-      turn[use] ^= 1u << slot;
-      if (++slot == a.slots) {
-        slot = 0;
-        ph ^= 1u;
-      }
-    };
+    // ---- queries and keys
+    Ring r(a.kslots);
     if (tiles > 0) {
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(a.nq * kSlotBytes));
         for (int k = 0; k + 1 < a.nq; ++k) tma_box_3d(qsm + k * kSlotBytes, &qn_map, k * 64, h, ex.q0 + qi0, &q_full);
         tma_box_3d(qsm + (a.nq - 1) * kSlotBytes, &qr_map, 0, h, ex.q0 + qi0, &q_full);
       }
       __syncwarp();
-      for (int t = 0; t <= tiles && !abort; ++t) {
-        if (t < tiles) {
-          const int tok = ex.k0 + t * kPreTile;
-          for (int k = 0; k < a.nq; ++k) {
-            if (!take()) break;
-            if (elect_one()) {
-              mbar_arrive_expect_tx(&full[0][slot], kSlotBytes);
-              if (k + 1 < a.nq)
-                tma_box_3d(ring + slot * kSlotBytes, &kn_map, k * 64, h, tok, &full[0][slot]);
-              else
-                tma_box_3d(ring + slot * kSlotBytes, &kr_map, 0, 0, tok, &full[0][slot]);
-            }
-            __syncwarp();
-            step(0);
-          }
+    }
+    for (int t = 0; t < tiles && !abort; ++t) {
+      const int tok = ex.k0 + t * kPreTile;
+      for (int k = 0; k < a.nq; ++k) {
+        if (!warp_wait(&kempty[r.slot], r.turn ^ 1u, abort)) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&kfull[r.slot], kSlotBytes);
+          if (k + 1 < a.nq)
+            tma_box_3d(kring + r.slot * kSlotBytes, &kn_map, k * 64, h, tok, &kfull[r.slot]);
+          else
+            tma_box_3d(kring + r.slot * kSlotBytes, &kr_map, 0, 0, tok, &kfull[r.slot]);
         }
-        if (t > 0 && !abort) {
-          const int tok = (t - 1) * kPreTile;
-          const int vs = (min(kPreTile, see1 - tok) + kVTok - 1) / kVTok;
-          for (int j = 0; j < vs; ++j) {
-            if (!take()) break;
-            if (elect_one()) {
-              mbar_arrive_expect_tx(&full[1][slot], static_cast<uint32_t>(a.nv * kVTok * 128));
-              for (int k = 0; k < a.nv; ++k)
-                tma_box_3d(ring + slot * kSlotBytes + k * kVTok * 128, &v_map, k * 64, h, ex.k0 + tok + j * kVTok,
-                           &full[1][slot]);
-            }
-            __syncwarp();
-            step(1);
-          }
-        }
-      }
-      if (abort) {
-        // give the copies in flight a bounded time to land
-        for (int s = 0; s < 2 * a.slots; ++s) {
-          const int u = s & 1, at = s >> 1;
-          bool late = false;
-          if ((fills[u] >> at) & 1u) mbar_wait(&full[u][at], ((turn[u] >> at) & 1u) ^ 1u, late);
-        }
-        bool late = false;
-        mbar_wait(&q_full, 0, late);
+        __syncwarp();
+        r.step();
       }
     }
+    if (abort) {
+      r.drain(kfull);
+      bool late = false;
+      if (tiles > 0) mbar_wait(&q_full, 0, late);
+    }
+  } else if (warp == 3) {
+    // ---- values
+    Ring r(a.vslots);
+    for (int t = 0; t < tiles && !abort; ++t) {
+      const int tok = t * kPreTile;
+      for (int j = 0; j < kPreTile / kVTok && tok + j * kVTok < see1; ++j) {
+        if (!warp_wait(&vempty[r.slot], r.turn ^ 1u, abort)) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&vfull[r.slot], static_cast<uint32_t>(a.nv * kVTok * 128));
+          for (int k = 0; k < a.nv; ++k)
+            tma_box_3d(vring + r.slot * kSlotBytes + k * kVTok * 128, &v_map, k * 64, h, ex.k0 + tok + j * kVTok,
+                       &vfull[r.slot]);
+        }
+        __syncwarp();
+        r.step();
+      }
+    }
+    if (abort) r.drain(vfull);
   } else if (warp == 1) {
     // ---- score products S = Q K^T
     constexpr uint32_t idesc = idesc_bf16(128, 128);
-    const uint32_t q_a = smem_u32(qsm), ring_a = smem_u32(ring);
-    int slot = 0;
-    uint32_t turn = 0;                                // parity of each slot's next fill for this issuer
+    const uint32_t q_a = smem_u32(qsm), ring_a = smem_u32(kring);
+    Ring r(a.kslots);
     if (tiles > 0) warp_wait(&q_full, 0, abort);
     for (int t = 0; t < tiles && !abort; ++t) {
       const uint32_t d = tmem + kPreScol + static_cast<uint32_t>(t & 1) * 128u;
       // tile t - 2's weights, which lie over its scores, have been multiplied
       if (t >= 2 && !warp_wait(&pv_done[t & 1], static_cast<uint32_t>((t >> 1) + 1) & 1u, abort)) break;
       for (int k = 0; k < a.nq; ++k) {
-        if (!warp_wait(&full[0][slot], (turn >> slot) & 1u, abort)) break;
-        turn ^= 1u << slot;
+        if (!warp_wait(&kfull[r.slot], r.turn, abort)) break;
         tc_fence_after();
         if (elect_one()) {
           const uint32_t sa = q_a + static_cast<uint32_t>(k) * kSlotBytes;
-          const uint32_t sb = ring_a + static_cast<uint32_t>(slot) * kSlotBytes;
+          const uint32_t sb = ring_a + static_cast<uint32_t>(r.slot) * kSlotBytes;
 #pragma unroll
           for (int m = 0; m < 4; ++m)
             mma_bf16(d, sdesc_sw128(sa + m * 32), sdesc_sw128(sb + m * 32), idesc, (k | m) != 0);
-          mma_commit(&empty[slot]);
+          mma_commit(&kempty[r.slot]);
           if (k + 1 == a.nq) mma_commit(&s_full[t & 1]);
         }
         __syncwarp();
-        if (++slot == a.slots) slot = 0;
-      }
-      if (t > 0) {                                    // tile t - 1's values
-        slot += kPreTile / kVTok;
-        if (slot >= a.slots) slot -= a.slots;
+        r.step();
       }
     }
     drain_mmas(&drain[0], abort);
   } else if (warp == 2) {
     // ---- output products O += P V
     const uint32_t idesc = idesc_bf16(128, (a.dv + 15) & ~15) | kIdescBMn;
-    const uint32_t ring_a = smem_u32(ring);
-    int slot = 0;
-    uint32_t turn = 0;                                // parity of each slot's next fill for this issuer
-    auto skip = [&](int n) {
-      slot += n;
-      if (slot >= a.slots) slot -= a.slots;
-    };
-    skip(a.nq);
+    const uint32_t ring_a = smem_u32(vring);
+    Ring r(a.vslots);
     for (int t = 0; t < tiles && !abort; ++t) {
-      if (t + 1 < tiles) skip(a.nq);
       const int valid = min(kPreTile, see1 - t * kPreTile);
       const int ks = (valid + 15) >> 4;
       const uint32_t p = tmem + kPreScol + static_cast<uint32_t>(t & 1) * 128u;
       if (!warp_wait(&p_full[t & 1], static_cast<uint32_t>(t >> 1) & 1u, abort)) break;
       for (int j = 0; 2 * j < ks; ++j) {
-        if (!warp_wait(&full[1][slot], (turn >> slot) & 1u, abort)) break;
-        turn ^= 1u << slot;
+        if (!warp_wait(&vfull[r.slot], r.turn, abort)) break;
         const int z0 = valid - j * kVTok;
         if (z0 < kVTok) {
           // keys of this slot that no query of the tile sees may hold anything
           // (0 x NaN): their weights are 0 and they are made 0 too
-          for (int k = 0; k < a.nv; ++k) zero_rows(ring + slot * kSlotBytes + k * kVTok * 128, z0, kVTok, lane);
+          for (int k = 0; k < a.nv; ++k) zero_rows(vring + r.slot * kSlotBytes + k * kVTok * 128, z0, kVTok, lane);
           fence_proxy_async_smem();
           __syncwarp();
         }
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t bd = sdesc_mn_sw128(ring_a + static_cast<uint32_t>(slot) * kSlotBytes, kVTok * 128);
+          const uint64_t bd = sdesc_mn_sw128(ring_a + static_cast<uint32_t>(r.slot) * kSlotBytes, kVTok * 128);
           // the weights of keys 64.. start 64 columns on
           const uint32_t pj = p + static_cast<uint32_t>((j >> 1) * 64 + (j & 1) * 16);
           mma_bf16_ts(tmem, pj, bd, idesc, (t | j) != 0);
           if (2 * j + 1 < ks) mma_bf16_ts(tmem, pj + 8, bd + 128u, idesc, 1u);
-          mma_commit(&empty[slot]);
+          mma_commit(&vempty[r.slot]);
           if (2 * j + 2 >= ks) mma_commit(&pv_done[t & 1]);
         }
         __syncwarp();
-        skip(1);
+        r.step();
       }
     }
     drain_mmas(&drain[1], abort);
@@ -322,18 +296,25 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       tc_fence_after();
       tmem_ld_cols<64>(sb, r);
       tmem_wait_ld_of(r);
-      float mx = -INFINITY;
       const int j0 = t * kPreTile + g * 64;
+      if (a.flip) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) r[j] ^= 0x80000000u;
+      }
       if ((t + 1) * kPreTile > see0) {
 #pragma unroll
         for (int j = 0; j < 64; ++j)
-          r[j] = j0 + j < see ? __float_as_uint(__uint_as_float(r[j]) * a.c) : 0xFF800000u;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 64; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * a.c);
+          if (j0 + j >= see) r[j] = 0xFF800000u;
       }
+      // four chains, so that the maximum is not a run of 64 dependent steps
+      float m4[4];
 #pragma unroll
-      for (int j = 0; j < 64; ++j) mx = fmaxf(mx, __uint_as_float(r[j]));
+      for (int x = 0; x < 4; ++x) m4[x] = fmaxf(__uint_as_float(r[x]), __uint_as_float(r[4 + x]));
+#pragma unroll
+      for (int j = 8; j < 64; j += 8)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) m4[x] = max3(m4[x], __uint_as_float(r[j + x]), __uint_as_float(r[j + 4 + x]));
+      float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.c;
       if (t == 0 || named_sync_or(1 + q4, 64, mx - m > kMaxSlack)) {
         xch[g][row] = mx;
         named_sync(1 + q4, 64);
@@ -361,14 +342,20 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
       // weights (rounded to bf16 for the MMA) and their fp32 sum (unrounded)
       uint32_t p[32];
-      float ls = 0.f;
+      const uint64_t c2 = pair2f(a.c, a.c), m2 = pair2f(-m, -m);
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        const float p0 = exp2_fast(__uint_as_float(r[2 * j]) - m), p1 = exp2_fast(__uint_as_float(r[2 * j + 1]) - m);
-        ls += p0 + p1;
-        p[j] = pack_bf16x2(p0, p1);
+        float x0, x1;
+        split2(fma2(pair2(r[2 * j], r[2 * j + 1]), c2, m2), x0, x1);
+        x0 = exp2_fast(x0);
+        x1 = exp2_fast(x1);
+        sum[j & 1] = add2(sum[j & 1], pair2f(x0, x1));
+        p[j] = pack_bf16x2(x0, x1);
       }
-      l += ls;
+      float s0, s1;
+      split2(add2(sum[0], sum[1]), s0, s1);
+      l += s0 + s1;
       tmem_st_cols<32>(sb, p);
       tmem_wait_st();
       tc_fence_before();
@@ -445,11 +432,14 @@ cudaError_t launch_mla_prefill(const MlaPrefillProblem& p, const DeviceInfo& dev
   a.dv = p.dv;
   a.nq = static_cast<int>(ceil_div(p.dn, 64)) + 1;
   a.nv = static_cast<int>(ceil_div(p.dv, 64));
-  a.c = p.scale * kLog2e;
+  a.flip = p.scale < 0.f;
+  a.c = positive_scale(a.flip ? -p.scale : p.scale);
   a.causal = p.causal;
   const int fixed = a.nq * kSlotBytes + 1024;
   int slots = (kPreSmem - 2048 - fixed) / kSlotBytes;
-  a.slots = slots > kPreMaxSlots ? kPreMaxSlots : slots;
+  if (slots > kPreMaxSlots) slots = kPreMaxSlots;
+  a.vslots = slots / 2;
+  a.kslots = slots - a.vslots;
 
   CUtensorMap m[5];
   if ((e = mla_tensor_map(&m[0], p.q_nope.p, p.dn, p.H, p.Tq, p.q_nope.head, p.q_nope.tok, 64, 1, kPreTile)) !=
@@ -465,7 +455,7 @@ cudaError_t launch_mla_prefill(const MlaPrefillProblem& p, const DeviceInfo& dev
   // at most one partly filled query tile per sequence
   const unsigned tiles = static_cast<unsigned>(p.Tq / kPreTile + p.S);
   return mla_launch(mla_prefill_kernel, dim3(tiles, static_cast<unsigned>(p.H)), kPreThreads,
-                    fixed + a.slots * kSlotBytes, s, m[0], m[1], m[2], m[3], m[4], a);
+                    fixed + slots * kSlotBytes, s, m[0], m[1], m[2], m[3], m[4], a);
 }
 
 uint32_t mla_prefill_read_clear_error() { return read_clear_word(g_mla_prefill_error); }
