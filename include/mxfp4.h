@@ -406,7 +406,7 @@ MXFP4_API mxfp4_status mxfp4_mla_store(const void* kv_dev, int64_t ld_kv, const 
 
 /* Workspace bytes mxfp4_mla_decode needs: the parts of sequences that are cut
  * between thread blocks.  max_len = max_pages * page_size.  0 where no
- * sequence can be cut (max_len <= 128) or an argument is not positive. */
+ * sequence can be cut (max_len <= 64) or an argument is not positive. */
 MXFP4_API size_t mxfp4_mla_decode_workspace_bytes(int S, int q_len, int H, int L, int64_t max_len);
 
 /*

@@ -8,25 +8,25 @@
 // byte, well below the card's 288, and HBM is the bound.
 //
 // A block takes up to 64 query rows of one sequence (a row group) and walks
-// the positions in tiles of 128.  The accumulator of 64 rows x 512 latent
-// values must stay in TMEM, whose 512 columns a 128-row fp32 accumulator of
-// that width would fill by itself, so both products are formed transposed:
-//   S^T [128 positions][rows] = C Q^T        (lanes = positions)
-//   O^T [128 latent values][rows] += C^T P^T (L / 128 blocks, 64 columns each)
-// which leaves room for two score tiles.  C feeds both products as the A
-// operand, once with the latent values along K and once along M.  The tile
-// (147 KB at L = 512) and the queries (74 KB) do not fit in shared memory
-// twice, so the latent part streams through a ring of 128 x 128 pieces twice:
-// from HBM for S^T, and from L2 shortly after for O^T.
+// the positions in tiles of 64, each read once: two tiles (74 KB each at
+// L = 512) and the queries (74 KB) fill shared memory.  The accumulator of
+// 64 rows x 512 latent values must stay in TMEM, whose 512 columns a 128-row
+// fp32 accumulator of that width would fill by itself, so the output product
+// is formed transposed:
+//   S   [64 rows][64 positions]      = Q C^T
+//   O^T [128 latent values][rows]   += C^T P^T   (L / 128 blocks of 64 columns)
+// which takes 256 columns and leaves room for two score tiles.  C is the B
+// operand of the first product (latent values along K) and the A operand of
+// the second (along M).
 //
-// Roles: warp 0 copies (every lane one box of a page), warp 1 issues the
-// score products, warp 2 the output products (two issuers, so that one's
-// waits on barriers overlap the other's MMAs), warps 4..7 hold the softmax:
-// thread = position, so a weight row P^T goes out as one 128-byte row.  The
-// running maximum of a query row is shared by the 128 threads; it is raised
-// only when some score passes it by 2^8 (first tile aside), which one barrier
-// with an OR decides, and each thread keeps the sums of its own positions
-// until the end of the sequence.
+// Roles: warp 0 copies, warp 1 issues the score products, warp 2 the output
+// products; warps 4..7 and 8..11 hold the softmax: thread = (row, half of the
+// tile's positions), in the lanes where a 64-row MMA leaves its rows (16 of
+// each 32).  A row's running maximum is raised only when a score passes it by
+// 2^8 (first tile aside), which one barrier with an OR decides.
+// A copying warp spends about 430 cycles on each wait, arrival and copy and
+// 16 on each further copy, so a tile comes in two groups, each under one
+// barrier: the first half of the latent, and the rest with the rotated key.
 //
 // Work split: the tiles of all row groups, in order, are cut evenly over the
 // grid; a block takes its stretch wherever sequences begin and end, so a
@@ -44,12 +44,12 @@ namespace mx {
 
 static __device__ uint32_t g_mla_decode_error;
 
-constexpr int kDecThreads = 256;
-constexpr int kTileTok = 128;                       // positions per tile
-constexpr int kChunkBytes = kTileTok * 128;         // 128 positions x 64 values
-constexpr int kDecStageBytes = 2 * kChunkBytes;     // 128 positions x 128 values
-constexpr int kDecMaxStages = 5;
+constexpr int kDecThreads = 384;
+constexpr int kTileTok = 64;                        // positions per tile
+constexpr int kChunkBytes = kTileTok * 128;         // 64 positions x 64 values
+constexpr int kDecMaxBufs = 4;
 constexpr int kDecSmem = 227 * 1024;
+constexpr int kDecStatic = 2048;                    // most of it that the static part takes
 constexpr int kDecScol = 256;                       // first TMEM column of the score tiles
 constexpr int kMaxCtas = 256;
 
@@ -65,8 +65,9 @@ struct DecodeArgs {
   int64_t capacity;       // positions a page-table row can hold
   int HB, TB, TPT;        // heads and tokens per box, tokens per row group
   int head_blocks, RT;    // row groups per token block, per sequence
-  int stages;
-  float c;                // scale * log2(e)
+  int bufs;               // tiles in shared memory
+  float c;                // |scale| * log2(e)
+  bool flip;              // scale < 0: the scores change sign first
 };
 
 // Positions of sequence s (a bad length is cut to what the table holds).
@@ -78,6 +79,29 @@ __device__ __forceinline__ int seq_len(const DecodeArgs& a, int s) {
 // (whose rows still have to be written).
 __device__ __forceinline__ int group_units(int len) { return len == 0 ? 1 : (len + kTileTok - 1) / kTileTok; }
 
+// total / n and the like, in 32 bits where they fit (a 64-bit division takes
+// several times as long, and this is on the way to the first load).
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// The units 0 .. total - 1 cut over n blocks, the first total % n of which
+// take one more.
+struct Cut {
+  int64_t q, r;
+  __device__ __forceinline__ Cut(int64_t total, int grid, int& n) {
+    n = total < grid ? static_cast<int>(total) : grid;
+    q = div64(total, n);
+    r = total - q * n;
+  }
+  __device__ __forceinline__ int64_t begin(int c) const { return c * q + (c < r ? c : r); }
+  __device__ __forceinline__ int owner(int64_t u) const {
+    const int64_t big = (q + 1) * r;
+    return static_cast<int>(u < big ? div64(u, q + 1) : r + div64(u - big, q));
+  }
+};
+
 // A stretch of one row group's tiles.
 struct Segment {
   int s, rt, len, t0, t1, nt;
@@ -86,6 +110,47 @@ struct Segment {
 struct Walk {
   int64_t left;       // units still to hand out
   int s, rt, off;
+  // The block's stretch, found by each warp for itself (one round of loads,
+  // no barrier).
+  __device__ __forceinline__ void start(const DecodeArgs& a) {
+    const int lane = threadIdx.x & 31;
+    const int per = (a.S + 31) >> 5, s0 = min(a.S, lane * per), s1 = min(a.S, s0 + per);
+    int64_t mine = 0;
+#pragma unroll 4
+    for (int i = s0; i < s1; ++i) mine += group_units(seq_len(a, i));
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int n;
+    const Cut cut(__shfl_sync(0xFFFFFFFFu, incl, 31) * a.RT, static_cast<int>(gridDim.x), n);
+    left = 0;
+    s = rt = off = 0;
+    const int b = static_cast<int>(blockIdx.x);
+    if (b >= n) return;
+    const int64_t ub = cut.begin(b);
+    left = cut.begin(b + 1) - ub;
+    int64_t at = (incl - mine) * a.RT;
+    const bool here = ub >= at && ub < incl * a.RT;
+    if (here) {
+      for (s = s0; s < s1; ++s) {
+        const int g = group_units(seq_len(a, s));
+        const int64_t u = static_cast<int64_t>(g) * a.RT;
+        if (ub < at + u) {
+          rt = static_cast<int>(div64(ub - at, g));
+          off = static_cast<int>(ub - at - static_cast<int64_t>(rt) * g);
+          break;
+        }
+        at += u;
+      }
+    }
+    const int from = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
+    s = __shfl_sync(0xFFFFFFFFu, s, from);
+    rt = __shfl_sync(0xFFFFFFFFu, rt, from);
+    off = __shfl_sync(0xFFFFFFFFu, off, from);
+  }
   __device__ __forceinline__ bool next(const DecodeArgs& a, Segment& g) {
     if (left <= 0) return false;
     g.s = s;
@@ -115,33 +180,6 @@ struct Walk {
   }
 };
 
-// Units before sequence `upto` and of all sequences, by every thread of the
-// block; `red` holds 2 x 32 values.
-__device__ __forceinline__ void unit_sums(const DecodeArgs& a, int upto, int64_t* red, int64_t& before,
-                                          int64_t& total) {
-  int64_t b = 0, t = 0;
-  for (int s = threadIdx.x; s < a.S; s += blockDim.x) {
-    const int64_t u = static_cast<int64_t>(group_units(seq_len(a, s))) * a.RT;
-    t += u;
-    if (s < upto) b += u;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
-    t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-  }
-  if ((threadIdx.x & 31) == 0) {
-    red[threadIdx.x >> 5] = b;
-    red[32 + (threadIdx.x >> 5)] = t;
-  }
-  __syncthreads();
-  before = total = 0;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
-    before += red[w];
-    total += red[32 + w];
-  }
-}
-
 // Floats of one part: rows x L accumulators, then the rows' maxima and sums.
 __host__ __device__ __forceinline__ int64_t part_floats(int rows, int L) {
   return static_cast<int64_t>(rows) * (L + 2);
@@ -161,143 +199,80 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                       const __grid_constant__ CUtensorMap cmap, const DecodeArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int nk = a.L >> 7;                                  // 128-value pieces of the latent
-  uint8_t* psm = smem;                                      // P^T: 128 positions x 128 bytes
-  uint8_t* rope = psm + kChunkBytes;                        // two rotated-key tiles
-  uint8_t* ring = rope + 2 * kChunkBytes;
-  uint8_t* qsm = ring + a.stages * kDecStageBytes;          // 2 nk + 1 chunks of NB rows x 64 values
+  const int nk = a.L >> 7;                                  // 128-value blocks of the latent
+  const int chunks = 2 * nk + 1;                            // 64-value chunks of a cache row
+  const int na = 2 * ((nk + 1) >> 1);                       // those of a tile's first group
+  const int tile_bytes = chunks * kChunkBytes;
+  // the 64-row score MMA reads 64 rows of a query chunk whatever NB is: the
+  // queries lie in front, so that what it reads past them is inside the buffer
+  uint8_t* qsm = smem;                                      // chunks of NB rows x 64 values
+  uint8_t* psm = qsm + chunks * NB * 128;                   // P: NB rows x 64 positions
+  uint8_t* ring = psm + NB * 128;
   constexpr int kQChunk = NB * 128;
 
-  __shared__ __align__(8) uint64_t full[2][kDecMaxStages], empty[kDecMaxStages];
-  __shared__ __align__(8) uint64_t rope_full[2], s_full[2], p_full[2];
-  __shared__ __align__(8) uint64_t q_full, pv_done, o_empty, drain[2];
+  __shared__ __align__(8) uint64_t full[2][kDecMaxBufs], empty[2][kDecMaxBufs];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], q_full, pv_done, o_empty, drain[2];
   __shared__ uint32_t tmem_slot;
-  __shared__ int64_t red64[64];
-  __shared__ Walk walk0;
-  __shared__ __align__(16) float mref[NB], fac[NB], colmax[4][NB];
-  __shared__ __align__(16) int lim[NB];
+  __shared__ __align__(16) float fac[64];
+  __shared__ float xch[2][64];
   __shared__ int64_t row_off[NB];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   bool abort = false;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&full[0][s], 1);
-      mbar_init(&full[1][s], 1);
-      mbar_init(&empty[s], 1);
-    }
+    for (int s = 0; s < kDecMaxBufs; ++s)
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&full[x][s], 1);
+        mbar_init(&empty[x][s], 1);
+      }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&rope_full[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], 256);
       mbar_init(&drain[i], 1);
     }
     mbar_init(&q_full, 1);
     mbar_init(&pv_done, 1);
-    mbar_init(&o_empty, 128);
+    mbar_init(&o_empty, 256);
     fence_mbar_init();
   }
   if (warp == 1) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
   }
-  griddep_wait();
-  // only now: the kernel behind reads seq_lens before its own wait
-  if (threadIdx.x == 0) griddep_launch_dependents();
-
-  // ---- this block's stretch of the units
-  {
-    int64_t none, total;
-    unit_sums(a, 0, red64, none, total);
-    // (at most one block per unit: blocks past that have no stretch)
-    const int64_t n = min(static_cast<int64_t>(gridDim.x), total);
-    const int64_t ub = blockIdx.x < n ? total * blockIdx.x / n : total;
-    const int64_t ue = blockIdx.x < n ? total * (blockIdx.x + 1) / n : total;
-    // the sequence that unit `ub` falls into: chunks of sequences per thread
-    const int per = (a.S + kDecThreads - 1) / kDecThreads;
-    const int s0 = threadIdx.x * per, s1 = min(a.S, s0 + per);
-    int64_t mine = 0;
-    for (int s = s0; s < s1; ++s) mine += static_cast<int64_t>(group_units(seq_len(a, s))) * a.RT;
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    __syncthreads();
-    if (lane == 31) red64[warp] = incl;
-    __syncthreads();
-    int64_t base = 0;
-    for (int w = 0; w < warp; ++w) base += red64[w];
-    int64_t at = base + incl - mine;
-    if (ub >= at && ub < at + mine) {
-      int s = s0;
-      for (; s < s1; ++s) {
-        const int64_t u = static_cast<int64_t>(group_units(seq_len(a, s))) * a.RT;
-        if (ub < at + u) break;
-        at += u;
-      }
-      const int g = group_units(seq_len(a, s));
-      walk0.left = ue - ub;
-      walk0.s = s;
-      walk0.rt = static_cast<int>((ub - at) / g);
-      walk0.off = static_cast<int>((ub - at) % g);
-    }
-    if (threadIdx.x == 0 && ub >= ue) walk0.left = 0;
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  Walk walk = walk0;
+  griddep_wait();
+  // only now: the kernel behind reads seq_lens before its own wait
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  Walk walk;
+  walk.start(a);
 
   if (warp == 0) {
-    // ---- copies.  Lane = (box of a tile, 64-value half of a piece).  A ring
-    // slot has two full barriers, for pieces of the score and of the output
-    // product: their issuers each see only their own pieces, and a barrier
-    // whose phases one issuer skipped could be taken for complete a turn early.
+    // ---- copies.  Lane = (box of the tile's positions, chunk), in turns.
     const int boxes = kTileTok / a.box_rows;
-    const int box = lane >> 1, half = lane & 1;
-    int slot = 0;
-    uint32_t ph = 0;
-    uint32_t fills[2] = {0, 0}, turn[2] = {0, 0};   // per slot: filled at all; parity of the next fill
+    Ring r(a.bufs);
     int i = 0, seg_no = 0;
-    bool have_prev = false;
-    int prev_page = 0, prev_row = 0, prev_boxes = 0;
-    int rope_issued = 0;
-    auto piece = [&](int use, int k, int page, int row, int nb) {
-      if (!warp_wait(&empty[slot], ph ^ 1u, abort)) return;
-      uint64_t* bar = &full[use][slot];
-      if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(nb * a.box_rows * 256));
-      __syncwarp();
-      if (box < nb)
-        tma_box_3d(ring + slot * kDecStageBytes + half * kChunkBytes + box * a.box_rows * 128, &cmap,
-                   k * 128 + half * 64, row, page, bar);
-      fills[use] |= 1u << slot;
-      turn[use] ^= 1u << slot;
-      if (++slot == a.stages) {
-        slot = 0;
-        ph ^= 1u;
-      }
-    };
     Segment g;
     while (!abort && walk.next_real(a, g)) {
-      // the queries: their chunk buffer is free once the last score product of
-      // the stretch before has read it
+      // the queries: their buffer is free once the last score product of the
+      // stretch before has read it
       if (seg_no > 0 && !warp_wait(&s_full[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort)) break;
       const int h0 = (g.rt % a.head_blocks) * a.HB;
       const int tk0 = g.s * a.q_len + (g.rt / a.head_blocks) * a.TPT;
-      if (lane == 0) mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>((2 * nk + 1) * a.HB * a.TB * 128));
+      if (lane == 0) mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(chunks * a.HB * a.TB * 128));
       __syncwarp();
       if (lane < 2 * nk) tma_box_3d(qsm + lane * kQChunk, &qmap, lane * 64, h0, tk0, &q_full);
       if (lane == 31) tma_box_3d(qsm + 2 * nk * kQChunk, &rmap, 0, h0, tk0, &q_full);
       ++seg_no;
       for (int t = g.t0; t < g.t1; ++t, ++i) {
         const int tok0 = t * kTileTok;
-        const int valid = min(kTileTok, g.len - tok0);
-        const int nb = (valid + a.box_rows - 1) / a.box_rows;
+        const int nb = (min(kTileTok, g.len - tok0) + a.box_rows - 1) / a.box_rows;   // boxes that hold anything
+        // lane's box in each group: pages are looked up once a tile
+        const int box = lane & (boxes - 1);
         int page = 0, row = 0;
-        if (box < nb && box < boxes) {
+        if (box < nb) {
           const int tok = tok0 + box * a.box_rows;
           const int col = tok / a.page_size;
           row = tok - col * a.page_size;
@@ -307,53 +282,36 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             page = a.num_pages;              // outside the map: the box is filled with zeros
           }
         }
-        for (int k = 0; k < nk && !abort; ++k) piece(0, k, page, row, nb);
+        uint8_t* buf = ring + r.slot * tile_bytes;
+        for (int x = 0; x < 2; ++x) {
+          const int c0 = x == 0 ? 0 : na, c1 = x == 0 ? na : chunks;
+          if (!warp_wait(&empty[x][r.slot], r.turn ^ 1u, abort)) break;
+          if (lane == 0)
+            mbar_arrive_expect_tx(&full[x][r.slot], static_cast<uint32_t>((c1 - c0) * nb * a.box_rows * 128));
+          __syncwarp();
+          if (box < nb)
+            for (int c = c0 + lane / boxes; c < c1; c += 32 / boxes)
+              tma_box_3d(buf + c * kChunkBytes + box * a.box_rows * 128, &cmap, c * 64, row, page, &full[x][r.slot]);
+          if (x == 0) r.half();
+        }
         if (abort) break;
-        // the rotated keys; the buffer is free once tile i - 2's scores are formed
-        if (i >= 2 && !warp_wait(&s_full[i & 1], static_cast<uint32_t>((i >> 1) + 1) & 1u, abort)) break;
-        if (lane == 0) mbar_arrive_expect_tx(&rope_full[i & 1], static_cast<uint32_t>(nb * a.box_rows * 128));
-        __syncwarp();
-        if (half == 0 && box < nb)
-          tma_box_3d(rope + (i & 1) * kChunkBytes + box * a.box_rows * 128, &cmap, a.L, row, page, &rope_full[i & 1]);
-        ++rope_issued;
-        if (have_prev)
-          for (int k = 0; k < nk && !abort; ++k) piece(1, k, prev_page, prev_row, prev_boxes);
-        if (abort) break;
-        have_prev = true;
-        prev_page = page;
-        prev_row = row;
-        prev_boxes = nb;
+        r.step();
       }
     }
-    if (have_prev)
-      for (int k = 0; k < nk && !abort; ++k) piece(1, k, prev_page, prev_row, prev_boxes);
     if (abort) {
       // give the copies in flight a bounded time to land
-      for (int s = 0; s < 2 * a.stages; ++s) {
-        const int u = s & 1, at = s >> 1;
-        bool late = false;
-        if ((fills[u] >> at) & 1u) mbar_wait(&full[u][at], ((turn[u] >> at) & 1u) ^ 1u, late);
-      }
-      for (int b = 0; b < 2 && b < rope_issued; ++b) {
-        bool late = false;
-        const int last = rope_issued - 1 - ((rope_issued - 1 - b) & 1);
-        mbar_wait(&rope_full[b], static_cast<uint32_t>(last >> 1) & 1u, late);
-      }
+      r.drain(full[1]);
+      r.drain_half(full[0]);
       bool late = false;
       if (seg_no > 0) mbar_wait(&q_full, static_cast<uint32_t>(seg_no - 1) & 1u, late);
     }
   } else if (warp == 1) {
-    // ---- score products S^T = C Q^T
-    constexpr uint32_t idesc = idesc_bf16(128, NB);
-    int slot = 0;
-    uint32_t turn = 0;                       // parity of each slot's next fill for this issuer
+    // ---- score products S = Q C^T
+    constexpr uint32_t idesc = idesc_bf16(64, kTileTok);
+    const uint32_t ring_a = smem_u32(ring), q_a = smem_u32(qsm);
+    Ring r(a.bufs);
     int i = 0, seg_no = 0;
     Segment g;
-    auto skip = [&](int n) {
-      slot += n;
-      while (slot >= a.stages) slot -= a.stages;
-    };
-    const uint32_t ring_a = smem_u32(ring), q_a = smem_u32(qsm), rope_a = smem_u32(rope);
     while (!abort && walk.next_real(a, g)) {
       if (!warp_wait(&q_full, static_cast<uint32_t>(seg_no) & 1u, abort)) break;
       ++seg_no;
@@ -361,170 +319,135 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const uint32_t d = tmem + kDecScol + static_cast<uint32_t>(i & 1) * 64u;
         // tile i - 2's scores have been read once its weights are out
         if (i >= 2 && !warp_wait(&p_full[i & 1], static_cast<uint32_t>((i >> 1) + 1) & 1u, abort)) break;
-        for (int k = 0; k < nk; ++k) {
-          if (!warp_wait(&full[0][slot], (turn >> slot) & 1u, abort)) break;
-          turn ^= 1u << slot;
+        const uint32_t sb = ring_a + static_cast<uint32_t>(r.slot * tile_bytes);
+        for (int x = 0; x < 2; ++x) {
+          const int c0 = x == 0 ? 0 : na, c1 = x == 0 ? na : chunks;
+          if (!warp_wait(&full[x][r.slot], r.turn, abort)) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t sa = ring_a + static_cast<uint32_t>(slot) * kDecStageBytes;
+            uint64_t ad = sdesc_sw128(q_a + static_cast<uint32_t>(c0 * kQChunk));
+            uint64_t bd = sdesc_sw128(sb + static_cast<uint32_t>(c0 * kChunkBytes));
+            for (int c = c0; c < c1; ++c, ad += kQChunk >> 4, bd += kChunkBytes >> 4) {
 #pragma unroll
-            for (int m = 0; m < 8; ++m)
-              mma_bf16(d, sdesc_sw128(sa + (m >> 2) * kChunkBytes + (m & 3) * 32),
-                       sdesc_sw128(q_a + (2 * k + (m >> 2)) * kQChunk + (m & 3) * 32), idesc, (k | m) != 0);
-            mma_commit(&empty[slot]);
+              for (int m = 0; m < 4; ++m) mma_bf16(d, ad + 2 * m, bd + 2 * m, idesc, (c | m) != 0);
+            }
+            if (x == 1) mma_commit(&s_full[i & 1]);
           }
           __syncwarp();
-          skip(1);
         }
-        if (abort || !warp_wait(&rope_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, abort)) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t sa = rope_a + static_cast<uint32_t>(i & 1) * kChunkBytes;
-#pragma unroll
-          for (int m = 0; m < 4; ++m)
-            mma_bf16(d, sdesc_sw128(sa + m * 32), sdesc_sw128(q_a + 2 * nk * kQChunk + m * 32), idesc, 1u);
-          mma_commit(&s_full[i & 1]);
-        }
-        __syncwarp();
-        if (i > 0) skip(nk);                 // tile i - 1's pieces for the output product
+        if (abort) break;
+        r.step();
       }
     }
     drain_mmas(&drain[0], abort);
   } else if (warp == 2) {
     // ---- output products O^T += C^T P^T
-    constexpr uint32_t idesc = idesc_bf16(128, NB) | kIdescAMn | kIdescBMn;
-    int slot = 0;
-    uint32_t turn = 0;                       // parity of each slot's next fill for this issuer
+    constexpr uint32_t idesc = idesc_bf16(128, NB) | kIdescAMn;
+    const uint32_t ring_a = smem_u32(ring);
+    const uint64_t pd = sdesc_sw128(smem_u32(psm));
+    Ring r(a.bufs);
     int i = 0, seg_no = 0;
-    auto skip = [&](int n) {
-      slot += n;
-      while (slot >= a.stages) slot -= a.stages;
-    };
-    const uint32_t ring_a = smem_u32(ring), p_a = smem_u32(psm);
-    Segment g, ahead;
-    bool more = walk.next_real(a, ahead);
-    skip(nk);                                // tile 0's pieces for the scores
-    while (!abort && more) {
-      g = ahead;
-      more = walk.next_real(a, ahead);
+    Segment g;
+    while (!abort && walk.next_real(a, g)) {
       // the accumulator: the stretch before has been read out
       if (seg_no > 0 && !warp_wait(&o_empty, static_cast<uint32_t>(seg_no - 1) & 1u, abort)) break;
       ++seg_no;
       for (int t = g.t0; t < g.t1; ++t, ++i) {
-        if (more || t + 1 < g.t1) skip(nk);  // tile i + 1's pieces for the scores
         const int valid = min(kTileTok, g.len - t * kTileTok);
         const int ks = (valid + 15) >> 4;    // 16-position steps that hold anything
+        // (the weights come from scores of this very tile: it has landed)
         if (!warp_wait(&p_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, abort)) break;
-        for (int k = 0; k < nk; ++k) {
-          if (!warp_wait(&full[1][slot], (turn >> slot) & 1u, abort)) break;
-          turn ^= 1u << slot;
-          if ((valid & 15) != 0) {
-            // rows of the last step past the sequence may hold anything
-            // (0 x NaN): their weights are 0 and they are made 0 too
-            uint8_t* st = ring + slot * kDecStageBytes;
-            zero_rows(st, valid, ks * 16, lane);
-            zero_rows(st + kChunkBytes, valid, ks * 16, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t ad = sdesc_mn_sw128(ring_a + static_cast<uint32_t>(slot) * kDecStageBytes, kChunkBytes);
-            const uint64_t bd = sdesc_mn_sw128(p_a, kChunkBytes);
-            for (int m = 0; m < ks; ++m)
-              mma_bf16(tmem + static_cast<uint32_t>(k) * 64u, ad + static_cast<uint64_t>(m) * 128u,
-                       bd + static_cast<uint64_t>(m) * 128u, idesc, t != g.t0 || m != 0);
-            mma_commit(&empty[slot]);
-          }
+        if ((valid & 15) != 0) {
+          // rows of the last step past the sequence may hold anything
+          // (0 x NaN): their weights are 0 and they are made 0 too
+          for (int c = 0; c < 2 * nk; ++c)
+            zero_rows(ring + r.slot * tile_bytes + c * kChunkBytes, valid, ks * 16, lane);
+          fence_proxy_async_smem();
           __syncwarp();
-          skip(1);
         }
-        if (abort) break;
-        if (elect_one()) mma_commit(&pv_done);
+        tc_fence_after();
+        if (elect_one()) {
+          uint64_t ad = sdesc_mn_sw128(ring_a + static_cast<uint32_t>(r.slot * tile_bytes), kChunkBytes);
+          for (int k = 0; k < nk; ++k, ad += (2 * kChunkBytes) >> 4) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              if (m < ks)
+                mma_bf16(tmem + static_cast<uint32_t>(k) * 64u, ad + m * 128, pd + m * 2, idesc, t != g.t0 || m != 0);
+            if (2 * k + 2 == na) mma_commit(&empty[0][r.slot]);
+          }
+          mma_commit(&empty[1][r.slot]);
+          mma_commit(&pv_done);
+        }
         __syncwarp();
+        r.step();
       }
     }
     drain_mmas(&drain[1], abort);
   } else if (warp >= 4) {
     // ---- softmax and output.  These threads meet at named barriers, so they
-    // walk every tile even after a wait has given up.
-    const int w = warp & 3, tid = threadIdx.x - 128;
+    // walk every tile even after a wait has given up.  A 64-row MMA leaves row
+    // 16 w + x in lane 32 w + x (x < 16); the other lanes only keep company.
+    const int w = warp & 3, half = (warp - 4) >> 2, tid = threadIdx.x - 128;
+    const int row = 16 * w + (lane & 15);
+    const bool mine = lane < 16 && row < NB;
     const uint32_t tl = tmem + (static_cast<uint32_t>(w * 32) << 16);
-    float l[NB];
+    const int kb0 = half == 0 ? 0 : (nk + 1) >> 1, kb1 = half == 0 ? (nk + 1) >> 1 : nk;   // this half's latent blocks
     int i = 0;
     Segment g;
     while (walk.next(a, g)) {
-      // the rows of this group
-      if (tid < NB) {
-        int tok, head;
-        const bool on = group_row(a, g.rt, tid, tok, head);
-        const int n = g.len - a.q_len + 1 + tok;
-        lim[tid] = on && n > 0 ? min(n, g.len) : 0;
-        row_off[tid] = on ? (static_cast<int64_t>(g.s) * a.q_len + tok) * a.o_tok + head * a.o_head : -1;
-      }
-      named_sync(1, 128);
+      int tok, head, see = 0;
+      const bool on = group_row(a, g.rt, row, tok, head) && mine;
+      const int64_t at = static_cast<int64_t>(g.s) * a.q_len + tok;
+      if (on) see = max(0, min(g.len, g.len - a.q_len + 1 + tok));
+      if (half == 0 && mine) row_off[row] = on ? at * a.o_tok + head * a.o_head : -1;
+      named_sync(1, 256);
       const bool whole = g.t0 == 0 && g.t1 == g.nt;
       if (g.len > 0) {
-#pragma unroll
-        for (int j = 0; j < NB; ++j) l[j] = 0.f;
+        float m = 0.f, l = 0.f;
         for (int t = g.t0; t < g.t1; ++t, ++i) {
-          const int pos = t * kTileTok + tid;
-          // every row sees the whole tile: lim of the first token is the least
-          const bool inside = (t + 1) * kTileTok <= g.len - a.q_len + 1;
-          uint32_t r[NB];
+          const bool first = t == g.t0;
+          uint32_t x[32];
           mbar_wait(&s_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, abort);
           __syncwarp();
           tc_fence_after();
-          tmem_ld_cols<NB>(tl + kDecScol + static_cast<uint32_t>(i & 1) * 64u, r);
-          tmem_wait_ld_of(r);
-          if (!inside) {
+          tmem_ld_cols<32>(tl + kDecScol + static_cast<uint32_t>((i & 1) * 64 + half * 32), x);
+          tmem_wait_ld_of(x);
+          if (a.flip) {
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
-              r[j] = pos < lim[j] ? __float_as_uint(__uint_as_float(r[j]) * a.c) : 0xFF800000u;
-          } else {
-#pragma unroll
-            for (int j = 0; j < NB; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * a.c);
+            for (int j = 0; j < 32; ++j) x[j] ^= 0x80000000u;
           }
-          const bool first = t == g.t0;
-          bool raise = first;
-          if (!first) {
-            float mx = -INFINITY;
+          const int j0 = t * kTileTok + half * 32;
+          if (j0 + 32 > see) {               // (also every row that pads the group)
 #pragma unroll
-            for (int j = 0; j < NB; j += 4) {
-              const float4 m = *reinterpret_cast<const float4*>(&mref[j]);
-              mx = fmaxf(mx, fmaxf(fmaxf(__uint_as_float(r[j]) - m.x, __uint_as_float(r[j + 1]) - m.y),
-                                   fmaxf(__uint_as_float(r[j + 2]) - m.z, __uint_as_float(r[j + 3]) - m.w)));
-            }
-            raise = named_sync_or(1, 128, mx > kMaxSlack);
+            for (int j = 0; j < 32; ++j)
+              if (j0 + j >= see) x[j] = 0xFF800000u;
           }
-          if (raise) {
-            float keep0 = -INFINITY, keep1 = -INFINITY;
+          float m4[4];
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-              float v = __uint_as_float(r[j]);
+          for (int e = 0; e < 4; ++e) m4[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[4 + e]));
 #pragma unroll
-              for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-              if (lane == (j & 31)) {
-                if (j < 32) keep0 = v;
-                else keep1 = v;
-              }
+          for (int j = 8; j < 32; j += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(x[j + e]), __uint_as_float(x[j + 4 + e]));
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.c;
+          if (first || named_sync_or(1, 256, mx - m > kMaxSlack)) {
+            if (mine) xch[half][row] = mx;
+            named_sync(1, 256);
+            if (mine) {
+              float mn = fmaxf(mx, xch[half ^ 1][row]);
+              if (!first) mn = fmaxf(mn, m);
+              if (mn == -INFINITY) mn = 0.f;           // a row that sees nothing here sees nothing later
+              const float f = exp2_fast(m - mn);
+              if (half == 0) fac[row] = f;
+              l *= f;
+              m = mn;
             }
-            if (lane < NB) colmax[w][lane] = keep0;
-            if (NB > 32) colmax[w][32 + lane] = keep1;
-            named_sync(1, 128);
-            if (tid < NB) {
-              float m = fmaxf(fmaxf(colmax[0][tid], colmax[1][tid]), fmaxf(colmax[2][tid], colmax[3][tid]));
-              if (!first) m = fmaxf(m, mref[tid]);
-              if (m == -INFINITY) m = 0.f;           // a row that sees nothing here sees nothing later
-              fac[tid] = first ? 0.f : exp2_fast(mref[tid] - m);
-              mref[tid] = m;
-            }
-            named_sync(1, 128);
+            named_sync(1, 256);
             if (!first) {
               mbar_wait(&pv_done, static_cast<uint32_t>(i - 1) & 1u, abort);
               __syncwarp();
               tc_fence_after();
-              for (int k = 0; k < nk; ++k) {
+              for (int k = kb0; k < kb1; ++k) {
 #pragma unroll
                 for (int j = 0; j < NB; j += 16) {
                   uint32_t o[16];
@@ -536,96 +459,62 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 }
               }
               tmem_wait_st();
-#pragma unroll
-              for (int j = 0; j < NB; ++j) l[j] *= fac[j];
             }
           }
-          // weights, their sums, and the tile P^T (fp32 sums of the unrounded
-          // weights; the weights themselves are rounded to bf16 for the MMA)
+          // weights (rounded to bf16 for the MMA) and their fp32 sum (unrounded)
+          uint32_t p[16];
+          const uint64_t c2 = pair2f(a.c, a.c), m2 = pair2f(-m, -m);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int j = 0; j < NB; j += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(&mref[j]);
-            const float mm[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float p = exp2_fast(__uint_as_float(r[j + e]) - mm[e]);
-              l[j + e] += p;
-              r[j + e] = __float_as_uint(p);
-            }
+          for (int j = 0; j < 16; ++j) {
+            float x0, x1;
+            split2(fma2(pair2(x[2 * j], x[2 * j + 1]), c2, m2), x0, x1);
+            x0 = exp2_fast(x0);
+            x1 = exp2_fast(x1);
+            sum[j & 1] = add2(sum[j & 1], pair2f(x0, x1));
+            p[j] = pack_bf16x2(x0, x1);
           }
+          float s0, s1;
+          split2(add2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
           if (i > 0) {
+            // the product before has read its weights
             mbar_wait(&pv_done, static_cast<uint32_t>(i - 1) & 1u, abort);
             __syncwarp();
           }
-          uint8_t* prow = psm + tid * 128;
+          if (mine) {
+            uint8_t* prow = psm + row * 128;
 #pragma unroll
-          for (int ch = 0; ch < NB / 8; ++ch) {
-            const uint32_t* v = &r[8 * ch];
-            *reinterpret_cast<uint4*>(prow + ((ch ^ (tid & 7)) << 4)) =
-                make_uint4(pack_bf16x2(__uint_as_float(v[0]), __uint_as_float(v[1])),
-                           pack_bf16x2(__uint_as_float(v[2]), __uint_as_float(v[3])),
-                           pack_bf16x2(__uint_as_float(v[4]), __uint_as_float(v[5])),
-                           pack_bf16x2(__uint_as_float(v[6]), __uint_as_float(v[7])));
+            for (int ch = 0; ch < 4; ++ch)
+              *reinterpret_cast<uint4*>(prow + (((half * 4 + ch) ^ (row & 7)) << 4)) =
+                  make_uint4(p[4 * ch], p[4 * ch + 1], p[4 * ch + 2], p[4 * ch + 3]);
           }
           fence_proxy_async_smem();
           tc_fence_before();
           mbar_arrive(&p_full[i & 1]);
         }
-        // sums over the 128 positions of each thread's share: halves of the
-        // columns change hands until a lane holds its own
-        {
-          int n = NB / 2, o = 16;
-#pragma unroll
-          for (; n >= 1 && o >= 1; n >>= 1, o >>= 1) {
-            const bool up = (lane & o) != 0;
-#pragma unroll
-            for (int j = 0; j < NB / 2; ++j) {
-              if (j < n) {
-                const float give = up ? l[j] : l[j + n], have = up ? l[j + n] : l[j];
-                l[j] = have + __shfl_xor_sync(0xFFFFFFFFu, give, o);
-              }
-            }
-          }
-#pragma unroll
-          for (; o >= 1; o >>= 1) l[0] += __shfl_xor_sync(0xFFFFFFFFu, l[0], o);
-        }
-        if (NB == 64) {
-          colmax[w][2 * lane] = l[0];
-          colmax[w][2 * lane + 1] = l[1];
-        } else if (NB == 32) {
-          colmax[w][lane] = l[0];
-        } else if ((lane & 1) == 0) {
-          colmax[w][lane >> 1] = l[0];
-        }
-        named_sync(1, 128);
+        named_sync(1, 256);                  // fac and xch are free
+        if (mine) xch[half][row] = l;
+        named_sync(1, 256);
         float* part = a.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (g.t0 == 0 ? 1 : 0)) * part_floats(NB, a.L);
-        if (tid < NB) {
-          const float sum = (colmax[0][tid] + colmax[1][tid]) + (colmax[2][tid] + colmax[3][tid]);
+        if (half == 0 && mine) {
+          const float sum = xch[0][row] + xch[1][row];
           if (whole) {
-            fac[tid] = sum == 0.f ? 0.f : 1.0f / sum;
-            if (a.lse != nullptr && row_off[tid] >= 0) {
-              int tok, head;
-              group_row(a, g.rt, tid, tok, head);
-              a.lse[(static_cast<int64_t>(g.s) * a.q_len + tok) * a.H + head] =
-                  sum == 0.f ? -INFINITY : (mref[tid] + log2_fast(sum)) * kLn2;
-            }
-          } else if (row_off[tid] >= 0) {
-            part[static_cast<int64_t>(NB) * a.L + tid] = sum == 0.f ? -INFINITY : mref[tid];
-            part[static_cast<int64_t>(NB) * a.L + NB + tid] = sum;
+            fac[row] = sum == 0.f ? 0.f : 1.0f / sum;
+            if (a.lse != nullptr && on) a.lse[at * a.H + head] = sum == 0.f ? -INFINITY : (m + log2_fast(sum)) * kLn2;
+          } else if (on) {
+            part[static_cast<int64_t>(NB) * a.L + row] = sum == 0.f ? -INFINITY : m;
+            part[static_cast<int64_t>(NB) * a.L + NB + row] = sum;
           }
         }
-        named_sync(1, 128);
+        named_sync(1, 256);
         mbar_wait(&pv_done, static_cast<uint32_t>(i - 1) & 1u, abort);
         __syncwarp();
         tc_fence_after();
-        for (int k = 0; k < nk; ++k) {
+        for (int k = kb0; k < kb1; ++k) {
           uint32_t o[NB];
           tmem_ld_cols<NB>(tl + k * 64, o);
           tmem_wait_ld_of(o);
-          if (k == nk - 1) {
-            tc_fence_before();
-            mbar_arrive(&o_empty);
-          }
           const int d = k * 128 + w * 32 + lane;
           if (whole) {
             // two rows per pass: lane pairs swap a value so that each lane
@@ -647,20 +536,18 @@ __global__ void __launch_bounds__(kDecThreads, 1)
               if (row_off[j] >= 0) part[static_cast<int64_t>(j) * a.L + d] = __uint_as_float(o[j]);
           }
         }
+        tc_fence_before();
+        mbar_arrive(&o_empty);
       } else {
         // an empty sequence: its rows are zero, their log-sum -inf
         for (int j = 0; j < NB; ++j) {
           if (row_off[j] < 0) continue;
-          for (int d = tid * 8; d < a.L; d += 128 * 8)
+          for (int d = tid * 8; d < a.L; d += 256 * 8)
             *reinterpret_cast<uint4*>(a.out + row_off[j] + d) = make_uint4(0, 0, 0, 0);
-          if (a.lse != nullptr && tid == 0) {
-            int tok, head;
-            group_row(a, g.rt, j, tok, head);
-            a.lse[(static_cast<int64_t>(g.s) * a.q_len + tok) * a.H + head] = -INFINITY;
-          }
         }
+        if (half == 0 && on && a.lse != nullptr) a.lse[at * a.H + head] = -INFINITY;
       }
-      named_sync(1, 128);                    // the row tables are rewritten next
+      named_sync(1, 256);                    // the row table is rewritten next
     }
   }
   if (abort) atomicOr(&g_mla_decode_error, kErrTimeout);
@@ -678,18 +565,39 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 constexpr int kCombThreads = 512;
 
 __global__ void __launch_bounds__(kCombThreads) mla_combine_kernel(const DecodeArgs a, int grid, int NB, int rows) {
-  __shared__ int64_t red64[64];
+  __shared__ int64_t sums[2][kCombThreads / 32];
   __shared__ float wsum[4][kMlaMaxLatent];
   __shared__ float lsum[4];
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int group = blockIdx.x, s = group / a.RT, rt = group % a.RT;
-  int64_t before, total;
-  unit_sums(a, s, red64, before, total);     // seq_lens: complete before the kernel ahead let this one start
+  // units before this sequence and of all (seq_lens: complete before the
+  // kernel ahead let this one start)
+  int64_t before = 0, total = 0;
+  for (int i = threadIdx.x; i < a.S; i += kCombThreads) {
+    const int64_t u = group_units(seq_len(a, i));
+    total += u;
+    if (i < s) before += u;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+    total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    sums[0][threadIdx.x >> 5] = before;
+    sums[1][threadIdx.x >> 5] = total;
+  }
+  __syncthreads();
+  before = total = 0;
+  for (int w = 0; w < kCombThreads / 32; ++w) {
+    before += sums[0][w];
+    total += sums[1][w];
+  }
   const int units = group_units(seq_len(a, s));
-  const int64_t u0 = before + static_cast<int64_t>(rt) * units, u1 = u0 + units;
-  // owner(u): the block c whose stretch [c total / n, (c + 1) total / n) holds u
-  const int64_t n = min(static_cast<int64_t>(grid), total);
-  const int c0 = static_cast<int>(((u0 + 1) * n - 1) / total), c1 = static_cast<int>((u1 * n - 1) / total);
+  const int64_t u0 = before * a.RT + static_cast<int64_t>(rt) * units;
+  int n;
+  const Cut cut(total * a.RT, grid, n);
+  const int c0 = cut.owner(u0), c1 = cut.owner(u0 + units - 1);
   griddep_wait();                            // (every block: the grid must not end before the one ahead)
   if (c0 == c1) return;                      // not cut: written by its block
   const int64_t pf = part_floats(NB, a.L);
@@ -791,12 +699,12 @@ static cudaError_t launch_decode_nb(const CUtensorMap (&maps)[3], DecodeArgs a, 
     if (e != cudaSuccess) return e;
     g_decode_attr[kIdx][dev.device].store(true, std::memory_order_release);
   }
-  // ring stages that fit beside the queries, the weights and two rotated-key tiles
-  const int fixed = 3 * kChunkBytes + (a.L / 64 + 1) * NB * 128 + 1024;
-  int st = (kDecSmem - 4096 - fixed) / kDecStageBytes;
-  if (st > kDecMaxStages) st = kDecMaxStages;
-  a.stages = st;
-  return mla_launch(kern, dim3(static_cast<unsigned>(grid)), kDecThreads, fixed + st * kDecStageBytes, s, maps[0],
+  // tiles that fit beside the queries and the weights
+  const int chunks = a.L / 64 + 1;
+  const int fixed = (chunks + 1) * NB * 128 + 1024, tile = chunks * kChunkBytes;
+  a.bufs = (kDecSmem - kDecStatic - fixed) / tile;
+  if (a.bufs > kDecMaxBufs) a.bufs = kDecMaxBufs;
+  return mla_launch(kern, dim3(static_cast<unsigned>(grid)), kDecThreads, fixed + a.bufs * tile, s, maps[0],
                     maps[1], maps[2], a);
 }
 
@@ -829,7 +737,8 @@ cudaError_t launch_mla_decode(const MlaDecodeProblem& p, const DeviceInfo& dev, 
   a.TPT = r.TPT;
   a.head_blocks = r.head_blocks;
   a.RT = r.RT;
-  a.c = p.scale * kLog2e;
+  a.flip = p.scale < 0.f;
+  a.c = positive_scale(a.flip ? -p.scale : p.scale);
 
   CUtensorMap maps[3];
   const int64_t T = static_cast<int64_t>(p.S) * p.q_len;

@@ -145,10 +145,10 @@ def test_refusals_of_each(capi):
 
 def test_workspace_query(capi):
     q = capi.mxfp4_mla_decode_workspace_bytes
-    assert q(4, 1, 64, 512, 128) == 0 and q(0, 1, 64, 512, 4096) == 0 and q(4, 1, 64, 0, 4096) == 0
-    assert q(4, 1, 64, 512, 129) > 0
+    assert q(4, 1, 64, 512, 64) == 0 and q(0, 1, 64, 512, 4096) == 0 and q(4, 1, 64, 0, 4096) == 0
+    assert q(4, 1, 64, 512, 65) > 0
     part = 64 * (512 + 2) * 4
-    assert q(1, 1, 64, 512, 256) == 2 * 2 * part                  # two tiles: two blocks, two parts each
+    assert q(1, 1, 64, 512, 128) == 2 * 2 * part                  # two tiles: two blocks, two parts each
     assert q(1000, 4, 128, 512, 10 ** 6) <= 256 * 2 * part        # bounded by the grid
     assert q(1, 1, 8, 512, 10 ** 6) < q(1, 1, 64, 512, 10 ** 6)   # fewer rows, smaller parts
 
