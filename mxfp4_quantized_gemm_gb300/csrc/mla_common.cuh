@@ -84,6 +84,10 @@ __device__ __forceinline__ void drain_mmas(uint64_t* bar, bool abort) {
   __syncwarp();
 }
 
+__device__ __forceinline__ void prefetch_tensor_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // One box of a 3-D tensor map -> shared memory, completion counted on `bar`.
 __device__ __forceinline__ void tma_box_3d(void* smem_dst, const CUtensorMap* map, int c0, int c1, int c2,
                                            uint64_t* bar) {

@@ -26,7 +26,8 @@
 // 2^8 (first tile aside), which one barrier with an OR decides.
 // A copying warp spends about 430 cycles on each wait, arrival and copy and
 // 16 on each further copy, so a tile comes in two groups, each under one
-// barrier: the first half of the latent, and the rest with the rotated key.
+// barrier: all but the last 128 latent values, and those with the rotated key
+// (so that little is left to multiply when the last of a tile lands).
 //
 // Work split: the tiles of all row groups, in order, are cut evenly over the
 // grid; a block takes its stretch wherever sequences begin and end, so a
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int nk = a.L >> 7;                                  // 128-value blocks of the latent
   const int chunks = 2 * nk + 1;                            // 64-value chunks of a cache row
-  const int na = 2 * ((nk + 1) >> 1);                       // those of a tile's first group
+  const int na = nk > 1 ? 2 * (nk - 1) : 2;                 // those of a tile's first group
   const int tile_bytes = chunks * kChunkBytes;
   // the 64-row score MMA reads 64 rows of a query chunk whatever NB is: the
   // queries lie in front, so that what it reads past them is inside the buffer
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     mbar_init(&o_empty, 256);
     fence_mbar_init();
   }
+  if (warp == 0 && lane < 3) prefetch_tensor_map(lane == 0 ? &qmap : (lane == 1 ? &rmap : &cmap));
   if (warp == 1) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     int i = 0;
     Segment g;
     while (walk.next(a, g)) {
-      int tok, head, see = 0;
+      int tok, head, see = mine ? 0 : 0x7FFFFFFF;
       const bool on = group_row(a, g.rt, row, tok, head) && mine;
       const int64_t at = static_cast<int64_t>(g.s) * a.q_len + tok;
       if (on) see = max(0, min(g.len, g.len - a.q_len + 1 + tok));
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             for (int j = 0; j < 32; ++j) x[j] ^= 0x80000000u;
           }
           const int j0 = t * kTileTok + half * 32;
-          if (j0 + 32 > see) {               // (also every row that pads the group)
+          if (j0 + 32 > see) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (j0 + j >= see) x[j] = 0xFF800000u;
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           for (int j = 8; j < 32; j += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(x[j + e]), __uint_as_float(x[j + 4 + e]));
-          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.c;
+          const float mx = mine ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.c : -INFINITY;
           if (first || named_sync_or(1, 256, mx - m > kMaxSlack)) {
             if (mine) xch[half][row] = mx;
             named_sync(1, 256);
@@ -515,6 +517,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           uint32_t o[NB];
           tmem_ld_cols<NB>(tl + k * 64, o);
           tmem_wait_ld_of(o);
+          if (k + 1 == kb1) {
+            tc_fence_before();
+            mbar_arrive(&o_empty);
+          }
           const int d = k * 128 + w * 32 + lane;
           if (whole) {
             // two rows per pass: lane pairs swap a value so that each lane
@@ -531,13 +537,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 *reinterpret_cast<uint32_t*>(a.out + off + (d & ~1)) = odd ? pack_bf16x2(got, x1) : pack_bf16x2(x0, got);
             }
           } else {
+            // (rows that pad the group too: nothing reads them)
+            float* dst = part + d;
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
-              if (row_off[j] >= 0) part[static_cast<int64_t>(j) * a.L + d] = __uint_as_float(o[j]);
+            for (int j = 0; j < NB; ++j, dst += a.L) *dst = __uint_as_float(o[j]);
           }
         }
-        tc_fence_before();
-        mbar_arrive(&o_empty);
+        if (kb0 == kb1) mbar_arrive(&o_empty);
       } else {
         // an empty sequence: its rows are zero, their log-sum -inf
         for (int j = 0; j < NB; ++j) {
@@ -559,17 +565,20 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
 // ------------------------------------------------------------------ joining
 // out[r] = sum_p 2^(m_p - M) O_p[r] / sum_p 2^(m_p - M) l_p over the parts p
-// of a row group that was cut between blocks, in block order (the result
-// does not depend on timing).  One block per group and `rows` rows; four
-// groups of 128 threads (four values each, L <= 512) share out the parts.
+// of a row group that was cut between blocks (the order of the sums depends
+// on the shape alone).  A unit of work is a row's 128 latent values: `warps`
+// warps share its parts out (lane = four values) and meet in shared memory;
+// a block of 16 warps takes 16 / warps units.  Bound by the latency of the
+// parts' loads (L2), so all of a warp's loads go out together.
 constexpr int kCombThreads = 512;
 
-__global__ void __launch_bounds__(kCombThreads) mla_combine_kernel(const DecodeArgs a, int grid, int NB, int rows) {
+__global__ void __launch_bounds__(kCombThreads) mla_combine_kernel(const DecodeArgs a, int grid, int NB, int warps) {
   __shared__ int64_t sums[2][kCombThreads / 32];
-  __shared__ float wsum[4][kMlaMaxLatent];
-  __shared__ float lsum[4];
+  __shared__ __align__(16) float4 acc_s[16][32];
+  __shared__ float2 ml_s[16];
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int group = blockIdx.x, s = group / a.RT, rt = group % a.RT;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // units before this sequence and of all (seq_lens: complete before the
   // kernel ahead let this one start)
   int64_t before = 0, total = 0;
@@ -583,9 +592,9 @@ __global__ void __launch_bounds__(kCombThreads) mla_combine_kernel(const DecodeA
     before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
     total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
   }
-  if ((threadIdx.x & 31) == 0) {
-    sums[0][threadIdx.x >> 5] = before;
-    sums[1][threadIdx.x >> 5] = total;
+  if (lane == 0) {
+    sums[0][warp] = before;
+    sums[1][warp] = total;
   }
   __syncthreads();
   before = total = 0;
@@ -600,52 +609,80 @@ __global__ void __launch_bounds__(kCombThreads) mla_combine_kernel(const DecodeA
   const int c0 = cut.owner(u0), c1 = cut.owner(u0 + units - 1);
   griddep_wait();                            // (every block: the grid must not end before the one ahead)
   if (c0 == c1) return;                      // not cut: written by its block
-  const int64_t pf = part_floats(NB, a.L);
-  const int tg = threadIdx.x >> 7, x = threadIdx.x & 127;
-  auto part = [&](int c) { return a.parts + (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * pf; };
-  for (int j = blockIdx.y * rows; j < min(NB, static_cast<int>(blockIdx.y + 1) * rows); ++j) {
-    int tok, head;
-    if (!group_row(a, rt, j, tok, head)) continue;
-    const int64_t mo = static_cast<int64_t>(NB) * a.L + j;
-    float M = -INFINITY;
-    for (int c = c0; c <= c1; ++c) M = fmaxf(M, part(c)[mo]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f;
-#pragma unroll 4
-    for (int c = c0 + tg; c <= c1; c += 4) {
-      const float* p = part(c);
-      const float lp = p[mo + NB];
-      const float wgt = exp2_fast(p[mo] - ref);
-      const float4 v = 4 * x < a.L ? *reinterpret_cast<const float4*>(p + static_cast<int64_t>(j) * a.L + 4 * x)
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-      if (lp != 0.f) {                       // a part whose positions this row does not see
-        l += wgt * lp;
-        acc[0] += wgt * v.x;
-        acc[1] += wgt * v.y;
-        acc[2] += wgt * v.z;
-        acc[3] += wgt * v.w;
+  const int nk = a.L >> 7, per = 16 / warps; // units a block takes at a time
+  const int team = warp / warps, member = warp % warps;
+  const int unit = blockIdx.y * per + team;
+  const int j = unit / nk, k = unit % nk;    // row and 128-value block
+  int tok = 0, head = 0;
+  const bool on = j < NB && group_row(a, rt, j, tok, head);
+  float M = -INFINITY, l = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (on) {
+    const int64_t pf = part_floats(NB, a.L);
+    // the part of block c: the one it begins the group with, or goes on with
+    const float* base = a.parts + static_cast<int64_t>(j) * a.L + k * 128 + lane * 4;
+    const float* stat = a.parts + static_cast<int64_t>(NB) * a.L + j;
+    constexpr int kBatch = 8;
+    for (int c = c0 + member; c <= c1; c += kBatch * warps) {
+      float4 o[kBatch];
+      float m[kBatch], ls[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int ci = c + i * warps;
+        const int64_t at = (static_cast<int64_t>(ci) * 2 + (ci == c0 ? 1 : 0)) * pf;
+        const bool in = ci <= c1;
+        m[i] = in ? stat[at] : -INFINITY;
+        ls[i] = in ? stat[at + NB] : 0.f;
+        o[i] = in ? *reinterpret_cast<const float4*>(base + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float Mn = M;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) Mn = fmaxf(Mn, m[i]);
+      const float ref = Mn == -INFINITY ? 0.f : Mn, f = exp2_fast(M - ref);
+      l *= f;
+      v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+      M = Mn;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (ls[i] == 0.f) continue;          // no part, or one whose positions this row does not see
+        const float wgt = exp2_fast(m[i] - ref);
+        l += wgt * ls[i];
+        v.x += wgt * o[i].x;
+        v.y += wgt * o[i].y;
+        v.z += wgt * o[i].z;
+        v.w += wgt * o[i].w;
       }
     }
-    if (x == 0) lsum[tg] = l;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) wsum[tg][4 * x + e] = acc[e];
-    __syncthreads();
-    const float lt = (lsum[0] + lsum[1]) + (lsum[2] + lsum[3]);
-    if (tg == 0 && 4 * x < a.L) {
-      float o[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float v = (wsum[0][4 * x + e] + wsum[1][4 * x + e]) + (wsum[2][4 * x + e] + wsum[3][4 * x + e]);
-        o[e] = lt == 0.f ? 0.f : v / lt;
-      }
-      __nv_bfloat16* dst = a.out + (static_cast<int64_t>(s) * a.q_len + tok) * a.o_tok + head * a.o_head + 4 * x;
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-      if (x == 0 && a.lse != nullptr)
-        a.lse[(static_cast<int64_t>(s) * a.q_len + tok) * a.H + head] =
-            lt == 0.f ? -INFINITY : (M + log2_fast(lt)) * kLn2;
-    }
-    __syncthreads();
   }
+  if (warps > 1) {
+    acc_s[warp][lane] = v;
+    if (lane == 0) ml_s[warp] = make_float2(M, l);
+    __syncthreads();
+    if (member != 0) return;
+    float Mt = M;
+    for (int w = 1; w < warps; ++w) Mt = fmaxf(Mt, ml_s[warp + w].x);
+    const float ref = Mt == -INFINITY ? 0.f : Mt, f = exp2_fast(M - ref);
+    l *= f;
+    v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+    for (int w = 1; w < warps; ++w) {
+      const float2 ml = ml_s[warp + w];
+      if (ml.y == 0.f) continue;
+      const float wgt = exp2_fast(ml.x - ref);
+      const float4 o = acc_s[warp + w][lane];
+      l += wgt * ml.y;
+      v.x += wgt * o.x;
+      v.y += wgt * o.y;
+      v.z += wgt * o.z;
+      v.w += wgt * o.w;
+    }
+    M = Mt;
+  }
+  if (!on) return;
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  const int64_t at = static_cast<int64_t>(s) * a.q_len + tok;
+  *reinterpret_cast<uint2*>(a.out + at * a.o_tok + head * a.o_head + k * 128 + lane * 4) =
+      l == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+  if (k == 0 && lane == 0 && a.lse != nullptr) a.lse[at * a.H + head] = l == 0.f ? -INFINITY : (M + log2_fast(l)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host
@@ -756,12 +793,14 @@ cudaError_t launch_mla_decode(const MlaDecodeProblem& p, const DeviceInfo& dev, 
                  : (r.NB == 32 ? launch_decode_nb<32>(maps, a, grid, dev, s)
                                : launch_decode_nb<64>(maps, a, grid, dev, s));
   if (e != cudaSuccess || a.capacity <= kTileTok) return e;
-  // rows per joining block: enough blocks for a few per SM
+  // warps that share a row's parts out: for the parts of a group that the
+  // grid cuts on average, eight to a warp
   const int64_t groups = static_cast<int64_t>(p.S) * r.RT;
-  int rows = static_cast<int>(groups * r.NB / (4 * dev.sm_count));
-  rows = rows < 1 ? 1 : (rows > 16 ? 16 : rows);
-  return mla_launch(mla_combine_kernel, dim3(static_cast<unsigned>(groups), static_cast<unsigned>(ceil_div(r.NB, rows))),
-                    kCombThreads, 0, s, a, grid, r.NB, rows);
+  int warps = 1;
+  while (warps < 16 && static_cast<int64_t>(warps) * 8 * groups < grid + groups) warps *= 2;
+  const int units = r.NB * (p.L / 128), per = 16 / warps;
+  return mla_launch(mla_combine_kernel, dim3(static_cast<unsigned>(groups), static_cast<unsigned>(ceil_div(units, per))),
+                    kCombThreads, 0, s, a, grid, r.NB, warps);
 }
 
 uint32_t mla_decode_read_clear_error() { return read_clear_word(g_mla_decode_error); }
