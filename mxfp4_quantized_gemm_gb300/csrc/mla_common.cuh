@@ -194,6 +194,16 @@ __device__ __forceinline__ bool named_sync_or(int id, int threads, bool pred) {
   return r != 0;
 }
 
+// A predicated 4-byte store (no branch in a run of them).
+__device__ __forceinline__ void st_global_if(void* p, uint32_t v, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.u32 q, %2, 0;\n\t"
+      "@q st.global.b32 [%0], %1;\n\t}" ::"l"(p),
+      "r"(v), "r"(static_cast<uint32_t>(on))
+      : "memory");
+}
+
 // Zeroes 16-byte chunks of rows [row0, row1) of a 128-byte-row tile, by one
 // warp (whole rows: the swizzle permutes chunks within a row).
 __device__ __forceinline__ void zero_rows(uint8_t* tile, int row0, int row1, int lane) {

@@ -22,7 +22,9 @@
 // Roles: warp 0 copies, warp 1 issues the score products, warp 2 the output
 // products; warps 4..7 and 8..11 hold the softmax: thread = (row, half of the
 // tile's positions), in the lanes where a 64-row MMA leaves its rows (16 of
-// each 32).  A row's running maximum is raised only when a score passes it by
+// each 32); warps 12..15 write a finished accumulator out while the softmax
+// is at the next stretch (131 KB of fp32 for a part: done by the softmax warps
+// it stood for 17000 cycles between two stretches, four tiles' worth).  A row's running maximum is raised only when a score passes it by
 // 2^8 (first tile aside), which one barrier with an OR decides.
 // A copying warp spends about 430 cycles on each wait, arrival and copy and
 // 16 on each further copy, so a tile comes in two groups, each under one
@@ -45,7 +47,7 @@ namespace mx {
 
 static __device__ uint32_t g_mla_decode_error;
 
-constexpr int kDecThreads = 384;
+constexpr int kDecThreads = 512;
 constexpr int kTileTok = 64;                        // positions per tile
 constexpr int kChunkBytes = kTileTok * 128;         // 64 positions x 64 values
 constexpr int kDecMaxBufs = 4;
@@ -186,6 +188,11 @@ __host__ __device__ __forceinline__ int64_t part_floats(int rows, int L) {
   return static_cast<int64_t>(rows) * (L + 2);
 }
 
+// The part that block c leaves of the group it begins, or goes on with.
+__device__ __forceinline__ float* part_of(const DecodeArgs& a, int rows, int c, bool begins) {
+  return a.parts + (static_cast<int64_t>(c) * 2 + (begins ? 1 : 0)) * part_floats(rows, a.L);
+}
+
 // Row j of a row group: its token and head; false for rows that pad the group.
 __device__ __forceinline__ bool group_row(const DecodeArgs& a, int rt, int j, int& tok, int& head) {
   const int ti = j / a.HB;
@@ -212,11 +219,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   constexpr int kQChunk = NB * 128;
 
   __shared__ __align__(8) uint64_t full[2][kDecMaxBufs], empty[2][kDecMaxBufs];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], q_full, pv_done, o_empty, drain[2];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], q_full, pv_done, o_full, o_empty, fin_full, drain[2];
   __shared__ uint32_t tmem_slot;
   __shared__ __align__(16) float fac[64];
   __shared__ float xch[2][64];
-  __shared__ int64_t row_off[NB];
+  // 1 / sum of a finished stretch's rows, for the warps that write it out (by
+  // the stretch's number's parity)
+  __shared__ __align__(16) float fin[2][NB];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   bool abort = false;
@@ -233,7 +242,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     mbar_init(&q_full, 1);
     mbar_init(&pv_done, 1);
-    mbar_init(&o_empty, 256);
+    mbar_init(&o_full, 1);
+    mbar_init(&o_empty, 128);
+    mbar_init(&fin_full, 256);
     fence_mbar_init();
   }
   if (warp == 0 && lane < 3) prefetch_tensor_map(lane == 0 ? &qmap : (lane == 1 ? &rmap : &cmap));
@@ -379,30 +390,29 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           }
           mma_commit(&empty[1][r.slot]);
           mma_commit(&pv_done);
+          if (t + 1 == g.t1) mma_commit(&o_full);
         }
         __syncwarp();
         r.step();
       }
     }
     drain_mmas(&drain[1], abort);
-  } else if (warp >= 4) {
-    // ---- softmax and output.  These threads meet at named barriers, so they
-    // walk every tile even after a wait has given up.  A 64-row MMA leaves row
-    // 16 w + x in lane 32 w + x (x < 16); the other lanes only keep company.
+  } else if (warp >= 4 && warp < 12) {
+    // ---- softmax.  These threads meet at named barriers, so they walk every
+    // tile even after a wait has given up.  A 64-row MMA leaves row 16 w + x in
+    // lane 32 w + x (x < 16); the other lanes only keep company.
     const int w = warp & 3, half = (warp - 4) >> 2, tid = threadIdx.x - 128;
     const int row = 16 * w + (lane & 15);
     const bool mine = lane < 16 && row < NB;
     const uint32_t tl = tmem + (static_cast<uint32_t>(w * 32) << 16);
     const int kb0 = half == 0 ? 0 : (nk + 1) >> 1, kb1 = half == 0 ? (nk + 1) >> 1 : nk;   // this half's latent blocks
-    int i = 0;
+    int i = 0, seg_no = 0;
     Segment g;
     while (walk.next(a, g)) {
       int tok, head, see = mine ? 0 : 0x7FFFFFFF;
       const bool on = group_row(a, g.rt, row, tok, head) && mine;
       const int64_t at = static_cast<int64_t>(g.s) * a.q_len + tok;
       if (on) see = max(0, min(g.len, g.len - a.q_len + 1 + tok));
-      if (half == 0 && mine) row_off[row] = on ? at * a.o_tok + head * a.o_head : -1;
-      named_sync(1, 256);
       const bool whole = g.t0 == 0 && g.t1 == g.nt;
       if (g.len > 0) {
         float m = 0.f, l = 0.f;
@@ -449,8 +459,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
               mbar_wait(&pv_done, static_cast<uint32_t>(i - 1) & 1u, abort);
               __syncwarp();
               tc_fence_after();
+#pragma unroll 1
               for (int k = kb0; k < kb1; ++k) {
-#pragma unroll
+#pragma unroll 1
                 for (int j = 0; j < NB; j += 16) {
                   uint32_t o[16];
                   tmem_ld16(tl + k * 64 + j, o);
@@ -495,65 +506,91 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           tc_fence_before();
           mbar_arrive(&p_full[i & 1]);
         }
-        named_sync(1, 256);                  // fac and xch are free
+        named_sync(1, 256);                  // xch is free
         if (mine) xch[half][row] = l;
         named_sync(1, 256);
-        float* part = a.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (g.t0 == 0 ? 1 : 0)) * part_floats(NB, a.L);
         if (half == 0 && mine) {
           const float sum = xch[0][row] + xch[1][row];
+          fin[seg_no & 1][row] = sum == 0.f ? 0.f : 1.0f / sum;
           if (whole) {
-            fac[row] = sum == 0.f ? 0.f : 1.0f / sum;
             if (a.lse != nullptr && on) a.lse[at * a.H + head] = sum == 0.f ? -INFINITY : (m + log2_fast(sum)) * kLn2;
           } else if (on) {
-            part[static_cast<int64_t>(NB) * a.L + row] = sum == 0.f ? -INFINITY : m;
-            part[static_cast<int64_t>(NB) * a.L + NB + row] = sum;
+            float* part = part_of(a, NB, blockIdx.x, g.t0 == 0) + static_cast<int64_t>(NB) * a.L;
+            part[row] = sum == 0.f ? -INFINITY : m;
+            part[NB + row] = sum;
           }
         }
-        named_sync(1, 256);
-        mbar_wait(&pv_done, static_cast<uint32_t>(i - 1) & 1u, abort);
-        __syncwarp();
-        tc_fence_after();
-        for (int k = kb0; k < kb1; ++k) {
-          uint32_t o[NB];
-          tmem_ld_cols<NB>(tl + k * 64, o);
+        mbar_arrive(&fin_full);
+        ++seg_no;
+      } else {
+        // an empty sequence: its rows are zero, their log-sum -inf
+        for (int j = 0; j < NB; ++j) {
+          int tj, hj;
+          if (!group_row(a, g.rt, j, tj, hj)) continue;
+          __nv_bfloat16* dst = a.out + (static_cast<int64_t>(g.s) * a.q_len + tj) * a.o_tok + hj * a.o_head;
+          for (int d = tid * 8; d < a.L; d += 256 * 8) *reinterpret_cast<uint4*>(dst + d) = make_uint4(0, 0, 0, 0);
+        }
+        if (half == 0 && on && a.lse != nullptr) a.lse[at * a.H + head] = -INFINITY;
+      }
+    }
+  } else if (warp >= 12) {
+    // ---- finished accumulators: latent value 128 k + 32 w + lane of all rows
+    const int w = warp & 3;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(w * 32) << 16);
+    constexpr int kCols = NB < 32 ? NB : 32;
+    int seg_no = 0;
+    Segment g;
+    while (walk.next_real(a, g)) {
+      const int par = seg_no & 1;
+      mbar_wait(&fin_full, static_cast<uint32_t>(par), abort);
+      mbar_wait(&o_full, static_cast<uint32_t>(par), abort);
+      __syncwarp();
+      tc_fence_after();
+      const bool whole = g.t0 == 0 && g.t1 == g.nt;
+      float* part = whole ? nullptr : part_of(a, NB, blockIdx.x, g.t0 == 0);
+      // where rows lane and 32 + lane go (-1: nowhere)
+      int64_t off[NB > 32 ? 2 : 1];
+#pragma unroll
+      for (int x = 0; x < (NB > 32 ? 2 : 1); ++x) {
+        int tok, head;
+        off[x] = x * 32 + lane < NB && group_row(a, g.rt, x * 32 + lane, tok, head)
+                     ? (static_cast<int64_t>(g.s) * a.q_len + tok) * a.o_tok + head * a.o_head
+                     : -1;
+      }
+#pragma unroll 1
+      for (int k = 0; k < nk; ++k) {
+        const int d = k * 128 + w * 32 + lane;
+#pragma unroll
+        for (int j0 = 0; j0 < NB; j0 += kCols) {
+          uint32_t o[kCols];
+          tmem_ld_cols<kCols>(tl + k * 64 + j0, o);
           tmem_wait_ld_of(o);
-          if (k + 1 == kb1) {
+          if (k + 1 == nk && j0 + kCols == NB) {
             tc_fence_before();
             mbar_arrive(&o_empty);
           }
-          const int d = k * 128 + w * 32 + lane;
           if (whole) {
             // two rows per pass: lane pairs swap a value so that each lane
             // stores two neighbouring ones
 #pragma unroll
-            for (int j = 0; j < NB; j += 2) {
-              const float f0 = fac[j], f1 = fac[j + 1];
+            for (int j = 0; j < kCols; j += 2) {
+              const float f0 = fin[par][j0 + j], f1 = fin[par][j0 + j + 1];
               const float x0 = f0 == 0.f ? 0.f : __uint_as_float(o[j]) * f0;
               const float x1 = f1 == 0.f ? 0.f : __uint_as_float(o[j + 1]) * f1;
               const bool odd = (lane & 1) != 0;
               const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? x0 : x1, 1);
-              const int64_t off = row_off[j + (odd ? 1 : 0)];
-              if (off >= 0)
-                *reinterpret_cast<uint32_t*>(a.out + off + (d & ~1)) = odd ? pack_bf16x2(got, x1) : pack_bf16x2(x0, got);
+              const int64_t to = __shfl_sync(0xFFFFFFFFu, off[j0 >> 5], (j0 + j + (lane & 1)) & 31);
+              st_global_if(a.out + to + (d & ~1), odd ? pack_bf16x2(got, x1) : pack_bf16x2(x0, got), to >= 0);
             }
           } else {
             // (rows that pad the group too: nothing reads them)
-            float* dst = part + d;
+            float* dst = part + static_cast<int64_t>(j0) * a.L + d;
 #pragma unroll
-            for (int j = 0; j < NB; ++j, dst += a.L) *dst = __uint_as_float(o[j]);
+            for (int j = 0; j < kCols; ++j, dst += a.L) *dst = __uint_as_float(o[j]);
           }
         }
-        if (kb0 == kb1) mbar_arrive(&o_empty);
-      } else {
-        // an empty sequence: its rows are zero, their log-sum -inf
-        for (int j = 0; j < NB; ++j) {
-          if (row_off[j] < 0) continue;
-          for (int d = tid * 8; d < a.L; d += 256 * 8)
-            *reinterpret_cast<uint4*>(a.out + row_off[j] + d) = make_uint4(0, 0, 0, 0);
-        }
-        if (half == 0 && on && a.lse != nullptr) a.lse[at * a.H + head] = -INFINITY;
       }
-      named_sync(1, 256);                    // the row table is rewritten next
+      ++seg_no;
     }
   }
   if (abort) atomicOr(&g_mla_decode_error, kErrTimeout);
@@ -568,21 +605,21 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 // of a row group that was cut between blocks (the order of the sums depends
 // on the shape alone).  A unit of work is a row's 128 latent values: `warps`
 // warps share its parts out (lane = four values) and meet in shared memory;
-// a block of 16 warps takes 16 / warps units.  Bound by the latency of the
-// parts' loads (L2), so all of a warp's loads go out together.
-constexpr int kCombThreads = 512;
+// a block of 8 warps takes 8 / warps units.  Bound by the latency of the
+// parts' loads (L2): four go out together.
+constexpr int kCombWarps = 8;
 
-__global__ void __launch_bounds__(kCombThreads) mla_combine_kernel(const DecodeArgs a, int grid, int NB, int warps) {
-  __shared__ int64_t sums[2][kCombThreads / 32];
-  __shared__ __align__(16) float4 acc_s[16][32];
-  __shared__ float2 ml_s[16];
+__global__ void __launch_bounds__(kCombWarps * 32, 4) mla_combine_kernel(const DecodeArgs a, int grid, int NB, int warps) {
+  __shared__ int64_t sums[2][kCombWarps];
+  __shared__ __align__(16) float4 acc_s[kCombWarps][32];
+  __shared__ float2 ml_s[kCombWarps];
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int group = blockIdx.x, s = group / a.RT, rt = group % a.RT;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // units before this sequence and of all (seq_lens: complete before the
   // kernel ahead let this one start)
   int64_t before = 0, total = 0;
-  for (int i = threadIdx.x; i < a.S; i += kCombThreads) {
+  for (int i = threadIdx.x; i < a.S; i += kCombWarps * 32) {
     const int64_t u = group_units(seq_len(a, i));
     total += u;
     if (i < s) before += u;
@@ -598,7 +635,7 @@ __global__ void __launch_bounds__(kCombThreads) mla_combine_kernel(const DecodeA
   }
   __syncthreads();
   before = total = 0;
-  for (int w = 0; w < kCombThreads / 32; ++w) {
+  for (int w = 0; w < kCombWarps; ++w) {
     before += sums[0][w];
     total += sums[1][w];
   }
@@ -609,7 +646,7 @@ __global__ void __launch_bounds__(kCombThreads) mla_combine_kernel(const DecodeA
   const int c0 = cut.owner(u0), c1 = cut.owner(u0 + units - 1);
   griddep_wait();                            // (every block: the grid must not end before the one ahead)
   if (c0 == c1) return;                      // not cut: written by its block
-  const int nk = a.L >> 7, per = 16 / warps; // units a block takes at a time
+  const int nk = a.L >> 7, per = kCombWarps / warps;   // units a block takes at a time
   const int team = warp / warps, member = warp % warps;
   const int unit = blockIdx.y * per + team;
   const int j = unit / nk, k = unit % nk;    // row and 128-value block
@@ -622,7 +659,7 @@ __global__ void __launch_bounds__(kCombThreads) mla_combine_kernel(const DecodeA
     // the part of block c: the one it begins the group with, or goes on with
     const float* base = a.parts + static_cast<int64_t>(j) * a.L + k * 128 + lane * 4;
     const float* stat = a.parts + static_cast<int64_t>(NB) * a.L + j;
-    constexpr int kBatch = 8;
+    constexpr int kBatch = 4;
     for (int c = c0 + member; c <= c1; c += kBatch * warps) {
       float4 o[kBatch];
       float m[kBatch], ls[kBatch];
@@ -794,13 +831,13 @@ cudaError_t launch_mla_decode(const MlaDecodeProblem& p, const DeviceInfo& dev, 
                                : launch_decode_nb<64>(maps, a, grid, dev, s));
   if (e != cudaSuccess || a.capacity <= kTileTok) return e;
   // warps that share a row's parts out: for the parts of a group that the
-  // grid cuts on average, eight to a warp
+  // grid cuts on average, four to a warp
   const int64_t groups = static_cast<int64_t>(p.S) * r.RT;
   int warps = 1;
-  while (warps < 16 && static_cast<int64_t>(warps) * 8 * groups < grid + groups) warps *= 2;
-  const int units = r.NB * (p.L / 128), per = 16 / warps;
+  while (warps < kCombWarps && static_cast<int64_t>(warps) * 4 * groups < grid + groups) warps *= 2;
+  const int units = r.NB * (p.L / 128), per = kCombWarps / warps;
   return mla_launch(mla_combine_kernel, dim3(static_cast<unsigned>(groups), static_cast<unsigned>(ceil_div(units, per))),
-                    kCombThreads, 0, s, a, grid, r.NB, warps);
+                    kCombWarps * 32, 0, s, a, grid, r.NB, warps);
 }
 
 uint32_t mla_decode_read_clear_error() { return read_clear_word(g_mla_decode_error); }
