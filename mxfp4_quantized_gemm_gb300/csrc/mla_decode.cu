@@ -265,10 +265,25 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   if (warp == 0) {
     // ---- copies.  Lane = (box of the tile's positions, chunk), in turns.
     const int boxes = kTileTok / a.box_rows;
+    const int box = lane & (boxes - 1);      // the lane's box, in every group
     Ring r(a.bufs);
     int i = 0, seg_no = 0;
-    Segment g;
+    Segment g{};
+    // The page and row of the lane's box of tile t, and the boxes that hold
+    // anything; asked for a tile ahead.
+    int page = 0, row = 0, nb = 0;
+    auto look_up = [&](int t) {
+      const int tok0 = t * kTileTok;
+      nb = (min(kTileTok, g.len - tok0) + a.box_rows - 1) / a.box_rows;
+      if (box < nb) {
+        const int tok = tok0 + box * a.box_rows;
+        const int col = tok / a.page_size;
+        row = tok - col * a.page_size;
+        page = __ldg(a.page_table + g.s * a.table_stride + col);
+      }
+    };
     while (!abort && walk.next_real(a, g)) {
+      look_up(g.t0);
       // the queries: their buffer is free once the last score product of the
       // stretch before has read it
       if (seg_no > 0 && !warp_wait(&s_full[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort)) break;
@@ -280,31 +295,24 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       if (lane == 31) tma_box_3d(qsm + 2 * nk * kQChunk, &rmap, 0, h0, tk0, &q_full);
       ++seg_no;
       for (int t = g.t0; t < g.t1; ++t, ++i) {
-        const int tok0 = t * kTileTok;
-        const int nb = (min(kTileTok, g.len - tok0) + a.box_rows - 1) / a.box_rows;   // boxes that hold anything
-        // lane's box in each group: pages are looked up once a tile
-        const int box = lane & (boxes - 1);
-        int page = 0, row = 0;
-        if (box < nb) {
-          const int tok = tok0 + box * a.box_rows;
-          const int col = tok / a.page_size;
-          row = tok - col * a.page_size;
-          page = __ldg(a.page_table + g.s * a.table_stride + col);
-          if (page < 0 || page >= a.num_pages) {
-            atomicOr(&g_mla_decode_error, kErrIndex);
-            page = a.num_pages;              // outside the map: the box is filled with zeros
-          }
+        const int cur_nb = nb, cur_row = row;
+        int cur_page = page;
+        if (box < cur_nb && (cur_page < 0 || cur_page >= a.num_pages)) {
+          atomicOr(&g_mla_decode_error, kErrIndex);
+          cur_page = a.num_pages;            // outside the map: the box is filled with zeros
         }
+        if (t + 1 < g.t1) look_up(t + 1);
         uint8_t* buf = ring + r.slot * tile_bytes;
         for (int x = 0; x < 2; ++x) {
           const int c0 = x == 0 ? 0 : na, c1 = x == 0 ? na : chunks;
           if (!warp_wait(&empty[x][r.slot], r.turn ^ 1u, abort)) break;
           if (lane == 0)
-            mbar_arrive_expect_tx(&full[x][r.slot], static_cast<uint32_t>((c1 - c0) * nb * a.box_rows * 128));
+            mbar_arrive_expect_tx(&full[x][r.slot], static_cast<uint32_t>((c1 - c0) * cur_nb * a.box_rows * 128));
           __syncwarp();
-          if (box < nb)
+          if (box < cur_nb)
             for (int c = c0 + lane / boxes; c < c1; c += 32 / boxes)
-              tma_box_3d(buf + c * kChunkBytes + box * a.box_rows * 128, &cmap, c * 64, row, page, &full[x][r.slot]);
+              tma_box_3d(buf + c * kChunkBytes + box * a.box_rows * 128, &cmap, c * 64, cur_row, cur_page,
+                         &full[x][r.slot]);
           if (x == 0) r.half();
         }
         if (abort) break;
@@ -324,7 +332,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const uint32_t ring_a = smem_u32(ring), q_a = smem_u32(qsm);
     Ring r(a.bufs);
     int i = 0, seg_no = 0;
-    Segment g;
+    Segment g{};
     while (!abort && walk.next_real(a, g)) {
       if (!warp_wait(&q_full, static_cast<uint32_t>(seg_no) & 1u, abort)) break;
       ++seg_no;
@@ -360,7 +368,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const uint64_t pd = sdesc_sw128(smem_u32(psm));
     Ring r(a.bufs);
     int i = 0, seg_no = 0;
-    Segment g;
+    Segment g{};
     while (!abort && walk.next_real(a, g)) {
       // the accumulator: the stretch before has been read out
       if (seg_no > 0 && !warp_wait(&o_empty, static_cast<uint32_t>(seg_no - 1) & 1u, abort)) break;
@@ -397,7 +405,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       }
     }
     drain_mmas(&drain[1], abort);
-  } else if (warp >= 4 && warp < 12) {
+  } else if (warp >= 4) {
+   const Walk walk0 = walk;
+   if (warp < 12) {
     // ---- softmax.  These threads meet at named barriers, so they walk every
     // tile even after a wait has given up.  A 64-row MMA leaves row 16 w + x in
     // lane 32 w + x (x < 16); the other lanes only keep company.
@@ -407,7 +417,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const uint32_t tl = tmem + (static_cast<uint32_t>(w * 32) << 16);
     const int kb0 = half == 0 ? 0 : (nk + 1) >> 1, kb1 = half == 0 ? (nk + 1) >> 1 : nk;   // this half's latent blocks
     int i = 0, seg_no = 0;
-    Segment g;
+    Segment g{};
     while (walk.next(a, g)) {
       int tok, head, see = mine ? 0 : 0x7FFFFFFF;
       const bool on = group_row(a, g.rt, row, tok, head) && mine;
@@ -533,14 +543,20 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (half == 0 && on && a.lse != nullptr) a.lse[at * a.H + head] = -INFINITY;
       }
     }
-  } else if (warp >= 12) {
-    // ---- finished accumulators: latent value 128 k + 32 w + lane of all rows
-    const int w = warp & 3;
+   }
+    // ---- finished accumulators: latent value 128 k + 32 w + lane of all rows.
+    // Warps 12..15 write out all but the block's last, which the softmax warps
+    // have nothing else to do beside: there each four take every third block k.
+    const int w = warp & 3, four = (warp >> 2) - 1;     // 0, 1: softmax, 2: warps 12..15
     const uint32_t tl = tmem + (static_cast<uint32_t>(w * 32) << 16);
     constexpr int kCols = NB < 32 ? NB : 32;
+    const bool odd = (lane & 1) != 0;
     int seg_no = 0;
-    Segment g;
-    while (walk.next_real(a, g)) {
+    Segment g{};
+    walk = walk0;
+    for (; walk.next_real(a, g); ++seg_no) {
+      const bool last = walk.left <= 0;
+      if (warp < 12 && !last) continue;
       const int par = seg_no & 1;
       mbar_wait(&fin_full, static_cast<uint32_t>(par), abort);
       mbar_wait(&o_full, static_cast<uint32_t>(par), abort);
@@ -548,39 +564,44 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       tc_fence_after();
       const bool whole = g.t0 == 0 && g.t1 == g.nt;
       float* part = whole ? nullptr : part_of(a, NB, blockIdx.x, g.t0 == 0);
-      // where rows lane and 32 + lane go (-1: nowhere)
-      int64_t off[NB > 32 ? 2 : 1];
-#pragma unroll
-      for (int x = 0; x < (NB > 32 ? 2 : 1); ++x) {
-        int tok, head;
-        off[x] = x * 32 + lane < NB && group_row(a, g.rt, x * 32 + lane, tok, head)
-                     ? (static_cast<int64_t>(g.s) * a.q_len + tok) * a.o_tok + head * a.o_head
-                     : -1;
-      }
+      const int tok0 = (g.rt / a.head_blocks) * a.TPT, h0 = (g.rt % a.head_blocks) * a.HB;
+      __nv_bfloat16* out0 = a.out + (static_cast<int64_t>(g.s) * a.q_len + tok0) * a.o_tok + h0 * a.o_head;
 #pragma unroll 1
-      for (int k = 0; k < nk; ++k) {
+      for (int k = last ? four : 0; k < nk; k += last ? 3 : 1) {
         const int d = k * 128 + w * 32 + lane;
-#pragma unroll
+        // the next row's place in the group and in the output
+        int hi = 0, ti = 0;
+        __nv_bfloat16* dst = out0 + (d & ~1);
+#pragma unroll 1
         for (int j0 = 0; j0 < NB; j0 += kCols) {
           uint32_t o[kCols];
           tmem_ld_cols<kCols>(tl + k * 64 + j0, o);
           tmem_wait_ld_of(o);
-          if (k + 1 == nk && j0 + kCols == NB) {
+          if (!last && k + 1 == nk && j0 + kCols == NB) {
             tc_fence_before();
             mbar_arrive(&o_empty);
           }
           if (whole) {
             // two rows per pass: lane pairs swap a value so that each lane
-            // stores two neighbouring ones
+            // stores two neighbouring ones, of the even or of the odd row
 #pragma unroll
             for (int j = 0; j < kCols; j += 2) {
               const float f0 = fin[par][j0 + j], f1 = fin[par][j0 + j + 1];
               const float x0 = f0 == 0.f ? 0.f : __uint_as_float(o[j]) * f0;
               const float x1 = f1 == 0.f ? 0.f : __uint_as_float(o[j + 1]) * f1;
-              const bool odd = (lane & 1) != 0;
               const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? x0 : x1, 1);
-              const int64_t to = __shfl_sync(0xFFFFFFFFu, off[j0 >> 5], (j0 + j + (lane & 1)) & 31);
-              st_global_if(a.out + to + (d & ~1), odd ? pack_bf16x2(got, x1) : pack_bf16x2(x0, got), to >= 0);
+              const uint32_t v = odd ? pack_bf16x2(got, x1) : pack_bf16x2(x0, got);
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const bool on = ti < a.TB && tok0 + ti < a.q_len && h0 + hi < a.H;
+                st_global_if(dst, v, on && odd == (x == 1));
+                dst += a.o_head;
+                if (++hi == a.HB) {
+                  hi = 0;
+                  ++ti;
+                  dst += a.o_tok - a.HB * a.o_head;
+                }
+              }
             }
           } else {
             // (rows that pad the group too: nothing reads them)
@@ -590,7 +611,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           }
         }
       }
-      ++seg_no;
     }
   }
   if (abort) atomicOr(&g_mla_decode_error, kErrTimeout);
@@ -603,15 +623,17 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 // ------------------------------------------------------------------ joining
 // out[r] = sum_p 2^(m_p - M) O_p[r] / sum_p 2^(m_p - M) l_p over the parts p
 // of a row group that was cut between blocks (the order of the sums depends
-// on the shape alone).  A unit of work is a row's 128 latent values: `warps`
-// warps share its parts out (lane = four values) and meet in shared memory;
-// a block of 8 warps takes 8 / warps units.  Bound by the latency of the
-// parts' loads (L2): four go out together.
+// on the shape alone).  A unit of work is V x 128 latent values of a row
+// (lane = V times four values): `warps` warps share its parts out and meet in
+// shared memory; a block of 8 warps takes 8 / warps units.  Bound by latency
+// (the lengths, then the parts, from L2), so a call should fit the card at
+// once: whole rows to a warp where there are many, and eight loads in flight.
 constexpr int kCombWarps = 8;
 
-__global__ void __launch_bounds__(kCombWarps * 32, 4) mla_combine_kernel(const DecodeArgs a, int grid, int NB, int warps) {
+template <int V>
+__global__ void __launch_bounds__(kCombWarps * 32, 3) mla_combine_kernel(const DecodeArgs a, int grid, int NB, int warps) {
   __shared__ int64_t sums[2][kCombWarps];
-  __shared__ __align__(16) float4 acc_s[kCombWarps][32];
+  __shared__ __align__(16) float4 acc_s[kCombWarps][V][32];
   __shared__ float2 ml_s[kCombWarps];
   if (threadIdx.x == 0) griddep_launch_dependents();
   const int group = blockIdx.x, s = group / a.RT, rt = group % a.RT;
@@ -646,22 +668,24 @@ __global__ void __launch_bounds__(kCombWarps * 32, 4) mla_combine_kernel(const D
   const int c0 = cut.owner(u0), c1 = cut.owner(u0 + units - 1);
   griddep_wait();                            // (every block: the grid must not end before the one ahead)
   if (c0 == c1) return;                      // not cut: written by its block
-  const int nk = a.L >> 7, per = kCombWarps / warps;   // units a block takes at a time
+  const int nk = a.L / (128 * V), per = kCombWarps / warps;   // units a block takes at a time
   const int team = warp / warps, member = warp % warps;
   const int unit = blockIdx.y * per + team;
-  const int j = unit / nk, k = unit % nk;    // row and 128-value block
+  const int j = unit / nk, k = unit % nk;    // row and its V x 128 values
   int tok = 0, head = 0;
   const bool on = j < NB && group_row(a, rt, j, tok, head);
   float M = -INFINITY, l = 0.f;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 v[V];
+#pragma unroll
+  for (int x = 0; x < V; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (on) {
     const int64_t pf = part_floats(NB, a.L);
     // the part of block c: the one it begins the group with, or goes on with
-    const float* base = a.parts + static_cast<int64_t>(j) * a.L + k * 128 + lane * 4;
+    const float* base = a.parts + static_cast<int64_t>(j) * a.L + k * V * 128 + lane * 4;
     const float* stat = a.parts + static_cast<int64_t>(NB) * a.L + j;
-    constexpr int kBatch = 4;
+    constexpr int kBatch = V >= 4 ? 2 : (V == 2 ? 4 : 8);
     for (int c = c0 + member; c <= c1; c += kBatch * warps) {
-      float4 o[kBatch];
+      float4 o[kBatch][V];
       float m[kBatch], ls[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
@@ -670,29 +694,36 @@ __global__ void __launch_bounds__(kCombWarps * 32, 4) mla_combine_kernel(const D
         const bool in = ci <= c1;
         m[i] = in ? stat[at] : -INFINITY;
         ls[i] = in ? stat[at + NB] : 0.f;
-        o[i] = in ? *reinterpret_cast<const float4*>(base + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < V; ++x)
+          o[i][x] = in ? *reinterpret_cast<const float4*>(base + at + x * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       float Mn = M;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) Mn = fmaxf(Mn, m[i]);
       const float ref = Mn == -INFINITY ? 0.f : Mn, f = exp2_fast(M - ref);
       l *= f;
-      v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+#pragma unroll
+      for (int x = 0; x < V; ++x) v[x] = make_float4(v[x].x * f, v[x].y * f, v[x].z * f, v[x].w * f);
       M = Mn;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         if (ls[i] == 0.f) continue;          // no part, or one whose positions this row does not see
         const float wgt = exp2_fast(m[i] - ref);
         l += wgt * ls[i];
-        v.x += wgt * o[i].x;
-        v.y += wgt * o[i].y;
-        v.z += wgt * o[i].z;
-        v.w += wgt * o[i].w;
+#pragma unroll
+        for (int x = 0; x < V; ++x) {
+          v[x].x += wgt * o[i][x].x;
+          v[x].y += wgt * o[i][x].y;
+          v[x].z += wgt * o[i][x].z;
+          v[x].w += wgt * o[i][x].w;
+        }
       }
     }
   }
   if (warps > 1) {
-    acc_s[warp][lane] = v;
+#pragma unroll
+    for (int x = 0; x < V; ++x) acc_s[warp][x][lane] = v[x];
     if (lane == 0) ml_s[warp] = make_float2(M, l);
     __syncthreads();
     if (member != 0) return;
@@ -700,25 +731,33 @@ __global__ void __launch_bounds__(kCombWarps * 32, 4) mla_combine_kernel(const D
     for (int w = 1; w < warps; ++w) Mt = fmaxf(Mt, ml_s[warp + w].x);
     const float ref = Mt == -INFINITY ? 0.f : Mt, f = exp2_fast(M - ref);
     l *= f;
-    v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+#pragma unroll
+    for (int x = 0; x < V; ++x) v[x] = make_float4(v[x].x * f, v[x].y * f, v[x].z * f, v[x].w * f);
     for (int w = 1; w < warps; ++w) {
       const float2 ml = ml_s[warp + w];
       if (ml.y == 0.f) continue;
       const float wgt = exp2_fast(ml.x - ref);
-      const float4 o = acc_s[warp + w][lane];
       l += wgt * ml.y;
-      v.x += wgt * o.x;
-      v.y += wgt * o.y;
-      v.z += wgt * o.z;
-      v.w += wgt * o.w;
+#pragma unroll
+      for (int x = 0; x < V; ++x) {
+        const float4 o = acc_s[warp + w][x][lane];
+        v[x].x += wgt * o.x;
+        v[x].y += wgt * o.y;
+        v[x].z += wgt * o.z;
+        v[x].w += wgt * o.w;
+      }
     }
     M = Mt;
   }
   if (!on) return;
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   const int64_t at = static_cast<int64_t>(s) * a.q_len + tok;
-  *reinterpret_cast<uint2*>(a.out + at * a.o_tok + head * a.o_head + k * 128 + lane * 4) =
-      l == 0.f ? make_uint2(0u, 0u) : make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+  __nv_bfloat16* dst = a.out + at * a.o_tok + head * a.o_head + k * V * 128 + lane * 4;
+#pragma unroll
+  for (int x = 0; x < V; ++x)
+    *reinterpret_cast<uint2*>(dst + x * 128) =
+        l == 0.f ? make_uint2(0u, 0u)
+                 : make_uint2(pack_bf16x2(v[x].x * inv, v[x].y * inv), pack_bf16x2(v[x].z * inv, v[x].w * inv));
   if (k == 0 && lane == 0 && a.lse != nullptr) a.lse[at * a.H + head] = l == 0.f ? -INFINITY : (M + log2_fast(l)) * kLn2;
 }
 
@@ -830,13 +869,17 @@ cudaError_t launch_mla_decode(const MlaDecodeProblem& p, const DeviceInfo& dev, 
                  : (r.NB == 32 ? launch_decode_nb<32>(maps, a, grid, dev, s)
                                : launch_decode_nb<64>(maps, a, grid, dev, s));
   if (e != cudaSuccess || a.capacity <= kTileTok) return e;
-  // warps that share a row's parts out: for the parts of a group that the
-  // grid cuts on average, four to a warp
+  // a whole row to a warp where there are rows for a few warps per SM; warps
+  // that share a row's parts out: for the parts of a group that the grid cuts
+  // on average, four to a warp
   const int64_t groups = static_cast<int64_t>(p.S) * r.RT;
+  const int nk = p.L / 128;
+  const int V = groups * r.NB <= dev.sm_count || nk == 3 ? 1 : nk;
   int warps = 1;
   while (warps < kCombWarps && static_cast<int64_t>(warps) * 4 * groups < grid + groups) warps *= 2;
-  const int units = r.NB * (p.L / 128), per = kCombWarps / warps;
-  return mla_launch(mla_combine_kernel, dim3(static_cast<unsigned>(groups), static_cast<unsigned>(ceil_div(units, per))),
+  const int units = r.NB * (nk / V), per = kCombWarps / warps;
+  auto join = V == 4 ? mla_combine_kernel<4> : (V == 2 ? mla_combine_kernel<2> : mla_combine_kernel<1>);
+  return mla_launch(join, dim3(static_cast<unsigned>(groups), static_cast<unsigned>(ceil_div(units, per))),
                     kCombWarps * 32, 0, s, a, grid, r.NB, warps);
 }
 
