@@ -41,37 +41,23 @@ struct Ring {
   int n;
   int slot = 0;
   uint32_t turn = 0;
-  int filled = 0, half_filled = 0, half_slot = 0;
-  uint32_t half_turn = 0;
   __device__ __forceinline__ explicit Ring(int slots) : n(slots) {}
   __device__ __forceinline__ void step() {
-    if (filled < n) ++filled;
     if (++slot == n) {
       slot = 0;
       turn ^= 1u;
     }
   }
-  // A slot filled in two halves with barriers of their own: the first is on its way.
-  __device__ __forceinline__ void half() {
-    half_slot = slot;
-    half_turn = turn;
-    if (half_filled < n) ++half_filled;
-  }
-  __device__ __forceinline__ void drain_half(uint64_t* full) const {
-    for (int s = 0; s < half_filled; ++s) {
-      bool late = false;
-      mbar_wait(&full[s], s <= half_slot ? half_turn : half_turn ^ 1u, late);
-    }
-  }
-  // For the filling warp, after a wait that gave up: a bounded wait for the
-  // copies in flight.
-  __device__ __forceinline__ void drain(uint64_t* full) const {
-    for (int s = 0; s < filled; ++s) {
-      bool late = false;
-      mbar_wait(&full[s], s < slot ? turn : turn ^ 1u, late);
-    }
-  }
 };
+// For the filling warp, after a wait that gave up: a bounded wait for the
+// copies of the `fills` fills so far that may be in flight (the last of each
+// of the n slots).
+__device__ __forceinline__ void drain_copies(uint64_t* full, int fills, int n) {
+  for (int f = fills > n ? fills - n : 0; f < fills; ++f) {
+    bool late = false;
+    mbar_wait(&full[f % n], static_cast<uint32_t>(f / n) & 1u, late);
+  }
+}
 
 // After a wait that gave up, by a whole warp that issued MMAs: a bounded wait
 // for those in flight, before their TMEM is freed.

@@ -29,7 +29,9 @@
 // A copying warp spends about 430 cycles on each wait, arrival and copy and
 // 16 on each further copy, so a tile comes in two groups, each under one
 // barrier: all but the last 128 latent values, and those with the rotated key
-// (so that little is left to multiply when the last of a tile lands).
+// (little is left to multiply when the last of a tile lands).  A group per
+// 128 values, given back as the output product is done with it, was no faster
+// (86.4 against 85.4 us at 64 sequences of up to 8192).
 //
 // Work split: the tiles of all row groups, in order, are cut evenly over the
 // grid; a block takes its stretch wherever sequences begin and end, so a
@@ -209,8 +211,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int nk = a.L >> 7;                                  // 128-value blocks of the latent
   const int chunks = 2 * nk + 1;                            // 64-value chunks of a cache row
-  const int na = nk > 1 ? 2 * (nk - 1) : 2;                 // those of a tile's first group
   const int tile_bytes = chunks * kChunkBytes;
+  const int groups = nk > 1 ? 2 : 1;                        // of a tile's chunks
+  const int split = 2 * (nk - 1);                           // the last group's first chunk
   // the 64-row score MMA reads 64 rows of a query chunk whatever NB is: the
   // queries lie in front, so that what it reads past them is inside the buffer
   uint8_t* qsm = smem;                                      // chunks of NB rows x 64 values
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const int boxes = kTileTok / a.box_rows;
     const int box = lane & (boxes - 1);      // the lane's box, in every group
     Ring r(a.bufs);
-    int i = 0, seg_no = 0;
+    int i = 0, seg_no = 0, fills = 0;
     Segment g{};
     // The page and row of the lane's box of tile t, and the boxes that hold
     // anything; asked for a tile ahead.
@@ -303,8 +306,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         if (t + 1 < g.t1) look_up(t + 1);
         uint8_t* buf = ring + r.slot * tile_bytes;
-        for (int x = 0; x < 2; ++x) {
-          const int c0 = x == 0 ? 0 : na, c1 = x == 0 ? na : chunks;
+        for (int x = 0; x < groups; ++x) {
+          const int c0 = x == 0 ? 0 : split, c1 = x + 1 == groups ? chunks : split;
           if (!warp_wait(&empty[x][r.slot], r.turn ^ 1u, abort)) break;
           if (lane == 0)
             mbar_arrive_expect_tx(&full[x][r.slot], static_cast<uint32_t>((c1 - c0) * cur_nb * a.box_rows * 128));
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             for (int c = c0 + lane / boxes; c < c1; c += 32 / boxes)
               tma_box_3d(buf + c * kChunkBytes + box * a.box_rows * 128, &cmap, c * 64, cur_row, cur_page,
                          &full[x][r.slot]);
-          if (x == 0) r.half();
+          ++fills;
         }
         if (abort) break;
         r.step();
@@ -321,8 +324,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     if (abort) {
       // give the copies in flight a bounded time to land
-      r.drain(full[1]);
-      r.drain_half(full[0]);
+      for (int x = 0; x < groups; ++x) drain_copies(full[x], (fills + groups - 1 - x) / groups, a.bufs);
       bool late = false;
       if (seg_no > 0) mbar_wait(&q_full, static_cast<uint32_t>(seg_no - 1) & 1u, late);
     }
@@ -341,8 +343,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         // tile i - 2's scores have been read once its weights are out
         if (i >= 2 && !warp_wait(&p_full[i & 1], static_cast<uint32_t>((i >> 1) + 1) & 1u, abort)) break;
         const uint32_t sb = ring_a + static_cast<uint32_t>(r.slot * tile_bytes);
-        for (int x = 0; x < 2; ++x) {
-          const int c0 = x == 0 ? 0 : na, c1 = x == 0 ? na : chunks;
+        for (int x = 0; x < groups; ++x) {
+          const int c0 = x == 0 ? 0 : split, c1 = x + 1 == groups ? chunks : split;
           if (!warp_wait(&full[x][r.slot], r.turn, abort)) break;
           tc_fence_after();
           if (elect_one()) {
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
               for (int m = 0; m < 4; ++m) mma_bf16(d, ad + 2 * m, bd + 2 * m, idesc, (c | m) != 0);
             }
-            if (x == 1) mma_commit(&s_full[i & 1]);
+            if (x + 1 == groups) mma_commit(&s_full[i & 1]);
           }
           __syncwarp();
         }
@@ -394,9 +396,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             for (int m = 0; m < 4; ++m)
               if (m < ks)
                 mma_bf16(tmem + static_cast<uint32_t>(k) * 64u, ad + m * 128, pd + m * 2, idesc, t != g.t0 || m != 0);
-            if (2 * k + 2 == na) mma_commit(&empty[0][r.slot]);
+            if (k + 2 == nk) mma_commit(&empty[0][r.slot]);
           }
-          mma_commit(&empty[1][r.slot]);
+          mma_commit(&empty[groups - 1][r.slot]);
           mma_commit(&pv_done);
           if (t + 1 == g.t1) mma_commit(&o_full);
         }

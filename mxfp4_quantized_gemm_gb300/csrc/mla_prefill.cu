@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   if (warp == 0) {
     // ---- queries and keys
     Ring r(a.kslots);
+    int fills = 0;
     if (tiles > 0) {
       if (elect_one()) {
         mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(a.nq * kSlotBytes));
@@ -192,16 +193,18 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         __syncwarp();
         r.step();
+        ++fills;
       }
     }
     if (abort) {
-      r.drain(kfull);
+      drain_copies(kfull, fills, r.n);
       bool late = false;
       if (tiles > 0) mbar_wait(&q_full, 0, late);
     }
   } else if (warp == 3) {
     // ---- values
     Ring r(a.vslots);
+    int fills = 0;
     for (int t = 0; t < tiles && !abort; ++t) {
       const int tok = t * kPreTile;
       for (int j = 0; j < kPreTile / kVTok && tok + j * kVTok < see1; ++j) {
@@ -214,9 +217,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         __syncwarp();
         r.step();
+        ++fills;
       }
     }
-    if (abort) r.drain(vfull);
+    if (abort) drain_copies(vfull, fills, r.n);
   } else if (warp == 1) {
     // ---- score products S = Q K^T
     constexpr uint32_t idesc = idesc_bf16(128, 128);

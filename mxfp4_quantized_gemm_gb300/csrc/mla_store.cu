@@ -12,7 +12,11 @@
 // One block per token: warp 0 holds the latent row in registers, and every
 // thread of the other warps rotates 16 values of a head, the unit in which
 // both pairings are closed (two 16-byte vectors holding pairs 8u..8u+7): its
-// sixteen table values are loaded once and serve all the heads it visits.
+// sixteen table values are loaded once and serve all the heads it visits.  Two
+// heads are in flight per thread, asked for before the position is known, and
+// eight blocks fit an SM: a token takes about 2.5 us from launch to store, so
+// it is the tokens in flight that carry the bandwidth (one head a thread and
+// three blocks per SM: 50 us at 8192 tokens x 64 heads; now 26.7 us, 5.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -52,30 +56,33 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
+__device__ __forceinline__ float lo16(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi16(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
 // Unit u (0..3) of a 64-element row: vectors 2u, 2u + 1 interleaved, u and
-// u + 4 otherwise; c, s: cos and sin of pairs 8u..8u+7.
+// u + 4 otherwise; c, s: cos and sin of pairs 8u..8u+7.  Word by word, so that
+// few values are unpacked at a time.
 __device__ __forceinline__ void rotate_unit(uint4& va, uint4& vb, const float (&c)[8], const float (&s)[8],
                                             bool interleaved) {
-  float a[8], b[8], oa[8], ob[8];
-  unpack8(va, a);
-  unpack8(vb, b);
+  uint32_t a[4] = {va.x, va.y, va.z, va.w}, b[4] = {vb.x, vb.y, vb.z, vb.w};
   if (interleaved) {
+    // a word is a pair
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      oa[2 * i] = a[2 * i] * c[i] - a[2 * i + 1] * s[i];
-      oa[2 * i + 1] = a[2 * i + 1] * c[i] + a[2 * i] * s[i];
-      ob[2 * i] = b[2 * i] * c[4 + i] - b[2 * i + 1] * s[4 + i];
-      ob[2 * i + 1] = b[2 * i + 1] * c[4 + i] + b[2 * i] * s[4 + i];
+      const float a0 = lo16(a[i]), a1 = hi16(a[i]), b0 = lo16(b[i]), b1 = hi16(b[i]);
+      a[i] = pack_bf16x2(a0 * c[i] - a1 * s[i], a1 * c[i] + a0 * s[i]);
+      b[i] = pack_bf16x2(b0 * c[4 + i] - b1 * s[4 + i], b1 * c[4 + i] + b0 * s[4 + i]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      oa[i] = a[i] * c[i] - b[i] * s[i];
-      ob[i] = b[i] * c[i] + a[i] * s[i];
+    for (int i = 0; i < 4; ++i) {
+      const float a0 = lo16(a[i]), a1 = hi16(a[i]), b0 = lo16(b[i]), b1 = hi16(b[i]);
+      a[i] = pack_bf16x2(a0 * c[2 * i] - b0 * s[2 * i], a1 * c[2 * i + 1] - b1 * s[2 * i + 1]);
+      b[i] = pack_bf16x2(b0 * c[2 * i] + a0 * s[2 * i], b1 * c[2 * i + 1] + a1 * s[2 * i + 1]);
     }
   }
-  va = pack8(oa);
-  vb = pack8(ob);
+  va = make_uint4(a[0], a[1], a[2], a[3]);
+  vb = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
 __device__ __forceinline__ void load_angles(const float* row, int u, float (&c)[8], float (&s)[8]) {
@@ -95,17 +102,18 @@ __device__ __forceinline__ void load_angles(const float* row, int u, float (&c)[
   }
 }
 
-__global__ void __launch_bounds__(288) mla_store_kernel(const StoreArgs a) {
+constexpr int kStoreThreads = 160;            // warp 0: the cache row; four warps: the queries
+
+__global__ void __launch_bounds__(kStoreThreads, 8) mla_store_kernel(const StoreArgs a) {
   if (threadIdx.x == 0) griddep_launch_dependents();
   griddep_wait();
   const int64_t t = blockIdx.x;
-  const int64_t pos = __ldg(a.positions + t);
-  const bool pos_ok = pos >= 0 && pos < a.max_pos;
   const int step = a.interleaved ? 1 : 4;              // distance of a unit's two vectors
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
     // ---- the cache row
-    const int64_t slot = __ldg(a.slots + t);
+    const int64_t pos = __ldg(a.positions + t), slot = __ldg(a.slots + t);
+    const bool pos_ok = pos >= 0 && pos < a.max_pos;
     const bool slot_ok = slot >= 0 && slot < static_cast<int64_t>(a.num_pages) * a.page_size;
     if (lane == 0 && (!pos_ok || (slot >= 0 && !slot_ok))) atomicOr(&g_mla_store_error, kErrIndex);
     if (!pos_ok || !slot_ok) return;
@@ -113,16 +121,12 @@ __global__ void __launch_bounds__(288) mla_store_kernel(const StoreArgs a) {
     uint16_t* row = a.cache + (slot / a.page_size) * a.page_stride +
                     (slot % a.page_size) * static_cast<int64_t>(a.L + kMlaRope);
     const int nv = a.L >> 3;                           // 16-byte vectors of the latent, at most 64
-    float f[2][8], g[2][8];
-    float ss = 0.f;
+    uint4 xv[2], gv[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int v = lane + 32 * i;
-      const bool on = v < nv;
-      unpack8(on ? __ldg(reinterpret_cast<const uint4*>(x) + v) : make_uint4(0, 0, 0, 0), f[i]);
-      unpack8(on ? __ldg(reinterpret_cast<const uint4*>(a.gamma) + v) : make_uint4(0, 0, 0, 0), g[i]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss += f[i][e] * f[i][e];
+      xv[i] = v < nv ? __ldg(reinterpret_cast<const uint4*>(x) + v) : make_uint4(0, 0, 0, 0);
+      gv[i] = v < nv ? __ldg(reinterpret_cast<const uint4*>(a.gamma) + v) : make_uint4(0, 0, 0, 0);
     }
     if (lane < 4) {
       // the shared key, while the sum is on its way
@@ -135,6 +139,14 @@ __global__ void __launch_bounds__(288) mla_store_kernel(const StoreArgs a) {
       reinterpret_cast<uint4*>(row)[v0 + step] = vb;
     }
     __syncwarp();
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float f[8];
+      unpack8(xv[i], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss += f[e] * f[e];
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
     const float inv = 1.0f / sqrtf(ss / static_cast<float>(a.L) + a.eps);
@@ -142,28 +154,46 @@ __global__ void __launch_bounds__(288) mla_store_kernel(const StoreArgs a) {
     for (int i = 0; i < 2; ++i) {
       const int v = lane + 32 * i;
       if (v < nv) {
+        float f[8], g[8];
+        unpack8(xv[i], f);
+        unpack8(gv[i], g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[i][e] = f[i][e] * inv * g[i][e];
-        reinterpret_cast<uint4*>(row)[v] = pack8(f[i]);
+        for (int e = 0; e < 8; ++e) f[e] = f[e] * inv * g[e];
+        reinterpret_cast<uint4*>(row)[v] = pack8(f);
       }
     }
     return;
   }
   // ---- the queries
-  if (!pos_ok) return;
   const int first = threadIdx.x - 32, stride = (blockDim.x - 32) >> 2;
   const int u = first & 3;
-  if ((first >> 2) >= a.H) return;
+  int h = first >> 2;
+  if (h >= a.H) return;
+  const int v0 = a.interleaved ? 2 * u : u;
+  const uint16_t* src = a.q + t * a.q_tok + h * a.q_head;
+  uint16_t* dst = a.q_out + t * a.o_tok + h * a.o_head;
+  auto load = [&](const uint16_t* p, uint4 (&v)[2]) {
+    v[0] = reinterpret_cast<const uint4*>(p)[v0];
+    v[1] = reinterpret_cast<const uint4*>(p)[v0 + step];
+  };
+  uint4 x[2], y[2];
+  load(src, x);
+  if (h + stride < a.H) load(src + stride * a.q_head, y);
+  const int64_t pos = __ldg(a.positions + t);
+  if (pos < 0 || pos >= a.max_pos) return;
   float c[8], s[8];
   load_angles(a.cos_sin + pos * kMlaRope, u, c, s);
-  const int v0 = a.interleaved ? 2 * u : u;
-  for (int h = first >> 2; h < a.H; h += stride) {
-    const uint4* src = reinterpret_cast<const uint4*>(a.q + t * a.q_tok + h * a.q_head);
-    uint4* dst = reinterpret_cast<uint4*>(a.q_out + t * a.o_tok + h * a.o_head);
-    uint4 va = src[v0], vb = src[v0 + step];
-    rotate_unit(va, vb, c, s, a.interleaved);
-    dst[v0] = va;
-    dst[v0 + step] = vb;
+  while (true) {
+    rotate_unit(x[0], x[1], c, s, a.interleaved);
+    reinterpret_cast<uint4*>(dst)[v0] = x[0];
+    reinterpret_cast<uint4*>(dst)[v0 + step] = x[1];
+    h += stride;
+    if (h >= a.H) return;
+    src += stride * a.q_head;
+    dst += stride * a.o_head;
+    x[0] = y[0];
+    x[1] = y[1];
+    if (h + stride < a.H) load(src + stride * a.q_head, y);
   }
 }
 
@@ -190,9 +220,9 @@ cudaError_t launch_mla_store(const MlaStoreProblem& p, const DeviceInfo&, cudaSt
   a.L = p.L;
   a.eps = p.eps;
   a.interleaved = p.interleaved;
-  int units = p.H * 4;                       // 16-value units of a token's queries
-  if (units > 256) units = 256;
-  const int threads = 32 + static_cast<int>(ceil_div(units, 32)) * 32;
+  const int64_t units = static_cast<int64_t>(p.H) * 4;                       // 16-value units of a token's queries
+  const int64_t warps = ceil_div(units, 32);
+  const int threads = warps < kStoreThreads / 32 - 1 ? 32 + static_cast<int>(warps) * 32 : kStoreThreads;
   return mla_launch(mla_store_kernel, dim3(static_cast<unsigned>(p.T)), threads, 0, s, a);
 }
 
