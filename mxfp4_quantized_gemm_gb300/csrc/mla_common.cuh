@@ -33,6 +33,60 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, bool& 
   return !abort;
 }
 
+// The same across the CTAs of a cluster, for phases that another CTA's threads
+// or MMAs complete.
+template <bool kCluster>
+__device__ __forceinline__ bool warp_wait_in(uint64_t* bar, uint32_t parity, bool& abort) {
+  if (kCluster)
+    mbar_wait_cluster(bar, parity, abort);
+  else
+    mbar_wait(bar, parity, abort);
+  abort = __any_sync(0xFFFFFFFFu, abort);
+  return !abort;
+}
+// One arrival on the barrier at the same offset in the CTA of rank `rank`,
+// ordering this thread's own operations before it.
+__device__ __forceinline__ void mbar_arrive_remote(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), rank))
+               : "memory");
+}
+
+// bf16 MMAs of one CTA, or of a CTA pair (cta_group::2, issued by rank 0): A
+// from shared memory, or from TMEM (_ts).
+template <bool kPair>
+__device__ __forceinline__ void mma_bf16_of(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  if (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    mma_bf16(d, adesc, bdesc, idesc, acc);
+}
+template <bool kPair>
+__device__ __forceinline__ void mma_bf16_ts_of(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t acc) {
+  if (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    mma_bf16_ts(d, a_tmem, bdesc, idesc, acc);
+}
+// Arrive (in both CTAs of a pair) when the issuing thread's MMAs so far are done.
+template <bool kPair>
+__device__ __forceinline__ void mma_commit_of(uint64_t* bar) {
+  if (kPair)
+    mma_commit_pair(bar);
+  else
+    mma_commit(bar);
+}
+
 // A place in a ring of n slots with a full and an empty barrier each: the slot
 // and the parity of the current turn round the ring.  One warp fills it and
 // one warp empties it (a warp that skipped another's phases could take a
@@ -61,9 +115,10 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, int fills, int n) {
 
 // After a wait that gave up, by a whole warp that issued MMAs: a bounded wait
 // for those in flight, before their TMEM is freed.
+template <bool kPair = false>
 __device__ __forceinline__ void drain_mmas(uint64_t* bar, bool abort) {
   if (!abort) return;
-  if (elect_one()) mma_commit(bar);
+  if (elect_one()) mma_commit_of<kPair>(bar);
   __syncwarp();
   bool late = false;
   mbar_wait(bar, 0, late);
@@ -245,20 +300,30 @@ inline cudaError_t mla_tensor_map(CUtensorMap* map, const void* p, int64_t d0, i
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Launch as a programmatic dependent of the kernel ahead on the stream.
+// Launch as a programmatic dependent of the kernel ahead on the stream, in
+// clusters of `cluster` blocks.
 template <typename... Params, typename... Args>
-cudaError_t mla_launch(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, Args&&... args) {
+cudaError_t mla_launch_clusters(void (*kern)(Params...), dim3 grid, int cluster, int threads, int smem, cudaStream_t s,
+                                Args&&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+}
+template <typename... Params, typename... Args>
+cudaError_t mla_launch(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, Args&&... args) {
+  return mla_launch_clusters(kern, grid, 1, threads, smem, s, static_cast<Args&&>(args)...);
 }
 
 // Reads and clears a translation unit's device error word.

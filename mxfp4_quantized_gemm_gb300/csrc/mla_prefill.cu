@@ -14,17 +14,31 @@
 // the value tile is read in place from the expanding projection's output
 // [token][head][dn + dv] (its rows are the MMA's K: N-contiguous operand).
 //
-// Roles: warp 0 copies keys and warp 3 values, each through a ring of 16 KB
-// slots of its own (64 values of 128 keys; all values of 32 keys); warp 1
-// issues the score products, warp 2 the output products; warps 4..7 and 8..11 hold the softmax, thread = (query,
-// half of the tile's keys).  Each query's running maximum is raised only when
-// a score passes it by 2^8, decided per 32 queries by a barrier with an OR
-// over the two warps that hold them.
+// Long prompts run in pairs of blocks (kPair: a 2-CTA cluster, cta_group::2
+// MMAs of 256 queries).  One block alone is held by shared memory: at dn + R =
+// dv = 256 a tile's MMAs take 2144 cycles, while its operands (1536 cycles at
+// 128 bytes a cycle) and the copies that bring them (1024) share the same
+// memory, and its MMAs ran at 124 (scores) and 175 cycles (output) instead of
+// 71 and 126.  In a pair each block holds and reads half of the keys (rows) and
+// half of the values (columns), and its copies halve too.
 //
-// Two copying warps because one is too slow: a wait, an arrival and a tensor
-// copy take a warp about 430 cycles whatever the copy's size (16 more for each
-// further copy under the same wait), 38 bytes a cycle with 16 KB slots, and
-// the products use 62.  One warp for both: 2096 us at 8192 tokens x 64 heads.
+// Roles: warp 0 copies keys and warp 3 values, each through a ring of 32 KB
+// slots of its own; warp 1 issues every product (in rank 0 of a pair; in rank
+// 1 warps 1 and 2 pass on to rank 0 that their keys and values have landed);
+// warps 4..7 and 8..11 hold the softmax, thread = (query, half of the tile's
+// keys).  Each query's running maximum is raised only when a score passes it
+// by 2^8, decided per 32 queries by a barrier with an OR over the two warps
+// that hold them.
+//
+// Order of the products: S(0), S(1), O(0), S(2), O(1), ...  The next scores go
+// first, so that their softmax runs beside the product of the tile before,
+// and S(t + 2) may overwrite the weights of tile t as soon as O(t), issued
+// before it by the same thread, has read them.
+//
+// Slot size: an issuing warp spends about 50 cycles an MMA and 155 a slot
+// (wait, commit); a copying warp spends 430 cycles a slot (wait, arrival,
+// copy) and 16 for each further copy.  With one or two slots a tile both stay
+// below the MMAs' time; with four (16 KB) they did not.
 //
 // Blocks are ordered head by head and, within a head, from the last queries
 // (most keys) to the first: blocks that run together share a head's keys and
@@ -41,12 +55,26 @@ namespace mx {
 static __device__ uint32_t g_mla_prefill_error;
 
 constexpr int kPreThreads = 384;
-constexpr int kPreTile = 128;                 // queries, and keys per tile
-constexpr int kSlotBytes = 16384;             // 128 keys x 64 values, or 32 keys x 256 values
-constexpr int kVTok = 32;                     // keys per value slot
-constexpr int kPreMaxSlots = 12;              // ring slots, keys' and values' together
+constexpr int kPreTile = 128;                 // queries of a block, and keys per tile
+constexpr int kPreChunk = 16384;              // 128 rows x 64 values
+constexpr int kSlotBytes = 2 * kPreChunk;
+constexpr int kPreMaxSlots = 4;               // slots of a ring
 constexpr int kPreSmem = 227 * 1024;
+constexpr int kPreStatic = 2048;              // most of it that the static part takes
 constexpr int kPreScol = 256;                 // first TMEM column of the score tiles
+
+// A slot holds, of a block alone, 128 values of 128 keys or all values of 64
+// keys (two value slots a tile); of a block of a pair, all values of its 64
+// keys or its half of the values of 128 keys.
+template <bool kPair>
+struct PreShape {
+  static constexpr int kKeyRows = kPair ? 64 : 128;     // keys in a key slot
+  static constexpr int kKeyChunks = kPair ? 4 : 2;      // 64-value chunks in a key slot
+  static constexpr int kKeyChunkBytes = kKeyRows * 128;
+  static constexpr int kValRows = kPair ? 128 : 64;     // keys in a value slot
+  static constexpr int kValBlockBytes = kValRows * 128; // 64 values of them
+  static constexpr int kQueries = kPair ? 256 : 128;
+};
 
 struct PrefillArgs {
   const int32_t* cu_q;
@@ -56,7 +84,7 @@ struct PrefillArgs {
   int64_t o_tok, o_head;
   int S, H, Tq, Tk, dn, dv;
   int nq;               // 64-value chunks of q and k (the last is the rotated one)
-  int nv;               // 64-value blocks of v
+  int dvn;              // dv rounded up to the MMA's N
   int kslots, vslots;   // ring slots of the keys and of the values
   float c;              // |scale| * log2(e)
   bool flip;            // scale < 0: the scores change sign first
@@ -77,51 +105,81 @@ __device__ __forceinline__ Extent extent(const PrefillArgs& a, int s) {
   return e;
 }
 
+// Keys of a value slot that no query of the tile sees may hold anything (0 x
+// NaN): their weights are 0 and they are made 0 too, by one warp.  `valid`: the
+// slot's keys that count.  True if there were any to clear.
+template <int kRows>
+__device__ __forceinline__ bool clear_values(uint8_t* slot, int nv, int valid, int lane) {
+  if (valid >= kRows) return false;
+  for (int k = 0; k < nv; ++k) zero_rows(slot + k * kRows * 128, valid, kRows, lane);
+  fence_proxy_async_smem();
+  __syncwarp();
+  return true;
+}
+
+// A bounded wait for an MMA's commit (of rank 0, in a pair).
+template <bool kPair>
+__device__ __forceinline__ void wait_mma(uint64_t* bar, uint32_t parity, bool& abort) {
+  if (kPair)
+    mbar_wait_cluster(bar, parity, abort);
+  else
+    mbar_wait(bar, parity, abort);
+}
+
+template <bool kPair>
 __global__ void __launch_bounds__(kPreThreads, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_constant__ CUtensorMap qr_map,
                        const __grid_constant__ CUtensorMap kn_map, const __grid_constant__ CUtensorMap kr_map,
                        const __grid_constant__ CUtensorMap v_map, const PrefillArgs a) {
+  using Shape = PreShape<kPair>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qsm = smem;                                // nq chunks of 128 queries x 64 values
-  uint8_t* kring = qsm + a.nq * kSlotBytes;
+  uint8_t* kring = qsm + a.nq * kPreChunk;
   uint8_t* vring = kring + a.kslots * kSlotBytes;
 
   __shared__ __align__(8) uint64_t kfull[kPreMaxSlots], kempty[kPreMaxSlots], vfull[kPreMaxSlots], vempty[kPreMaxSlots];
-  __shared__ __align__(8) uint64_t q_full, s_full[2], p_full[2], pv_done[2], drain[2];
+  __shared__ __align__(8) uint64_t q_full, s_full[2], p_full[2], pv_done[2], drained;
   __shared__ uint32_t tmem_slot;
   __shared__ int scan[kPreThreads / 32];
   __shared__ int at_seq, at_tile;
   __shared__ float xch[2][kPreTile];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+  const bool leader = rank == 0;
   bool abort = false;
   if (threadIdx.x == 0) {
+    // rank 0's full barriers also count rank 1: one arrival for its copies, one
+    // per softmax warp for its weights
+    const uint32_t both = kPair && leader ? 2 : 1;
     for (int s = 0; s < kPreMaxSlots; ++s) {
-      mbar_init(&kfull[s], 1);
+      mbar_init(&kfull[s], both);
       mbar_init(&kempty[s], 1);
-      mbar_init(&vfull[s], 1);
+      mbar_init(&vfull[s], both);
       mbar_init(&vempty[s], 1);
     }
-    mbar_init(&q_full, 1);
+    mbar_init(&q_full, both);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 256);
+      mbar_init(&p_full[i], kPair ? 256 + 8 : 256);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&drain[i], 1);
     }
+    mbar_init(&drained, 1);
     at_seq = -1;
     fence_mbar_init();
   }
+  if (warp == 0 && lane < 5)
+    prefetch_tensor_map(lane == 0 ? &qn_map : (lane == 1 ? &qr_map : (lane == 2 ? &kn_map : (lane == 3 ? &kr_map : &v_map))));
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
 
-  // ---- this block's sequence and query tile: tiles in reverse order
+  // ---- this block's (pair's) sequence and query tile: tiles in reverse order
   {
     const int per = (a.S + kPreThreads - 1) / kPreThreads;
     const int s0 = threadIdx.x * per, s1 = min(a.S, s0 + per);
     int mine = 0;
-    for (int s = s0; s < s1; ++s) mine += (extent(a, s).qn + kPreTile - 1) / kPreTile;
+    for (int s = s0; s < s1; ++s) mine += (extent(a, s).qn + Shape::kQueries - 1) / Shape::kQueries;
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -135,11 +193,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       if (w < warp) base += scan[w];
       total += scan[w];
     }
-    const int want = total - 1 - static_cast<int>(blockIdx.x);
+    const int want = total - 1 - static_cast<int>(kPair ? blockIdx.x >> 1 : blockIdx.x);
     int at = base + incl - mine;
     if (want >= at && want < at + mine) {
       for (int s = s0; s < s1; ++s) {
-        const int n = (extent(a, s).qn + kPreTile - 1) / kPreTile;
+        const int n = (extent(a, s).qn + Shape::kQueries - 1) / Shape::kQueries;
         if (want < at + n) {
           at_tile = want - at;
           at_seq = s;
@@ -150,22 +208,29 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     }
     __syncthreads();
   }
-  if (at_seq < 0) return;                             // more blocks than tiles
+  if (at_seq < 0) return;                             // more blocks than tiles (both blocks of a pair)
   if (warp == 1) {
-    tmem_alloc(&tmem_slot, 512);
-    tmem_relinquish();
+    if (kPair) {
+      tmem_alloc_pair(&tmem_slot, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&tmem_slot, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (kPair) cluster_sync_all();                      // both blocks' barriers and TMEM exist
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const Extent ex = extent(a, at_seq);
   const int h = blockIdx.y;
-  const int qi0 = at_tile * kPreTile;                 // first query of the tile, within its sequence
-  const int rows = min(kPreTile, ex.qn - qi0);
-  // keys visible to the tile's first and last query
+  const int pq0 = at_tile * Shape::kQueries;          // first query of the block or pair, within its sequence
+  const int qi0 = pq0 + static_cast<int>(rank) * kPreTile;      // ... and of this block
+  const int rows = clamp_to(ex.qn - qi0, kPreTile);   // (0 in rank 1 of a pair whose sequence ends in rank 0)
+  // keys visible to this block's first query, and to the last of the pair
   const int see0 = a.causal ? clamp_to(qi0 + 1 + ex.kn - ex.qn, ex.kn) : ex.kn;
-  const int see1 = a.causal ? clamp_to(qi0 + rows + ex.kn - ex.qn, ex.kn) : ex.kn;
+  const int see1 = a.causal ? clamp_to(min(pq0 + Shape::kQueries, ex.qn) + ex.kn - ex.qn, ex.kn) : ex.kn;
   const int tiles = (see1 + kPreTile - 1) / kPreTile;
 
   if (warp == 0) {
@@ -174,22 +239,26 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     int fills = 0;
     if (tiles > 0) {
       if (elect_one()) {
-        mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(a.nq * kSlotBytes));
-        for (int k = 0; k + 1 < a.nq; ++k) tma_box_3d(qsm + k * kSlotBytes, &qn_map, k * 64, h, ex.q0 + qi0, &q_full);
-        tma_box_3d(qsm + (a.nq - 1) * kSlotBytes, &qr_map, 0, h, ex.q0 + qi0, &q_full);
+        mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(a.nq * kPreChunk));
+        for (int k = 0; k + 1 < a.nq; ++k) tma_box_3d(qsm + k * kPreChunk, &qn_map, k * 64, h, ex.q0 + qi0, &q_full);
+        tma_box_3d(qsm + (a.nq - 1) * kPreChunk, &qr_map, 0, h, ex.q0 + qi0, &q_full);
       }
       __syncwarp();
     }
     for (int t = 0; t < tiles && !abort; ++t) {
-      const int tok = ex.k0 + t * kPreTile;
-      for (int k = 0; k < a.nq; ++k) {
-        if (!warp_wait(&kempty[r.slot], r.turn ^ 1u, abort)) break;
+      const int tok = ex.k0 + t * kPreTile + static_cast<int>(rank) * Shape::kKeyRows;
+      for (int k = 0; k < a.nq; k += Shape::kKeyChunks) {
+        if (!warp_wait_in<kPair>(&kempty[r.slot], r.turn ^ 1u, abort)) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&kfull[r.slot], kSlotBytes);
-          if (k + 1 < a.nq)
-            tma_box_3d(kring + r.slot * kSlotBytes, &kn_map, k * 64, h, tok, &kfull[r.slot]);
-          else
-            tma_box_3d(kring + r.slot * kSlotBytes, &kr_map, 0, 0, tok, &kfull[r.slot]);
+          const int n = min(Shape::kKeyChunks, a.nq - k);       // chunks of this slot
+          uint8_t* dst = kring + r.slot * kSlotBytes;
+          mbar_arrive_expect_tx(&kfull[r.slot], static_cast<uint32_t>(n * Shape::kKeyChunkBytes));
+          for (int x = 0; x < n; ++x) {
+            if (k + x + 1 < a.nq)
+              tma_box_3d(dst + x * Shape::kKeyChunkBytes, &kn_map, (k + x) * 64, h, tok, &kfull[r.slot]);
+            else
+              tma_box_3d(dst + x * Shape::kKeyChunkBytes, &kr_map, 0, 0, tok, &kfull[r.slot]);
+          }
         }
         __syncwarp();
         r.step();
@@ -197,22 +266,25 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
     }
     if (abort) {
+      // give the copies in flight a bounded time to land (rank 0's barriers may
+      // wait for rank 1 as well: bounded all the same)
       drain_copies(kfull, fills, r.n);
       bool late = false;
       if (tiles > 0) mbar_wait(&q_full, 0, late);
     }
   } else if (warp == 3) {
     // ---- values
+    const int half = kPair ? a.dvn >> 1 : a.dvn;      // this block's columns
+    const int v0 = static_cast<int>(rank) * half, nv = (half + 63) >> 6;
     Ring r(a.vslots);
     int fills = 0;
     for (int t = 0; t < tiles && !abort; ++t) {
-      const int tok = t * kPreTile;
-      for (int j = 0; j < kPreTile / kVTok && tok + j * kVTok < see1; ++j) {
-        if (!warp_wait(&vempty[r.slot], r.turn ^ 1u, abort)) break;
+      for (int tok = t * kPreTile; tok < min((t + 1) * kPreTile, see1); tok += Shape::kValRows) {
+        if (!warp_wait_in<kPair>(&vempty[r.slot], r.turn ^ 1u, abort)) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&vfull[r.slot], static_cast<uint32_t>(a.nv * kVTok * 128));
-          for (int k = 0; k < a.nv; ++k)
-            tma_box_3d(vring + r.slot * kSlotBytes + k * kVTok * 128, &v_map, k * 64, h, ex.k0 + tok + j * kVTok,
+          mbar_arrive_expect_tx(&vfull[r.slot], static_cast<uint32_t>(nv * Shape::kValBlockBytes));
+          for (int k = 0; k < nv; ++k)
+            tma_box_3d(vring + r.slot * kSlotBytes + k * Shape::kValBlockBytes, &v_map, v0 + k * 64, h, ex.k0 + tok,
                        &vfull[r.slot]);
         }
         __syncwarp();
@@ -221,68 +293,100 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
     }
     if (abort) drain_copies(vfull, fills, r.n);
-  } else if (warp == 1) {
-    // ---- score products S = Q K^T
-    constexpr uint32_t idesc = idesc_bf16(128, 128);
-    const uint32_t q_a = smem_u32(qsm), ring_a = smem_u32(kring);
-    Ring r(a.kslots);
-    if (tiles > 0) warp_wait(&q_full, 0, abort);
-    for (int t = 0; t < tiles && !abort; ++t) {
-      const uint32_t d = tmem + kPreScol + static_cast<uint32_t>(t & 1) * 128u;
-      // tile t - 2's weights, which lie over its scores, have been multiplied
-      if (t >= 2 && !warp_wait(&pv_done[t & 1], static_cast<uint32_t>((t >> 1) + 1) & 1u, abort)) break;
-      for (int k = 0; k < a.nq; ++k) {
-        if (!warp_wait(&kfull[r.slot], r.turn, abort)) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t sa = q_a + static_cast<uint32_t>(k) * kSlotBytes;
-          const uint32_t sb = ring_a + static_cast<uint32_t>(r.slot) * kSlotBytes;
+  } else if (warp == 1 && leader) {
+    // ---- the products
+    constexpr uint32_t idesc_s = idesc_bf16(Shape::kQueries, 128);
+    const uint32_t idesc_o = idesc_bf16(Shape::kQueries, a.dvn) | kIdescBMn;
+    const uint32_t q_a = smem_u32(qsm), k_a = smem_u32(kring), v_a = smem_u32(vring);
+    const int nv = ((kPair ? a.dvn >> 1 : a.dvn) + 63) >> 6;
+    Ring rk(a.kslots), rv(a.vslots);
+    if (tiles > 0) warp_wait_in<kPair>(&q_full, 0, abort);
+    for (int t = 0; t <= tiles && !abort; ++t) {
+      if (t < tiles) {
+        // S(t) = Q K^T; its score tile is free: the weights over it were
+        // waited for and their product issued one turn ago
+        const uint32_t d = tmem + kPreScol + static_cast<uint32_t>(t & 1) * 128u;
+        for (int k = 0; k < a.nq; k += Shape::kKeyChunks) {
+          if (!warp_wait_in<kPair>(&kfull[rk.slot], rk.turn, abort)) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t sa = q_a + static_cast<uint32_t>(k) * kPreChunk;
+            const uint32_t sb = k_a + static_cast<uint32_t>(rk.slot) * kSlotBytes;
 #pragma unroll
-          for (int m = 0; m < 4; ++m)
-            mma_bf16(d, sdesc_sw128(sa + m * 32), sdesc_sw128(sb + m * 32), idesc, (k | m) != 0);
-          mma_commit(&kempty[r.slot]);
-          if (k + 1 == a.nq) mma_commit(&s_full[t & 1]);
+            for (int x = 0; x < Shape::kKeyChunks; ++x) {
+              if (k + x >= a.nq) break;
+#pragma unroll
+              for (int m = 0; m < 4; ++m)
+                mma_bf16_of<kPair>(d, sdesc_sw128(sa + x * kPreChunk + m * 32),
+                                   sdesc_sw128(sb + x * Shape::kKeyChunkBytes + m * 32), idesc_s, (k | x | m) != 0);
+            }
+            mma_commit_of<kPair>(&kempty[rk.slot]);
+            if (k + Shape::kKeyChunks >= a.nq) mma_commit_of<kPair>(&s_full[t & 1]);
+          }
+          __syncwarp();
+          rk.step();
         }
-        __syncwarp();
-        r.step();
+      }
+      if (t > 0 && !abort) {
+        // O += P(u) V(u), u = t - 1
+        const int u = t - 1;
+        const int valid = min(kPreTile, see1 - u * kPreTile);
+        const int ks = (valid + 15) >> 4;             // 16-key steps that hold anything
+        const uint32_t p = tmem + kPreScol + static_cast<uint32_t>(u & 1) * 128u;
+        if (!warp_wait_in<kPair>(&p_full[u & 1], static_cast<uint32_t>(u >> 1) & 1u, abort)) break;
+        constexpr int kSteps = Shape::kValRows / 16;
+        for (int j = 0; kSteps * j < ks; ++j) {
+          if (!warp_wait_in<kPair>(&vfull[rv.slot], rv.turn, abort)) break;
+          clear_values<Shape::kValRows>(vring + rv.slot * kSlotBytes, nv, valid - j * Shape::kValRows, lane);
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t bd =
+                sdesc_mn_sw128(v_a + static_cast<uint32_t>(rv.slot) * kSlotBytes, Shape::kValBlockBytes);
+#pragma unroll
+            for (int m = 0; m < kSteps; ++m) {
+              const int step = kSteps * j + m;        // the weights of keys 64.. start 64 columns on
+              if (step < ks)
+                mma_bf16_ts_of<kPair>(tmem, p + static_cast<uint32_t>((step >> 2) * 64 + (step & 3) * 8), bd + m * 128,
+                                      idesc_o, (u | step) != 0);
+            }
+            mma_commit_of<kPair>(&vempty[rv.slot]);
+            if (kSteps * (j + 1) >= ks) mma_commit_of<kPair>(&pv_done[u & 1]);
+          }
+          __syncwarp();
+          rv.step();
+        }
       }
     }
-    drain_mmas(&drain[0], abort);
-  } else if (warp == 2) {
-    // ---- output products O += P V
-    const uint32_t idesc = idesc_bf16(128, (a.dv + 15) & ~15) | kIdescBMn;
-    const uint32_t ring_a = smem_u32(vring);
+    drain_mmas<kPair>(&drained, abort);
+  } else if (kPair && warp == 1) {
+    // ---- rank 1: its queries and keys have landed
+    Ring r(a.kslots);
+    if (tiles > 0 && warp_wait(&q_full, 0, abort)) {
+      if (elect_one()) mbar_arrive_remote(&q_full, 0);
+      __syncwarp();
+    }
+    for (int t = 0; t < tiles && !abort; ++t) {
+      if (!warp_wait(&kfull[r.slot], r.turn, abort)) break;     // (one slot a tile)
+      if (elect_one()) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&kfull[r.slot]), 0));
+      __syncwarp();
+      r.step();
+    }
+  } else if (kPair && warp == 2 && !leader) {
+    // ---- rank 1: its values have landed
+    const int nv = ((a.dvn >> 1) + 63) >> 6;
     Ring r(a.vslots);
     for (int t = 0; t < tiles && !abort; ++t) {
-      const int valid = min(kPreTile, see1 - t * kPreTile);
-      const int ks = (valid + 15) >> 4;
-      const uint32_t p = tmem + kPreScol + static_cast<uint32_t>(t & 1) * 128u;
-      if (!warp_wait(&p_full[t & 1], static_cast<uint32_t>(t >> 1) & 1u, abort)) break;
-      for (int j = 0; 2 * j < ks; ++j) {
-        if (!warp_wait(&vfull[r.slot], r.turn, abort)) break;
-        const int z0 = valid - j * kVTok;
-        if (z0 < kVTok) {
-          // keys of this slot that no query of the tile sees may hold anything
-          // (0 x NaN): their weights are 0 and they are made 0 too
-          for (int k = 0; k < a.nv; ++k) zero_rows(vring + r.slot * kSlotBytes + k * kVTok * 128, z0, kVTok, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t bd = sdesc_mn_sw128(ring_a + static_cast<uint32_t>(r.slot) * kSlotBytes, kVTok * 128);
-          // the weights of keys 64.. start 64 columns on
-          const uint32_t pj = p + static_cast<uint32_t>((j >> 1) * 64 + (j & 1) * 16);
-          mma_bf16_ts(tmem, pj, bd, idesc, (t | j) != 0);
-          if (2 * j + 1 < ks) mma_bf16_ts(tmem, pj + 8, bd + 128u, idesc, 1u);
-          mma_commit(&vempty[r.slot]);
-          if (2 * j + 2 >= ks) mma_commit(&pv_done[t & 1]);
-        }
-        __syncwarp();
-        r.step();
+      if (!warp_wait(&vfull[r.slot], r.turn, abort)) break;
+      const bool cleared = clear_values<Shape::kValRows>(vring + r.slot * kSlotBytes, nv, see1 - t * kPreTile, lane);
+      if (elect_one()) {
+        if (cleared)
+          mbar_arrive_remote(&vfull[r.slot], 0);
+        else
+          mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&vfull[r.slot]), 0));
       }
+      __syncwarp();
+      r.step();
     }
-    drain_mmas(&drain[1], abort);
   } else if (warp >= 4) {
     // ---- softmax.  Warps w and w + 4 hold the same 32 queries and meet at
     // named barriers, so they walk every tile even after a wait has given up.
@@ -295,7 +399,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     for (int t = 0; t < tiles; ++t) {
       const uint32_t sb = tl + kPreScol + static_cast<uint32_t>((t & 1) * 128 + g * 64);
       uint32_t r[64];
-      mbar_wait(&s_full[t & 1], static_cast<uint32_t>(t >> 1) & 1u, abort);
+      wait_mma<kPair>(&s_full[t & 1], static_cast<uint32_t>(t >> 1) & 1u, abort);
       __syncwarp();
       tc_fence_after();
       tmem_ld_cols<64>(sb, r);
@@ -328,7 +432,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (t > 0) {
           const float f = exp2_fast(m - mn);
           l *= f;
-          mbar_wait(&pv_done[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1) & 1u, abort);
+          wait_mma<kPair>(&pv_done[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1) & 1u, abort);
           __syncwarp();
           tc_fence_after();
           for (int c = g * (dvp >> 1); c < (g + 1) * (dvp >> 1); c += 16) {
@@ -363,14 +467,21 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       tmem_st_cols<32>(sb, p);
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&p_full[t & 1]);
+      if (kPair && !leader) {
+        // (the weights are in TMEM, complete and fenced; there is no memory for a
+        // release to order, and it would take 1 us)
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&p_full[t & 1]), 0));
+      } else {
+        mbar_arrive(&p_full[t & 1]);
+      }
     }
     // ---- output
     xch[g][row] = l;
     named_sync(1 + q4, 64);
     l = xch[0][row] + xch[1][row];
     if (tiles > 0) {
-      mbar_wait(&pv_done[(tiles - 1) & 1], static_cast<uint32_t>((tiles - 1) >> 1) & 1u, abort);
+      wait_mma<kPair>(&pv_done[(tiles - 1) & 1], static_cast<uint32_t>((tiles - 1) >> 1) & 1u, abort);
       __syncwarp();
       tc_fence_after();
     }
@@ -402,25 +513,59 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   if (abort) atomicOr(&g_mla_prefill_error, kErrTimeout);
   tc_fence_before();
   __syncthreads();
+  if (kPair) cluster_sync_all();                      // no MMA or arrival of either block is under way
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) {
+    if (kPair)
+      tmem_dealloc_pair(tmem, 512);
+    else
+      tmem_dealloc(tmem, 512);
+  }
 }
 
 // ------------------------------------------------------------------ host
-static std::atomic<bool> g_prefill_attr[64];
+static std::atomic<bool> g_prefill_attr[2][64];
+
+template <bool kPair>
+static cudaError_t launch_prefill(const MlaPrefillProblem& p, PrefillArgs a, const DeviceInfo& dev, cudaStream_t s) {
+  using Shape = PreShape<kPair>;
+  auto kern = mla_prefill_kernel<kPair>;
+  cudaError_t e;
+  if (!g_prefill_attr[kPair ? 1 : 0][dev.device].load(std::memory_order_acquire)) {
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kPreSmem - static_cast<int>(fa.sharedSizeBytes));
+    if (e != cudaSuccess) return e;
+    g_prefill_attr[kPair ? 1 : 0][dev.device].store(true, std::memory_order_release);
+  }
+  // N of the output product: a multiple of 16, of 32 over a pair
+  a.dvn = kPair ? (p.dv + 31) & ~31 : (p.dv + 15) & ~15;
+  const int fixed = a.nq * kPreChunk + 1024;
+  const int slots = (kPreSmem - kPreStatic - fixed) / kSlotBytes;   // 5 or 6
+  a.vslots = slots / 2;
+  a.kslots = slots - a.vslots;
+  CUtensorMap m[5];
+  if ((e = mla_tensor_map(&m[0], p.q_nope.p, p.dn, p.H, p.Tq, p.q_nope.head, p.q_nope.tok, 64, 1, kPreTile)) !=
+          cudaSuccess ||
+      (e = mla_tensor_map(&m[1], p.q_rope.p, kMlaRope, p.H, p.Tq, p.q_rope.head, p.q_rope.tok, 64, 1, kPreTile)) !=
+          cudaSuccess ||
+      (e = mla_tensor_map(&m[2], p.k_nope.p, p.dn, p.H, p.Tk, p.k_nope.head, p.k_nope.tok, 64, 1, Shape::kKeyRows)) !=
+          cudaSuccess ||
+      (e = mla_tensor_map(&m[3], p.k_rope.p, kMlaRope, 1, p.Tk, kMlaRope, p.k_rope.tok, 64, 1, Shape::kKeyRows)) !=
+          cudaSuccess ||
+      (e = mla_tensor_map(&m[4], p.v.p, p.dv, p.H, p.Tk, p.v.head, p.v.tok, 64, 1, Shape::kValRows)) != cudaSuccess)
+    return e;
+  // at most one partly filled query tile per sequence
+  const unsigned tiles = static_cast<unsigned>(p.Tq / Shape::kQueries + p.S);
+  return mla_launch_clusters(kern, dim3(tiles * (kPair ? 2 : 1), static_cast<unsigned>(p.H)), kPair ? 2 : 1, kPreThreads,
+                             fixed + slots * kSlotBytes, s, m[0], m[1], m[2], m[3], m[4], a);
+}
 
 cudaError_t launch_mla_prefill(const MlaPrefillProblem& p, const DeviceInfo& dev, cudaStream_t s) {
   if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
-  cudaError_t e = mla_bind_context();
+  const cudaError_t e = mla_bind_context();
   if (e != cudaSuccess) return e;
-  if (!g_prefill_attr[dev.device].load(std::memory_order_acquire)) {
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, mla_prefill_kernel)) != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kPreSmem - static_cast<int>(fa.sharedSizeBytes));
-    if (e != cudaSuccess) return e;
-    g_prefill_attr[dev.device].store(true, std::memory_order_release);
-  }
   PrefillArgs a{};
   a.cu_q = p.cu_q;
   a.cu_k = p.cu_k;
@@ -435,31 +580,12 @@ cudaError_t launch_mla_prefill(const MlaPrefillProblem& p, const DeviceInfo& dev
   a.dn = p.dn;
   a.dv = p.dv;
   a.nq = static_cast<int>(ceil_div(p.dn, 64)) + 1;
-  a.nv = static_cast<int>(ceil_div(p.dv, 64));
   a.flip = p.scale < 0.f;
   a.c = positive_scale(a.flip ? -p.scale : p.scale);
   a.causal = p.causal;
-  const int fixed = a.nq * kSlotBytes + 1024;
-  int slots = (kPreSmem - 2048 - fixed) / kSlotBytes;
-  if (slots > kPreMaxSlots) slots = kPreMaxSlots;
-  a.vslots = slots / 2;
-  a.kslots = slots - a.vslots;
-
-  CUtensorMap m[5];
-  if ((e = mla_tensor_map(&m[0], p.q_nope.p, p.dn, p.H, p.Tq, p.q_nope.head, p.q_nope.tok, 64, 1, kPreTile)) !=
-          cudaSuccess ||
-      (e = mla_tensor_map(&m[1], p.q_rope.p, kMlaRope, p.H, p.Tq, p.q_rope.head, p.q_rope.tok, 64, 1, kPreTile)) !=
-          cudaSuccess ||
-      (e = mla_tensor_map(&m[2], p.k_nope.p, p.dn, p.H, p.Tk, p.k_nope.head, p.k_nope.tok, 64, 1, kPreTile)) !=
-          cudaSuccess ||
-      (e = mla_tensor_map(&m[3], p.k_rope.p, kMlaRope, 1, p.Tk, kMlaRope, p.k_rope.tok, 64, 1, kPreTile)) !=
-          cudaSuccess ||
-      (e = mla_tensor_map(&m[4], p.v.p, p.dv, p.H, p.Tk, p.v.head, p.v.tok, 64, 1, kVTok)) != cudaSuccess)
-    return e;
-  // at most one partly filled query tile per sequence
-  const unsigned tiles = static_cast<unsigned>(p.Tq / kPreTile + p.S);
-  return mla_launch(mla_prefill_kernel, dim3(tiles, static_cast<unsigned>(p.H)), kPreThreads,
-                    fixed + slots * kSlotBytes, s, m[0], m[1], m[2], m[3], m[4], a);
+  // a pair where the average prompt fills more than one block of it
+  return p.Tq > static_cast<int64_t>(p.S) * kPreTile ? launch_prefill<true>(p, a, dev, s)
+                                                     : launch_prefill<false>(p, a, dev, s);
 }
 
 uint32_t mla_prefill_read_clear_error() { return read_clear_word(g_mla_prefill_error); }
