@@ -105,6 +105,40 @@ __device__ __forceinline__ Extent extent(const PrefillArgs& a, int s) {
   return e;
 }
 
+// Sequence and query tile (of kQ queries) of a block, the tiles taken in
+// reverse order; found by each warp for itself.  False past the last tile.
+template <int kQ>
+__device__ __forceinline__ bool find_tile(const PrefillArgs& a, int block, int& seq, int& tile) {
+  const int lane = threadIdx.x & 31;
+  const int per = (a.S + 31) >> 5, s0 = min(a.S, lane * per), s1 = min(a.S, s0 + per);
+  int mine = 0;
+#pragma unroll 4
+  for (int s = s0; s < s1; ++s) mine += (extent(a, s).qn + kQ - 1) / kQ;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const int want = __shfl_sync(0xFFFFFFFFu, incl, 31) - 1 - block;
+  int at = incl - mine;
+  const bool here = want >= at && want < incl;
+  seq = tile = 0;
+  if (here) {
+    for (seq = s0; seq < s1; ++seq) {
+      const int n = (extent(a, seq).qn + kQ - 1) / kQ;
+      if (want < at + n) break;
+      at += n;
+    }
+    tile = want - at;
+  }
+  const uint32_t hit = __ballot_sync(0xFFFFFFFFu, here);
+  if (hit == 0) return false;
+  seq = __shfl_sync(0xFFFFFFFFu, seq, __ffs(hit) - 1);
+  tile = __shfl_sync(0xFFFFFFFFu, tile, __ffs(hit) - 1);
+  return true;
+}
+
 // Keys of a value slot that no query of the tile sees may hold anything (0 x
 // NaN): their weights are 0 and they are made 0 too, by one warp.  `valid`: the
 // slot's keys that count.  True if there were any to clear.
@@ -130,7 +164,8 @@ template <bool kPair>
 __global__ void __launch_bounds__(kPreThreads, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_constant__ CUtensorMap qr_map,
                        const __grid_constant__ CUtensorMap kn_map, const __grid_constant__ CUtensorMap kr_map,
-                       const __grid_constant__ CUtensorMap v_map, const PrefillArgs a) {
+                       const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap o_map,
+                       const PrefillArgs a) {
   using Shape = PreShape<kPair>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -141,8 +176,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   __shared__ __align__(8) uint64_t kfull[kPreMaxSlots], kempty[kPreMaxSlots], vfull[kPreMaxSlots], vempty[kPreMaxSlots];
   __shared__ __align__(8) uint64_t q_full, s_full[2], p_full[2], pv_done[2], drained;
   __shared__ uint32_t tmem_slot;
-  __shared__ int scan[kPreThreads / 32];
-  __shared__ int at_seq, at_tile;
   __shared__ float xch[2][kPreTile];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -166,49 +199,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(&drained, 1);
-    at_seq = -1;
     fence_mbar_init();
   }
   if (warp == 0 && lane < 5)
     prefetch_tensor_map(lane == 0 ? &qn_map : (lane == 1 ? &qr_map : (lane == 2 ? &kn_map : (lane == 3 ? &kr_map : &v_map))));
-  griddep_wait();
-  if (threadIdx.x == 0) griddep_launch_dependents();
-
-  // ---- this block's (pair's) sequence and query tile: tiles in reverse order
-  {
-    const int per = (a.S + kPreThreads - 1) / kPreThreads;
-    const int s0 = threadIdx.x * per, s1 = min(a.S, s0 + per);
-    int mine = 0;
-    for (int s = s0; s < s1; ++s) mine += (extent(a, s).qn + Shape::kQueries - 1) / Shape::kQueries;
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    int base = 0, total = 0;
-    for (int w = 0; w < kPreThreads / 32; ++w) {
-      if (w < warp) base += scan[w];
-      total += scan[w];
-    }
-    const int want = total - 1 - static_cast<int>(kPair ? blockIdx.x >> 1 : blockIdx.x);
-    int at = base + incl - mine;
-    if (want >= at && want < at + mine) {
-      for (int s = s0; s < s1; ++s) {
-        const int n = (extent(a, s).qn + Shape::kQueries - 1) / Shape::kQueries;
-        if (want < at + n) {
-          at_tile = want - at;
-          at_seq = s;
-          break;
-        }
-        at += n;
-      }
-    }
-    __syncthreads();
-  }
-  if (at_seq < 0) return;                             // more blocks than tiles (both blocks of a pair)
   if (warp == 1) {
     if (kPair) {
       tmem_alloc_pair(&tmem_slot, 512);
@@ -223,7 +217,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   if (kPair) cluster_sync_all();                      // both blocks' barriers and TMEM exist
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const Extent ex = extent(a, at_seq);
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  int at_seq, at_tile;
+  // (a block or pair past the last tile has nothing to do but meet the others at the end)
+  const bool work = find_tile<Shape::kQueries>(a, static_cast<int>(kPair ? blockIdx.x >> 1 : blockIdx.x), at_seq, at_tile);
+  const Extent ex = work ? extent(a, at_seq) : Extent{0, 0, 0, 0};
   const int h = blockIdx.y;
   const int pq0 = at_tile * Shape::kQueries;          // first query of the block or pair, within its sequence
   const int qi0 = pq0 + static_cast<int>(rank) * kPreTile;      // ... and of this block
@@ -488,24 +487,41 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     const float f = l == 0.f ? 0.f : 1.0f / l;
     const int64_t tok = static_cast<int64_t>(ex.q0) + qi0 + row;
     __nv_bfloat16* dst = a.out + tok * a.o_tok + h * a.o_head;
+    // A full tile goes through shared memory (every MMA that reads it is done)
+    // and out by tensor stores, 64 values of 128 queries each; rows of a tile
+    // that ends a sequence are stored one by one, so that the next sequence's
+    // stay untouched.  (Row by row throughout: 7500 cycles a block, 16 of each
+    // 128-byte line at a time.)
+    const bool full_tile = rows == kPreTile;
+#pragma unroll 1
     for (int c = g * (dvp >> 1); c < (g + 1) * (dvp >> 1); c += 16) {
       uint32_t o[16];
       if (tiles > 0) {
         tmem_ld16(tl + c, o);
         tmem_wait_ld_of(o);
       }
-      if (row < rows) {
+      uint4 w[2];
+      uint32_t* wv = reinterpret_cast<uint32_t*>(w);
 #pragma unroll
-        for (int e = 0; e < 16; e += 8) {
-          if (c + e >= a.dv) break;                   // dv is a multiple of 8
-          uint32_t w[4];
+      for (int x = 0; x < 8; ++x)
+        wv[x] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * x]) * f, __uint_as_float(o[2 * x + 1]) * f);
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            w[x] = l == 0.f ? 0u
-                            : pack_bf16x2(__uint_as_float(o[e + 2 * x]) * f, __uint_as_float(o[e + 2 * x + 1]) * f);
-          *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+      for (int x = 0; x < 2; ++x) {
+        const int e = c + 8 * x;                      // dv is a multiple of 8
+        if (full_tile)
+          *reinterpret_cast<uint4*>(smem + (e >> 6) * kPreChunk + row * 128 + ((((e & 63) >> 3) ^ (row & 7)) << 4)) = w[x];
+        else if (row < rows && e < a.dv)
+          *reinterpret_cast<uint4*>(dst + e) = w[x];
       }
+    }
+    if (full_tile) {
+      fence_proxy_async_smem();
+      named_sync(5, 256);
+      if (warp == 4 && elect_one()) {
+        for (int k = 0; k * 64 < a.dv; ++k) tma_store_3d(&o_map, smem + k * kPreChunk, k * 64, h, ex.q0 + qi0);
+        tma_store_wait();
+      }
+      __syncwarp();
     }
     if (g == 0 && row < rows && a.lse != nullptr)
       a.lse[tok * a.H + h] = l == 0.f ? -INFINITY : (m + log2_fast(l)) * kLn2;
@@ -545,7 +561,7 @@ static cudaError_t launch_prefill(const MlaPrefillProblem& p, PrefillArgs a, con
   const int slots = (kPreSmem - kPreStatic - fixed) / kSlotBytes;   // 5 or 6
   a.vslots = slots / 2;
   a.kslots = slots - a.vslots;
-  CUtensorMap m[5];
+  CUtensorMap m[6];
   if ((e = mla_tensor_map(&m[0], p.q_nope.p, p.dn, p.H, p.Tq, p.q_nope.head, p.q_nope.tok, 64, 1, kPreTile)) !=
           cudaSuccess ||
       (e = mla_tensor_map(&m[1], p.q_rope.p, kMlaRope, p.H, p.Tq, p.q_rope.head, p.q_rope.tok, 64, 1, kPreTile)) !=
@@ -554,12 +570,13 @@ static cudaError_t launch_prefill(const MlaPrefillProblem& p, PrefillArgs a, con
           cudaSuccess ||
       (e = mla_tensor_map(&m[3], p.k_rope.p, kMlaRope, 1, p.Tk, kMlaRope, p.k_rope.tok, 64, 1, Shape::kKeyRows)) !=
           cudaSuccess ||
-      (e = mla_tensor_map(&m[4], p.v.p, p.dv, p.H, p.Tk, p.v.head, p.v.tok, 64, 1, Shape::kValRows)) != cudaSuccess)
+      (e = mla_tensor_map(&m[4], p.v.p, p.dv, p.H, p.Tk, p.v.head, p.v.tok, 64, 1, Shape::kValRows)) != cudaSuccess ||
+      (e = mla_tensor_map(&m[5], p.out.p, p.dv, p.H, p.Tq, p.out.head, p.out.tok, 64, 1, kPreTile)) != cudaSuccess)
     return e;
   // at most one partly filled query tile per sequence
   const unsigned tiles = static_cast<unsigned>(p.Tq / Shape::kQueries + p.S);
   return mla_launch_clusters(kern, dim3(tiles * (kPair ? 2 : 1), static_cast<unsigned>(p.H)), kPair ? 2 : 1, kPreThreads,
-                             fixed + slots * kSlotBytes, s, m[0], m[1], m[2], m[3], m[4], a);
+                             fixed + slots * kSlotBytes, s, m[0], m[1], m[2], m[3], m[4], m[5], a);
 }
 
 cudaError_t launch_mla_prefill(const MlaPrefillProblem& p, const DeviceInfo& dev, cudaStream_t s) {
