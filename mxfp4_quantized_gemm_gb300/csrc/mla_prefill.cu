@@ -40,9 +40,13 @@
 // copy) and 16 for each further copy.  With one or two slots a tile both stay
 // below the MMAs' time; with four (16 KB) they did not.
 //
-// Blocks are ordered head by head and, within a head, from the last queries
-// (most keys) to the first: blocks that run together share a head's keys and
-// values in L2, and the shortest run last.
+// The grid is one block (or pair) per SM (pair of SMs) that walks query tiles:
+// the next tile's copies and first scores run while the softmax warps write the
+// last one out.  (A block per tile spent 14000 cycles on each, the time of six
+// key tiles, before its first and after its last product.)  Tiles are ordered
+// head by head and, within a head, from the last queries (most keys) to the
+// first, and dealt in rounds that change direction: blocks that run together
+// share a head's keys and values in L2, and their loads even out.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <atomic>
@@ -74,6 +78,7 @@ struct PreShape {
   static constexpr int kValRows = kPair ? 128 : 64;     // keys in a value slot
   static constexpr int kValBlockBytes = kValRows * 128; // 64 values of them
   static constexpr int kQueries = kPair ? 256 : 128;
+  static constexpr int kBlocks = kPair ? 2 : 1;
 };
 
 struct PrefillArgs {
@@ -105,39 +110,78 @@ __device__ __forceinline__ Extent extent(const PrefillArgs& a, int s) {
   return e;
 }
 
-// Sequence and query tile (of kQ queries) of a block, the tiles taken in
-// reverse order; found by each warp for itself.  False past the last tile.
-template <int kQ>
-__device__ __forceinline__ bool find_tile(const PrefillArgs& a, int block, int& seq, int& tile) {
-  const int lane = threadIdx.x & 31;
-  const int per = (a.S + 31) >> 5, s0 = min(a.S, lane * per), s1 = min(a.S, s0 + per);
-  int mine = 0;
+// A query tile of a block or pair, and what its keys amount to.
+struct QueryTile {
+  Extent ex;
+  int h;
+  int qi0;     // this block's first query, within its sequence
+  int rows;    // this block's queries (0 in rank 1 of a pair whose sequence ends in rank 0)
+  int see0;    // keys visible to this block's first query ...
+  int see1;    // ... and to the last of the block or pair
+  int tiles;   // key tiles
+};
+
+// The query tiles of a block or pair, found by each warp for itself; a lane
+// holds the prefix sum of its share of the sequences.
+template <bool kPair>
+struct QueryTiles {
+  int s0, s1, first, incl, total, round, rank;
+  __device__ __forceinline__ QueryTiles(const PrefillArgs& a, int rank_) : round(0), rank(rank_) {
+    constexpr int kQ = PreShape<kPair>::kQueries;
+    const int lane = threadIdx.x & 31, per = (a.S + 31) >> 5;
+    s0 = min(a.S, lane * per);
+    s1 = min(a.S, s0 + per);
+    int mine = 0;
 #pragma unroll 4
-  for (int s = s0; s < s1; ++s) mine += (extent(a, s).qn + kQ - 1) / kQ;
-  int incl = mine;
+    for (int s = s0; s < s1; ++s) mine += (extent(a, s).qn + kQ - 1) / kQ;
+    incl = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  const int want = __shfl_sync(0xFFFFFFFFu, incl, 31) - 1 - block;
-  int at = incl - mine;
-  const bool here = want >= at && want < incl;
-  seq = tile = 0;
-  if (here) {
-    for (seq = s0; seq < s1; ++seq) {
-      const int n = (extent(a, seq).qn + kQ - 1) / kQ;
-      if (want < at + n) break;
-      at += n;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += v;
     }
-    tile = want - at;
+    first = incl - mine;
+    total = __shfl_sync(0xFFFFFFFFu, incl, 31);
   }
-  const uint32_t hit = __ballot_sync(0xFFFFFFFFu, here);
-  if (hit == 0) return false;
-  seq = __shfl_sync(0xFFFFFFFFu, seq, __ffs(hit) - 1);
-  tile = __shfl_sync(0xFFFFFFFFu, tile, __ffs(hit) - 1);
-  return true;
-}
+  __device__ __forceinline__ bool next(const PrefillArgs& a, QueryTile& x) {
+    constexpr int kQ = PreShape<kPair>::kQueries;
+    const int n = static_cast<int>(gridDim.x) / PreShape<kPair>::kBlocks;
+    const int c = static_cast<int>(blockIdx.x) / PreShape<kPair>::kBlocks;
+    const int64_t at = static_cast<int64_t>(round) * n + ((round & 1) ? n - 1 - c : c);
+    const int64_t all = static_cast<int64_t>(total) * a.H;
+    if (at >= all) return false;                      // (the rounds that follow lie past the end too)
+    ++round;
+    x.h = static_cast<int>(at / total);
+    const int want = total - 1 - static_cast<int>(at - static_cast<int64_t>(x.h) * total);
+    // the lane whose share holds it
+    const bool here = want >= first && want < incl;
+    int seq = 0, tile = want - first;
+    if (here)
+      for (seq = s0; seq < s1; ++seq) {
+        const int m = (extent(a, seq).qn + kQ - 1) / kQ;
+        if (tile < m) break;
+        tile -= m;
+      }
+    const int from = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
+    seq = __shfl_sync(0xFFFFFFFFu, seq, from);
+    tile = __shfl_sync(0xFFFFFFFFu, tile, from);
+    x.ex = extent(a, seq);
+    const int pq0 = tile * kQ;
+    x.qi0 = pq0 + rank * kPreTile;
+    x.rows = clamp_to(x.ex.qn - x.qi0, kPreTile);
+    const int back = x.ex.kn - x.ex.qn;
+    x.see0 = a.causal ? clamp_to(x.qi0 + 1 + back, x.ex.kn) : x.ex.kn;
+    x.see1 = a.causal ? clamp_to(min(pq0 + kQ, x.ex.qn) + back, x.ex.kn) : x.ex.kn;
+    x.tiles = (x.see1 + kPreTile - 1) / kPreTile;
+    return true;
+  }
+  // the next tile that sees any key
+  __device__ __forceinline__ bool next_real(const PrefillArgs& a, QueryTile& x) {
+    while (next(a, x))
+      if (x.tiles > 0) return true;
+    return false;
+  }
+};
 
 // Keys of a value slot that no query of the tile sees may hold anything (0 x
 // NaN): their weights are 0 and they are made 0 too, by one warp.  `valid`: the
@@ -172,6 +216,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   uint8_t* qsm = smem;                                // nq chunks of 128 queries x 64 values
   uint8_t* kring = qsm + a.nq * kPreChunk;
   uint8_t* vring = kring + a.kslots * kSlotBytes;
+  uint8_t* osm = vring + a.vslots * kSlotBytes;       // two 64-value blocks of 128 queries, on their way out
 
   __shared__ __align__(8) uint64_t kfull[kPreMaxSlots], kempty[kPreMaxSlots], vfull[kPreMaxSlots], vempty[kPreMaxSlots];
   __shared__ __align__(8) uint64_t q_full, s_full[2], p_full[2], pv_done[2], drained;
@@ -219,49 +264,43 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   const uint32_t tmem = tmem_slot;
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  int at_seq, at_tile;
-  // (a block or pair past the last tile has nothing to do but meet the others at the end)
-  const bool work = find_tile<Shape::kQueries>(a, static_cast<int>(kPair ? blockIdx.x >> 1 : blockIdx.x), at_seq, at_tile);
-  const Extent ex = work ? extent(a, at_seq) : Extent{0, 0, 0, 0};
-  const int h = blockIdx.y;
-  const int pq0 = at_tile * Shape::kQueries;          // first query of the block or pair, within its sequence
-  const int qi0 = pq0 + static_cast<int>(rank) * kPreTile;      // ... and of this block
-  const int rows = clamp_to(ex.qn - qi0, kPreTile);   // (0 in rank 1 of a pair whose sequence ends in rank 0)
-  // keys visible to this block's first query, and to the last of the pair
-  const int see0 = a.causal ? clamp_to(qi0 + 1 + ex.kn - ex.qn, ex.kn) : ex.kn;
-  const int see1 = a.causal ? clamp_to(min(pq0 + Shape::kQueries, ex.qn) + ex.kn - ex.qn, ex.kn) : ex.kn;
-  const int tiles = (see1 + kPreTile - 1) / kPreTile;
+  QueryTiles<kPair> walk(a, static_cast<int>(rank));
+  QueryTile x;
 
   if (warp == 0) {
     // ---- queries and keys
     Ring r(a.kslots);
-    int fills = 0;
-    if (tiles > 0) {
+    int fills = 0, i = 0, no = 0;
+    while (!abort && walk.next_real(a, x)) {
+      // the queries' place is free once the last scores of the tile before are formed
+      if (no > 0 && !warp_wait_in<kPair>(&s_full[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort)) break;
       if (elect_one()) {
         mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(a.nq * kPreChunk));
-        for (int k = 0; k + 1 < a.nq; ++k) tma_box_3d(qsm + k * kPreChunk, &qn_map, k * 64, h, ex.q0 + qi0, &q_full);
-        tma_box_3d(qsm + (a.nq - 1) * kPreChunk, &qr_map, 0, h, ex.q0 + qi0, &q_full);
+        for (int k = 0; k + 1 < a.nq; ++k)
+          tma_box_3d(qsm + k * kPreChunk, &qn_map, k * 64, x.h, x.ex.q0 + x.qi0, &q_full);
+        tma_box_3d(qsm + (a.nq - 1) * kPreChunk, &qr_map, 0, x.h, x.ex.q0 + x.qi0, &q_full);
       }
       __syncwarp();
-    }
-    for (int t = 0; t < tiles && !abort; ++t) {
-      const int tok = ex.k0 + t * kPreTile + static_cast<int>(rank) * Shape::kKeyRows;
-      for (int k = 0; k < a.nq; k += Shape::kKeyChunks) {
-        if (!warp_wait_in<kPair>(&kempty[r.slot], r.turn ^ 1u, abort)) break;
-        if (elect_one()) {
-          const int n = min(Shape::kKeyChunks, a.nq - k);       // chunks of this slot
-          uint8_t* dst = kring + r.slot * kSlotBytes;
-          mbar_arrive_expect_tx(&kfull[r.slot], static_cast<uint32_t>(n * Shape::kKeyChunkBytes));
-          for (int x = 0; x < n; ++x) {
-            if (k + x + 1 < a.nq)
-              tma_box_3d(dst + x * Shape::kKeyChunkBytes, &kn_map, (k + x) * 64, h, tok, &kfull[r.slot]);
-            else
-              tma_box_3d(dst + x * Shape::kKeyChunkBytes, &kr_map, 0, 0, tok, &kfull[r.slot]);
+      ++no;
+      for (int t = 0; t < x.tiles && !abort; ++t, ++i) {
+        const int tok = x.ex.k0 + t * kPreTile + static_cast<int>(rank) * Shape::kKeyRows;
+        for (int k = 0; k < a.nq; k += Shape::kKeyChunks) {
+          if (!warp_wait_in<kPair>(&kempty[r.slot], r.turn ^ 1u, abort)) break;
+          if (elect_one()) {
+            const int n = min(Shape::kKeyChunks, a.nq - k);     // chunks of this slot
+            uint8_t* dst = kring + r.slot * kSlotBytes;
+            mbar_arrive_expect_tx(&kfull[r.slot], static_cast<uint32_t>(n * Shape::kKeyChunkBytes));
+            for (int y = 0; y < n; ++y) {
+              if (k + y + 1 < a.nq)
+                tma_box_3d(dst + y * Shape::kKeyChunkBytes, &kn_map, (k + y) * 64, x.h, tok, &kfull[r.slot]);
+              else
+                tma_box_3d(dst + y * Shape::kKeyChunkBytes, &kr_map, 0, 0, tok, &kfull[r.slot]);
+            }
           }
+          __syncwarp();
+          r.step();
+          ++fills;
         }
-        __syncwarp();
-        r.step();
-        ++fills;
       }
     }
     if (abort) {
@@ -269,7 +308,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       // wait for rank 1 as well: bounded all the same)
       drain_copies(kfull, fills, r.n);
       bool late = false;
-      if (tiles > 0) mbar_wait(&q_full, 0, late);
+      if (no > 0) mbar_wait(&q_full, static_cast<uint32_t>(no - 1) & 1u, late);
     }
   } else if (warp == 3) {
     // ---- values
@@ -277,18 +316,20 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     const int v0 = static_cast<int>(rank) * half, nv = (half + 63) >> 6;
     Ring r(a.vslots);
     int fills = 0;
-    for (int t = 0; t < tiles && !abort; ++t) {
-      for (int tok = t * kPreTile; tok < min((t + 1) * kPreTile, see1); tok += Shape::kValRows) {
-        if (!warp_wait_in<kPair>(&vempty[r.slot], r.turn ^ 1u, abort)) break;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(&vfull[r.slot], static_cast<uint32_t>(nv * Shape::kValBlockBytes));
-          for (int k = 0; k < nv; ++k)
-            tma_box_3d(vring + r.slot * kSlotBytes + k * Shape::kValBlockBytes, &v_map, v0 + k * 64, h, ex.k0 + tok,
-                       &vfull[r.slot]);
+    while (!abort && walk.next_real(a, x)) {
+      for (int t = 0; t < x.tiles && !abort; ++t) {
+        for (int tok = t * kPreTile; tok < min((t + 1) * kPreTile, x.see1); tok += Shape::kValRows) {
+          if (!warp_wait_in<kPair>(&vempty[r.slot], r.turn ^ 1u, abort)) break;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&vfull[r.slot], static_cast<uint32_t>(nv * Shape::kValBlockBytes));
+            for (int k = 0; k < nv; ++k)
+              tma_box_3d(vring + r.slot * kSlotBytes + k * Shape::kValBlockBytes, &v_map, v0 + k * 64, x.h,
+                         x.ex.k0 + tok, &vfull[r.slot]);
+          }
+          __syncwarp();
+          r.step();
+          ++fills;
         }
-        __syncwarp();
-        r.step();
-        ++fills;
       }
     }
     if (abort) drain_copies(vfull, fills, r.n);
@@ -299,12 +340,40 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     const uint32_t q_a = smem_u32(qsm), k_a = smem_u32(kring), v_a = smem_u32(vring);
     const int nv = ((kPair ? a.dvn >> 1 : a.dvn) + 63) >> 6;
     Ring rk(a.kslots), rv(a.vslots);
-    if (tiles > 0) warp_wait_in<kPair>(&q_full, 0, abort);
-    for (int t = 0; t <= tiles && !abort; ++t) {
-      if (t < tiles) {
-        // S(t) = Q K^T; its score tile is free: the weights over it were
+    // O += P(u) V(u) of tile number u: `valid` of its keys count; `first` of its query tile
+    auto output = [&](int u, int valid, bool first) {
+      const int ks = (valid + 15) >> 4;               // 16-key steps that hold anything
+      const uint32_t p = tmem + kPreScol + static_cast<uint32_t>(u & 1) * 128u;
+      if (!warp_wait_in<kPair>(&p_full[u & 1], static_cast<uint32_t>(u >> 1) & 1u, abort)) return;
+      constexpr int kSteps = Shape::kValRows / 16;
+      for (int j = 0; kSteps * j < ks; ++j) {
+        if (!warp_wait_in<kPair>(&vfull[rv.slot], rv.turn, abort)) return;
+        clear_values<Shape::kValRows>(vring + rv.slot * kSlotBytes, nv, valid - j * Shape::kValRows, lane);
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t bd = sdesc_mn_sw128(v_a + static_cast<uint32_t>(rv.slot) * kSlotBytes, Shape::kValBlockBytes);
+#pragma unroll
+          for (int m = 0; m < kSteps; ++m) {
+            const int step = kSteps * j + m;          // the weights of keys 64.. start 64 columns on
+            if (step < ks)
+              mma_bf16_ts_of<kPair>(tmem, p + static_cast<uint32_t>((step >> 2) * 64 + (step & 3) * 8), bd + m * 128,
+                                    idesc_o, !first || step != 0);
+          }
+          mma_commit_of<kPair>(&vempty[rv.slot]);
+          if (kSteps * (j + 1) >= ks) mma_commit_of<kPair>(&pv_done[u & 1]);
+        }
+        __syncwarp();
+        rv.step();
+      }
+    };
+    int i = 0, no = 0;
+    while (!abort && walk.next_real(a, x)) {
+      if (!warp_wait_in<kPair>(&q_full, static_cast<uint32_t>(no) & 1u, abort)) break;
+      ++no;
+      for (int t = 0; t < x.tiles && !abort; ++t, ++i) {
+        // S(i) = Q K^T; its score tile is free: the weights over it were
         // waited for and their product issued one turn ago
-        const uint32_t d = tmem + kPreScol + static_cast<uint32_t>(t & 1) * 128u;
+        const uint32_t d = tmem + kPreScol + static_cast<uint32_t>(i & 1) * 128u;
         for (int k = 0; k < a.nq; k += Shape::kKeyChunks) {
           if (!warp_wait_in<kPair>(&kfull[rk.slot], rk.turn, abort)) break;
           tc_fence_after();
@@ -312,79 +381,57 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             const uint32_t sa = q_a + static_cast<uint32_t>(k) * kPreChunk;
             const uint32_t sb = k_a + static_cast<uint32_t>(rk.slot) * kSlotBytes;
 #pragma unroll
-            for (int x = 0; x < Shape::kKeyChunks; ++x) {
-              if (k + x >= a.nq) break;
+            for (int y = 0; y < Shape::kKeyChunks; ++y) {
+              if (k + y >= a.nq) break;
 #pragma unroll
               for (int m = 0; m < 4; ++m)
-                mma_bf16_of<kPair>(d, sdesc_sw128(sa + x * kPreChunk + m * 32),
-                                   sdesc_sw128(sb + x * Shape::kKeyChunkBytes + m * 32), idesc_s, (k | x | m) != 0);
+                mma_bf16_of<kPair>(d, sdesc_sw128(sa + y * kPreChunk + m * 32),
+                                   sdesc_sw128(sb + y * Shape::kKeyChunkBytes + m * 32), idesc_s, (k | y | m) != 0);
             }
             mma_commit_of<kPair>(&kempty[rk.slot]);
-            if (k + Shape::kKeyChunks >= a.nq) mma_commit_of<kPair>(&s_full[t & 1]);
+            if (k + Shape::kKeyChunks >= a.nq) mma_commit_of<kPair>(&s_full[i & 1]);
           }
           __syncwarp();
           rk.step();
         }
+        if (t > 0 && !abort) output(i - 1, kPreTile, t == 1);
       }
-      if (t > 0 && !abort) {
-        // O += P(u) V(u), u = t - 1
-        const int u = t - 1;
-        const int valid = min(kPreTile, see1 - u * kPreTile);
-        const int ks = (valid + 15) >> 4;             // 16-key steps that hold anything
-        const uint32_t p = tmem + kPreScol + static_cast<uint32_t>(u & 1) * 128u;
-        if (!warp_wait_in<kPair>(&p_full[u & 1], static_cast<uint32_t>(u >> 1) & 1u, abort)) break;
-        constexpr int kSteps = Shape::kValRows / 16;
-        for (int j = 0; kSteps * j < ks; ++j) {
-          if (!warp_wait_in<kPair>(&vfull[rv.slot], rv.turn, abort)) break;
-          clear_values<Shape::kValRows>(vring + rv.slot * kSlotBytes, nv, valid - j * Shape::kValRows, lane);
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t bd =
-                sdesc_mn_sw128(v_a + static_cast<uint32_t>(rv.slot) * kSlotBytes, Shape::kValBlockBytes);
-#pragma unroll
-            for (int m = 0; m < kSteps; ++m) {
-              const int step = kSteps * j + m;        // the weights of keys 64.. start 64 columns on
-              if (step < ks)
-                mma_bf16_ts_of<kPair>(tmem, p + static_cast<uint32_t>((step >> 2) * 64 + (step & 3) * 8), bd + m * 128,
-                                      idesc_o, (u | step) != 0);
-            }
-            mma_commit_of<kPair>(&vempty[rv.slot]);
-            if (kSteps * (j + 1) >= ks) mma_commit_of<kPair>(&pv_done[u & 1]);
-          }
-          __syncwarp();
-          rv.step();
-        }
-      }
+      if (!abort) output(i - 1, x.see1 - (x.tiles - 1) * kPreTile, x.tiles == 1);
     }
     drain_mmas<kPair>(&drained, abort);
   } else if (kPair && warp == 1) {
     // ---- rank 1: its queries and keys have landed
     Ring r(a.kslots);
-    if (tiles > 0 && warp_wait(&q_full, 0, abort)) {
-      if (elect_one()) mbar_arrive_remote(&q_full, 0);
+    int no = 0;
+    while (!abort && walk.next_real(a, x)) {
+      if (!warp_wait(&q_full, static_cast<uint32_t>(no) & 1u, abort)) break;
+      ++no;
+      if (elect_one()) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&q_full), 0));
       __syncwarp();
-    }
-    for (int t = 0; t < tiles && !abort; ++t) {
-      if (!warp_wait(&kfull[r.slot], r.turn, abort)) break;     // (one slot a tile)
-      if (elect_one()) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&kfull[r.slot]), 0));
-      __syncwarp();
-      r.step();
+      for (int t = 0; t < x.tiles; ++t) {
+        if (!warp_wait(&kfull[r.slot], r.turn, abort)) break;   // (one slot a tile)
+        if (elect_one()) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&kfull[r.slot]), 0));
+        __syncwarp();
+        r.step();
+      }
     }
   } else if (kPair && warp == 2 && !leader) {
     // ---- rank 1: its values have landed
     const int nv = ((a.dvn >> 1) + 63) >> 6;
     Ring r(a.vslots);
-    for (int t = 0; t < tiles && !abort; ++t) {
-      if (!warp_wait(&vfull[r.slot], r.turn, abort)) break;
-      const bool cleared = clear_values<Shape::kValRows>(vring + r.slot * kSlotBytes, nv, see1 - t * kPreTile, lane);
-      if (elect_one()) {
-        if (cleared)
-          mbar_arrive_remote(&vfull[r.slot], 0);
-        else
-          mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&vfull[r.slot]), 0));
+    while (!abort && walk.next_real(a, x)) {
+      for (int t = 0; t < x.tiles; ++t) {
+        if (!warp_wait(&vfull[r.slot], r.turn, abort)) break;
+        const bool cleared = clear_values<Shape::kValRows>(vring + r.slot * kSlotBytes, nv, x.see1 - t * kPreTile, lane);
+        if (elect_one()) {
+          if (cleared)
+            mbar_arrive_remote(&vfull[r.slot], 0);
+          else
+            mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&vfull[r.slot]), 0));
+        }
+        __syncwarp();
+        r.step();
       }
-      __syncwarp();
-      r.step();
     }
   } else if (warp >= 4) {
     // ---- softmax.  Warps w and w + 4 hold the same 32 queries and meet at
@@ -392,139 +439,154 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     const int q4 = warp & 3, g = (warp - 4) >> 2;
     const int row = q4 * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
-    const int see = row < rows ? (a.causal ? clamp_to(qi0 + row + 1 + ex.kn - ex.qn, ex.kn) : ex.kn) : 0;
     const int dvp = (a.dv + 31) & ~31;                // accumulator columns, in halves of 16
-    float m = 0.f, l = 0.f;
-    for (int t = 0; t < tiles; ++t) {
-      const uint32_t sb = tl + kPreScol + static_cast<uint32_t>((t & 1) * 128 + g * 64);
-      uint32_t r[64];
-      wait_mma<kPair>(&s_full[t & 1], static_cast<uint32_t>(t >> 1) & 1u, abort);
-      __syncwarp();
-      tc_fence_after();
-      tmem_ld_cols<64>(sb, r);
-      tmem_wait_ld_of(r);
-      const int j0 = t * kPreTile + g * 64;
-      if (a.flip) {
+    int i = 0;
+    while (walk.next(a, x)) {
+      const int back = x.ex.kn - x.ex.qn;
+      const int see = row < x.rows ? (a.causal ? clamp_to(x.qi0 + row + 1 + back, x.ex.kn) : x.ex.kn) : 0;
+      float m = 0.f, l = 0.f;
+      for (int t = 0; t < x.tiles; ++t, ++i) {
+        const uint32_t sb = tl + kPreScol + static_cast<uint32_t>((i & 1) * 128 + g * 64);
+        uint32_t r[64];
+        wait_mma<kPair>(&s_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, abort);
+        __syncwarp();
+        tc_fence_after();
+        tmem_ld_cols<64>(sb, r);
+        tmem_wait_ld_of(r);
+        const int j0 = t * kPreTile + g * 64;
+        if (a.flip) {
 #pragma unroll
-        for (int j = 0; j < 64; ++j) r[j] ^= 0x80000000u;
-      }
-      if ((t + 1) * kPreTile > see0) {
+          for (int j = 0; j < 64; ++j) r[j] ^= 0x80000000u;
+        }
+        if ((t + 1) * kPreTile > x.see0) {
 #pragma unroll
-        for (int j = 0; j < 64; ++j)
-          if (j0 + j >= see) r[j] = 0xFF800000u;
-      }
-      // four chains, so that the maximum is not a run of 64 dependent steps
-      float m4[4];
+          for (int j = 0; j < 64; ++j)
+            if (j0 + j >= see) r[j] = 0xFF800000u;
+        }
+        // four chains, so that the maximum is not a run of 64 dependent steps
+        float m4[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) m4[x] = fmaxf(__uint_as_float(r[x]), __uint_as_float(r[4 + x]));
+        for (int e = 0; e < 4; ++e) m4[e] = fmaxf(__uint_as_float(r[e]), __uint_as_float(r[4 + e]));
 #pragma unroll
-      for (int j = 8; j < 64; j += 8)
+        for (int j = 8; j < 64; j += 8)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) m4[x] = max3(m4[x], __uint_as_float(r[j + x]), __uint_as_float(r[j + 4 + x]));
-      float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.c;
-      if (t == 0 || named_sync_or(1 + q4, 64, mx - m > kMaxSlack)) {
-        xch[g][row] = mx;
-        named_sync(1 + q4, 64);
-        float mn = fmaxf(mx, xch[g ^ 1][row]);
-        if (t > 0) mn = fmaxf(mn, m);
-        if (mn == -INFINITY) mn = 0.f;                // a query that sees no key of the first tile sees none
-        if (t > 0) {
-          const float f = exp2_fast(m - mn);
-          l *= f;
-          wait_mma<kPair>(&pv_done[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1) & 1u, abort);
+          for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(r[j + e]), __uint_as_float(r[j + 4 + e]));
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.c;
+        if (t == 0 || named_sync_or(1 + q4, 64, mx - m > kMaxSlack)) {
+          xch[g][row] = mx;
+          named_sync(1 + q4, 64);
+          float mn = fmaxf(mx, xch[g ^ 1][row]);
+          if (t > 0) mn = fmaxf(mn, m);
+          if (mn == -INFINITY) mn = 0.f;              // a query that sees no key of the first tile sees none
+          if (t > 0) {
+            const float f = exp2_fast(m - mn);
+            l *= f;
+            wait_mma<kPair>(&pv_done[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort);
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = g * (dvp >> 1); c < (g + 1) * (dvp >> 1); c += 16) {
+              uint32_t o[16];
+              tmem_ld16(tl + c, o);
+              tmem_wait_ld_of(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(tl + c, o);
+            }
+            tmem_wait_st();
+          }
+          m = mn;
+          named_sync(1 + q4, 64);                     // xch is free again
+        }
+        // weights (rounded to bf16 for the MMA) and their fp32 sum (unrounded)
+        uint32_t p[32];
+        const uint64_t c2 = pair2f(a.c, a.c), m2 = pair2f(-m, -m);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          float x0, x1;
+          split2(fma2(pair2(r[2 * j], r[2 * j + 1]), c2, m2), x0, x1);
+          x0 = exp2_fast(x0);
+          x1 = exp2_fast(x1);
+          sum[j & 1] = add2(sum[j & 1], pair2f(x0, x1));
+          p[j] = pack_bf16x2(x0, x1);
+        }
+        float s0, s1;
+        split2(add2(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
+        tmem_st_cols<32>(sb, p);
+        tmem_wait_st();
+        tc_fence_before();
+        if (kPair && !leader) {
+          // (the weights are in TMEM, complete and fenced; there is no memory for
+          // a release to order, and it would take 1 us)
           __syncwarp();
-          tc_fence_after();
-          for (int c = g * (dvp >> 1); c < (g + 1) * (dvp >> 1); c += 16) {
-            uint32_t o[16];
+          if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&p_full[i & 1]), 0));
+        } else {
+          mbar_arrive(&p_full[i & 1]);
+        }
+      }
+      // ---- output
+      xch[g][row] = l;
+      named_sync(1 + q4, 64);
+      l = xch[0][row] + xch[1][row];
+      named_sync(1 + q4, 64);                         // xch is free again
+      if (x.tiles > 0) {
+        wait_mma<kPair>(&pv_done[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort);
+        __syncwarp();
+        tc_fence_after();
+      }
+      const float f = l == 0.f ? 0.f : 1.0f / l;
+      const int64_t tok = static_cast<int64_t>(x.ex.q0) + x.qi0 + row;
+      __nv_bfloat16* dst = a.out + tok * a.o_tok + x.h * a.o_head;
+      // A full tile goes out through shared memory by tensor stores, 64 values
+      // of 128 queries each (four warps at a time, through a buffer of their
+      // own); rows of a tile that ends a sequence are stored one by one, so that
+      // the next sequence's stay untouched.  (Row by row throughout, 16 of each
+      // 128-byte line at a time: 7500 cycles a tile.)
+      const bool full_tile = x.rows == kPreTile;
+      uint8_t* stage = osm + g * kPreChunk;
+      // four warps each take every second 64-value block
+#pragma unroll 1
+      for (int b = g; b * 64 < a.dv; b += 2) {
+        if (full_tile) {
+          if (row == 0) tma_store_wait_read();
+          __syncwarp();
+          named_sync(5 + g, 128);                     // the buffer has been read
+        }
+#pragma unroll 1
+        for (int c = b * 64; c < min(b * 64 + 64, dvp); c += 16) {
+          uint32_t o[16];
+          if (x.tiles > 0) {
             tmem_ld16(tl + c, o);
             tmem_wait_ld_of(o);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st16(tl + c, o);
           }
-          tmem_wait_st();
+          uint4 w[2];
+          uint32_t* wv = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            wv[e] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int e = c + 8 * y;                  // dv is a multiple of 8
+            if (full_tile)
+              *reinterpret_cast<uint4*>(stage + row * 128 + ((((e & 63) >> 3) ^ (row & 7)) << 4)) = w[y];
+            else if (row < x.rows && e < a.dv)
+              *reinterpret_cast<uint4*>(dst + e) = w[y];
+          }
         }
-        m = mn;
-        named_sync(1 + q4, 64);                       // xch is free again
+        if (full_tile) {
+          fence_proxy_async_smem();
+          named_sync(5 + g, 128);
+          if (row == 0) tma_store_3d(&o_map, stage, b * 64, x.h, x.ex.q0 + x.qi0);
+          __syncwarp();
+        }
       }
-      // weights (rounded to bf16 for the MMA) and their fp32 sum (unrounded)
-      uint32_t p[32];
-      const uint64_t c2 = pair2f(a.c, a.c), m2 = pair2f(-m, -m);
-      uint64_t sum[2] = {0, 0};
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        float x0, x1;
-        split2(fma2(pair2(r[2 * j], r[2 * j + 1]), c2, m2), x0, x1);
-        x0 = exp2_fast(x0);
-        x1 = exp2_fast(x1);
-        sum[j & 1] = add2(sum[j & 1], pair2f(x0, x1));
-        p[j] = pack_bf16x2(x0, x1);
-      }
-      float s0, s1;
-      split2(add2(sum[0], sum[1]), s0, s1);
-      l += s0 + s1;
-      tmem_st_cols<32>(sb, p);
-      tmem_wait_st();
-      tc_fence_before();
-      if (kPair && !leader) {
-        // (the weights are in TMEM, complete and fenced; there is no memory for a
-        // release to order, and it would take 1 us)
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&p_full[t & 1]), 0));
-      } else {
-        mbar_arrive(&p_full[t & 1]);
-      }
+      if (g == 0 && row < x.rows && a.lse != nullptr)
+        a.lse[tok * a.H + x.h] = l == 0.f ? -INFINITY : (m + log2_fast(l)) * kLn2;
     }
-    // ---- output
-    xch[g][row] = l;
-    named_sync(1 + q4, 64);
-    l = xch[0][row] + xch[1][row];
-    if (tiles > 0) {
-      wait_mma<kPair>(&pv_done[(tiles - 1) & 1], static_cast<uint32_t>((tiles - 1) >> 1) & 1u, abort);
-      __syncwarp();
-      tc_fence_after();
-    }
-    const float f = l == 0.f ? 0.f : 1.0f / l;
-    const int64_t tok = static_cast<int64_t>(ex.q0) + qi0 + row;
-    __nv_bfloat16* dst = a.out + tok * a.o_tok + h * a.o_head;
-    // A full tile goes through shared memory (every MMA that reads it is done)
-    // and out by tensor stores, 64 values of 128 queries each; rows of a tile
-    // that ends a sequence are stored one by one, so that the next sequence's
-    // stay untouched.  (Row by row throughout: 7500 cycles a block, 16 of each
-    // 128-byte line at a time.)
-    const bool full_tile = rows == kPreTile;
-#pragma unroll 1
-    for (int c = g * (dvp >> 1); c < (g + 1) * (dvp >> 1); c += 16) {
-      uint32_t o[16];
-      if (tiles > 0) {
-        tmem_ld16(tl + c, o);
-        tmem_wait_ld_of(o);
-      }
-      uint4 w[2];
-      uint32_t* wv = reinterpret_cast<uint32_t*>(w);
-#pragma unroll
-      for (int x = 0; x < 8; ++x)
-        wv[x] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * x]) * f, __uint_as_float(o[2 * x + 1]) * f);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int e = c + 8 * x;                      // dv is a multiple of 8
-        if (full_tile)
-          *reinterpret_cast<uint4*>(smem + (e >> 6) * kPreChunk + row * 128 + ((((e & 63) >> 3) ^ (row & 7)) << 4)) = w[x];
-        else if (row < rows && e < a.dv)
-          *reinterpret_cast<uint4*>(dst + e) = w[x];
-      }
-    }
-    if (full_tile) {
-      fence_proxy_async_smem();
-      named_sync(5, 256);
-      if (warp == 4 && elect_one()) {
-        for (int k = 0; k * 64 < a.dv; ++k) tma_store_3d(&o_map, smem + k * kPreChunk, k * 64, h, ex.q0 + qi0);
-        tma_store_wait();
-      }
-      __syncwarp();
-    }
-    if (g == 0 && row < rows && a.lse != nullptr)
-      a.lse[tok * a.H + h] = l == 0.f ? -INFINITY : (m + log2_fast(l)) * kLn2;
+    if (row == 0) tma_store_wait_read();
+    __syncwarp();
   }
   if (abort) atomicOr(&g_mla_prefill_error, kErrTimeout);
   tc_fence_before();
@@ -540,25 +602,44 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 }
 
 // ------------------------------------------------------------------ host
-static std::atomic<bool> g_prefill_attr[2][64];
+static std::atomic<int> g_prefill_grid[2][64];   // blocks that fit the device at once
 
 template <bool kPair>
 static cudaError_t launch_prefill(const MlaPrefillProblem& p, PrefillArgs a, const DeviceInfo& dev, cudaStream_t s) {
   using Shape = PreShape<kPair>;
   auto kern = mla_prefill_kernel<kPair>;
   cudaError_t e;
-  if (!g_prefill_attr[kPair ? 1 : 0][dev.device].load(std::memory_order_acquire)) {
+  const int most = kPreSmem - kPreStatic;
+  int fit = g_prefill_grid[kPair ? 1 : 0][dev.device].load(std::memory_order_acquire);
+  if (fit == 0) {
     cudaFuncAttributes fa;
     if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kPreSmem - static_cast<int>(fa.sharedSizeBytes));
     if (e != cudaSuccess) return e;
-    g_prefill_attr[kPair ? 1 : 0][dev.device].store(true, std::memory_order_release);
+    fit = dev.sm_count;
+    if (kPair) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count) & ~1u);
+      cfg.blockDim = dim3(kPreThreads);
+      cfg.dynamicSmemBytes = static_cast<size_t>(most);
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int clusters = 0;
+      if ((e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg)) != cudaSuccess) return e;
+      if (clusters < 1) return cudaErrorInvalidConfiguration;
+      fit = 2 * clusters;
+    }
+    g_prefill_grid[kPair ? 1 : 0][dev.device].store(fit, std::memory_order_release);
   }
   // N of the output product: a multiple of 16, of 32 over a pair
   a.dvn = kPair ? (p.dv + 31) & ~31 : (p.dv + 15) & ~15;
-  const int fixed = a.nq * kPreChunk + 1024;
-  const int slots = (kPreSmem - kPreStatic - fixed) / kSlotBytes;   // 5 or 6
+  const int fixed = a.nq * kPreChunk + 2 * kPreChunk + 1024;
+  const int slots = (most - fixed) / kSlotBytes;      // 4 or 5
   a.vslots = slots / 2;
   a.kslots = slots - a.vslots;
   CUtensorMap m[6];
@@ -573,10 +654,11 @@ static cudaError_t launch_prefill(const MlaPrefillProblem& p, PrefillArgs a, con
       (e = mla_tensor_map(&m[4], p.v.p, p.dv, p.H, p.Tk, p.v.head, p.v.tok, 64, 1, Shape::kValRows)) != cudaSuccess ||
       (e = mla_tensor_map(&m[5], p.out.p, p.dv, p.H, p.Tq, p.out.head, p.out.tok, 64, 1, kPreTile)) != cudaSuccess)
     return e;
-  // at most one partly filled query tile per sequence
-  const unsigned tiles = static_cast<unsigned>(p.Tq / Shape::kQueries + p.S);
-  return mla_launch_clusters(kern, dim3(tiles * (kPair ? 2 : 1), static_cast<unsigned>(p.H)), kPair ? 2 : 1, kPreThreads,
-                             fixed + slots * kSlotBytes, s, m[0], m[1], m[2], m[3], m[4], m[5], a);
+  // no more blocks than tiles (at most one partly filled tile per sequence)
+  const int64_t blocks = (static_cast<int64_t>(p.Tq) / Shape::kQueries + p.S) * p.H * Shape::kBlocks;
+  const unsigned grid = static_cast<unsigned>(blocks < fit ? blocks : fit);
+  return mla_launch_clusters(kern, dim3(grid), Shape::kBlocks, kPreThreads, fixed + slots * kSlotBytes, s, m[0], m[1],
+                             m[2], m[3], m[4], m[5], a);
 }
 
 cudaError_t launch_mla_prefill(const MlaPrefillProblem& p, const DeviceInfo& dev, cudaStream_t s) {
