@@ -26,24 +26,15 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // A bounded mbarrier wait by a whole converged warp, whose lanes go on (or
-// give up) together.
+// give up) together.  Also where another CTA of the cluster arrives: what its
+// arrival announces (copies, MMAs, TMEM) is read by the tensor core, and an
+// acquire at cluster scope takes 2000 cycles where this thread has stores under way.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, bool& abort) {
   mbar_wait(bar, parity, abort);
   abort = __any_sync(0xFFFFFFFFu, abort);
   return !abort;
 }
 
-// The same across the CTAs of a cluster, for phases that another CTA's threads
-// or MMAs complete.
-template <bool kCluster>
-__device__ __forceinline__ bool warp_wait_in(uint64_t* bar, uint32_t parity, bool& abort) {
-  if (kCluster)
-    mbar_wait_cluster(bar, parity, abort);
-  else
-    mbar_wait(bar, parity, abort);
-  abort = __any_sync(0xFFFFFFFFu, abort);
-  return !abort;
-}
 // One arrival on the barrier at the same offset in the CTA of rank `rank`,
 // ordering this thread's own operations before it.
 __device__ __forceinline__ void mbar_arrive_remote(uint64_t* bar, uint32_t rank) {

@@ -195,15 +195,6 @@ __device__ __forceinline__ bool clear_values(uint8_t* slot, int nv, int valid, i
   return true;
 }
 
-// A bounded wait for an MMA's commit (of rank 0, in a pair).
-template <bool kPair>
-__device__ __forceinline__ void wait_mma(uint64_t* bar, uint32_t parity, bool& abort) {
-  if (kPair)
-    mbar_wait_cluster(bar, parity, abort);
-  else
-    mbar_wait(bar, parity, abort);
-}
-
 template <bool kPair>
 __global__ void __launch_bounds__(kPreThreads, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap qn_map, const __grid_constant__ CUtensorMap qr_map,
@@ -273,7 +264,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     int fills = 0, i = 0, no = 0;
     while (!abort && walk.next_real(a, x)) {
       // the queries' place is free once the last scores of the tile before are formed
-      if (no > 0 && !warp_wait_in<kPair>(&s_full[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort)) break;
+      if (no > 0 && !warp_wait(&s_full[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort)) break;
       if (elect_one()) {
         mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(a.nq * kPreChunk));
         for (int k = 0; k + 1 < a.nq; ++k)
@@ -285,7 +276,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       for (int t = 0; t < x.tiles && !abort; ++t, ++i) {
         const int tok = x.ex.k0 + t * kPreTile + static_cast<int>(rank) * Shape::kKeyRows;
         for (int k = 0; k < a.nq; k += Shape::kKeyChunks) {
-          if (!warp_wait_in<kPair>(&kempty[r.slot], r.turn ^ 1u, abort)) break;
+          if (!warp_wait(&kempty[r.slot], r.turn ^ 1u, abort)) break;
           if (elect_one()) {
             const int n = min(Shape::kKeyChunks, a.nq - k);     // chunks of this slot
             uint8_t* dst = kring + r.slot * kSlotBytes;
@@ -319,7 +310,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     while (!abort && walk.next_real(a, x)) {
       for (int t = 0; t < x.tiles && !abort; ++t) {
         for (int tok = t * kPreTile; tok < min((t + 1) * kPreTile, x.see1); tok += Shape::kValRows) {
-          if (!warp_wait_in<kPair>(&vempty[r.slot], r.turn ^ 1u, abort)) break;
+          if (!warp_wait(&vempty[r.slot], r.turn ^ 1u, abort)) break;
           if (elect_one()) {
             mbar_arrive_expect_tx(&vfull[r.slot], static_cast<uint32_t>(nv * Shape::kValBlockBytes));
             for (int k = 0; k < nv; ++k)
@@ -344,10 +335,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     auto output = [&](int u, int valid, bool first) {
       const int ks = (valid + 15) >> 4;               // 16-key steps that hold anything
       const uint32_t p = tmem + kPreScol + static_cast<uint32_t>(u & 1) * 128u;
-      if (!warp_wait_in<kPair>(&p_full[u & 1], static_cast<uint32_t>(u >> 1) & 1u, abort)) return;
+      if (!warp_wait(&p_full[u & 1], static_cast<uint32_t>(u >> 1) & 1u, abort)) return;
       constexpr int kSteps = Shape::kValRows / 16;
       for (int j = 0; kSteps * j < ks; ++j) {
-        if (!warp_wait_in<kPair>(&vfull[rv.slot], rv.turn, abort)) return;
+        if (!warp_wait(&vfull[rv.slot], rv.turn, abort)) return;
         clear_values<Shape::kValRows>(vring + rv.slot * kSlotBytes, nv, valid - j * Shape::kValRows, lane);
         tc_fence_after();
         if (elect_one()) {
@@ -368,14 +359,14 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     };
     int i = 0, no = 0;
     while (!abort && walk.next_real(a, x)) {
-      if (!warp_wait_in<kPair>(&q_full, static_cast<uint32_t>(no) & 1u, abort)) break;
+      if (!warp_wait(&q_full, static_cast<uint32_t>(no) & 1u, abort)) break;
       ++no;
       for (int t = 0; t < x.tiles && !abort; ++t, ++i) {
         // S(i) = Q K^T; its score tile is free: the weights over it were
         // waited for and their product issued one turn ago
         const uint32_t d = tmem + kPreScol + static_cast<uint32_t>(i & 1) * 128u;
         for (int k = 0; k < a.nq; k += Shape::kKeyChunks) {
-          if (!warp_wait_in<kPair>(&kfull[rk.slot], rk.turn, abort)) break;
+          if (!warp_wait(&kfull[rk.slot], rk.turn, abort)) break;
           tc_fence_after();
           if (elect_one()) {
             const uint32_t sa = q_a + static_cast<uint32_t>(k) * kPreChunk;
@@ -448,7 +439,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       for (int t = 0; t < x.tiles; ++t, ++i) {
         const uint32_t sb = tl + kPreScol + static_cast<uint32_t>((i & 1) * 128 + g * 64);
         uint32_t r[64];
-        wait_mma<kPair>(&s_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, abort);
+        mbar_wait(&s_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, abort);
         __syncwarp();
         tc_fence_after();
         tmem_ld_cols<64>(sb, r);
@@ -481,7 +472,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (t > 0) {
             const float f = exp2_fast(m - mn);
             l *= f;
-            wait_mma<kPair>(&pv_done[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort);
+            mbar_wait(&pv_done[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort);
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
@@ -532,7 +523,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       l = xch[0][row] + xch[1][row];
       named_sync(1 + q4, 64);                         // xch is free again
       if (x.tiles > 0) {
-        wait_mma<kPair>(&pv_done[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort);
+        mbar_wait(&pv_done[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort);
         __syncwarp();
         tc_fence_after();
       }
