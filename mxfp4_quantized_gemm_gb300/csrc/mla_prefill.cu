@@ -122,9 +122,11 @@ struct QueryTile {
 };
 
 // The query tiles of a block or pair, found by each warp for itself; a lane
-// holds the prefix sum of its share of the sequences.
+// holds the prefix sum of its share of the sequences (and, of up to 32, its
+// sequence: the way from one query tile to the next then has no loads on it).
 template <bool kPair>
 struct QueryTiles {
+  Extent own;
   int s0, s1, first, incl, total, round, rank;
   __device__ __forceinline__ QueryTiles(const PrefillArgs& a, int rank_) : round(0), rank(rank_) {
     constexpr int kQ = PreShape<kPair>::kQueries;
@@ -132,8 +134,13 @@ struct QueryTiles {
     s0 = min(a.S, lane * per);
     s1 = min(a.S, s0 + per);
     int mine = 0;
+    own = lane < a.S ? extent(a, lane) : Extent{0, 0, 0, 0};
+    if (a.S <= 32) {
+      mine = (own.qn + kQ - 1) / kQ;
+    } else {
 #pragma unroll 4
-    for (int s = s0; s < s1; ++s) mine += (extent(a, s).qn + kQ - 1) / kQ;
+      for (int s = s0; s < s1; ++s) mine += (extent(a, s).qn + kQ - 1) / kQ;
+    }
     incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -151,21 +158,28 @@ struct QueryTiles {
     const int64_t all = static_cast<int64_t>(total) * a.H;
     if (at >= all) return false;                      // (the rounds that follow lie past the end too)
     ++round;
-    x.h = static_cast<int>(at / total);
+    // (a 64-bit division takes several times a 32-bit one)
+    x.h = all <= 0x7FFFFFFF ? static_cast<int>(at) / total : static_cast<int>(at / total);
     const int want = total - 1 - static_cast<int>(at - static_cast<int64_t>(x.h) * total);
     // the lane whose share holds it
     const bool here = want >= first && want < incl;
     int seq = 0, tile = want - first;
-    if (here)
+    if (here && a.S > 32)
       for (seq = s0; seq < s1; ++seq) {
         const int m = (extent(a, seq).qn + kQ - 1) / kQ;
         if (tile < m) break;
         tile -= m;
       }
     const int from = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
-    seq = __shfl_sync(0xFFFFFFFFu, seq, from);
     tile = __shfl_sync(0xFFFFFFFFu, tile, from);
-    x.ex = extent(a, seq);
+    if (a.S <= 32) {
+      x.ex.q0 = __shfl_sync(0xFFFFFFFFu, own.q0, from);
+      x.ex.qn = __shfl_sync(0xFFFFFFFFu, own.qn, from);
+      x.ex.k0 = __shfl_sync(0xFFFFFFFFu, own.k0, from);
+      x.ex.kn = __shfl_sync(0xFFFFFFFFu, own.kn, from);
+    } else {
+      x.ex = extent(a, __shfl_sync(0xFFFFFFFFu, seq, from));
+    }
     const int pq0 = tile * kQ;
     x.qi0 = pq0 + rank * kPreTile;
     x.rows = clamp_to(x.ex.qn - x.qi0, kPreTile);
@@ -540,30 +554,30 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       // four warps each take every second 64-value block
 #pragma unroll 1
       for (int b = g; b * 64 < a.dv; b += 2) {
-        if (full_tile) {
-          if (row == 0) tma_store_wait_read();
-          __syncwarp();
-          named_sync(5 + g, 128);                     // the buffer has been read
-        }
 #pragma unroll 1
-        for (int c = b * 64; c < min(b * 64 + 64, dvp); c += 16) {
-          uint32_t o[16];
+        for (int c = b * 64; c < min(b * 64 + 64, dvp); c += 32) {
+          uint32_t o[32];
           if (x.tiles > 0) {
-            tmem_ld16(tl + c, o);
+            tmem_ld_cols<32>(tl + c, o);
             tmem_wait_ld_of(o);
           }
-          uint4 w[2];
+          uint4 w[4];
           uint32_t* wv = reinterpret_cast<uint32_t*>(w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
+          for (int e = 0; e < 16; ++e)
             wv[e] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
+          if (full_tile) {
+            if ((c & 63) == 0) {
+              if (row == 0) tma_store_wait_read();
+              named_sync(5 + g, 128);                 // the buffer has been read
+            }
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int e = c + 8 * y;                  // dv is a multiple of 8
-            if (full_tile)
-              *reinterpret_cast<uint4*>(stage + row * 128 + ((((e & 63) >> 3) ^ (row & 7)) << 4)) = w[y];
-            else if (row < x.rows && e < a.dv)
-              *reinterpret_cast<uint4*>(dst + e) = w[y];
+            for (int y = 0; y < 4; ++y)
+              *reinterpret_cast<uint4*>(stage + row * 128 + (((((c & 63) >> 3) + y) ^ (row & 7)) << 4)) = w[y];
+          } else if (row < x.rows) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if (c + y * 8 < a.dv) *reinterpret_cast<uint4*>(dst + c + y * 8) = w[y];   // dv is a multiple of 8
           }
         }
         if (full_tile) {
