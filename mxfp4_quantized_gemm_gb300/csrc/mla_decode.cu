@@ -606,10 +606,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
               }
             }
           } else {
-            // (rows that pad the group too: nothing reads them)
             float* dst = part + static_cast<int64_t>(j0) * a.L + d;
+            const int n = a.HB * a.TB - j0;  // rows that pad the group are not read again
 #pragma unroll
-            for (int j = 0; j < kCols; ++j, dst += a.L) *dst = __uint_as_float(o[j]);
+            for (int j = 0; j < kCols; ++j, dst += a.L)
+              if (j < n) *dst = __uint_as_float(o[j]);
           }
         }
       }
@@ -879,7 +880,11 @@ cudaError_t launch_mla_decode(const MlaDecodeProblem& p, const DeviceInfo& dev, 
   const int V = groups * r.NB <= dev.sm_count || nk == 3 ? 1 : nk;
   int warps = 1;
   while (warps < kCombWarps && static_cast<int64_t>(warps) * 4 * groups < grid + groups) warps *= 2;
-  const int units = r.NB * (nk / V), per = kCombWarps / warps;
+  // ... but no second round of blocks (three fit an SM), which costs more than
+  // a round of loads
+  const int units = r.HB * r.TB * (nk / V);
+  while (warps > 1 && groups * ceil_div(static_cast<int64_t>(units) * warps, kCombWarps) > 3 * dev.sm_count) warps /= 2;
+  const int per = kCombWarps / warps;
   auto join = V == 4 ? mla_combine_kernel<4> : (V == 2 ? mla_combine_kernel<2> : mla_combine_kernel<1>);
   return mla_launch(join, dim3(static_cast<unsigned>(groups), static_cast<unsigned>(ceil_div(units, per))),
                     kCombWarps * 32, 0, s, a, grid, r.NB, warps);
