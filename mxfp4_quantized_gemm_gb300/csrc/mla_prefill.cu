@@ -571,19 +571,19 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       tc_fence_after();
       const float l = fin[row], f = l == 0.f ? 0.f : 1.0f / l;
       __nv_bfloat16* dst = a.out + (static_cast<int64_t>(x.ex.q0) + x.qi0 + row) * a.o_tok + x.h * a.o_head;
-      // 32 full rows go out through shared memory by tensor stores of 64 values
-      // each, warp by warp (two buffers of its own in turn); rows of a tile that
-      // ends a sequence are stored one by one, so that the next sequence's stay
+      // A full tile goes out through shared memory by tensor stores, 64 values
+      // of 128 queries each (two buffers in turn); rows of a tile that ends a
+      // sequence are stored one by one, so that the next sequence's stay
       // untouched.  (Row by row throughout, 16 of each 128-byte line at a time:
       // 7500 cycles a tile.)
-      const bool full_rows = x.rows >= q4 * 32 + 32;
+      const bool full_tile = x.rows == kPreTile;
 #pragma unroll 1
-      for (int b = 0; b * 64 < a.dv; ++b) {
-        uint32_t o[64];
+      for (int c = 0; c < a.dv; c += 32) {
+        uint32_t o[32];
         if (x.tiles > 0) {
-          tmem_ld_cols<64>(tl + b * 64, o);
+          tmem_ld_cols<32>(tl + c, o);
           tmem_wait_ld_of(o);
-          if (b * 64 + 64 >= a.dv) {
+          if (c + 32 >= a.dv) {
             // the accumulator is free
             tc_fence_before();
             if (kPair && !leader) {
@@ -594,31 +594,35 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             }
           }
         }
+        uint4 w[4];
+        uint32_t* wv = reinterpret_cast<uint32_t*>(w);
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          o[e] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
-        if (full_rows) {
-          uint8_t* stage = osm + (box++ & 1) * kPreChunk + q4 * 4096;
-          if (lane == 0) tma_store_wait_read<1>();
-          __syncwarp();                               // the buffer has been read
+        for (int e = 0; e < 16; ++e)
+          wv[e] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
+        if (full_tile) {
+          uint8_t* stage = osm + (box & 1) * kPreChunk;
+          if ((c & 63) == 0) {
+            if (row == 0) tma_store_wait_read<1>();
+            named_sync(5, 128);                       // the buffer has been read
+          }
 #pragma unroll
-          for (int y = 0; y < 8; ++y)
-            *reinterpret_cast<uint4*>(stage + lane * 128 + ((y ^ (lane & 7)) << 4)) =
-                make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tma_store_3d(&o_map, stage, b * 64, x.h, x.ex.q0 + x.qi0 + q4 * 32);
-          __syncwarp();
+          for (int y = 0; y < 4; ++y)
+            *reinterpret_cast<uint4*>(stage + row * 128 + (((((c & 63) >> 3) + y) ^ (row & 7)) << 4)) = w[y];
+          if ((c & 63) != 0 || c + 32 >= a.dv) {
+            fence_proxy_async_smem();
+            named_sync(5, 128);
+            if (row == 0) tma_store_3d(&o_map, stage, c & ~63, x.h, x.ex.q0 + x.qi0);
+            __syncwarp();
+            ++box;
+          }
         } else if (row < x.rows) {
 #pragma unroll
-          for (int y = 0; y < 8; ++y)
-            if (b * 64 + y * 8 < a.dv)                // dv is a multiple of 8
-              *reinterpret_cast<uint4*>(dst + b * 64 + y * 8) =
-                  make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+          for (int y = 0; y < 4; ++y)
+            if (c + y * 8 < a.dv) *reinterpret_cast<uint4*>(dst + c + y * 8) = w[y];   // dv is a multiple of 8
         }
       }
     }
-    if (lane == 0) tma_store_wait_read<0>();
+    if (row == 0) tma_store_wait_read<0>();
     __syncwarp();
   }
   if (abort) atomicOr(&g_mla_prefill_error, kErrTimeout);
@@ -685,7 +689,7 @@ static cudaError_t launch_prefill(const MlaPrefillProblem& p, PrefillArgs a, con
       (e = mla_tensor_map(&m[3], p.k_rope.p, kMlaRope, 1, p.Tk, kMlaRope, p.k_rope.tok, 64, 1, Shape::kKeyRows)) !=
           cudaSuccess ||
       (e = mla_tensor_map(&m[4], p.v.p, p.dv, p.H, p.Tk, p.v.head, p.v.tok, 64, 1, Shape::kValRows)) != cudaSuccess ||
-      (e = mla_tensor_map(&m[5], p.out.p, p.dv, p.H, p.Tq, p.out.head, p.out.tok, 64, 1, 32)) != cudaSuccess)
+      (e = mla_tensor_map(&m[5], p.out.p, p.dv, p.H, p.Tq, p.out.head, p.out.tok, 64, 1, kPreTile)) != cudaSuccess)
     return e;
   // no more blocks than tiles (at most one partly filled tile per sequence)
   const int64_t blocks = (static_cast<int64_t>(p.Tq) / Shape::kQueries + p.S) * p.H * Shape::kBlocks;
