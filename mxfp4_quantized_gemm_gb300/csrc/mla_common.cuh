@@ -131,7 +131,7 @@ __device__ __forceinline__ void tma_box_3d(void* smem_dst, const CUtensorMap* ma
 }
 
 // One box, shared memory -> a 3-D tensor map; and the wait, by the same thread,
-// until its boxes (but the last few) have been read from shared memory (which may then be used
+// until its boxes have been read from shared memory (which may then be used
 // again, or given up: the writes complete with the grid).
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int c0, int c1, int c2) {
   asm volatile(
@@ -140,20 +140,8 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
       "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(smem_src))
       : "memory");
 }
-template <int kPending>   // all but the last kPending
 __device__ __forceinline__ void tma_store_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
-}
-
-// Takes registers up to N a thread (kMore), or gives those above N back, for
-// the calling warpgroup; the shares of all warpgroups together must not exceed
-// the launch's.
-template <int N, bool kMore>
-__device__ __forceinline__ void set_max_registers() {
-  if (kMore)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-  else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // Descriptor of an operand whose M or N elements are contiguous (64 of them

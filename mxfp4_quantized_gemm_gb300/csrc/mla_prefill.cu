@@ -26,9 +26,7 @@
 // slots of its own; warp 1 issues every product (in rank 0 of a pair; in rank
 // 1 warps 1 and 2 pass on to rank 0 that their keys and values have landed);
 // warps 4..7 and 8..11 hold the softmax, thread = (query, half of the tile's
-// keys); warps 12..15 write a finished query tile out (thread = query) while
-// the softmax is at the next one.  The registers of a launch (128 a thread) are
-// dealt out anew, 168 to the softmax's 64 scores a thread.  Each query's running maximum is raised only when a score passes it
+// keys).  Each query's running maximum is raised only when a score passes it
 // by 2^8, decided per 32 queries by a barrier with an OR over the two warps
 // that hold them.
 //
@@ -60,7 +58,7 @@ namespace mx {
 
 static __device__ uint32_t g_mla_prefill_error;
 
-constexpr int kPreThreads = 512;
+constexpr int kPreThreads = 384;
 constexpr int kPreTile = 128;                 // queries of a block, and keys per tile
 constexpr int kPreChunk = 16384;              // 128 rows x 64 values
 constexpr int kSlotBytes = 2 * kPreChunk;
@@ -226,10 +224,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   uint8_t* osm = vring + a.vslots * kSlotBytes;       // two 64-value blocks of 128 queries, on their way out
 
   __shared__ __align__(8) uint64_t kfull[kPreMaxSlots], kempty[kPreMaxSlots], vfull[kPreMaxSlots], vempty[kPreMaxSlots];
-  __shared__ __align__(8) uint64_t q_full, s_full[2], p_full[2], pv_done[2], fin_full, o_empty, drained;
+  __shared__ __align__(8) uint64_t q_full, s_full[2], p_full[2], pv_done[2], drained;
   __shared__ uint32_t tmem_slot;
   __shared__ float xch[2][kPreTile];
-  __shared__ float fin[kPreTile];                     // sums of a finished tile's queries
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = kPair ? cluster_ctarank() : 0u;
@@ -251,8 +248,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       mbar_init(&p_full[i], kPair ? 256 + 8 : 256);
       mbar_init(&pv_done[i], 1);
     }
-    mbar_init(&fin_full, 128);
-    mbar_init(&o_empty, kPair ? 128 + 4 : 128);
     mbar_init(&drained, 1);
     fence_mbar_init();
   }
@@ -277,10 +272,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   QueryTiles<kPair> walk(a, static_cast<int>(rank));
   QueryTile x;
 
-  // registers of the four warpgroups: 72 + 2 x 168 + 104 = 4 x 128
-  if (warp < 4) {
-   set_max_registers<72, false>();
-   if (warp == 0) {
+  if (warp == 0) {
     // ---- queries and keys
     Ring r(a.kslots);
     int fills = 0, i = 0, no = 0;
@@ -323,7 +315,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       bool late = false;
       if (no > 0) mbar_wait(&q_full, static_cast<uint32_t>(no - 1) & 1u, late);
     }
-   } else if (warp == 3) {
+  } else if (warp == 3) {
     // ---- values
     const int half = kPair ? a.dvn >> 1 : a.dvn;      // this block's columns
     const int v0 = static_cast<int>(rank) * half, nv = (half + 63) >> 6;
@@ -346,20 +338,17 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
     }
     if (abort) drain_copies(vfull, fills, r.n);
-   } else if (warp == 1 && leader) {
+  } else if (warp == 1 && leader) {
     // ---- the products
     constexpr uint32_t idesc_s = idesc_bf16(Shape::kQueries, 128);
     const uint32_t idesc_o = idesc_bf16(Shape::kQueries, a.dvn) | kIdescBMn;
     const uint32_t q_a = smem_u32(qsm), k_a = smem_u32(kring), v_a = smem_u32(vring);
     const int nv = ((kPair ? a.dvn >> 1 : a.dvn) + 63) >> 6;
     Ring rk(a.kslots), rv(a.vslots);
-    int i = 0, no = 0;                                // tiles, query tiles
     // O += P(u) V(u) of tile number u: `valid` of its keys count; `first` of its query tile
     auto output = [&](int u, int valid, bool first) {
       const int ks = (valid + 15) >> 4;               // 16-key steps that hold anything
       const uint32_t p = tmem + kPreScol + static_cast<uint32_t>(u & 1) * 128u;
-      // the accumulator: the query tile before has been read out
-      if (first && no > 1 && !warp_wait(&o_empty, static_cast<uint32_t>(no) & 1u, abort)) return;
       if (!warp_wait(&p_full[u & 1], static_cast<uint32_t>(u >> 1) & 1u, abort)) return;
       constexpr int kSteps = Shape::kValRows / 16;
       for (int j = 0; kSteps * j < ks; ++j) {
@@ -382,6 +371,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         rv.step();
       }
     };
+    int i = 0, no = 0;
     while (!abort && walk.next_real(a, x)) {
       if (!warp_wait(&q_full, static_cast<uint32_t>(no) & 1u, abort)) break;
       ++no;
@@ -414,7 +404,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       if (!abort) output(i - 1, x.see1 - (x.tiles - 1) * kPreTile, x.tiles == 1);
     }
     drain_mmas<kPair>(&drained, abort);
-   } else if (kPair && warp == 1) {
+  } else if (kPair && warp == 1) {
     // ---- rank 1: its queries and keys have landed
     Ring r(a.kslots);
     int no = 0;
@@ -430,7 +420,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         r.step();
       }
     }
-   } else if (kPair && warp == 2 && !leader) {
+  } else if (kPair && warp == 2 && !leader) {
     // ---- rank 1: its values have landed
     const int nv = ((a.dvn >> 1) + 63) >> 6;
     Ring r(a.vslots);
@@ -448,9 +438,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         r.step();
       }
     }
-   }
-  } else if (warp < 12) {
-    set_max_registers<168, true>();
+  } else if (warp >= 4) {
     // ---- softmax.  Warps w and w + 4 hold the same 32 queries and meet at
     // named barriers, so they walk every tile even after a wait has given up.
     const int q4 = warp & 3, g = (warp - 4) >> 2;
@@ -543,86 +531,66 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           mbar_arrive(&p_full[i & 1]);
         }
       }
-      // ---- sums, for the warps that write the tile out
+      // ---- output
       xch[g][row] = l;
       named_sync(1 + q4, 64);
-      if (g == 0) {
-        l += xch[1][row];
-        fin[row] = l;
-        if (row < x.rows && a.lse != nullptr)
-          a.lse[(static_cast<int64_t>(x.ex.q0) + x.qi0 + row) * a.H + x.h] =
-              l == 0.f ? -INFINITY : (m + log2_fast(l)) * kLn2;
-        mbar_arrive(&fin_full);
-      }
+      l = xch[0][row] + xch[1][row];
       named_sync(1 + q4, 64);                         // xch is free again
-    }
-  } else {
-    set_max_registers<104, false>();
-    // ---- finished query tiles
-    const int q4 = warp & 3, row = q4 * 32 + lane;
-    const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
-    int i = 0, no = 0, box = 0;
-    while (walk.next(a, x)) {
-      i += x.tiles;
-      mbar_wait(&fin_full, static_cast<uint32_t>(no) & 1u, abort);
-      ++no;
-      if (x.tiles > 0) mbar_wait(&pv_done[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort);
-      __syncwarp();
-      tc_fence_after();
-      const float l = fin[row], f = l == 0.f ? 0.f : 1.0f / l;
-      __nv_bfloat16* dst = a.out + (static_cast<int64_t>(x.ex.q0) + x.qi0 + row) * a.o_tok + x.h * a.o_head;
+      if (x.tiles > 0) {
+        mbar_wait(&pv_done[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort);
+        __syncwarp();
+        tc_fence_after();
+      }
+      const float f = l == 0.f ? 0.f : 1.0f / l;
+      const int64_t tok = static_cast<int64_t>(x.ex.q0) + x.qi0 + row;
+      __nv_bfloat16* dst = a.out + tok * a.o_tok + x.h * a.o_head;
       // A full tile goes out through shared memory by tensor stores, 64 values
-      // of 128 queries each (two buffers in turn); rows of a tile that ends a
-      // sequence are stored one by one, so that the next sequence's stay
-      // untouched.  (Row by row throughout, 16 of each 128-byte line at a time:
-      // 7500 cycles a tile.)
+      // of 128 queries each (four warps at a time, through a buffer of their
+      // own); rows of a tile that ends a sequence are stored one by one, so that
+      // the next sequence's stay untouched.  (Row by row throughout, 16 of each
+      // 128-byte line at a time: 7500 cycles a tile.)
       const bool full_tile = x.rows == kPreTile;
+      uint8_t* stage = osm + g * kPreChunk;
+      // four warps each take every second 64-value block
 #pragma unroll 1
-      for (int c = 0; c < a.dv; c += 32) {
-        uint32_t o[32];
-        if (x.tiles > 0) {
-          tmem_ld_cols<32>(tl + c, o);
-          tmem_wait_ld_of(o);
-          if (c + 32 >= a.dv) {
-            // the accumulator is free
-            tc_fence_before();
-            if (kPair && !leader) {
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&o_empty), 0));
-            } else {
-              mbar_arrive(&o_empty);
+      for (int b = g; b * 64 < a.dv; b += 2) {
+#pragma unroll 1
+        for (int c = b * 64; c < min(b * 64 + 64, dvp); c += 32) {
+          uint32_t o[32];
+          if (x.tiles > 0) {
+            tmem_ld_cols<32>(tl + c, o);
+            tmem_wait_ld_of(o);
+          }
+          uint4 w[4];
+          uint32_t* wv = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            wv[e] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
+          if (full_tile) {
+            if ((c & 63) == 0) {
+              if (row == 0) tma_store_wait_read();
+              named_sync(5 + g, 128);                 // the buffer has been read
             }
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              *reinterpret_cast<uint4*>(stage + row * 128 + (((((c & 63) >> 3) + y) ^ (row & 7)) << 4)) = w[y];
+          } else if (row < x.rows) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if (c + y * 8 < a.dv) *reinterpret_cast<uint4*>(dst + c + y * 8) = w[y];   // dv is a multiple of 8
           }
         }
-        uint4 w[4];
-        uint32_t* wv = reinterpret_cast<uint32_t*>(w);
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          wv[e] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
         if (full_tile) {
-          uint8_t* stage = osm + (box & 1) * kPreChunk;
-          if ((c & 63) == 0) {
-            if (row == 0) tma_store_wait_read<1>();
-            named_sync(5, 128);                       // the buffer has been read
-          }
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            *reinterpret_cast<uint4*>(stage + row * 128 + (((((c & 63) >> 3) + y) ^ (row & 7)) << 4)) = w[y];
-          if ((c & 63) != 0 || c + 32 >= a.dv) {
-            fence_proxy_async_smem();
-            named_sync(5, 128);
-            if (row == 0) tma_store_3d(&o_map, stage, c & ~63, x.h, x.ex.q0 + x.qi0);
-            __syncwarp();
-            ++box;
-          }
-        } else if (row < x.rows) {
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            if (c + y * 8 < a.dv) *reinterpret_cast<uint4*>(dst + c + y * 8) = w[y];   // dv is a multiple of 8
+          fence_proxy_async_smem();
+          named_sync(5 + g, 128);
+          if (row == 0) tma_store_3d(&o_map, stage, b * 64, x.h, x.ex.q0 + x.qi0);
+          __syncwarp();
         }
       }
+      if (g == 0 && row < x.rows && a.lse != nullptr)
+        a.lse[tok * a.H + x.h] = l == 0.f ? -INFINITY : (m + log2_fast(l)) * kLn2;
     }
-    if (row == 0) tma_store_wait_read<0>();
+    if (row == 0) tma_store_wait_read();
     __syncwarp();
   }
   if (abort) atomicOr(&g_mla_prefill_error, kErrTimeout);
