@@ -222,13 +222,17 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   constexpr int kQChunk = NB * 128;
 
   __shared__ __align__(8) uint64_t full[2][kDecMaxBufs], empty[2][kDecMaxBufs];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], q_full, pv_done, o_full, o_empty, fin_full, drain[2];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], q_full, q_empty, pv_done, o_empty, drain[2];
+  // of a stretch, by its number's parity: the softmax may be a whole stretch
+  // ahead of the warps that write out, but not two
+  __shared__ __align__(8) uint64_t o_full[2], fin_full[2];
   __shared__ uint32_t tmem_slot;
   __shared__ __align__(16) float fac[64];
   __shared__ float xch[2][64];
-  // 1 / sum of a finished stretch's rows, for the warps that write it out (by
-  // the stretch's number's parity)
-  __shared__ __align__(16) float fin[2][NB];
+  // 1 / sum of a finished stretch's rows, for the warps that write it out.  They
+  // give the accumulator back before they are done with the sums, so that those
+  // of two further stretches may come in beside them: three in use at most.
+  __shared__ __align__(16) float fin[4][NB];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   bool abort = false;
@@ -242,12 +246,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 256);
       mbar_init(&drain[i], 1);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&fin_full[i], 256);
     }
     mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
     mbar_init(&pv_done, 1);
-    mbar_init(&o_full, 1);
     mbar_init(&o_empty, 128);
-    mbar_init(&fin_full, 256);
     fence_mbar_init();
   }
   if (warp == 0 && lane < 3) prefetch_tensor_map(lane == 0 ? &qmap : (lane == 1 ? &rmap : &cmap));
@@ -270,7 +275,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const int boxes = kTileTok / a.box_rows;
     const int box = lane & (boxes - 1);      // the lane's box, in every group
     Ring r(a.bufs);
-    int i = 0, seg_no = 0, fills = 0;
+    int seg_no = 0, fills = 0;
     Segment g{};
     // The page and row of the lane's box of tile t, and the boxes that hold
     // anything; asked for a tile ahead.
@@ -288,8 +293,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     while (!abort && walk.next_real(a, g)) {
       look_up(g.t0);
       // the queries: their buffer is free once the last score product of the
-      // stretch before has read it
-      if (seg_no > 0 && !warp_wait(&s_full[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort)) break;
+      // stretch before has read it (a barrier of its own: a parity says nothing
+      // about one that may be two phases behind, as s_full is to this warp)
+      if (seg_no > 0 && !warp_wait(&q_empty, static_cast<uint32_t>(seg_no - 1) & 1u, abort)) break;
       const int h0 = (g.rt % a.head_blocks) * a.HB;
       const int tk0 = g.s * a.q_len + (g.rt / a.head_blocks) * a.TPT;
       if (lane == 0) mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(chunks * a.HB * a.TB * 128));
@@ -297,7 +303,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       if (lane < 2 * nk) tma_box_3d(qsm + lane * kQChunk, &qmap, lane * 64, h0, tk0, &q_full);
       if (lane == 31) tma_box_3d(qsm + 2 * nk * kQChunk, &rmap, 0, h0, tk0, &q_full);
       ++seg_no;
-      for (int t = g.t0; t < g.t1; ++t, ++i) {
+      for (int t = g.t0; t < g.t1; ++t) {
         const int cur_nb = nb, cur_row = row;
         int cur_page = page;
         if (box < cur_nb && (cur_page < 0 || cur_page >= a.num_pages)) {
@@ -354,7 +360,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 #pragma unroll
               for (int m = 0; m < 4; ++m) mma_bf16(d, ad + 2 * m, bd + 2 * m, idesc, (c | m) != 0);
             }
-            if (x + 1 == groups) mma_commit(&s_full[i & 1]);
+            if (x + 1 == groups) {
+              mma_commit(&s_full[i & 1]);
+              if (t + 1 == g.t1) mma_commit(&q_empty);
+            }
           }
           __syncwarp();
         }
@@ -400,7 +409,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           }
           mma_commit(&empty[groups - 1][r.slot]);
           mma_commit(&pv_done);
-          if (t + 1 == g.t1) mma_commit(&o_full);
+          if (t + 1 == g.t1) mma_commit(&o_full[(seg_no - 1) & 1]);
         }
         __syncwarp();
         r.step();
@@ -523,7 +532,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         named_sync(1, 256);
         if (half == 0 && mine) {
           const float sum = xch[0][row] + xch[1][row];
-          fin[seg_no & 1][row] = sum == 0.f ? 0.f : 1.0f / sum;
+          fin[seg_no & 3][row] = sum == 0.f ? 0.f : 1.0f / sum;
           if (whole) {
             if (a.lse != nullptr && on) a.lse[at * a.H + head] = sum == 0.f ? -INFINITY : (m + log2_fast(sum)) * kLn2;
           } else if (on) {
@@ -532,7 +541,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             part[NB + row] = sum;
           }
         }
-        mbar_arrive(&fin_full);
+        mbar_arrive(&fin_full[seg_no & 1]);
         ++seg_no;
       } else {
         // an empty sequence: its rows are zero, their log-sum -inf
@@ -559,9 +568,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     for (; walk.next_real(a, g); ++seg_no) {
       const bool last = walk.left <= 0;
       if (warp < 12 && !last) continue;
-      const int par = seg_no & 1;
-      mbar_wait(&fin_full, static_cast<uint32_t>(par), abort);
-      mbar_wait(&o_full, static_cast<uint32_t>(par), abort);
+      mbar_wait(&fin_full[seg_no & 1], static_cast<uint32_t>(seg_no >> 1) & 1u, abort);
+      mbar_wait(&o_full[seg_no & 1], static_cast<uint32_t>(seg_no >> 1) & 1u, abort);
+      const float* inv = fin[seg_no & 3];
       __syncwarp();
       tc_fence_after();
       const bool whole = g.t0 == 0 && g.t1 == g.nt;
@@ -588,7 +597,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             // stores two neighbouring ones, of the even or of the odd row
 #pragma unroll
             for (int j = 0; j < kCols; j += 2) {
-              const float f0 = fin[par][j0 + j], f1 = fin[par][j0 + j + 1];
+              const float f0 = inv[j0 + j], f1 = inv[j0 + j + 1];
               const float x0 = f0 == 0.f ? 0.f : __uint_as_float(o[j]) * f0;
               const float x1 = f1 == 0.f ? 0.f : __uint_as_float(o[j + 1]) * f1;
               const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? x0 : x1, 1);

@@ -148,6 +148,20 @@ def test_decode_many_sequences(capi):
     decode_case(capi, [int(v) for v in g.integers(0, 40, 300)], 4, 1, 8)
 
 
+def test_decode_long_ragged_sequences(capi):
+    # blocks that go from one sequence into the next, and sequences over many blocks
+    decode_case(capi, [5000, 1, 2900, 64, 65, 3777, 0, 1234, 700], 64, 1, 64)
+    decode_case(capi, [2100, 63, 1500, 1], 48, 2, 128, seed=9)
+
+
+@pytest.mark.parametrize("lat", [128, 256, 512])
+def test_decode_many_short_sequences(capi, lat):
+    # several sequences to a block, so that the next one's queries and
+    # positions are asked for while the last one's are in use
+    g = np.random.default_rng(lat)
+    decode_case(capi, [int(v) for v in g.integers(0, 200, 700)], 16, 1, 64, lat=lat, seed=lat)
+
+
 def test_decode_rising_and_peaked_scores(capi):
     # scores that keep passing the running maximum, far outside the slack, and
     # weights of one position alone
@@ -299,6 +313,23 @@ def test_prefill_rising_and_peaked_scores(capi):
     cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
     args = (q[..., :192], q[..., 192:], kv[..., :192], kr, kv[..., 192:])
     for scale in (0.06, 0.8, -0.2):
+@pytest.mark.parametrize("most", [400, 200])
+def test_prefill_many_tiles_per_block(capi, most):
+    # several query tiles for every block (pairs of blocks above 128 tokens a
+    # prompt, single blocks below), some of them without a key
+    g = np.random.default_rng(most)
+    new = [int(v) for v in g.integers(1, most, 40)] + [most]
+    old = [int(v) for v in g.integers(-60, 200, 41)]
+    old = [max(b, -a) for a, b in zip(new, old)]
+    prefill_case(capi, new, old, 9, 64, 64, True)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1])
+def test_scores_scaled_by_zero_and_below(capi, scale):
+    decode_case(capi, [300, 5, 0], 8, 2, 16, scale=scale)
+    prefill_case(capi, [70, 200], [0, 30], 2, 64, 72, True, scale=scale)
+
+
         out, lse = run_prefill(capi, *args, cu, cu, scale, True)
         want = ref.prefill(*(f64(t) for t in args), [0, n], [0, n], scale, True)
         check_attention(out, lse, want, n, 256, f"scale {scale}")
