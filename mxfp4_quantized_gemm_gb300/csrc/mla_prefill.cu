@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   uint8_t* osm = vring + a.vslots * kSlotBytes;       // two 64-value blocks of 128 queries, on their way out
 
   __shared__ __align__(8) uint64_t kfull[kPreMaxSlots], kempty[kPreMaxSlots], vfull[kPreMaxSlots], vempty[kPreMaxSlots];
-  __shared__ __align__(8) uint64_t q_full, s_full[2], p_full[2], pv_done[2], drained;
+  __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], drained;
   __shared__ uint32_t tmem_slot;
   __shared__ float xch[2][kPreTile];
 
@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       mbar_init(&vempty[s], 1);
     }
     mbar_init(&q_full, both);
+    mbar_init(&q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], kPair ? 256 + 8 : 256);
@@ -275,10 +276,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   if (warp == 0) {
     // ---- queries and keys
     Ring r(a.kslots);
-    int fills = 0, i = 0, no = 0;
+    int fills = 0, no = 0;
     while (!abort && walk.next_real(a, x)) {
-      // the queries' place is free once the last scores of the tile before are formed
-      if (no > 0 && !warp_wait(&s_full[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort)) break;
+      // the queries' place is free once the last scores of the tile before are
+      // formed.  (A barrier of its own, with one phase a query tile: a parity
+      // says nothing about a barrier that may be two phases behind, as s_full
+      // is to a warp that does not wait for each of its phases.)
+      if (no > 0 && !warp_wait(&q_empty, static_cast<uint32_t>(no - 1) & 1u, abort)) break;
       if (elect_one()) {
         mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(a.nq * kPreChunk));
         for (int k = 0; k + 1 < a.nq; ++k)
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
       __syncwarp();
       ++no;
-      for (int t = 0; t < x.tiles && !abort; ++t, ++i) {
+      for (int t = 0; t < x.tiles && !abort; ++t) {
         const int tok = x.ex.k0 + t * kPreTile + static_cast<int>(rank) * Shape::kKeyRows;
         for (int k = 0; k < a.nq; k += Shape::kKeyChunks) {
           if (!warp_wait(&kempty[r.slot], r.turn ^ 1u, abort)) break;
@@ -394,7 +398,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                                    sdesc_sw128(sb + y * Shape::kKeyChunkBytes + m * 32), idesc_s, (k | y | m) != 0);
             }
             mma_commit_of<kPair>(&kempty[rk.slot]);
-            if (k + Shape::kKeyChunks >= a.nq) mma_commit_of<kPair>(&s_full[i & 1]);
+            if (k + Shape::kKeyChunks >= a.nq) {
+              mma_commit_of<kPair>(&s_full[i & 1]);
+              if (t + 1 == x.tiles) mma_commit_of<kPair>(&q_empty);
+            }
           }
           __syncwarp();
           rk.step();

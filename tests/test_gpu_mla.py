@@ -290,6 +290,13 @@ def test_prefill_widths(capi, dn, dv, causal):
     prefill_case(capi, [70, 140], [0, 33], 2, dn, dv, causal, seed=dn + dv)
 
 
+@pytest.mark.parametrize("dn,dv", [(64, 64), (8, 8), (72, 40), (128, 136), (192, 128), (120, 256), (184, 200)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_widths_in_pairs(capi, dn, dv, causal):
+    # prompts above 128 tokens on average take pairs of blocks
+    prefill_case(capi, [300, 150], [0, 45], 2, dn, dv, causal, seed=dn + dv)
+
+
 @pytest.mark.parametrize("causal", [True, False])
 def test_prefill_ragged_with_context(capi, causal):
     prefill_case(capi, [5, 130, 1, 64, 1], [300, 0, 129, 64, 0], 3, 192, 256, causal)
@@ -306,13 +313,6 @@ def test_prefill_many_prompts(capi):
     prefill_case(capi, [int(v) for v in g.integers(0, 5, 500)], [int(v) for v in g.integers(0, 4, 500)], 1, 64, 64, True)
 
 
-def test_prefill_rising_and_peaked_scores(capi):
-    n, H = 520, 2
-    q, kv, kr = rnd(91, n, H, 256), rnd(92, n, H, 448), rnd(93, n, R)
-    kv = (kv.float() * torch.linspace(0.05, 8.0, n, device="cuda")[:, None, None]).to(BF)
-    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
-    args = (q[..., :192], q[..., 192:], kv[..., :192], kr, kv[..., 192:])
-    for scale in (0.06, 0.8, -0.2):
 @pytest.mark.parametrize("most", [400, 200])
 def test_prefill_many_tiles_per_block(capi, most):
     # several query tiles for every block (pairs of blocks above 128 tokens a
@@ -330,6 +330,13 @@ def test_scores_scaled_by_zero_and_below(capi, scale):
     prefill_case(capi, [70, 200], [0, 30], 2, 64, 72, True, scale=scale)
 
 
+def test_prefill_rising_and_peaked_scores(capi):
+    n, H = 520, 2
+    q, kv, kr = rnd(91, n, H, 256), rnd(92, n, H, 448), rnd(93, n, R)
+    kv = (kv.float() * torch.linspace(0.05, 8.0, n, device="cuda")[:, None, None]).to(BF)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    args = (q[..., :192], q[..., 192:], kv[..., :192], kr, kv[..., 192:])
+    for scale in (0.06, 0.8, -0.2):
         out, lse = run_prefill(capi, *args, cu, cu, scale, True)
         want = ref.prefill(*(f64(t) for t in args), [0, n], [0, n], scale, True)
         check_attention(out, lse, want, n, 256, f"scale {scale}")
