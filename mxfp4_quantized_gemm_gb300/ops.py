@@ -19,6 +19,13 @@ including the pages' flattening of 3-D activations to 2-D for the GEMM.
     torch.ops.mxfp4.linear_mxfp4_out(x, w_packed, bias, N) -> (codes, scales)   # next layer's input
     torch.ops.mxfp4.linear_split_cat(x, w_packed, bias, z, s1, s2) -> (cat, split)   # per-group split + cat
     torch.ops.mxfp4.a16wfp4_bmm(x, w_packed, N, batch_major) -> out
+
+and the latent attention between the absorbed K-up and V-up products (bf16
+activations, a paged cache [pages, page, L + R] of latent | rotated key):
+
+    torch.ops.mxfp4.mla_store(kv, gamma, eps, q_rope, cos_sin, positions, slots, cache, interleaved) -> q_rot   # cache updated
+    torch.ops.mxfp4.mla_decode(q_lat, q_rope, cache, page_table, seq_lens, scale) -> (out, lse)
+    torch.ops.mxfp4.mla_prefill(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, scale, causal) -> (out, lse)
 """
 
 from __future__ import annotations
@@ -349,3 +356,172 @@ def _(x, w_packed, N, batch_major):
     B, M, K = x.shape
     _check_weights("mxfp4::a16wfp4_bmm", w_packed, B, N, K)
     return x.new_empty(*((M, B, N) if batch_major else (B, M, N)), dtype=torch.bfloat16)
+
+
+# ------------------------------------------------------- latent attention
+_MLA_ROPE = 64
+
+
+def _vec(t: Tensor) -> Tensor:
+    """t as the latent-attention calls take it: innermost dimension contiguous,
+    16-byte aligned rows (a copy where it is neither)."""
+    ok = t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(
+        n == 1 or (s > 0 and s % 8 == 0) for n, s in zip(t.shape[:-1], t.stride()[:-1]))
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
+
+
+def _check_cache(where: str, cache: Tensor) -> tuple[int, int, int]:
+    torch._check(cache.dim() == 3, lambda: f"{where}: cache must be [pages, page, L + {_MLA_ROPE}]")
+    pages, page, width = cache.shape
+    L = width - _MLA_ROPE
+    torch._check(pages > 0 and page > 0 and page % 8 == 0,
+                 lambda: f"{where}: cache has {pages} pages of {page} rows; pages must hold a multiple of 8")
+    torch._check(L > 0 and L % 128 == 0 and L <= 512,
+                 lambda: f"{where}: a latent of {L} values; multiples of 128 up to 512 are supported")
+    torch._check(cache.stride(2) == 1 and cache.stride(1) == width,
+                 lambda: f"{where}: the rows of a page must be contiguous")
+    return pages, page, L
+
+
+def _check_mla_store(kv, gamma, q_rope, cos_sin, positions, slots, cache) -> int:
+    where = "mxfp4::mla_store"
+    bf, i64 = torch.bfloat16, torch.int64
+    _check_args(where, kv, gamma, q_rope, cos_sin, positions, slots, cache,
+                dtypes=(bf, bf, bf, torch.float32, i64, i64, bf))
+    _, _, L = _check_cache(where, cache)
+    T = kv.shape[0]
+    torch._check(kv.dim() == 2 and kv.shape[1] == L + _MLA_ROPE,
+                 lambda: f"{where}: kv must be [T, {L + _MLA_ROPE}], got {tuple(kv.shape)}")
+    torch._check(q_rope.dim() == 3 and q_rope.shape[0] == T and q_rope.shape[2] == _MLA_ROPE,
+                 lambda: f"{where}: q_rope must be [T, H, {_MLA_ROPE}], got {tuple(q_rope.shape)}")
+    torch._check(gamma.numel() == L, lambda: f"{where}: gamma has {gamma.numel()} elements, L = {L}")
+    torch._check(cos_sin.dim() == 2 and cos_sin.shape[0] > 0 and cos_sin.shape[1] == _MLA_ROPE,
+                 lambda: f"{where}: cos_sin must be [positions, {_MLA_ROPE}], got {tuple(cos_sin.shape)}")
+    torch._check(positions.numel() == T and slots.numel() == T,
+                 lambda: f"{where}: {positions.numel()} positions and {slots.numel()} slots for {T} tokens")
+    return L
+
+
+@custom_op("mxfp4::mla_store", mutates_args=("cache",))
+def mla_store(kv: Tensor, gamma: Tensor, eps: float, q_rope: Tensor, cos_sin: Tensor, positions: Tensor,
+              slots: Tensor, cache: Tensor, interleaved: bool) -> Tensor:
+    """The new tokens' cache rows (RMSNorm of kv's latent, rotated key) written
+    at their slots, and q_rope [T, H, 64] rotated; a token with a negative slot
+    leaves the cache alone."""
+    L = _check_mla_store(kv, gamma, q_rope, cos_sin, positions, slots, cache)
+    T, H, _ = q_rope.shape
+    q_out = torch.empty(T, H, _MLA_ROPE, dtype=torch.bfloat16, device=kv.device)
+    if T == 0:
+        return q_out
+    kv, q = _vec(kv), _vec(q_rope)
+    _capi().mxfp4_mla_store(kv, kv.stride(0), gamma.contiguous(), eps, q if H else None, q.stride(0), q.stride(1),
+                            q_out if H else None, q_out.stride(0), q_out.stride(1), H, cos_sin.contiguous(),
+                            cos_sin.shape[0], positions.contiguous(), slots.contiguous(), cache, cache.stride(0),
+                            cache.shape[1], cache.shape[0], T, L, _MLA_ROPE, interleaved, _stream(kv))
+    return q_out
+
+
+@mla_store.register_fake
+def _(kv, gamma, eps, q_rope, cos_sin, positions, slots, cache, interleaved):
+    _check_mla_store(kv, gamma, q_rope, cos_sin, positions, slots, cache)
+    return kv.new_empty(q_rope.shape)
+
+
+def _check_mla_decode(q_lat, q_rope, cache, page_table, seq_lens) -> int:
+    where = "mxfp4::mla_decode"
+    bf, i32 = torch.bfloat16, torch.int32
+    _check_args(where, q_lat, q_rope, cache, page_table, seq_lens, dtypes=(bf, bf, bf, i32, i32))
+    _, _, L = _check_cache(where, cache)
+    torch._check(q_lat.dim() == 3 and q_lat.shape[2] == L,
+                 lambda: f"{where}: q_lat must be [H, T, {L}], got {tuple(q_lat.shape)}")
+    H, T = q_lat.shape[0], q_lat.shape[1]
+    torch._check(H > 0 and q_rope.shape == (T, H, _MLA_ROPE),
+                 lambda: f"{where}: q_rope must be [{T}, {H}, {_MLA_ROPE}], got {tuple(q_rope.shape)}")
+    torch._check(page_table.dim() == 2 and page_table.shape[1] > 0 and seq_lens.dim() == 1
+                 and seq_lens.shape[0] == page_table.shape[0],
+                 lambda: f"{where}: page_table must be [S, pages] and seq_lens [S], got {tuple(page_table.shape)} and "
+                         f"{tuple(seq_lens.shape)}")
+    S = seq_lens.shape[0]
+    torch._check(S > 0 and T % S == 0 if T else True,
+                 lambda: f"{where}: {T} tokens do not share out over {S} sequences")
+    return L
+
+
+@custom_op("mxfp4::mla_decode", mutates_args=())
+def mla_decode(q_lat: Tensor, q_rope: Tensor, cache: Tensor, page_table: Tensor, seq_lens: Tensor,
+               scale: float) -> tuple[Tensor, Tensor]:
+    """Absorbed attention of the newest T / S tokens of each of S sequences:
+    q_lat [H, T, L] (the K-up product), q_rope [T, H, 64] -> out [H, T, L] (the
+    V-up product's input) and the log-sum-exp [T, H]."""
+    L = _check_mla_decode(q_lat, q_rope, cache, page_table, seq_lens)
+    c = _capi()
+    H, T, _ = q_lat.shape
+    S = seq_lens.shape[0]
+    out = torch.empty(H, T, L, dtype=torch.bfloat16, device=q_lat.device)
+    lse = torch.empty(T, H, dtype=torch.float32, device=q_lat.device)
+    if T == 0:
+        return out, lse
+    q_lat, q_rope, lens = _vec(q_lat), _vec(q_rope), seq_lens.contiguous()
+    table = page_table if page_table.stride(1) == 1 else page_table.contiguous()
+    nbytes = c.mxfp4_mla_decode_workspace_bytes(S, T // S, H, L, table.shape[1] * cache.shape[1])
+    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q_lat.device)
+    c.mxfp4_mla_decode(q_lat, q_lat.stride(1), q_lat.stride(0), q_rope, q_rope.stride(0), q_rope.stride(1), cache,
+                       cache.stride(0), cache.shape[1], cache.shape[0], table, table.stride(0), table.shape[1], lens,
+                       out, out.stride(1), out.stride(0), lse, S, T // S, H, L, _MLA_ROPE, scale, ws, nbytes,
+                       _stream(q_lat))
+    return out, lse
+
+
+@mla_decode.register_fake
+def _(q_lat, q_rope, cache, page_table, seq_lens, scale):
+    _check_mla_decode(q_lat, q_rope, cache, page_table, seq_lens)
+    return q_lat.new_empty(q_lat.shape), q_lat.new_empty(q_lat.shape[1], q_lat.shape[0], dtype=torch.float32)
+
+
+def _check_mla_prefill(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k) -> None:
+    where = "mxfp4::mla_prefill"
+    bf, i32 = torch.bfloat16, torch.int32
+    _check_args(where, q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, dtypes=(bf, bf, bf, bf, bf, i32, i32))
+    torch._check(q_nope.dim() == 3 and k_nope.dim() == 3 and v.dim() == 3,
+                 lambda: f"{where}: q_nope, k_nope and v must be [tokens, H, *]")
+    T, H, dn = q_nope.shape
+    N, dv = v.shape[0], v.shape[2]
+    torch._check(H > 0 and 0 < dn <= 192 and dn % 8 == 0 and 0 < dv <= 256 and dv % 8 == 0,
+                 lambda: f"{where}: H = {H}, dn = {dn} (multiples of 8 up to 192), dv = {dv} (up to 256)")
+    torch._check(q_rope.shape == (T, H, _MLA_ROPE) and k_nope.shape == (N, H, dn) and v.shape[1] == H
+                 and k_rope.shape == (N, _MLA_ROPE),
+                 lambda: f"{where}: q_rope {tuple(q_rope.shape)}, k_nope {tuple(k_nope.shape)}, k_rope "
+                         f"{tuple(k_rope.shape)}, v {tuple(v.shape)} do not go with q_nope {tuple(q_nope.shape)}")
+    torch._check(cu_q.dim() == 1 and cu_q.shape == cu_k.shape and cu_q.shape[0] > 1,
+                 lambda: f"{where}: cu_q and cu_k must both be [S + 1]")
+
+
+@custom_op("mxfp4::mla_prefill", mutates_args=())
+def mla_prefill(q_nope: Tensor, q_rope: Tensor, k_nope: Tensor, k_rope: Tensor, v: Tensor, cu_q: Tensor,
+                cu_k: Tensor, scale: float, causal: bool) -> tuple[Tensor, Tensor]:
+    """Expanded attention of ragged prompts (sequence s: queries cu_q[s] ..
+    cu_q[s + 1], keys cu_k[s] ..): out [T, H, dv] and the log-sum-exp [T, H].
+    k_rope [N, 64] is shared by all heads; views of one projection are read in
+    place."""
+    _check_mla_prefill(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k)
+    T, H, dn = q_nope.shape
+    N, dv = v.shape[0], v.shape[2]
+    out = torch.empty(T, H, dv, dtype=torch.bfloat16, device=v.device)
+    lse = torch.empty(T, H, dtype=torch.float32, device=v.device)
+    if T == 0:
+        return out, lse
+    if N == 0:
+        return out.zero_(), lse.fill_(float("-inf"))
+    qn, qr, kn, kr, vv = _vec(q_nope), _vec(q_rope), _vec(k_nope), _vec(k_rope), _vec(v)
+    _capi().mxfp4_mla_prefill(qn, qn.stride(0), qn.stride(1), qr, qr.stride(0), qr.stride(1), kn, kn.stride(0),
+                              kn.stride(1), kr, kr.stride(0), vv, vv.stride(0), vv.stride(1), cu_q.contiguous(),
+                              cu_k.contiguous(), cu_q.shape[0] - 1, out, out.stride(0), out.stride(1), lse, T, N, H,
+                              dn, _MLA_ROPE, dv, scale, causal, _stream(v))
+    return out, lse
+
+
+@mla_prefill.register_fake
+def _(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, scale, causal):
+    _check_mla_prefill(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k)
+    T, H = q_nope.shape[0], q_nope.shape[1]
+    return q_nope.new_empty(T, H, v.shape[2]), q_nope.new_empty(T, H, dtype=torch.float32)

@@ -155,3 +155,75 @@ def test_workspace_query(capi):
 
 def test_error_status_has_a_name(capi):
     assert capi.mxfp4_status_string(capi.ERR_INDEX) == "MXFP4_ERR_INDEX"
+
+
+# -------------------------------------------------- operators without a GPU
+def test_operators_trace_and_refuse_on_meta_tensors():
+    import torch
+
+    from mxfp4_quantized_gemm_gb300 import ops  # noqa: F401
+    mx, bf = torch.ops.mxfp4, torch.bfloat16
+
+    def meta(*shape, dtype=bf):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+
+    cache = meta(10, 64, 576)
+    i32, i64, f32 = torch.int32, torch.int64, torch.float32
+    q = mx.mla_store(meta(5, 576), meta(512), 1e-6, meta(5, 8, 64), meta(100, 64, dtype=f32), meta(5, dtype=i64),
+                     meta(5, dtype=i64), cache, False)
+    assert q.shape == (5, 8, 64)
+    out, lse = mx.mla_decode(meta(8, 6, 512), meta(6, 8, 64), cache, meta(3, 4, dtype=i32), meta(3, dtype=i32), 0.1)
+    assert out.shape == (8, 6, 512) and lse.shape == (6, 8) and lse.dtype == f32
+    cu = meta(3, dtype=i32)
+    out, lse = mx.mla_prefill(meta(7, 8, 128), meta(7, 8, 64), meta(9, 8, 128), meta(9, 64), meta(9, 8, 256), cu, cu,
+                              0.1, True)
+    assert out.shape == (7, 8, 256) and lse.shape == (7, 8)
+
+    def store(**change):
+        a = dict(kv=meta(5, 576), gamma=meta(512), eps=1e-6, q_rope=meta(5, 8, 64), cos_sin=meta(100, 64, dtype=f32),
+                 positions=meta(5, dtype=i64), slots=meta(5, dtype=i64), cache=cache, interleaved=True)
+        a.update(change)
+        with pytest.raises(RuntimeError, match="mla_store"):
+            mx.mla_store(**a)
+
+    store(kv=meta(5, 512))
+    store(kv=meta(5, 576, dtype=f32))
+    store(gamma=meta(500))
+    store(q_rope=meta(5, 8, 32))
+    store(q_rope=meta(4, 8, 64))
+    store(cos_sin=meta(100, 64))
+    store(positions=meta(5, dtype=i32))
+    store(slots=meta(6, dtype=i64))
+    store(cache=meta(10, 60, 576), kv=meta(5, 576))
+    store(cache=meta(10, 64, 564), kv=meta(5, 564))
+    store(cache=meta(10, 576, 64).transpose(1, 2))
+
+    def decode(**change):
+        a = dict(q_lat=meta(8, 6, 512), q_rope=meta(6, 8, 64), cache=cache, page_table=meta(3, 4, dtype=i32),
+                 seq_lens=meta(3, dtype=i32), scale=0.1)
+        a.update(change)
+        with pytest.raises(RuntimeError, match="mla_decode"):
+            mx.mla_decode(**a)
+
+    decode(q_lat=meta(8, 6, 256))
+    decode(q_rope=meta(8, 6, 64))
+    decode(page_table=meta(3, 4, dtype=i64))
+    decode(page_table=meta(2, 4, dtype=i32))
+    decode(seq_lens=meta(4, dtype=i32), page_table=meta(4, 4, dtype=i32))
+    decode(cache=meta(10, 64, 576, dtype=f32))
+
+    def prefill(**change):
+        a = dict(q_nope=meta(7, 8, 128), q_rope=meta(7, 8, 64), k_nope=meta(9, 8, 128), k_rope=meta(9, 64),
+                 v=meta(9, 8, 256), cu_q=cu, cu_k=cu, scale=0.1, causal=True)
+        a.update(change)
+        with pytest.raises(RuntimeError, match="mla_prefill"):
+            mx.mla_prefill(**a)
+
+    prefill(q_nope=meta(7, 8, 200), k_nope=meta(9, 8, 200))
+    prefill(v=meta(9, 8, 264))
+    prefill(v=meta(9, 8, 100))
+    prefill(v=meta(9, 4, 256))
+    prefill(k_rope=meta(9, 8, 64))
+    prefill(q_rope=meta(9, 8, 64))
+    prefill(cu_q=meta(4, dtype=i32))
+    prefill(cu_k=meta(3, dtype=i64))
