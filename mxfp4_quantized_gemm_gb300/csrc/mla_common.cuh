@@ -130,6 +130,16 @@ __device__ __forceinline__ void tma_box_3d(void* smem_dst, const CUtensorMap* ma
       : "memory");
 }
 
+// The same of a 4-D tensor map.
+__device__ __forceinline__ void tma_box_4d(void* smem_dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                           uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // One box, shared memory -> a 3-D tensor map; and the wait, by the same thread,
 // until its boxes have been read from shared memory (which may then be used
 // again, or given up: the writes complete with the grid).
@@ -288,21 +298,37 @@ inline PFN_cuTensorMapEncodeTiled_v12000 mla_tensor_map_encoder() {
   return fn;
 }
 
-// Tensor map of a bf16 tensor [d2][d1][d0] with strides (elements) s1, s2 of
-// its outer dimensions, read in boxes b0 x b1 x b2 with the 128-byte swizzle
+// Tensor map of a bf16 tensor of `n` dimensions (innermost first) with strides
+// (elements) of all but the innermost, read in boxes with the 128-byte swizzle
 // and zero fill outside.
-inline cudaError_t mla_tensor_map(CUtensorMap* map, const void* p, int64_t d0, int64_t d1, int64_t d2, int64_t s1,
-                                  int64_t s2, int b0, int b1, int b2) {
+template <int n>
+cudaError_t mla_tensor_map_nd(CUtensorMap* map, const void* p, const int64_t (&d)[n], const int64_t (&stride)[n - 1],
+                              const int (&b)[n]) {
   auto encode = mla_tensor_map_encoder();
   if (encode == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(d2)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(b0), static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2)};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr,
+  cuuint64_t dims[n], strides[n - 1];
+  cuuint32_t box[n], estr[n];
+  for (int i = 0; i < n; ++i) {
+    dims[i] = static_cast<cuuint64_t>(d[i]);
+    box[i] = static_cast<cuuint32_t>(b[i]);
+    estr[i] = 1;
+  }
+  for (int i = 0; i + 1 < n; ++i) strides[i] = static_cast<cuuint64_t>(stride[i]) * 2;
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n, const_cast<void*>(p), dims, strides, box, estr,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+// [d2][d1][d0]
+inline cudaError_t mla_tensor_map(CUtensorMap* map, const void* p, int64_t d0, int64_t d1, int64_t d2, int64_t s1,
+                                  int64_t s2, int b0, int b1, int b2) {
+  return mla_tensor_map_nd<3>(map, p, {d0, d1, d2}, {s1, s2}, {b0, b1, b2});
+}
+// The same tensor as 64-value chunks of d0 (a multiple of 64), `chunks` of them
+// to a box, which lie one behind the other: [chunk][b2][b1][64].
+inline cudaError_t mla_tensor_map_chunks(CUtensorMap* map, const void* p, int64_t d0, int64_t d1, int64_t d2, int64_t s1,
+                                         int64_t s2, int chunks, int b1, int b2) {
+  return mla_tensor_map_nd<4>(map, p, {64, d1, d2, d0 / 64}, {s1, s2, 64}, {64, b1, b2, chunks});
 }
 
 // Launch as a programmatic dependent of the kernel ahead on the stream, in

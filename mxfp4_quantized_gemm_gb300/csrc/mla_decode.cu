@@ -71,6 +71,7 @@ struct DecodeArgs {
   int HB, TB, TPT;        // heads and tokens per box, tokens per row group
   int head_blocks, RT;    // row groups per token block, per sequence
   int bufs;               // tiles in shared memory
+  int q_box, wide;        // chunks of the queries per copy; whether a copy takes all of a tile's group
   float c;                // |scale| * log2(e)
   bool flip;              // scale < 0: the scores change sign first
 };
@@ -206,7 +207,8 @@ __device__ __forceinline__ bool group_row(const DecodeArgs& a, int rt, int j, in
 template <int NB>
 __global__ void __launch_bounds__(kDecThreads, 1)
     mla_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap rmap,
-                      const __grid_constant__ CUtensorMap cmap, const DecodeArgs a) {
+                      const __grid_constant__ CUtensorMap cmap0, const __grid_constant__ CUtensorMap cmap1,
+                      const DecodeArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int nk = a.L >> 7;                                  // 128-value blocks of the latent
@@ -255,7 +257,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     mbar_init(&o_empty, 128);
     fence_mbar_init();
   }
-  if (warp == 0 && lane < 3) prefetch_tensor_map(lane == 0 ? &qmap : (lane == 1 ? &rmap : &cmap));
+  if (warp == 0 && lane < 4)
+    prefetch_tensor_map(lane == 0 ? &qmap : (lane == 1 ? &rmap : (lane == 2 ? &cmap0 : &cmap1)));
   if (warp == 1) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
@@ -300,8 +303,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const int tk0 = g.s * a.q_len + (g.rt / a.head_blocks) * a.TPT;
       if (lane == 0) mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(chunks * a.HB * a.TB * 128));
       __syncwarp();
-      if (lane < 2 * nk) tma_box_3d(qsm + lane * kQChunk, &qmap, lane * 64, h0, tk0, &q_full);
-      if (lane == 31) tma_box_3d(qsm + 2 * nk * kQChunk, &rmap, 0, h0, tk0, &q_full);
+      if (elect_one()) {
+        for (int c = 0; c < 2 * nk; c += a.q_box) tma_box_4d(qsm + c * kQChunk, &qmap, 0, h0, tk0, c, &q_full);
+        tma_box_4d(qsm + 2 * nk * kQChunk, &rmap, 0, h0, tk0, 0, &q_full);
+      }
+      __syncwarp();
       ++seg_no;
       for (int t = g.t0; t < g.t1; ++t) {
         const int cur_nb = nb, cur_row = row;
@@ -315,13 +321,22 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         for (int x = 0; x < groups; ++x) {
           const int c0 = x == 0 ? 0 : split, c1 = x + 1 == groups ? chunks : split;
           if (!warp_wait(&empty[x][r.slot], r.turn ^ 1u, abort)) break;
-          if (lane == 0)
-            mbar_arrive_expect_tx(&full[x][r.slot], static_cast<uint32_t>((c1 - c0) * cur_nb * a.box_rows * 128));
+          const uint32_t bytes = static_cast<uint32_t>((c1 - c0) * cur_nb * a.box_rows * 128);
+          if (a.wide) {
+            // (a tile is one box's rows: every lane has the same page and row)
+            if (elect_one()) {
+              mbar_arrive_expect_tx(&full[x][r.slot], bytes);
+              tma_box_4d(buf + c0 * kChunkBytes, x == 0 ? &cmap0 : &cmap1, 0, cur_row, cur_page, c0, &full[x][r.slot]);
+            }
+          } else {
+            if (lane == 0) mbar_arrive_expect_tx(&full[x][r.slot], bytes);
+            __syncwarp();
+            if (box < cur_nb)
+              for (int c = c0 + lane / boxes; c < c1; c += 32 / boxes)
+                tma_box_4d(buf + c * kChunkBytes + box * a.box_rows * 128, &cmap0, 0, cur_row, cur_page, c,
+                           &full[x][r.slot]);
+          }
           __syncwarp();
-          if (box < cur_nb)
-            for (int c = c0 + lane / boxes; c < c1; c += 32 / boxes)
-              tma_box_3d(buf + c * kChunkBytes + box * a.box_rows * 128, &cmap, c * 64, cur_row, cur_page,
-                         &full[x][r.slot]);
           ++fills;
         }
         if (abort) break;
@@ -811,7 +826,7 @@ bool mla_decode_fits(int S, int q_len, int H) {
 static std::atomic<bool> g_decode_attr[3][64];
 
 template <int NB>
-static cudaError_t launch_decode_nb(const CUtensorMap (&maps)[3], DecodeArgs a, int grid, const DeviceInfo& dev,
+static cudaError_t launch_decode_nb(const CUtensorMap (&maps)[4], DecodeArgs a, int grid, const DeviceInfo& dev,
                                     cudaStream_t s) {
   constexpr int kIdx = NB == 64 ? 2 : (NB == 32 ? 1 : 0);
   auto kern = mla_decode_kernel<NB>;
@@ -830,7 +845,7 @@ static cudaError_t launch_decode_nb(const CUtensorMap (&maps)[3], DecodeArgs a, 
   a.bufs = (kDecSmem - kDecStatic - fixed) / tile;
   if (a.bufs > kDecMaxBufs) a.bufs = kDecMaxBufs;
   return mla_launch(kern, dim3(static_cast<unsigned>(grid)), kDecThreads, fixed + a.bufs * tile, s, maps[0],
-                    maps[1], maps[2], a);
+                    maps[1], maps[2], maps[3], a);
 }
 
 cudaError_t launch_mla_decode(const MlaDecodeProblem& p, const DeviceInfo& dev, cudaStream_t s) {
@@ -865,17 +880,27 @@ cudaError_t launch_mla_decode(const MlaDecodeProblem& p, const DeviceInfo& dev, 
   a.flip = p.scale < 0.f;
   a.c = positive_scale(a.flip ? -p.scale : p.scale);
 
-  CUtensorMap maps[3];
+  // Chunks to a copy: all of the queries, or of a tile's group, where their rows
+  // lie as the products want them (a full group of rows, pages of whole tiles).
+  // A copy of one chunk takes as long to issue as one of all of them.
+  const int values = 2 * (p.L / 128), split = values > 2 ? values - 2 : values + 1;
+  a.q_box = r.HB * r.TB == r.NB ? values : 1;
+  a.wide = a.box_rows == kTileTok ? 1 : 0;
+  CUtensorMap maps[4];
   const int64_t T = static_cast<int64_t>(p.S) * p.q_len;
   const int64_t row = p.L + kMlaRope;
-  if ((e = mla_tensor_map(&maps[0], p.q_lat.p, p.L, p.H, T, p.q_lat.head, p.q_lat.tok, 64, r.HB, r.TB)) != cudaSuccess)
-    return e;
-  if ((e = mla_tensor_map(&maps[1], p.q_rope.p, kMlaRope, p.H, T, p.q_rope.head, p.q_rope.tok, 64, r.HB, r.TB)) !=
+  if ((e = mla_tensor_map_chunks(&maps[0], p.q_lat.p, p.L, p.H, T, p.q_lat.head, p.q_lat.tok, a.q_box, r.HB, r.TB)) !=
       cudaSuccess)
     return e;
-  if ((e = mla_tensor_map(&maps[2], p.cache.p, row, p.cache.page_size, p.cache.num_pages, row, p.cache.page_stride, 64,
-                          a.box_rows, 1)) != cudaSuccess)
+  if ((e = mla_tensor_map_chunks(&maps[1], p.q_rope.p, kMlaRope, p.H, T, p.q_rope.head, p.q_rope.tok, 1, r.HB, r.TB)) !=
+      cudaSuccess)
     return e;
+  for (int x = 0; x < 2; ++x) {
+    const int box = !a.wide ? 1 : (x == 0 ? split : 3);
+    if ((e = mla_tensor_map_chunks(&maps[2 + x], p.cache.p, row, p.cache.page_size, p.cache.num_pages, row,
+                                   p.cache.page_stride, box, a.box_rows, 1)) != cudaSuccess)
+      return e;
+  }
   const int grid = decode_grid(p.S, r, a.capacity, dev.sm_count);
   e = r.NB == 16 ? launch_decode_nb<16>(maps, a, grid, dev, s)
                  : (r.NB == 32 ? launch_decode_nb<32>(maps, a, grid, dev, s)
