@@ -121,15 +121,50 @@ struct QueryTile {
   int tiles;   // key tiles
 };
 
-// The query tiles of a block or pair, found by each warp for itself; a lane
-// holds the prefix sum of its share of the sequences (and, of up to 32, its
-// sequence: the way from one query tile to the next then has no loads on it).
+// The query tiles of a block or pair.  A sequence whose queries are no whole
+// number of tiles has the short one in front, where causal queries see the
+// fewest keys.
+//
+// Up to 32 sequences (a lane each) and 64 rounds: the tiles are numbered by
+// their keys, the most first, head by head within a number, and dealt out to
+// and fro; that leaves the blocks' loads 1..5% apart where dealing them out in
+// sequence order left 5..20%.  A block takes what it was dealt in the order of
+// the heads, so that all blocks are at about the same heads at a time and find
+// their keys and values in L2.  Its list is made by all its warps together.
+// Otherwise: in sequence order, last tile first, head by head, found by each
+// warp for itself (more rounds even out by themselves).
+struct ListedTile {
+  uint32_t tile, seq_head;                 // seq_head: the sequence in the upper 5 bits
+};
+constexpr int kPreListed = 64;
+
 template <bool kPair>
 struct QueryTiles {
-  Extent own;
+  static constexpr int kQ = PreShape<kPair>::kQueries;
+  Extent own;                              // up to 32 sequences: the lane's
   int s0, s1, first, incl, total, round, rank;
-  __device__ __forceinline__ QueryTiles(const PrefillArgs& a, int rank_) : round(0), rank(rank_) {
-    constexpr int kQ = PreShape<kPair>::kQueries;
+  int listed;                              // tiles of the list, or -1
+  const ListedTile* list;
+  // of the lane's sequence: the first of its tiles with `keys` key tiles or more
+  __device__ __forceinline__ int with_keys(const PrefillArgs& a, int keys) const {
+    const int n = incl - first;
+    if (keys <= 0) return 0;
+    const int64_t need = static_cast<int64_t>(keys - 1) * kPreTile + 1;
+    if (own.kn < need) return n;
+    if (!a.causal) return 0;
+    // tile t ends before query (t + 1) kQ - short, which sees `back` keys more
+    const int64_t end = need - (own.kn - own.qn) + (n * static_cast<int64_t>(kQ) - own.qn);
+    const int64_t t = ((end + kQ - 1) >> (kPair ? 8 : 7)) - 1;
+    return t < 0 ? 0 : (t > n ? n : static_cast<int>(t));
+  }
+  // what a round deals to this block or pair
+  __device__ __forceinline__ int64_t dealt(int r) const {
+    const int n = static_cast<int>(gridDim.x) / PreShape<kPair>::kBlocks;
+    const int c = static_cast<int>(blockIdx.x) / PreShape<kPair>::kBlocks;
+    return static_cast<int64_t>(r) * n + ((r & 1) ? n - 1 - c : c);
+  }
+  // (all threads of the block)
+  __device__ __forceinline__ QueryTiles(const PrefillArgs& a, int rank_, ListedTile* room) : round(0), rank(rank_), list(room) {
     const int lane = threadIdx.x & 31, per = (a.S + 31) >> 5;
     s0 = min(a.S, lane * per);
     s1 = min(a.S, s0 + per);
@@ -149,43 +184,81 @@ struct QueryTiles {
     }
     first = incl - mine;
     total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+    const int64_t n = gridDim.x / PreShape<kPair>::kBlocks, all = static_cast<int64_t>(total) * a.H;
+    listed = -1;
+    if (a.S > 32 || all > kPreListed * n) return;
+    const int rounds = (static_cast<int>(all) + static_cast<int>(n) - 1) / static_cast<int>(n);
+    listed = rounds - (rounds > 0 && dealt(rounds - 1) >= all ? 1 : 0);
+    const int most = static_cast<int>(
+        __reduce_max_sync(0xFFFFFFFFu, (static_cast<uint32_t>(own.kn) + kPreTile - 1) / kPreTile));
+    auto head = [&](int r) { return r < listed ? static_cast<int>(dealt(r)) % a.H : 0x7FFFFFFF; };
+    const int h0 = head(lane), h1 = head(lane + 32);
+    for (int r = threadIdx.x >> 5; r < listed; r += kPreThreads / 32) {
+      const int at = static_cast<int>(dealt(r)), number = at / a.H, h = at - number * a.H;
+      const int place = __popc(__ballot_sync(0xFFFFFFFFu, h0 < h || (h0 == h && lane < r))) +
+                        __popc(__ballot_sync(0xFFFFFFFFu, h1 < h || (h1 == h && lane + 32 < r)));
+      // its key tiles: the most that more than `number` tiles have
+      int lo = 0, hi = most;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__reduce_add_sync(0xFFFFFFFFu, mine - with_keys(a, mid)) > number)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const int from_tile = with_keys(a, lo), to_tile = with_keys(a, lo + 1);
+      const int skip = number - __reduce_add_sync(0xFFFFFFFFu, mine - to_tile);
+      int upto = to_tile - from_tile;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, upto > skip)) - 1)
+        room[place] = ListedTile{static_cast<uint32_t>(to_tile - (upto - skip)),
+                                 static_cast<uint32_t>(lane) << 27 | static_cast<uint32_t>(h)};
+    }
+    __syncthreads();
   }
   __device__ __forceinline__ bool next(const PrefillArgs& a, QueryTile& x) {
-    constexpr int kQ = PreShape<kPair>::kQueries;
-    const int n = static_cast<int>(gridDim.x) / PreShape<kPair>::kBlocks;
-    const int c = static_cast<int>(blockIdx.x) / PreShape<kPair>::kBlocks;
-    const int64_t at = static_cast<int64_t>(round) * n + ((round & 1) ? n - 1 - c : c);
-    const int64_t all = static_cast<int64_t>(total) * a.H;
-    if (at >= all) return false;                      // (the rounds that follow lie past the end too)
-    ++round;
-    // (a 64-bit division takes several times a 32-bit one)
-    x.h = all <= 0x7FFFFFFF ? static_cast<int>(at) / total : static_cast<int>(at / total);
-    const int want = total - 1 - static_cast<int>(at - static_cast<int64_t>(x.h) * total);
-    // the lane whose share holds it
-    const bool here = want >= first && want < incl;
-    int seq = 0, tile = want - first;
-    if (here && a.S > 32)
-      for (seq = s0; seq < s1; ++seq) {
-        const int m = (extent(a, seq).qn + kQ - 1) / kQ;
-        if (tile < m) break;
-        tile -= m;
-      }
-    const int from = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
-    tile = __shfl_sync(0xFFFFFFFFu, tile, from);
-    if (a.S <= 32) {
+    int tile;
+    if (listed >= 0) {
+      if (round >= listed) return false;
+      const ListedTile at = list[round++];
+      const int from = static_cast<int>(at.seq_head >> 27);
+      tile = static_cast<int>(at.tile);
+      x.h = static_cast<int>(at.seq_head & 0x07FFFFFFu);
       x.ex.q0 = __shfl_sync(0xFFFFFFFFu, own.q0, from);
       x.ex.qn = __shfl_sync(0xFFFFFFFFu, own.qn, from);
       x.ex.k0 = __shfl_sync(0xFFFFFFFFu, own.k0, from);
       x.ex.kn = __shfl_sync(0xFFFFFFFFu, own.kn, from);
     } else {
+      const int64_t all = static_cast<int64_t>(total) * a.H, at = dealt(round);
+      if (at >= all) return false;                    // (the rounds that follow lie past the end too)
+      ++round;
+      // (a 64-bit division takes several times a 32-bit one)
+      x.h = all <= 0x7FFFFFFF ? static_cast<int>(at) / total : static_cast<int>(at / total);
+      const int want = total - 1 - static_cast<int>(at - static_cast<int64_t>(x.h) * total);
+      // the lane whose share holds it
+      const bool here = want >= first && want < incl;
+      int seq = 0;
+      tile = want - first;
+      if (here)
+        for (seq = s0; seq < s1; ++seq) {
+          const int m = (extent(a, seq).qn + kQ - 1) / kQ;
+          if (tile < m) break;
+          tile -= m;
+        }
+      const int from = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
+      tile = __shfl_sync(0xFFFFFFFFu, tile, from);
       x.ex = extent(a, __shfl_sync(0xFFFFFFFFu, seq, from));
     }
-    const int pq0 = tile * kQ;
-    x.qi0 = pq0 + rank * kPreTile;
-    x.rows = clamp_to(x.ex.qn - x.qi0, kPreTile);
+    const int end = x.ex.qn - ((x.ex.qn + kQ - 1) / kQ - 1 - tile) * kQ;   // one past its last query
+    x.qi0 = max(0, end - kQ) + rank * kPreTile;
+    x.rows = clamp_to(end - x.qi0, kPreTile);
     const int back = x.ex.kn - x.ex.qn;
     x.see0 = a.causal ? clamp_to(x.qi0 + 1 + back, x.ex.kn) : x.ex.kn;
-    x.see1 = a.causal ? clamp_to(min(pq0 + kQ, x.ex.qn) + back, x.ex.kn) : x.ex.kn;
+    x.see1 = a.causal ? clamp_to(end + back, x.ex.kn) : x.ex.kn;
     x.tiles = (x.see1 + kPreTile - 1) / kPreTile;
     return true;
   }
@@ -227,6 +300,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   __shared__ __align__(8) uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], drained;
   __shared__ uint32_t tmem_slot;
   __shared__ float xch[2][kPreTile];
+  __shared__ ListedTile list[kPreListed];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = kPair ? cluster_ctarank() : 0u;
@@ -270,7 +344,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   const uint32_t tmem = tmem_slot;
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  QueryTiles<kPair> walk(a, static_cast<int>(rank));
+  QueryTiles<kPair> walk(a, static_cast<int>(rank), list);
   QueryTile x;
 
   if (warp == 0) {
@@ -376,7 +450,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       }
     };
     int i = 0, no = 0;
-    while (!abort && walk.next_real(a, x)) {
+    bool more = walk.next_real(a, x);
+    while (!abort && more) {
       if (!warp_wait(&q_full, static_cast<uint32_t>(no) & 1u, abort)) break;
       ++no;
       for (int t = 0; t < x.tiles && !abort; ++t, ++i) {
@@ -408,7 +483,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         if (t > 0 && !abort) output(i - 1, kPreTile, t == 1);
       }
-      if (!abort) output(i - 1, x.see1 - (x.tiles - 1) * kPreTile, x.tiles == 1);
+      const int last = x.see1 - (x.tiles - 1) * kPreTile;
+      const bool only = x.tiles == 1;
+      more = walk.next_real(a, x);                    // (beside the last softmax)
+      if (!abort) output(i - 1, last, only);
     }
     drain_mmas<kPair>(&drained, abort);
   } else if (kPair && warp == 1) {
@@ -453,7 +531,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     const uint32_t tl = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
     const int dvp = (a.dv + 31) & ~31;                // accumulator columns, in halves of 16
     int i = 0;
-    while (walk.next(a, x)) {
+    QueryTile then;
+    for (bool more = walk.next(a, x); more; x = then) {
       const int back = x.ex.kn - x.ex.qn;
       const int see = row < x.rows ? (a.causal ? clamp_to(x.qi0 + row + 1 + back, x.ex.kn) : x.ex.kn) : 0;
       float m = 0.f, l = 0.f;
@@ -543,6 +622,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       named_sync(1 + q4, 64);
       l = xch[0][row] + xch[1][row];
       named_sync(1 + q4, 64);                         // xch is free again
+      more = walk.next(a, then);                      // (beside the last output product)
       if (x.tiles > 0) {
         mbar_wait(&pv_done[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort);
         __syncwarp();
