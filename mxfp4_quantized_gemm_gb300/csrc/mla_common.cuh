@@ -140,6 +140,13 @@ __device__ __forceinline__ void tma_box_4d(void* smem_dst, const CUtensorMap* ma
       : "memory");
 }
 
+// A word that another kernel may be writing: read from L2, and never kept in L1.
+__device__ __forceinline__ int ld_relaxed(const int* p) {
+  int v;
+  asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // One box, shared memory -> a 3-D tensor map; and the wait, by the same thread,
 // until its boxes have been read from shared memory (which may then be used
 // again, or given up: the writes complete with the grid).

@@ -78,10 +78,10 @@ struct DecodeArgs {
 };
 
 // Positions of sequence s (a bad length is cut to what the table holds).
-__device__ __forceinline__ int seq_len(const DecodeArgs& a, int s) {
-  const int n = __ldg(a.seq_lens + s);
+__device__ __forceinline__ int cut_len(const DecodeArgs& a, int n) {
   return n < 0 ? 0 : (n > a.capacity ? static_cast<int>(a.capacity) : n);
 }
+__device__ __forceinline__ int seq_len(const DecodeArgs& a, int s) { return cut_len(a, __ldg(a.seq_lens + s)); }
 // Work units of one row group: `over` for going over to it (queries to fetch, a
 // part or the rows before it to write out), then its tiles; or one for an empty
 // sequence (whose rows still have to be written).
@@ -120,14 +120,34 @@ struct Segment {
 struct Walk {
   int64_t left;       // units still to hand out
   int s, rt, off;
+  int own[2];         // up to 64 sequences: the lengths of the lane's
+  static constexpr int kOwn = 64;
+  // (from L2: it may be read before the kernels ahead are done, and again then)
+  __device__ __forceinline__ void read_own(const DecodeArgs& a) {
+    const int lane = threadIdx.x & 31, s0 = a.S <= 32 ? lane : 2 * lane, s1 = a.S <= 32 ? a.S : s0 + 1;
+    const int n0 = s0 < a.S ? ld_relaxed(a.seq_lens + s0) : 0, n1 = s1 < a.S ? ld_relaxed(a.seq_lens + s1) : 0;
+    own[0] = cut_len(a, n0);
+    own[1] = cut_len(a, n1);
+  }
+  // (the whole warp)
+  __device__ __forceinline__ int len_of(const DecodeArgs& a, int seq) const {
+    if (a.S <= 32) return __shfl_sync(0xFFFFFFFFu, own[0], seq);
+    if (a.S <= kOwn) return __shfl_sync(0xFFFFFFFFu, (seq & 1) ? own[1] : own[0], seq >> 1);
+    return seq_len(a, seq);
+  }
   // The block's stretch, found by each warp for itself (one round of loads,
   // no barrier).
   __device__ __forceinline__ void start(const DecodeArgs& a) {
     const int lane = threadIdx.x & 31;
     const int per = (a.S + 31) >> 5, s0 = min(a.S, lane * per), s1 = min(a.S, s0 + per);
     int64_t mine = 0;
+    if (a.S <= kOwn) {
+      if (s0 < s1) mine = group_units(a, own[0]);
+      if (s0 + 1 < s1) mine += group_units(a, own[1]);
+    } else {
 #pragma unroll 4
-    for (int i = s0; i < s1; ++i) mine += group_units(a, seq_len(a, i));
+      for (int i = s0; i < s1; ++i) mine += group_units(a, seq_len(a, i));
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -146,7 +166,7 @@ struct Walk {
     const bool here = ub >= at && ub < incl * a.RT;
     if (here) {
       for (s = s0; s < s1; ++s) {
-        const int g = group_units(a, seq_len(a, s));
+        const int g = group_units(a, a.S <= kOwn ? (s == s0 ? own[0] : own[1]) : seq_len(a, s));
         const int64_t u = static_cast<int64_t>(g) * a.RT;
         if (ub < at + u) {
           rt = static_cast<int>(div64(ub - at, g));
@@ -165,7 +185,7 @@ struct Walk {
     while (left > 0) {
       g.s = s;
       g.rt = rt;
-      g.len = seq_len(a, s);
+      g.len = len_of(a, s);
       const int units = group_units(a, g.len), from = off;
       g.nt = g.len == 0 ? 0 : units - a.over;
       const int64_t room = units - off;
@@ -181,7 +201,7 @@ struct Walk {
           ++s;
         }
         // nothing but going over to the next group: left to the block behind
-        if (left > 0 && left <= a.over && seq_len(a, s) > 0) left = 0;
+        if (left > 0 && left <= a.over && len_of(a, s) > 0) left = 0;
       }
       if (g.len == 0 || g.t0 < g.t1) return true;
     }
@@ -276,11 +296,30 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  griddep_wait();
-  // only now: the kernel behind reads seq_lens before its own wait
-  if (threadIdx.x == 0) griddep_launch_dependents();
+  // The lengths are most often what they were a while ago: up to 64 are read
+  // and the stretch found while the kernels ahead still run, and read again
+  // when they are done.  (All of it behind the wait, with its code still to be
+  // fetched, put the first copy 6000 to 9000 cycles behind it.)
   Walk walk;
-  walk.start(a);
+  walk.left = 0;
+  if (a.S <= Walk::kOwn) {
+    walk.read_own(a);
+    walk.start(a);
+  }
+  // after the wait: whether the stretch was not as found, and now is
+  auto settle = [&]() {
+    if (a.S <= Walk::kOwn) {
+      const int was0 = walk.own[0], was1 = walk.own[1];
+      walk.read_own(a);
+      if (!__any_sync(0xFFFFFFFFu, walk.own[0] != was0 || walk.own[1] != was1)) return false;
+    }
+    walk.start(a);
+    return true;
+  };
+  if (warp != 0) {
+    griddep_wait();
+    settle();
+  }
 
   if (warp == 0) {
     // ---- copies.  Lane = (box of the tile's positions, chunk), in turns.
@@ -292,18 +331,32 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     // The page and row of the lane's box of tile t, and the boxes that hold
     // anything; asked for a tile ahead.
     int page = 0, row = 0, nb = 0;
-    auto look_up = [&](int t) {
+    const int32_t* entry = a.page_table;
+    auto find = [&](int t) {
       const int tok0 = t * kTileTok;
       nb = (min(kTileTok, g.len - tok0) + a.box_rows - 1) / a.box_rows;
       if (box < nb) {
         const int tok = tok0 + box * a.box_rows;
         const int col = tok / a.page_size;
         row = tok - col * a.page_size;
-        page = __ldg(a.page_table + g.s * a.table_stride + col);
+        entry = a.page_table + g.s * a.table_stride + col;
       }
     };
-    while (!abort && walk.next_real(a, g)) {
-      look_up(g.t0);
+    bool sure = false;                       // the kernels ahead are done
+    while (!abort) {
+      const bool more = walk.next_real(a, g);
+      if (more) find(g.t0);
+      if (!sure) {
+        griddep_wait();
+        sure = true;
+        // only now: the kernel behind reads seq_lens before its own wait
+        if (lane == 0) griddep_launch_dependents();
+        if (more && box < nb) page = __ldg(entry);
+        if (settle()) continue;
+      } else if (more && box < nb) {
+        page = __ldg(entry);
+      }
+      if (!more) break;
       // the queries: their buffer is free once the last score product of the
       // stretch before has read it (a barrier of its own: a parity says nothing
       // about one that may be two phases behind, as s_full is to this warp)
@@ -325,7 +378,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           atomicOr(&g_mla_decode_error, kErrIndex);
           cur_page = a.num_pages;            // outside the map: the box is filled with zeros
         }
-        if (t + 1 < g.t1) look_up(t + 1);
+        if (t + 1 < g.t1) {
+          find(t + 1);
+          if (box < nb) page = __ldg(entry);
+        }
         uint8_t* buf = ring + r.slot * tile_bytes;
         for (int x = 0; x < groups; ++x) {
           const int c0 = x == 0 ? 0 : split, c1 = x + 1 == groups ? chunks : split;
