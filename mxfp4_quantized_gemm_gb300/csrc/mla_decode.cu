@@ -26,12 +26,14 @@
 // is at the next stretch (131 KB of fp32 for a part: done by the softmax warps
 // it stood for 17000 cycles between two stretches, four tiles' worth).  A row's running maximum is raised only when a score passes it by
 // 2^8 (first tile aside), which one barrier with an OR decides.
-// A copying warp spends about 430 cycles on each wait, arrival and copy and
-// 16 on each further copy, so a tile comes in two groups, each under one
-// barrier: all but the last 128 latent values, and those with the rotated key
-// (little is left to multiply when the last of a tile lands).  A group per
-// 128 values, given back as the output product is done with it, was no faster
-// (86.4 against 85.4 us at 64 sequences of up to 8192).
+// A copying warp spends about 430 cycles on each wait, arrival and copy, and
+// each copy more costs it 16 by one thread and about 100 by lanes in turns.  Where
+// a page holds whole tiles a group of chunks is one copy, and a tile comes in
+// groups of 128 latent values, the last with the rotated key: each is multiplied
+// as it lands and given back as the output product is done with it (16 x 4096
+// 25.0 us, in two groups 25.5).  Smaller pages take a copy for each box of rows
+// and chunk, by lanes that hold a box's page each, in two groups (32 x 3001 in
+// pages of 16: 27.8 us; in four groups 30.4, by one thread 34.3).
 //
 // Work split: the tiles of all row groups, in order, are cut evenly over the
 // grid; a block takes its stretch wherever sequences begin and end, so a
@@ -243,8 +245,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   const int nk = a.L >> 7;                                  // 128-value blocks of the latent
   const int chunks = 2 * nk + 1;                            // 64-value chunks of a cache row
   const int tile_bytes = chunks * kChunkBytes;
-  const int groups = nk > 1 ? 2 : 1;                        // of a tile's chunks
-  const int split = 2 * (nk - 1);                           // the last group's first chunk
+  // groups of a tile's chunks: the last three chunks, and in front of them two
+  // to a group, or one group of all
+  const int groups = a.wide || nk == 1 ? nk : 2;
   // the 64-row score MMA reads 64 rows of a query chunk whatever NB is: the
   // queries lie in front, so that what it reads past them is inside the buffer
   uint8_t* qsm = smem;                                      // chunks of NB rows x 64 values
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   uint8_t* ring = psm + NB * 128;
   constexpr int kQChunk = NB * 128;
 
-  __shared__ __align__(8) uint64_t full[2][kDecMaxBufs], empty[2][kDecMaxBufs];
+  __shared__ __align__(8) uint64_t full[4][kDecMaxBufs], empty[4][kDecMaxBufs];
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], q_full, q_empty, pv_done, o_empty, drain[2];
   // of a stretch, by its number's parity: the softmax may be a whole stretch
   // ahead of the warps that write out, but not two
@@ -263,13 +266,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   // 1 / sum of a finished stretch's rows, for the warps that write it out.  They
   // give the accumulator back before they are done with the sums, so that those
   // of two further stretches may come in beside them: three in use at most.
-  __shared__ __align__(16) float fin[4][NB];
+  __shared__ __align__(16) float fin[3][NB];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   bool abort = false;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kDecMaxBufs; ++s)
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < 4; ++x) {
         mbar_init(&full[x][s], 1);
         mbar_init(&empty[x][s], 1);
       }
@@ -383,15 +386,16 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           if (box < nb) page = __ldg(entry);
         }
         uint8_t* buf = ring + r.slot * tile_bytes;
-        for (int x = 0; x < groups; ++x) {
-          const int c0 = x == 0 ? 0 : split, c1 = x + 1 == groups ? chunks : split;
+        for (int x = 0, c0 = 0; x < groups; ++x) {
+          const int c1 = x + 1 == groups ? chunks : (groups == nk ? 2 * x + 2 : 2 * nk - 2);
           if (!warp_wait(&empty[x][r.slot], r.turn ^ 1u, abort)) break;
           const uint32_t bytes = static_cast<uint32_t>((c1 - c0) * cur_nb * a.box_rows * 128);
           if (a.wide) {
             // (a tile is one box's rows: every lane has the same page and row)
             if (elect_one()) {
               mbar_arrive_expect_tx(&full[x][r.slot], bytes);
-              tma_box_4d(buf + c0 * kChunkBytes, x == 0 ? &cmap0 : &cmap1, 0, cur_row, cur_page, c0, &full[x][r.slot]);
+              tma_box_4d(buf + c0 * kChunkBytes, x + 1 < groups ? &cmap0 : &cmap1, 0, cur_row, cur_page, c0,
+                         &full[x][r.slot]);
             }
           } else {
             if (lane == 0) mbar_arrive_expect_tx(&full[x][r.slot], bytes);
@@ -402,6 +406,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                            &full[x][r.slot]);
           }
           __syncwarp();
+          c0 = c1;
           ++fills;
         }
         if (abort) break;
@@ -429,8 +434,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         // tile i - 2's scores have been read once its weights are out
         if (i >= 2 && !warp_wait(&p_full[i & 1], static_cast<uint32_t>((i >> 1) + 1) & 1u, abort)) break;
         const uint32_t sb = ring_a + static_cast<uint32_t>(r.slot * tile_bytes);
-        for (int x = 0; x < groups; ++x) {
-          const int c0 = x == 0 ? 0 : split, c1 = x + 1 == groups ? chunks : split;
+        for (int x = 0, c0 = 0; x < groups; ++x) {
+          const int c1 = x + 1 == groups ? chunks : (groups == nk ? 2 * x + 2 : 2 * nk - 2);
           if (!warp_wait(&full[x][r.slot], r.turn, abort)) break;
           tc_fence_after();
           if (elect_one()) {
@@ -446,6 +451,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             }
           }
           __syncwarp();
+          c0 = c1;
         }
         if (abort) break;
         r.step();
@@ -485,9 +491,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             for (int m = 0; m < 4; ++m)
               if (m < ks)
                 mma_bf16(tmem + static_cast<uint32_t>(k) * 64u, ad + m * 128, pd + m * 2, idesc, t != g.t0 || m != 0);
-            if (k + 2 == nk) mma_commit(&empty[0][r.slot]);
+            if (groups == nk || k + 2 >= nk) mma_commit(&empty[k + groups - nk][r.slot]);
           }
-          mma_commit(&empty[groups - 1][r.slot]);
           mma_commit(&pv_done);
           if (t + 1 == g.t1) mma_commit(&o_full[(seg_no - 1) & 1]);
         }
@@ -612,7 +617,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         named_sync(1, 256);
         if (half == 0 && mine) {
           const float sum = xch[0][row] + xch[1][row];
-          fin[seg_no & 3][row] = sum == 0.f ? 0.f : 1.0f / sum;
+          fin[seg_no % 3][row] = sum == 0.f ? 0.f : 1.0f / sum;
           if (whole) {
             if (a.lse != nullptr && on) a.lse[at * a.H + head] = sum == 0.f ? -INFINITY : (m + log2_fast(sum)) * kLn2;
           } else if (on) {
@@ -650,7 +655,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       if (warp < 12 && !last) continue;
       mbar_wait(&fin_full[seg_no & 1], static_cast<uint32_t>(seg_no >> 1) & 1u, abort);
       mbar_wait(&o_full[seg_no & 1], static_cast<uint32_t>(seg_no >> 1) & 1u, abort);
-      const float* inv = fin[seg_no & 3];
+      const float* inv = fin[seg_no % 3];
       __syncwarp();
       tc_fence_after();
       const bool whole = g.t0 == 0 && g.t1 == g.nt;
@@ -955,7 +960,7 @@ cudaError_t launch_mla_decode(const MlaDecodeProblem& p, const DeviceInfo& dev, 
   // Chunks to a copy: all of the queries, or of a tile's group, where their rows
   // lie as the products want them (a full group of rows, pages of whole tiles).
   // A copy of one chunk takes as long to issue as one of all of them.
-  const int values = 2 * (p.L / 128), split = values > 2 ? values - 2 : values + 1;
+  const int values = 2 * (p.L / 128);
   a.q_box = r.HB * r.TB == r.NB ? values : 1;
   a.wide = a.box_rows == kTileTok ? 1 : 0;
   CUtensorMap maps[4];
@@ -968,7 +973,7 @@ cudaError_t launch_mla_decode(const MlaDecodeProblem& p, const DeviceInfo& dev, 
       cudaSuccess)
     return e;
   for (int x = 0; x < 2; ++x) {
-    const int box = !a.wide ? 1 : (x == 0 ? split : 3);
+    const int box = !a.wide ? 1 : (x == 0 ? 2 : 3);
     if ((e = mla_tensor_map_chunks(&maps[2 + x], p.cache.p, row, p.cache.page_size, p.cache.num_pages, row,
                                    p.cache.page_stride, box, a.box_rows, 1)) != cudaSuccess)
       return e;
