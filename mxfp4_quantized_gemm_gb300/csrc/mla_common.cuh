@@ -186,6 +186,17 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
 #pragma unroll
   for (int i = 0; i < N; i += 16) tmem_ld16(taddr + i, *reinterpret_cast<uint32_t(*)[16]>(&r[i]));
 }
+// 16 lanes x 32 columns, over the whole warp: thread t holds, of columns 8 j +
+// 2 (t % 4) and the next, lane t / 4 in r[4 j], r[4 j + 1] and lane t / 4 + 8 in
+// r[4 j + 2], r[4 j + 3].
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 template <int N>
 __device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
 #pragma unroll

@@ -506,59 +506,76 @@ __global__ void __launch_bounds__(kDecThreads, 1)
    if (warp < 12) {
     // ---- softmax.  These threads meet at named barriers, so they walk every
     // tile even after a wait has given up.  A 64-row MMA leaves row 16 w + x in
-    // lane 32 w + x (x < 16); the other lanes only keep company.
+    // lane 32 w + x (x < 16); read 16 lanes at a time, a thread has two rows, of
+    // which the four threads of a quad hold eight columns each.  (A row to a
+    // thread left half the lanes idle: 1200 cycles a tile.)
     const int w = warp & 3, half = (warp - 4) >> 2, tid = threadIdx.x - 128;
-    const int row = 16 * w + (lane & 15);
-    const bool mine = lane < 16 && row < NB;
+    const int quad = lane & 3, row[2] = {16 * w + (lane >> 2), 16 * w + (lane >> 2) + 8};
+    const bool mine = 16 * w < NB;           // (NB is 16, 32 or 64)
     const uint32_t tl = tmem + (static_cast<uint32_t>(w * 32) << 16);
     const int kb0 = half == 0 ? 0 : (nk + 1) >> 1, kb1 = half == 0 ? (nk + 1) >> 1 : nk;   // this half's latent blocks
     int i = 0, seg_no = 0;
     Segment g{};
     while (walk.next(a, g)) {
-      int tok, head, see = mine ? 0 : 0x7FFFFFFF;
-      const bool on = group_row(a, g.rt, row, tok, head) && mine;
-      const int64_t at = static_cast<int64_t>(g.s) * a.q_len + tok;
-      if (on) see = max(0, min(g.len, g.len - a.q_len + 1 + tok));
+      int tok[2], head[2], see[2];
+      bool on[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        on[e] = group_row(a, g.rt, row[e], tok[e], head[e]) && mine;
+        see[e] = on[e] ? max(0, min(g.len, g.len - a.q_len + 1 + tok[e])) : 0;
+      }
       const bool whole = g.t0 == 0 && g.t1 == g.nt;
       if (g.len > 0) {
-        float m = 0.f, l = 0.f;
+        float m[2] = {0.f, 0.f}, l[2] = {0.f, 0.f};    // l: of the thread's own columns
         for (int t = g.t0; t < g.t1; ++t, ++i) {
           const bool first = t == g.t0;
-          uint32_t x[32];
+          uint32_t x[16];
           mbar_wait(&s_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, abort);
           __syncwarp();
           tc_fence_after();
-          tmem_ld_cols<32>(tl + kDecScol + static_cast<uint32_t>((i & 1) * 64 + half * 32), x);
+          tmem_ld_16x32(tl + kDecScol + static_cast<uint32_t>((i & 1) * 64 + half * 32), x);
           tmem_wait_ld_of(x);
           if (a.flip) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] ^= 0x80000000u;
+            for (int j = 0; j < 16; ++j) x[j] ^= 0x80000000u;
           }
           const int j0 = t * kTileTok + half * 32;
-          if (j0 + 32 > see) {
+          if (j0 + 32 > min(see[0], see[1])) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j0 + j >= see) x[j] = 0xFF800000u;
+            for (int j = 0; j < 16; ++j)
+              if (j0 + (j >> 2) * 8 + quad * 2 + (j & 1) >= see[(j >> 1) & 1]) x[j] = 0xFF800000u;
           }
-          float m4[4];
+          float mx[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) m4[e] = fmaxf(__uint_as_float(x[e]), __uint_as_float(x[4 + e]));
+          for (int e = 0; e < 2; ++e) {
+            const float a0 = fmaxf(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+            const float a1 = fmaxf(__uint_as_float(x[4 + 2 * e]), __uint_as_float(x[5 + 2 * e]));
+            mx[e] = fmaxf(max3(a0, __uint_as_float(x[8 + 2 * e]), __uint_as_float(x[9 + 2 * e])),
+                          max3(a1, __uint_as_float(x[12 + 2 * e]), __uint_as_float(x[13 + 2 * e])));
+          }
 #pragma unroll
-          for (int j = 8; j < 32; j += 8)
+          for (int o = 1; o < 4; o <<= 1)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) m4[e] = max3(m4[e], __uint_as_float(x[j + e]), __uint_as_float(x[j + 4 + e]));
-          const float mx = mine ? fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.c : -INFINITY;
-          if (first || named_sync_or(1, 256, mx - m > kMaxSlack)) {
-            if (mine) xch[half][row] = mx;
+            for (int e = 0; e < 2; ++e) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], o));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mx[e] *= a.c;
+          if (first || named_sync_or(1, 256, mine && fmaxf(mx[0] - m[0], mx[1] - m[1]) > kMaxSlack)) {
+            if (mine && quad == 0) {
+              xch[half][row[0]] = mx[0];
+              xch[half][row[1]] = mx[1];
+            }
             named_sync(1, 256);
             if (mine) {
-              float mn = fmaxf(mx, xch[half ^ 1][row]);
-              if (!first) mn = fmaxf(mn, m);
-              if (mn == -INFINITY) mn = 0.f;           // a row that sees nothing here sees nothing later
-              const float f = exp2_fast(m - mn);
-              if (half == 0) fac[row] = f;
-              l *= f;
-              m = mn;
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float mn = fmaxf(mx[e], xch[half ^ 1][row[e]]);
+                if (!first) mn = fmaxf(mn, m[e]);
+                if (mn == -INFINITY) mn = 0.f;         // a row that sees nothing here sees nothing later
+                const float f = exp2_fast(m[e] - mn);
+                if (half == 0 && quad == 0) fac[row[e]] = f;
+                l[e] = first ? 0.f : l[e] * f;         // (f may be infinite at first: m is no maximum yet)
+                m[e] = mn;
+              }
             }
             named_sync(1, 256);
             if (!first) {
@@ -581,49 +598,67 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             }
           }
           // weights (rounded to bf16 for the MMA) and their fp32 sum (unrounded)
-          uint32_t p[16];
-          const uint64_t c2 = pair2f(a.c, a.c), m2 = pair2f(-m, -m);
+          uint32_t p[8];                     // [columns 8 j ..][row]
+          const uint64_t c2 = pair2f(a.c, a.c);
           uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
+          for (int j = 0; j < 8; ++j) {
+            const int e = j & 1;
             float x0, x1;
-            split2(fma2(pair2(x[2 * j], x[2 * j + 1]), c2, m2), x0, x1);
+            split2(fma2(pair2(x[2 * j], x[2 * j + 1]), c2, pair2f(-m[e], -m[e])), x0, x1);
             x0 = exp2_fast(x0);
             x1 = exp2_fast(x1);
-            sum[j & 1] = add2(sum[j & 1], pair2f(x0, x1));
+            sum[e] = add2(sum[e], pair2f(x0, x1));
             p[j] = pack_bf16x2(x0, x1);
           }
-          float s0, s1;
-          split2(add2(sum[0], sum[1]), s0, s1);
-          l += s0 + s1;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float s0, s1;
+            split2(sum[e], s0, s1);
+            l[e] += s0 + s1;
+          }
           if (i > 0) {
             // the product before has read its weights
             mbar_wait(&pv_done, static_cast<uint32_t>(i - 1) & 1u, abort);
             __syncwarp();
           }
           if (mine) {
-            uint8_t* prow = psm + row * 128;
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-              *reinterpret_cast<uint4*>(prow + (((half * 4 + ch) ^ (row & 7)) << 4)) =
-                  make_uint4(p[4 * ch], p[4 * ch + 1], p[4 * ch + 2], p[4 * ch + 3]);
+            for (int j = 0; j < 8; ++j) {
+              const int r = row[j & 1];
+              *reinterpret_cast<uint32_t*>(psm + r * 128 + (((half * 4 + (j >> 1)) ^ (r & 7)) << 4) + quad * 4) = p[j];
+            }
           }
           fence_proxy_async_smem();
           tc_fence_before();
           mbar_arrive(&p_full[i & 1]);
         }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
+          l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
+        }
         named_sync(1, 256);                  // xch is free
-        if (mine) xch[half][row] = l;
+        if (mine && quad == 0) {
+          xch[half][row[0]] = l[0];
+          xch[half][row[1]] = l[1];
+        }
         named_sync(1, 256);
-        if (half == 0 && mine) {
-          const float sum = xch[0][row] + xch[1][row];
-          fin[seg_no % 3][row] = sum == 0.f ? 0.f : 1.0f / sum;
-          if (whole) {
-            if (a.lse != nullptr && on) a.lse[at * a.H + head] = sum == 0.f ? -INFINITY : (m + log2_fast(sum)) * kLn2;
-          } else if (on) {
-            float* part = part_of(a, NB, blockIdx.x, g.t0 == 0) + static_cast<int64_t>(NB) * a.L;
-            part[row] = sum == 0.f ? -INFINITY : m;
-            part[NB + row] = sum;
+        if (half == 0 && mine && quad == 0) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = row[e];
+            const float sum = xch[0][r] + xch[1][r];
+            fin[seg_no % 3][r] = sum == 0.f ? 0.f : 1.0f / sum;
+            if (whole) {
+              if (a.lse != nullptr && on[e])
+                a.lse[(static_cast<int64_t>(g.s) * a.q_len + tok[e]) * a.H + head[e]] =
+                    sum == 0.f ? -INFINITY : (m[e] + log2_fast(sum)) * kLn2;
+            } else if (on[e]) {
+              float* part = part_of(a, NB, blockIdx.x, g.t0 == 0) + static_cast<int64_t>(NB) * a.L;
+              part[r] = sum == 0.f ? -INFINITY : m[e];
+              part[NB + r] = sum;
+            }
           }
         }
         mbar_arrive(&fin_full[seg_no & 1]);
@@ -636,7 +671,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           __nv_bfloat16* dst = a.out + (static_cast<int64_t>(g.s) * a.q_len + tj) * a.o_tok + hj * a.o_head;
           for (int d = tid * 8; d < a.L; d += 256 * 8) *reinterpret_cast<uint4*>(dst + d) = make_uint4(0, 0, 0, 0);
         }
-        if (half == 0 && on && a.lse != nullptr) a.lse[at * a.H + head] = -INFINITY;
+        if (half == 0 && quad == 0 && a.lse != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (on[e]) a.lse[(static_cast<int64_t>(g.s) * a.q_len + tok[e]) * a.H + head[e]] = -INFINITY;
+        }
       }
     }
    }

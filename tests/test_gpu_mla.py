@@ -342,6 +342,29 @@ def test_prefill_rising_and_peaked_scores(capi):
         check_attention(out, lse, want, n, 256, f"scale {scale}")
 
 
+@pytest.mark.parametrize("shift", [-64.0, 64.0])
+def test_scores_far_from_zero(capi, shift):
+    # every score is about -+270 (beyond what 2^x holds), from one value of the
+    # rotated key: the sums are those of the rest
+    lens, H, page = [700, 40, 64], 8, 16
+    q_lat, q_rope = rnd(101, H, 3, L), rnd(102, 3, H, R)
+    cache, table = paged(103, lens, page)
+    q_rope[..., 0], cache[..., L] = 100.0, torch.where(cache[..., L].isnan(), cache[..., L], shift)
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    scale = 1 / 24
+    out, lse = run_decode(capi, q_lat, q_rope, cache, table, ln, 1, scale)
+    want = ref.decode(f64(q_lat), f64(q_rope), f64(cache), table.cpu().numpy(), lens, 1, scale)
+    check_attention(out, lse, want, 700, L + R, f"decode, shift {shift}")
+    n = 300
+    q, kv, kr = rnd(104, n, H, 192 + R), rnd(105, n, H, 192 + 256), rnd(106, n, R)
+    q[..., 192], kr[:, 0] = 100.0, shift
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    args = (q[..., :192], q[..., 192:], kv[..., :192], kr, kv[..., 192:])
+    out, lse = run_prefill(capi, *args, cu, cu, scale, True)
+    want = ref.prefill(*(f64(t) for t in args), [0, n], [0, n], scale, True)
+    check_attention(out, lse, want, n, 256, f"prefill, shift {shift}")
+
+
 def test_prefill_ignores_what_lies_past_a_sequence(capi):
     # the rows after each sequence's keys are another's, or NaN
     H, n = 2, 150
