@@ -638,17 +638,19 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
           l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
         }
-        named_sync(1, 256);                  // xch is free
-        if (mine && quad == 0) {
-          xch[half][row[0]] = l[0];
-          xch[half][row[1]] = l[1];
+        // the halves' sums meet in fac: the next stretch writes xch before any
+        // barrier, but fac only behind one
+        named_sync(1, 256);                  // fac is free
+        if (half == 1 && mine && quad == 0) {
+          fac[row[0]] = l[0];
+          fac[row[1]] = l[1];
         }
         named_sync(1, 256);
         if (half == 0 && mine && quad == 0) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int r = row[e];
-            const float sum = xch[0][r] + xch[1][r];
+            const float sum = l[e] + fac[r];
             fin[seg_no % 3][r] = sum == 0.f ? 0.f : 1.0f / sum;
             if (whole) {
               if (a.lse != nullptr && on[e])

@@ -162,6 +162,11 @@ def test_decode_many_short_sequences(capi, lat):
     decode_case(capi, [int(v) for v in g.integers(0, 200, 700)], 16, 1, 64, lat=lat, seed=lat)
 
 
+def test_decode_many_row_groups(capi):
+    # 24 row groups a sequence: dozens of tiles for every block, cut in the middle
+    decode_case(capi, [1000, 0, 900, 64, 1, 1111, 777, 1024], 192, 8, 64, lat=128, seed=4)
+
+
 def test_decode_rising_and_peaked_scores(capi):
     # scores that keep passing the running maximum, far outside the slack, and
     # weights of one position alone
