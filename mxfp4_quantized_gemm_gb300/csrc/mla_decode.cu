@@ -87,9 +87,15 @@ __device__ __forceinline__ int seq_len(const DecodeArgs& a, int s) { return cut_
 // Work units of one row group: `over` for going over to it (queries to fetch, a
 // part or the rows before it to write out), then its tiles; or one for an empty
 // sequence (whose rows still have to be written).
-__device__ __forceinline__ int group_units(const DecodeArgs& a, int len) {
-  return len == 0 ? 1 : a.over + (len + kTileTok - 1) / kTileTok;
+__device__ __forceinline__ int group_units(int over, int len) {
+  return len == 0 ? 1 : over + (len + kTileTok - 1) / kTileTok;
 }
+// Going over counts as three tiles where the blocks have 24 units and more of it
+// counted as one, else as one: see decode_over.
+__device__ __forceinline__ bool long_stretches(const DecodeArgs& a, int64_t units, int grid) {
+  return a.over > 0 && units * a.RT >= 24 * static_cast<int64_t>(grid);
+}
+constexpr int kLongOver = 3;
 
 // total / n and the like, in 32 bits where they fit (a 64-bit division takes
 // several times as long, and this is on the way to the first load).
@@ -122,6 +128,7 @@ struct Segment {
 struct Walk {
   int64_t left;       // units still to hand out
   int s, rt, off;
+  int over;           // units of going over to a row group
   int own[2];         // up to 64 sequences: the lengths of the lane's
   static constexpr int kOwn = 64;
   // (from L2: it may be read before the kernels ahead are done, and again then)
@@ -142,19 +149,28 @@ struct Walk {
   __device__ __forceinline__ void start(const DecodeArgs& a) {
     const int lane = threadIdx.x & 31;
     const int per = (a.S + 31) >> 5, s0 = min(a.S, lane * per), s1 = min(a.S, s0 + per);
-    int64_t mine = 0;
-    if (a.S <= kOwn) {
-      if (s0 < s1) mine = group_units(a, own[0]);
-      if (s0 + 1 < s1) mine += group_units(a, own[1]);
-    } else {
+    int64_t mine = 0, incl = 0;
+    auto count = [&]() {
+      mine = 0;
+      if (a.S <= kOwn) {
+        if (s0 < s1) mine = group_units(over, own[0]);
+        if (s0 + 1 < s1) mine += group_units(over, own[1]);
+      } else {
 #pragma unroll 4
-      for (int i = s0; i < s1; ++i) mine += group_units(a, seq_len(a, i));
-    }
-    int64_t incl = mine;
+        for (int i = s0; i < s1; ++i) mine += group_units(over, seq_len(a, i));
+      }
+      incl = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += v;
+      }
+    };
+    over = a.over;
+    count();
+    if (long_stretches(a, __shfl_sync(0xFFFFFFFFu, incl, 31), static_cast<int>(gridDim.x))) {
+      over = kLongOver;
+      count();
     }
     int n;
     const Cut cut(__shfl_sync(0xFFFFFFFFu, incl, 31) * a.RT, static_cast<int>(gridDim.x), n);
@@ -168,7 +184,7 @@ struct Walk {
     const bool here = ub >= at && ub < incl * a.RT;
     if (here) {
       for (s = s0; s < s1; ++s) {
-        const int g = group_units(a, a.S <= kOwn ? (s == s0 ? own[0] : own[1]) : seq_len(a, s));
+        const int g = group_units(over, a.S <= kOwn ? (s == s0 ? own[0] : own[1]) : seq_len(a, s));
         const int64_t u = static_cast<int64_t>(g) * a.RT;
         if (ub < at + u) {
           rt = static_cast<int>(div64(ub - at, g));
@@ -188,14 +204,14 @@ struct Walk {
       g.s = s;
       g.rt = rt;
       g.len = len_of(a, s);
-      const int units = group_units(a, g.len), from = off;
-      g.nt = g.len == 0 ? 0 : units - a.over;
+      const int units = group_units(over, g.len), from = off;
+      g.nt = g.len == 0 ? 0 : units - over;
       const int64_t room = units - off;
       const int take = static_cast<int>(left < room ? left : room);
       left -= take;
       off += take;
-      g.t0 = max(0, from - a.over);
-      g.t1 = min(g.nt, max(0, off - a.over));
+      g.t0 = max(0, from - over);
+      g.t1 = min(g.nt, max(0, off - over));
       if (off == units) {
         off = 0;
         if (++rt == a.RT) {
@@ -203,7 +219,7 @@ struct Walk {
           ++s;
         }
         // nothing but going over to the next group: left to the block behind
-        if (left > 0 && left <= a.over && len_of(a, s) > 0) left = 0;
+        if (left > 0 && left <= over && len_of(a, s) > 0) left = 0;
       }
       if (g.len == 0 || g.t0 < g.t1) return true;
     }
@@ -779,31 +795,41 @@ __global__ void __launch_bounds__(kCombWarps * 32, 3) mla_combine_kernel(const D
   // units before this sequence and of all (seq_lens: complete before the
   // kernel ahead let this one start)
   int64_t before = 0, total = 0;
-  for (int i = threadIdx.x; i < a.S; i += kCombWarps * 32) {
-    const int64_t u = group_units(a, seq_len(a, i));
-    total += u;
-    if (i < s) before += u;
-  }
+  int over = a.over;
+  auto count = [&]() {
+    before = total = 0;
+    for (int i = threadIdx.x; i < a.S; i += kCombWarps * 32) {
+      const int64_t u = group_units(over, seq_len(a, i));
+      total += u;
+      if (i < s) before += u;
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
-    total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+      total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+    }
+    if (lane == 0) {
+      sums[0][warp] = before;
+      sums[1][warp] = total;
+    }
+    __syncthreads();
+    before = total = 0;
+    for (int w = 0; w < kCombWarps; ++w) {
+      before += sums[0][w];
+      total += sums[1][w];
+    }
+  };
+  count();
+  if (long_stretches(a, total, grid)) {      // (the whole block)
+    over = kLongOver;
+    __syncthreads();                         // the sums have been read
+    count();
   }
-  if (lane == 0) {
-    sums[0][warp] = before;
-    sums[1][warp] = total;
-  }
-  __syncthreads();
-  before = total = 0;
-  for (int w = 0; w < kCombWarps; ++w) {
-    before += sums[0][w];
-    total += sums[1][w];
-  }
-  const int units = group_units(a, seq_len(a, s));
+  const int units = group_units(over, seq_len(a, s));
   const int64_t u0 = before * a.RT + static_cast<int64_t>(rt) * units;
   int n;
   const Cut cut(total * a.RT, grid, n);
-  const int c0 = cut.owner(u0 + min(units - 1, a.over)), c1 = cut.owner(u0 + units - 1);   // of the first and the last tile
+  const int c0 = cut.owner(u0 + min(units - 1, over)), c1 = cut.owner(u0 + units - 1);   // of the first and the last tile
   griddep_wait();                            // (every block: the grid must not end before the one ahead)
   if (c0 == c1) return;                      // not cut: written by its block
   const int nk = a.L / (128 * V), per = kCombWarps / warps;   // units a block takes at a time
@@ -917,10 +943,13 @@ static RowSplit split_rows(int q_len, int H) {
   return r;
 }
 
-// Going over to another row group is counted as one tile where 64 rows have to
-// be written out for it (24 ragged sequences of up to 6000, 128 rows: 53.4 -> 50.2
-// us; 59 of up to 221, 128 rows: 33.8 -> 29.5), and as nothing for fewer (65 of
-// up to 426, 32 rows: 16.7 us, 18.2 with it).
+// Going over to another row group is counted as a tile where 64 rows have to be
+// written out for it, and as three in long stretches, where many blocks go over
+// in the middle of their work (counted as 0, 1, 3, ragged lengths, 64 or 128
+// rows: 13 sequences up to 4052 22.1, 20.6, 20.7 us; 59 up to 1647 55.4, 53.0,
+// 51.7; 30 up to 2450, ten tiles a block, 35.2, 33.6, 34.9; 29 up to 8201, 15 tiles
+// a block, 48.7, 47.0, 47.4; 100 up to 4190, 28 tiles a block, 86.2, 84.7, 79.4).  For fewer rows it is nothing (65 up to 426,
+// 32 rows: 16.7, 18.2, 19.2).
 static int decode_over(int NB) { return NB == 64 ? 1 : 0; }
 
 static int decode_grid(int S, const RowSplit& r, int64_t capacity, int sm_count) {
