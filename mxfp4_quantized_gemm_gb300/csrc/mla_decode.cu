@@ -149,8 +149,10 @@ struct Walk {
   __device__ __forceinline__ void start(const DecodeArgs& a) {
     const int lane = threadIdx.x & 31;
     const int per = (a.S + 31) >> 5, s0 = min(a.S, lane * per), s1 = min(a.S, s0 + per);
-    int64_t mine = 0, incl = 0;
-    auto count = [&]() {
+    int64_t mine, incl;
+    over = a.over;
+#pragma unroll 1
+    for (;;) {                               // (once, or twice in long stretches)
       mine = 0;
       if (a.S <= kOwn) {
         if (s0 < s1) mine = group_units(over, own[0]);
@@ -165,12 +167,8 @@ struct Walk {
         const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += v;
       }
-    };
-    over = a.over;
-    count();
-    if (long_stretches(a, __shfl_sync(0xFFFFFFFFu, incl, 31), static_cast<int>(gridDim.x))) {
+      if (over == kLongOver || !long_stretches(a, __shfl_sync(0xFFFFFFFFu, incl, 31), static_cast<int>(gridDim.x))) break;
       over = kLongOver;
-      count();
     }
     int n;
     const Cut cut(__shfl_sync(0xFFFFFFFFu, incl, 31) * a.RT, static_cast<int>(gridDim.x), n);
@@ -796,7 +794,8 @@ __global__ void __launch_bounds__(kCombWarps * 32, 3) mla_combine_kernel(const D
   // kernel ahead let this one start)
   int64_t before = 0, total = 0;
   int over = a.over;
-  auto count = [&]() {
+#pragma unroll 1
+  for (;;) {                                 // (as the blocks ahead: once or twice)
     before = total = 0;
     for (int i = threadIdx.x; i < a.S; i += kCombWarps * 32) {
       const int64_t u = group_units(over, seq_len(a, i));
@@ -818,12 +817,9 @@ __global__ void __launch_bounds__(kCombWarps * 32, 3) mla_combine_kernel(const D
       before += sums[0][w];
       total += sums[1][w];
     }
-  };
-  count();
-  if (long_stretches(a, total, grid)) {      // (the whole block)
+    if (over == kLongOver || !long_stretches(a, total, grid)) break;
     over = kLongOver;
     __syncthreads();                         // the sums have been read
-    count();
   }
   const int units = group_units(over, seq_len(a, s));
   const int64_t u0 = before * a.RT + static_cast<int64_t>(rt) * units;
