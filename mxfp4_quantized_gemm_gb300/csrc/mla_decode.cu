@@ -20,12 +20,18 @@
 // the second (along M).
 //
 // Roles: warp 0 copies, warp 1 issues the score products, warp 2 the output
-// products; warps 4..7 and 8..11 hold the softmax: thread = (row, half of the
-// tile's positions), in the lanes where a 64-row MMA leaves its rows (16 of
-// each 32); warps 12..15 write a finished accumulator out while the softmax
-// is at the next stretch (131 KB of fp32 for a part: done by the softmax warps
-// it stood for 17000 cycles between two stretches, four tiles' worth).  A row's running maximum is raised only when a score passes it by
-// 2^8 (first tile aside), which one barrier with an OR decides.
+// products; warps 4..7 and 8..11 hold the softmax of a half of the tile's
+// positions each; warps 12..15 write a finished accumulator out while the
+// softmax is at the next stretch (131 KB of fp32 for a part: done by the softmax
+// warps it stood for 17000 cycles between two stretches, four tiles' worth).  A
+// row's running maximum is raised only when a score passes it by 2^8 (first
+// tile aside), which one barrier with an OR decides.
+//
+// Where a tile's time goes (64 sequences of 4096, cycles of 4100 a tile): its
+// place is free again about 8000 cycles after it was asked for, two at a time:
+// 3200 to 3700 until it lands from HBM, 1600 of score products, 1000 of softmax,
+// 1300 of output products.  Shared memory alone needs 2500 (operands and copies
+// at 128 bytes a cycle).  A third tile does not fit beside the queries.
 // A copying warp spends about 430 cycles on each wait, arrival and copy, and
 // each copy more costs it 16 by one thread and about 100 by lanes in turns.  Where
 // a page holds whole tiles a group of chunks is one copy, and a tile comes in
@@ -40,6 +46,11 @@
 // single long sequence spreads over all SMs.  A row group cut between blocks
 // leaves unnormalized parts (fp32, with maximum and sum) that
 // mla_combine_kernel joins.
+//
+// Measured (HBM share by the bytes of the cache read once): 64 ragged sequences
+// of up to 8192, 64 rows: 80.5 us, 4.4 TB/s; one of 131072: 42.7 us, 3.5 TB/s; 16 of
+// up to 4096: 24.7 us, of which 2 to the first copy, 12 of tiles, 2 to write the
+// parts out and 6 to join them.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <atomic>
@@ -780,6 +791,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 // shared memory; a block of 8 warps takes 8 / warps units.  Bound by latency
 // (the lengths, then the parts, from L2), so a call should fit the card at
 // once: whole rows to a warp where there are many, and eight loads in flight.
+// The 20 MB of parts of 152 blocks take 2 to 5 us; four rows of a value to a
+// store and a lane (512 contiguous bytes) took as long.
 constexpr int kCombWarps = 8;
 
 template <int V>
@@ -948,16 +961,20 @@ static RowSplit split_rows(int q_len, int H) {
 // 32 rows: 16.7, 18.2, 19.2).
 static int decode_over(int NB) { return NB == 64 ? 1 : 0; }
 
-static int decode_grid(int S, const RowSplit& r, int64_t capacity, int sm_count) {
-  const int64_t most = static_cast<int64_t>(S) * r.RT * (decode_over(r.NB) + ceil_div(capacity > 0 ? capacity : 1, kTileTok));
+// Blocks of a call, and what going over counts as (nothing where each tile has a
+// block of its own).
+static int decode_grid(int S, const RowSplit& r, int64_t capacity, int sm_count, int* over) {
+  const int64_t most = static_cast<int64_t>(S) * r.RT * ceil_div(capacity > 0 ? capacity : 1, kTileTok);
   const int lim = sm_count < kMaxCtas ? sm_count : kMaxCtas;
+  *over = most > lim ? decode_over(r.NB) : 0;
   return static_cast<int>(most < lim ? most : lim);
 }
 
 size_t mla_decode_workspace(int S, int q_len, int H, int L, int64_t max_len, int sm_count) {
   if (max_len <= kTileTok) return 0;         // one tile a sequence: nothing is cut
   const RowSplit r = split_rows(q_len, H);
-  return static_cast<size_t>(decode_grid(S, r, max_len, sm_count)) * 2 * part_floats(r.NB, L) * sizeof(float);
+  int over;
+  return static_cast<size_t>(decode_grid(S, r, max_len, sm_count, &over)) * 2 * part_floats(r.NB, L) * sizeof(float);
 }
 
 bool mla_decode_fits(int S, int q_len, int H) {
@@ -1019,7 +1036,6 @@ cudaError_t launch_mla_decode(const MlaDecodeProblem& p, const DeviceInfo& dev, 
   a.TPT = r.TPT;
   a.head_blocks = r.head_blocks;
   a.RT = r.RT;
-  a.over = decode_over(r.NB);
   a.flip = p.scale < 0.f;
   a.c = positive_scale(a.flip ? -p.scale : p.scale);
 
@@ -1044,7 +1060,7 @@ cudaError_t launch_mla_decode(const MlaDecodeProblem& p, const DeviceInfo& dev, 
                                    p.cache.page_stride, box, a.box_rows, 1)) != cudaSuccess)
       return e;
   }
-  const int grid = decode_grid(p.S, r, a.capacity, dev.sm_count);
+  const int grid = decode_grid(p.S, r, a.capacity, dev.sm_count, &a.over);
   e = r.NB == 16 ? launch_decode_nb<16>(maps, a, grid, dev, s)
                  : (r.NB == 32 ? launch_decode_nb<32>(maps, a, grid, dev, s)
                                : launch_decode_nb<64>(maps, a, grid, dev, s));

@@ -43,10 +43,14 @@
 // The grid is one block (or pair) per SM (pair of SMs) that walks query tiles:
 // the next tile's copies and first scores run while the softmax warps write the
 // last one out.  (A block per tile spent 14000 cycles on each, the time of six
-// key tiles, before its first and after its last product.)  Tiles are ordered
-// head by head and, within a head, from the last queries (most keys) to the
-// first, and dealt in rounds that change direction: blocks that run together
-// share a head's keys and values in L2, and their loads even out.
+// key tiles, before its first and after its last product.)  How they are dealt
+// out: QueryTiles.
+//
+// Measured (dn + R = dv = 256, 64 heads): 8192 tokens 1326 us, 1.66 PFLOP/s, the
+// rate that the card's power limit leaves a long run of matrix products; six
+// ragged prompts of 156 to 781 tokens on up to 1000 others 153 us: of a query
+// tile's 10 us, 7 key tiles at 1.16 us, then 1.7 until the last product is done
+// and 1.7 to write it out, during which the next tile's scores are formed.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <atomic>
