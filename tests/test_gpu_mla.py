@@ -162,6 +162,33 @@ def test_decode_many_short_sequences(capi, lat):
     decode_case(capi, [int(v) for v in g.integers(0, 200, 700)], 16, 1, 64, lat=lat, seed=lat)
 
 
+@pytest.mark.parametrize("S", [31, 32, 33, 50, 63, 64, 65])
+def test_decode_sequences_per_lane(capi, S):
+    # lengths of one, two and more sequences to a lane, empty ones among them
+    g = np.random.default_rng(S)
+    decode_case(capi, [int(v) * int(v % 7 > 0) for v in g.integers(0, 400, S)], 64, 1, 64, lat=128, seed=S)
+
+
+def test_decode_lengths_written_just_before(capi):
+    # each call's lengths differ from the last call's and are written on the
+    # device right before it, with another of the library's kernels between
+    H, page, lat = 16, 64, 128
+    full = [640] * 5
+    q_lat, q_rope = rnd(131, H, 5, lat), rnd(132, 5, H, R)
+    cache, table = paged(133, full, page, lat, R)
+    lens = [[640, 3, 0, 129, 64], [1, 640, 500, 0, 65], [640] * 5, [0, 0, 63, 1, 0], [333, 222, 111, 55, 27]] * 3
+    on_device = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ln = torch.zeros(5, dtype=torch.int32, device="cuda")
+    got = []
+    for i in range(len(lens)):
+        ln.copy_(on_device[i])
+        got.append(run_decode(capi, q_lat, q_rope, cache, table, ln, 1, 0.07))
+        run_decode(capi, q_lat, q_rope, cache, table, ln, 1, 0.07)
+    for n, (out, lse) in zip(lens, got):
+        want = ref.decode(f64(q_lat), f64(q_rope), f64(cache), table.cpu().numpy(), n, 1, 0.07)
+        check_attention(out, lse, want, max(n), lat + R, f"lens {n}")
+
+
 def test_decode_many_row_groups(capi):
     # 24 row groups a sequence: dozens of tiles for every block, cut in the middle
     decode_case(capi, [1000, 0, 900, 64, 1, 1111, 777, 1024], 192, 8, 64, lat=128, seed=4)
