@@ -189,6 +189,48 @@ def test_decode_lengths_written_just_before(capi):
         check_attention(out, lse, want, max(n), lat + R, f"lens {n}")
 
 
+@pytest.mark.parametrize("S", [4, 40])
+def test_decode_lengths_written_by_the_kernel_ahead(capi, S):
+    # the store kernel lets the next kernel start before it writes; here what it
+    # writes (a rotated query: 1.0 pairs are a length beyond the table, -1.0
+    # pairs a negative one) is the lengths, others in each call
+    H, page, lat, cap = 8, 64, 128, 256
+    q_lat, q_rope = rnd(141, H, S, lat), rnd(142, S, H, R)
+    cache, table = paged(143, [cap] * S, page, lat, R)
+    kv, gamma = rnd(144, 1, lat + R), rnd(145, lat)
+    cos_sin = torch.cat((torch.ones(1, R // 2), torch.zeros(1, R // 2)), 1).cuda()
+    pos, no_slot = torch.zeros(1, dtype=torch.int64, device="cuda"), torch.full((1,), -1, dtype=torch.int64, device="cuda")
+    g = np.random.default_rng(S)
+    masks = [g.integers(0, 2, 2 * R // 2) for _ in range(12)]
+    qs = [torch.from_numpy(np.where(np.repeat(m, 2), 1.0, -1.0)).to(BF).reshape(1, 2, R).cuda() for m in masks]
+    q_out = torch.zeros(1, 2, R, dtype=BF, device="cuda")
+    lens = q_out.view(torch.int32).reshape(-1)[:S]
+    ws = torch.empty(capi.mxfp4_mla_decode_workspace_bytes(S, 1, H, lat, cap), dtype=torch.uint8, device="cuda")
+    got = [(torch.empty(H, S, lat, dtype=BF, device="cuda"), torch.empty(S, H, device="cuda")) for _ in qs]
+
+    def calls():
+        for q, (out, lse) in zip(qs, got):
+            run_store(capi, kv, gamma, 1e-6, q, q_out, cos_sin, pos, no_slot, cache, lat, True)
+            capi.mxfp4_mla_decode(q_lat, q_lat.stride(1), q_lat.stride(0), q_rope, q_rope.stride(0), q_rope.stride(1),
+                                  cache, cache.stride(0), page, cache.shape[0], table, table.stride(0), table.shape[1],
+                                  lens, out, out.stride(1), out.stride(0), lse, S, 1, H, lat, R, 0.07, ws, ws.numel(),
+                                  None)
+
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()              # (one call right behind the other)
+    with torch.cuda.graph(graph):
+        calls()
+    for out, lse in got:
+        out.fill_(float("nan"))
+    graph.replay()
+    torch.cuda.synchronize()
+    for m, (out, lse) in zip(masks, got):
+        n = [cap * int(v) for v in m[:S]]
+        want = ref.decode(f64(q_lat), f64(q_rope), f64(cache), table.cpu().numpy(), n, 1, 0.07)
+        check_attention(out, lse, want, cap, lat + R, f"lens {n}")
+
+
 def test_decode_many_row_groups(capi):
     # 24 row groups a sequence: dozens of tiles for every block, cut in the middle
     decode_case(capi, [1000, 0, 900, 64, 1, 1111, 777, 1024], 192, 8, 64, lat=128, seed=4)
