@@ -26,19 +26,72 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // A bounded mbarrier wait by a whole converged warp, whose lanes go on (or
-// give up) together.  Also where another CTA of the cluster arrives: what its
-// arrival announces (copies, MMAs, TMEM) is read by the tensor core, and an
-// acquire at cluster scope takes 2000 cycles where this thread has stores under way.
+// give up) together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, bool& abort) {
   mbar_wait(bar, parity, abort);
   abort = __any_sync(0xFFFFFFFFu, abort);
   return !abort;
 }
+// The same for a barrier on which, in a pair of CTAs, the peer's copies,
+// threads or MMAs arrive as well: acquiring at the scope of both.
+template <bool kPair>
+__device__ __forceinline__ bool warp_wait_of(uint64_t* bar, uint32_t parity, bool& abort) {
+  if (kPair)
+    mbar_wait_cluster(bar, parity, abort);
+  else
+    mbar_wait(bar, parity, abort);
+  abort = __any_sync(0xFFFFFFFFu, abort);
+  return !abort;
+}
 
-// One arrival on the barrier at the same offset in the CTA of rank `rank`,
-// ordering this thread's own operations before it.
-__device__ __forceinline__ void mbar_arrive_remote(uint64_t* bar, uint32_t rank) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), rank))
+// The bounded wait of a thread that goes on with TMEM alone, which its
+// tcgen05.fence::after_thread_sync orders behind the wait: in a pair relaxed at
+// cluster scope, the form that PTX gives for tcgen05 operations handed from
+// thread to thread.  (An acquire at that scope would order ordinary memory too,
+// and takes 2000 cycles where the thread has stores under way.)
+__device__ __forceinline__ bool mbar_try_wait_relaxed_cluster(uint32_t bar_addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar_addr), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+template <bool kPair>
+__device__ __forceinline__ bool mbar_wait_tmem_of(uint64_t* bar, uint32_t parity, bool& abort) {
+  if (!kPair) return mbar_wait(bar, parity, abort);
+  if (abort) return false;
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait_relaxed_cluster(a, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait_relaxed_cluster(a, parity)) {
+    if (clock64() - t0 > kWaitCycles) {
+      abort = true;
+      return false;
+    }
+  }
+  return true;
+}
+template <bool kPair>
+__device__ __forceinline__ bool warp_wait_tmem_of(uint64_t* bar, uint32_t parity, bool& abort) {
+  mbar_wait_tmem_of<kPair>(bar, parity, abort);
+  abort = __any_sync(0xFFFFFFFFu, abort);
+  return !abort;
+}
+
+// One arrival on a barrier of another CTA (address from mapa_shared), ordering
+// this thread's own operations before it.
+__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// One arrival there that also announces bytes of this thread's copies to come
+// (relaxed: the copies' own completion orders what they write).
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cluster_addr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
+               "r"(bytes)
                : "memory");
 }
 
@@ -130,7 +183,18 @@ __device__ __forceinline__ void tma_box_3d(void* smem_dst, const CUtensorMap* ma
       : "memory");
 }
 
-// The same of a 4-D tensor map.
+// The same, completion counted on a barrier of either CTA of a pair (address
+// from mapa_shared).
+__device__ __forceinline__ void tma_box_3d_pair(void* smem_dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                                uint32_t cluster_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+      "%3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(cluster_bar)
+      : "memory");
+}
+
+// One box of a 4-D tensor map.
 __device__ __forceinline__ void tma_box_4d(void* smem_dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
                                            uint64_t* bar) {
   asm volatile(

@@ -23,9 +23,9 @@
 // half of the values (columns), and its copies halve too.
 //
 // Roles: warp 0 copies keys and warp 3 values, each through a ring of 32 KB
-// slots of its own; warp 1 issues every product (in rank 0 of a pair; in rank
-// 1 warps 1 and 2 pass on to rank 0 that their keys and values have landed);
-// warps 4..7 and 8..11 hold the softmax, thread = (query, half of the tile's
+// slots of its own; warp 1 issues every product (in rank 0 of a pair, whose
+// barriers count the copies of both blocks; warp 2 of rank 1 clears the rest of
+// value tiles that end a sequence, and only then lets rank 0 have them); warps 4..7 and 8..11 hold the softmax, thread = (query, half of the tile's
 // keys).  Each query's running maximum is raised only when a score passes it
 // by 2^8, decided per 32 queries by a barrier with an OR over the two warps
 // that hold them.
@@ -276,14 +276,13 @@ struct QueryTiles {
 
 // Keys of a value slot that no query of the tile sees may hold anything (0 x
 // NaN): their weights are 0 and they are made 0 too, by one warp.  `valid`: the
-// slot's keys that count.  True if there were any to clear.
+// slot's keys that count.
 template <int kRows>
-__device__ __forceinline__ bool clear_values(uint8_t* slot, int nv, int valid, int lane) {
-  if (valid >= kRows) return false;
+__device__ __forceinline__ void clear_values(uint8_t* slot, int nv, int valid, int lane) {
+  if (valid >= kRows) return;
   for (int k = 0; k < nv; ++k) zero_rows(slot + k * kRows * 128, valid, kRows, lane);
   fence_proxy_async_smem();
   __syncwarp();
-  return true;
 }
 
 template <bool kPair>
@@ -311,8 +310,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   const bool leader = rank == 0;
   bool abort = false;
   if (threadIdx.x == 0) {
-    // rank 0's full barriers also count rank 1: one arrival for its copies, one
-    // per softmax warp for its weights
+    // rank 0's full barriers also count rank 1: its copies (one arrival, and
+    // their bytes), and its weights (one arrival per softmax thread)
     const uint32_t both = kPair && leader ? 2 : 1;
     for (int s = 0; s < kPreMaxSlots; ++s) {
       mbar_init(&kfull[s], both);
@@ -324,7 +323,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     mbar_init(&q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kPair ? 256 + 8 : 256);
+      mbar_init(&p_full[i], kPair ? 512 : 256);
       mbar_init(&pv_done[i], 1);
     }
     mbar_init(&drained, 1);
@@ -350,6 +349,22 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   if (threadIdx.x == 0) griddep_launch_dependents();
   QueryTiles<kPair> walk(a, static_cast<int>(rank), list);
   QueryTile x;
+  // Copies of a pair are counted on rank 0's barriers, where the products that
+  // read both blocks' shared memory are issued.  (Barriers of rank 1's own with
+  // warps that pass their phases on would hand the copies over by threads that
+  // neither wrote nor read them, a hop later.)
+  auto expect = [&](uint64_t* bar, int bytes) {
+    if (kPair)
+      mbar_arrive_expect_tx_cluster(mapa_shared(smem_u32(bar), 0), static_cast<uint32_t>(bytes));
+    else
+      mbar_arrive_expect_tx(bar, static_cast<uint32_t>(bytes));
+  };
+  auto copy = [&](void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+    if (kPair)
+      tma_box_3d_pair(dst, map, c0, c1, c2, mapa_shared(smem_u32(bar), 0));
+    else
+      tma_box_3d(dst, map, c0, c1, c2, bar);
+  };
 
   if (warp == 0) {
     // ---- queries and keys
@@ -360,28 +375,28 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       // formed.  (A barrier of its own, with one phase a query tile: a parity
       // says nothing about a barrier that may be two phases behind, as s_full
       // is to a warp that does not wait for each of its phases.)
-      if (no > 0 && !warp_wait(&q_empty, static_cast<uint32_t>(no - 1) & 1u, abort)) break;
+      if (no > 0 && !warp_wait_of<kPair>(&q_empty, static_cast<uint32_t>(no - 1) & 1u, abort)) break;
       if (elect_one()) {
-        mbar_arrive_expect_tx(&q_full, static_cast<uint32_t>(a.nq * kPreChunk));
+        expect(&q_full, a.nq * kPreChunk);
         for (int k = 0; k + 1 < a.nq; ++k)
-          tma_box_3d(qsm + k * kPreChunk, &qn_map, k * 64, x.h, x.ex.q0 + x.qi0, &q_full);
-        tma_box_3d(qsm + (a.nq - 1) * kPreChunk, &qr_map, 0, x.h, x.ex.q0 + x.qi0, &q_full);
+          copy(qsm + k * kPreChunk, &qn_map, k * 64, x.h, x.ex.q0 + x.qi0, &q_full);
+        copy(qsm + (a.nq - 1) * kPreChunk, &qr_map, 0, x.h, x.ex.q0 + x.qi0, &q_full);
       }
       __syncwarp();
       ++no;
       for (int t = 0; t < x.tiles && !abort; ++t) {
         const int tok = x.ex.k0 + t * kPreTile + static_cast<int>(rank) * Shape::kKeyRows;
         for (int k = 0; k < a.nq; k += Shape::kKeyChunks) {
-          if (!warp_wait(&kempty[r.slot], r.turn ^ 1u, abort)) break;
+          if (!warp_wait_of<kPair>(&kempty[r.slot], r.turn ^ 1u, abort)) break;
           if (elect_one()) {
             const int n = min(Shape::kKeyChunks, a.nq - k);     // chunks of this slot
             uint8_t* dst = kring + r.slot * kSlotBytes;
-            mbar_arrive_expect_tx(&kfull[r.slot], static_cast<uint32_t>(n * Shape::kKeyChunkBytes));
+            expect(&kfull[r.slot], n * Shape::kKeyChunkBytes);
             for (int y = 0; y < n; ++y) {
               if (k + y + 1 < a.nq)
-                tma_box_3d(dst + y * Shape::kKeyChunkBytes, &kn_map, (k + y) * 64, x.h, tok, &kfull[r.slot]);
+                copy(dst + y * Shape::kKeyChunkBytes, &kn_map, (k + y) * 64, x.h, tok, &kfull[r.slot]);
               else
-                tma_box_3d(dst + y * Shape::kKeyChunkBytes, &kr_map, 0, 0, tok, &kfull[r.slot]);
+                copy(dst + y * Shape::kKeyChunkBytes, &kr_map, 0, 0, tok, &kfull[r.slot]);
             }
           }
           __syncwarp();
@@ -390,9 +405,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
       }
     }
-    if (abort) {
+    if (abort && leader) {
       // give the copies in flight a bounded time to land (rank 0's barriers may
-      // wait for rank 1 as well: bounded all the same)
+      // wait for rank 1 as well: bounded all the same; rank 1's copies, which
+      // are counted there, are older than the wait that gave up here, as all
+      // of a warp's are)
       drain_copies(kfull, fills, r.n);
       bool late = false;
       if (no > 0) mbar_wait(&q_full, static_cast<uint32_t>(no - 1) & 1u, late);
@@ -406,12 +423,20 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     while (!abort && walk.next_real(a, x)) {
       for (int t = 0; t < x.tiles && !abort; ++t) {
         for (int tok = t * kPreTile; tok < min((t + 1) * kPreTile, x.see1); tok += Shape::kValRows) {
-          if (!warp_wait(&vempty[r.slot], r.turn ^ 1u, abort)) break;
+          if (!warp_wait_of<kPair>(&vempty[r.slot], r.turn ^ 1u, abort)) break;
           if (elect_one()) {
-            mbar_arrive_expect_tx(&vfull[r.slot], static_cast<uint32_t>(nv * Shape::kValBlockBytes));
-            for (int k = 0; k < nv; ++k)
-              tma_box_3d(vring + r.slot * kSlotBytes + k * Shape::kValBlockBytes, &v_map, v0 + k * 64, x.h,
-                         x.ex.k0 + tok, &vfull[r.slot]);
+            const int bytes = nv * Shape::kValBlockBytes;
+            uint8_t* dst = vring + r.slot * kSlotBytes;
+            if (kPair && !leader && tok + kPreTile > x.see1) {
+              // (to be cleared first: counted here, and passed on by warp 2)
+              mbar_arrive_expect_tx(&vfull[r.slot], static_cast<uint32_t>(bytes));
+              for (int k = 0; k < nv; ++k)
+                tma_box_3d(dst + k * Shape::kValBlockBytes, &v_map, v0 + k * 64, x.h, x.ex.k0 + tok, &vfull[r.slot]);
+            } else {
+              expect(&vfull[r.slot], bytes);
+              for (int k = 0; k < nv; ++k)
+                copy(dst + k * Shape::kValBlockBytes, &v_map, v0 + k * 64, x.h, x.ex.k0 + tok, &vfull[r.slot]);
+            }
           }
           __syncwarp();
           r.step();
@@ -419,7 +444,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
       }
     }
-    if (abort) drain_copies(vfull, fills, r.n);
+    if (abort && leader) drain_copies(vfull, fills, r.n);
   } else if (warp == 1 && leader) {
     // ---- the products
     constexpr uint32_t idesc_s = idesc_bf16(Shape::kQueries, 128);
@@ -431,10 +456,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     auto output = [&](int u, int valid, bool first) {
       const int ks = (valid + 15) >> 4;               // 16-key steps that hold anything
       const uint32_t p = tmem + kPreScol + static_cast<uint32_t>(u & 1) * 128u;
-      if (!warp_wait(&p_full[u & 1], static_cast<uint32_t>(u >> 1) & 1u, abort)) return;
+      if (!warp_wait_tmem_of<kPair>(&p_full[u & 1], static_cast<uint32_t>(u >> 1) & 1u, abort)) return;
       constexpr int kSteps = Shape::kValRows / 16;
       for (int j = 0; kSteps * j < ks; ++j) {
-        if (!warp_wait(&vfull[rv.slot], rv.turn, abort)) return;
+        if (!warp_wait_of<kPair>(&vfull[rv.slot], rv.turn, abort)) return;
         clear_values<Shape::kValRows>(vring + rv.slot * kSlotBytes, nv, valid - j * Shape::kValRows, lane);
         tc_fence_after();
         if (elect_one()) {
@@ -456,14 +481,14 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     int i = 0, no = 0;
     bool more = walk.next_real(a, x);
     while (!abort && more) {
-      if (!warp_wait(&q_full, static_cast<uint32_t>(no) & 1u, abort)) break;
+      if (!warp_wait_of<kPair>(&q_full, static_cast<uint32_t>(no) & 1u, abort)) break;
       ++no;
       for (int t = 0; t < x.tiles && !abort; ++t, ++i) {
         // S(i) = Q K^T; its score tile is free: the weights over it were
         // waited for and their product issued one turn ago
         const uint32_t d = tmem + kPreScol + static_cast<uint32_t>(i & 1) * 128u;
         for (int k = 0; k < a.nq; k += Shape::kKeyChunks) {
-          if (!warp_wait(&kfull[rk.slot], rk.turn, abort)) break;
+          if (!warp_wait_of<kPair>(&kfull[rk.slot], rk.turn, abort)) break;
           tc_fence_after();
           if (elect_one()) {
             const uint32_t sa = q_a + static_cast<uint32_t>(k) * kPreChunk;
@@ -493,38 +518,22 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       if (!abort) output(i - 1, last, only);
     }
     drain_mmas<kPair>(&drained, abort);
-  } else if (kPair && warp == 1) {
-    // ---- rank 1: its queries and keys have landed
-    Ring r(a.kslots);
-    int no = 0;
-    while (!abort && walk.next_real(a, x)) {
-      if (!warp_wait(&q_full, static_cast<uint32_t>(no) & 1u, abort)) break;
-      ++no;
-      if (elect_one()) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&q_full), 0));
-      __syncwarp();
-      for (int t = 0; t < x.tiles; ++t) {
-        if (!warp_wait(&kfull[r.slot], r.turn, abort)) break;   // (one slot a tile)
-        if (elect_one()) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&kfull[r.slot]), 0));
-        __syncwarp();
-        r.step();
-      }
-    }
   } else if (kPair && warp == 2 && !leader) {
-    // ---- rank 1: its values have landed
+    // ---- rank 1: value tiles that end a sequence.  (A slot's phases here are
+    // its tiles of that kind: the next one is copied only when rank 0's product
+    // has given this one back.)
     const int nv = ((a.dvn >> 1) + 63) >> 6;
     Ring r(a.vslots);
+    uint32_t phases = 0;                              // bit: the parity of a slot's next phase
     while (!abort && walk.next_real(a, x)) {
-      for (int t = 0; t < x.tiles; ++t) {
-        if (!warp_wait(&vfull[r.slot], r.turn, abort)) break;
-        const bool cleared = clear_values<Shape::kValRows>(vring + r.slot * kSlotBytes, nv, x.see1 - t * kPreTile, lane);
-        if (elect_one()) {
-          if (cleared)
-            mbar_arrive_remote(&vfull[r.slot], 0);
-          else
-            mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&vfull[r.slot]), 0));
-        }
+      for (int t = 0; t < x.tiles; ++t, r.step()) {
+        const int valid = x.see1 - t * kPreTile;
+        if (valid >= kPreTile) continue;
+        if (!warp_wait(&vfull[r.slot], (phases >> r.slot) & 1u, abort)) break;
+        phases ^= 1u << r.slot;
+        clear_values<Shape::kValRows>(vring + r.slot * kSlotBytes, nv, valid, lane);
+        if (elect_one()) mbar_arrive_cluster_release(mapa_shared(smem_u32(&vfull[r.slot]), 0));
         __syncwarp();
-        r.step();
       }
     }
   } else if (warp >= 4) {
@@ -543,7 +552,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       for (int t = 0; t < x.tiles; ++t, ++i) {
         const uint32_t sb = tl + kPreScol + static_cast<uint32_t>((i & 1) * 128 + g * 64);
         uint32_t r[64];
-        mbar_wait(&s_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, abort);
+        mbar_wait_tmem_of<kPair>(&s_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, abort);
         __syncwarp();
         tc_fence_after();
         tmem_ld_cols<64>(sb, r);
@@ -576,7 +585,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (t > 0) {
             const float f = exp2_fast(m - mn);
             l *= f;
-            mbar_wait(&pv_done[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort);
+            mbar_wait_tmem_of<kPair>(&pv_done[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort);
             __syncwarp();
             tc_fence_after();
 #pragma unroll 1
@@ -613,10 +622,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         tmem_wait_st();
         tc_fence_before();
         if (kPair && !leader) {
-          // (the weights are in TMEM, complete and fenced; there is no memory for
-          // a release to order, and it would take 1 us)
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&p_full[i & 1]), 0));
+          // Weights in TMEM, handed on as PTX has tcgen05 operations handed from
+          // thread to thread: completed and fenced by each thread, which then
+          // arrives; a relaxed wait and a fence on the other side.  (Ordinary
+          // memory is not part of it.  A release here, with an acquire there,
+          // makes 8192 tokens x 64 heads 1777 us in place of 1325, and a local
+          // barrier with one thread that passes it on with a release 1512.)
+          mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&p_full[i & 1]), 0));
         } else {
           mbar_arrive(&p_full[i & 1]);
         }
@@ -628,7 +640,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       named_sync(1 + q4, 64);                         // xch is free again
       more = walk.next(a, then);                      // (beside the last output product)
       if (x.tiles > 0) {
-        mbar_wait(&pv_done[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort);
+        mbar_wait_tmem_of<kPair>(&pv_done[(i - 1) & 1], static_cast<uint32_t>((i - 1) >> 1) & 1u, abort);
         __syncwarp();
         tc_fence_after();
       }
