@@ -553,6 +553,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         const uint32_t sb = tl + kPreScol + static_cast<uint32_t>((i & 1) * 128 + g * 64);
         uint32_t r[64];
         mbar_wait_tmem_of<kPair>(&s_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, abort);
+        // O(i - 2) was done before S(i), but its arrival here is another message:
+        // waited for, so that no phase of the barrier is skipped
+        if (i >= 2) mbar_wait_tmem_of<kPair>(&pv_done[i & 1], static_cast<uint32_t>((i - 2) >> 1) & 1u, abort);
         __syncwarp();
         tc_fence_after();
         tmem_ld_cols<64>(sb, r);

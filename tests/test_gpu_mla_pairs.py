@@ -57,3 +57,23 @@ def test_pairs_repeat_their_bits_beside_keys_of_nan(capi, dn, dv, causal):
             noise.sort()                        # other code in the instruction caches
         again, lse2 = run_prefill(capi, *args, cq, ck, scale, causal)
         assert torch.equal(again, out) and torch.equal(lse2, lse), f"call {i}"
+
+
+def test_pairs_rescale_after_tiles_that_need_none(capi):
+    # scores that pass the running maximum by far in some key tiles and not at
+    # all in those between, one to five of them
+    n, H, dn, dv = 2300, 8, 64, 64
+    q, kv, kr = rnd(11, n, H, dn + R), rnd(12, n, H, dn + dv), rnd(13, n, R)
+    rise = [0, 1, 3, 4, 7, 12, 13, 17]
+    for k, t in enumerate(rise):
+        kv[128 * t: 128 * (t + 1), :, :dn] *= 2.0 ** k
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    args = (q[..., :dn], q[..., dn:], kv[..., :dn], kr, kv[..., dn:])
+    scale = 0.02
+    out, lse = run_prefill(capi, *args, cu, cu, scale, True)
+    some = [0, H - 1]
+    want = ref.prefill(*(f64(t[:, some] if t.dim() == 3 else t) for t in args), [0, n], [0, n], scale, True)
+    check_attention(out[:, some], lse[:, some], want, n, dn + R, "rising in steps")
+    for i in range(20):
+        again, lse2 = run_prefill(capi, *args, cu, cu, scale, True)
+        assert torch.equal(again, out) and torch.equal(lse2, lse), f"call {i}"
