@@ -72,8 +72,8 @@ typedef enum {
     MXFP4_ERR_CUDA = 5,               /* a CUDA runtime call or launch failed       */
     MXFP4_ERR_TIMEOUT = 6,            /* a device-side wait gave up                 */
     MXFP4_ERR_NO_DEVICE = 7,          /* no usable sm_103 device is current         */
-    MXFP4_ERR_INDEX = 8               /* a page, slot or position read on the device
-                                         was out of range (mxfp4_get_device_error)  */
+    MXFP4_ERR_INDEX = 8               /* a page, slot, position or prompt offset read on the
+                                         device was out of range (mxfp4_get_device_error)   */
 } mxfp4_status;
 
 typedef enum {
@@ -359,10 +359,12 @@ MXFP4_API size_t mxfp4_gemm_noalloc_max_scratch_bytes(void);
  * strides are multiples of 8 (MISALIGNED otherwise); a stride of a dimension
  * of more than one entry is positive (UNSUPPORTED_SHAPE otherwise).
  *
- * Indexes that live on the device (pages, slots, positions, lengths) cannot
- * be checked before the launch.  The kernels check them: nothing is read or
- * written out of range, the rows concerned are unspecified or left as they
- * were, and mxfp4_get_device_error() reports MXFP4_ERR_INDEX.
+ * Indexes that live on the device cannot be checked before the launch.  The
+ * kernels check them, and nothing is read or written out of range.  A page,
+ * slot, position or prompt offset that is out of range leaves the rows
+ * concerned unspecified or as they were, and mxfp4_get_device_error() reports
+ * MXFP4_ERR_INDEX.  A sequence length out of range is no error: it is cut to
+ * what the page table can hold (mxfp4_mla_decode).
  *
  * Softmax statistics and sums are fp32; the softmax weights are rounded to
  * bf16 for the second product, and each output once to bf16.  Cache rows past
@@ -456,7 +458,10 @@ MXFP4_API mxfp4_status mxfp4_mla_decode(const void* q_lat_dev, int64_t ql_tok, i
  *   k_nope_dev, v_dev       bf16 [Tk][H][dn], [Tk][H][dv] by their strides
  *                           (views of one expanding projection [Tk][H][dn + dv])
  *   k_rope_dev              bf16 [Tk][R], row stride kr_tok
- *   cu_q_dev, cu_k_dev      int32 [S + 1], ascending from 0 to Tq and Tk
+ *   cu_q_dev, cu_k_dev      int32 [S + 1], ascending (equal neighbours: an empty
+ *                           sequence); cu_q from 0 to Tq, cu_k within 0 .. Tk.
+ *                           Others are an index error; rows of out and lse
+ *                           outside cu_q[0] .. cu_q[S] are not written
  *   out_dev                 bf16 [Tq][H][dv] by its strides
  *   lse_dev                 fp32 [Tq][H] contiguous, or NULL
  * dn and dv are multiples of 8, dn at most 192, dv at most 256; R is 64; H at

@@ -104,6 +104,7 @@ struct PrefillArgs {
 struct Extent {
   int q0, qn, k0, kn;
 };
+// (Offsets out of range are cut here, and reported by check_offsets.)
 __device__ __forceinline__ int clamp_to(int v, int hi) { return v < 0 ? 0 : (v > hi ? hi : v); }
 __device__ __forceinline__ Extent extent(const PrefillArgs& a, int s) {
   Extent e;
@@ -112,6 +113,18 @@ __device__ __forceinline__ Extent extent(const PrefillArgs& a, int s) {
   e.k0 = clamp_to(__ldg(a.cu_k + s), a.Tk);
   e.kn = max(0, clamp_to(__ldg(a.cu_k + s + 1), a.Tk) - e.k0);
   return e;
+}
+
+// By one warp of the grid: both offsets ascending inside the tensors, and the
+// queries' from 0 to the last row (the rows that they leave out are not written).
+__device__ __forceinline__ void check_offsets(const PrefillArgs& a, int lane) {
+  bool bad = false;
+  for (int s = lane; s <= a.S; s += 32) {
+    const int q = __ldg(a.cu_q + s), k = __ldg(a.cu_k + s);
+    bad |= s == 0 ? q != 0 || k < 0 : q < __ldg(a.cu_q + s - 1) || k < __ldg(a.cu_k + s - 1);
+    bad |= s == a.S && (q != a.Tq || k > a.Tk);
+  }
+  if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) atomicOr(&g_mla_prefill_error, kErrIndex);
 }
 
 // A query tile of a block or pair, and what its keys amount to.
@@ -536,6 +549,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         __syncwarp();
       }
     }
+  } else if (warp == 2 && blockIdx.x == 0) {
+    check_offsets(a, lane);
   } else if (warp >= 4) {
     // ---- softmax.  Warps w and w + 4 hold the same 32 queries and meet at
     // named barriers, so they walk every tile even after a wait has given up.

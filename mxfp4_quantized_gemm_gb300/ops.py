@@ -502,7 +502,8 @@ def mla_prefill(q_nope: Tensor, q_rope: Tensor, k_nope: Tensor, k_rope: Tensor, 
     """Expanded attention of ragged prompts (sequence s: queries cu_q[s] ..
     cu_q[s + 1], keys cu_k[s] ..): out [T, H, dv] and the log-sum-exp [T, H].
     k_rope [N, 64] is shared by all heads; views of one projection are read in
-    place."""
+    place.  cu_q must ascend from 0 to T and cu_k within 0 .. N (checked on the
+    device: mxfp4_get_device_error); rows that cu_q leaves out are not written."""
     _check_mla_prefill(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k)
     T, H, dn = q_nope.shape
     N, dv = v.shape[0], v.shape[2]
