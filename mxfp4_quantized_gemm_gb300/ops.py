@@ -414,8 +414,8 @@ def mla_store(kv: Tensor, gamma: Tensor, eps: float, q_rope: Tensor, cos_sin: Te
     if T == 0:
         return q_out
     kv, q = _vec(kv), _vec(q_rope)
-    _capi().mxfp4_mla_store(kv, kv.stride(0), gamma.contiguous(), eps, q if H else None, q.stride(0), q.stride(1),
-                            q_out if H else None, q_out.stride(0), q_out.stride(1), H, cos_sin.contiguous(),
+    _capi().mxfp4_mla_store(kv, kv.stride(0), _vec(gamma.contiguous()), eps, q if H else None, q.stride(0), q.stride(1),
+                            q_out if H else None, q_out.stride(0), q_out.stride(1), H, _vec(cos_sin.contiguous()),
                             cos_sin.shape[0], positions.contiguous(), slots.contiguous(), cache, cache.stride(0),
                             cache.shape[1], cache.shape[0], T, L, _MLA_ROPE, interleaved, _stream(kv))
     return q_out
@@ -462,7 +462,9 @@ def mla_decode(q_lat: Tensor, q_rope: Tensor, cache: Tensor, page_table: Tensor,
     if T == 0:
         return out, lse
     q_lat, q_rope, lens = _vec(q_lat), _vec(q_rope), seq_lens.contiguous()
-    table = page_table if page_table.stride(1) == 1 else page_table.contiguous()
+    rows_apart = S == 1 or page_table.stride(0) >= page_table.shape[1]      # (not so in an expanded table)
+    table = page_table if page_table.stride(1) == 1 and rows_apart else page_table.clone(
+        memory_format=torch.contiguous_format)
     nbytes = c.mxfp4_mla_decode_workspace_bytes(S, T // S, H, L, table.shape[1] * cache.shape[1])
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q_lat.device)
     c.mxfp4_mla_decode(q_lat, q_lat.stride(1), q_lat.stride(0), q_rope, q_rope.stride(0), q_rope.stride(1), cache,
