@@ -28,6 +28,7 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "tensor_map.h"
 #include "layout.cuh"
 #include "ptx.cuh"
 
@@ -533,32 +534,6 @@ __global__ void __launch_bounds__(kBmmThreads, 1) a16wfp4_bmm_ts_kernel(const __
 }
 
 // ------------------------------------------------------------------ host
-// The calling host thread's device context, made current if the runtime has
-// not bound it in this thread yet: cuTensorMapEncodeTiled is a driver call
-// and runs in the thread's current context, which the runtime binds lazily
-// (cudaFree(nullptr) binds it and frees nothing).
-static cudaError_t bind_device_context() {
-  static thread_local bool bound = false;
-  if (bound) return cudaSuccess;
-  const cudaError_t e = cudaFree(nullptr);
-  if (e == cudaSuccess) bound = true;
-  return e;
-}
-
-// The driver's tensor-map encoder, looked up once (thread-safe static init).
-static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    return nullptr;
-  }();
-  return fn;
-}
-
 static std::atomic<bool> g_bmm_attr[64];      // kernel attribute set on this device
 static std::atomic<bool> g_bmm_ts_attr[64];   // the same for a16wfp4_bmm_ts_kernel
 

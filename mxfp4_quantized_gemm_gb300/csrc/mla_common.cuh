@@ -8,6 +8,7 @@
 
 #include "mla.h"
 #include "ptx.cuh"
+#include "tensor_map.h"
 
 namespace mx {
 
@@ -357,36 +358,13 @@ inline float positive_scale(float scale) {
   return c < 1.17549435e-38f ? 1.17549435e-38f : c;
 }
 
-// The calling host thread's device context, made current if the runtime has
-// not bound it yet (cuTensorMapEncodeTiled is a driver call).
-inline cudaError_t mla_bind_context() {
-  static thread_local bool bound = false;
-  if (bound) return cudaSuccess;
-  const cudaError_t e = cudaFree(nullptr);
-  if (e == cudaSuccess) bound = true;
-  return e;
-}
-
-inline PFN_cuTensorMapEncodeTiled_v12000 mla_tensor_map_encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    return nullptr;
-  }();
-  return fn;
-}
-
 // Tensor map of a bf16 tensor of `n` dimensions (innermost first) with strides
 // (elements) of all but the innermost, read in boxes with the 128-byte swizzle
 // and zero fill outside.
 template <int n>
 cudaError_t mla_tensor_map_nd(CUtensorMap* map, const void* p, const int64_t (&d)[n], const int64_t (&stride)[n - 1],
                               const int (&b)[n]) {
-  auto encode = mla_tensor_map_encoder();
+  auto encode = tensor_map_encoder();
   if (encode == nullptr) return cudaErrorNotSupported;
   cuuint64_t dims[n], strides[n - 1];
   cuuint32_t box[n], estr[n];

@@ -1009,7 +1009,7 @@ static cudaError_t launch_decode_nb(const CUtensorMap (&maps)[4], DecodeArgs a, 
 
 cudaError_t launch_mla_decode(const MlaDecodeProblem& p, const DeviceInfo& dev, cudaStream_t s) {
   if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
-  cudaError_t e = mla_bind_context();
+  cudaError_t e = bind_device_context();
   if (e != cudaSuccess) return e;
   const RowSplit r = split_rows(p.q_len, p.H);
   DecodeArgs a{};

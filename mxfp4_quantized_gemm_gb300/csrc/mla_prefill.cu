@@ -789,7 +789,7 @@ static cudaError_t launch_prefill(const MlaPrefillProblem& p, PrefillArgs a, con
 
 cudaError_t launch_mla_prefill(const MlaPrefillProblem& p, const DeviceInfo& dev, cudaStream_t s) {
   if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
-  const cudaError_t e = mla_bind_context();
+  const cudaError_t e = bind_device_context();
   if (e != cudaSuccess) return e;
   PrefillArgs a{};
   a.cu_q = p.cu_q;
