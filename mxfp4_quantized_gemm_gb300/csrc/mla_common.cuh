@@ -148,6 +148,13 @@ struct Ring {
     }
   }
 };
+// For the filling warp, at its end: the last `n` of its `fills` fills have been
+// emptied (a wait for the phase of each slot that no further fill waits for).
+template <bool kPair>
+__device__ __forceinline__ void wait_emptied(uint64_t* empty, int fills, int n, bool& abort) {
+  for (int f = fills > n ? fills - n : 0; f < fills; ++f)
+    if (!warp_wait_of<kPair>(&empty[f % n], static_cast<uint32_t>(f / n) & 1u, abort)) return;
+}
 // For the filling warp, after a wait that gave up: a bounded wait for the
 // copies of the `fills` fills so far that may be in flight (the last of each
 // of the n slots).

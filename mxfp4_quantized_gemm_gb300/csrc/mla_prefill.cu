@@ -418,6 +418,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
       }
     }
+    // the products' last arrivals here, which in a pair come from rank 0 and
+    // must not find a block that has ended
+    wait_emptied<kPair>(kempty, fills, r.n, abort);
+    if (no > 0) warp_wait_of<kPair>(&q_empty, static_cast<uint32_t>(no - 1) & 1u, abort);
     if (abort && leader) {
       // give the copies in flight a bounded time to land (rank 0's barriers may
       // wait for rank 1 as well: bounded all the same; rank 1's copies, which
@@ -457,6 +461,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
       }
     }
+    wait_emptied<kPair>(vempty, fills, r.n, abort);
     if (abort && leader) drain_copies(vfull, fills, r.n);
   } else if (warp == 1 && leader) {
     // ---- the products
