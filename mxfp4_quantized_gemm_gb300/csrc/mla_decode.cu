@@ -31,7 +31,9 @@
 // place is free again about 8000 cycles after it was asked for, two at a time:
 // 3200 to 3700 until it lands from HBM, 1600 of score products, 1000 of softmax,
 // 1300 of output products.  Shared memory alone needs 2500 (operands and copies
-// at 128 bytes a cycle).  A third tile does not fit beside the queries.
+// at 128 bytes a cycle), and so it is how long a place is held, with two of them,
+// that sets the pace.  A third tile does not fit beside 64 rows of queries; beside
+// 16 or 32 rows 2.8 or 2.5 tiles would, of which two whole ones are used.
 // A copying warp spends about 430 cycles on each wait, arrival and copy, and
 // each copy more costs it 16 by one thread and about 100 by lanes in turns.  Where
 // a page holds whole tiles a group of chunks is one copy, and a tile comes in
@@ -47,10 +49,14 @@
 // leaves unnormalized parts (fp32, with maximum and sum) that
 // mla_combine_kernel joins.
 //
-// Measured (HBM share by the bytes of the cache read once): 64 ragged sequences
-// of up to 8192, 64 rows: 80.5 us, 4.4 TB/s; one of 131072: 42.7 us, 3.5 TB/s; 16 of
-// up to 4096: 24.7 us, of which 2 to the first copy, 12 of tiles, 2 to write the
-// parts out and 6 to join them.
+// Measured (rates by the bytes of the cache read once): 64 ragged sequences of up
+// to 8192, 64 rows: 80.3 us, 4.3 TB/s; one of 131072: 42.8 us, 3.5 TB/s; 16 of up to
+// 4096: 24.6 us.  From the end of the call ahead, in us (time stamps of calls in
+// a graph, median block; where a block ends, the last one in brackets):
+//                   first copy landed   last weights   block's end    joined, last
+//   16 x 4096              3.4              11.0       14.2 (16.3)       22.5
+//   1 x 131072             4.4              29.8       33.0 (34.7)       41.8
+//   64 x 8192              3.7              63.6       66.7 (74.4)       82.1
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <atomic>
@@ -953,12 +959,11 @@ static RowSplit split_rows(int q_len, int H) {
 }
 
 // Going over to another row group is counted as a tile where 64 rows have to be
-// written out for it, and as three in long stretches, where many blocks go over
-// in the middle of their work (counted as 0, 1, 3, ragged lengths, 64 or 128
-// rows: 13 sequences up to 4052 22.1, 20.6, 20.7 us; 59 up to 1647 55.4, 53.0,
-// 51.7; 30 up to 2450, ten tiles a block, 35.2, 33.6, 34.9; 29 up to 8201, 15 tiles
-// a block, 48.7, 47.0, 47.4; 100 up to 4190, 28 tiles a block, 86.2, 84.7, 79.4).  For fewer rows it is nothing (65 up to 426,
-// 32 rows: 16.7, 18.2, 19.2).
+// written out for it, and as three where the blocks have 24 units and more, so
+// that many go over in the middle of their work.  Counted as 0, 1, 3 (ragged
+// lengths): 10 tiles a block 35.2, 33.6, 34.9 us; 15 48.7, 47.0, 47.4; 28 86.2, 84.7,
+// 79.4.  For groups of fewer rows it is nothing (32 rows, 65 sequences of up to
+// 426: 16.7, 18.2, 19.2).
 static int decode_over(int NB) { return NB == 64 ? 1 : 0; }
 
 // Blocks of a call, and what going over counts as (nothing where each tile has a

@@ -46,11 +46,12 @@
 // key tiles, before its first and after its last product.)  How they are dealt
 // out: QueryTiles.
 //
-// Measured (dn + R = dv = 256, 64 heads): 8192 tokens 1320 us, 1.67 PFLOP/s, the
-// rate that the card's power limit leaves a long run of matrix products; six
-// ragged prompts of 156 to 781 tokens on up to 1000 others 152 us: of a query
-// tile's 10 us, 7 key tiles at 1.16 us, then 1.7 until the last product is done
-// and 1.7 to write it out, during which the next tile's scores are formed.
+// Measured (dn + R = dv = 256, 64 heads; from card to card): 8192 tokens 1310 to
+// 1335 us, 1.65 to 1.68 PFLOP/s, the rate that the power limit leaves a long run
+// of matrix products; six ragged prompts of 156 to 781 tokens on up to 1000
+// others 147 to 153 us: of a query tile's 10 us, 7 key tiles at 1.16 us, then 1.7
+// until the last product is done and 1.7 to write it out, during which the next
+// tile's scores are formed.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <atomic>
