@@ -479,11 +479,130 @@ MXFP4_API mxfp4_status mxfp4_mla_prefill(const void* q_nope_dev, int64_t qn_tok,
                                          void* stream);
 
 /*
+ * Mixture of experts in MXFP4: the router's choice, each routed token times
+ * its expert's W4A4 weights, and the experts' whole gated network.  The
+ * pages' models have such layers (PR #39598 names them); the operators follow
+ * the published definitions.  They serve: nothing here has a gradient.
+ *
+ * A token t has top_k slots; slot j names expert ids[t][j] (int32).  A
+ * negative id is an empty slot (a padding token of a captured batch, or a
+ * choice the router could not make): it takes no part.  An id >= E is treated
+ * as an empty slot and mxfp4_get_device_error() reports MXFP4_ERR_INDEX.
+ * The same expert may stand in several slots of a token; each counts.
+ *
+ * Limits: E at most 1024, top_k at most 32, K even, T * top_k at most 2^28.
+ * Row strides (ld*) are in elements and at least the row's length; a single
+ * row's stride is not read.  bf16 and fp32 pointers need their type's
+ * alignment only (rows whose pointer and stride allow 16-byte accesses are
+ * faster); packed weights and workspaces are 16-byte aligned.  Workspaces
+ * need no initialization; calls sharing one must be ordered on the GPU.
+ * Deterministic: the same call gives the same bits.
+ */
+typedef enum {
+    MXFP4_DTYPE_BF16 = 0,
+    MXFP4_DTYPE_F32 = 1
+} mxfp4_dtype;
+
+typedef enum {
+    MXFP4_MOE_SOFTMAX = 0,
+    MXFP4_MOE_SIGMOID = 1
+} mxfp4_moe_score;
+
+typedef enum {
+    MXFP4_MOE_SILU = 0,         /* gate * sigmoid(gate) * up                                */
+    MXFP4_MOE_GELU_TANH = 1,    /* gate * (1 + tanh(sqrt(2/pi) (gate + 0.044715 gate^3))) / 2 * up */
+    MXFP4_MOE_SWIGLU_CLAMP = 2  /* gate = min(gate, limit), up within +-limit:
+                                   gate * sigmoid(alpha * gate) * (up + 1)                  */
+} mxfp4_moe_act;
+
+/*
+ * The router.  For each token, with x its E logits:
+ *   s = softmax(x) or 1 / (1 + exp(-x));  c_i = s_i + bias_i (c = s without)
+ *   n_group > 1: the experts fall into n_group groups of E / n_group
+ *     neighbours; a group's value is the sum of its group_top (1 or 2) highest
+ *     c, and only the topk_group groups of highest value keep their experts
+ *   ids[t][0 .. top_k): the experts of highest c, highest first
+ *   weights[t][j] = scale * s_id, or with renormalize != 0
+ *     scale * s_id / (the sum of s over the chosen)
+ * Equal values go to the lower index, of experts and groups.  The choice is
+ * that of c evaluated in 64 bits (of the logits where there is no bias), the
+ * weights are fp32.  A logit of -inf (or NaN), or a c of -inf or NaN, switches
+ * its expert off: it is never chosen, and a token with fewer than top_k
+ * experts left gets -1 and weight 0 in its last slots.  Logits of +inf share
+ * the softmax's whole weight.
+ *
+ *   logits_dev    bf16 or fp32 [T][ld >= E]
+ *   bias_dev      fp32 [E], or NULL
+ *   weights_dev   fp32 [T][top_k] contiguous; ids_dev int32 [T][top_k]
+ * E is a multiple of n_group; n_group at most 32; topk_group <= n_group;
+ * top_k <= topk_group * E / n_group.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
+ * MISALIGNED, CUDA.
+ */
+MXFP4_API mxfp4_status mxfp4_moe_route(const void* logits_dev, mxfp4_dtype dtype, int64_t ld, const float* bias_dev,
+                                       int T, int E, int top_k, mxfp4_moe_score score, int n_group, int topk_group,
+                                       int group_top, int renormalize, float scale, float* weights_dev,
+                                       int32_t* ids_dev, void* stream);
+
+/* Workspace bytes of the two calls below; 0 where an argument is refused. */
+MXFP4_API size_t mxfp4_moe_linear_workspace_bytes(int T, int top_k, int E, int N, int K);
+MXFP4_API size_t mxfp4_moe_ffn_workspace_bytes(int T, int top_k, int E, int K, int I, int N);
+
+/*
+ * Each routed token times its expert's weights: mxfp4_gemm's result with the
+ * weights of expert e = ids[t][j],
+ *   out[t * top_k + j] = bf16_RNE( sum_k deq(Q(x[t]))_k deq(W_e)[n][k] + bias[e][n] )
+ * fp32 accumulation, bias in the epilogue.  The row of an empty slot is zeros.
+ * A row per slot (the experts' second product) is the same call with
+ * T * top_k tokens of one slot.
+ *
+ *   x_dev         bf16 [T][ldx >= K]
+ *   w_packed_dev  mxfp4_pack_weights of E matrices [N][K]
+ *   bias_dev      bf16 [E][N] contiguous, or NULL
+ *   out_dev       bf16 [T * top_k][ldo >= N]
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE, CUDA.
+ */
+MXFP4_API mxfp4_status mxfp4_moe_linear(const void* x_dev, int64_t ldx, const int32_t* ids_dev,
+                                        const void* w_packed_dev, const void* bias_dev, void* out_dev, int64_t ldo,
+                                        int T, int top_k, int E, int N, int K, void* workspace_dev,
+                                        size_t workspace_bytes, void* stream);
+
+/*
+ * The experts' gated network.  For slot j of token t with e = ids[t][j]:
+ *   z   = W_gate_up[e] Q(x[t]) + bias_gate_up[e]        2 I values, fp32:
+ *         gate i at 2 i, up i at 2 i + 1
+ *   h   = act(gate, up) in fp32, quantized per 1x32 (one rounding from fp32,
+ *         the scale and rounding rule of mxfp4_quant_act)
+ *   y_j = bf16_RNE( W_down[e] h + bias_down[e] )
+ *   out[t] = bf16_RNE( residual[t] + sum_j weights[t][j] * y_j ), summed in
+ *         fp32 in the order of the slots
+ * A token without experts gives its residual (zeros without one).  One expert
+ * with ids of 0 and weights of 1 is a dense gated network.
+ *
+ *   x_dev            bf16 [T][ldx >= K]
+ *   weights_dev      fp32 [T][top_k] contiguous (empty slots' are not used)
+ *   w_gate_up_dev    mxfp4_pack_weights of E matrices [2 I][K] whose rows
+ *                    alternate gate and up; bias bf16 [E][2 I] alike, or NULL
+ *   w_down_dev       mxfp4_pack_weights of E matrices [N][I]; bias [E][N] or NULL
+ *   residual_dev     bf16 [T][ldr >= N], or NULL; may be out_dev itself with
+ *                    the same stride
+ *   out_dev          bf16 [T][ldo >= N]; must not overlap x
+ *   alpha, limit     of MXFP4_MOE_SWIGLU_CLAMP, else ignored
+ * I is even.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE,
+ * CUDA.
+ */
+MXFP4_API mxfp4_status mxfp4_moe_ffn(const void* x_dev, int64_t ldx, const int32_t* ids_dev, const float* weights_dev,
+                                     const void* w_gate_up_dev, const void* bias_gate_up_dev, const void* w_down_dev,
+                                     const void* bias_down_dev, const void* residual_dev, int64_t ldr, void* out_dev,
+                                     int64_t ldo, int T, int top_k, int E, int K, int I, int N, mxfp4_moe_act act,
+                                     float alpha, float limit, void* workspace_dev, size_t workspace_bytes,
+                                     void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the library's device error
  * words on the current device.  Returns MXFP4_ERR_TIMEOUT if a kernel gave
  * up a bounded wait since the last call, MXFP4_ERR_INDEX if a latent-attention
- * kernel met an index out of range, MXFP4_OK otherwise (or MXFP4_ERR_CUDA if
- * the synchronisation itself failed).
+ * or mixture-of-experts kernel met an index out of range, MXFP4_OK otherwise
+ * (or MXFP4_ERR_CUDA if the synchronisation itself failed).
  */
 MXFP4_API mxfp4_status mxfp4_get_device_error(void* stream);
 

@@ -29,6 +29,9 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED_SHAPE, ERR_MISALIGNED, ERR_WORKSPACE, ERR_C
     ERR_NO_DEVICE, ERR_INDEX = range(9)
 LAYOUT_ROWMAJOR, LAYOUT_TILED = 0, 1
 OUT_BMN, OUT_MBN = 0, 1
+DTYPE_BF16, DTYPE_F32 = 0, 1
+MOE_SOFTMAX, MOE_SIGMOID = 0, 1
+MOE_SILU, MOE_GELU_TANH, MOE_SWIGLU_CLAMP = 0, 1, 2
 
 _p, _i, _sz, _l, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64, ctypes.c_float
 
@@ -54,6 +57,12 @@ _SIGNATURES = {
                               _i, _f, _p, _sz, _p]),
     "mxfp4_mla_prefill": (_i, [_p, _l, _l, _p, _l, _l, _p, _l, _l, _p, _l, _p, _l, _l, _p, _p, _i, _p, _l, _l, _p, _i,
                                _i, _i, _i, _i, _i, _f, _i, _p]),
+    "mxfp4_moe_route": (_i, [_p, _i, _l, _p, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p]),
+    "mxfp4_moe_linear_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "mxfp4_moe_linear": (_i, [_p, _l, _p, _p, _p, _p, _l, _i, _i, _i, _i, _i, _p, _sz, _p]),
+    "mxfp4_moe_ffn_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "mxfp4_moe_ffn": (_i, [_p, _l, _p, _p, _p, _p, _p, _p, _p, _l, _p, _l, _i, _i, _i, _i, _i, _i, _i, _f, _f, _p, _sz,
+                           _p]),
     "mxfp4_get_device_error": (_i, [_p]),
     "mxfp4_gemm_noalloc": (_i, [_p, _i, _p, _p, _p, _i, _i, _i, _i, _p]),
     "mxfp4_gemm_noalloc_max_scratch_bytes": (_sz, []),
@@ -229,6 +238,38 @@ def mxfp4_mla_prefill(q_nope, qn_tok: int, qn_head: int, q_rope, qr_tok: int, qr
                                  _ptr(out), o_tok, o_head, _ptr(lse), Tq, Tk, H, dn, R, dv, scale,
                                  1 if causal else 0, _stream(stream)),
            "mxfp4_mla_prefill")
+
+
+def mxfp4_moe_route(logits, dtype: int, ld: int, bias, T: int, E: int, top_k: int, score: int, n_group: int,
+                    topk_group: int, group_top: int, renormalize: bool, scale: float, weights, ids,
+                    stream=None) -> None:
+    _check(lib.mxfp4_moe_route(_ptr(logits), dtype, ld, _ptr(bias), T, E, top_k, score, n_group, topk_group, group_top,
+                               1 if renormalize else 0, scale, _ptr(weights), _ptr(ids), _stream(stream)),
+           "mxfp4_moe_route")
+
+
+def mxfp4_moe_linear_workspace_bytes(T: int, top_k: int, E: int, N: int, K: int) -> int:
+    return lib.mxfp4_moe_linear_workspace_bytes(T, top_k, E, N, K)
+
+
+def mxfp4_moe_linear(x, ldx: int, ids, w_packed, bias, out, ldo: int, T: int, top_k: int, E: int, N: int, K: int,
+                     workspace, workspace_bytes: int, stream=None) -> None:
+    _check(lib.mxfp4_moe_linear(_ptr(x), ldx, _ptr(ids), _ptr(w_packed), _ptr(bias), _ptr(out), ldo, T, top_k, E, N, K,
+                                _ptr(workspace), workspace_bytes, _stream(stream)),
+           "mxfp4_moe_linear")
+
+
+def mxfp4_moe_ffn_workspace_bytes(T: int, top_k: int, E: int, K: int, I: int, N: int) -> int:
+    return lib.mxfp4_moe_ffn_workspace_bytes(T, top_k, E, K, I, N)
+
+
+def mxfp4_moe_ffn(x, ldx: int, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, residual, ldr: int, out,
+                  ldo: int, T: int, top_k: int, E: int, K: int, I: int, N: int, act: int, alpha: float, limit: float,
+                  workspace, workspace_bytes: int, stream=None) -> None:
+    _check(lib.mxfp4_moe_ffn(_ptr(x), ldx, _ptr(ids), _ptr(weights), _ptr(w_gate_up), _ptr(bias_gate_up), _ptr(w_down),
+                             _ptr(bias_down), _ptr(residual), ldr, _ptr(out), ldo, T, top_k, E, K, I, N, act, alpha,
+                             limit, _ptr(workspace), workspace_bytes, _stream(stream)),
+           "mxfp4_moe_ffn")
 
 
 def mxfp4_get_device_error(stream=None) -> int:

@@ -11,6 +11,7 @@
 #include "mxfp4_diag.h"
 #include "internal.h"
 #include "mla.h"
+#include "moe.h"
 #include "norm_quant.h"
 
 namespace mx {
@@ -497,6 +498,168 @@ mxfp4_status mxfp4_mla_prefill(const void* q_nope, int64_t qn_tok, int64_t qn_he
   return from_cuda(launch_mla_prefill(p, dev, static_cast<cudaStream_t>(stream)));
 }
 
+// ------------------------------------------------------ mixture of experts
+
+static bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+mxfp4_status mxfp4_moe_route(const void* logits, mxfp4_dtype dtype, int64_t ld, const float* bias, int T, int E,
+                             int top_k, mxfp4_moe_score score, int n_group, int topk_group, int group_top,
+                             int renormalize, float scale, float* weights, int32_t* ids, void* stream) {
+  if (logits == nullptr || weights == nullptr || ids == nullptr) return MXFP4_ERR_INVALID_ARG;
+  if (T <= 0 || E <= 0 || top_k <= 0 || n_group <= 0 || topk_group <= 0) return MXFP4_ERR_INVALID_ARG;
+  if (dtype != MXFP4_DTYPE_BF16 && dtype != MXFP4_DTYPE_F32) return MXFP4_ERR_INVALID_ARG;
+  if (score != MXFP4_MOE_SOFTMAX && score != MXFP4_MOE_SIGMOID) return MXFP4_ERR_INVALID_ARG;
+  if (group_top != 1 && group_top != 2) return MXFP4_ERR_INVALID_ARG;
+  if (E > kMoeMaxExperts || top_k > kMoeMaxTopK || n_group > kMoeMaxGroups || E % n_group != 0 ||
+      topk_group > n_group || top_k > E / n_group * topk_group || (T > 1 && ld < E))
+    return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned_to(logits, dtype == MXFP4_DTYPE_BF16 ? 2 : 4) || !aligned_to(bias, 4) || !aligned_to(weights, 4) ||
+      !aligned_to(ids, 4))
+    return MXFP4_ERR_MISALIGNED;
+  DeviceInfo dev;
+  const mxfp4_status st = device_ready(&dev);
+  if (st != MXFP4_OK) return st;
+  const MoeRouteProblem p{logits,  dtype == MXFP4_DTYPE_BF16, ld, bias, T, E, top_k, score == MXFP4_MOE_SIGMOID,
+                          n_group, topk_group, group_top, renormalize != 0, scale, weights, ids};
+  return from_cuda(launch_moe_route(p, dev, static_cast<cudaStream_t>(stream)));
+}
+
+// Workspace carve-up of the experts' calls, each region 1 KiB aligned: plan,
+// blocked activations, (ffn: blocked activations of the second product, the
+// pairs' results,) parts of cut tiles.
+struct MoeWorkspace {
+  size_t plan, a, h, results, parts, total;
+  int64_t ldp;   // row stride of the pairs' results
+};
+static MoeWorkspace moe_workspace_layout(int64_t P, int E, int K, int I, int N, int sm_count) {
+  const int64_t rt = moe_max_tiles(P, E);
+  MoeWorkspace w{};
+  w.plan = 0;
+  w.a = round_up(moe_plan_bytes(P, E), 1024);
+  w.h = w.a + static_cast<size_t>(rt * (padded_k(K) / kKTile)) * kMoeBlockBytes;
+  w.results = w.h + (I > 0 ? static_cast<size_t>(rt * (padded_k(I) / kKTile)) * kMoeBlockBytes : 0);
+  w.ldp = ceil_div(N, 8) * 8;
+  w.parts = w.results + (I > 0 ? round_up(static_cast<size_t>(P * w.ldp) * 2, 1024) : 0);
+  w.total = w.parts + moe_gemm_parts_bytes(sm_count);
+  return w;
+}
+
+// Sizes both experts' calls share; P = T * top_k pairs.
+static mxfp4_status check_moe(int T, int top_k, int E, int K, int64_t columns) {
+  if (T <= 0 || top_k <= 0 || E <= 0 || K <= 0 || columns <= 0) return MXFP4_ERR_INVALID_ARG;
+  const int64_t P = static_cast<int64_t>(T) * top_k;
+  if ((K & 1) || E > kMoeMaxExperts || top_k > kMoeMaxTopK || P > (int64_t{1} << 28) || columns > (int64_t{1} << 26) ||
+      K > (1 << 26))
+    return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  // tiles, k-steps and rows are counted in 32 bits on the device
+  if (moe_max_tiles(P, E) * ceil_div(columns, 256) > (int64_t{1} << 30)) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  return MXFP4_OK;
+}
+
+size_t mxfp4_moe_linear_workspace_bytes(int T, int top_k, int E, int N, int K) {
+  if (check_moe(T, top_k, E, K, N) != MXFP4_OK) return 0;
+  return moe_workspace_layout(static_cast<int64_t>(T) * top_k, E, K, 0, N, current_sm_count()).total;
+}
+
+size_t mxfp4_moe_ffn_workspace_bytes(int T, int top_k, int E, int K, int I, int N) {
+  if (I <= 0 || check_moe(T, top_k, E, K, N) != MXFP4_OK ||
+      check_moe(T, top_k, E, K, 2 * static_cast<int64_t>(I)) != MXFP4_OK || (I & 1))
+    return 0;
+  return moe_workspace_layout(static_cast<int64_t>(T) * top_k, E, K, I, N, current_sm_count()).total;
+}
+
+mxfp4_status mxfp4_moe_linear(const void* x, int64_t ldx, const int32_t* ids, const void* w_packed, const void* bias,
+                              void* out, int64_t ldo, int T, int top_k, int E, int N, int K, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (x == nullptr || ids == nullptr || w_packed == nullptr || out == nullptr) return MXFP4_ERR_INVALID_ARG;
+  mxfp4_status st = check_moe(T, top_k, E, K, N);
+  if (st != MXFP4_OK) return st;
+  const int64_t P = static_cast<int64_t>(T) * top_k;
+  if ((T > 1 && ldx < K) || (P > 1 && ldo < N)) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned_to(x, 2) || !aligned_to(bias, 2) || !aligned_to(out, 2) || !aligned_to(ids, 4) || !aligned16(w_packed))
+    return MXFP4_ERR_MISALIGNED;
+  const MoeWorkspace w = moe_workspace_layout(P, E, K, 0, N, current_sm_count());
+  if (workspace == nullptr || workspace_bytes < w.total) return MXFP4_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return MXFP4_ERR_MISALIGNED;
+  DeviceInfo dev;
+  if ((st = device_ready(&dev)) != MXFP4_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const MoePlan plan = moe_plan_at(ws + w.plan, P, E);
+  cudaError_t e = launch_moe_plan(ids, static_cast<int>(P), E, plan, dev, s);
+  if (e == cudaSuccess) e = launch_moe_gather(x, ldx, T, top_k, K, plan, ws + w.a, out, ldo, N, dev, s);
+  MoeGemmProblem p{};
+  p.a_blocks = ws + w.a;
+  p.w_packed = static_cast<const uint8_t*>(w_packed);
+  p.bias = bias;
+  p.E = E;
+  p.N = N;
+  p.K = K;
+  p.out = out;
+  p.ldo = ldo;
+  p.which = 0;
+  p.parts = reinterpret_cast<float*>(ws + w.parts);
+  if (e == cudaSuccess) e = launch_moe_gemm(p, plan, dev, s);
+  return from_cuda(e);
+}
+
+mxfp4_status mxfp4_moe_ffn(const void* x, int64_t ldx, const int32_t* ids, const float* weights,
+                           const void* w_gate_up, const void* bias_gate_up, const void* w_down, const void* bias_down,
+                           const void* residual, int64_t ldr, void* out, int64_t ldo, int T, int top_k, int E, int K,
+                           int I, int N, mxfp4_moe_act act, float alpha, float limit, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (x == nullptr || ids == nullptr || weights == nullptr || w_gate_up == nullptr || w_down == nullptr || out == nullptr)
+    return MXFP4_ERR_INVALID_ARG;
+  if (I <= 0) return MXFP4_ERR_INVALID_ARG;
+  if (act != MXFP4_MOE_SILU && act != MXFP4_MOE_GELU_TANH && act != MXFP4_MOE_SWIGLU_CLAMP) return MXFP4_ERR_INVALID_ARG;
+  mxfp4_status st = check_moe(T, top_k, E, K, N);
+  if (st == MXFP4_OK) st = check_moe(T, top_k, E, K, 2 * static_cast<int64_t>(I));
+  if (st != MXFP4_OK) return st;
+  if ((I & 1) || (T > 1 && (ldx < K || ldo < N || (residual != nullptr && ldr < N)))) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  const int64_t P = static_cast<int64_t>(T) * top_k;
+  if (!aligned_to(x, 2) || !aligned_to(bias_gate_up, 2) || !aligned_to(bias_down, 2) || !aligned_to(residual, 2) ||
+      !aligned_to(out, 2) || !aligned_to(ids, 4) || !aligned_to(weights, 4) || !aligned16(w_gate_up) ||
+      !aligned16(w_down))
+    return MXFP4_ERR_MISALIGNED;
+  const MoeWorkspace w = moe_workspace_layout(P, E, K, I, N, current_sm_count());
+  if (workspace == nullptr || workspace_bytes < w.total) return MXFP4_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return MXFP4_ERR_MISALIGNED;
+  DeviceInfo dev;
+  if ((st = device_ready(&dev)) != MXFP4_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const MoePlan plan = moe_plan_at(ws + w.plan, P, E);
+  cudaError_t e = launch_moe_plan(ids, static_cast<int>(P), E, plan, dev, s);
+  if (e == cudaSuccess) e = launch_moe_gather(x, ldx, T, top_k, K, plan, ws + w.a, nullptr, 0, 0, dev, s);
+  MoeGemmProblem p{};
+  p.a_blocks = ws + w.a;
+  p.w_packed = static_cast<const uint8_t*>(w_gate_up);
+  p.bias = bias_gate_up;
+  p.E = E;
+  p.N = 2 * I;
+  p.K = K;
+  p.h_blocks = ws + w.h;
+  p.act = static_cast<MoeAct>(act);
+  p.alpha = alpha;
+  p.limit = limit;
+  p.which = 0;
+  p.parts = reinterpret_cast<float*>(ws + w.parts);
+  if (e == cudaSuccess) e = launch_moe_gemm(p, plan, dev, s);
+  p.a_blocks = ws + w.h;
+  p.w_packed = static_cast<const uint8_t*>(w_down);
+  p.bias = bias_down;
+  p.N = N;
+  p.K = I;
+  p.h_blocks = nullptr;
+  p.out = ws + w.results;
+  p.ldo = w.ldp;
+  p.which = 1;
+  if (e == cudaSuccess) e = launch_moe_gemm(p, plan, dev, s);
+  if (e == cudaSuccess)
+    e = launch_moe_combine(ws + w.results, w.ldp, weights, plan, residual, ldr, out, ldo, T, top_k, N, dev, s);
+  return from_cuda(e);
+}
+
 mxfp4_status mxfp4_diag_set_wait_cycles(long long cycles) {
   if (cycles < 0) return MXFP4_ERR_INVALID_ARG;
   set_norm_wait_cycles(cycles);
@@ -518,7 +681,8 @@ mxfp4_status mxfp4_get_device_error(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MXFP4_ERR_CUDA;
   const uint32_t err = quant_read_clear_error() | gemm_read_clear_error() | decode_read_clear_error() |
                        bmm_read_clear_error() | norm_read_clear_error() | mla_store_read_clear_error() |
-                       mla_decode_read_clear_error() | mla_prefill_read_clear_error();
+                       mla_decode_read_clear_error() | mla_prefill_read_clear_error() |
+                       moe_plan_read_clear_error() | moe_gemm_read_clear_error();
   if (err & kErrTimeout) return MXFP4_ERR_TIMEOUT;
   return (err & kErrIndex) ? MXFP4_ERR_INDEX : MXFP4_OK;
 }

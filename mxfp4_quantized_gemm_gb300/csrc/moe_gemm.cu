@@ -1,0 +1,497 @@
+// Grouped W4A4 MXFP4 products of a mixture of experts on the sm_103a
+// block-scaled tensor cores.
+//
+//   y[r][n] = sum_k deq(A)[r][k] * deq(W[expert(r)])[n][k] + bias[expert(r)][n]
+//
+// for the rows r that the plan sorted by expert (row tiles of 128, each of
+// one expert), as
+//   rows:   out[pair(r)][n] = bf16_RNE(y), or
+//   gated:  columns are pairs (gate, up); h = act(gate, up) in fp32 is
+//           quantized per 1x32 (one rounding) into the blocked activations of
+//           the second product.
+//
+// Few tokens: the weights of the experts they reach are nearly all the bytes
+// and HBM is the bound.  Many: the tensor pipe's four MMAs and scale copies
+// per 256-wide k-step.  One kernel serves both, one CTA per SM: the ring, the
+// tile (128 activation rows x 256 weight rows) and the roles are those of
+// gemm.cu, and only the live rows of a row tile are loaded and stored.
+//
+// The number of tiles is known on the device only, so every CTA derives its
+// share from the plan (struct Walk): whole rounds of units of a few tiles of
+// one row tile, then what is left cut evenly along (tile, k-step) over all
+// CTAs.  A cut tile's parts go to memory in fp32; the CTA whose part arrives
+// last (a counter per tile) adds them in CTA order, so the sum does not
+// depend on who is last, and no CTA ever waits for another.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "gemm_common.cuh"
+#include "internal.h"
+#include "layout.cuh"
+#include "moe.h"
+#include "ptx.cuh"
+
+namespace mx {
+
+static __device__ uint32_t g_moe_gemm_error;
+
+namespace {
+
+using C = Cfg<128>;
+constexpr int kUnit = 4;                           // tiles of one row tile that a CTA takes in turn
+constexpr int kPartFloats = 128 * kTileN;          // one part of a cut tile
+constexpr int kMinSteps = 2;                       // k-steps a CTA takes at least where tiles are cut
+
+struct MoeArgs {
+  const uint8_t* a_blocks;
+  const uint8_t* w_packed;
+  size_t w_stride;                                 // bytes of one expert's packed weights
+  const uint16_t* bias;
+  int N, KT, n_tiles, unit;
+  uint16_t* out;
+  int64_t ldo;
+  uint8_t* h_blocks;
+  int KT2;
+  int act;
+  float alpha, limit;
+  const int32_t* hdr;
+  const int32_t* tile;
+  const int32_t* row_pair;
+  int32_t* tickets;
+  float* parts;
+};
+
+struct Segment {
+  int rt, nt, k0, len, left;   // row tile, column tile, k-steps; left: index among the cut tiles, or -1
+};
+
+// A CTA's share of the tiles, segment by segment; every role walks it alike.
+struct Walk {
+  int units_per_row, units, rounds, r, i;
+  int t0, its, parts_ctas, it, it1;
+
+  __device__ __forceinline__ void init(const MoeArgs& g, int row_tiles) {
+    const int G = gridDim.x, c = blockIdx.x;
+    units_per_row = (g.n_tiles + g.unit - 1) / g.unit;
+    units = row_tiles * units_per_row;
+    rounds = units / G;
+    const int rest = units - rounds * G;
+    r = 0;
+    i = 0;
+    it = it1 = its = 0;
+    t0 = 0;
+    parts_ctas = 1;
+    if (rest * 100 >= 92 * G) {                    // nearly a whole round: cutting it would cost more than it saves
+      ++rounds;
+    } else if (rest > 0) {
+      const int u0 = rounds * G;
+      t0 = (u0 / units_per_row) * g.n_tiles + (u0 % units_per_row) * g.unit;
+      its = (row_tiles * g.n_tiles - t0) * g.KT;
+      parts_ctas = its / kMinSteps < G ? its / kMinSteps : G;
+      if (parts_ctas < 1) parts_ctas = 1;
+      if (c < parts_ctas) {
+        it = sk_begin(c, its, parts_ctas);
+        it1 = sk_begin(c + 1, its, parts_ctas);
+      }
+    }
+  }
+
+  __device__ __forceinline__ bool next(const MoeArgs& g, Segment& s) {
+    if (r < rounds) {
+      const int u = r * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+      if (u < units) {
+        s.rt = u / units_per_row;
+        const int n0 = (u - s.rt * units_per_row) * g.unit;
+        s.nt = n0 + i;
+        s.k0 = 0;
+        s.len = g.KT;
+        s.left = -1;
+        if (++i == g.unit || s.nt + 1 == g.n_tiles) {
+          i = 0;
+          ++r;
+        }
+        return true;
+      }
+      r = rounds;
+    }
+    if (it >= it1) return false;
+    s.left = it / g.KT;
+    s.k0 = it - s.left * g.KT;
+    s.len = g.KT - s.k0 < it1 - it ? g.KT - s.k0 : it1 - it;
+    const int t = t0 + s.left;
+    s.rt = t / g.n_tiles;
+    s.nt = t - s.rt * g.n_tiles;
+    it += s.len;
+    return true;
+  }
+};
+
+__device__ __forceinline__ int loaded_rows(int live) { return (live + 15) & ~15; }
+
+__device__ __forceinline__ void epi_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+// One 1x32 block of fp32 values held by one thread: its 16 code bytes and,
+// the return value, its scale byte, by the rule of quant_math.cuh applied to
+// the fp32 values (no step through bf16).
+__device__ __forceinline__ uint32_t quantize32_f32(const float (&v)[32], uint4& codes) {
+  uint32_t am = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) am = max(am, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  const uint32_t ef = am >> 23;
+  const bool nonfinite = ef == 0xFF;
+  const uint32_t sbyte = nonfinite ? 0xFFu : (ef > 2 ? ef - 2 : 0u);
+  const float inv = __uint_as_float((254u - (nonfinite ? 0u : sbyte)) << 23);   // 2^(127 - sbyte)
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t d;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(d)
+        : "f"(v[8 * q] * inv), "f"(v[8 * q + 1] * inv), "f"(v[8 * q + 2] * inv), "f"(v[8 * q + 3] * inv),
+          "f"(v[8 * q + 4] * inv), "f"(v[8 * q + 5] * inv), "f"(v[8 * q + 6] * inv), "f"(v[8 * q + 7] * inv));
+    w[q] = nonfinite ? 0u : d;
+  }
+  codes = make_uint4(w[0], w[1], w[2], w[3]);
+  return sbyte;
+}
+
+__device__ __forceinline__ float gated(int act, float alpha, float limit, float gate, float up) {
+  if (act == static_cast<int>(MoeAct::kGeluTanh)) {
+    const float u = 0.7978845608028654f * fmaf(0.044715f * gate * gate, gate, gate);
+    // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u))
+    return __fdividef(gate, 1.f + __expf(-2.f * u)) * up;
+  }
+  if (act == static_cast<int>(MoeAct::kSwigluClamp)) {
+    gate = fminf(gate, limit);
+    up = fminf(fmaxf(up, -limit), limit);
+    return __fdividef(gate, 1.f + __expf(-alpha * gate)) * (up + 1.f);
+  }
+  return __fdividef(gate, 1.f + __expf(-gate)) * up;
+}
+
+// 128 columns of one row (acc), from column n0 of its expert: stored as
+// bf16, or gated and quantized.
+template <bool kGated>
+__device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, int expert, int rl, int h, uint32_t (&acc)[128]) {
+  const int n0 = s.nt * kTileN + h * 128;
+  const uint16_t* bias = g.bias != nullptr ? g.bias + static_cast<size_t>(expert) * g.N : nullptr;
+  if constexpr (!kGated) {
+    const int pair = __ldcg(g.row_pair + s.rt * kRowTile + rl);
+    OutView o{};
+    o.out = reinterpret_cast<__nv_bfloat16*>(g.out) + static_cast<int64_t>(pair) * g.ldo;
+    o.bias = reinterpret_cast<const __nv_bfloat16*>(bias);
+    o.N = g.N;
+#pragma unroll
+    for (int c0 = 0; c0 < 128; c0 += 32) {
+      float v[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(acc[c0 + c]);
+      store_chunk_bf16(o, 0, n0 + c0, v);
+    }
+  } else {
+    const int kt2 = s.nt >> 1, grp = s.nt & 1;
+    uint8_t* blk = g.h_blocks + (static_cast<size_t>(s.rt) * g.KT2 + kt2) * kMoeBlockBytes;
+    uint32_t scales = 0;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const int n = n0 + 64 * b + 2 * j;
+        float gate = __uint_as_float(acc[64 * b + 2 * j]), up = __uint_as_float(acc[64 * b + 2 * j + 1]);
+        if (bias != nullptr && n < g.N) {
+          gate += bf16_bits_to_float(__ldg(bias + n));
+          up += bf16_bits_to_float(__ldg(bias + n + 1));
+        }
+        // columns past N (a partial last tile) are zeros: their weights are
+        v[j] = n < g.N ? gated(g.act, g.alpha, g.limit, gate, up) : 0.f;
+      }
+      uint4 codes;
+      const uint32_t sb = n0 + 64 * b < g.N ? quantize32_f32(v, codes) : 0x7Fu;
+      if (n0 + 64 * b >= g.N) codes = make_uint4(0, 0, 0, 0);
+      scales |= sb << (8 * b);
+      const int chunk = grp * 4 + h * 2 + b;
+      *reinterpret_cast<uint4*>(blk + (rl << 7) + ((chunk ^ (rl & 7)) << 4)) = codes;
+    }
+    uint8_t* sc = blk + kTileBytes + ((rl & 31) << 4) + ((rl >> 5) << 2) + 2 * h;
+    *reinterpret_cast<uint16_t*>(sc + (grp << 9)) = static_cast<uint16_t>(scales);
+    // the last k-tile's second half has no columns: its weights are zero
+    // codes, and a scale of 1 keeps the product zero whatever is there
+    if (grp == 0 && s.nt + 1 == g.n_tiles) *reinterpret_cast<uint16_t*>(sc + kAtomBytes) = 0x7F7F;
+  }
+}
+
+template <bool kGated>
+__global__ void __launch_bounds__(kThreads, 1) moe_gemm_kernel(const __grid_constant__ MoeArgs g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRing);
+  uint64_t* empty = full + C::kStages;
+  uint64_t* acc_full = empty + C::kStages;
+  uint64_t* acc_empty = acc_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 1);
+  volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  bool abort = false;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, kEpiThreads);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // The plan is complete when this kernel starts: the kernel before it lets
+  // it start only after its own wait for the plan.  So the first weights are
+  // requested before the wait for the activations.
+  Walk walk;
+  walk.init(g, __ldcg(g.hdr));
+  Segment s;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- producer: a stage is the weight block of one k-step (one bulk
+      // copy) and the live activation rows' codes and scales
+      int i = 0;
+      bool waited = false;
+      const uint8_t* pend_a[C::kStages];
+      int pend_rows[C::kStages];
+      auto a_load = [&](int st, const uint8_t* blk, int rows) {
+        uint8_t* dst = smem + st * C::kStageBytes + C::kW;
+        if (rows == kRowTile) {
+          bulk_g2s(dst, blk, C::kALoad + C::kSA, &full[st]);
+        } else {
+          bulk_g2s(dst, blk, rows * 128, &full[st]);
+          bulk_g2s(dst + C::kA, blk + kTileBytes, C::kSA, &full[st]);
+        }
+      };
+      while (!abort && walk.next(g, s)) {
+        const int info = __ldcg(g.tile + s.rt);
+        const int rows = loaded_rows(info >> 16);
+        const uint8_t* w = g.w_packed + static_cast<size_t>(info & 0xFFFF) * g.w_stride +
+                           static_cast<size_t>(s.nt * g.KT + s.k0) * kWeightBlockBytes;
+        const uint8_t* a = g.a_blocks + (static_cast<size_t>(s.rt) * g.KT + s.k0) * kMoeBlockBytes;
+        for (int j = 0; j < s.len; ++j, ++i, w += kWeightBlockBytes, a += kMoeBlockBytes) {
+          const int st = i % C::kStages;
+          if (i >= C::kStages && !waited) {        // the ring is full of weights: now the activations
+            griddep_wait();
+            waited = true;
+#pragma unroll
+            for (int q = 0; q < C::kStages; ++q) a_load(q, pend_a[q], pend_rows[q]);
+          }
+          if (!mbar_wait(&empty[st], ((i / C::kStages) & 1) ^ 1, abort)) break;
+          mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(C::kW + rows * 128 + C::kSA));
+          bulk_g2s(smem + st * C::kStageBytes, w, kWeightBlockBytes, &full[st]);
+          if (waited) {
+            a_load(st, a, rows);
+          } else {
+#pragma unroll
+            for (int q = 0; q < C::kStages; ++q)
+              if (q == st) {
+                pend_a[q] = a;
+                pend_rows[q] = rows;
+              }
+          }
+        }
+      }
+      if (!waited) {
+        griddep_wait();
+#pragma unroll
+        for (int q = 0; q < C::kStages; ++q)
+          if (q < i) a_load(q, pend_a[q], pend_rows[q]);
+      }
+      if (abort) {   // the copies in flight land before the block may end
+        bool late = false;
+        for (int q = i < C::kStages ? 0 : i - C::kStages; q < i; ++q)
+          mbar_wait(&full[q % C::kStages], (q / C::kStages) & 1, late);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---- MMA issuer: one accumulator, one segment at a time; the
+      // activation scales of a row tile stay in TMEM across its column tiles
+      // where they fit (K <= 6144), as in gemm.cu.
+      constexpr uint32_t kSfaRes = C::kSfBase + C::kStages * 16u;
+      const bool resident = kSfaRes + 8u * static_cast<uint32_t>(g.KT) <= C::kTmemCols;
+      int cur_rt = -1;
+      uint32_t have = 0;
+      int i = 0;
+      for (int seg = 0; !abort && walk.next(g, s); ++seg) {
+        if (s.rt != cur_rt) {
+          cur_rt = s.rt;
+          have = 0;
+        }
+        for (int j = 0; j < s.len; ++j, ++i) {
+          const int st = i % C::kStages;
+          if (!mbar_wait(&full[st], (i / C::kStages) & 1, abort)) break;
+          tc_fence_after();
+          const uint32_t base = smem_u32(smem + st * C::kStageBytes);
+          const int k = s.k0 + j;
+          const uint32_t sfa_col = resident ? kSfaRes + 8u * k : C::kSfBase + st * C::kSfSlot;
+          const uint32_t sfb_col = resident ? C::kSfBase + 16u * st : sfa_col + C::kSfbOff;
+          issue_stage_scales_sfa<C>(tmem, base, sfb_col, sfa_col, !resident || ((have >> k) & 1u) == 0);
+          if (resident) have |= 1u << k;
+          if (j == 0) {
+            if (!mbar_wait(acc_empty, (seg & 1) ^ 1, abort)) break;
+            tc_fence_after();
+          }
+          issue_stage_mmas_sfa<C>(tmem, base, sfb_col, sfa_col, j != 0 ? 1u : 0u);
+          mma_commit(&empty[st]);
+        }
+        mma_commit(acc_full);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- epilogue: warp w drains accumulator rows 32 (w % 4).., columns 128 h..
+    griddep_wait();
+    griddep_launch_dependents();
+    const int q = warp & 3;
+    const int h = (warp - 2) >> 2;
+    const int rl = q * 32 + lane;
+    for (int seg = 0; walk.next(g, s); ++seg) {
+      const int info = __ldcg(g.tile + s.rt);
+      const int rows = info >> 16, expert = info & 0xFFFF;
+      const bool ok = mbar_wait(acc_full, seg & 1, abort);
+      tc_fence_after();
+      uint32_t r[128];
+      if (q * 32 < rows) {
+#pragma unroll
+        for (int c0 = 0; c0 < 128; c0 += 16)
+          tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + h * 128 + c0,
+                    *reinterpret_cast<uint32_t(*)[16]>(&r[c0]));
+        tmem_wait_ld();
+      }
+      tc_fence_before();
+      mbar_arrive(acc_empty);                     // accumulator free for the next segment
+      const bool live = rl < rows;
+      if (!ok) {
+#pragma unroll
+        for (int c = 0; c < 128; ++c) r[c] = 0u;
+      }
+      if (s.len == g.KT) {
+        if (live) finish<kGated>(g, s, expert, rl, h, r);
+        continue;
+      }
+      // A cut tile: this CTA's part to its slot, 16-byte groups of columns
+      // [h][group][row] so that a warp's lanes write side by side; the last
+      // of the tile's CTAs adds the parts in CTA order.
+      const int c_lo = sk_owner(s.left * g.KT, walk.its, walk.parts_ctas);
+      const int c_hi = sk_owner(s.left * g.KT + g.KT - 1, walk.its, walk.parts_ctas);
+      auto slot_of = [&](int c) {
+        const int second = sk_begin(c, walk.its, walk.parts_ctas) / g.KT == s.left ? 0 : 1;
+        return reinterpret_cast<uint4*>(g.parts + static_cast<size_t>(2 * c + second) * kPartFloats) + h * 32 * 128 + rl;
+      };
+      if (live) {
+        uint4* p = slot_of(blockIdx.x);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) __stcg(p + c * 128, make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]));
+      }
+      __threadfence();
+      epi_barrier();
+      if (threadIdx.x == 64) {
+        const int before = atomicAdd(g.tickets + s.left, 1);
+        __threadfence();
+        *last_flag = before == c_hi - c_lo;
+      }
+      epi_barrier();
+      const bool last = *last_flag != 0;
+      if (last && live) {
+        __threadfence();
+#pragma unroll
+        for (int c = 0; c < 128; ++c) r[c] = 0u;
+        for (int cc = c_lo; cc <= c_hi; ++cc) {
+          const uint4* p = slot_of(cc);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const uint4 v = __ldcg(p + c * 128);
+            r[4 * c] = __float_as_uint(__uint_as_float(r[4 * c]) + __uint_as_float(v.x));
+            r[4 * c + 1] = __float_as_uint(__uint_as_float(r[4 * c + 1]) + __uint_as_float(v.y));
+            r[4 * c + 2] = __float_as_uint(__uint_as_float(r[4 * c + 2]) + __uint_as_float(v.z));
+            r[4 * c + 3] = __float_as_uint(__uint_as_float(r[4 * c + 3]) + __uint_as_float(v.w));
+          }
+        }
+        finish<kGated>(g, s, expert, rl, h, r);
+      }
+      epi_barrier();                              // the flag may be written again
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+  if (abort) atomicOr(&g_moe_gemm_error, kErrTimeout);
+}
+
+std::atomic<bool> g_attr_set[64][2];
+
+template <bool kGated>
+cudaError_t launch(const MoeArgs& a, const DeviceInfo& dev, cudaStream_t s) {
+  if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
+  if (!g_attr_set[dev.device][kGated].load(std::memory_order_acquire)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(moe_gemm_kernel<kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    g_attr_set[dev.device][kGated].store(true, std::memory_order_release);
+  }
+  return launch_pdl(moe_gemm_kernel<kGated>, dev.sm_count, kThreads, C::kSmem, s, a);
+}
+
+}  // namespace
+
+size_t moe_gemm_parts_bytes(int sm_count) { return static_cast<size_t>(2) * sm_count * kPartFloats * sizeof(float); }
+
+cudaError_t launch_moe_gemm(const MoeGemmProblem& p, const MoePlan& plan, const DeviceInfo& dev, cudaStream_t s) {
+  MoeArgs a{};
+  a.a_blocks = p.a_blocks;
+  a.w_packed = p.w_packed;
+  a.w_stride = static_cast<size_t>(weight_packed_bytes(p.N, p.K));
+  a.bias = static_cast<const uint16_t*>(p.bias);
+  a.N = p.N;
+  a.KT = static_cast<int>(padded_k(p.K) / kKTile);
+  a.n_tiles = static_cast<int>(ceil_div(p.N, kTileN));
+  a.unit = a.n_tiles < kUnit ? a.n_tiles : kUnit;
+  a.out = static_cast<uint16_t*>(p.out);
+  a.ldo = p.ldo;
+  a.h_blocks = p.h_blocks;
+  a.KT2 = static_cast<int>(padded_k(p.N / 2) / kKTile);
+  a.act = static_cast<int>(p.act);
+  a.alpha = p.alpha;
+  a.limit = p.limit;
+  a.hdr = plan.hdr;
+  a.tile = plan.tile;
+  a.row_pair = plan.row_pair;
+  a.tickets = plan.tickets + p.which * kMoeTickets;
+  a.parts = p.parts;
+  return p.h_blocks != nullptr ? launch<true>(a, dev, s) : launch<false>(a, dev, s);
+}
+
+uint32_t moe_gemm_read_clear_error() {
+  uint32_t v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_moe_gemm_error, sizeof(v)) != cudaSuccess) return 0;
+  cudaMemcpyToSymbol(g_moe_gemm_error, &zero, sizeof(zero));
+  return v;
+}
+
+}  // namespace mx
