@@ -44,6 +44,18 @@ using C = Cfg<128>;
 constexpr int kUnit = 4;                           // tiles of one row tile that a CTA takes in turn
 constexpr int kPartFloats = 128 * kTileN;          // one part of a cut tile
 constexpr int kMinSteps = 2;                       // k-steps a CTA takes at least where tiles are cut
+// Warps 0..3: producer, MMA issuer and two that only make the first warpgroup
+// whole; warps 4..11: epilogue.  The epilogue holds 128 columns of a row in
+// registers: it takes over what the first warpgroup gives up (56 + 2 x 224 =
+// 3 x 168 registers, the launch's).  With 168 it spilled a kilobyte a thread.
+constexpr int kMoeThreads = 384;
+constexpr int kFirstEpiWarp = 4;
+// Staging of the bf16 rows: per epilogue warp 32 rows x 32 columns, rows 80
+// bytes apart (the 16-byte accesses of 8 lanes then meet 8 different banks).
+constexpr int kStagePitch = 80;
+constexpr int kStageWarp = 32 * kStagePitch;
+constexpr int kMoeSmem = C::kSmem + 8 * kStageWarp;
+static_assert(kMoeSmem <= kMaxSmem, "ring and staging exceed shared memory");
 
 struct MoeArgs {
   const uint8_t* a_blocks;
@@ -53,6 +65,7 @@ struct MoeArgs {
   int N, KT, n_tiles, unit;
   uint16_t* out;
   int64_t ldo;
+  int out_vec;                                     // rows of out allow 16-byte accesses
   uint8_t* h_blocks;
   int KT2;
   int act;
@@ -133,6 +146,50 @@ __device__ __forceinline__ int loaded_rows(int live) { return (live + 15) & ~15;
 
 __device__ __forceinline__ void epi_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
+// Place of the part of cut tile `left` that CTA c leaves (each CTA's range cuts
+// at most two tiles).
+__device__ __forceinline__ int part_slot(const Walk& w, int KT, int left, int c) {
+  return 2 * c + (sk_begin(c, w.its, w.parts_ctas) / KT == left ? 0 : 1);
+}
+
+// Where 8 columns (group c8 of 32) of a row stand in a part: 1 KiB per row,
+// the groups rotated by the row, so that a warp's lanes hit different L2
+// slices both when they hold the same group of 32 rows (the writer: with
+// rows at the same place the stores took ten times as long) and when they
+// hold the groups of one row (the reader, 1 KiB side by side).
+__device__ __forceinline__ int part_at(int row, int c8) { return row * kTileN + ((c8 ^ row) & 31) * 8; }
+// 32 bytes at once, cached in L2 only.
+__device__ __forceinline__ void stg_32B(float* p, const uint32_t* r) {
+  asm volatile("st.global.cg.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void ldg_32B(const float* p, float (&v)[8]) {
+  asm volatile("ld.global.cg.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+               : "l"(p));
+}
+
+// E8M0 byte of a block whose largest magnitude has fp32 bits `am`, by the rule
+// of quant_math.cuh, and the multiplier 2^(127 - byte) of its values.
+__device__ __forceinline__ uint32_t scale_byte_f32(uint32_t am, float& inv) {
+  const uint32_t ef = am >> 23;
+  const uint32_t sbyte = ef == 0xFF ? 0xFFu : (ef > 2 ? ef - 2 : 0u);
+  inv = __uint_as_float((254u - (ef == 0xFF ? 0u : sbyte)) << 23);
+  return sbyte;
+}
+// Codes of 4 scaled values, 2 bytes, the first in the lowest nibble.
+__device__ __forceinline__ uint32_t e2m1_codes4_f32(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "mov.b32 %0, {b0, b1, 0, 0};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
 // One 1x32 block of fp32 values held by one thread: its 16 code bytes and,
 // the return value, its scale byte, by the rule of quant_math.cuh applied to
 // the fp32 values (no step through bf16).
@@ -140,10 +197,9 @@ __device__ __forceinline__ uint32_t quantize32_f32(const float (&v)[32], uint4& 
   uint32_t am = 0;
 #pragma unroll
   for (int i = 0; i < 32; ++i) am = max(am, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  const uint32_t ef = am >> 23;
-  const bool nonfinite = ef == 0xFF;
-  const uint32_t sbyte = nonfinite ? 0xFFu : (ef > 2 ? ef - 2 : 0u);
-  const float inv = __uint_as_float((254u - (nonfinite ? 0u : sbyte)) << 23);   // 2^(127 - sbyte)
+  float inv;
+  const uint32_t sbyte = scale_byte_f32(am, inv);
+  const bool nonfinite = sbyte == 0xFFu;
   uint32_t w[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -177,26 +233,57 @@ __device__ __forceinline__ float gated(int act, float alpha, float limit, float 
   return __fdividef(gate, 1.f + __expf(-gate)) * up;
 }
 
-// 128 columns of one row (acc), from column n0 of its expert: stored as
-// bf16, or gated and quantized.
+// 128 columns of one row (acc), from column n0 of its expert: stored as bf16,
+// or gated and quantized.  Rows of bf16 go through the warp's staging area, 32
+// columns at a time, so that four lanes write 64 neighbouring bytes of a row
+// (written by the lane that holds the row, 16 bytes apart by a whole row, they
+// took twice as long).  All 32 lanes call this together.
 template <bool kGated>
-__device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, int expert, int rl, int h, uint32_t (&acc)[128]) {
+__device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, int expert, int rows, int rl, int h, int lane,
+                                       uint8_t* stage, uint32_t (&acc)[128]) {
   const int n0 = s.nt * kTileN + h * 128;
   const uint16_t* bias = g.bias != nullptr ? g.bias + static_cast<size_t>(expert) * g.N : nullptr;
   if constexpr (!kGated) {
-    const int pair = __ldcg(g.row_pair + s.rt * kRowTile + rl);
-    OutView o{};
-    o.out = reinterpret_cast<__nv_bfloat16*>(g.out) + static_cast<int64_t>(pair) * g.ldo;
-    o.bias = reinterpret_cast<const __nv_bfloat16*>(bias);
-    o.N = g.N;
+    const int pair = rl < rows ? __ldcg(g.row_pair + s.rt * kRowTile + rl) : -1;
+    const bool vec = g.out_vec != 0;
+    int pairs[4];                                  // of the rows this lane writes: lane / 4 + 8 i
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pairs[i] = __shfl_sync(0xFFFFFFFFu, pair, (lane >> 2) + 8 * i);
 #pragma unroll
     for (int c0 = 0; c0 < 128; c0 += 32) {
-      float v[32];
+      if (n0 + c0 >= g.N) break;                   // uniform
 #pragma unroll
-      for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(acc[c0 + c]);
-      store_chunk_bf16(o, 0, n0 + c0, v);
+      for (int c = 0; c < 32; c += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] = __uint_as_float(acc[c0 + c + i]);
+          if (bias != nullptr && n0 + c0 + c + i < g.N) v[i] += bf16_bits_to_float(__ldg(bias + n0 + c0 + c + i));
+        }
+        *reinterpret_cast<uint4*>(stage + lane * kStagePitch + 2 * c) =
+            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+      }
+      __syncwarp();
+      const int n = n0 + c0 + 8 * (lane & 3);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (pairs[i] < 0 || n >= g.N) continue;
+        const uint8_t* src = stage + ((lane >> 2) + 8 * i) * kStagePitch + 16 * (lane & 3);
+        const uint4 w = *reinterpret_cast<const uint4*>(src);
+        uint16_t* dst = g.out + static_cast<int64_t>(pairs[i]) * g.ldo + n;
+        if (vec && n + 8 <= g.N) {
+          *reinterpret_cast<uint4*>(dst) = w;
+        } else {
+          const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < g.N) dst[e] = static_cast<uint16_t>(q[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+      __syncwarp();
     }
   } else {
+    if (rl >= rows) return;
     const int kt2 = s.nt >> 1, grp = s.nt & 1;
     uint8_t* blk = g.h_blocks + (static_cast<size_t>(s.rt) * g.KT2 + kt2) * kMoeBlockBytes;
     uint32_t scales = 0;
@@ -229,8 +316,107 @@ __device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, int e
   }
 }
 
+// The sum of a cut tile's parts in CTA order, by all epilogue warps: a warp
+// takes a row, a lane 8 columns of it (32 bytes of each part: a whole sector),
+// so that the loads of a row's parts are in flight together and the row is
+// stored by neighbouring lanes.  A gated row's 1x32 blocks are 8 lanes each.
 template <bool kGated>
-__global__ void __launch_bounds__(kThreads, 1) moe_gemm_kernel(const __grid_constant__ MoeArgs g) {
+__device__ __forceinline__ void finish_cut(const MoeArgs& g, const Walk& walk, const Segment& s, int expert, int rows,
+                                           int warp, int lane) {
+  const int c_lo = sk_owner(s.left * g.KT, walk.its, walk.parts_ctas);
+  const int c_hi = sk_owner(s.left * g.KT + g.KT - 1, walk.its, walk.parts_ctas);
+  const int n0 = s.nt * kTileN + 8 * lane;
+  const uint16_t* bias = g.bias != nullptr ? g.bias + static_cast<size_t>(expert) * g.N : nullptr;
+  float b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = bias != nullptr && n0 + i < g.N ? bf16_bits_to_float(__ldg(bias + n0 + i)) : 0.f;
+  constexpr int kRows = 4, kAhead = 2;
+  const int count = c_hi - c_lo + 1;
+  // lane l: where the part of contributor l (of each 32) stands
+  auto place = [&](int first) { return first + lane < count ? part_slot(walk, g.KT, s.left, c_lo + first + lane) : 0; };
+  const int place0 = place(0);
+  for (int row0 = warp; row0 < rows; row0 += 8 * kRows) {
+    float acc[kRows][8];
+    int pair[kRows];
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[q][i] = 0.f;
+      pair[q] = !kGated && row0 + 8 * q < rows ? __ldcg(g.row_pair + s.rt * kRowTile + row0 + 8 * q) : 0;
+    }
+    for (int c = 0; c < count; c += kAhead) {
+      float v[kAhead][kRows][8];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        int slot = __shfl_sync(0xFFFFFFFFu, place0, (c + a) & 31);
+        if (c + a >= 32 && c + a < count) slot = part_slot(walk, g.KT, s.left, c_lo + c + a);
+        const float* p = g.parts + static_cast<size_t>(slot) * kPartFloats;
+#pragma unroll
+        for (int q = 0; q < kRows; ++q) {
+          const int row = row0 + 8 * q;
+          if (c + a < count && row < rows) {
+            ldg_32B(p + part_at(row, lane), v[a][q]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[a][q][i] = 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+        for (int q = 0; q < kRows; ++q)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[q][i] += v[a][q][i];
+    }
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+      const int row = row0 + 8 * q;
+      if (row >= rows) break;                     // warp-uniform
+      if (bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[q][i] += b[i];
+      }
+      if constexpr (!kGated) {
+        uint16_t* dst = g.out + static_cast<int64_t>(pair[q]) * g.ldo + n0;
+        if (g.out_vec != 0 && n0 + 8 <= g.N) {
+          *reinterpret_cast<uint4*>(dst) =
+              make_uint4(pack_bf16x2(acc[q][0], acc[q][1]), pack_bf16x2(acc[q][2], acc[q][3]),
+                         pack_bf16x2(acc[q][4], acc[q][5]), pack_bf16x2(acc[q][6], acc[q][7]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (n0 + i < g.N) dst[i] = static_cast<uint16_t>(pack_bf16x2(acc[q][i], 0.f));
+        }
+      } else {
+        float h[4];
+        uint32_t am = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          h[i] = n0 + 2 * i < g.N ? gated(g.act, g.alpha, g.limit, acc[q][2 * i], acc[q][2 * i + 1]) : 0.f;
+          am = max(am, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+        }
+        am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+        am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+        am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 4));
+        float inv;
+        const uint32_t sbyte = scale_byte_f32(am, inv);
+        const uint32_t codes = sbyte == 0xFFu ? 0u : e2m1_codes4_f32(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
+        const int grp = s.nt & 1, chunk = grp * 4 + (lane >> 3);
+        uint8_t* blk = g.h_blocks + (static_cast<size_t>(s.rt) * g.KT2 + (s.nt >> 1)) * kMoeBlockBytes;
+        *reinterpret_cast<uint16_t*>(blk + (row << 7) + ((chunk ^ (row & 7)) << 4) + 2 * (lane & 7)) =
+            static_cast<uint16_t>(codes);
+        uint8_t* sc = blk + kTileBytes + ((row & 31) << 4) + ((row >> 5) << 2);
+        // (a block past the last column is zeros: scale 1, as padding has)
+        if ((lane & 7) == 0) sc[(grp << 9) + (lane >> 3)] = n0 < g.N ? static_cast<uint8_t>(sbyte) : static_cast<uint8_t>(0x7F);
+        if (lane == 0 && grp == 0 && s.nt + 1 == g.n_tiles) *reinterpret_cast<uint32_t*>(sc + kAtomBytes) = 0x7F7F7F7Fu;
+      }
+    }
+  }
+}
+
+template <bool kGated>
+__global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_constant__ MoeArgs g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kRing);
@@ -239,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_gemm_kernel(const __grid_cons
   uint64_t* acc_empty = acc_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 1);
   volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint8_t* staging = smem + C::kRing + 512;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   bool abort = false;
@@ -267,7 +454,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_gemm_kernel(const __grid_cons
   walk.init(g, __ldcg(g.hdr));
   Segment s;
 
-  if (warp == 0) {
+  if (warp < kFirstEpiWarp) {
+   asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+   if (warp == 0) {
     if (lane == 0) {
       // ---- producer: a stage is the weight block of one k-step (one bulk
       // copy) and the live activation rows' codes and scales
@@ -362,13 +551,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_gemm_kernel(const __grid_cons
       }
     }
     __syncwarp();
+   }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // ---- epilogue: warp w drains accumulator rows 32 (w % 4).., columns 128 h..
     griddep_wait();
     griddep_launch_dependents();
     const int q = warp & 3;
-    const int h = (warp - 2) >> 2;
+    const int h = (warp - kFirstEpiWarp) >> 2;
     const int rl = q * 32 + lane;
+    uint8_t* stage = staging + (warp - kFirstEpiWarp) * kStageWarp;
     for (int seg = 0; walk.next(g, s); ++seg) {
       const int info = __ldcg(g.tile + s.rt);
       const int rows = info >> 16, expert = info & 0xFFFF;
@@ -390,48 +582,29 @@ __global__ void __launch_bounds__(kThreads, 1) moe_gemm_kernel(const __grid_cons
         for (int c = 0; c < 128; ++c) r[c] = 0u;
       }
       if (s.len == g.KT) {
-        if (live) finish<kGated>(g, s, expert, rl, h, r);
+        if (q * 32 < rows) finish<kGated>(g, s, expert, rows, rl, h, lane, stage, r);
         continue;
       }
-      // A cut tile: this CTA's part to its slot, 16-byte groups of columns
-      // [h][group][row] so that a warp's lanes write side by side; the last
-      // of the tile's CTAs adds the parts in CTA order.
-      const int c_lo = sk_owner(s.left * g.KT, walk.its, walk.parts_ctas);
-      const int c_hi = sk_owner(s.left * g.KT + g.KT - 1, walk.its, walk.parts_ctas);
-      auto slot_of = [&](int c) {
-        const int second = sk_begin(c, walk.its, walk.parts_ctas) / g.KT == s.left ? 0 : 1;
-        return reinterpret_cast<uint4*>(g.parts + static_cast<size_t>(2 * c + second) * kPartFloats) + h * 32 * 128 + rl;
-      };
+      // A cut tile: this CTA's part to its slot; the last of the tile's CTAs
+      // adds the parts.
       if (live) {
-        uint4* p = slot_of(blockIdx.x);
+        float* p = g.parts + static_cast<size_t>(part_slot(walk, g.KT, s.left, blockIdx.x)) * kPartFloats;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) __stcg(p + c * 128, make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]));
+        for (int c = 0; c < 16; ++c) stg_32B(p + part_at(rl, h * 16 + c), &r[8 * c]);
       }
       __threadfence();
       epi_barrier();
-      if (threadIdx.x == 64) {
+      if (threadIdx.x == kFirstEpiWarp * 32) {
+        const int others = sk_owner(s.left * g.KT + g.KT - 1, walk.its, walk.parts_ctas) -
+                           sk_owner(s.left * g.KT, walk.its, walk.parts_ctas);
         const int before = atomicAdd(g.tickets + s.left, 1);
         __threadfence();
-        *last_flag = before == c_hi - c_lo;
+        *last_flag = before == others;
       }
       epi_barrier();
-      const bool last = *last_flag != 0;
-      if (last && live) {
+      if (*last_flag != 0) {
         __threadfence();
-#pragma unroll
-        for (int c = 0; c < 128; ++c) r[c] = 0u;
-        for (int cc = c_lo; cc <= c_hi; ++cc) {
-          const uint4* p = slot_of(cc);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const uint4 v = __ldcg(p + c * 128);
-            r[4 * c] = __float_as_uint(__uint_as_float(r[4 * c]) + __uint_as_float(v.x));
-            r[4 * c + 1] = __float_as_uint(__uint_as_float(r[4 * c + 1]) + __uint_as_float(v.y));
-            r[4 * c + 2] = __float_as_uint(__uint_as_float(r[4 * c + 2]) + __uint_as_float(v.z));
-            r[4 * c + 3] = __float_as_uint(__uint_as_float(r[4 * c + 3]) + __uint_as_float(v.w));
-          }
-        }
-        finish<kGated>(g, s, expert, rl, h, r);
+        finish_cut<kGated>(g, walk, s, expert, rows, warp - kFirstEpiWarp, lane);
       }
       epi_barrier();                              // the flag may be written again
     }
@@ -451,11 +624,11 @@ cudaError_t launch(const MoeArgs& a, const DeviceInfo& dev, cudaStream_t s) {
   if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
   if (!g_attr_set[dev.device][kGated].load(std::memory_order_acquire)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(moe_gemm_kernel<kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        cudaFuncSetAttribute(moe_gemm_kernel<kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoeSmem);
     if (e != cudaSuccess) return e;
     g_attr_set[dev.device][kGated].store(true, std::memory_order_release);
   }
-  return launch_pdl(moe_gemm_kernel<kGated>, dev.sm_count, kThreads, C::kSmem, s, a);
+  return launch_pdl(moe_gemm_kernel<kGated>, dev.sm_count, kMoeThreads, kMoeSmem, s, a);
 }
 
 }  // namespace
@@ -474,6 +647,7 @@ cudaError_t launch_moe_gemm(const MoeGemmProblem& p, const MoePlan& plan, const 
   a.unit = a.n_tiles < kUnit ? a.n_tiles : kUnit;
   a.out = static_cast<uint16_t*>(p.out);
   a.ldo = p.ldo;
+  a.out_vec = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.ldo % 8 == 0;
   a.h_blocks = p.h_blocks;
   a.KT2 = static_cast<int>(padded_k(p.N / 2) / kKTile);
   a.act = static_cast<int>(p.act);
