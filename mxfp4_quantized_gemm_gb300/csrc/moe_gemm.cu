@@ -44,6 +44,8 @@ using C = Cfg<128>;
 constexpr int kUnit = 4;                           // tiles of one row tile that a CTA takes in turn
 constexpr int kPartFloats = 128 * kTileN;          // one part of a cut tile
 constexpr int kMinSteps = 2;                       // k-steps a CTA takes at least where tiles are cut
+constexpr int kCutSteps = 12;                      // what cutting costs, in k-steps (see Walk)
+constexpr int kFewRows = 32;                       // rows up to which a tile is finished row by row
 // Warps 0..3: producer, MMA issuer and two that only make the first warpgroup
 // whole; warps 4..11: epilogue.  The epilogue holds 128 columns of a row in
 // registers: it takes over what the first warpgroup gives up (56 + 2 x 224 =
@@ -78,65 +80,95 @@ struct MoeArgs {
 };
 
 struct Segment {
-  int rt, nt, k0, len, left;   // row tile, column tile, k-steps; left: index among the cut tiles, or -1
+  int rt, nt;    // row tile, column tile
+  int half;      // 0, 1: that half of the column tile; -1: all of it
+  int k0, len;   // k-steps
+  int left;      // index among the cut tiles, or -1
 };
 
 // A CTA's share of the tiles, segment by segment; every role walks it alike.
+//  1. whole rounds of units: `unit` neighbouring tiles of one row tile, whose
+//     activations (and their scales in TMEM) serve them all;
+//  2. whole rounds of single tiles;
+//  3. the fewer than G tiles left: each on a CTA of its own, or as halves on
+//     two, or cut evenly along (tile, k-step) over all CTAs, whichever takes
+//     the fewest k-steps, with kCutSteps for the cut's sums (measured: 5 to 7
+//     us from a cut tile's last product to its result; a k-step takes 0.5).
 struct Walk {
-  int units_per_row, units, rounds, r, i;
-  int t0, its, parts_ctas, it, it1;
+  int units_per_row, unit_end, u, i;   // units: this CTA's next, tile of it
+  int t_end, t;                        // single tiles: this CTA's next
+  int h_end, h;                        // halves (two per tile from t_end)
+  int its, parts_ctas, it, it1;        // cut tiles from t_end
 
   __device__ __forceinline__ void init(const MoeArgs& g, int row_tiles) {
     const int G = gridDim.x, c = blockIdx.x;
     units_per_row = (g.n_tiles + g.unit - 1) / g.unit;
-    units = row_tiles * units_per_row;
-    rounds = units / G;
-    const int rest = units - rounds * G;
-    r = 0;
+    const int rounds = row_tiles * units_per_row / G;
+    unit_end = rounds * G;
+    u = c;
     i = 0;
-    it = it1 = its = 0;
-    t0 = 0;
+    const int t0 = (unit_end / units_per_row) * g.n_tiles + (unit_end % units_per_row) * g.unit;
+    const int tiles = row_tiles * g.n_tiles;
+    const int singles = (tiles - t0) / G;
+    t = t0 + c;
+    t_end = t0 + singles * G;
+    const int rest = tiles - t_end;
+    h = h_end = its = it = it1 = 0;
     parts_ctas = 1;
-    if (rest * 100 >= 92 * G) {                    // nearly a whole round: cutting it would cost more than it saves
-      ++rounds;
-    } else if (rest > 0) {
-      const int u0 = rounds * G;
-      t0 = (u0 / units_per_row) * g.n_tiles + (u0 % units_per_row) * g.unit;
-      its = (row_tiles * g.n_tiles - t0) * g.KT;
+    if (rest == 0) return;
+    const int whole = 2 * rest > G ? g.KT : (g.KT + 1) / 2;
+    if (static_cast<long long>(rest) * g.KT / G + kCutSteps < whole) {
+      its = rest * g.KT;
       parts_ctas = its / kMinSteps < G ? its / kMinSteps : G;
       if (parts_ctas < 1) parts_ctas = 1;
       if (c < parts_ctas) {
         it = sk_begin(c, its, parts_ctas);
         it1 = sk_begin(c + 1, its, parts_ctas);
       }
+    } else if (2 * rest > G) {
+      t_end = tiles;
+    } else {
+      h = c;
+      h_end = 2 * rest;
     }
   }
 
+  __device__ __forceinline__ void place(const MoeArgs& g, int tile, Segment& s) {
+    s.rt = tile / g.n_tiles;
+    s.nt = tile - s.rt * g.n_tiles;
+    s.half = -1;
+    s.k0 = 0;
+    s.len = g.KT;
+    s.left = -1;
+  }
+
   __device__ __forceinline__ bool next(const MoeArgs& g, Segment& s) {
-    if (r < rounds) {
-      const int u = r * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-      if (u < units) {
-        s.rt = u / units_per_row;
-        const int n0 = (u - s.rt * units_per_row) * g.unit;
-        s.nt = n0 + i;
-        s.k0 = 0;
-        s.len = g.KT;
-        s.left = -1;
-        if (++i == g.unit || s.nt + 1 == g.n_tiles) {
-          i = 0;
-          ++r;
-        }
-        return true;
+    if (u < unit_end) {
+      const int rt = u / units_per_row, n0 = (u - rt * units_per_row) * g.unit;
+      place(g, rt * g.n_tiles + n0 + i, s);
+      if (++i == g.unit || s.nt + 1 == g.n_tiles) {
+        i = 0;
+        u += gridDim.x;
       }
-      r = rounds;
+      return true;
+    }
+    if (t < t_end) {
+      place(g, t, s);
+      t += gridDim.x;
+      return true;
+    }
+    if (h < h_end) {
+      place(g, t_end + (h >> 1), s);
+      s.half = h & 1;
+      h += gridDim.x;
+      return true;
     }
     if (it >= it1) return false;
-    s.left = it / g.KT;
-    s.k0 = it - s.left * g.KT;
+    const int left = it / g.KT;
+    place(g, t_end + left, s);
+    s.left = left;
+    s.k0 = it - left * g.KT;
     s.len = g.KT - s.k0 < it1 - it ? g.KT - s.k0 : it1 - it;
-    const int t = t0 + s.left;
-    s.rt = t / g.n_tiles;
-    s.nt = t - s.rt * g.n_tiles;
     it += s.len;
     return true;
   }
@@ -241,6 +273,10 @@ __device__ __forceinline__ float gated(int act, float alpha, float limit, float 
 template <bool kGated>
 __device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, int expert, int rows, int rl, int h, int lane,
                                        uint8_t* stage, uint32_t (&acc)[128]) {
+  if (s.half >= 0) {
+    if (h != 0) return;                            // half a tile is in the first 128 columns
+    h = s.half;
+  }
   const int n0 = s.nt * kTileN + h * 128;
   const uint16_t* bias = g.bias != nullptr ? g.bias + static_cast<size_t>(expert) * g.N : nullptr;
   if constexpr (!kGated) {
@@ -316,25 +352,74 @@ __device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, int e
   }
 }
 
+// One row of a tile, 8 columns per lane (group c8 of the tile's 32, where `on`):
+// + bias, stored as bf16 by neighbouring lanes, or gated and quantized, 8
+// lanes per 1x32 block.  All 32 lanes call this together.
+template <bool kGated>
+__device__ __forceinline__ void finish_row(const MoeArgs& g, const Segment& s, int row, int pair, int c8, bool on,
+                                           const float (&b)[8], float (&v)[8]) {
+  const int n0 = s.nt * kTileN + 8 * c8;
+  if (g.bias != nullptr) {                         // (no + 0 without one: -0 stays)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += b[i];
+  }
+  if constexpr (!kGated) {
+    if (!on || n0 >= g.N) return;
+    uint16_t* dst = g.out + static_cast<int64_t>(pair) * g.ldo + n0;
+    if (g.out_vec != 0 && n0 + 8 <= g.N) {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (n0 + i < g.N) dst[i] = static_cast<uint16_t>(pack_bf16x2(v[i], 0.f));
+    }
+  } else {
+    float h[4];
+    uint32_t am = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      h[i] = n0 + 2 * i < g.N ? gated(g.act, g.alpha, g.limit, v[2 * i], v[2 * i + 1]) : 0.f;
+      am = max(am, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+    }
+    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 4));
+    if (!on) return;
+    float inv;
+    const uint32_t sbyte = scale_byte_f32(am, inv);
+    const uint32_t codes = sbyte == 0xFFu ? 0u : e2m1_codes4_f32(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
+    const int grp = s.nt & 1, chunk = grp * 4 + (c8 >> 3);
+    uint8_t* blk = g.h_blocks + (static_cast<size_t>(s.rt) * g.KT2 + (s.nt >> 1)) * kMoeBlockBytes;
+    *reinterpret_cast<uint16_t*>(blk + (row << 7) + ((chunk ^ (row & 7)) << 4) + 2 * (c8 & 7)) =
+        static_cast<uint16_t>(codes);
+    uint8_t* sc = blk + kTileBytes + ((row & 31) << 4) + ((row >> 5) << 2);
+    // (a block past the last column is zeros: scale 1, as padding has)
+    if ((c8 & 7) == 0) sc[(grp << 9) + (c8 >> 3)] = n0 < g.N ? static_cast<uint8_t>(sbyte) : static_cast<uint8_t>(0x7F);
+    if (c8 == 0 && grp == 0 && s.nt + 1 == g.n_tiles) *reinterpret_cast<uint32_t*>(sc + kAtomBytes) = 0x7F7F7F7Fu;
+  }
+}
+
+__device__ __forceinline__ void load_bias8(const MoeArgs& g, const Segment& s, int expert, int c8, float (&b)[8]) {
+  const int n0 = s.nt * kTileN + 8 * c8;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    b[i] = g.bias != nullptr && n0 + i < g.N
+               ? bf16_bits_to_float(__ldg(g.bias + static_cast<size_t>(expert) * g.N + n0 + i)) : 0.f;
+}
+
 // The sum of a cut tile's parts in CTA order, by all epilogue warps: a warp
 // takes a row, a lane 8 columns of it (32 bytes of each part: a whole sector),
-// so that the loads of a row's parts are in flight together and the row is
-// stored by neighbouring lanes.  A gated row's 1x32 blocks are 8 lanes each.
+// so that the loads of several rows and parts are in flight together.
 template <bool kGated>
 __device__ __forceinline__ void finish_cut(const MoeArgs& g, const Walk& walk, const Segment& s, int expert, int rows,
-                                           int warp, int lane) {
-  const int c_lo = sk_owner(s.left * g.KT, walk.its, walk.parts_ctas);
-  const int c_hi = sk_owner(s.left * g.KT + g.KT - 1, walk.its, walk.parts_ctas);
-  const int n0 = s.nt * kTileN + 8 * lane;
-  const uint16_t* bias = g.bias != nullptr ? g.bias + static_cast<size_t>(expert) * g.N : nullptr;
+                                           int c_lo, int c_hi, int warp, int lane) {
   float b[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = bias != nullptr && n0 + i < g.N ? bf16_bits_to_float(__ldg(bias + n0 + i)) : 0.f;
+  load_bias8(g, s, expert, lane, b);
   constexpr int kRows = 4, kAhead = 2;
   const int count = c_hi - c_lo + 1;
-  // lane l: where the part of contributor l (of each 32) stands
-  auto place = [&](int first) { return first + lane < count ? part_slot(walk, g.KT, s.left, c_lo + first + lane) : 0; };
-  const int place0 = place(0);
+  // lane l: where the part of contributor l stands
+  const int place0 = lane < count ? part_slot(walk, g.KT, s.left, c_lo + lane) : 0;
   for (int row0 = warp; row0 < rows; row0 += 8 * kRows) {
     float acc[kRows][8];
     int pair[kRows];
@@ -370,49 +455,31 @@ __device__ __forceinline__ void finish_cut(const MoeArgs& g, const Walk& walk, c
           for (int i = 0; i < 8; ++i) acc[q][i] += v[a][q][i];
     }
 #pragma unroll
-    for (int q = 0; q < kRows; ++q) {
-      const int row = row0 + 8 * q;
-      if (row >= rows) break;                     // warp-uniform
-      if (bias != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[q][i] += b[i];
-      }
-      if constexpr (!kGated) {
-        uint16_t* dst = g.out + static_cast<int64_t>(pair[q]) * g.ldo + n0;
-        if (g.out_vec != 0 && n0 + 8 <= g.N) {
-          *reinterpret_cast<uint4*>(dst) =
-              make_uint4(pack_bf16x2(acc[q][0], acc[q][1]), pack_bf16x2(acc[q][2], acc[q][3]),
-                         pack_bf16x2(acc[q][4], acc[q][5]), pack_bf16x2(acc[q][6], acc[q][7]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (n0 + i < g.N) dst[i] = static_cast<uint16_t>(pack_bf16x2(acc[q][i], 0.f));
-        }
-      } else {
-        float h[4];
-        uint32_t am = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          h[i] = n0 + 2 * i < g.N ? gated(g.act, g.alpha, g.limit, acc[q][2 * i], acc[q][2 * i + 1]) : 0.f;
-          am = max(am, __float_as_uint(h[i]) & 0x7FFFFFFFu);
-        }
-        am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-        am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-        am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 4));
-        float inv;
-        const uint32_t sbyte = scale_byte_f32(am, inv);
-        const uint32_t codes = sbyte == 0xFFu ? 0u : e2m1_codes4_f32(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv);
-        const int grp = s.nt & 1, chunk = grp * 4 + (lane >> 3);
-        uint8_t* blk = g.h_blocks + (static_cast<size_t>(s.rt) * g.KT2 + (s.nt >> 1)) * kMoeBlockBytes;
-        *reinterpret_cast<uint16_t*>(blk + (row << 7) + ((chunk ^ (row & 7)) << 4) + 2 * (lane & 7)) =
-            static_cast<uint16_t>(codes);
-        uint8_t* sc = blk + kTileBytes + ((row & 31) << 4) + ((row >> 5) << 2);
-        // (a block past the last column is zeros: scale 1, as padding has)
-        if ((lane & 7) == 0) sc[(grp << 9) + (lane >> 3)] = n0 < g.N ? static_cast<uint8_t>(sbyte) : static_cast<uint8_t>(0x7F);
-        if (lane == 0 && grp == 0 && s.nt + 1 == g.n_tiles) *reinterpret_cast<uint32_t*>(sc + kAtomBytes) = 0x7F7F7F7Fu;
-      }
-    }
+    for (int q = 0; q < kRows; ++q)
+      if (row0 + 8 * q < rows) finish_row<kGated>(g, s, row0 + 8 * q, pair[q], lane, true, b, acc[q]);   // (uniform)
   }
+}
+
+// The scale copies and MMAs of a stage that holds half a weight block (128
+// rows: a code tile, then its two scale atoms), as issue_stage_*_sfa.
+constexpr int kHalfScales = 2 * kTileBytes;        // offset of the half's atoms in the stage
+__device__ __forceinline__ void issue_half_scales(uint32_t tmem, uint32_t stage, uint32_t sfb_col, uint32_t sfa_col,
+                                                  bool copy_a) {
+  const uint32_t sw_s = stage + kHalfScales, sa_s = stage + C::kW + C::kA;
+  if (copy_a) {
+    tmem_cp_scales(tmem + sfa_col + 0, sdesc_scales(sa_s));
+    tmem_cp_scales(tmem + sfa_col + 4, sdesc_scales(sa_s + kAtomBytes));
+  }
+#pragma unroll
+  for (int a = 0; a < 2; ++a) tmem_cp_scales(tmem + sfb_col + a * 8, sdesc_scales(sw_s + a * kAtomBytes));
+}
+__device__ __forceinline__ void issue_half_mmas(uint32_t tmem, uint32_t stage, uint32_t sfb_col, uint32_t sfa_col,
+                                                uint32_t accumulate) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    mma_mxf4(tmem, sdesc_sw128(stage + C::kW + 32 * q), sdesc_sw128(stage + 32 * q),
+             idesc_mxf4(128, 128, (q & 1) * 2, (q & 1) * 2), tmem + sfa_col + 4 * (q >> 1), tmem + sfb_col + 8 * (q >> 1),
+             (accumulate != 0 || q != 0) ? 1u : 0u);
 }
 
 template <bool kGated>
@@ -488,8 +555,15 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
             for (int q = 0; q < C::kStages; ++q) a_load(q, pend_a[q], pend_rows[q]);
           }
           if (!mbar_wait(&empty[st], ((i / C::kStages) & 1) ^ 1, abort)) break;
-          mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(C::kW + rows * 128 + C::kSA));
-          bulk_g2s(smem + st * C::kStageBytes, w, kWeightBlockBytes, &full[st]);
+          uint8_t* dst = smem + st * C::kStageBytes;
+          if (s.half < 0) {
+            mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(C::kW + rows * 128 + C::kSA));
+            bulk_g2s(dst, w, kWeightBlockBytes, &full[st]);
+          } else {
+            mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(C::kW / 2 + rows * 128 + C::kSA));
+            bulk_g2s(dst, w + s.half * kTileBytes, kTileBytes, &full[st]);
+            bulk_g2s(dst + kHalfScales, w + 2 * kTileBytes + s.half * 2 * kAtomBytes, 2 * kAtomBytes, &full[st]);
+          }
           if (waited) {
             a_load(st, a, rows);
           } else {
@@ -538,13 +612,20 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
           const int k = s.k0 + j;
           const uint32_t sfa_col = resident ? kSfaRes + 8u * k : C::kSfBase + st * C::kSfSlot;
           const uint32_t sfb_col = resident ? C::kSfBase + 16u * st : sfa_col + C::kSfbOff;
-          issue_stage_scales_sfa<C>(tmem, base, sfb_col, sfa_col, !resident || ((have >> k) & 1u) == 0);
+          const bool copy_a = !resident || ((have >> k) & 1u) == 0;
+          if (s.half < 0)
+            issue_stage_scales_sfa<C>(tmem, base, sfb_col, sfa_col, copy_a);
+          else
+            issue_half_scales(tmem, base, sfb_col, sfa_col, copy_a);
           if (resident) have |= 1u << k;
           if (j == 0) {
             if (!mbar_wait(acc_empty, (seg & 1) ^ 1, abort)) break;
             tc_fence_after();
           }
-          issue_stage_mmas_sfa<C>(tmem, base, sfb_col, sfa_col, j != 0 ? 1u : 0u);
+          if (s.half < 0)
+            issue_stage_mmas_sfa<C>(tmem, base, sfb_col, sfa_col, j != 0 ? 1u : 0u);
+          else
+            issue_half_mmas(tmem, base, sfb_col, sfa_col, j != 0 ? 1u : 0u);
           mma_commit(&empty[st]);
         }
         mma_commit(acc_full);
@@ -561,9 +642,20 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     const int h = (warp - kFirstEpiWarp) >> 2;
     const int rl = q * 32 + lane;
     uint8_t* stage = staging + (warp - kFirstEpiWarp) * kStageWarp;
+    const int ew = warp - kFirstEpiWarp;
+    bool staged = false;                          // a warp's staging area may still be read by its warp
     for (int seg = 0; walk.next(g, s); ++seg) {
       const int info = __ldcg(g.tile + s.rt);
       const int rows = info >> 16, expert = info & 0xFFFF;
+      const bool whole = s.len == g.KT, few = whole && rows <= kFewRows;
+      const int first_c8 = s.half > 0 ? 16 : 0;
+      // what a tile of few rows needs beside its sums is asked for before the wait
+      int pair = 0;
+      float b[8];
+      if (few) {
+        if (!kGated && lane < rows) pair = __ldcg(g.row_pair + s.rt * kRowTile + lane);
+        load_bias8(g, s, expert, (lane + first_c8) & 31, b);
+      }
       const bool ok = mbar_wait(acc_full, seg & 1, abort);
       tc_fence_after();
       uint32_t r[128];
@@ -581,8 +673,36 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
 #pragma unroll
         for (int c = 0; c < 128; ++c) r[c] = 0u;
       }
-      if (s.len == g.KT) {
+      if (few) {
+        // Few rows: the lanes that hold them hand their columns out through
+        // shared memory, 16 rows at a time, a row to a warp.
+        float* sums = reinterpret_cast<float*>(staging);
+        if (staged) epi_barrier();
+        staged = false;
+        for (int row0 = 0; row0 < rows; row0 += 16) {
+          if (q == 0 && live && (lane >> 4) == (row0 >> 4) && (s.half < 0 || h == 0)) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              uint32_t* p = reinterpret_cast<uint32_t*>(sums + part_at(lane - row0, h * 16 + c));
+              *reinterpret_cast<uint4*>(p) = make_uint4(r[8 * c], r[8 * c + 1], r[8 * c + 2], r[8 * c + 3]);
+              *reinterpret_cast<uint4*>(p + 4) = make_uint4(r[8 * c + 4], r[8 * c + 5], r[8 * c + 6], r[8 * c + 7]);
+            }
+          }
+          epi_barrier();
+          for (int row = row0 + ew; row < rows && row < row0 + 16; row += 8) {
+            const float4* p = reinterpret_cast<const float4*>(sums + part_at(row - row0, lane));
+            const float4 lo = p[0], hi = p[1];
+            float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            finish_row<kGated>(g, s, row, __shfl_sync(0xFFFFFFFFu, pair, row), (lane + first_c8) & 31,
+                               s.half < 0 || lane < 16, b, v);
+          }
+          epi_barrier();
+        }
+        continue;
+      }
+      if (whole) {
         if (q * 32 < rows) finish<kGated>(g, s, expert, rows, rl, h, lane, stage, r);
+        staged = true;
         continue;
       }
       // A cut tile: this CTA's part to its slot; the last of the tile's CTAs
@@ -592,20 +712,17 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
 #pragma unroll
         for (int c = 0; c < 16; ++c) stg_32B(p + part_at(rl, h * 16 + c), &r[8 * c]);
       }
-      __threadfence();
+      const int c_lo = sk_owner(s.left * g.KT, walk.its, walk.parts_ctas);
+      const int c_hi = sk_owner(s.left * g.KT + g.KT - 1, walk.its, walk.parts_ctas);
       epi_barrier();
       if (threadIdx.x == kFirstEpiWarp * 32) {
-        const int others = sk_owner(s.left * g.KT + g.KT - 1, walk.its, walk.parts_ctas) -
-                           sk_owner(s.left * g.KT, walk.its, walk.parts_ctas);
+        __threadfence();                          // the barrier's writes before the count
         const int before = atomicAdd(g.tickets + s.left, 1);
-        __threadfence();
-        *last_flag = before == others;
+        __threadfence();                          // the count before the others' parts
+        *last_flag = before == c_hi - c_lo;
       }
       epi_barrier();
-      if (*last_flag != 0) {
-        __threadfence();
-        finish_cut<kGated>(g, walk, s, expert, rows, warp - kFirstEpiWarp, lane);
-      }
+      if (*last_flag != 0) finish_cut<kGated>(g, walk, s, expert, rows, c_lo, c_hi, ew, lane);
       epi_barrier();                              // the flag may be written again
     }
   }
