@@ -70,8 +70,7 @@ struct MoeArgs {
   int out_vec;                                     // rows of out allow 16-byte accesses
   uint8_t* h_blocks;
   int KT2;
-  int act;
-  float alpha, limit;
+  float a1, a3, limit, shift;                      // of the activation (see gated)
   const int32_t* hdr;
   const int32_t* tile;
   const int32_t* row_pair;
@@ -88,39 +87,48 @@ struct Segment {
 
 // A CTA's share of the tiles, segment by segment; every role walks it alike.
 //  1. whole rounds of units: `unit` neighbouring tiles of one row tile, whose
-//     activations (and their scales in TMEM) serve them all;
+//     activations (and their scales in TMEM) serve them all; the last round
+//     may leave a twelfth of the CTAs without one;
 //  2. whole rounds of single tiles;
 //  3. the fewer than G tiles left: each on a CTA of its own, or as halves on
-//     two, or cut evenly along (tile, k-step) over all CTAs, whichever takes
-//     the fewest k-steps, with kCutSteps for the cut's sums (measured: 5 to 7
-//     us from a cut tile's last product to its result; a k-step takes 0.5).
+//     two, or cut evenly along (tile, k-step) over all CTAs together with one
+//     of the rounds before, whichever takes the fewest k-steps, with kCutSteps
+//     for the cut's sums.  A tile is cut for at most four CTAs: the sum reads
+//     every part (ten parts of 128 rows took 30 us).
 struct Walk {
-  int units_per_row, unit_end, u, i;   // units: this CTA's next, tile of it
-  int t_end, t;                        // single tiles: this CTA's next
-  int h_end, h;                        // halves (two per tile from t_end)
-  int its, parts_ctas, it, it1;        // cut tiles from t_end
+  int units_per_row, unit_end, units, u, i;   // units: this CTA's next, tile of it
+  int t_end, t;                               // single tiles: this CTA's next
+  int h_end, h;                               // halves (two per tile from t_end)
+  int its, parts_ctas, it, it1;               // cut tiles from t_end
 
   __device__ __forceinline__ void init(const MoeArgs& g, int row_tiles) {
     const int G = gridDim.x, c = blockIdx.x;
     units_per_row = (g.n_tiles + g.unit - 1) / g.unit;
-    const int rounds = row_tiles * units_per_row / G;
-    unit_end = rounds * G;
+    units = row_tiles * units_per_row;
+    int rounds = units / G;
+    const int tiles = row_tiles * g.n_tiles;
+    h = h_end = its = it = it1 = 0;
+    parts_ctas = 1;
     u = c;
     i = 0;
+    t = t_end = tiles;
+    if ((units - rounds * G) * 12 >= 11 * G) ++rounds;
+    unit_end = rounds * G;
+    if (unit_end >= units) return;
     const int t0 = (unit_end / units_per_row) * g.n_tiles + (unit_end % units_per_row) * g.unit;
-    const int tiles = row_tiles * g.n_tiles;
     const int singles = (tiles - t0) / G;
     t = t0 + c;
     t_end = t0 + singles * G;
     const int rest = tiles - t_end;
-    h = h_end = its = it = it1 = 0;
-    parts_ctas = 1;
     if (rest == 0) return;
     const int whole = 2 * rest > G ? g.KT : (g.KT + 1) / 2;
-    if (static_cast<long long>(rest) * g.KT / G + kCutSteps < whole) {
-      its = rest * g.KT;
+    const int even = static_cast<int>(static_cast<long long>(rest) * g.KT / G), quarter = (g.KT + 3) / 4;
+    if ((singles > 0 ? even : (even > quarter ? even : quarter)) + kCutSteps < whole) {
+      if (singles > 0) t_end -= G;
+      const int cut = tiles - t_end;
+      its = cut * g.KT;
       parts_ctas = its / kMinSteps < G ? its / kMinSteps : G;
-      if (parts_ctas < 1) parts_ctas = 1;
+      if (parts_ctas > 4 * cut) parts_ctas = 4 * cut;
       if (c < parts_ctas) {
         it = sk_begin(c, its, parts_ctas);
         it1 = sk_begin(c + 1, its, parts_ctas);
@@ -143,7 +151,7 @@ struct Walk {
   }
 
   __device__ __forceinline__ bool next(const MoeArgs& g, Segment& s) {
-    if (u < unit_end) {
+    if (u < unit_end && u < units) {
       const int rt = u / units_per_row, n0 = (u - rt * units_per_row) * g.unit;
       place(g, rt * g.n_tiles + n0 + i, s);
       if (++i == g.unit || s.nt + 1 == g.n_tiles) {
@@ -173,6 +181,13 @@ struct Walk {
     return true;
   }
 };
+
+// The k-step a segment begins with.  Whole tiles start at different steps and
+// wrap around: CTAs that share a row tile or a column tile would otherwise ask
+// L2 for the same blocks at the same time.
+__device__ __forceinline__ int first_step(const MoeArgs& g, const Segment& s) {
+  return s.len == g.KT ? (3 * s.nt + 7 * s.rt) % g.KT : s.k0;
+}
 
 __device__ __forceinline__ int loaded_rows(int live) { return (live + 15) & ~15; }
 
@@ -251,92 +266,107 @@ __device__ __forceinline__ uint32_t quantize32_f32(const float (&v)[32], uint4& 
   return sbyte;
 }
 
-__device__ __forceinline__ float gated(int act, float alpha, float limit, float gate, float up) {
-  if (act == static_cast<int>(MoeAct::kGeluTanh)) {
-    const float u = 0.7978845608028654f * fmaf(0.044715f * gate * gate, gate, gate);
-    // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u))
-    return __fdividef(gate, 1.f + __expf(-2.f * u)) * up;
-  }
-  if (act == static_cast<int>(MoeAct::kSwigluClamp)) {
-    gate = fminf(gate, limit);
-    up = fminf(fmaxf(up, -limit), limit);
-    return __fdividef(gate, 1.f + __expf(-alpha * gate)) * (up + 1.f);
-  }
-  return __fdividef(gate, 1.f + __expf(-gate)) * up;
+// All three activations are g / (1 + 2^(g (a1 + a3 g^2))) (u + shift) with g and
+// u clamped: SiLU and the clamped form with a1 = -alpha log2 e, the tanh form
+// of GELU since (1 + tanh v) / 2 = 1 / (1 + exp(-2 v)).  (As three branches,
+// unrolled over a row, the code outgrew the instruction cache: 16000 cycles a
+// tile instead of 2500.)  The clamps keep a NaN.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float gated(const MoeArgs& g, float gate, float up) {
+  gate = min_nan(gate, g.limit);
+  up = max_nan(min_nan(up, g.limit), -g.limit);
+  const float z = gate * fmaf(g.a3, gate * gate, g.a1);
+  return __fdividef(gate, 1.f + exp2_approx(z)) * (up + g.shift);
 }
 
 // 128 columns of one row (acc), from column n0 of its expert: stored as bf16,
 // or gated and quantized.  Rows of bf16 go through the warp's staging area, 32
 // columns at a time, so that four lanes write 64 neighbouring bytes of a row
 // (written by the lane that holds the row, 16 bytes apart by a whole row, they
-// took twice as long).  All 32 lanes call this together.
+// took twice as long).  `pair`: the row's pair, -1 past the live rows.  All 32
+// lanes call this together.
 template <bool kGated>
-__device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, int expert, int rows, int rl, int h, int lane,
+__device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, int expert, int pair, int rl, int h, int lane,
                                        uint8_t* stage, uint32_t (&acc)[128]) {
   if (s.half >= 0) {
     if (h != 0) return;                            // half a tile is in the first 128 columns
     h = s.half;
   }
   const int n0 = s.nt * kTileN + h * 128;
-  const uint16_t* bias = g.bias != nullptr ? g.bias + static_cast<size_t>(expert) * g.N : nullptr;
-  if constexpr (!kGated) {
-    const int pair = rl < rows ? __ldcg(g.row_pair + s.rt * kRowTile + rl) : -1;
-    const bool vec = g.out_vec != 0;
-    int pairs[4];                                  // of the rows this lane writes: lane / 4 + 8 i
+  if (g.bias != nullptr) {                         // (no + 0 without one: -0 stays)
+    const uint16_t* bias = g.bias + static_cast<size_t>(expert) * g.N + n0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pairs[i] = __shfl_sync(0xFFFFFFFFu, pair, (lane >> 2) + 8 * i);
+    for (int c = 0; c < 128; ++c)
+      if (n0 + c < g.N) acc[c] = __float_as_uint(__uint_as_float(acc[c]) + bf16_bits_to_float(__ldg(bias + c)));
+  }
+  if constexpr (!kGated) {
+    int64_t row[4];                                // offsets of the rows this lane writes: lane / 4 + 8 i
+    uint32_t on = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = __shfl_sync(0xFFFFFFFFu, pair, (lane >> 2) + 8 * i);
+      row[i] = static_cast<int64_t>(p) * g.ldo + n0 + 8 * (lane & 3);
+      on |= p >= 0 ? 1u << i : 0u;
+    }
 #pragma unroll
     for (int c0 = 0; c0 < 128; c0 += 32) {
       if (n0 + c0 >= g.N) break;                   // uniform
 #pragma unroll
       for (int c = 0; c < 32; c += 8) {
-        float v[8];
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[i] = __uint_as_float(acc[c0 + c + i]);
-          if (bias != nullptr && n0 + c0 + c + i < g.N) v[i] += bf16_bits_to_float(__ldg(bias + n0 + c0 + c + i));
-        }
-        *reinterpret_cast<uint4*>(stage + lane * kStagePitch + 2 * c) =
-            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+        for (int i = 0; i < 4; ++i)
+          w[i] = pack_bf16x2(__uint_as_float(acc[c0 + c + 2 * i]), __uint_as_float(acc[c0 + c + 2 * i + 1]));
+        *reinterpret_cast<uint4*>(stage + lane * kStagePitch + 2 * c) = make_uint4(w[0], w[1], w[2], w[3]);
       }
       __syncwarp();
-      const int n = n0 + c0 + 8 * (lane & 3);
+      uint4 w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (pairs[i] < 0 || n >= g.N) continue;
-        const uint8_t* src = stage + ((lane >> 2) + 8 * i) * kStagePitch + 16 * (lane & 3);
-        const uint4 w = *reinterpret_cast<const uint4*>(src);
-        uint16_t* dst = g.out + static_cast<int64_t>(pairs[i]) * g.ldo + n;
-        if (vec && n + 8 <= g.N) {
-          *reinterpret_cast<uint4*>(dst) = w;
-        } else {
-          const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+      for (int i = 0; i < 4; ++i)
+        w[i] = *reinterpret_cast<const uint4*>(stage + ((lane >> 2) + 8 * i) * kStagePitch + 16 * (lane & 3));
+      __syncwarp();
+      if (g.out_vec != 0 && n0 + c0 + 32 <= g.N) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((on >> i) & 1u) *reinterpret_cast<uint4*>(g.out + row[i] + c0) = w[i];
+      } else {
+        const int n = n0 + c0 + 8 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (!((on >> i) & 1u)) continue;
+          const uint32_t q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (n + e < g.N) dst[e] = static_cast<uint16_t>(q[e >> 1] >> (16 * (e & 1)));
+            if (n + e < g.N) g.out[row[i] + c0 + e] = static_cast<uint16_t>(q[e >> 1] >> (16 * (e & 1)));
         }
       }
-      __syncwarp();
     }
   } else {
-    if (rl >= rows) return;
+    if (pair < 0) return;
     const int kt2 = s.nt >> 1, grp = s.nt & 1;
     uint8_t* blk = g.h_blocks + (static_cast<size_t>(s.rt) * g.KT2 + kt2) * kMoeBlockBytes;
     uint32_t scales = 0;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       float v[32];
+      // columns past N (a partial last tile) are zeros: their weights are
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const int n = n0 + 64 * b + 2 * j;
-        float gate = __uint_as_float(acc[64 * b + 2 * j]), up = __uint_as_float(acc[64 * b + 2 * j + 1]);
-        if (bias != nullptr && n < g.N) {
-          gate += bf16_bits_to_float(__ldg(bias + n));
-          up += bf16_bits_to_float(__ldg(bias + n + 1));
-        }
-        // columns past N (a partial last tile) are zeros: their weights are
-        v[j] = n < g.N ? gated(g.act, g.alpha, g.limit, gate, up) : 0.f;
-      }
+      for (int j = 0; j < 32; ++j)
+        v[j] = gated(g, __uint_as_float(acc[64 * b + 2 * j]), __uint_as_float(acc[64 * b + 2 * j + 1]));
       uint4 codes;
       const uint32_t sb = n0 + 64 * b < g.N ? quantize32_f32(v, codes) : 0x7Fu;
       if (n0 + 64 * b >= g.N) codes = make_uint4(0, 0, 0, 0);
@@ -379,7 +409,7 @@ __device__ __forceinline__ void finish_row(const MoeArgs& g, const Segment& s, i
     uint32_t am = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      h[i] = n0 + 2 * i < g.N ? gated(g.act, g.alpha, g.limit, v[2 * i], v[2 * i + 1]) : 0.f;
+      h[i] = n0 + 2 * i < g.N ? gated(g, v[2 * i], v[2 * i + 1]) : 0.f;
       am = max(am, __float_as_uint(h[i]) & 0x7FFFFFFFu);
     }
     am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
@@ -499,7 +529,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);   // both producers, and their bytes
       mbar_init(&empty[s], 1);
     }
     mbar_init(acc_full, 1);
@@ -523,64 +553,55 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
 
   if (warp < kFirstEpiWarp) {
    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-   if (warp == 0) {
+   if (warp == 0 || warp == 2) {
     if (lane == 0) {
-      // ---- producer: a stage is the weight block of one k-step (one bulk
-      // copy) and the live activation rows' codes and scales
-      int i = 0;
-      bool waited = false;
-      const uint8_t* pend_a[C::kStages];
-      int pend_rows[C::kStages];
-      auto a_load = [&](int st, const uint8_t* blk, int rows) {
-        uint8_t* dst = smem + st * C::kStageBytes + C::kW;
-        if (rows == kRowTile) {
-          bulk_g2s(dst, blk, C::kALoad + C::kSA, &full[st]);
-        } else {
-          bulk_g2s(dst, blk, rows * 128, &full[st]);
-          bulk_g2s(dst + C::kA, blk + kTileBytes, C::kSA, &full[st]);
-        }
-      };
+      // ---- producers: warp 0 brings the weight block of each k-step (one bulk
+      // copy), warp 2 the live activation rows' codes and scales.  The weights
+      // do not wait for the kernel before this one.
+      const bool weights = warp == 0;
+      if (!weights) griddep_wait();
+      int i = 0, st = 0;
+      uint32_t phase = 1;
       while (!abort && walk.next(g, s)) {
         const int info = __ldcg(g.tile + s.rt);
-        const int rows = loaded_rows(info >> 16);
-        const uint8_t* w = g.w_packed + static_cast<size_t>(info & 0xFFFF) * g.w_stride +
-                           static_cast<size_t>(s.nt * g.KT + s.k0) * kWeightBlockBytes;
-        const uint8_t* a = g.a_blocks + (static_cast<size_t>(s.rt) * g.KT + s.k0) * kMoeBlockBytes;
-        for (int j = 0; j < s.len; ++j, ++i, w += kWeightBlockBytes, a += kMoeBlockBytes) {
-          const int st = i % C::kStages;
-          if (i >= C::kStages && !waited) {        // the ring is full of weights: now the activations
-            griddep_wait();
-            waited = true;
-#pragma unroll
-            for (int q = 0; q < C::kStages; ++q) a_load(q, pend_a[q], pend_rows[q]);
-          }
-          if (!mbar_wait(&empty[st], ((i / C::kStages) & 1) ^ 1, abort)) break;
+        const uint8_t* base;
+        uint32_t bytes, pitch;
+        if (weights) {
+          base = g.w_packed + static_cast<size_t>(info & 0xFFFF) * g.w_stride +
+                 static_cast<size_t>(s.nt) * g.KT * kWeightBlockBytes;
+          bytes = s.half < 0 ? C::kW : C::kW / 2;
+          pitch = kWeightBlockBytes;
+        } else {
+          base = g.a_blocks + static_cast<size_t>(s.rt) * g.KT * kMoeBlockBytes;
+          bytes = loaded_rows(info >> 16) * 128 + C::kSA;
+          pitch = kMoeBlockBytes;
+        }
+        int k = first_step(g, s);
+        for (int j = 0; j < s.len; ++j) {
+          const uint8_t* src = base + static_cast<size_t>(k) * pitch;
+          if (++k == g.KT) k = 0;
+          if (!mbar_wait(&empty[st], phase, abort)) break;
           uint8_t* dst = smem + st * C::kStageBytes;
-          if (s.half < 0) {
-            mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(C::kW + rows * 128 + C::kSA));
-            bulk_g2s(dst, w, kWeightBlockBytes, &full[st]);
+          mbar_arrive_expect_tx(&full[st], bytes);
+          if (weights) {
+            if (s.half < 0) {
+              bulk_g2s(dst, src, kWeightBlockBytes, &full[st]);
+            } else {
+              bulk_g2s(dst, src + s.half * kTileBytes, kTileBytes, &full[st]);
+              bulk_g2s(dst + kHalfScales, src + 2 * kTileBytes + s.half * 2 * kAtomBytes, 2 * kAtomBytes, &full[st]);
+            }
+          } else if (bytes == C::kALoad + C::kSA) {
+            bulk_g2s(dst + C::kW, src, C::kALoad + C::kSA, &full[st]);
           } else {
-            mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(C::kW / 2 + rows * 128 + C::kSA));
-            bulk_g2s(dst, w + s.half * kTileBytes, kTileBytes, &full[st]);
-            bulk_g2s(dst + kHalfScales, w + 2 * kTileBytes + s.half * 2 * kAtomBytes, 2 * kAtomBytes, &full[st]);
+            bulk_g2s(dst + C::kW, src, bytes - C::kSA, &full[st]);
+            bulk_g2s(dst + C::kW + C::kA, src + kTileBytes, C::kSA, &full[st]);
           }
-          if (waited) {
-            a_load(st, a, rows);
-          } else {
-#pragma unroll
-            for (int q = 0; q < C::kStages; ++q)
-              if (q == st) {
-                pend_a[q] = a;
-                pend_rows[q] = rows;
-              }
+          ++i;
+          if (++st == C::kStages) {
+            st = 0;
+            phase ^= 1;
           }
         }
-      }
-      if (!waited) {
-        griddep_wait();
-#pragma unroll
-        for (int q = 0; q < C::kStages; ++q)
-          if (q < i) a_load(q, pend_a[q], pend_rows[q]);
       }
       if (abort) {   // the copies in flight land before the block may end
         bool late = false;
@@ -598,18 +619,20 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
       const bool resident = kSfaRes + 8u * static_cast<uint32_t>(g.KT) <= C::kTmemCols;
       int cur_rt = -1;
       uint32_t have = 0;
-      int i = 0;
+      int st = 0;
+      uint32_t phase = 0;
       for (int seg = 0; !abort && walk.next(g, s); ++seg) {
         if (s.rt != cur_rt) {
           cur_rt = s.rt;
           have = 0;
         }
-        for (int j = 0; j < s.len; ++j, ++i) {
-          const int st = i % C::kStages;
-          if (!mbar_wait(&full[st], (i / C::kStages) & 1, abort)) break;
+        int next_k = first_step(g, s);
+        for (int j = 0; j < s.len; ++j) {
+          const int k = next_k;
+          if (++next_k == g.KT) next_k = 0;
+          if (!mbar_wait(&full[st], phase, abort)) break;
           tc_fence_after();
           const uint32_t base = smem_u32(smem + st * C::kStageBytes);
-          const int k = s.k0 + j;
           const uint32_t sfa_col = resident ? kSfaRes + 8u * k : C::kSfBase + st * C::kSfSlot;
           const uint32_t sfb_col = resident ? C::kSfBase + 16u * st : sfa_col + C::kSfbOff;
           const bool copy_a = !resident || ((have >> k) & 1u) == 0;
@@ -627,6 +650,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
           else
             issue_half_mmas(tmem, base, sfb_col, sfa_col, j != 0 ? 1u : 0u);
           mma_commit(&empty[st]);
+          if (++st == C::kStages) {
+            st = 0;
+            phase ^= 1;
+          }
         }
         mma_commit(acc_full);
       }
@@ -650,10 +677,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
       const bool whole = s.len == g.KT, few = whole && rows <= kFewRows;
       const int first_c8 = s.half > 0 ? 16 : 0;
       // what a tile of few rows needs beside its sums is asked for before the wait
-      int pair = 0;
+      int pair = -1;
       float b[8];
+      if (whole && (few ? lane : rl) < rows) pair = kGated ? 0 : __ldcg(g.row_pair + s.rt * kRowTile + (few ? lane : rl));
       if (few) {
-        if (!kGated && lane < rows) pair = __ldcg(g.row_pair + s.rt * kRowTile + lane);
         load_bias8(g, s, expert, (lane + first_c8) & 31, b);
       }
       const bool ok = mbar_wait(acc_full, seg & 1, abort);
@@ -701,7 +728,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
         continue;
       }
       if (whole) {
-        if (q * 32 < rows) finish<kGated>(g, s, expert, rows, rl, h, lane, stage, r);
+        if (q * 32 < rows) finish<kGated>(g, s, expert, pair, rl, h, lane, stage, r);
         staged = true;
         continue;
       }
@@ -767,9 +794,11 @@ cudaError_t launch_moe_gemm(const MoeGemmProblem& p, const MoePlan& plan, const 
   a.out_vec = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.ldo % 8 == 0;
   a.h_blocks = p.h_blocks;
   a.KT2 = static_cast<int>(padded_k(p.N / 2) / kKTile);
-  a.act = static_cast<int>(p.act);
-  a.alpha = p.alpha;
-  a.limit = p.limit;
+  constexpr float kLog2e = 1.4426950408889634f;
+  a.limit = p.act == MoeAct::kSwigluClamp ? p.limit : __builtin_huge_valf();
+  a.shift = p.act == MoeAct::kSwigluClamp ? 1.f : 0.f;
+  a.a1 = -kLog2e * (p.act == MoeAct::kSwigluClamp ? p.alpha : p.act == MoeAct::kGeluTanh ? 1.5957691216057308f : 1.f);
+  a.a3 = p.act == MoeAct::kGeluTanh ? 0.044715f * a.a1 : 0.f;
   a.hdr = plan.hdr;
   a.tile = plan.tile;
   a.row_pair = plan.row_pair;
