@@ -538,7 +538,7 @@ static MoeWorkspace moe_workspace_layout(int64_t P, int E, int K, int I, int N, 
   w.a = round_up(moe_plan_bytes(P, E), 1024);
   w.h = w.a + static_cast<size_t>(rt * (padded_k(K) / kKTile)) * kMoeBlockBytes;
   w.results = w.h + (I > 0 ? static_cast<size_t>(rt * (padded_k(I) / kKTile)) * kMoeBlockBytes : 0);
-  w.ldp = ceil_div(N, 8) * 8;
+  w.ldp = ceil_div(N, 16) * 16;
   w.parts = w.results + (I > 0 ? round_up(static_cast<size_t>(P * w.ldp) * 2, 1024) : 0);
   w.total = w.parts + moe_gemm_parts_bytes(sm_count);
   return w;

@@ -46,17 +46,25 @@ constexpr int kPartFloats = 128 * kTileN;          // one part of a cut tile
 constexpr int kMinSteps = 2;                       // k-steps a CTA takes at least where tiles are cut
 constexpr int kCutSteps = 12;                      // what cutting costs, in k-steps (see Walk)
 constexpr int kFewRows = 32;                       // rows up to which a tile is finished row by row
-// Warps 0..3: producer, MMA issuer and two that only make the first warpgroup
-// whole; warps 4..11: epilogue.  The epilogue holds 128 columns of a row in
-// registers: it takes over what the first warpgroup gives up (56 + 2 x 224 =
-// 3 x 168 registers, the launch's).  With 168 it spilled a kilobyte a thread.
+// Warp 0 brings the weights, warp 2 the activations, warp 1 issues the MMAs,
+// warp 3 finds the segments for all of them; warps 4..11 are the epilogue.  The
+// epilogue holds 128 columns of a row in registers: it takes over what the
+// first warpgroup gives up (56 + 2 x 224 = 3 x 168 registers, the launch's).
+// With 168 it spilled a kilobyte a thread.
 constexpr int kMoeThreads = 384;
 constexpr int kFirstEpiWarp = 4;
-// Staging of the bf16 rows: per epilogue warp 32 rows x 32 columns, rows 80
-// bytes apart (the 16-byte accesses of 8 lanes then meet 8 different banks).
-constexpr int kStagePitch = 80;
-constexpr int kStageWarp = 32 * kStagePitch;
-constexpr int kMoeSmem = C::kSmem + 8 * kStageWarp;
+constexpr int kFewBatch = 16;                      // rows of a tile of few rows that are handed out at once
+// Staging of the bf16 rows: per epilogue warp 32 rows x 32 columns (64 bytes),
+// 16-byte pieces rotated by the row so that 8 lanes meet 8 different banks
+// both when they hold 8 rows and when they hold 2 rows' 4 pieces.
+constexpr int kStageWarp = 32 * 64;
+__device__ __forceinline__ int stage_at(int row, int piece) { return row * 64 + ((piece ^ (row >> 1)) & 3) * 16; }
+static_assert(8 * kStageWarp >= kFewBatch * kTileN * 4, "the rows handed out share the staging area");
+// Segments found ahead: the record of each and the pairs of its rows.
+constexpr int kSegs = 8;
+constexpr int kSegBytes = 32 + kRowTile * 4;
+constexpr int kSegReaders = 3 + 8;                 // both producers, the MMA issuer and the epilogue warps
+constexpr int kMoeSmem = C::kSmem + 8 * kStageWarp + kSegs * kSegBytes;
 static_assert(kMoeSmem <= kMaxSmem, "ring and staging exceed shared memory");
 
 struct MoeArgs {
@@ -78,14 +86,17 @@ struct MoeArgs {
   float* parts;
 };
 
-struct Segment {
-  int rt, nt;    // row tile, column tile
+struct __align__(16) Segment {
+  int rt, nt;    // row tile, column tile; rt < 0: no more segments
+  int k0, len;   // first k-step, k-steps
   int half;      // 0, 1: that half of the column tile; -1: all of it
-  int k0, len;   // k-steps
   int left;      // index among the cut tiles, or -1
+  int info;      // the row tile's expert | live rows << 16
+  int first;     // k-step it begins with (it wraps around)
 };
+static_assert(sizeof(Segment) == 32, "two 16-byte words");
 
-// A CTA's share of the tiles, segment by segment; every role walks it alike.
+// A CTA's share of the tiles, segment by segment.
 //  1. whole rounds of units: `unit` neighbouring tiles of one row tile, whose
 //     activations (and their scales in TMEM) serve them all; the last round
 //     may leave a twelfth of the CTAs without one;
@@ -190,6 +201,18 @@ __device__ __forceinline__ int first_step(const MoeArgs& g, const Segment& s) {
 }
 
 __device__ __forceinline__ int loaded_rows(int live) { return (live + 15) & ~15; }
+
+// One lane of the converged warp, chosen by the hardware: what it issues keeps
+// its descriptors in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 
 __device__ __forceinline__ void epi_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
@@ -331,29 +354,27 @@ __device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, int e
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           w[i] = pack_bf16x2(__uint_as_float(acc[c0 + c + 2 * i]), __uint_as_float(acc[c0 + c + 2 * i + 1]));
-        *reinterpret_cast<uint4*>(stage + lane * kStagePitch + 2 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(stage + stage_at(lane, c >> 3)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
       __syncwarp();
-      uint4 w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = *reinterpret_cast<const uint4*>(stage + ((lane >> 2) + 8 * i) * kStagePitch + 16 * (lane & 3));
-      __syncwarp();
       if (g.out_vec != 0 && n0 + c0 + 32 <= g.N) {
+        uint4 w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = *reinterpret_cast<const uint4*>(stage + stage_at((lane >> 2) + 8 * i, lane & 3));
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if ((on >> i) & 1u) *reinterpret_cast<uint4*>(g.out + row[i] + c0) = w[i];
-      } else {
-        const int n = n0 + c0 + 8 * (lane & 3);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (!((on >> i) & 1u)) continue;
-          const uint32_t q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (n + e < g.N) g.out[row[i] + c0 + e] = static_cast<uint16_t>(q[e >> 1] >> (16 * (e & 1)));
+      } else {                                     // rows that allow no wide access: a lane per column
+#pragma unroll 4
+        for (int i = 0; i < 32; ++i) {
+          const int p = __shfl_sync(0xFFFFFFFFu, pair, i);
+          if (p >= 0 && n0 + c0 + lane < g.N)
+            g.out[static_cast<int64_t>(p) * g.ldo + n0 + c0 + lane] =
+                *reinterpret_cast<const uint16_t*>(stage + stage_at(i, lane >> 3) + 2 * (lane & 7));
         }
       }
+      __syncwarp();
     }
   } else {
     if (pair < 0) return;
@@ -520,9 +541,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
   uint64_t* empty = full + C::kStages;
   uint64_t* acc_full = empty + C::kStages;
   uint64_t* acc_empty = acc_full + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 1);
+  uint64_t* seg_full = acc_empty + 1;
+  uint64_t* seg_empty = seg_full + kSegs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_empty + kSegs);
   volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint8_t* staging = smem + C::kRing + 512;
+  uint8_t* segs = staging + 8 * kStageWarp;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   bool abort = false;
@@ -534,6 +558,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, kEpiThreads);
+    for (int q = 0; q < kSegs; ++q) {
+      mbar_init(&seg_full[q], 1);
+      mbar_init(&seg_empty[q], kSegReaders);
+    }
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -544,12 +572,31 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // The plan is complete when this kernel starts: the kernel before it lets
-  // it start only after its own wait for the plan.  So the first weights are
-  // requested before the wait for the activations.
-  Walk walk;
-  walk.init(g, __ldcg(g.hdr));
+  // The next record of the ring of segments, for one reader; false at the end.
   Segment s;
+  int sslot = 0;
+  uint32_t sphase = 0;
+  auto next_segment = [&]() -> bool {
+    if (!mbar_wait(&seg_full[sslot], sphase, abort)) return false;
+    const int4* p = reinterpret_cast<const int4*>(segs + sslot * kSegBytes);
+    const int4 lo = p[0], hi = p[1];
+    s.rt = lo.x;
+    s.nt = lo.y;
+    s.k0 = lo.z;
+    s.len = lo.w;
+    s.half = hi.x;
+    s.left = hi.y;
+    s.info = hi.z;
+    s.first = hi.w;
+    return s.rt >= 0;
+  };
+  auto done_segment = [&]() {
+    mbar_arrive(&seg_empty[sslot]);
+    if (++sslot == kSegs) {
+      sslot = 0;
+      sphase ^= 1;
+    }
+  };
 
   if (warp < kFirstEpiWarp) {
    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -562,33 +609,34 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
       if (!weights) griddep_wait();
       int i = 0, st = 0;
       uint32_t phase = 1;
-      while (!abort && walk.next(g, s)) {
-        const int info = __ldcg(g.tile + s.rt);
+      while (next_segment()) {
+        const int info = s.info, len = s.len, half = s.half;
+        int k = s.first;
         const uint8_t* base;
         uint32_t bytes, pitch;
         if (weights) {
           base = g.w_packed + static_cast<size_t>(info & 0xFFFF) * g.w_stride +
                  static_cast<size_t>(s.nt) * g.KT * kWeightBlockBytes;
-          bytes = s.half < 0 ? C::kW : C::kW / 2;
+          bytes = half < 0 ? C::kW : C::kW / 2;
           pitch = kWeightBlockBytes;
         } else {
           base = g.a_blocks + static_cast<size_t>(s.rt) * g.KT * kMoeBlockBytes;
           bytes = loaded_rows(info >> 16) * 128 + C::kSA;
           pitch = kMoeBlockBytes;
         }
-        int k = first_step(g, s);
-        for (int j = 0; j < s.len; ++j) {
+        done_segment();
+        for (int j = 0; j < len; ++j) {
           const uint8_t* src = base + static_cast<size_t>(k) * pitch;
           if (++k == g.KT) k = 0;
           if (!mbar_wait(&empty[st], phase, abort)) break;
           uint8_t* dst = smem + st * C::kStageBytes;
           mbar_arrive_expect_tx(&full[st], bytes);
           if (weights) {
-            if (s.half < 0) {
+            if (half < 0) {
               bulk_g2s(dst, src, kWeightBlockBytes, &full[st]);
             } else {
-              bulk_g2s(dst, src + s.half * kTileBytes, kTileBytes, &full[st]);
-              bulk_g2s(dst + kHalfScales, src + 2 * kTileBytes + s.half * 2 * kAtomBytes, 2 * kAtomBytes, &full[st]);
+              bulk_g2s(dst, src + half * kTileBytes, kTileBytes, &full[st]);
+              bulk_g2s(dst + kHalfScales, src + 2 * kTileBytes + half * 2 * kAtomBytes, 2 * kAtomBytes, &full[st]);
             }
           } else if (bytes == C::kALoad + C::kSA) {
             bulk_g2s(dst + C::kW, src, C::kALoad + C::kSA, &full[st]);
@@ -611,54 +659,107 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---- MMA issuer: one accumulator, one segment at a time; the
-      // activation scales of a row tile stay in TMEM across its column tiles
-      // where they fit (K <= 6144), as in gemm.cu.
-      constexpr uint32_t kSfaRes = C::kSfBase + C::kStages * 16u;
-      const bool resident = kSfaRes + 8u * static_cast<uint32_t>(g.KT) <= C::kTmemCols;
-      int cur_rt = -1;
-      uint32_t have = 0;
-      int st = 0;
-      uint32_t phase = 0;
-      for (int seg = 0; !abort && walk.next(g, s); ++seg) {
-        if (s.rt != cur_rt) {
-          cur_rt = s.rt;
-          have = 0;
-        }
-        int next_k = first_step(g, s);
-        for (int j = 0; j < s.len; ++j) {
-          const int k = next_k;
-          if (++next_k == g.KT) next_k = 0;
-          if (!mbar_wait(&full[st], phase, abort)) break;
-          tc_fence_after();
-          const uint32_t base = smem_u32(smem + st * C::kStageBytes);
-          const uint32_t sfa_col = resident ? kSfaRes + 8u * k : C::kSfBase + st * C::kSfSlot;
-          const uint32_t sfb_col = resident ? C::kSfBase + 16u * st : sfa_col + C::kSfbOff;
-          const bool copy_a = !resident || ((have >> k) & 1u) == 0;
-          if (s.half < 0)
+    // ---- MMA issuer: one accumulator, one segment at a time; the activation
+    // scales of a row tile stay in TMEM across its column tiles where they fit
+    // (K <= 6144), as in gemm.cu.  The whole warp walks the stages and one
+    // elected lane issues (in a branch of lane 0 alone a k-step's four MMAs and
+    // four to six copies took 1050 cycles to issue).
+    constexpr uint32_t kSfaRes = C::kSfBase + C::kStages * 16u;
+    const bool resident = kSfaRes + 8u * static_cast<uint32_t>(g.KT) <= C::kTmemCols;
+    const uint32_t ring = smem_u32(smem);
+    int cur_rt = -1;
+    uint32_t have = 0;
+    int st = 0;
+    uint32_t phase = 0;
+    for (int seg = 0; next_segment(); ++seg) {
+      const int len = s.len, half = s.half;
+      int k = s.first;
+      if (s.rt != cur_rt) {
+        cur_rt = s.rt;
+        have = 0;
+      }
+      __syncwarp();
+      if (elect_one()) mbar_arrive(&seg_empty[sslot]);
+      if (++sslot == kSegs) {
+        sslot = 0;
+        sphase ^= 1;
+      }
+      for (int j = 0; j < len; ++j) {
+        mbar_wait(&full[st], phase, abort);
+        abort = __any_sync(0xFFFFFFFFu, abort);
+        if (abort) break;
+        tc_fence_after();
+        const uint32_t base = ring + st * C::kStageBytes;
+        const uint32_t sfa_col = resident ? kSfaRes + 8u * k : C::kSfBase + st * C::kSfSlot;
+        const uint32_t sfb_col = resident ? C::kSfBase + 16u * st : sfa_col + C::kSfbOff;
+        const bool copy_a = !resident || ((have >> (k & 31)) & 1u) == 0;
+        if (resident) have |= 1u << k;
+        if (elect_one()) {
+          if (half < 0)
             issue_stage_scales_sfa<C>(tmem, base, sfb_col, sfa_col, copy_a);
           else
             issue_half_scales(tmem, base, sfb_col, sfa_col, copy_a);
-          if (resident) have |= 1u << k;
-          if (j == 0) {
-            if (!mbar_wait(acc_empty, (seg & 1) ^ 1, abort)) break;
-            tc_fence_after();
-          }
-          if (s.half < 0)
+        }
+        __syncwarp();
+        if (j == 0) {
+          mbar_wait(acc_empty, (seg & 1) ^ 1, abort);
+          abort = __any_sync(0xFFFFFFFFu, abort);
+          if (abort) break;
+          tc_fence_after();
+        }
+        if (elect_one()) {
+          if (half < 0)
             issue_stage_mmas_sfa<C>(tmem, base, sfb_col, sfa_col, j != 0 ? 1u : 0u);
           else
             issue_half_mmas(tmem, base, sfb_col, sfa_col, j != 0 ? 1u : 0u);
           mma_commit(&empty[st]);
-          if (++st == C::kStages) {
-            st = 0;
-            phase ^= 1;
-          }
+          if (j + 1 == len) mma_commit(acc_full);
         }
-        mma_commit(acc_full);
+        __syncwarp();
+        if (++k == g.KT) k = 0;
+        if (++st == C::kStages) {
+          st = 0;
+          phase ^= 1;
+        }
       }
+      if (abort) break;
     }
     __syncwarp();
+   } else {
+    // ---- warp 3: the segments of this CTA, ahead of the other roles.  The plan
+    // is complete when this kernel starts: the kernel before it lets it start
+    // only after its own wait for the plan.  A segment's tile word and pairs
+    // are loaded while the one before it is handed out.
+    Walk walk;
+    walk.init(g, __ldcg(g.hdr));
+    int rt = -1;
+    int4 pairs = make_int4(-1, -1, -1, -1);
+    int info = 0;
+    bool more = true;
+    while (more && !abort) {
+      more = walk.next(g, s);
+      if (!more) s.rt = -1;
+      if (more && s.rt != rt) {
+        rt = s.rt;
+        info = __ldcg(g.tile + rt);
+        if (!kGated) pairs = __ldcg(reinterpret_cast<const int4*>(g.row_pair + static_cast<int64_t>(rt) * kRowTile) + lane);
+      }
+      mbar_wait(&seg_empty[sslot], sphase ^ 1, abort);
+      abort = __any_sync(0xFFFFFFFFu, abort);
+      if (abort) break;
+      uint8_t* rec = segs + sslot * kSegBytes;
+      if (lane == 0) {
+        reinterpret_cast<int4*>(rec)[0] = make_int4(s.rt, s.nt, s.k0, s.len);
+        reinterpret_cast<int4*>(rec)[1] = make_int4(s.half, s.left, info, more ? first_step(g, s) : 0);
+      }
+      if (!kGated) reinterpret_cast<int4*>(rec + 32)[lane] = pairs;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_full[sslot]);
+      if (++sslot == kSegs) {
+        sslot = 0;
+        sphase ^= 1;
+      }
+    }
    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
@@ -671,18 +772,26 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     uint8_t* stage = staging + (warp - kFirstEpiWarp) * kStageWarp;
     const int ew = warp - kFirstEpiWarp;
     bool staged = false;                          // a warp's staging area may still be read by its warp
-    for (int seg = 0; walk.next(g, s); ++seg) {
-      const int info = __ldcg(g.tile + s.rt);
-      const int rows = info >> 16, expert = info & 0xFFFF;
+    // how the cut tiles are dealt out, for their sums
+    Walk walk;
+    walk.init(g, __ldcg(g.hdr));
+    for (int seg = 0; next_segment(); ++seg) {
+      const int rows = s.info >> 16, expert = s.info & 0xFFFF;
       const bool whole = s.len == g.KT, few = whole && rows <= kFewRows;
       const int first_c8 = s.half > 0 ? 16 : 0;
-      // what a tile of few rows needs beside its sums is asked for before the wait
-      int pair = -1;
+      const int* pairs = reinterpret_cast<const int*>(segs + sslot * kSegBytes + 32);
+      const int pair = rl < rows ? (kGated ? 0 : pairs[rl]) : -1;
       float b[8];
-      if (whole && (few ? lane : rl) < rows) pair = kGated ? 0 : __ldcg(g.row_pair + s.rt * kRowTile + (few ? lane : rl));
-      if (few) {
-        load_bias8(g, s, expert, (lane + first_c8) & 31, b);
-      }
+      if (few) load_bias8(g, s, expert, (lane + first_c8) & 31, b);
+      // this warp has read the record (the pairs of few rows are read below)
+      auto release = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&seg_empty[sslot]);
+        if (++sslot == kSegs) {
+          sslot = 0;
+          sphase ^= 1;
+        }
+      };
       const bool ok = mbar_wait(acc_full, seg & 1, abort);
       tc_fence_after();
       uint32_t r[128];
@@ -720,13 +829,15 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
             const float4* p = reinterpret_cast<const float4*>(sums + part_at(row - row0, lane));
             const float4 lo = p[0], hi = p[1];
             float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            finish_row<kGated>(g, s, row, __shfl_sync(0xFFFFFFFFu, pair, row), (lane + first_c8) & 31,
+            finish_row<kGated>(g, s, row, kGated ? 0 : pairs[row], (lane + first_c8) & 31,
                                s.half < 0 || lane < 16, b, v);
           }
           epi_barrier();
         }
+        release();
         continue;
       }
+      release();
       if (whole) {
         if (q * 32 < rows) finish<kGated>(g, s, expert, pair, rl, h, lane, stage, r);
         staged = true;

@@ -44,6 +44,13 @@ struct PlanArgs {
   MoePlan plan;
 };
 
+// Ids p .. p + 3 (-1 past p1; p1 is P or a multiple of 128).
+__device__ __forceinline__ int4 load_ids(const int32_t* ids, int p, int p1, bool vec) {
+  if (vec && p + 3 < p1) return *reinterpret_cast<const int4*>(ids + p);
+  return make_int4(p < p1 ? ids[p] : -1, p + 1 < p1 ? ids[p + 1] : -1, p + 2 < p1 ? ids[p + 2] : -1,
+                   p + 3 < p1 ? ids[p + 3] : -1);
+}
+
 __global__ void __launch_bounds__(1024) moe_plan_kernel(const __grid_constant__ PlanArgs a) {
   __shared__ int hist[kMoeMaxExperts];
   __shared__ int wsum[32], wtile[32], wall[32];
@@ -53,19 +60,27 @@ __global__ void __launch_bounds__(1024) moe_plan_kernel(const __grid_constant__ 
   griddep_launch_dependents();
   griddep_wait();
   __syncthreads();
-  // The pairs are dealt to the warps in stretches of whole 32s, so that a
-  // warp meets them in order in the second pass.
-  const int per = (a.P + n_thr - 1) / n_thr * 32;   // pairs per warp
+  // The pairs are dealt to the warps in stretches of whole 128s, four
+  // neighbours to a lane, so that a warp meets them in order in both passes.
+  const int per = (a.P + n_warps * 128 - 1) / (n_warps * 128) * 128;   // pairs per warp
   const int p0 = warp * per < a.P ? warp * per : a.P, p1 = p0 + per < a.P ? p0 + per : a.P;
+  const bool vec = (reinterpret_cast<uintptr_t>(a.ids) & 15) == 0;
   bool bad = false;
+  int mine = 0;   // this expert's pairs among this lane's
 #pragma unroll 4
-  for (int p = p0 + lane; p < p1; p += 32) {
-    const int id = a.ids[p];
-    if (static_cast<uint32_t>(id) < static_cast<uint32_t>(a.E))
-      atomicAdd(&hist[id], 1);
-    else
-      bad = bad || id >= a.E;
+  for (int p = p0 + 4 * lane; p < p1; p += 128) {
+    const int4 v = load_ids(a.ids, p, p1, vec);
+    const int id[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (static_cast<uint32_t>(id[j]) < static_cast<uint32_t>(a.E))
+        atomicAdd(&hist[id[j]], 1);
+      else
+        bad = bad || id[j] >= a.E;
+      mine += id[j] == e;
+    }
   }
+  mine = __reduce_add_sync(0xFFFFFFFFu, mine);
   __syncthreads();
   // row tiles before this expert's, and in all
   int before = 0, all = 0;
@@ -76,10 +91,6 @@ __global__ void __launch_bounds__(1024) moe_plan_kernel(const __grid_constant__ 
   }
   before = __reduce_add_sync(0xFFFFFFFFu, before);
   all = __reduce_add_sync(0xFFFFFFFFu, all);
-  // this expert's pairs in this warp's stretch
-  int mine = 0;
-  for (int p = p0; p < p1; p += 32)
-    mine += __popc(__ballot_sync(0xFFFFFFFFu, p + lane < p1 && a.ids[p + lane] == e));
   if (lane == 0) {
     wsum[warp] = mine;
     wtile[warp] = before;
@@ -102,18 +113,29 @@ __global__ void __launch_bounds__(1024) moe_plan_kernel(const __grid_constant__ 
     const int live = n - i * kRowTile < kRowTile ? n - i * kRowTile : kRowTile;
     a.plan.tile[tile0 + i] = e | (live << 16);
   }
-  for (int p = p0; p < p1; p += 32) {
-    const int id = p + lane < p1 ? a.ids[p + lane] : -1;
-    const bool hit = id == e;
-    const uint32_t m = __ballot_sync(0xFFFFFFFFu, hit);
-    if (hit) {
-      const int r = tile0 * kRowTile + first + __popc(m & ((1u << lane) - 1u));
-      a.plan.row_pair[r] = p + lane;
-      a.plan.pos[p + lane] = r;
-    } else if (e == 0 && p + lane < p1 && static_cast<uint32_t>(id) >= static_cast<uint32_t>(a.E)) {
-      a.plan.pos[p + lane] = -1;
+  if (n == 0 && e != 0) return;
+#pragma unroll 4
+  for (int p = p0 + 4 * lane; p - 4 * lane < p1; p += 128) {   // whole warps loop
+    const int4 v = load_ids(a.ids, p, p1, vec);
+    const int id[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = __ballot_sync(0xFFFFFFFFu, id[j] == e);
+    if (e != 0 && (m[0] | m[1] | m[2] | m[3]) == 0) continue;
+    const uint32_t lower = (1u << lane) - 1u;
+    int r = tile0 * kRowTile + first + __popc(m[0] & lower) + __popc(m[1] & lower) + __popc(m[2] & lower) +
+            __popc(m[3] & lower);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (id[j] == e) {
+        a.plan.row_pair[r] = p + j;
+        a.plan.pos[p + j] = r;
+        ++r;
+      } else if (e == 0 && p + j < p1 && static_cast<uint32_t>(id[j]) >= static_cast<uint32_t>(a.E)) {
+        a.plan.pos[p + j] = -1;
+      }
     }
-    first += __popc(m);
+    first += __popc(m[0]) + __popc(m[1]) + __popc(m[2]) + __popc(m[3]);
   }
 }
 
@@ -259,7 +281,7 @@ __global__ void __launch_bounds__(128) moe_combine_kernel(const __grid_constant_
 
 size_t moe_plan_bytes(int64_t P, int E) {
   const int64_t rt = moe_max_tiles(P, E);
-  const size_t ints = static_cast<size_t>(rt) + static_cast<size_t>(rt) * kRowTile + static_cast<size_t>(P) + 2 * kMoeTickets;
+  const size_t ints = static_cast<size_t>(ceil_div(rt, 4) * 4) + static_cast<size_t>(rt) * kRowTile + static_cast<size_t>(P) + 2 * kMoeTickets;
   return kPlanHeader + 4 * ints + 64;
 }
 
@@ -268,7 +290,7 @@ MoePlan moe_plan_at(void* base, int64_t P, int E) {
   MoePlan p;
   p.hdr = static_cast<int32_t*>(base);
   p.tile = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(base) + kPlanHeader);
-  p.row_pair = p.tile + rt;
+  p.row_pair = p.tile + ceil_div(rt, 4) * 4;       // 16-byte aligned
   p.pos = p.row_pair + rt * kRowTile;
   p.tickets = p.pos + P;
   p.max_tiles = static_cast<int>(rt);
