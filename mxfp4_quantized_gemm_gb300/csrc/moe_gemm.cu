@@ -72,6 +72,7 @@ struct MoeArgs {
   const uint8_t* w_packed;
   size_t w_stride;                                 // bytes of one expert's packed weights
   const uint16_t* bias;
+  int bias_vec;                                    // rows of bias allow 16-byte loads
   int N, KT, n_tiles, unit;
   uint16_t* out;
   int64_t ldo;
@@ -92,7 +93,7 @@ struct __align__(16) Segment {
   int half;      // 0, 1: that half of the column tile; -1: all of it
   int left;      // index among the cut tiles, or -1
   int info;      // the row tile's expert | live rows << 16
-  int first;     // k-step it begins with (it wraps around)
+  int unused;
 };
 static_assert(sizeof(Segment) == 32, "two 16-byte words");
 
@@ -192,13 +193,6 @@ struct Walk {
     return true;
   }
 };
-
-// The k-step a segment begins with.  Whole tiles start at different steps and
-// wrap around: CTAs that share a row tile or a column tile would otherwise ask
-// L2 for the same blocks at the same time.
-__device__ __forceinline__ int first_step(const MoeArgs& g, const Segment& s) {
-  return s.len == g.KT ? (3 * s.nt + 7 * s.rt) % g.KT : s.k0;
-}
 
 __device__ __forceinline__ int loaded_rows(int live) { return (live + 15) & ~15; }
 
@@ -323,7 +317,7 @@ __device__ __forceinline__ float gated(const MoeArgs& g, float gate, float up) {
 // took twice as long).  `pair`: the row's pair, -1 past the live rows.  All 32
 // lanes call this together.
 template <bool kGated>
-__device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, int expert, int pair, int rl, int h, int lane,
+__device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, uint2 bias, int pair, int rl, int h, int lane,
                                        uint8_t* stage, uint32_t (&acc)[128]) {
   if (s.half >= 0) {
     if (h != 0) return;                            // half a tile is in the first 128 columns
@@ -331,10 +325,12 @@ __device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, int e
   }
   const int n0 = s.nt * kTileN + h * 128;
   if (g.bias != nullptr) {                         // (no + 0 without one: -0 stays)
-    const uint16_t* bias = g.bias + static_cast<size_t>(expert) * g.N + n0;
 #pragma unroll
-    for (int c = 0; c < 128; ++c)
-      if (n0 + c < g.N) acc[c] = __float_as_uint(__uint_as_float(acc[c]) + bf16_bits_to_float(__ldg(bias + c)));
+    for (int c = 0; c < 128; c += 2) {
+      const uint32_t w = __shfl_sync(0xFFFFFFFFu, (c & 2) ? bias.y : bias.x, c >> 2);
+      acc[c] = __float_as_uint(__uint_as_float(acc[c]) + __uint_as_float(w << 16));
+      acc[c + 1] = __float_as_uint(__uint_as_float(acc[c + 1]) + __uint_as_float(w & 0xFFFF0000u));
+    }
   }
   if constexpr (!kGated) {
     if (g.out_vec != 0 && n0 + 128 <= g.N) {
@@ -422,7 +418,6 @@ __device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, int e
       __syncwarp();
     }
   } else {
-    if (pair < 0) return;
     const int kt2 = s.nt >> 1, grp = s.nt & 1;
     uint8_t* blk = g.h_blocks + (static_cast<size_t>(s.rt) * g.KT2 + kt2) * kMoeBlockBytes;
     uint32_t scales = 0;
@@ -438,8 +433,9 @@ __device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, int e
       if (n0 + 64 * b >= g.N) codes = make_uint4(0, 0, 0, 0);
       scales |= sb << (8 * b);
       const int chunk = grp * 4 + h * 2 + b;
-      *reinterpret_cast<uint4*>(blk + (rl << 7) + ((chunk ^ (rl & 7)) << 4)) = codes;
+      if (pair >= 0) *reinterpret_cast<uint4*>(blk + (rl << 7) + ((chunk ^ (rl & 7)) << 4)) = codes;
     }
+    if (pair < 0) return;
     uint8_t* sc = blk + kTileBytes + ((rl & 31) << 4) + ((rl >> 5) << 2) + 2 * h;
     *reinterpret_cast<uint16_t*>(sc + (grp << 9)) = static_cast<uint16_t>(scales);
     // the last k-tile's second half has no columns: its weights are zero
@@ -453,11 +449,11 @@ __device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, int e
 // lanes per 1x32 block.  All 32 lanes call this together.
 template <bool kGated>
 __device__ __forceinline__ void finish_row(const MoeArgs& g, const Segment& s, int row, int pair, int c8, bool on,
-                                           const float (&b)[8], float (&v)[8]) {
+                                           const uint32_t (&b)[4], float (&v)[8]) {
   const int n0 = s.nt * kTileN + 8 * c8;
   if (g.bias != nullptr) {                         // (no + 0 without one: -0 stays)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b[i];
+    for (int i = 0; i < 8; ++i) v[i] += __uint_as_float((i & 1) ? (b[i >> 1] & 0xFFFF0000u) : (b[i >> 1] << 16));
   }
   if constexpr (!kGated) {
     if (!on || n0 >= g.N) return;
@@ -496,12 +492,31 @@ __device__ __forceinline__ void finish_row(const MoeArgs& g, const Segment& s, i
   }
 }
 
-__device__ __forceinline__ void load_bias8(const MoeArgs& g, const Segment& s, int expert, int c8, float (&b)[8]) {
-  const int n0 = s.nt * kTileN + 8 * c8;
+// n neighbouring bias values of an expert from column n0 (zeros past N or
+// without a bias) as words of two, by wide loads where rows allow them.
+template <int kN>
+__device__ __forceinline__ void load_bias(const MoeArgs& g, int expert, int n0, uint32_t (&w)[kN / 2]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    b[i] = g.bias != nullptr && n0 + i < g.N
-               ? bf16_bits_to_float(__ldg(g.bias + static_cast<size_t>(expert) * g.N + n0 + i)) : 0.f;
+  for (int i = 0; i < kN / 2; ++i) w[i] = 0;
+  if (g.bias == nullptr || n0 >= g.N) return;
+  const uint16_t* p = g.bias + static_cast<size_t>(expert) * g.N + n0;
+  if (g.bias_vec != 0 && n0 + kN <= g.N) {
+    if constexpr (kN == 8) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[3] = v.w;
+    } else {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = v.x;
+      w[1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (n0 + i < g.N) w[i >> 1] |= static_cast<uint32_t>(__ldg(p + i)) << (16 * (i & 1));
+  }
 }
 
 // The sum of a cut tile's parts in CTA order, by all epilogue warps: a warp
@@ -510,8 +525,8 @@ __device__ __forceinline__ void load_bias8(const MoeArgs& g, const Segment& s, i
 template <bool kGated>
 __device__ __forceinline__ void finish_cut(const MoeArgs& g, const Walk& walk, const Segment& s, int expert, int rows,
                                            int c_lo, int c_hi, int warp, int lane) {
-  float b[8];
-  load_bias8(g, s, expert, lane, b);
+  uint32_t b[4];
+  load_bias<8>(g, expert, s.nt * kTileN + 8 * lane, b);
   constexpr int kRows = 4, kAhead = 2;
   const int count = c_hi - c_lo + 1;
   // lane l: where the part of contributor l stands
@@ -632,7 +647,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     s.half = hi.x;
     s.left = hi.y;
     s.info = hi.z;
-    s.first = hi.w;
     return s.rt >= 0;
   };
   auto done_segment = [&]() {
@@ -656,7 +670,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
       uint32_t phase = 1;
       while (next_segment()) {
         const int info = s.info, len = s.len, half = s.half;
-        int k = s.first;
         const uint8_t* base;
         uint32_t bytes, pitch;
         if (weights) {
@@ -669,10 +682,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
           bytes = loaded_rows(info >> 16) * 128 + C::kSA;
           pitch = kMoeBlockBytes;
         }
+        const uint8_t* src = base + static_cast<size_t>(s.k0) * pitch;
         done_segment();
-        for (int j = 0; j < len; ++j) {
-          const uint8_t* src = base + static_cast<size_t>(k) * pitch;
-          if (++k == g.KT) k = 0;
+        for (int j = 0; j < len; ++j, src += pitch) {
           if (!mbar_wait(&empty[st], phase, abort)) break;
           uint8_t* dst = smem + st * C::kStageBytes;
           mbar_arrive_expect_tx(&full[st], bytes);
@@ -718,7 +730,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     uint32_t phase = 0;
     for (int seg = 0; next_segment(); ++seg) {
       const int len = s.len, half = s.half;
-      int k = s.first;
+      int k = s.k0;
       if (s.rt != cur_rt) {
         cur_rt = s.rt;
         have = 0;
@@ -761,7 +773,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
           if (j + 1 == len) mma_commit(acc_full);
         }
         __syncwarp();
-        if (++k == g.KT) k = 0;
+        ++k;
         if (++st == C::kStages) {
           st = 0;
           phase ^= 1;
@@ -795,7 +807,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
       uint8_t* rec = segs + sslot * kSegBytes;
       if (lane == 0) {
         reinterpret_cast<int4*>(rec)[0] = make_int4(s.rt, s.nt, s.k0, s.len);
-        reinterpret_cast<int4*>(rec)[1] = make_int4(s.half, s.left, info, more ? first_step(g, s) : 0);
+        reinterpret_cast<int4*>(rec)[1] = make_int4(s.half, s.left, info, 0);
       }
       if (!kGated) reinterpret_cast<int4*>(rec + 32)[lane] = pairs;
       __syncwarp();
@@ -826,8 +838,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
       const int first_c8 = s.half > 0 ? 16 : 0;
       const int* pairs = reinterpret_cast<const int*>(segs + sslot * kSegBytes + 32);
       const int pair = rl < rows ? (kGated ? 0 : pairs[rl]) : -1;
-      float b[8];
-      if (few) load_bias8(g, s, expert, (lane + first_c8) & 31, b);
+      uint32_t b[4] = {0, 0, 0, 0}, b4[2] = {0, 0};
+      if (few)
+        load_bias<8>(g, expert, s.nt * kTileN + 8 * ((lane + first_c8) & 31), b);
+      else
+        load_bias<4>(g, expert, s.nt * kTileN + (s.half < 0 ? h : s.half) * 128 + 4 * lane, b4);
       // this warp has read the record (the pairs of few rows are read below)
       auto release = [&]() {
         __syncwarp();
@@ -884,7 +899,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
       }
       release();
       if (whole) {
-        if (q * 32 < rows) finish<kGated>(g, s, expert, pair, rl, h, lane, stage, r);
+        if (q * 32 < rows) finish<kGated>(g, s, make_uint2(b4[0], b4[1]), pair, rl, h, lane, stage, r);
         staged = true;
         continue;
       }
@@ -941,6 +956,7 @@ cudaError_t launch_moe_gemm(const MoeGemmProblem& p, const MoePlan& plan, const 
   a.w_packed = p.w_packed;
   a.w_stride = static_cast<size_t>(weight_packed_bytes(p.N, p.K));
   a.bias = static_cast<const uint16_t*>(p.bias);
+  a.bias_vec = (reinterpret_cast<uintptr_t>(p.bias) & 15) == 0 && p.N % 8 == 0;
   a.N = p.N;
   a.KT = static_cast<int>(padded_k(p.K) / kKTile);
   a.n_tiles = static_cast<int>(ceil_div(p.N, kTileN));
