@@ -17,7 +17,8 @@
 // The choice is exact: where two neighbours of the order up to place k + 1 (or
 // the last group taken and the first left out) lie nearer than the dropped
 // bits and the fp32 evaluation's error bound, the warp decides the row again
-// in 64 bits.  Equal inputs are no such case: their order is by the index.
+// in pairs of fp32, and where that does not settle it either, in fp64.
+// Equal inputs are no such case: their order is by the index.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -51,15 +52,8 @@ __device__ __forceinline__ uint32_t key_of(float v) {
   const uint32_t b = __float_as_uint(v + 0.f);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
-__device__ __forceinline__ uint64_t key_of(double v) {
-  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
-  return (b >> 63) ? ~b : (b | (1ull << 63));
-}
 __device__ __forceinline__ float from_key(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
-__device__ __forceinline__ double from_key(uint64_t k) {
-  return __longlong_as_double(static_cast<long long>((k >> 63) ? (k & ~(1ull << 63)) : ~k));
 }
 __device__ __forceinline__ uint32_t warp_max(uint32_t k) { return __reduce_max_sync(kAll, k); }
 __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
@@ -73,178 +67,324 @@ __device__ __forceinline__ F warp_sum(F v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
   return v;
 }
-__device__ __forceinline__ float exp_of(float v) { return expf(v); }
-__device__ __forceinline__ double exp_of(double v) { return exp(v); }
-
-// The score of logit x, given the row's largest logit and 1 / the sum of the
+// The score of logit x, given the row's largest logit and the sum of the
 // exponentials relative to it (softmax).
-template <typename F>
-__device__ __forceinline__ F score_of(bool sigmoid, float x, float m, F sum) {
-  if (sigmoid) return F(1) / (F(1) + exp_of(-static_cast<F>(x)));
-  if (x == -INFINITY || !(sum > F(0))) return F(0);
-  return (x == m ? F(1) : exp_of(static_cast<F>(x) - static_cast<F>(m))) / sum;
+__device__ __forceinline__ float score_of(bool sigmoid, float x, float m, float sum) {
+  if (sigmoid) return 1.f / (1.f + expf(-x));
+  return sum > 0.f ? (x == m ? 1.f : expf(x - m)) / sum : 0.f;
 }
 
-// Keeps the higher two of (best, next) and (b, n).
-template <typename F>
-__device__ __forceinline__ void higher_two(F& best, F& next, F b, F n) {
-  const F low = best < b ? best : b;
-  best = best < b ? b : best;
-  next = next < n ? n : next;
-  next = next < low ? low : next;
+// ---- Rows that fp32 cannot decide are decided again in more bits: in pairs
+// of fp32 (high + low part, together to 2^-40), and the very few that these
+// leave open in fp64.  (A 64-bit operation of this GPU takes some hundred
+// cycles: in fp64 alone one such row took 17 us, as long as all the others.)
+struct Pair {
+  float h, l;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair quick_sum(float a, float b) {   // |a| >= |b|
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  const float p = __fmul_rn(a.h, b.h);
+  return quick_sum(p, __fmaf_rn(a.l, b.h, __fmaf_rn(a.h, b.l, __fmaf_rn(a.h, b.h, -p))));
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const Pair s = two_sum(a.h, b.h);
+  return quick_sum(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+}
+__device__ __forceinline__ Pair reciprocal(Pair a) {            // one Newton step from fp32's
+  const float q = __frcp_rn(a.h);
+  const float r = __fmaf_rn(-a.l, q, __fmaf_rn(-a.h, q, 1.f));
+  return quick_sum(q, __fmul_rn(q, r));
+}
+__device__ __forceinline__ double mul(double a, double b) { return a * b; }
+__device__ __forceinline__ double add(double a, double b) { return a + b; }
+__device__ __forceinline__ double reciprocal(double a) { return 1.0 / a; }
+
+// e^(x.h + x.l) for -80 <= x <= 80, to 2^-41: x = n ln 2 + r, |r| <= 0.35, with
+// ln 2 in three parts of which the first has 14 bits (its products with n are
+// exact); the Taylor sum of e^r to r^12 / 12!, whose terms from r^6 on need
+// one fp32 only.
+__device__ __forceinline__ Pair exp_pair(Pair x) {
+  constexpr float kLn2a = 0x1.62e0p-1f, kLn2b = 0x1.0bfbe8p-15f, kLn2c = 0x1.cf79acp-40f;
+  const float n = rintf(__fmul_rn(x.h, 1.44269504f));
+  const float a = __fmaf_rn(-n, kLn2a, x.h);
+  const float p = __fmul_rn(n, kLn2b), e = __fmaf_rn(n, kLn2b, -p);
+  Pair r = two_sum(a, -p);
+  r = quick_sum(r.h, __fadd_rn(__fmaf_rn(-n, kLn2c, __fsub_rn(r.l, e)), x.l));
+  float t = 0x1.1eed8ep-29f;                                     // 1 / 12!
+  t = __fmaf_rn(t, r.h, 0x1.ae6456p-26f);
+  t = __fmaf_rn(t, r.h, 0x1.27e4fcp-22f);
+  t = __fmaf_rn(t, r.h, 0x1.71de3ap-19f);
+  t = __fmaf_rn(t, r.h, 0x1.a01a02p-16f);
+  t = __fmaf_rn(t, r.h, 0x1.a01a02p-13f);
+  t = __fmaf_rn(t, r.h, 0x1.6c16c2p-10f);                        // 1 / 6!
+  Pair s = {t, 0.f};
+  s = add({0x1.111112p-7f, -0x1.dddddep-32f}, mul(s, r));        // 1 / 5!
+  s = add({0x1.555556p-5f, -0x1.555556p-30f}, mul(s, r));
+  s = add({0x1.555556p-3f, -0x1.555556p-28f}, mul(s, r));
+  s = add({0.5f, 0.f}, mul(s, r));
+  s = add({1.f, 0.f}, mul(s, r));
+  s = add({1.f, 0.f}, mul(s, r));
+  const float scale = __int_as_float((127 + static_cast<int>(n)) << 23);
+  return {__fmul_rn(s.h, scale), __fmul_rn(s.l, scale)};
 }
 
-// The value of a group whose highest two compared values are best and next.
-template <typename F>
-__device__ __forceinline__ F group_value(int top, F best, F next) {
-  return top == 2 && next != -static_cast<F>(INFINITY) ? best + next : best;
+// e^(x - m), 0 below e^-80 in pairs, and the sigmoid of x, as it is at -80 and
+// 80 beyond these in pairs (2^-115: far below what pairs tell apart near 1; the
+// sums of two such scores and the same bias are equal there, so near).
+__device__ __noinline__ void exp_of_difference(float x, float m, Pair& y) {
+  y = {x == m ? 1.f : 0.f, 0.f};
+  if (x == m || x == -INFINITY) return;
+  const Pair d = two_sum(x, -m);
+  if (d.h >= -80.f) y = exp_pair(d);
+}
+__device__ __noinline__ void exp_of_difference(float x, float m, double& y) {
+  y = x == m ? 1.0 : x == -INFINITY ? 0.0 : exp(static_cast<double>(x) - static_cast<double>(m));
+}
+__device__ __noinline__ void sigmoid_of(float x, Pair& y) {
+  y = reciprocal(add({1.f, 0.f}, exp_pair({fminf(fmaxf(-x, -80.f), 80.f), 0.f})));
+}
+__device__ __noinline__ void sigmoid_of(float x, double& y) { y = 1.0 / (1.0 + exp(-static_cast<double>(x))); }
+
+// s + b of a score and a bias; infinities of b stay.
+__device__ __forceinline__ Pair plus_bias(Pair s, float b) {
+  return isinf(b) ? Pair{b, 0.f} : add(s, Pair{b, 0.f});
+}
+__device__ __forceinline__ double plus_bias(double s, float b) { return s + static_cast<double>(b); }
+
+// Order-preserving 64-bit images (-0 as +0), never 0; that of -inf is the lowest.
+__device__ __forceinline__ uint64_t key_of(Pair v) {
+  return (static_cast<uint64_t>(key_of(v.h)) << 32) | key_of(v.l);
+}
+__device__ __forceinline__ uint64_t key_of(double v) {
+  uint64_t b = static_cast<uint64_t>(__double_as_longlong(v));
+  if (b == 1ull << 63) b = 0;
+  return (b >> 63) ? ~b : (b | (1ull << 63));
+}
+__device__ __forceinline__ void from_key(uint64_t k, Pair& v) {
+  v = {from_key(static_cast<uint32_t>(k >> 32)), from_key(static_cast<uint32_t>(k))};
+}
+__device__ __forceinline__ void from_key(uint64_t k, double& v) {
+  v = __longlong_as_double(static_cast<long long>((k >> 63) ? (k & ~(1ull << 63)) : ~k));
+}
+__device__ __forceinline__ Pair shuffled(Pair v, int o) {
+  return {__shfl_xor_sync(kAll, v.h, o), __shfl_xor_sync(kAll, v.l, o)};
+}
+__device__ __forceinline__ double shuffled(double v, int o) { return __shfl_xor_sync(kAll, v, o); }
+__device__ __forceinline__ float rounded(Pair v) { return v.h; }
+__device__ __forceinline__ float rounded(double v) { return static_cast<float>(v); }
+// Whether pairs leave open which of a >= b is higher, scores being good to
+// `error`; never so in fp64.
+__device__ __forceinline__ bool open(Pair a, Pair b, float error) {
+  return (a.h - b.h) + (a.l - b.l) <= error + 0x1p-44f * (fabsf(a.h) + fabsf(b.h));
+}
+__device__ __forceinline__ bool open(double, double, float) { return false; }
+
+// Decides row t in numbers F (Pair or double).  Lane l holds elements l * V ..
+// l * V + V - 1 of the row, so the lowest lane and place of equal values is the
+// lowest index.  At the end lane r < k holds the r-th choice: its index (-1:
+// none), its logit and its score.  Returns whether a comparison that mattered
+// stayed open.
+__device__ __forceinline__ float logit_at(const RouteArgs& a, int t, int i) {
+  const int64_t at = static_cast<int64_t>(t) * a.ld + i;
+  return a.bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(a.x)[at]) : static_cast<const float*>(a.x)[at];
 }
 
-// Decides one row in 64 bits.  Lane l holds elements l * V .. l * V + V - 1 of
-// the row, so the lowest lane and place of equal values is the lowest index.
-// At the end lane r < k holds the r-th choice: its index (-1: none), its logit
-// and its score.
-template <int V>
-__device__ __forceinline__ void decide_exactly(const RouteArgs& a, const float (&x)[V], int lane, int& idx, float& xsel,
-                                               double& ssel) {
-  using F = double;
-  using K = uint64_t;
-  const F ninf = -static_cast<F>(INFINITY);
+template <int V, typename F>
+__device__ __forceinline__ bool decide_in(const RouteArgs& a, int t, int lane, int& idx, float& xsel, float& ssel) {
   const bool biased = a.bias != nullptr, sigmoid = a.sigmoid != 0;
+  constexpr uint64_t none = 0;                     // the key of what is switched off
+  float x[V];
   float m = -INFINITY;
-  F sum = 0;
-  if (!sigmoid) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) m = fmaxf(m, x[j]);
-    m = from_key(warp_max(key_of(m)));
-    if (m > -INFINITY) {
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (x[j] != -INFINITY) sum += x[j] == m ? F(1) : exp_of(static_cast<F>(x[j]) - static_cast<F>(m));
-    }
-    sum = warp_sum(sum);
-  }
-  // what is compared; sums of logits would not order as sums of scores do
-  const bool by_score = a.groups > 1 && !biased && a.top == 2;
-  K key[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int i = lane * V + j;
-    F c = static_cast<F>(x[j]);
-    if (biased && i < a.E) c = score_of<F>(sigmoid, x[j], m, sum) + static_cast<F>(__ldg(a.bias + i));
-    key[j] = key_of(x[j] == -INFINITY || !(c == c) ? ninf : c);
+    const float v = lane * V + j < a.E ? logit_at(a, t, lane * V + j) : -INFINITY;
+    x[j] = v == v ? v : -INFINITY;
+    m = fmaxf(m, x[j]);
   }
+  m = from_key(warp_max(key_of(m)));
+  // what is compared; sums of logits would not order as sums of scores do
+  const bool by_score = a.groups > 1 && !biased && a.top == 2;
+  F s[V];
+  float unit = 1.f;                                // softmax: 1 / the sum
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if (sigmoid)
+      sigmoid_of(x[j], s[j]);
+    else
+      exp_of_difference(x[j], m, s[j]);
+  }
+  if (!sigmoid && m > -INFINITY) {
+    F sum = s[0];
+#pragma unroll
+    for (int j = 1; j < V; ++j) sum = add(sum, s[j]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum = add(sum, shuffled(sum, o));
+    const F r = reciprocal(sum);
+    unit = rounded(r);
+#pragma unroll
+    for (int j = 0; j < V; ++j) s[j] = mul(s[j], r);
+  }
+  uint64_t key[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const float b = biased && lane * V + j < a.E ? __ldg(a.bias + lane * V + j) : 0.f;
+    const bool on = x[j] > -INFINITY && b > -INFINITY;   // (a NaN bias switches off too)
+    key[j] = !on ? none : biased ? key_of(plus_bias(s[j], b)) : static_cast<uint64_t>(key_of(x[j])) << 32;
+  }
+  const float error = 0x1p-39f * unit;
+  bool near = false;
   if (a.groups > 1) {
     const int size = a.E / a.groups;
     const int span = size / V;                     // lanes of a group, where groups are whole lanes
     const bool whole = span * V == size && (span & (span - 1)) == 0 && span > 0;
-    K gkey = key_of(ninf);
+    uint64_t best = none, next = none;
+    auto meet = [&](uint64_t b, uint64_t n) {
+      next = max(max(next, n), min(best, b));
+      best = max(best, b);
+    };
+    auto compared = [&](int j) { return by_score && key[j] != none ? key_of(s[j]) : key[j]; };
+    auto value = [&]() {                           // the key of the group's value
+      if (best == none || a.top == 1 || next == none) return best;
+      F v1, v2;
+      from_key(best, v1);
+      from_key(next, v2);
+      return key_of(isinf(rounded(v1)) || isinf(rounded(v2)) ? v1 : add(v1, v2));
+    };
+    uint64_t gkey = none;
     int group = lane;                              // the group whose value this lane holds
     if (whole) {
-      F best = ninf, next = ninf;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        F v = from_key(key[j]);
-        if (by_score && v != ninf) v = score_of<F>(sigmoid, x[j], m, sum);
-        higher_two(best, next, v, ninf);
-      }
-      for (int o = 1; o < span; o <<= 1) {
-        const F b = __shfl_xor_sync(kAll, best, o), n = __shfl_xor_sync(kAll, next, o);
-        higher_two(best, next, b, n);
-      }
-      gkey = key_of(group_value(a.top, best, next));
+      for (int j = 0; j < V; ++j) meet(compared(j), none);
+      for (int o = 1; o < span; o <<= 1) meet(__shfl_xor_sync(kAll, best, o), __shfl_xor_sync(kAll, next, o));
+      gkey = value();
       group = lane / span;
     } else {
+#pragma unroll 1
       for (int g = 0; g < a.groups; ++g) {
-        F best = ninf, next = ninf;
+        best = next = none;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const int i = lane * V + j;
-          if (i >= g * size && i < (g + 1) * size) {
-            F v = from_key(key[j]);
-            if (by_score && v != ninf) v = score_of<F>(sigmoid, x[j], m, sum);
-            higher_two(best, next, v, ninf);
-          }
-        }
-        for (int o = 1; o < 32; o <<= 1) {
-          const F b = __shfl_xor_sync(kAll, best, o), n = __shfl_xor_sync(kAll, next, o);
-          higher_two(best, next, b, n);
-        }
-        if (lane == g) gkey = key_of(group_value(a.top, best, next));
+        for (int j = 0; j < V; ++j)
+          if ((lane * V + j) / size == g) meet(compared(j), none);
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) meet(__shfl_xor_sync(kAll, best, o), __shfl_xor_sync(kAll, next, o));
+        if (lane == g) gkey = value();
       }
     }
-    if (group >= a.groups) gkey = 0;               // (lanes past the last group)
+    if (group >= a.groups) gkey = none;            // (lanes past the last group)
     uint32_t kept = 0;
-    for (int r = 0; r < a.keep; ++r) {
-      const K top = warp_max(gkey);
+    uint64_t last = none;
+#pragma unroll 1
+    for (int r = 0; r <= a.keep; ++r) {
+      const uint64_t top = warp_max(gkey);
+      if (top == none) break;
+      if (r == a.keep) {
+        F v1, v2;
+        from_key(last, v1);
+        from_key(top, v2);
+        near = (biased || by_score) && last != top && open(v1, v2, 2.f * error);
+        break;
+      }
       const int g = __shfl_sync(kAll, group, __ffs(__ballot_sync(kAll, gkey == top)) - 1);
+      last = top;
       kept |= 1u << g;
-      if (group == g) gkey = 0;
+      if (group == g) gkey = none;
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int g = whole ? group : (lane * V + j) / size;
-      if (g >= a.groups || !((kept >> g) & 1u)) key[j] = key_of(ninf);
+      const int g = (lane * V + j) / size;
+      if (g >= a.groups || !((kept >> g) & 1u)) key[j] = none;
     }
   }
-
-  // k rounds of the maximum over the warp and the lowest lane that has it
+  // k rounds of the maximum over the warp and the lowest lane that has it, and
+  // one more to see how near the first one left out is
   idx = -1;
   xsel = 0.f;
-  const K none = key_of(ninf);
-  for (int r = 0; r < a.k; ++r) {
-    K best = key[0];
+  ssel = 0.f;
+  uint64_t mine = none, after = none;              // lane r: the key of choice r; every lane: of the one left out
+  int iafter = -1;
+#pragma unroll 1
+  for (int r = 0; r <= a.k; ++r) {
+    uint64_t best = key[0];
     int at = 0;
-    float bx = x[0];
+    float bs = rounded(s[0]);
 #pragma unroll
     for (int j = 1; j < V; ++j)
       if (key[j] > best) {
         best = key[j];
         at = j;
-        bx = x[j];
+        bs = rounded(s[j]);
       }
-    const K top = warp_max(best);
-    if (top <= none) break;
+    const uint64_t top = warp_max(best);
+    if (top == none) break;
     const int who = __ffs(__ballot_sync(kAll, best == top)) - 1;
     const int i = __shfl_sync(kAll, lane * V + at, who);
-    const float xv = __shfl_sync(kAll, bx, who);
+    const float sv = __shfl_sync(kAll, bs, who);
+    if (r == a.k) {
+      after = top;
+      iafter = i;
+      break;
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (lane == who && j == at) key[j] = 0;
+      if (lane == who && j == at) key[j] = none;
     if (lane == r) {
+      mine = top;
       idx = i;
-      xsel = xv;
+      ssel = sv;
     }
   }
-  ssel = idx >= 0 ? score_of<F>(sigmoid, xsel, m, sum) : F(0);
+  if (idx >= 0) xsel = logit_at(a, t, idx);
+  if (biased) {
+    uint64_t key2 = __shfl_down_sync(kAll, mine, 1);
+    int i2 = __shfl_down_sync(kAll, idx, 1);
+    if (lane == a.k - 1) {
+      key2 = after;
+      i2 = iafter;
+    }
+    if (lane < a.k && idx >= 0 && i2 >= 0) {
+      F v1, v2;
+      from_key(mine, v1);
+      from_key(key2, v2);
+      const bool same = xsel == logit_at(a, t, i2) && __ldg(a.bias + idx) == __ldg(a.bias + i2);
+      near = near || (open(v1, v2, error) && !same);
+    }
+  }
+  return __any_sync(kAll, near);
 }
 
 // The weight of this lane's choice.  Renormalised weights use scores relative
 // to the largest chosen one, which do not vanish where all scores are small.
-template <typename F>
-__device__ __forceinline__ float weight_of(const RouteArgs& a, int idx, float xsel, F ssel) {
+__device__ __forceinline__ float weight_of(const RouteArgs& a, int idx, float xsel, float ssel) {
   const bool on = idx >= 0;
-  if (!a.renorm) return on ? static_cast<float>(static_cast<F>(a.scale) * ssel) : 0.f;
+  if (!a.renorm) return on ? a.scale * ssel : 0.f;
   const float m = from_key(warp_max(key_of(on ? xsel : -INFINITY)));
-  F e = 0;
+  float e = 0.f;
   if (on) {
     if (a.sigmoid) {
-      const F c = m < 0.f ? static_cast<F>(m) : F(0);
-      e = F(1) / (exp_of(c) + exp_of(c - static_cast<F>(xsel)));
+      const float c = fminf(m, 0.f);
+      e = 1.f / (expf(c) + expf(c - xsel));
     } else {
-      e = xsel == m ? F(1) : exp_of(static_cast<F>(xsel) - static_cast<F>(m));
+      e = xsel == m ? 1.f : expf(xsel - m);
     }
   }
-  const F total = warp_sum(e);
-  return on ? static_cast<float>(static_cast<F>(a.scale) * e / total) : 0.f;
+  const float total = warp_sum(e);
+  return on ? a.scale * e / total : 0.f;
 }
 
-template <int V>
-__device__ __noinline__ void decide_in_64_bits(const RouteArgs& a, const float (&x)[V], int lane, int& idx, float& w) {
-  float xsel;
-  double ssel;
-  decide_exactly<V>(a, x, lane, idx, xsel, ssel);
-  w = weight_of<double>(a, idx, xsel, ssel);
+// A row that fp32 cannot decide, and its weights.
+template <int V, typename F>
+__device__ __noinline__ bool decide_again(const RouteArgs& a, int t, int lane, int& idx, float& w) {
+  float xsel, ssel;
+  const bool near = decide_in<V, F>(a, t, lane, idx, xsel, ssel);
+  w = weight_of(a, idx, xsel, ssel);
+  return near;
 }
 
 // This lane's V biases (zeros past E).
@@ -266,10 +406,11 @@ __device__ __forceinline__ void load_bias(const RouteArgs& a, int lane, float (&
   }
 }
 
-// key_of(v) with the place j in its lowest five bits, the lower place higher;
+// key_of(v) with the place j of V in its lowest bits, the lower place higher;
 // 0 for what is switched off.
-constexpr uint32_t kPlace = 31u;
+template <int V>
 __device__ __forceinline__ uint32_t placed_key(float v, int j) {
+  constexpr uint32_t kPlace = V - 1;
   return v > -INFINITY ? (key_of(v) & ~kPlace) | (kPlace - j) : 0u;   // (a NaN is switched off too)
 }
 
@@ -292,16 +433,13 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[V]) {
         }
 }
 
-__device__ __forceinline__ float logit_at(const RouteArgs& a, int t, int i) {
-  const int64_t at = static_cast<int64_t>(t) * a.ld + i;
-  return a.bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(a.x)[at]) : static_cast<const float*>(a.x)[at];
-}
-
 // Decides row t in fp32, as decide_exactly does.  Returns whether a comparison
 // that mattered was too near for fp32.
 template <int V>
 __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&x)[V], int lane, int& idx, float& xsel,
                                        float& ssel) {
+  constexpr uint32_t kPlace = V - 1;               // bits of a key that hold the place
+  constexpr float kDropped = V * 0x1p-23f;         // what they can be of a value
   const bool biased = a.bias != nullptr, sigmoid = a.sigmoid != 0;
   const bool by_score = a.groups > 1 && !biased && a.top == 2;
   float m = -INFINITY, sum = 0.f;
@@ -316,8 +454,9 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&
     }
     sum = warp_sum(sum);
   }
-  // Fast scores err by less than 2^-20 of the largest possible one, `unit`:
-  // the exponential of -v errs by (2 + 1.2 v) 2^-23 e^-v < 2^-21.
+  // Fast scores err by less than 2^-21 of the largest possible one, `unit`: the
+  // exponential of -v by at most (2 + 1.2 v) 2^-23 e^-v < 2^-22, which a sum or
+  // 1 + e^-v only divides; the division adds 2^-23.
   const float unit = sigmoid ? 1.f : sum > 0.f ? __fdividef(1.f, sum) : 0.f;
   auto fast_score = [&](float v) {
     return sigmoid ? __fdividef(1.f, 1.f + __expf(-v)) : (v == m ? 1.f : __expf(v - m)) * unit;
@@ -326,10 +465,10 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&
     float b[V];
     load_bias<V>(a, lane, b);
 #pragma unroll
-    for (int j = 0; j < V; ++j) key[j] = x[j] > -INFINITY ? placed_key(fast_score(x[j]) + b[j], j) : 0u;
+    for (int j = 0; j < V; ++j) key[j] = x[j] > -INFINITY ? placed_key<V>(fast_score(x[j]) + b[j], j) : 0u;
   } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) key[j] = placed_key(x[j], j);
+    for (int j = 0; j < V; ++j) key[j] = placed_key<V>(x[j], j);
   }
   sort_down<V>(key);
   bool near = false;
@@ -341,19 +480,19 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&
     uint32_t gkey = 0;
     float gerr = 0.f;
     int group = lane;                              // the group whose value this lane holds
-    // Of the values that stand for a key: the dropped bits (2^-18) and the scores' errors.
+    // Of the values that stand for a key: the dropped bits and the scores' errors.
     auto value_of = [&](uint32_t k, float& err) {
       if (k == 0) return -INFINITY;
       const float c = from_key(k & ~kPlace);
       const float v = by_score ? fast_score(c) : c;
-      err += biased ? 0x1p-18f * fabsf(c) + 0x1p-20f * unit
-                    : by_score ? 0x1p-20f * unit + 0x1p-17f * fabsf(c) * v : 0x1p-18f * fabsf(c);
+      err += biased ? kDropped * fabsf(c) + 0x1p-21f * unit
+                    : by_score ? 0x1p-21f * unit + 2.f * kDropped * fabsf(c) * v : kDropped * fabsf(c);
       return v;
     };
     auto set_group = [&](uint32_t best, uint32_t next) {
       float e = 0.f;
       const float v1 = value_of(best, e), v2 = a.top == 2 ? value_of(next, e) : -INFINITY;
-      gkey = best != 0 ? key_of(group_value(a.top, v1, v2)) : 0u;
+      gkey = best != 0 ? key_of(v2 > -INFINITY ? v1 + v2 : v1) : 0u;
       gerr = e + 0x1p-22f * fabsf(v1);
     };
     if (whole) {
@@ -418,6 +557,7 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&
     }
   }
 
+  near = __any_sync(kAll, near);
   // k rounds, and one more to see how near the first one left out is
   uint32_t mine = 0, after = 0;                    // lane r: what stands for choice r; every lane: for the one left out
   int iafter = -1;
@@ -452,16 +592,20 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&
     i2 = iafter;
     if (i2 >= 0) x2 = logit_at(a, t, i2);
   }
+  bool close = false;
+  auto tolerance = [&](float c) { return kDropped * fabsf(c) + 0x1p-21f * unit; };
   if (lane < a.k && idx >= 0 && i2 >= 0) {
     if (biased) {
       const float c1 = from_key(mine), c2 = from_key(key2);
       const bool same = xsel == x2 && __ldg(a.bias + idx) == __ldg(a.bias + i2);
-      near = near || (c1 - c2 <= 0x1p-18f * (fabsf(c1) + fabsf(c2)) + 0x1p-19f * unit && !same);
+      close = c1 - c2 <= tolerance(c1) + tolerance(c2) && !same;
     } else {
-      near = near || (mine == key2 && xsel != x2);
+      close = mine == key2 && xsel != x2;
     }
   }
-  ssel = idx >= 0 && !a.renorm ? score_of<float>(sigmoid, xsel, m, sum) : 0.f;
+  close = __any_sync(kAll, close);
+  near = near || close;
+  ssel = idx >= 0 && !a.renorm ? score_of(sigmoid, xsel, m, sum) : 0.f;
   return __any_sync(kAll, near);
 }
 
@@ -529,9 +673,11 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : V <= 16 ? 5 : 2) moe_route_k
   int idx;
   float xsel, ssel, w;
   if (decide<V>(a, t, x, lane, idx, xsel, ssel))
-    decide_in_64_bits<V>(a, x, lane, idx, w);
+{
+    if (decide_again<V, Pair>(a, t, lane, idx, w)) decide_again<V, double>(a, t, lane, idx, w);
+  }
   else
-    w = weight_of<float>(a, idx, xsel, ssel);
+    w = weight_of(a, idx, xsel, ssel);
   if (lane < a.k) {
     const int64_t o = static_cast<int64_t>(t) * a.k + lane;
     a.ids[o] = idx;
