@@ -538,7 +538,7 @@ static MoeWorkspace moe_workspace_layout(int64_t P, int E, int K, int I, int N, 
   w.a = round_up(moe_plan_bytes(P, E), 1024);
   w.h = w.a + static_cast<size_t>(rt * (padded_k(K) / kKTile)) * kMoeBlockBytes;
   w.results = w.h + (I > 0 ? static_cast<size_t>(rt * (padded_k(I) / kKTile)) * kMoeBlockBytes : 0);
-  w.ldp = ceil_div(N, 16) * 16;
+  w.ldp = weight_rows(N);   // whole tiles: no row of the results ends inside one
   w.parts = w.results + (I > 0 ? round_up(static_cast<size_t>(P * w.ldp) * 2, 1024) : 0);
   w.total = w.parts + moe_gemm_parts_bytes(sm_count);
   return w;
@@ -586,8 +586,7 @@ mxfp4_status mxfp4_moe_linear(const void* x, int64_t ldx, const int32_t* ids, co
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const MoePlan plan = moe_plan_at(ws + w.plan, P, E);
-  cudaError_t e = launch_moe_plan(ids, static_cast<int>(P), E, plan, dev, s);
-  if (e == cudaSuccess) e = launch_moe_gather(x, ldx, T, top_k, K, plan, ws + w.a, out, ldo, N, dev, s);
+  cudaError_t e = launch_moe_plan_gather(ids, E, x, ldx, T, top_k, K, plan, ws + w.a, out, ldo, N, dev, s);
   MoeGemmProblem p{};
   p.a_blocks = ws + w.a;
   p.w_packed = static_cast<const uint8_t*>(w_packed);
@@ -597,7 +596,9 @@ mxfp4_status mxfp4_moe_linear(const void* x, int64_t ldx, const int32_t* ids, co
   p.K = K;
   p.out = out;
   p.ldo = ldo;
+  p.out_n = N;
   p.which = 0;
+  p.plan_late = moe_plan_with_gather(static_cast<int>(P));
   p.parts = reinterpret_cast<float*>(ws + w.parts);
   if (e == cudaSuccess) e = launch_moe_gemm(p, plan, dev, s);
   return from_cuda(e);
@@ -629,8 +630,7 @@ mxfp4_status mxfp4_moe_ffn(const void* x, int64_t ldx, const int32_t* ids, const
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const MoePlan plan = moe_plan_at(ws + w.plan, P, E);
-  cudaError_t e = launch_moe_plan(ids, static_cast<int>(P), E, plan, dev, s);
-  if (e == cudaSuccess) e = launch_moe_gather(x, ldx, T, top_k, K, plan, ws + w.a, nullptr, 0, 0, dev, s);
+  cudaError_t e = launch_moe_plan_gather(ids, E, x, ldx, T, top_k, K, plan, ws + w.a, nullptr, 0, 0, dev, s);
   MoeGemmProblem p{};
   p.a_blocks = ws + w.a;
   p.w_packed = static_cast<const uint8_t*>(w_gate_up);
@@ -643,6 +643,7 @@ mxfp4_status mxfp4_moe_ffn(const void* x, int64_t ldx, const int32_t* ids, const
   p.alpha = alpha;
   p.limit = limit;
   p.which = 0;
+  p.plan_late = moe_plan_with_gather(static_cast<int>(P));
   p.parts = reinterpret_cast<float*>(ws + w.parts);
   if (e == cudaSuccess) e = launch_moe_gemm(p, plan, dev, s);
   p.a_blocks = ws + w.h;
@@ -653,7 +654,9 @@ mxfp4_status mxfp4_moe_ffn(const void* x, int64_t ldx, const int32_t* ids, const
   p.h_blocks = nullptr;
   p.out = ws + w.results;
   p.ldo = w.ldp;
+  p.out_n = static_cast<int>(w.ldp);
   p.which = 1;
+  p.plan_late = false;
   if (e == cudaSuccess) e = launch_moe_gemm(p, plan, dev, s);
   if (e == cudaSuccess)
     e = launch_moe_combine(ws + w.results, w.ldp, weights, plan, residual, ldr, out, ldo, T, top_k, N, dev, s);

@@ -47,12 +47,14 @@ inline int64_t moe_max_tiles(int64_t P, int E) { return P / kRowTile + (P < E ? 
 size_t moe_plan_bytes(int64_t P, int E);
 MoePlan moe_plan_at(void* base, int64_t P, int E);
 
-cudaError_t launch_moe_plan(const int32_t* ids, int P, int E, const MoePlan& plan, const DeviceInfo& dev,
-                            cudaStream_t s);
-// Q(x[t]) to the sorted rows of the token's pairs, in blocked form; rows of
-// `zero` (bf16 [P][ldz], N values, or null) whose pair has no expert are zeroed.
-cudaError_t launch_moe_gather(const void* x, int64_t ldx, int T, int top_k, int K, const MoePlan& plan,
-                              uint8_t* blocks, void* zero, int64_t ldz, int N, const DeviceInfo& dev, cudaStream_t s);
+// The plan, and Q(x[t]) to the sorted rows of the token's pairs in blocked form;
+// rows of `zero` (bf16 [P][ldz], N values, or null) whose pair has no expert are
+// zeroed.
+cudaError_t launch_moe_plan_gather(const int32_t* ids, int E, const void* x, int64_t ldx, int T, int top_k, int K,
+                                   const MoePlan& plan, uint8_t* blocks, void* zero, int64_t ldz, int N,
+                                   const DeviceInfo& dev, cudaStream_t s);
+// Whether the same kernel does both (the plan is complete only when it is).
+bool moe_plan_with_gather(int P);
 // out[t] = bf16(residual[t] + sum_j weights[t][j] * parts[t * top_k + j]).
 cudaError_t launch_moe_combine(const void* parts, int64_t ldp, const float* weights, const MoePlan& plan,
                                const void* residual, int64_t ldr, void* out, int64_t ldo, int T, int top_k, int N,
@@ -70,10 +72,12 @@ struct MoeGemmProblem {
   // the blocked activations of N / 2 columns.
   void* out;
   int64_t ldo;
+  int out_n;                // columns of out that may be written: N, or more where the row is padded
   uint8_t* h_blocks;
   MoeAct act;
   float alpha, limit;
   int which;                // ticket set
+  bool plan_late;           // the plan is not complete before the kernel ahead of this one is
   float* parts;             // moe_gemm_parts_bytes()
 };
 size_t moe_gemm_parts_bytes(int sm_count);

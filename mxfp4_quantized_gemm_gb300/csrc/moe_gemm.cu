@@ -54,11 +54,9 @@ constexpr int kFewRows = 32;                       // rows up to which a tile is
 constexpr int kMoeThreads = 384;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kFewBatch = 16;                      // rows of a tile of few rows that are handed out at once
-// Staging of the bf16 rows: per epilogue warp 32 rows x 32 columns (64 bytes),
-// 16-byte pieces rotated by the row so that 8 lanes meet 8 different banks
-// both when they hold 8 rows and when they hold 2 rows' 4 pieces.
-constexpr int kStageWarp = 32 * 64;
-__device__ __forceinline__ int stage_at(int row, int piece) { return row * 64 + ((piece ^ (row >> 1)) & 3) * 16; }
+// Staging of bf16 rows that allow no wide access: per epilogue warp 8 rows of
+// 128 columns.
+constexpr int kStageWarp = 8 * 256;
 static_assert(8 * kStageWarp >= kFewBatch * kTileN * 4, "the rows handed out share the staging area");
 // Segments found ahead: the record of each and the pairs of its rows.
 constexpr int kSegs = 8;
@@ -76,6 +74,7 @@ struct MoeArgs {
   int N, KT, n_tiles, unit;
   uint16_t* out;
   int64_t ldo;
+  int out_n;                                       // columns of out that may be written (N, or padding too)
   int out_vec;                                     // rows of out allow 16-byte accesses
   uint8_t* h_blocks;
   int KT2;
@@ -85,6 +84,7 @@ struct MoeArgs {
   const int32_t* row_pair;
   int32_t* tickets;
   float* parts;
+  int plan_late;                                   // the kernel before this one makes the plan
 };
 
 struct __align__(16) Segment {
@@ -311,11 +311,9 @@ __device__ __forceinline__ float gated(const MoeArgs& g, float gate, float up) {
 }
 
 // 128 columns of one row (acc), from column n0 of its expert: stored as bf16,
-// or gated and quantized.  Rows of bf16 go through the warp's staging area, 32
-// columns at a time, so that four lanes write 64 neighbouring bytes of a row
-// (written by the lane that holds the row, 16 bytes apart by a whole row, they
-// took twice as long).  `pair`: the row's pair, -1 past the live rows.  All 32
-// lanes call this together.
+// or gated and quantized.  `pair`: the row's pair, -1 past the live rows;
+// `bias`: of columns n0 + 4 lane .. n0 + 4 lane + 3.  All 32 lanes call this
+// together.
 template <bool kGated>
 __device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, uint2 bias, int pair, int rl, int h, int lane,
                                        uint8_t* stage, uint32_t (&acc)[128]) {
@@ -333,7 +331,7 @@ __device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, uint2
     }
   }
   if constexpr (!kGated) {
-    if (g.out_vec != 0 && n0 + 128 <= g.N) {
+    if (g.out_vec != 0 && n0 + 128 <= g.out_n) {
       // Four lanes exchange their rows' 16-column pieces until each holds the
       // same piece of all four rows: then they write 128 neighbouring bytes of a
       // row, whole cache lines.  (64 bytes at a time through shared memory, the
@@ -378,41 +376,61 @@ __device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, uint2
       }
       return;
     }
-    int64_t row[4];                                // offsets of the rows this lane writes: lane / 4 + 8 i
-    uint32_t on = 0;
+    // Rows that allow no wide access or end inside the tile: 8 rows at a time
+    // through the warp's staging area (16-byte pieces rotated by the row), then
+    // 16 bytes at an aligned address of the output by each lane, put together
+    // from the two pieces they span.  (Column by column, 64 bytes a row and
+    // store, 1500 x 2 tokens of 1001 columns took 30 us, 13 of them here.)
+    const int count = g.N - n0 < 128 ? g.N - n0 : 128;
+    for (int b = 0; b < 4; ++b) {
+      if ((lane >> 3) == b) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int p = __shfl_sync(0xFFFFFFFFu, pair, (lane >> 2) + 8 * i);
-      row[i] = static_cast<int64_t>(p) * g.ldo + n0 + 8 * (lane & 3);
-      on |= p >= 0 ? 1u << i : 0u;
-    }
-#pragma unroll
-    for (int c0 = 0; c0 < 128; c0 += 32) {
-      if (n0 + c0 >= g.N) break;                   // uniform
-#pragma unroll
-      for (int c = 0; c < 32; c += 8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = pack_bf16x2(__uint_as_float(acc[c0 + c + 2 * i]), __uint_as_float(acc[c0 + c + 2 * i + 1]));
-        *reinterpret_cast<uint4*>(stage + stage_at(lane, c >> 3)) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int c = 0; c < 16; ++c)
+          *reinterpret_cast<uint4*>(stage + (lane & 7) * 256 + ((c ^ lane) & 7) * 16 + (c & 8) * 16) = make_uint4(
+              pack_bf16x2(__uint_as_float(acc[8 * c]), __uint_as_float(acc[8 * c + 1])),
+              pack_bf16x2(__uint_as_float(acc[8 * c + 2]), __uint_as_float(acc[8 * c + 3])),
+              pack_bf16x2(__uint_as_float(acc[8 * c + 4]), __uint_as_float(acc[8 * c + 5])),
+              pack_bf16x2(__uint_as_float(acc[8 * c + 6]), __uint_as_float(acc[8 * c + 7])));
       }
       __syncwarp();
-      if (g.out_vec != 0 && n0 + c0 + 32 <= g.N) {
-        uint4 w[4];
+#pragma unroll 1
+      for (int at = lane; at < 8 * 17 + 24; at += 32) {   // (whole warps loop: 8 rows of 17 places)
+        const int r = at / 17, w = at - 17 * r;
+        const int p = __shfl_sync(0xFFFFFFFFu, pair, (8 * b + r) & 31);
+        if (r >= 8 || p < 0) continue;
+        uint16_t* dst = g.out + static_cast<int64_t>(p) * g.ldo + n0;
+        const int m = static_cast<int>((reinterpret_cast<uintptr_t>(dst) >> 1) & 7);
+        const int c = 8 * w - m;                   // the place's first column
+        if (c >= count) continue;
+        const uint8_t* src = stage + r * 256;
+        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;   // pieces w - 1 and w
+        if (w > 0) lo = *reinterpret_cast<const uint4*>(src + (((w - 1) ^ r) & 7) * 16 + ((w - 1) & 8) * 16);
+        if (w < 16) hi = *reinterpret_cast<const uint4*>(src + ((w ^ r) & 7) * 16 + (w & 8) * 16);
+        // 8 values from the (8 - m)-th of the two pieces on
+        uint32_t q[9] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w, 0};
+        const int skip = 8 - m;
+        if (skip & 8) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = *reinterpret_cast<const uint4*>(stage + stage_at((lane >> 2) + 8 * i, lane & 3));
+          for (int i = 0; i < 4; ++i) q[i] = q[i + 4];
+        }
+        if (skip & 4) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if ((on >> i) & 1u) *reinterpret_cast<uint4*>(g.out + row[i] + c0) = w[i];
-      } else {                                     // rows that allow no wide access: a lane per column
-#pragma unroll 4
-        for (int i = 0; i < 32; ++i) {
-          const int p = __shfl_sync(0xFFFFFFFFu, pair, i);
-          if (p >= 0 && n0 + c0 + lane < g.N)
-            g.out[static_cast<int64_t>(p) * g.ldo + n0 + c0 + lane] =
-                *reinterpret_cast<const uint16_t*>(stage + stage_at(i, lane >> 3) + 2 * (lane & 7));
+          for (int i = 0; i < 6; ++i) q[i] = q[i + 2];
+        }
+        if (skip & 2) {
+#pragma unroll
+          for (int i = 0; i < 5; ++i) q[i] = q[i + 1];
+        }
+        if (skip & 1) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q[i] = __funnelshift_r(q[i], q[i + 1], 16);
+        }
+        if (c >= 0 && c + 8 <= count) {
+          *reinterpret_cast<uint4*>(dst + c) = make_uint4(q[0], q[1], q[2], q[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (c + e >= 0 && c + e < count) dst[c + e] = static_cast<uint16_t>(q[e >> 1] >> (16 * (e & 1)));
         }
       }
       __syncwarp();
@@ -458,7 +476,7 @@ __device__ __forceinline__ void finish_row(const MoeArgs& g, const Segment& s, i
   if constexpr (!kGated) {
     if (!on || n0 >= g.N) return;
     uint16_t* dst = g.out + static_cast<int64_t>(pair) * g.ldo + n0;
-    if (g.out_vec != 0 && n0 + 8 <= g.N) {
+    if (g.out_vec != 0 && n0 + 8 <= g.out_n) {
       *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                                   pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     } else {
@@ -784,9 +802,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     __syncwarp();
    } else {
     // ---- warp 3: the segments of this CTA, ahead of the other roles.  The plan
-    // is complete when this kernel starts: the kernel before it lets it start
-    // only after its own wait for the plan.  A segment's tile word and pairs
-    // are loaded while the one before it is handed out.
+    // is complete when this kernel starts (the kernel before it lets it start
+    // only after its own wait for the plan), but where that kernel makes the
+    // plan.  A segment's tile word and pairs are loaded while the one before
+    // it is handed out.
+    if (g.plan_late) griddep_wait();
     Walk walk;
     walk.init(g, __ldcg(g.hdr));
     int rt = -1;
@@ -963,6 +983,7 @@ cudaError_t launch_moe_gemm(const MoeGemmProblem& p, const MoePlan& plan, const 
   a.unit = a.n_tiles < kUnit ? a.n_tiles : kUnit;
   a.out = static_cast<uint16_t*>(p.out);
   a.ldo = p.ldo;
+  a.out_n = p.out_n;
   a.out_vec = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0 && p.ldo % 16 == 0  ? 2
               : (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && p.ldo % 8 == 0 ? 1
                                                                                  : 0;
@@ -978,6 +999,7 @@ cudaError_t launch_moe_gemm(const MoeGemmProblem& p, const MoePlan& plan, const 
   a.row_pair = plan.row_pair;
   a.tickets = plan.tickets + p.which * kMoeTickets;
   a.parts = p.parts;
+  a.plan_late = p.plan_late;
   return p.h_blocks != nullptr ? launch<true>(a, dev, s) : launch<false>(a, dev, s);
 }
 

@@ -174,6 +174,39 @@ struct GatherArgs {
   int N;
 };
 
+// This lane's 8 values of k-tile kt of token t, and the block's quantization of
+// them written to the sorted rows of the token's pairs (lane j holds pair j's,
+// -1 without an expert: its row of `zero`, if any, is zeroed, each k-tile's
+// warp a share of it).
+__device__ __forceinline__ uint4 load_unit(const GatherArgs& a, int t, int kt, int lane) {
+  // load8_words indexes rows by an int leading dimension: the row's start is
+  // formed in 64 bits here
+  return load8_words(a.x + static_cast<int64_t>(t) * a.ldx, 0, 1, a.K, 0, kt * 256 + lane * 8, a.vec_ok != 0);
+}
+__device__ __forceinline__ void store_unit(const GatherArgs& a, int t, int kt, int lane, uint4 v, int pos) {
+  uint32_t sbyte;
+  const uint32_t packed = quantize8_words(v, sbyte);
+  const int b = lane >> 2;  // block of the k-tile; its group of four has one word of scales
+  uint32_t word = (kt * 8 + b < ((a.K + 31) >> 5) ? sbyte : 0x7Fu) << (8 * (b & 3));
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
+  word |= __shfl_xor_sync(0xFFFFFFFFu, word, 8);
+  for (int s = 0; s < a.k; ++s) {
+    const int r = __shfl_sync(0xFFFFFFFFu, pos, s);
+    if (r < 0) {
+      if (a.zero != nullptr) {
+        uint16_t* z = a.zero + (static_cast<int64_t>(t) * a.k + s) * a.ldz;
+        for (int n = kt * 32 + lane; n < a.N; n += a.KT * 32) z[n] = 0;
+      }
+      continue;
+    }
+    const int i = r & 127;
+    uint8_t* blk = a.blocks + (static_cast<size_t>(r >> 7) * a.KT + kt) * kMoeBlockBytes;
+    *reinterpret_cast<uint32_t*>(blk + (i << 7) + ((((lane >> 2) ^ (i & 7))) << 4) + ((lane & 3) << 2)) = packed;
+    if ((lane & 15) == 0)
+      *reinterpret_cast<uint32_t*>(blk + kTileBytes + ((lane >> 4) << 9) + ((i & 31) << 4) + ((i >> 5) << 2)) = word;
+  }
+}
+
 // A warp owns k-tile gw % KT of the tokens gw / KT, + R, ...; lane l holds
 // elements 8l..8l+7 of the k-tile, four lanes one 32-element block.
 __global__ void __launch_bounds__(256, 4) moe_gather_kernel(const __grid_constant__ GatherArgs a) {
@@ -184,10 +217,8 @@ __global__ void __launch_bounds__(256, 4) moe_gather_kernel(const __grid_constan
   griddep_wait();
   griddep_launch_dependents();
   if (gw >= a.KT * a.R) return;   // warp-uniform; the kernel has no block barrier
-  const int kt = gw % a.KT, r0 = gw / a.KT;
-  const int e0 = kt * 256 + lane * 8;
-  const int nb = (a.K + 31) >> 5;
-  for (int t = r0; t < a.T; t += 2 * a.R) {
+  const int kt = gw % a.KT;
+  for (int t = gw / a.KT; t < a.T; t += 2 * a.R) {
     uint4 v[2];
     int pos[2];
 #pragma unroll
@@ -196,37 +227,111 @@ __global__ void __launch_bounds__(256, 4) moe_gather_kernel(const __grid_constan
       v[j] = make_uint4(0, 0, 0, 0);
       pos[j] = -1;
       if (tt >= a.T) continue;
-      // load8_words' rows are indexed by int leading dimensions; the row's
-      // start is formed in 64 bits here
-      v[j] = load8_words(a.x + static_cast<int64_t>(tt) * a.ldx, 0, 1, a.K, 0, e0, a.vec_ok != 0);
+      v[j] = load_unit(a, tt, kt, lane);
       if (lane < a.k) pos[j] = __ldcg(a.plan.pos + static_cast<int64_t>(tt) * a.k + lane);
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int tt = t + j * a.R;
-      if (tt >= a.T) break;     // warp-uniform
-      uint32_t sbyte;
-      const uint32_t packed = quantize8_words(v[j], sbyte);
-      const int b = lane >> 2;  // block of the k-tile; its group of four has one word of scales
-      uint32_t word = (kt * 8 + b < nb ? sbyte : 0x7Fu) << (8 * (b & 3));
-      word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
-      word |= __shfl_xor_sync(0xFFFFFFFFu, word, 8);
-      for (int s = 0; s < a.k; ++s) {
-        const int r = __shfl_sync(0xFFFFFFFFu, pos[j], s);
-        if (r < 0) {
-          if (a.zero != nullptr) {   // its result row, each k-tile's warp a share of it
-            uint16_t* z = a.zero + (static_cast<int64_t>(tt) * a.k + s) * a.ldz;
-            for (int n = kt * 32 + lane; n < a.N; n += a.KT * 32) z[n] = 0;
-          }
-          continue;
-        }
-        const int i = r & 127;
-        uint8_t* blk = a.blocks + (static_cast<size_t>(r >> 7) * a.KT + kt) * kMoeBlockBytes;
-        *reinterpret_cast<uint32_t*>(blk + (i << 7) + ((((lane >> 2) ^ (i & 7))) << 4) + ((lane & 3) << 2)) = packed;
-        if ((lane & 15) == 0)
-          *reinterpret_cast<uint32_t*>(blk + kTileBytes + ((lane >> 4) << 9) + ((i & 31) << 4) + ((i >> 5) << 2)) = word;
-      }
+    for (int j = 0; j < 2; ++j)
+      if (t + j * a.R < a.T) store_unit(a, t + j * a.R, kt, lane, v[j], pos[j]);   // (uniform)
+  }
+}
+
+// Both in one kernel for few pairs, whose calls last no longer than some
+// launches: every block counts all ids for itself, every warp finds the places
+// of its tokens' pairs, and block 0 writes what else the plan holds.  The first
+// product can request no weights before it has ended, so that from some hundred
+// pairs on two kernels are faster (us, one kernel against two: 37 x 4 pairs
+// 24.6 / 26.1, one token of 8 32.8 / 33.7, 16 of 8 117 / 116, 64 of 8 166 / 162,
+// 300 x 3 33 / 28).
+constexpr int kFewPairs = 256;
+struct FewArgs {
+  GatherArgs g;
+  const int32_t* ids;
+  int P, E;
+};
+
+__global__ void __launch_bounds__(256, 4) moe_few_kernel(const __grid_constant__ FewArgs f) {
+  __shared__ __align__(16) int ids[kFewPairs];
+  __shared__ int first[kMoeMaxExperts], sums[8];
+  const GatherArgs& a = f.g;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gw = blockIdx.x * 8 + warp;
+  griddep_launch_dependents();
+  for (int e = tid; e < kMoeMaxExperts; e += 256) first[e] = 0;
+  griddep_wait();
+  const bool mine = gw < a.KT * a.R;
+  const int kt = gw % a.KT, t0 = gw / a.KT;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (mine && t0 < a.T) v = load_unit(a, t0, kt, lane);   // under way while the ids are counted
+  __syncthreads();
+  bool bad = false;
+  int id[kFewPairs / 256];
+#pragma unroll
+  for (int q = 0; q < kFewPairs / 256; ++q) id[q] = tid + 256 * q < f.P ? f.ids[tid + 256 * q] : -1;
+#pragma unroll
+  for (int q = 0; q < kFewPairs / 256; ++q) {
+    ids[tid + 256 * q] = id[q];
+    if (static_cast<uint32_t>(id[q]) < static_cast<uint32_t>(f.E))
+      atomicAdd(&first[id[q]], 1);
+    else
+      bad = bad || id[q] >= f.E;
+  }
+  __syncthreads();
+  // counts to first rows: row tiles before each expert's, four experts a thread
+  int n[4], tiles = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    n[q] = first[4 * tid + q];
+    tiles += (n[q] + kRowTile - 1) / kRowTile;
+  }
+  int upto = tiles;   // inclusive sum over the threads
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int w = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+    if (lane >= o) upto += w;
+  }
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) upto += sums[w];
+  int at = upto - tiles;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    first[4 * tid + q] = at * kRowTile;
+    for (int i = 0; i < n[q]; i += kRowTile, ++at)
+      if (blockIdx.x == 0) a.plan.tile[at] = (4 * tid + q) | ((n[q] - i < kRowTile ? n[q] - i : kRowTile) << 16);
+  }
+  if (blockIdx.x == 0) {
+    for (int i = tid; i < 2 * kMoeTickets; i += 256) a.plan.tickets[i] = 0;
+    if (tid == 255) a.plan.hdr[0] = upto;
+    if (bad) atomicOr(&g_moe_plan_error, kErrIndex);
+  }
+  __syncthreads();
+  if (!mine) return;
+  int slots = 1;   // a.k, up to a power of two
+  while (slots < a.k) slots *= 2;
+  for (int t = t0; t < a.T; t += a.R) {
+    if (t != t0) v = load_unit(a, t, kt, lane);
+    // lane j: the row of pair j of the token, after the pairs before it of its
+    // expert.  `share` lanes count for each pair, every one a part of the ids.
+    const int p0 = t * a.k;
+    const int e = lane < a.k ? ids[p0 + lane] : -1;
+    const bool on = static_cast<uint32_t>(e) < static_cast<uint32_t>(f.E);
+    const int share = 32 / slots, pair = lane / share;
+    const int other = __shfl_sync(0xFFFFFFFFu, e, pair), before = p0 + pair;
+    int n_before = 0;
+    for (int c = 4 * (lane % share); c < before; c += 4 * share) {
+      const int4 w = *reinterpret_cast<const int4*>(ids + c);
+      n_before += (w.x == other) + (w.y == other && c + 1 < before) + (w.z == other && c + 2 < before) +
+                  (w.w == other && c + 3 < before);
     }
+    for (int o = 1; o < share; o <<= 1) n_before += __shfl_xor_sync(0xFFFFFFFFu, n_before, o);
+    n_before = __shfl_sync(0xFFFFFFFFu, n_before, (lane * share) & 31);
+    const int pos = on ? first[e] + n_before : -1;
+    if (kt == 0 && lane < a.k) {
+      a.plan.pos[p0 + lane] = pos;
+      if (on) a.plan.row_pair[pos] = p0 + lane;
+    }
+    store_unit(a, t, kt, lane, v, pos);
   }
 }
 
@@ -319,15 +424,10 @@ MoePlan moe_plan_at(void* base, int64_t P, int E) {
   return p;
 }
 
-cudaError_t launch_moe_plan(const int32_t* ids, int P, int E, const MoePlan& plan, const DeviceInfo& dev,
-                            cudaStream_t s) {
-  (void)dev;
-  const PlanArgs a{ids, P, E, plan};
-  return launch_pdl(moe_plan_kernel, E, P <= 1024 ? 256 : 1024, E * (kHists + 1) * 4, s, a);
-}
-
-cudaError_t launch_moe_gather(const void* x, int64_t ldx, int T, int top_k, int K, const MoePlan& plan,
-                              uint8_t* blocks, void* zero, int64_t ldz, int N, const DeviceInfo& dev, cudaStream_t s) {
+cudaError_t launch_moe_plan_gather(const int32_t* ids, int E, const void* x, int64_t ldx, int T, int top_k, int K,
+                                   const MoePlan& plan, uint8_t* blocks, void* zero, int64_t ldz, int N,
+                                   const DeviceInfo& dev, cudaStream_t s) {
+  const int P = T * top_k;
   GatherArgs a{};
   a.x = static_cast<const uint16_t*>(x);
   a.ldx = ldx;
@@ -345,8 +445,14 @@ cudaError_t launch_moe_gather(const void* x, int64_t ldx, int T, int top_k, int 
   if (r > T) r = T;
   if (r < 1) r = 1;
   a.R = static_cast<int>(r);
-  return launch_pdl(moe_gather_kernel, static_cast<int>((static_cast<int64_t>(a.KT) * r + 7) / 8), 256, 0, s, a);
+  const int grid = static_cast<int>((static_cast<int64_t>(a.KT) * r + 7) / 8);
+  if (moe_plan_with_gather(P)) return launch_pdl(moe_few_kernel, grid, 256, 0, s, FewArgs{a, ids, P, E});
+  const PlanArgs p{ids, P, E, plan};
+  const cudaError_t e = launch_pdl(moe_plan_kernel, E, 1024, E * (kHists + 1) * 4, s, p);
+  return e != cudaSuccess ? e : launch_pdl(moe_gather_kernel, grid, 256, 0, s, a);
 }
+
+bool moe_plan_with_gather(int P) { return P <= kFewPairs; }
 
 cudaError_t launch_moe_combine(const void* parts, int64_t ldp, const float* weights, const MoePlan& plan,
                                const void* residual, int64_t ldr, void* out, int64_t ldo, int T, int top_k, int N,
