@@ -26,6 +26,13 @@ activations, a paged cache [pages, page, L + R] of latent | rotated key):
     torch.ops.mxfp4.mla_store(kv, gamma, eps, q_rope, cos_sin, positions, slots, cache, interleaved) -> q_rot   # cache updated
     torch.ops.mxfp4.mla_decode(q_lat, q_rope, cache, page_table, seq_lens, scale) -> (out, lse)
     torch.ops.mxfp4.mla_prefill(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, scale, causal) -> (out, lse)
+
+and mixture-of-experts layers in MXFP4 (ids int32, negative for an empty slot):
+
+    torch.ops.mxfp4.moe_route(logits, bias, top_k, score, n_group, topk_group, group_top, renormalize, scale) -> (weights, ids)
+    torch.ops.mxfp4.moe_linear(x, ids, w_packed, bias, E, N) -> out [.., top_k, N]
+    torch.ops.mxfp4.moe_ffn(x, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, residual, E, I, N, act, alpha, limit) -> out
+    torch.ops.mxfp4.pack_gate_up(codes, scales, K) -> packed     # gate rows, then up rows, as moe_ffn takes them
 """
 
 from __future__ import annotations
@@ -528,3 +535,185 @@ def _(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k, scale, causal):
     _check_mla_prefill(q_nope, q_rope, k_nope, k_rope, v, cu_q, cu_k)
     T, H = q_nope.shape[0], q_nope.shape[1]
     return q_nope.new_empty(T, H, v.shape[2]), q_nope.new_empty(T, H, dtype=torch.float32)
+
+
+# ----------------------------------------------------- mixture of experts
+_MOE_SCORES = ("softmax", "sigmoid")
+_MOE_ACTS = ("silu", "gelu_tanh", "swiglu_clamp")
+
+
+def _packed(t: Tensor) -> Tensor:
+    """Packed weights as the library takes them: contiguous, 16-byte aligned (a copy where they are not)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _rows(t: Tensor, n: int) -> Tensor:
+    """t as rows of n neighbouring values, a positive stride apart (a copy where it is not)."""
+    r = t.reshape(-1, n)
+    ok = (n == 1 or r.stride(1) == 1) and (r.shape[0] <= 1 or r.stride(0) >= n)
+    return r if ok else r.clone(memory_format=torch.contiguous_format)
+
+
+@custom_op("mxfp4::pack_gate_up", mutates_args=())
+def pack_gate_up(codes: Tensor, scales: Tensor, K: int) -> Tensor:
+    """pack_weights for moe_ffn of weights that hold their gate rows before
+    their up rows: codes [.., 2 I, K/2], scales [.., 2 I, ceil(K/32)]."""
+    _check_pack_gate_up(codes, scales, K)
+    c, s = (t.unflatten(-2, (2, -1)).transpose(-3, -2).flatten(-3, -2) for t in (codes, scales))
+    return pack_weights(c, s, K)
+
+
+def _check_pack_gate_up(codes, scales, K) -> None:
+    _check_pack("mxfp4::pack_gate_up", codes, scales, K)
+    torch._check(codes.shape[-2] % 2 == 0, lambda: f"mxfp4::pack_gate_up: {codes.shape[-2]} rows are not gate and up")
+
+
+@pack_gate_up.register_fake
+def _(codes, scales, K):
+    _check_pack_gate_up(codes, scales, K)
+    B = codes.shape[0] if codes.dim() == 3 else 1
+    return codes.new_empty(_packed_weight_bytes(B, codes.shape[-2], K), dtype=torch.uint8)
+
+
+def _check_moe_route(logits, bias, top_k, score, n_group, topk_group, group_top) -> None:
+    where = "mxfp4::moe_route"
+    _check_args(where, logits, bias, dtypes=(None, torch.float32))
+    torch._check(logits.dtype in (torch.bfloat16, torch.float32),
+                 lambda: f"{where}: logits must be bfloat16 or float32, got {logits.dtype}")
+    torch._check(score in _MOE_SCORES, lambda: f"{where}: score {score!r} is none of {_MOE_SCORES}")
+    torch._check(logits.dim() >= 1, lambda: f"{where}: logits must be [.., E]")
+    E = logits.shape[-1]
+    torch._check(0 < E <= 1024 and 0 < top_k <= 32, lambda: f"{where}: E = {E} (at most 1024), top_k = {top_k} (at most 32)")
+    torch._check(0 < n_group <= 32 and E % n_group == 0 and 0 < topk_group <= n_group and group_top in (1, 2),
+                 lambda: f"{where}: {n_group} groups of {E} experts, {topk_group} kept by their best {group_top}")
+    torch._check(top_k <= E // n_group * topk_group, lambda: f"{where}: top_k = {top_k} of {E // n_group * topk_group} experts")
+    if bias is not None:
+        torch._check(bias.numel() == E, lambda: f"{where}: bias has {bias.numel()} elements, E = {E}")
+
+
+@custom_op("mxfp4::moe_route", mutates_args=())
+def moe_route(logits: Tensor, bias: Optional[Tensor], top_k: int, score: str, n_group: int, topk_group: int,
+              group_top: int, renormalize: bool, scale: float) -> tuple[Tensor, Tensor]:
+    """The top_k experts of each token by softmax or sigmoid score (+ bias) of
+    logits [.., E], within the topk_group best of n_group groups: weights
+    [.., top_k] fp32 and ids [.., top_k] int32, -1 where none is left."""
+    _check_moe_route(logits, bias, top_k, score, n_group, topk_group, group_top)
+    c = _capi()
+    E = logits.shape[-1]
+    weights = torch.empty(*logits.shape[:-1], top_k, dtype=torch.float32, device=logits.device)
+    ids = torch.empty(*logits.shape[:-1], top_k, dtype=torch.int32, device=logits.device)
+    x = _rows(logits, E)
+    if x.shape[0]:
+        with torch.cuda.device(x.device):
+            c.mxfp4_moe_route(x, c.DTYPE_BF16 if x.dtype == torch.bfloat16 else c.DTYPE_F32, x.stride(0),
+                              None if bias is None else bias.contiguous(), x.shape[0], E, top_k,
+                              _MOE_SCORES.index(score), n_group, topk_group, group_top, renormalize, scale, weights,
+                              ids, _stream(x))
+    return weights, ids
+
+
+@moe_route.register_fake
+def _(logits, bias, top_k, score, n_group, topk_group, group_top, renormalize, scale):
+    _check_moe_route(logits, bias, top_k, score, n_group, topk_group, group_top)
+    shape = (*logits.shape[:-1], top_k)
+    return logits.new_empty(shape, dtype=torch.float32), logits.new_empty(shape, dtype=torch.int32)
+
+
+def _check_moe(where: str, x: Tensor, ids: Tensor, E: int) -> tuple[int, int]:
+    torch._check(x.dim() >= 1 and ids.dim() == x.dim() and ids.shape[:-1] == x.shape[:-1],
+                 lambda: f"{where}: ids {tuple(ids.shape)} do not go with x {tuple(x.shape)}")
+    K, k = x.shape[-1], ids.shape[-1]
+    torch._check(0 < k <= 32 and 0 < E <= 1024, lambda: f"{where}: {k} slots (at most 32) of {E} experts (at most 1024)")
+    return K, k
+
+
+def _check_moe_bias(where: str, bias: Optional[Tensor], E: int, N: int) -> None:
+    if bias is not None:
+        torch._check(bias.numel() == E * N, lambda: f"{where}: bias must be [{E}, {N}], got {tuple(bias.shape)}")
+
+
+def _check_moe_linear(x, ids, w_packed, bias, E, N) -> tuple[int, int]:
+    where = "mxfp4::moe_linear"
+    _check_args(where, x, ids, w_packed, bias, dtypes=(torch.bfloat16, torch.int32, torch.uint8, torch.bfloat16))
+    K, k = _check_moe(where, x, ids, E)
+    _check_weights(where, w_packed, E, N, K)
+    _check_moe_bias(where, bias, E, N)
+    return K, k
+
+
+@custom_op("mxfp4::moe_linear", mutates_args=())
+def moe_linear(x: Tensor, ids: Tensor, w_packed: Tensor, bias: Optional[Tensor], E: int, N: int) -> Tensor:
+    """linear() of each token with the weights of each of its experts: x
+    [.., K], ids [.., top_k], E packed matrices [N, K], bias [E, N] ->
+    [.., top_k, N] bf16; the row of an empty slot is zeros."""
+    K, k = _check_moe_linear(x, ids, w_packed, bias, E, N)
+    c = _capi()
+    out = torch.empty(*x.shape[:-1], k, N, dtype=torch.bfloat16, device=x.device)
+    x2 = _rows(x, K)
+    T = x2.shape[0]
+    if T:
+        with torch.cuda.device(x.device):
+            nbytes = c.mxfp4_moe_linear_workspace_bytes(T, k, E, N, K)
+            ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=x.device)
+            c.mxfp4_moe_linear(x2, x2.stride(0), ids.contiguous(), _packed(w_packed),
+                               None if bias is None else bias.contiguous(), out, N, T, k, E, N, K, ws, nbytes,
+                               _stream(x))
+    return out
+
+
+@moe_linear.register_fake
+def _(x, ids, w_packed, bias, E, N):
+    _, k = _check_moe_linear(x, ids, w_packed, bias, E, N)
+    return x.new_empty(*x.shape[:-1], k, N)
+
+
+def _check_moe_ffn(x, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, residual, E, I, N, act) -> tuple[int, int]:
+    where = "mxfp4::moe_ffn"
+    bf = torch.bfloat16
+    _check_args(where, x, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, residual,
+                dtypes=(bf, torch.int32, torch.float32, torch.uint8, bf, torch.uint8, bf, bf))
+    K, k = _check_moe(where, x, ids, E)
+    torch._check(weights.shape == ids.shape, lambda: f"{where}: weights {tuple(weights.shape)}, ids {tuple(ids.shape)}")
+    torch._check(act in _MOE_ACTS, lambda: f"{where}: act {act!r} is none of {_MOE_ACTS}")
+    torch._check(I > 0 and I % 2 == 0, lambda: f"{where}: I = {I} must be positive and even")
+    _check_weights(where, w_gate_up, E, 2 * I, K)
+    _check_weights(where, w_down, E, N, I)
+    _check_moe_bias(where, bias_gate_up, E, 2 * I)
+    _check_moe_bias(where, bias_down, E, N)
+    if residual is not None:
+        torch._check(residual.shape == (*x.shape[:-1], N),
+                     lambda: f"{where}: residual {tuple(residual.shape)} is not {(*x.shape[:-1], N)}")
+    return K, k
+
+
+@custom_op("mxfp4::moe_ffn", mutates_args=())
+def moe_ffn(x: Tensor, ids: Tensor, weights: Tensor, w_gate_up: Tensor, bias_gate_up: Optional[Tensor], w_down: Tensor,
+            bias_down: Optional[Tensor], residual: Optional[Tensor], E: int, I: int, N: int, act: str, alpha: float,
+            limit: float) -> Tensor:
+    """The experts' gated network of each token, weighted, summed and added to
+    the residual: x [.., K], ids and weights [.., top_k], E packed matrices
+    [2 I, K] (rows alternating gate and up: pack_gate_up) and [N, I] ->
+    [.., N] bf16.  act: silu, gelu_tanh or swiglu_clamp (of alpha and limit)."""
+    K, k = _check_moe_ffn(x, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, residual, E, I, N, act)
+    c = _capi()
+    out = torch.empty(*x.shape[:-1], N, dtype=torch.bfloat16, device=x.device)
+    x2 = _rows(x, K)
+    T = x2.shape[0]
+    if T:
+        res = None if residual is None else _rows(residual, N)
+        with torch.cuda.device(x.device):
+            nbytes = c.mxfp4_moe_ffn_workspace_bytes(T, k, E, K, I, N)
+            ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=x.device)
+            c.mxfp4_moe_ffn(x2, x2.stride(0), ids.contiguous(), weights.contiguous(), _packed(w_gate_up),
+                            None if bias_gate_up is None else bias_gate_up.contiguous(), _packed(w_down),
+                            None if bias_down is None else bias_down.contiguous(), res,
+                            0 if res is None else res.stride(0), out, N, T, k, E, K, I, N, _MOE_ACTS.index(act), alpha,
+                            limit, ws, nbytes, _stream(x))
+    return out
+
+
+@moe_ffn.register_fake
+def _(x, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, residual, E, I, N, act, alpha, limit):
+    _check_moe_ffn(x, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, residual, E, I, N, act)
+    return x.new_empty(*x.shape[:-1], N)
