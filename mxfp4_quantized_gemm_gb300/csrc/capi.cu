@@ -551,8 +551,11 @@ static mxfp4_status check_moe(int T, int top_k, int E, int K, int64_t columns) {
   if ((K & 1) || E > kMoeMaxExperts || top_k > kMoeMaxTopK || P > (int64_t{1} << 28) || columns > (int64_t{1} << 26) ||
       K > (1 << 26))
     return MXFP4_ERR_UNSUPPORTED_SHAPE;
-  // tiles, k-steps and rows are counted in 32 bits on the device
-  if (moe_max_tiles(P, E) * ceil_div(columns, 256) > (int64_t{1} << 30)) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  // tiles, k-steps and rows are counted in 32 bits on the device, the blocked
+  // activations (17 KiB per row tile and k-tile) in 16-byte pieces
+  if (moe_max_tiles(P, E) * ceil_div(K, 256) > (int64_t{3} << 20)) return MXFP4_ERR_UNSUPPORTED_SHAPE;
+  if (moe_max_tiles(P, E) * ceil_div(columns, 256) > (int64_t{1} << 30) || T * ceil_div(columns, 1024) > (int64_t{1} << 30))
+    return MXFP4_ERR_UNSUPPORTED_SHAPE;
   return MXFP4_OK;
 }
 

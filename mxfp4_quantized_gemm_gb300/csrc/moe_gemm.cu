@@ -545,7 +545,7 @@ __device__ __forceinline__ void finish_cut(const MoeArgs& g, const Walk& walk, c
                                            int c_lo, int c_hi, int warp, int lane) {
   uint32_t b[4];
   load_bias<8>(g, expert, s.nt * kTileN + 8 * lane, b);
-  constexpr int kRows = 4, kAhead = 2;
+  constexpr int kRows = 2, kAhead = 2;
   const int count = c_hi - c_lo + 1;
   // lane l: where the part of contributor l stands
   const int place0 = lane < count ? part_slot(walk, g.KT, s.left, c_lo + lane) : 0;

@@ -190,20 +190,27 @@ __device__ __forceinline__ void store_unit(const GatherArgs& a, int t, int kt, i
   uint32_t word = (kt * 8 + b < ((a.K + 31) >> 5) ? sbyte : 0x7Fu) << (8 * (b & 3));
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, 8);
+  // Lane j, for pair j: the row's place in 16-byte pieces (a multiple of 8: the
+  // lowest bits hold the row's rotation), and its row of scales in the block.
+  constexpr uint32_t kNowhere = 0xFFFFFFFFu;
+  const int i = pos & 127;
+  const uint32_t place = pos < 0 ? kNowhere
+                                 : (static_cast<uint32_t>(pos >> 7) * a.KT + kt) * (kMoeBlockBytes / 16) + 8 * i + (i & 7);
+  const int scale = kTileBytes - 128 * i + ((i & 31) << 4) + ((i >> 5) << 2);   // bytes from the row's codes
+  const int mine = ((lane & 3) << 2), mine_scale = (lane >> 4) << 9;
   for (int s = 0; s < a.k; ++s) {
-    const int r = __shfl_sync(0xFFFFFFFFu, pos, s);
-    if (r < 0) {
+    const uint32_t at = __shfl_sync(0xFFFFFFFFu, place, s);
+    const int sc = __shfl_sync(0xFFFFFFFFu, scale, s);
+    if (at == kNowhere) {
       if (a.zero != nullptr) {
         uint16_t* z = a.zero + (static_cast<int64_t>(t) * a.k + s) * a.ldz;
         for (int n = kt * 32 + lane; n < a.N; n += a.KT * 32) z[n] = 0;
       }
       continue;
     }
-    const int i = r & 127;
-    uint8_t* blk = a.blocks + (static_cast<size_t>(r >> 7) * a.KT + kt) * kMoeBlockBytes;
-    *reinterpret_cast<uint32_t*>(blk + (i << 7) + ((((lane >> 2) ^ (i & 7))) << 4) + ((lane & 3) << 2)) = packed;
-    if ((lane & 15) == 0)
-      *reinterpret_cast<uint32_t*>(blk + kTileBytes + ((lane >> 4) << 9) + ((i & 31) << 4) + ((i >> 5) << 2)) = word;
+    uint8_t* row = a.blocks + static_cast<size_t>(at & ~7u) * 16;
+    *reinterpret_cast<uint32_t*>(row + (((lane >> 2) ^ (at & 7)) << 4) + mine) = packed;
+    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(row + sc + mine_scale) = word;
   }
 }
 
@@ -345,62 +352,77 @@ struct CombineArgs {
   int64_t ldr;
   uint16_t* out;
   int64_t ldo;
-  int k, N;
+  int k, N, chunks;         // chunks: blocks of a token
   int vec_ok;               // residual and out allow 16-byte accesses
 };
 
-// One thread per token and 8 columns, kUnroll results in flight.
-__global__ void __launch_bounds__(128) moe_combine_kernel(const __grid_constant__ CombineArgs a) {
-  constexpr int kUnroll = 4;
+// One thread per token and 8 columns, kUnroll results in flight; the blocks of a
+// token follow one another, as its results do in memory.  A result is asked for
+// beside the word that says whether there is one, and the residual before both
+// (each behind the other, the sum over 8192 x 8 pairs took 170 us).
+template <int kUnroll>
+__global__ void __launch_bounds__(256) moe_combine_kernel(const __grid_constant__ CombineArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t t = blockIdx.x;
-  const int n = (blockIdx.y * 128 + threadIdx.x) * 8;
+  const int64_t t = blockIdx.x / a.chunks;
+  const int n = ((blockIdx.x - static_cast<int>(t) * a.chunks) * 256 + threadIdx.x) * 8;
   if (n >= a.N) return;
+  uint16_t* o = a.out + t * a.ldo + n;
+  const bool whole = a.vec_ok != 0 && n + 8 <= a.N;
+  uint4 res = make_uint4(0, 0, 0, 0);
+  if (a.residual != nullptr) {
+    const uint16_t* r = a.residual + t * a.ldr + n;
+    if (whole) {
+      res = *reinterpret_cast<const uint4*>(r);
+    } else {
+      uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (n + i < a.N) w[i >> 1] |= static_cast<uint32_t>(r[i]) << (16 * (i & 1));
+      res = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
   float acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  auto add = [&](uint4 v, float w) {
+    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      acc[2 * i] = fmaf(w, __uint_as_float(q[i] << 16), acc[2 * i]);
+      acc[2 * i + 1] = fmaf(w, __uint_as_float(q[i] & 0xFFFF0000u), acc[2 * i + 1]);
+    }
+  };
+  const int64_t p0 = t * a.k;
   for (int s0 = 0; s0 < a.k; s0 += kUnroll) {
     uint4 v[kUnroll];
     float w[kUnroll];
+    int pos[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int64_t p = t * a.k + s0 + u;
-      const bool on = s0 + u < a.k && __ldcg(a.pos + p) >= 0;
-      w[u] = on ? a.weights[p] : 0.f;
-      v[u] = on ? __ldcg(reinterpret_cast<const uint4*>(a.parts + p * a.ldp + n)) : make_uint4(0, 0, 0, 0);
+      // past the last slot the first one's again, unused (a test would hold the
+      // loads apart: 157 us instead of 148)
+      const int64_t p = p0 + (s0 + u < a.k ? s0 + u : 0);
+      v[u] = __ldcg(reinterpret_cast<const uint4*>(a.parts + p * a.ldp + n));
+      pos[u] = __ldcg(a.pos + p);
+      w[u] = a.weights[p];
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const uint32_t q[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[2 * i] = fmaf(w[u], __uint_as_float(q[i] << 16), acc[2 * i]);
-        acc[2 * i + 1] = fmaf(w[u], __uint_as_float(q[i] & 0xFFFF0000u), acc[2 * i + 1]);
-      }
+      const bool on = s0 + u < a.k && pos[u] >= 0;   // (what an empty slot has in memory may be anything)
+      add(make_uint4(on ? v[u].x : 0u, on ? v[u].y : 0u, on ? v[u].z : 0u, on ? v[u].w : 0u), on ? w[u] : 0.f);
     }
   }
-  uint16_t* o = a.out + t * a.ldo + n;
-  const uint16_t* res = a.residual != nullptr ? a.residual + t * a.ldr + n : nullptr;
-  if (a.vec_ok != 0 && n + 8 <= a.N) {
-    if (res != nullptr) {
-      const uint4 r = *reinterpret_cast<const uint4*>(res);
-      const uint32_t q[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[2 * i] += __uint_as_float(q[i] << 16);
-        acc[2 * i + 1] += __uint_as_float(q[i] & 0xFFFF0000u);
-      }
-    }
-    *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
-                                              pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
+  if (a.residual != nullptr) add(res, 1.f);
+  const uint4 r = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
+                             pack_bf16x2(acc[6], acc[7]));
+  if (whole) {
+    *reinterpret_cast<uint4*>(o) = r;
   } else {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (n + i < a.N) {
-        const float v = acc[i] + (res != nullptr ? bf16_bits_to_float(res[i]) : 0.f);
-        o[i] = static_cast<uint16_t>(pack_bf16x2(v, 0.f));
-      }
+      if (n + i < a.N) o[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
   }
 }
 
@@ -471,16 +493,19 @@ cudaError_t launch_moe_combine(const void* parts, int64_t ldp, const float* weig
   a.N = N;
   a.vec_ok = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && ldo % 8 == 0 &&
              (residual == nullptr || ((reinterpret_cast<uintptr_t>(residual) & 15) == 0 && ldr % 8 == 0));
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(T), static_cast<unsigned>(ceil_div(N, 1024)), 1);
-  cfg.blockDim = dim3(128, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, moe_combine_kernel, a);
+  a.chunks = static_cast<int>(ceil_div(N, 2048));
+  // slots at once: of four, three and two (all of one) the most that divide the
+  // slots with the fewest left over
+  int unroll = top_k < 4 ? top_k : 4;
+  for (int u = unroll - 1; u >= 2; --u)
+    if (ceil_div(top_k, u) * u < ceil_div(top_k, unroll) * unroll) unroll = u;
+  const int grid = T * a.chunks;
+  switch (unroll) {
+    case 1: return launch_pdl(moe_combine_kernel<1>, grid, 256, 0, s, a);
+    case 2: return launch_pdl(moe_combine_kernel<2>, grid, 256, 0, s, a);
+    case 3: return launch_pdl(moe_combine_kernel<3>, grid, 256, 0, s, a);
+    default: return launch_pdl(moe_combine_kernel<4>, grid, 256, 0, s, a);
+  }
 }
 
 uint32_t moe_plan_read_clear_error() {
