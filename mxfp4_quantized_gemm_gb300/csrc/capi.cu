@@ -662,7 +662,7 @@ mxfp4_status mxfp4_moe_ffn(const void* x, int64_t ldx, const int32_t* ids, const
   p.plan_late = false;
   if (e == cudaSuccess) e = launch_moe_gemm(p, plan, dev, s);
   if (e == cudaSuccess)
-    e = launch_moe_combine(ws + w.results, w.ldp, weights, plan, residual, ldr, out, ldo, T, top_k, N, dev, s);
+    e = launch_moe_combine(ws + w.results, w.ldp, weights, plan, residual, ldr, out, ldo, T, top_k, N, s);
   return from_cuda(e);
 }
 

@@ -58,7 +58,7 @@ bool moe_plan_with_gather(int P);
 // out[t] = bf16(residual[t] + sum_j weights[t][j] * parts[t * top_k + j]).
 cudaError_t launch_moe_combine(const void* parts, int64_t ldp, const float* weights, const MoePlan& plan,
                                const void* residual, int64_t ldr, void* out, int64_t ldo, int T, int top_k, int N,
-                               const DeviceInfo& dev, cudaStream_t s);
+                               cudaStream_t s);
 uint32_t moe_plan_read_clear_error();
 
 enum class MoeAct : int { kSilu = 0, kGeluTanh = 1, kSwigluClamp = 2 };

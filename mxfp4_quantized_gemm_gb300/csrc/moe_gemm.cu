@@ -81,6 +81,7 @@ struct MoeArgs {
   float a1, a3, limit, shift;                      // of the activation (see gated)
   const int32_t* hdr;
   const int32_t* tile;
+  int max_tiles;
   const int32_t* row_pair;
   int32_t* tickets;
   float* parts;
@@ -93,7 +94,6 @@ struct __align__(16) Segment {
   int half;      // 0, 1: that half of the column tile; -1: all of it
   int left;      // index among the cut tiles, or -1
   int info;      // the row tile's expert | live rows << 16
-  int unused;
 };
 static_assert(sizeof(Segment) == 32, "two 16-byte words");
 
@@ -759,22 +759,38 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
         sslot = 0;
         sphase ^= 1;
       }
-      for (int j = 0; j < len; ++j) {
+      // Two k-steps at a time where both have landed: their scales are copied
+      // together, then the MMAs follow (8192 tokens' first product 289 -> 280 us).
+      for (int j = 0; j < len;) {
         mbar_wait(&full[st], phase, abort);
         abort = __any_sync(0xFFFFFFFFu, abort);
         if (abort) break;
+        const int st2 = st + 1 == C::kStages ? 0 : st + 1;
+        const uint32_t phase2 = st2 == 0 ? phase ^ 1 : phase;
+        int n = 1;
+        if (j + 1 < len && __all_sync(0xFFFFFFFFu, mbar_test_wait(smem_u32(&full[st2]), phase2))) n = 2;
         tc_fence_after();
-        const uint32_t base = ring + st * C::kStageBytes;
-        const uint32_t sfa_col = resident ? kSfaRes + 8u * k : C::kSfBase + st * C::kSfSlot;
-        const uint32_t sfb_col = resident ? C::kSfBase + 16u * st : sfa_col + C::kSfbOff;
-        const bool copy_a = !resident || ((have >> (k & 31)) & 1u) == 0;
-        if (resident) have |= 1u << k;
+        auto columns = [&](int x, int slot, uint32_t& sfa, uint32_t& sfb) {
+          sfa = resident ? kSfaRes + 8u * (k + x) : C::kSfBase + slot * C::kSfSlot;
+          sfb = resident ? C::kSfBase + 16u * slot : sfa + C::kSfbOff;
+        };
+        uint32_t sfa[2], sfb[2];
+        columns(0, st, sfa[0], sfb[0]);
+        columns(1, st2, sfa[1], sfb[1]);
         if (elect_one()) {
-          if (half < 0)
-            issue_stage_scales_sfa<C>(tmem, base, sfb_col, sfa_col, copy_a);
-          else
-            issue_half_scales(tmem, base, sfb_col, sfa_col, copy_a);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (x < n) {
+              const uint32_t base = ring + (x == 0 ? st : st2) * C::kStageBytes;
+              const bool copy_a = !resident || ((have >> ((k + x) & 31)) & 1u) == 0;
+              if (half < 0)
+                issue_stage_scales_sfa<C>(tmem, base, sfb[x], sfa[x], copy_a);
+              else
+                issue_half_scales(tmem, base, sfb[x], sfa[x], copy_a);
+            }
+          }
         }
+        if (resident) have |= (n == 2 ? 3u : 1u) << k;
         __syncwarp();
         if (j == 0) {
           mbar_wait(acc_empty, (seg & 1) ^ 1, abort);
@@ -783,17 +799,25 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
           tc_fence_after();
         }
         if (elect_one()) {
-          if (half < 0)
-            issue_stage_mmas_sfa<C>(tmem, base, sfb_col, sfa_col, j != 0 ? 1u : 0u);
-          else
-            issue_half_mmas(tmem, base, sfb_col, sfa_col, j != 0 ? 1u : 0u);
-          mma_commit(&empty[st]);
-          if (j + 1 == len) mma_commit(acc_full);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (x < n) {
+              const uint32_t base = ring + (x == 0 ? st : st2) * C::kStageBytes;
+              if (half < 0)
+                issue_stage_mmas_sfa<C>(tmem, base, sfb[x], sfa[x], j + x != 0 ? 1u : 0u);
+              else
+                issue_half_mmas(tmem, base, sfb[x], sfa[x], j + x != 0 ? 1u : 0u);
+              mma_commit(&empty[x == 0 ? st : st2]);
+            }
+          }
+          if (j + n == len) mma_commit(acc_full);
         }
         __syncwarp();
-        ++k;
-        if (++st == C::kStages) {
-          st = 0;
+        j += n;
+        k += n;
+        st += n;
+        if (st >= C::kStages) {
+          st -= C::kStages;
           phase ^= 1;
         }
       }
@@ -807,6 +831,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     // plan.  A segment's tile word and pairs are loaded while the one before
     // it is handed out.
     if (g.plan_late) griddep_wait();
+    const int tiles32 = lane < g.max_tiles ? __ldcg(g.tile + lane) : 0;   // beside their number, for the first segments
     Walk walk;
     walk.init(g, __ldcg(g.hdr));
     int rt = -1;
@@ -818,7 +843,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
       if (!more) s.rt = -1;
       if (more && s.rt != rt) {
         rt = s.rt;
-        info = __ldcg(g.tile + rt);
+        info = rt < 32 ? __shfl_sync(0xFFFFFFFFu, tiles32, rt & 31) : __ldcg(g.tile + rt);
         if (!kGated) pairs = __ldcg(reinterpret_cast<const int4*>(g.row_pair + static_cast<int64_t>(rt) * kRowTile) + lane);
       }
       mbar_wait(&seg_empty[sslot], sphase ^ 1, abort);
@@ -996,6 +1021,7 @@ cudaError_t launch_moe_gemm(const MoeGemmProblem& p, const MoePlan& plan, const 
   a.a3 = p.act == MoeAct::kGeluTanh ? 0.044715f * a.a1 : 0.f;
   a.hdr = plan.hdr;
   a.tile = plan.tile;
+  a.max_tiles = plan.max_tiles;
   a.row_pair = plan.row_pair;
   a.tickets = plan.tickets + p.which * kMoeTickets;
   a.parts = p.parts;

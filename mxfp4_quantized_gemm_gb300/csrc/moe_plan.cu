@@ -190,6 +190,13 @@ __device__ __forceinline__ void store_unit(const GatherArgs& a, int t, int kt, i
   uint32_t word = (kt * 8 + b < ((a.K + 31) >> 5) ? sbyte : 0x7Fu) << (8 * (b & 3));
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, 4);
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, 8);
+  // All of the block's codes for each of its four lanes: lane l writes block
+  // l / 4 of one pair in four, so that a store covers the k-tile of four rows.
+  uint4 codes;
+  codes.x = __shfl_sync(0xFFFFFFFFu, packed, lane & ~3);
+  codes.y = __shfl_sync(0xFFFFFFFFu, packed, (lane & ~3) + 1);
+  codes.z = __shfl_sync(0xFFFFFFFFu, packed, (lane & ~3) + 2);
+  codes.w = __shfl_sync(0xFFFFFFFFu, packed, (lane & ~3) + 3);
   // Lane j, for pair j: the row's place in 16-byte pieces (a multiple of 8: the
   // lowest bits hold the row's rotation), and its row of scales in the block.
   constexpr uint32_t kNowhere = 0xFFFFFFFFu;
@@ -197,20 +204,18 @@ __device__ __forceinline__ void store_unit(const GatherArgs& a, int t, int kt, i
   const uint32_t place = pos < 0 ? kNowhere
                                  : (static_cast<uint32_t>(pos >> 7) * a.KT + kt) * (kMoeBlockBytes / 16) + 8 * i + (i & 7);
   const int scale = kTileBytes - 128 * i + ((i & 31) << 4) + ((i >> 5) << 2);   // bytes from the row's codes
-  const int mine = ((lane & 3) << 2), mine_scale = (lane >> 4) << 9;
-  for (int s = 0; s < a.k; ++s) {
+  for (int s = lane & 3; s < a.k + (lane & 3); s += 4) {   // (whole warps loop; lanes >= k hold no place)
     const uint32_t at = __shfl_sync(0xFFFFFFFFu, place, s);
     const int sc = __shfl_sync(0xFFFFFFFFu, scale, s);
-    if (at == kNowhere) {
-      if (a.zero != nullptr) {
-        uint16_t* z = a.zero + (static_cast<int64_t>(t) * a.k + s) * a.ldz;
-        for (int n = kt * 32 + lane; n < a.N; n += a.KT * 32) z[n] = 0;
-      }
-      continue;
-    }
+    if (at == kNowhere) continue;
     uint8_t* row = a.blocks + static_cast<size_t>(at & ~7u) * 16;
-    *reinterpret_cast<uint32_t*>(row + (((lane >> 2) ^ (at & 7)) << 4) + mine) = packed;
-    if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(row + sc + mine_scale) = word;
+    *reinterpret_cast<uint4*>(row + ((b ^ (at & 7)) << 4)) = codes;
+    if ((b & 3) == 0) *reinterpret_cast<uint32_t*>(row + sc + ((b >> 2) << 9)) = word;
+  }
+  if (a.zero == nullptr) return;
+  for (uint32_t none = __ballot_sync(0xFFFFFFFFu, lane < a.k && pos < 0); none != 0; none &= none - 1) {
+    uint16_t* z = a.zero + (static_cast<int64_t>(t) * a.k + __ffs(none) - 1) * a.ldz;
+    for (int n = kt * 32 + lane; n < a.N; n += a.KT * 32) z[n] = 0;
   }
 }
 
@@ -463,14 +468,18 @@ cudaError_t launch_moe_plan_gather(const int32_t* ids, int E, const void* x, int
   a.zero = static_cast<uint16_t*>(zero);
   a.ldz = ldz;
   a.N = N;
-  int64_t r = static_cast<int64_t>(dev.sm_count) * (T <= kDecodeMaxM ? 1 : 8) * 8 / a.KT;
+  // eight warps a block, five blocks an SM (all that its registers let it hold);
+  // one for few tokens, whose warps have one unit each all the same
+  int64_t r = static_cast<int64_t>(dev.sm_count) * (T <= kDecodeMaxM ? 1 : 5) * 8 / a.KT;
   if (r > T) r = T;
   if (r < 1) r = 1;
   a.R = static_cast<int>(r);
   const int grid = static_cast<int>((static_cast<int64_t>(a.KT) * r + 7) / 8);
   if (moe_plan_with_gather(P)) return launch_pdl(moe_few_kernel, grid, 256, 0, s, FewArgs{a, ids, P, E});
   const PlanArgs p{ids, P, E, plan};
-  const cudaError_t e = launch_pdl(moe_plan_kernel, E, 1024, E * (kHists + 1) * 4, s, p);
+  // few pairs give a large block's barriers more to do than its lanes (us, 256
+  // threads against 1024: 512 pairs 3.8 / 5.3, 900 3.7 / 4.9, 3000 5.1 / 4.8)
+  const cudaError_t e = launch_pdl(moe_plan_kernel, E, P <= 2048 ? 256 : 1024, E * (kHists + 1) * 4, s, p);
   return e != cudaSuccess ? e : launch_pdl(moe_gather_kernel, grid, 256, 0, s, a);
 }
 
@@ -478,8 +487,7 @@ bool moe_plan_with_gather(int P) { return P <= kFewPairs; }
 
 cudaError_t launch_moe_combine(const void* parts, int64_t ldp, const float* weights, const MoePlan& plan,
                                const void* residual, int64_t ldr, void* out, int64_t ldo, int T, int top_k, int N,
-                               const DeviceInfo& dev, cudaStream_t s) {
-  (void)dev;
+                               cudaStream_t s) {
   CombineArgs a{};
   a.parts = static_cast<const uint16_t*>(parts);
   a.ldp = ldp;
