@@ -490,7 +490,9 @@ MXFP4_API mxfp4_status mxfp4_mla_prefill(const void* q_nope_dev, int64_t qn_tok,
  * as an empty slot and mxfp4_get_device_error() reports MXFP4_ERR_INDEX.
  * The same expert may stand in several slots of a token; each counts.
  *
- * Limits: E at most 1024, top_k at most 32, K even, T * top_k at most 2^28.
+ * Limits: E at most 1024, top_k at most 32, K even, T * top_k at most 2^28;
+ * for the experts' calls also (T * top_k / 128 + min(T * top_k, E)) *
+ * ceil(K / 256) at most 3 * 2^20 (12 million routed rows of 8192).
  * Row strides (ld*) are in elements and at least the row's length; a single
  * row's stride is not read.  bf16 and fp32 pointers need their type's
  * alignment only (rows whose pointer and stride allow 16-byte accesses are
@@ -558,7 +560,7 @@ MXFP4_API size_t mxfp4_moe_ffn_workspace_bytes(int T, int top_k, int E, int K, i
  *   x_dev         bf16 [T][ldx >= K]
  *   w_packed_dev  mxfp4_pack_weights of E matrices [N][K]
  *   bias_dev      bf16 [E][N] contiguous, or NULL
- *   out_dev       bf16 [T * top_k][ldo >= N]
+ *   out_dev       bf16 [T * top_k][ldo >= N]; must not overlap x
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE, CUDA.
  */
 MXFP4_API mxfp4_status mxfp4_moe_linear(const void* x_dev, int64_t ldx, const int32_t* ids_dev,

@@ -530,6 +530,9 @@ mxfp4_status mxfp4_moe_route(const void* logits, mxfp4_dtype dtype, int64_t ld, 
 struct MoeWorkspace {
   size_t plan, a, h, results, parts, total;
   int64_t ldp;   // row stride of the pairs' results
+  float* parts_at(uint8_t* ws) const {   // 32-byte accesses, whereas a workspace is 16-byte aligned
+    return reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(ws + parts) + 31) & ~static_cast<uintptr_t>(31));
+  }
 };
 static MoeWorkspace moe_workspace_layout(int64_t P, int E, int K, int I, int N, int sm_count) {
   const int64_t rt = moe_max_tiles(P, E);
@@ -540,7 +543,7 @@ static MoeWorkspace moe_workspace_layout(int64_t P, int E, int K, int I, int N, 
   w.results = w.h + (I > 0 ? static_cast<size_t>(rt * (padded_k(I) / kKTile)) * kMoeBlockBytes : 0);
   w.ldp = weight_rows(N);   // whole tiles: no row of the results ends inside one
   w.parts = w.results + (I > 0 ? round_up(static_cast<size_t>(P * w.ldp) * 2, 1024) : 0);
-  w.total = w.parts + moe_gemm_parts_bytes(sm_count);
+  w.total = w.parts + moe_gemm_parts_bytes(sm_count) + 16;   // (the parts start at a multiple of 32)
   return w;
 }
 
@@ -602,7 +605,7 @@ mxfp4_status mxfp4_moe_linear(const void* x, int64_t ldx, const int32_t* ids, co
   p.out_n = N;
   p.which = 0;
   p.plan_late = moe_plan_with_gather(static_cast<int>(P));
-  p.parts = reinterpret_cast<float*>(ws + w.parts);
+  p.parts = w.parts_at(ws);
   if (e == cudaSuccess) e = launch_moe_gemm(p, plan, dev, s);
   return from_cuda(e);
 }
@@ -647,7 +650,7 @@ mxfp4_status mxfp4_moe_ffn(const void* x, int64_t ldx, const int32_t* ids, const
   p.limit = limit;
   p.which = 0;
   p.plan_late = moe_plan_with_gather(static_cast<int>(P));
-  p.parts = reinterpret_cast<float*>(ws + w.parts);
+  p.parts = w.parts_at(ws);
   if (e == cudaSuccess) e = launch_moe_gemm(p, plan, dev, s);
   p.a_blocks = ws + w.h;
   p.w_packed = static_cast<const uint8_t*>(w_down);

@@ -74,6 +74,26 @@ def test_cut_tiles(capi, T):
     check_rows(capi, T, 1, 1, 300, 14336, ids, np.arange(T), seed=T)
 
 
+@pytest.mark.parametrize("at", [16, 48])
+def test_cut_tiles_with_a_workspace_aligned_to_16_bytes(capi, at):
+    # the parts of cut tiles are read and written 32 bytes at a time
+    T, K = 40, 14336
+    w = Experts(capi, 1, 300, K, 8, True)
+    x, ids = dev_bf16(synth.activations(T, K, 8)), torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    n = capi.mxfp4_moe_linear_workspace_bytes(T, 1, 1, 300, K)
+    room = workspace(n + 128)
+    got = run_linear(capi, x, ids, w, ws=room[at:at + n])
+    assert torch.equal(got, run_linear(capi, x, ids, w))
+    assert (room[at + n:] == 0xFF).all() and (room[:at] == 0xFF).all()
+    up, down = Experts(capi, 1, 2 * 130, K, 4, True), Experts(capi, 1, 72, 130, 5, True)
+    weights = torch.ones(T, 1, device="cuda")
+    n = capi.mxfp4_moe_ffn_workspace_bytes(T, 1, 1, K, 130, 72)
+    room = workspace(n + 128)
+    got = run_ffn(capi, x, ids, weights, up, down, "silu", ws=room[at:at + n])
+    assert torch.equal(got, run_ffn(capi, x, ids, weights, up, down, "silu"))
+    assert (room[at + n:] == 0xFF).all() and (room[:at] == 0xFF).all()
+
+
 def test_cut_tiles_after_whole_rounds(capi):
     T = 5120
     ids = np.zeros((T, 1), dtype=np.int32)

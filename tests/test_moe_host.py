@@ -123,6 +123,7 @@ def test_refusals_common(capi, fn):
     if "workspace" in base:
         assert status(capi, fn, base, K=255) == capi.ERR_UNSUPPORTED_SHAPE
         assert status(capi, fn, base, T=1 << 28) == capi.ERR_UNSUPPORTED_SHAPE
+        assert status(capi, fn, base, T=1 << 27, K=1024, ldx=1024) == capi.ERR_UNSUPPORTED_SHAPE   # row tiles x k-tiles
         assert status(capi, fn, base, workspace=None) == capi.ERR_WORKSPACE
         assert status(capi, fn, base, workspace_bytes=1000) == capi.ERR_WORKSPACE
         assert status(capi, fn, base, workspace=A + 8) == capi.ERR_MISALIGNED
