@@ -521,7 +521,7 @@ mxfp4_status mxfp4_moe_route(const void* logits, mxfp4_dtype dtype, int64_t ld, 
   if (st != MXFP4_OK) return st;
   const MoeRouteProblem p{logits,  dtype == MXFP4_DTYPE_BF16, ld, bias, T, E, top_k, score == MXFP4_MOE_SIGMOID,
                           n_group, topk_group, group_top, renormalize != 0, scale, weights, ids};
-  return from_cuda(launch_moe_route(p, dev, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_moe_route(p, static_cast<cudaStream_t>(stream)));
 }
 
 // Workspace carve-up of the experts' calls, each region 1 KiB aligned: plan,
@@ -604,7 +604,8 @@ mxfp4_status mxfp4_moe_linear(const void* x, int64_t ldx, const int32_t* ids, co
   p.ldo = ldo;
   p.out_n = N;
   p.which = 0;
-  p.plan_late = moe_plan_with_gather(static_cast<int>(P));
+  p.ids = P <= kMoeFewPairs ? ids : nullptr;
+  p.P = static_cast<int>(P);
   p.parts = w.parts_at(ws);
   if (e == cudaSuccess) e = launch_moe_gemm(p, plan, dev, s);
   return from_cuda(e);
@@ -649,7 +650,8 @@ mxfp4_status mxfp4_moe_ffn(const void* x, int64_t ldx, const int32_t* ids, const
   p.alpha = alpha;
   p.limit = limit;
   p.which = 0;
-  p.plan_late = moe_plan_with_gather(static_cast<int>(P));
+  p.ids = P <= kMoeFewPairs ? ids : nullptr;
+  p.P = static_cast<int>(P);
   p.parts = w.parts_at(ws);
   if (e == cudaSuccess) e = launch_moe_gemm(p, plan, dev, s);
   p.a_blocks = ws + w.h;
@@ -662,7 +664,7 @@ mxfp4_status mxfp4_moe_ffn(const void* x, int64_t ldx, const int32_t* ids, const
   p.ldo = w.ldp;
   p.out_n = static_cast<int>(w.ldp);
   p.which = 1;
-  p.plan_late = false;
+  p.ids = nullptr;
   if (e == cudaSuccess) e = launch_moe_gemm(p, plan, dev, s);
   if (e == cudaSuccess)
     e = launch_moe_combine(ws + w.results, w.ldp, weights, plan, residual, ldr, out, ldo, T, top_k, N, s);

@@ -29,7 +29,7 @@ struct MoeRouteProblem {
   float* weights;          // [T][top_k]
   int32_t* ids;            // [T][top_k]
 };
-cudaError_t launch_moe_route(const MoeRouteProblem& p, const DeviceInfo& dev, cudaStream_t s);
+cudaError_t launch_moe_route(const MoeRouteProblem& p, cudaStream_t s);
 
 // The routed pairs (token t, slot j), pair t * top_k + j, sorted by expert:
 // every expert's rows fill row tiles of 128, in the order of the pairs.
@@ -53,8 +53,9 @@ MoePlan moe_plan_at(void* base, int64_t P, int E);
 cudaError_t launch_moe_plan_gather(const int32_t* ids, int E, const void* x, int64_t ldx, int T, int top_k, int K,
                                    const MoePlan& plan, uint8_t* blocks, void* zero, int64_t ldz, int N,
                                    const DeviceInfo& dev, cudaStream_t s);
-// Whether the same kernel does both (the plan is complete only when it is).
-bool moe_plan_with_gather(int P);
+// Pairs up to which one kernel does both; the first product then starts beside
+// it and finds the plan from the ids itself.
+constexpr int kMoeFewPairs = 256;
 // out[t] = bf16(residual[t] + sum_j weights[t][j] * parts[t * top_k + j]).
 cudaError_t launch_moe_combine(const void* parts, int64_t ldp, const float* weights, const MoePlan& plan,
                                const void* residual, int64_t ldr, void* out, int64_t ldo, int T, int top_k, int N,
@@ -77,7 +78,8 @@ struct MoeGemmProblem {
   MoeAct act;
   float alpha, limit;
   int which;                // ticket set
-  bool plan_late;           // the plan is not complete before the kernel ahead of this one is
+  const int32_t* ids;       // of at most kMoeFewPairs pairs where the kernel ahead makes the plan, else null
+  int P;
   float* parts;             // moe_gemm_parts_bytes()
 };
 size_t moe_gemm_parts_bytes(int sm_count);

@@ -62,7 +62,11 @@ static_assert(8 * kStageWarp >= kFewBatch * kTileN * 4, "the rows handed out sha
 constexpr int kSegs = 8;
 constexpr int kSegBytes = 32 + kRowTile * 4;
 constexpr int kSegReaders = 3 + 8;                 // both producers, the MMA issuer and the epilogue warps
-constexpr int kMoeSmem = C::kSmem + 8 * kStageWarp + kSegs * kSegBytes;
+// Of few pairs: their ids, the number of row tiles, each one's expert.
+constexpr int kFewWords = kMoeFewPairs + 2 + kMoeFewPairs + 2;
+constexpr int kMoeSmem = C::kSmem + 8 * kStageWarp + kSegs * kSegBytes + kFewWords * 2;
+static_assert(kMoeFewPairs <= 2 * kRowTile, "few pairs of an expert fill two row tiles at most");
+static_assert(kMoeMaxExperts * 4 <= 8 * kStageWarp, "the counts of few pairs stand in the staging area");
 static_assert(kMoeSmem <= kMaxSmem, "ring and staging exceed shared memory");
 
 struct MoeArgs {
@@ -85,7 +89,8 @@ struct MoeArgs {
   const int32_t* row_pair;
   int32_t* tickets;
   float* parts;
-  int plan_late;                                   // the kernel before this one makes the plan
+  const int32_t* ids;                              // of few pairs (else null): see FewPlan
+  int P, E;
 };
 
 struct __align__(16) Segment {
@@ -191,6 +196,57 @@ struct Walk {
     s.len = g.KT - s.k0 < it1 - it ? g.KT - s.k0 : it1 - it;
     it += s.len;
     return true;
+  }
+};
+
+// The plan of few pairs, found from the ids by one warp: the kernel that writes
+// the plan for the others is still at work then, and this one can request its
+// weights beside it (the first product's start waits for it otherwise).
+struct FewPlan {
+  // The ids, the number of row tiles and their experts to `w`; counts: room for
+  // E words.
+  static __device__ __forceinline__ void init(const MoeArgs& g, int lane, int* counts, uint16_t* w) {
+    int id[kMoeFewPairs / 32];
+#pragma unroll
+    for (int q = 0; q < kMoeFewPairs / 32; ++q) id[q] = lane + 32 * q < g.P ? __ldcg(g.ids + lane + 32 * q) : -1;
+    for (int e = lane; e < g.E; e += 32) counts[e] = 0;
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < kMoeFewPairs / 32; ++q) {
+      const bool on = static_cast<uint32_t>(id[q]) < static_cast<uint32_t>(g.E);
+      if (on) atomicAdd(&counts[id[q]], 1);
+      w[lane + 32 * q] = on ? static_cast<uint16_t>(id[q]) : static_cast<uint16_t>(0xFFFF);
+    }
+    __syncwarp();
+    const int per = (g.E + 31) / 32, e0 = lane * per, e1 = e0 + per < g.E ? e0 + per : g.E;
+    int n = 0;
+    for (int e = e0; e < e1; ++e) n += (counts[e] + kRowTile - 1) / kRowTile;
+    int upto = n;   // inclusive sum over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) w[kMoeFewPairs] = static_cast<uint16_t>(upto);
+    uint16_t* tile = w + kMoeFewPairs + 1 + upto - n;
+    for (int e = e0; e < e1; ++e)
+      for (int i = counts[e]; i > 0; i -= kRowTile) *tile++ = static_cast<uint16_t>(e);
+  }
+  static __device__ __forceinline__ int row_tiles(const uint16_t* w) { return w[kMoeFewPairs]; }
+  // The word of row tile rt, as the plan's; its pairs to pairs[0 ..].
+  static __device__ __forceinline__ int tile(const uint16_t* w, int rt, int lane, int* pairs) {
+    const uint16_t* experts = w + kMoeFewPairs + 1;
+    const int e = experts[rt];
+    int row = rt > 0 && experts[rt - 1] == e ? -kRowTile : 0;   // of the expert's first pair
+#pragma unroll 1
+    for (int q = 0; q < kMoeFewPairs; q += 32) {
+      const bool on = w[q + lane] == e;
+      const uint32_t m = __ballot_sync(0xFFFFFFFFu, on);
+      const int mine = row + __popc(m & ((1u << lane) - 1u));
+      if (on && mine >= 0 && mine < kRowTile) pairs[mine] = q + lane;
+      row += __popc(m);
+    }
+    return e | ((row < kRowTile ? row : kRowTile) << 16);
   }
 };
 
@@ -646,6 +702,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
+  if (warp == 3 && g.ids != nullptr)
+    FewPlan::init(g, lane, reinterpret_cast<int*>(staging), reinterpret_cast<uint16_t*>(segs + kSegs * kSegBytes));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -827,13 +885,15 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
    } else {
     // ---- warp 3: the segments of this CTA, ahead of the other roles.  The plan
     // is complete when this kernel starts (the kernel before it lets it start
-    // only after its own wait for the plan), but where that kernel makes the
-    // plan.  A segment's tile word and pairs are loaded while the one before
-    // it is handed out.
-    if (g.plan_late) griddep_wait();
-    const int tiles32 = lane < g.max_tiles ? __ldcg(g.tile + lane) : 0;   // beside their number, for the first segments
+    // only after its own wait for the plan); that of few pairs it finds itself.
+    // A segment's tile word and pairs are loaded while the one before it is
+    // handed out.
+    const bool few_pairs = g.ids != nullptr;
+    const uint16_t* found = reinterpret_cast<const uint16_t*>(segs + kSegs * kSegBytes);
+    int tiles32 = 0;
+    if (!few_pairs && lane < g.max_tiles) tiles32 = __ldcg(g.tile + lane);   // beside their number, for the first segments
     Walk walk;
-    walk.init(g, __ldcg(g.hdr));
+    walk.init(g, few_pairs ? FewPlan::row_tiles(found) : __ldcg(g.hdr));
     int rt = -1;
     int4 pairs = make_int4(-1, -1, -1, -1);
     int info = 0;
@@ -843,18 +903,24 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
       if (!more) s.rt = -1;
       if (more && s.rt != rt) {
         rt = s.rt;
-        info = rt < 32 ? __shfl_sync(0xFFFFFFFFu, tiles32, rt & 31) : __ldcg(g.tile + rt);
-        if (!kGated) pairs = __ldcg(reinterpret_cast<const int4*>(g.row_pair + static_cast<int64_t>(rt) * kRowTile) + lane);
+        if (!few_pairs) {
+          info = rt < 32 ? __shfl_sync(0xFFFFFFFFu, tiles32, rt & 31) : __ldcg(g.tile + rt);
+          if (!kGated) pairs = __ldcg(reinterpret_cast<const int4*>(g.row_pair + static_cast<int64_t>(rt) * kRowTile) + lane);
+        }
       }
       mbar_wait(&seg_empty[sslot], sphase ^ 1, abort);
       abort = __any_sync(0xFFFFFFFFu, abort);
       if (abort) break;
       uint8_t* rec = segs + sslot * kSegBytes;
+      if (few_pairs) {
+        if (more) info = FewPlan::tile(found, rt, lane, reinterpret_cast<int*>(rec + 32));
+      } else if (!kGated) {
+        reinterpret_cast<int4*>(rec + 32)[lane] = pairs;
+      }
       if (lane == 0) {
         reinterpret_cast<int4*>(rec)[0] = make_int4(s.rt, s.nt, s.k0, s.len);
         reinterpret_cast<int4*>(rec)[1] = make_int4(s.half, s.left, info, 0);
       }
-      if (!kGated) reinterpret_cast<int4*>(rec + 32)[lane] = pairs;
       __syncwarp();
       if (lane == 0) mbar_arrive(&seg_full[sslot]);
       if (++sslot == kSegs) {
@@ -1025,7 +1091,9 @@ cudaError_t launch_moe_gemm(const MoeGemmProblem& p, const MoePlan& plan, const 
   a.row_pair = plan.row_pair;
   a.tickets = plan.tickets + p.which * kMoeTickets;
   a.parts = p.parts;
-  a.plan_late = p.plan_late;
+  a.ids = p.ids;
+  a.P = p.P;
+  a.E = p.E;
   return p.h_blocks != nullptr ? launch<true>(a, dev, s) : launch<false>(a, dev, s);
 }
 

@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(256, 4) moe_gather_kernel(const __grid_constan
 // pairs on two kernels are faster (us, one kernel against two: 37 x 4 pairs
 // 24.6 / 26.1, one token of 8 32.8 / 33.7, 16 of 8 117 / 116, 64 of 8 166 / 162,
 // 300 x 3 33 / 28).
-constexpr int kFewPairs = 256;
+constexpr int kFewPairs = kMoeFewPairs;
 struct FewArgs {
   GatherArgs g;
   const int32_t* ids;
@@ -268,9 +268,11 @@ __global__ void __launch_bounds__(256, 4) moe_few_kernel(const __grid_constant__
   const GatherArgs& a = f.g;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gw = blockIdx.x * 8 + warp;
-  griddep_launch_dependents();
   for (int e = tid; e < kMoeMaxExperts; e += 256) first[e] = 0;
+  // The product behind this kernel reads the ids before it waits for it, so it
+  // is let go only once they are there.
   griddep_wait();
+  griddep_launch_dependents();
   const bool mine = gw < a.KT * a.R;
   const int kt = gw % a.KT, t0 = gw / a.KT;
   uint4 v = make_uint4(0, 0, 0, 0);
@@ -475,15 +477,13 @@ cudaError_t launch_moe_plan_gather(const int32_t* ids, int E, const void* x, int
   if (r < 1) r = 1;
   a.R = static_cast<int>(r);
   const int grid = static_cast<int>((static_cast<int64_t>(a.KT) * r + 7) / 8);
-  if (moe_plan_with_gather(P)) return launch_pdl(moe_few_kernel, grid, 256, 0, s, FewArgs{a, ids, P, E});
+  if (P <= kFewPairs) return launch_pdl(moe_few_kernel, grid, 256, 0, s, FewArgs{a, ids, P, E});
   const PlanArgs p{ids, P, E, plan};
   // few pairs give a large block's barriers more to do than its lanes (us, 256
   // threads against 1024: 512 pairs 3.8 / 5.3, 900 3.7 / 4.9, 3000 5.1 / 4.8)
   const cudaError_t e = launch_pdl(moe_plan_kernel, E, P <= 2048 ? 256 : 1024, E * (kHists + 1) * 4, s, p);
   return e != cudaSuccess ? e : launch_pdl(moe_gather_kernel, grid, 256, 0, s, a);
 }
-
-bool moe_plan_with_gather(int P) { return P <= kFewPairs; }
 
 cudaError_t launch_moe_combine(const void* parts, int64_t ldp, const float* weights, const MoePlan& plan,
                                const void* residual, int64_t ldr, void* out, int64_t ldo, int T, int top_k, int N,

@@ -672,12 +672,11 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : V <= 16 ? 5 : 2) moe_route_k
   load_row<V>(a, t, lane, x);
   int idx;
   float xsel, ssel, w;
-  if (decide<V>(a, t, x, lane, idx, xsel, ssel))
-{
+  if (decide<V>(a, t, x, lane, idx, xsel, ssel)) {
     if (decide_again<V, Pair>(a, t, lane, idx, w)) decide_again<V, double>(a, t, lane, idx, w);
-  }
-  else
+  } else {
     w = weight_of(a, idx, xsel, ssel);
+  }
   if (lane < a.k) {
     const int64_t o = static_cast<int64_t>(t) * a.k + lane;
     a.ids[o] = idx;
@@ -687,11 +686,11 @@ __global__ void __launch_bounds__(128, V <= 8 ? 8 : V <= 16 ? 5 : 2) moe_route_k
 
 }  // namespace
 
-cudaError_t launch_moe_route(const MoeRouteProblem& p, const DeviceInfo& dev, cudaStream_t s) {
-  (void)dev;
+cudaError_t launch_moe_route(const MoeRouteProblem& p, cudaStream_t s) {
   const RouteArgs a{p.logits, p.bias, p.ld, p.weights, p.ids, p.T, p.E, p.top_k, p.sigmoid, p.n_group, p.topk_group,
                     p.group_top, p.renormalize, p.bf16,
-                    (reinterpret_cast<uintptr_t>(p.logits) & 15) == 0 && p.ld % 8 == 0, (reinterpret_cast<uintptr_t>(p.bias) & 15) == 0, p.scale};
+                    (reinterpret_cast<uintptr_t>(p.logits) & 15) == 0 && p.ld % 8 == 0,
+                    (reinterpret_cast<uintptr_t>(p.bias) & 15) == 0, p.scale};
   const int grid = static_cast<int>(ceil_div(p.T, 4));
   if (p.E <= 32) return launch_pdl(moe_route_kernel<1>, grid, 128, 0, s, a);
   if (p.E <= 64) return launch_pdl(moe_route_kernel<2>, grid, 128, 0, s, a);
