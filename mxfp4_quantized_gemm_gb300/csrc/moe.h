@@ -41,7 +41,7 @@ struct MoePlan {
   int32_t* tickets;        // [2][kMoeTickets]: parts that have arrived, per cut tile of either product
   int max_tiles;
 };
-constexpr int kMoeTickets = 4096;
+constexpr int kMoeTickets = 1024;   // cut tiles: fewer than two a CTA
 // Row tiles that P pairs over E experts fill at most.
 inline int64_t moe_max_tiles(int64_t P, int E) { return P / kRowTile + (P < E ? P : E); }
 size_t moe_plan_bytes(int64_t P, int E);
