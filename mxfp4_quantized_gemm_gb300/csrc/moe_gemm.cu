@@ -58,9 +58,8 @@ constexpr int kFewBatch = 16;                      // rows of a tile of few rows
 // 128 columns.
 constexpr int kStageWarp = 8 * 256;
 static_assert(8 * kStageWarp >= kFewBatch * kTileN * 4, "the rows handed out share the staging area");
-// Segments found ahead: the record of each and the pairs of its rows.
-constexpr int kSegs = 8;
-constexpr int kSegBytes = 32 + kRowTile * 4;
+constexpr int kSegs = 8;                           // segments found ahead
+constexpr int kSegBytes = 32;
 constexpr int kSegReaders = 3 + 8;                 // both producers, the MMA issuer and the epilogue warps
 // Of few pairs: their ids, the number of row tiles, each one's expert.
 constexpr int kFewWords = kMoeFewPairs + 2 + kMoeFewPairs + 2;
@@ -233,20 +232,14 @@ struct FewPlan {
       for (int i = counts[e]; i > 0; i -= kRowTile) *tile++ = static_cast<uint16_t>(e);
   }
   static __device__ __forceinline__ int row_tiles(const uint16_t* w) { return w[kMoeFewPairs]; }
-  // The word of row tile rt, as the plan's; its pairs to pairs[0 ..].
-  static __device__ __forceinline__ int tile(const uint16_t* w, int rt, int lane, int* pairs) {
+  // The word of row tile rt, as the plan's.
+  static __device__ __forceinline__ int tile(const uint16_t* w, int rt, int lane) {
     const uint16_t* experts = w + kMoeFewPairs + 1;
     const int e = experts[rt];
-    int row = rt > 0 && experts[rt - 1] == e ? -kRowTile : 0;   // of the expert's first pair
+    int rows = rt > 0 && experts[rt - 1] == e ? -kRowTile : 0;   // without the expert's first tile, if this is its second
 #pragma unroll 1
-    for (int q = 0; q < kMoeFewPairs; q += 32) {
-      const bool on = w[q + lane] == e;
-      const uint32_t m = __ballot_sync(0xFFFFFFFFu, on);
-      const int mine = row + __popc(m & ((1u << lane) - 1u));
-      if (on && mine >= 0 && mine < kRowTile) pairs[mine] = q + lane;
-      row += __popc(m);
-    }
-    return e | ((row < kRowTile ? row : kRowTile) << 16);
+    for (int q = 0; q < kMoeFewPairs; q += 32) rows += __popc(__ballot_sync(0xFFFFFFFFu, w[q + lane] == e));
+    return e | ((rows < kRowTile ? rows : kRowTile) << 16);
   }
 };
 
@@ -886,8 +879,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     // ---- warp 3: the segments of this CTA, ahead of the other roles.  The plan
     // is complete when this kernel starts (the kernel before it lets it start
     // only after its own wait for the plan); that of few pairs it finds itself.
-    // A segment's tile word and pairs are loaded while the one before it is
-    // handed out.
+    // A segment's tile word is loaded while the one before it is handed out.
     const bool few_pairs = g.ids != nullptr;
     const uint16_t* found = reinterpret_cast<const uint16_t*>(segs + kSegs * kSegBytes);
     int tiles32 = 0;
@@ -895,7 +887,6 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     Walk walk;
     walk.init(g, few_pairs ? FewPlan::row_tiles(found) : __ldcg(g.hdr));
     int rt = -1;
-    int4 pairs = make_int4(-1, -1, -1, -1);
     int info = 0;
     bool more = true;
     while (more && !abort) {
@@ -903,20 +894,14 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
       if (!more) s.rt = -1;
       if (more && s.rt != rt) {
         rt = s.rt;
-        if (!few_pairs) {
-          info = rt < 32 ? __shfl_sync(0xFFFFFFFFu, tiles32, rt & 31) : __ldcg(g.tile + rt);
-          if (!kGated) pairs = __ldcg(reinterpret_cast<const int4*>(g.row_pair + static_cast<int64_t>(rt) * kRowTile) + lane);
-        }
+        info = few_pairs ? FewPlan::tile(found, rt, lane)
+               : rt < 32 ? __shfl_sync(0xFFFFFFFFu, tiles32, rt & 31)
+                         : __ldcg(g.tile + rt);
       }
       mbar_wait(&seg_empty[sslot], sphase ^ 1, abort);
       abort = __any_sync(0xFFFFFFFFu, abort);
       if (abort) break;
       uint8_t* rec = segs + sslot * kSegBytes;
-      if (few_pairs) {
-        if (more) info = FewPlan::tile(found, rt, lane, reinterpret_cast<int*>(rec + 32));
-      } else if (!kGated) {
-        reinterpret_cast<int4*>(rec + 32)[lane] = pairs;
-      }
       if (lane == 0) {
         reinterpret_cast<int4*>(rec)[0] = make_int4(s.rt, s.nt, s.k0, s.len);
         reinterpret_cast<int4*>(rec)[1] = make_int4(s.half, s.left, info, 0);
@@ -943,26 +928,31 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     // how the cut tiles are dealt out, for their sums
     Walk walk;
     walk.init(g, __ldcg(g.hdr));
+    int pair_rt = -1, pair_of_row = -1;           // the row tile whose pairs this lane has: of row rl, or of row lane
+    bool pair_few = false;                        // where the tile has few rows
     for (int seg = 0; next_segment(); ++seg) {
       const int rows = s.info >> 16, expert = s.info & 0xFFFF;
       const bool whole = s.len == g.KT, few = whole && rows <= kFewRows;
       const int first_c8 = s.half > 0 ? 16 : 0;
-      const int* pairs = reinterpret_cast<const int*>(segs + sslot * kSegBytes + 32);
-      const int pair = rl < rows ? (kGated ? 0 : pairs[rl]) : -1;
+      if (!kGated && (s.rt != pair_rt || few != pair_few)) {
+        pair_rt = s.rt;
+        pair_few = few;
+        const int row = few ? lane : rl;
+        pair_of_row = row < rows ? __ldcg(g.row_pair + static_cast<int64_t>(s.rt) * kRowTile + row) : -1;
+      }
+      const int pair = kGated ? (rl < rows ? 0 : -1) : pair_of_row;
       uint32_t b[4] = {0, 0, 0, 0}, b4[2] = {0, 0};
       if (few)
         load_bias<8>(g, expert, s.nt * kTileN + 8 * ((lane + first_c8) & 31), b);
       else
         load_bias<4>(g, expert, s.nt * kTileN + (s.half < 0 ? h : s.half) * 128 + 4 * lane, b4);
-      // this warp has read the record (the pairs of few rows are read below)
-      auto release = [&]() {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&seg_empty[sslot]);
-        if (++sslot == kSegs) {
-          sslot = 0;
-          sphase ^= 1;
-        }
-      };
+      // this warp has read the record
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[sslot]);
+      if (++sslot == kSegs) {
+        sslot = 0;
+        sphase ^= 1;
+      }
       const bool ok = mbar_wait(acc_full, seg & 1, abort);
       tc_fence_after();
       uint32_t r[128];
@@ -1000,15 +990,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
             const float4* p = reinterpret_cast<const float4*>(sums + part_at(row - row0, lane));
             const float4 lo = p[0], hi = p[1];
             float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            finish_row<kGated>(g, s, row, kGated ? 0 : pairs[row], (lane + first_c8) & 31,
+            finish_row<kGated>(g, s, row, kGated ? 0 : __shfl_sync(0xFFFFFFFFu, pair, row), (lane + first_c8) & 31,
                                s.half < 0 || lane < 16, b, v);
           }
           epi_barrier();
         }
-        release();
         continue;
       }
-      release();
       if (whole) {
         if (q * 32 < rows) finish<kGated>(g, s, make_uint2(b4[0], b4[1]), pair, rl, h, lane, stage, r);
         staged = true;
