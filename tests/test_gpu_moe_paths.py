@@ -107,6 +107,25 @@ def test_scales_that_stay_and_that_do_not(capi, K):
     check_rows(capi, 150, 1, 2, 1100, K, ids, np.arange(0, 150, 3), seed=K)
 
 
+@pytest.mark.parametrize("K", [130, 256, 512, 700, 6144, 6400, 6600])
+@pytest.mark.parametrize("T", [5, 60, 70])
+def test_halves_of_few_rows(capi, T, K):
+    # few tiles: halves on a block each, finished row by row up to 32 rows; scales
+    # that stay (up to K = 6144) and that do not
+    ids = (np.arange(T) % 3 == 0).astype(np.int32)[:, None]
+    check_rows(capi, T, 1, 2, 300, K, ids, np.arange(T), seed=K + T)
+
+
+@pytest.mark.parametrize("K,I", [(700, 130), (6400, 520)])
+def test_gated_halves_of_few_rows(capi, K, I):
+    T = 40
+    up, down = Experts(capi, 2, 2 * I, K, 4, True), Experts(capi, 2, 300, I, 5, True)
+    x = synth.activations(T, K, 4)
+    ids, w = routing(T, 2, 1, K)
+    out = run_ffn(capi, dev_bf16(x), dev_i32(ids), dev_f32(w), up, down, "silu")
+    check_ffn(out, want_ffn(x, ids, w, up, down, "silu"), f"gated halves, K={K}")
+
+
 @pytest.mark.parametrize("T", [2, 150])
 def test_gated_cut_tiles(capi, T):
     up, down = Experts(capi, 1, 2 * 130, 14336, 4, True), Experts(capi, 1, 72, 130, 5, True)
