@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
       mbar_init(&empty[s], 1);
     }
     mbar_init(acc_full, 1);
-    mbar_init(acc_empty, kEpiThreads);
+    mbar_init(acc_empty, kEpiThreads / 32);
     for (int q = 0; q < kSegs; ++q) {
       mbar_init(&seg_full[q], 1);
       mbar_init(&seg_empty[q], kSegReaders);
@@ -964,7 +964,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
         tmem_wait_ld();
       }
       tc_fence_before();
-      mbar_arrive(acc_empty);                     // accumulator free for the next segment
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);      // accumulator free for the next segment
       const bool live = rl < rows;
       if (!ok) {
 #pragma unroll
