@@ -480,9 +480,8 @@ MXFP4_API mxfp4_status mxfp4_mla_prefill(const void* q_nope_dev, int64_t qn_tok,
 
 /*
  * Mixture of experts in MXFP4: the router's choice, each routed token times
- * its expert's W4A4 weights, and the experts' whole gated network.  The
- * pages' models have such layers (PR #39598 names them); the operators follow
- * the published definitions.  They serve: nothing here has a gradient.
+ * its expert's W4A4 weights, and the experts' whole gated network, by the
+ * published definitions.  They serve: nothing here has a gradient.
  *
  * A token t has top_k slots; slot j names expert ids[t][j] (int32).  A
  * negative id is an empty slot (a padding token of a captured batch, or a
@@ -497,7 +496,9 @@ MXFP4_API mxfp4_status mxfp4_mla_prefill(const void* q_nope_dev, int64_t qn_tok,
  * row's stride is not read.  bf16 and fp32 pointers need their type's
  * alignment only (rows whose pointer and stride allow 16-byte accesses are
  * faster); packed weights and workspaces are 16-byte aligned.  Workspaces
- * need no initialization; calls sharing one must be ordered on the GPU.
+ * need no initialization; calls sharing one must be ordered on the GPU.  The
+ * kernels read all inputs, packed weights too, behind the kernels ahead of the
+ * call: mxfp4_weights_updated is not needed for them.
  * Deterministic: the same call gives the same bits.
  */
 typedef enum {

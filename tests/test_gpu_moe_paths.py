@@ -217,6 +217,38 @@ def test_captured_and_replayed_with_new_values(capi, T):
     assert capi.mxfp4_get_device_error() == capi.OK
 
 
+@pytest.mark.parametrize("T", [6, 200])
+def test_weights_and_ids_written_by_the_kernels_before(capi, T):
+    # copies straight before the calls, in one graph: no ordering call is needed
+    up, down, x, ids, w, r = ffn_case(capi, T, 4, 6, 512, 320, 384, 31)
+    up2, down2, x2, ids2, w2, _ = ffn_case(capi, T, 4, 6, 512, 320, 384, 41)
+    want = run_ffn(capi, x2, ids2, w2, up2, down2, "silu", r)
+    want_rows = run_linear(capi, x2, ids2, up2)
+    out, rows = torch.zeros_like(want), torch.zeros_like(want_rows)
+    ws, ws2 = workspace(ws_bytes(capi, ids, up, down)), workspace(ws_bytes(capi, ids, up, down))
+    sources = [(x, x2), (ids, ids2), (w, w2), (up.bias_dev, up2.bias_dev), (down.bias_dev, down2.bias_dev),
+               (down.packed, down2.packed), (up.packed, up2.packed)]
+    first = [a.clone() for a, _ in sources]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for a, b in sources:
+                a.copy_(b)
+            run_ffn(capi, x, ids, w, up, down, "silu", r, out=out, ws=ws)
+            run_linear(capi, x, ids, up, out=rows, ws=ws2)
+            for (a, _), b in zip(sources, first):
+                a.copy_(b)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        out.zero_()
+        rows.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(rows, want_rows)
+
+
 def test_two_streams_with_a_workspace_each(capi):
     cases = [ffn_case(capi, 50, 3, 6, 256, 128, 256, 20), ffn_case(capi, 333, 2, 4, 384, 256, 200, 21)]
     want = [run_ffn(capi, *c[2:5], c[0], c[1], "silu", c[5]) for c in cases]
