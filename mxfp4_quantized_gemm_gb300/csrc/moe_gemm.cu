@@ -48,7 +48,7 @@ using C = Cfg<128>;
 constexpr int kUnit = 4;                           // tiles of one row tile that a CTA takes in turn
 constexpr int kPartFloats = 128 * kTileN;          // one part of a cut tile
 constexpr int kMinSteps = 2;                       // k-steps a CTA takes at least where tiles are cut
-constexpr int kCutSteps = 12;                      // what cutting costs, in k-steps (see Walk)
+constexpr int kCutSteps = 12, kCutRows = 10;       // what cutting costs, in k-steps: 12 and one for 10 rows (see Walk)
 constexpr int kFewRows = 32;                       // rows up to which a tile is finished row by row
 // Warp 0 brings the weights, warp 2 the activations, warp 1 issues the MMAs,
 // warp 3 finds the segments for all of them; warps 4..11 are the epilogue.  The
@@ -107,14 +107,17 @@ static_assert(sizeof(Segment) == 32, "two 16-byte words");
 
 // A CTA's share of the tiles, segment by segment.
 //  1. whole rounds of units: `unit` neighbouring tiles of one row tile, whose
-//     activations (and their scales in TMEM) serve them all; the last round
-//     may leave a twelfth of the CTAs without one;
+//     activations (and their scales in TMEM) serve them all (8192 x 8 of 64:
+//     units of four 690 us, of eight 694, of one or two slower still);
 //  2. whole rounds of single tiles;
 //  3. the fewer than G tiles left: each on a CTA of its own, or as halves on
 //     two, or cut evenly along (tile, k-step) over all CTAs together with one
-//     of the rounds before, whichever takes the fewest k-steps, with kCutSteps
-//     for the cut's sums.  A tile is cut for at most four CTAs: the sum reads
-//     every part (ten parts of 128 rows took 30 us).
+//     of the rounds before, whichever takes the fewest k-steps, with the cost
+//     of the cut's sums: what every row of a tile leaves in memory is written
+//     and read once per part.  A tile is cut for at most four CTAs: the sum reads
+//     every part (ten parts of 128 rows took 30 us).  16 rows of K = 14336 by
+//     512 to 2048 columns take 24 us, uncut 34; 500 rows by 2048 uncut 42, cut 46;
+//     2048 rows of K = 28672 by 2048 columns uncut 110, cut 124.
 struct Walk {
   int units_per_row, unit_end, units, u, i;   // units: this CTA's next, tile of it
   int t_end, t;                               // single tiles: this CTA's next
@@ -125,14 +128,13 @@ struct Walk {
     const int G = gridDim.x, c = blockIdx.x;
     units_per_row = (g.n_tiles + g.unit - 1) / g.unit;
     units = row_tiles * units_per_row;
-    int rounds = units / G;
+    const int rounds = units / G;
     const int tiles = row_tiles * g.n_tiles;
     h = h_end = its = it = it1 = 0;
     parts_ctas = 1;
     u = c;
     i = 0;
     t = t_end = tiles;
-    if ((units - rounds * G) * 12 >= 11 * G) ++rounds;
     unit_end = rounds * G;
     if (unit_end >= units) return;
     const int t0 = (unit_end / units_per_row) * g.n_tiles + (unit_end % units_per_row) * g.unit;
@@ -142,8 +144,9 @@ struct Walk {
     const int rest = tiles - t_end;
     if (rest == 0) return;
     const int whole = 2 * rest > G ? g.KT : (g.KT + 1) / 2;
+    const int rows = g.P / row_tiles, cost = kCutSteps + (rows < kRowTile ? rows : kRowTile) / kCutRows;
     const int even = static_cast<int>(static_cast<long long>(rest) * g.KT / G), quarter = (g.KT + 3) / 4;
-    if ((singles > 0 ? even : (even > quarter ? even : quarter)) + kCutSteps < whole) {
+    if ((singles > 0 ? even : (even > quarter ? even : quarter)) + cost < whole) {
       if (singles > 0) t_end -= G;
       const int cut = tiles - t_end;
       its = cut * g.KT;

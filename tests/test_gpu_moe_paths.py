@@ -74,10 +74,17 @@ def test_cut_tiles(capi, T):
     check_rows(capi, T, 1, 1, 300, 14336, ids, np.arange(T), seed=T)
 
 
+@pytest.mark.parametrize("T", [40, 200])
+def test_cut_tiles_of_many_rows(capi, T):
+    # 112 k-steps: worth a cut with any number of rows
+    ids = np.zeros((T, 1), dtype=np.int32)
+    check_rows(capi, T, 1, 1, 300, 28672, ids, np.arange(0, T, 3), seed=T)
+
+
 @pytest.mark.parametrize("at", [16, 48])
 def test_cut_tiles_with_a_workspace_aligned_to_16_bytes(capi, at):
     # the parts of cut tiles are read and written 32 bytes at a time
-    T, K = 40, 14336
+    T, K = 40, 28672
     w = Experts(capi, 1, 300, K, 8, True)
     x, ids = dev_bf16(synth.activations(T, K, 8)), torch.zeros(T, 1, dtype=torch.int32, device="cuda")
     n = capi.mxfp4_moe_linear_workspace_bytes(T, 1, 1, 300, K)
@@ -105,6 +112,15 @@ def test_cut_tiles_after_whole_rounds(capi):
 def test_scales_that_stay_and_that_do_not(capi, K):
     ids = routing(150, 2, 1, K)[0]
     check_rows(capi, 150, 1, 2, 1100, K, ids, np.arange(0, 150, 3), seed=K)
+
+
+def test_gated_cut_tiles_of_many_rows(capi):
+    T, K = 150, 28672
+    up, down = Experts(capi, 1, 2 * 130, K, 4, True), Experts(capi, 1, 72, 130, 5, True)
+    x = synth.activations(T, K, 4)
+    ids, w = np.zeros((T, 1), dtype=np.int32), np.ones((T, 1), dtype=np.float32)
+    out = run_ffn(capi, dev_bf16(x), dev_i32(ids), dev_f32(w), up, down, "silu")
+    check_ffn(out, want_ffn(x, ids, w, up, down, "silu"), "gated, cut, 150 rows of 28672")
 
 
 @pytest.mark.parametrize("K", [130, 256, 512, 700, 6144, 6400, 6600])
