@@ -243,7 +243,8 @@ struct FewPlan {
   static __device__ __forceinline__ int tile(const uint16_t* w, int rt, int lane) {
     const uint16_t* experts = w + kMoeFewPairs + 1;
     const int e = experts[rt];
-    int rows = rt > 0 && experts[rt - 1] == e ? -kRowTile : 0;   // without the expert's first tile, if this is its second
+    // the expert's rows, without its first tile's if this is its second
+    int rows = rt > 0 && experts[rt - 1] == e ? -kRowTile : 0;
 #pragma unroll 1
     for (int q = 0; q < kMoeFewPairs; q += 32) rows += __popc(__ballot_sync(0xFFFFFFFFu, w[q + lane] == e));
     return e | ((rows < kRowTile ? rows : kRowTile) << 16);
@@ -371,8 +372,8 @@ __device__ __forceinline__ float gated(const MoeArgs& g, float gate, float up) {
 // `bias`: of columns n0 + 4 lane .. n0 + 4 lane + 3.  All 32 lanes call this
 // together.
 template <bool kGated>
-__device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, uint2 bias, int pair, int rl, int h, int lane,
-                                       uint8_t* stage, uint32_t (&acc)[128]) {
+__device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, uint2 bias, int pair, int rl, int h,
+                                       int lane, uint8_t* stage, uint32_t (&acc)[128]) {
   if (s.half >= 0) {
     if (h != 0) return;                            // half a tile is in the first 128 columns
     h = s.half;
@@ -400,7 +401,8 @@ __device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, uint2
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            w[j][i] = pack_bf16x2(__uint_as_float(acc[c0 + 16 * j + 2 * i]), __uint_as_float(acc[c0 + 16 * j + 2 * i + 1]));
+            w[j][i] = pack_bf16x2(__uint_as_float(acc[c0 + 16 * j + 2 * i]),
+                                  __uint_as_float(acc[c0 + 16 * j + 2 * i + 1]));
 #pragma unroll
         for (int bit = 1; bit < 4; bit <<= 1) {
           const bool up = (q & bit) != 0;
@@ -663,7 +665,8 @@ __device__ __forceinline__ void issue_half_mmas(uint32_t tmem, uint32_t stage, u
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     mma_mxf4(tmem, sdesc_sw128(stage + C::kW + 32 * q), sdesc_sw128(stage + 32 * q),
-             idesc_mxf4(128, 128, (q & 1) * 2, (q & 1) * 2), tmem + sfa_col + 4 * (q >> 1), tmem + sfb_col + 8 * (q >> 1),
+             idesc_mxf4(128, 128, (q & 1) * 2, (q & 1) * 2), tmem + sfa_col + 4 * (q >> 1),
+             tmem + sfb_col + 8 * (q >> 1),
              (accumulate != 0 || q != 0) ? 1u : 0u);
 }
 
@@ -889,8 +892,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     // A segment's tile word is loaded while the one before it is handed out.
     const bool few_pairs = g.ids != nullptr;
     const uint16_t* found = reinterpret_cast<const uint16_t*>(segs + kSegs * kSegBytes);
-    int tiles32 = 0;
-    if (!few_pairs && lane < g.max_tiles) tiles32 = __ldcg(g.tile + lane);   // beside their number, for the first segments
+    int tiles32 = 0;                              // loaded beside their number, for the first segments
+    if (!few_pairs && lane < g.max_tiles) tiles32 = __ldcg(g.tile + lane);
     Walk walk;
     walk.init(g, few_pairs ? FewPlan::row_tiles(found) : __ldcg(g.hdr));
     int rt = -1;

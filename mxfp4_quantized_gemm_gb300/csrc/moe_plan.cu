@@ -204,8 +204,8 @@ __device__ __forceinline__ void store_unit(const GatherArgs& a, int t, int kt, i
   // lowest bits hold the row's rotation), and its row of scales in the block.
   constexpr uint32_t kNowhere = 0xFFFFFFFFu;
   const int i = pos & 127;
-  const uint32_t place = pos < 0 ? kNowhere
-                                 : (static_cast<uint32_t>(pos >> 7) * a.KT + kt) * (kMoeBlockBytes / 16) + 8 * i + (i & 7);
+  const uint32_t block = static_cast<uint32_t>(pos >> 7) * a.KT + kt;
+  const uint32_t place = pos < 0 ? kNowhere : block * (kMoeBlockBytes / 16) + 8 * i + (i & 7);
   const int scale = kTileBytes - 128 * i + ((i & 31) << 4) + ((i >> 5) << 2);   // bytes from the row's codes
   for (int s = lane & 3; s < a.k + (lane & 3); s += 4) {   // (whole warps loop; lanes >= k hold no place)
     const uint32_t at = __shfl_sync(0xFFFFFFFFu, place, s);
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(256) moe_combine_kernel(const __grid_constant_
 
 size_t moe_plan_bytes(int64_t P, int E) {
   const int64_t rt = moe_max_tiles(P, E);
-  const size_t ints = static_cast<size_t>(ceil_div(rt, 4) * 4) + static_cast<size_t>(rt) * kRowTile + static_cast<size_t>(P) + 2 * kMoeTickets;
+  const size_t ints = static_cast<size_t>(ceil_div(rt, 4) * 4 + rt * kRowTile + P + 2 * kMoeTickets);
   return kPlanHeader + 4 * ints + 64;
 }
 

@@ -187,16 +187,16 @@ __device__ __forceinline__ bool open(Pair a, Pair b, float error) {
 }
 __device__ __forceinline__ bool open(double, double, float) { return false; }
 
-// Decides row t in numbers F (Pair or double).  Lane l holds elements l * V ..
-// l * V + V - 1 of the row, so the lowest lane and place of equal values is the
-// lowest index.  At the end lane r < k holds the r-th choice: its index (-1:
-// none), its logit and its score.  Returns whether a comparison that mattered
-// stayed open.
 __device__ __forceinline__ float logit_at(const RouteArgs& a, int t, int i) {
   const int64_t at = static_cast<int64_t>(t) * a.ld + i;
   return a.bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(a.x)[at]) : static_cast<const float*>(a.x)[at];
 }
 
+// Decides row t in numbers F (Pair or double).  Lane l holds elements l * V ..
+// l * V + V - 1 of the row, so the lowest lane and place of equal values is the
+// lowest index.  At the end lane r < k holds the r-th choice: its index (-1:
+// none), its logit and its score.  Returns whether a comparison that mattered
+// stayed open.
 template <int V, typename F>
 __device__ __forceinline__ bool decide_in(const RouteArgs& a, int t, int lane, int& idx, float& xsel, float& ssel) {
   const bool biased = a.bias != nullptr, sigmoid = a.sigmoid != 0;
@@ -434,8 +434,8 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[V]) {
         }
 }
 
-// Decides row t in fp32, as decide_exactly does.  Returns whether a comparison
-// that mattered was too near for fp32.
+// Decides row t in fp32, as decide_in does.  Returns whether a comparison that
+// mattered was too near for fp32.
 template <int V>
 __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&x)[V], int lane, int& idx, float& xsel,
                                        float& ssel) {
@@ -655,7 +655,8 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, int t, int lane, fl
     for (int j = 0; j < V; ++j) {
       x[j] = -INFINITY;
       if (lane * V + j < a.E)
-        x[j] = a.bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(a.x)[at + j]) : static_cast<const float*>(a.x)[at + j];
+        x[j] = a.bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(a.x)[at + j])
+                      : static_cast<const float*>(a.x)[at + j];
     }
   }
 #pragma unroll
@@ -663,7 +664,8 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, int t, int lane, fl
 }
 
 template <int V>
-__global__ void __launch_bounds__(128, V <= 8 ? 8 : V <= 16 ? 5 : 2) moe_route_kernel(const __grid_constant__ RouteArgs a) {
+__global__ void __launch_bounds__(128, V <= 8 ? 8 : V <= 16 ? 5 : 2)
+    moe_route_kernel(const __grid_constant__ RouteArgs a) {
   const int lane = threadIdx.x & 31;
   const int t = static_cast<int>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   griddep_launch_dependents();

@@ -280,6 +280,49 @@ def test_two_streams_with_a_workspace_each(capi):
         assert torch.equal(a, b)
 
 
+def test_two_host_threads_whose_first_calls_are_theirs(capi):
+    # one captures its first call and replays it, the other calls beside it
+    import threading
+    cases = [ffn_case(capi, 50, 3, 6, 256, 128, 256, 20), ffn_case(capi, 333, 2, 4, 384, 256, 200, 21)]
+    want = [run_ffn(capi, *c[2:5], c[0], c[1], "silu", c[5]) for c in cases]
+    outs = [torch.zeros_like(v) for v in want]
+    wss = [workspace(ws_bytes(capi, c[3], c[0], c[1])) for c in cases]
+    torch.cuda.synchronize()
+    errors = []
+
+    def call(i, stream=None):
+        c = cases[i]
+        run_ffn(capi, *c[2:5], c[0], c[1], "silu", c[5], out=outs[i], ws=wss[i], stream=stream)
+
+    def captured():
+        try:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, capture_error_mode="thread_local"):
+                call(0)
+            for _ in range(10):
+                graph.replay()
+            torch.cuda.synchronize()
+        except Exception as e:      # noqa: BLE001 (told to the main thread)
+            errors.append(e)
+
+    def eager():
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(10):
+                call(1, s)
+            s.synchronize()
+        except Exception as e:      # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=f) for f in (captured, eager)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
 def test_one_expert_is_the_dense_layer(capi):
     # moe_linear of one expert against mxfp4_gemm: both within 2 ulp of the same
     # exact value; here on values whose sums are exact in fp32, so the same bits
