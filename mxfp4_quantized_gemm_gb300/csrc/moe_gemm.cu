@@ -59,8 +59,9 @@ constexpr int kMoeThreads = 384;
 constexpr int kFirstEpiWarp = 4;
 constexpr int kFewBatch = 16;                      // rows of a tile of few rows that are handed out at once
 // Staging of bf16 rows that allow no wide access: per epilogue warp 8 rows of
-// 128 columns.
-constexpr int kStageWarp = 8 * 256;
+// 128 columns, a pitch apart whose 16-byte pieces meet different banks.
+constexpr int kStagePitch = 256 + 16;
+constexpr int kStageWarp = 8 * kStagePitch;
 static_assert(8 * kStageWarp >= kFewBatch * kTileN * 4, "the rows handed out share the staging area");
 constexpr int kSegs = 8;                           // segments found ahead
 constexpr int kSegBytes = 32;
@@ -435,61 +436,40 @@ __device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, uint2
       return;
     }
     // Rows that allow no wide access or end inside the tile: 8 rows at a time
-    // through the warp's staging area (16-byte pieces rotated by the row), then
-    // 16 bytes at an aligned address of the output by each lane, put together
-    // from the two pieces they span.  (Column by column, 64 bytes a row and
-    // store, 1500 x 2 tokens of 1001 columns took 30 us, 13 of them here.)
+    // through the warp's staging area, then a row at a time in aligned words of
+    // two columns, which straddle the staged ones where the row starts at an odd
+    // column: 24.5 us for 1500 x 2 tokens of 1001 columns, 19 of 1024 (L2 takes
+    // whole lines several times as fast).  Column by column it took 30, by 16 bytes a
+    // lane, put together from two pieces at a place that depends on the row, 25.5.
     const int count = g.N - n0 < 128 ? g.N - n0 : 128;
     for (int b = 0; b < 4; ++b) {
       if ((lane >> 3) == b) {
 #pragma unroll
         for (int c = 0; c < 16; ++c)
-          *reinterpret_cast<uint4*>(stage + (lane & 7) * 256 + ((c ^ lane) & 7) * 16 + (c & 8) * 16) = make_uint4(
+          *reinterpret_cast<uint4*>(stage + (lane & 7) * kStagePitch + c * 16) = make_uint4(
               pack_bf16x2(__uint_as_float(acc[8 * c]), __uint_as_float(acc[8 * c + 1])),
               pack_bf16x2(__uint_as_float(acc[8 * c + 2]), __uint_as_float(acc[8 * c + 3])),
               pack_bf16x2(__uint_as_float(acc[8 * c + 4]), __uint_as_float(acc[8 * c + 5])),
               pack_bf16x2(__uint_as_float(acc[8 * c + 6]), __uint_as_float(acc[8 * c + 7])));
       }
       __syncwarp();
-#pragma unroll 1
-      for (int at = lane; at < 8 * 17 + 24; at += 32) {   // (whole warps loop: 8 rows of 17 places)
-        const int r = at / 17, w = at - 17 * r;
-        const int p = __shfl_sync(0xFFFFFFFFu, pair, (8 * b + r) & 31);
-        if (r >= 8 || p < 0) continue;
-        uint16_t* dst = g.out + static_cast<int64_t>(p) * g.ldo + n0;
-        const int m = static_cast<int>((reinterpret_cast<uintptr_t>(dst) >> 1) & 7);
-        const int c = 8 * w - m;                   // the place's first column
-        if (c >= count) continue;
-        const uint8_t* src = stage + r * 256;
-        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;   // pieces w - 1 and w
-        if (w > 0) lo = *reinterpret_cast<const uint4*>(src + (((w - 1) ^ r) & 7) * 16 + ((w - 1) & 8) * 16);
-        if (w < 16) hi = *reinterpret_cast<const uint4*>(src + ((w ^ r) & 7) * 16 + (w & 8) * 16);
-        // 8 values from the (8 - m)-th of the two pieces on
-        uint32_t q[9] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w, 0};
-        const int skip = 8 - m;
-        if (skip & 8) {
+#pragma unroll 4
+      for (int r = 0; r < 8; ++r) {
+        const int p = __shfl_sync(0xFFFFFFFFu, pair, 8 * b + r);
+        uint16_t* dst = g.out + static_cast<int64_t>(p < 0 ? 0 : p) * g.ldo + n0;
+        const int end = p < 0 ? 0 : count;
+        const uint32_t* row = reinterpret_cast<const uint32_t*>(stage + r * kStagePitch);
+        const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1) & 1;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) q[i] = q[i + 4];
+        for (int u = 0; u < 2; ++u) {
+          const int i = lane + 32 * u, c = 2 * i + odd;
+          const uint32_t v = __funnelshift_r(row[i], row[i + 1], 16 * odd);   // (past the row's end: unused)
+          if (c + 1 < end)
+            *reinterpret_cast<uint32_t*>(dst + c) = v;
+          else if (c < end)
+            dst[c] = static_cast<uint16_t>(v);
         }
-        if (skip & 4) {
-#pragma unroll
-          for (int i = 0; i < 6; ++i) q[i] = q[i + 2];
-        }
-        if (skip & 2) {
-#pragma unroll
-          for (int i = 0; i < 5; ++i) q[i] = q[i + 1];
-        }
-        if (skip & 1) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) q[i] = __funnelshift_r(q[i], q[i + 1], 16);
-        }
-        if (c >= 0 && c + 8 <= count) {
-          *reinterpret_cast<uint4*>(dst + c) = make_uint4(q[0], q[1], q[2], q[3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c + e >= 0 && c + e < count) dst[c + e] = static_cast<uint16_t>(q[e >> 1] >> (16 * (e & 1)));
-        }
+        if (odd != 0 && lane == 0 && end > 0) dst[0] = static_cast<uint16_t>(row[0]);
       }
       __syncwarp();
     }
