@@ -49,7 +49,9 @@ constexpr int kUnit = 4;                           // tiles of one row tile that
 constexpr int kPartFloats = 128 * kTileN;          // one part of a cut tile
 constexpr int kMinSteps = 2;                       // k-steps a CTA takes at least where tiles are cut
 constexpr int kCutSteps = 12, kCutRows = 10;       // what cutting costs, in k-steps: 12 and one for 10 rows (see Walk)
-constexpr int kFewRows = 32;                       // rows up to which a tile is finished row by row
+// Rows up to which a tile is finished row by row (16 alike; 48: 300 x 3 of 20 24.5
+// us in place of 23.0, 1024 x 8 of 64 163 in place of 152).
+constexpr int kFewRows = 32;
 // Warp 0 brings the weights, warp 2 the activations, warp 1 issues the MMAs,
 // warp 3 finds the segments for all of them; warps 4..11 are the epilogue.  The
 // epilogue holds 128 columns of a row in registers: it takes over what the
@@ -438,9 +440,8 @@ __device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, uint2
     // Rows that allow no wide access or end inside the tile: 8 rows at a time
     // through the warp's staging area, then a row at a time in aligned words of
     // two columns, which straddle the staged ones where the row starts at an odd
-    // column: 24.5 us for 1500 x 2 tokens of 1001 columns, 19 of 1024 (L2 takes
-    // whole lines several times as fast).  Column by column it took 30, by 16 bytes a
-    // lane, put together from two pieces at a place that depends on the row, 25.5.
+    // column: 24.5 us for 1500 x 2 tokens of 1001 columns, of 1024 six less (whole
+    // lines).  Column by column it took 30, by 16 bytes a lane, put together from two pieces at a place that depends on the row, 25.5.
     const int count = g.N - n0 < 128 ? g.N - n0 : 128;
     for (int b = 0; b < 4; ++b) {
       if ((lane >> 3) == b) {
