@@ -664,6 +664,9 @@ __device__ __forceinline__ void copy_scales(const StageDescs& d, uint32_t sfb, u
     tmem_cp_scales(sfb + 12, scale_desc(d.scales + kSw + 3 * kAtom));
   }
 }
+__device__ __forceinline__ void commit_at(uint32_t bar) {   // mma_commit of a barrier's shared address
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
 template <int kN>
 __device__ __forceinline__ void issue_mmas(uint32_t tmem, const StageDescs& d, uint32_t sfb, uint32_t sfa,
                                            uint32_t accumulate) {
@@ -807,6 +810,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     constexpr uint32_t kSfaRes = C::kSfBase + C::kStages * 16u;
     const bool resident = kSfaRes + 8u * static_cast<uint32_t>(g.KT) <= C::kTmemCols;
     const uint32_t ring = smem_u32(smem);
+    const uint32_t full_at = smem_u32(full), empty_at = smem_u32(empty), full_acc_at = smem_u32(acc_full);
+    // columns of the scales of k-step k in stage st
+    const uint32_t sfa0 = tmem + (resident ? kSfaRes : C::kSfBase), sfa_k = resident ? 8 : 0;
+    const uint32_t sfb0 = tmem + C::kSfBase + (resident ? 0 : C::kSfbOff), sfb_st = resident ? 16 : C::kSfSlot;
+    const uint32_t sfa_st = resident ? 0 : C::kSfSlot;
     int cur_rt = -1;
     uint32_t have = 0;
     int st = 0;
@@ -827,50 +835,53 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
       // Two k-steps at a time where both have landed: their scales are copied
       // together, then the MMAs follow (8192 tokens' first product 289 -> 280 us).
       for (int j = 0; j < len;) {
-        mbar_wait(&full[st], phase, abort);
-        abort = __any_sync(0xFFFFFFFFu, abort);
-        if (abort) break;
+        if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(full_at + 8 * st, phase))) {
+          mbar_wait(&full[st], phase, abort);
+          abort = __any_sync(0xFFFFFFFFu, abort);
+          if (abort) break;
+        }
         const int st2 = st + 1 == C::kStages ? 0 : st + 1;
         const uint32_t phase2 = st2 == 0 ? phase ^ 1 : phase;
         int n = 1;
-        if (j + 1 < len && __all_sync(0xFFFFFFFFu, mbar_test_wait(smem_u32(&full[st2]), phase2))) n = 2;
+        if (j + 1 < len && __all_sync(0xFFFFFFFFu, mbar_test_wait(full_at + 8 * st2, phase2))) n = 2;
         tc_fence_after();
         const StageDescs d1(ring + st * C::kStageBytes), d2(ring + st2 * C::kStageBytes);
-        const uint32_t sfa1 = resident ? tmem + kSfaRes + 8u * k : tmem + C::kSfBase + st * C::kSfSlot;
-        const uint32_t sfa2 = resident ? sfa1 + 8u : tmem + C::kSfBase + st2 * C::kSfSlot;
-        const uint32_t sfb1 = resident ? tmem + C::kSfBase + 16u * st : sfa1 + C::kSfbOff;
-        const uint32_t sfb2 = resident ? tmem + C::kSfBase + 16u * st2 : sfa2 + C::kSfbOff;
-        if (elect_one()) {
+        const uint32_t sfa1 = sfa0 + sfa_k * k + sfa_st * st, sfa2 = sfa0 + sfa_k * (k + 1) + sfa_st * st2;
+        const uint32_t sfb1 = sfb0 + sfb_st * st, sfb2 = sfb0 + sfb_st * st2;
+        const uint32_t done1 = empty_at + 8 * st, done2 = empty_at + 8 * st2;
+        auto copies = [&]() {
           copy_scales(d1, sfb1, sfa1, ((have >> (k & 31)) & 1u) == 0, half >= 0);
           if (n == 2) copy_scales(d2, sfb2, sfa2, ((have >> ((k + 1) & 31)) & 1u) == 0, half >= 0);
-        }
-        if (resident) have |= (n == 2 ? 3u : 1u) << k;
-        __syncwarp();
+        };
+        auto mmas = [&]() {
+          if (half < 0)
+            issue_mmas<kTileN>(tmem, d1, sfb1, sfa1, j != 0 ? 1u : 0u);
+          else
+            issue_mmas<128>(tmem, d1, sfb1, sfa1, j != 0 ? 1u : 0u);
+          commit_at(done1);
+          if (n == 2) {
+            if (half < 0)
+              issue_mmas<kTileN>(tmem, d2, sfb2, sfa2, 1u);
+            else
+              issue_mmas<128>(tmem, d2, sfb2, sfa2, 1u);
+            commit_at(done2);
+          }
+          if (j + n == len) commit_at(full_acc_at);
+        };
         if (j == 0) {
+          if (elect_one()) copies();
+          __syncwarp();
           mbar_wait(acc_empty, (seg & 1) ^ 1, abort);
           abort = __any_sync(0xFFFFFFFFu, abort);
           if (abort) break;
           tc_fence_after();
-        }
-        if (elect_one()) {
-          if (half < 0) {
-            issue_mmas<kTileN>(tmem, d1, sfb1, sfa1, j != 0 ? 1u : 0u);
-            mma_commit(&empty[st]);
-            if (n == 2) {
-              issue_mmas<kTileN>(tmem, d2, sfb2, sfa2, 1u);
-              mma_commit(&empty[st2]);
-            }
-          } else {
-            issue_mmas<128>(tmem, d1, sfb1, sfa1, j != 0 ? 1u : 0u);
-            mma_commit(&empty[st]);
-            if (n == 2) {
-              issue_mmas<128>(tmem, d2, sfb2, sfa2, 1u);
-              mma_commit(&empty[st2]);
-            }
-          }
-          if (j + n == len) mma_commit(acc_full);
+          if (elect_one()) mmas();
+        } else if (elect_one()) {
+          copies();
+          mmas();
         }
         __syncwarp();
+        if (resident) have |= (n == 2 ? 3u : 1u) << k;
         j += n;
         k += n;
         st += n;
