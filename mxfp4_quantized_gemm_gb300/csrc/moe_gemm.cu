@@ -12,10 +12,10 @@
 //
 // Few tokens: the weights of the experts they reach are nearly all the bytes
 // and HBM is the bound (64 x 8 of 128 experts, a network of 5120 x 1024: 152 us,
-// 0.86 of the measured rate over the whole call).  Many: the tensor pipe's four
-// MMAs and scale copies per 256-wide k-step, 970 cycles of which the MMAs are
-// 530 (8192 x 8 of 64: 280 us gated, 191 us rows; the second writes 64 KB a tile
-// of four k-steps and leaves the pipe idle while its accumulator is read).
+// 0.87 of the measured rate over the whole call).  Many: the tensor pipe's four
+// MMAs and scale copies per 256-wide k-step, 790 cycles alone, 835 here (8192 x 8
+// of 64, gated: 252 us); the rows of the same call are bound by HBM's writes (671
+// MB in 188 us; nothing but writes goes at 3.85 TB/s).
 // One kernel serves both, one CTA per SM: the ring, the
 // tile (128 activation rows x 256 weight rows) and the roles are those of
 // gemm.cu, and only the live rows of a row tile are loaded and stored.
@@ -111,7 +111,7 @@ static_assert(sizeof(Segment) == 32, "two 16-byte words");
 // A CTA's share of the tiles, segment by segment.
 //  1. whole rounds of units: `unit` neighbouring tiles of one row tile, whose
 //     activations (and their scales in TMEM) serve them all (8192 x 8 of 64:
-//     units of four 690 us, of eight 694, of one or two slower still);
+//     units of four were 690 us, of eight 694, of one or two slower still);
 //  2. whole rounds of single tiles;
 //  3. the fewer than G tiles left: each on a CTA of its own, or as halves on
 //     two, or cut evenly along (tile, k-step) over all CTAs together with one
@@ -631,8 +631,9 @@ __device__ __forceinline__ void finish_cut(const MoeArgs& g, const Walk& walk, c
 // The scale copies and MMAs of a k-step, from the stage's descriptors.  What the
 // issuing warp does between them holds the tensor pipe up, so the stage's two
 // descriptors are formed once and the others are sums with constants: no
-// address in shared memory carries into the fields above it (8192 tokens: 265 +
-// 188 us; 278 + 192 with every descriptor formed from its address).
+// address in shared memory carries into the fields above it (8192 tokens' first
+// product 252 us; 278 with every descriptor formed from its address and the
+// barriers' addresses with them).
 struct StageDescs {
   uint32_t tile, scales;   // low words at the stage's start; the high words are constants
   __device__ __forceinline__ explicit StageDescs(uint32_t stage)
@@ -833,7 +834,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
         sphase ^= 1;
       }
       // Two k-steps at a time where both have landed: their scales are copied
-      // together, then the MMAs follow (8192 tokens' first product 289 -> 280 us).
+      // together, then the MMAs follow (8192 tokens' first product 289 -> 280 us when
+      // it was brought in; three or four at a time 7 and 12% slower).
       for (int j = 0; j < len;) {
         if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(full_at + 8 * st, phase))) {
           mbar_wait(&full[st], phase, abort);
