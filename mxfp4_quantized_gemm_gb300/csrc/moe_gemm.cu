@@ -833,44 +833,25 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
         sslot = 0;
         sphase ^= 1;
       }
-      // Two k-steps at a time where both have landed: their scales are copied
-      // together, then the MMAs follow (8192 tokens' first product 289 -> 280 us when
-      // it was brought in; three or four at a time 7 and 12% slower).
-      for (int j = 0; j < len;) {
+      for (int j = 0; j < len; ++j, ++k) {
         if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(full_at + 8 * st, phase))) {
           mbar_wait(&full[st], phase, abort);
           abort = __any_sync(0xFFFFFFFFu, abort);
           if (abort) break;
         }
-        const int st2 = st + 1 == C::kStages ? 0 : st + 1;
-        const uint32_t phase2 = st2 == 0 ? phase ^ 1 : phase;
-        int n = 1;
-        if (j + 1 < len && __all_sync(0xFFFFFFFFu, mbar_test_wait(full_at + 8 * st2, phase2))) n = 2;
         tc_fence_after();
-        const StageDescs d1(ring + st * C::kStageBytes), d2(ring + st2 * C::kStageBytes);
-        const uint32_t sfa1 = sfa0 + sfa_k * k + sfa_st * st, sfa2 = sfa0 + sfa_k * (k + 1) + sfa_st * st2;
-        const uint32_t sfb1 = sfb0 + sfb_st * st, sfb2 = sfb0 + sfb_st * st2;
-        const uint32_t done1 = empty_at + 8 * st, done2 = empty_at + 8 * st2;
-        auto copies = [&]() {
-          copy_scales(d1, sfb1, sfa1, ((have >> (k & 31)) & 1u) == 0, half >= 0);
-          if (n == 2) copy_scales(d2, sfb2, sfa2, ((have >> ((k + 1) & 31)) & 1u) == 0, half >= 0);
-        };
+        const StageDescs d(ring + st * C::kStageBytes);
+        const uint32_t sfa = sfa0 + sfa_k * k + sfa_st * st, sfb = sfb0 + sfb_st * st;
+        auto copies = [&]() { copy_scales(d, sfb, sfa, ((have >> (k & 31)) & 1u) == 0, half >= 0); };
         auto mmas = [&]() {
           if (half < 0)
-            issue_mmas<kTileN>(tmem, d1, sfb1, sfa1, j != 0 ? 1u : 0u);
+            issue_mmas<kTileN>(tmem, d, sfb, sfa, j != 0 ? 1u : 0u);
           else
-            issue_mmas<128>(tmem, d1, sfb1, sfa1, j != 0 ? 1u : 0u);
-          commit_at(done1);
-          if (n == 2) {
-            if (half < 0)
-              issue_mmas<kTileN>(tmem, d2, sfb2, sfa2, 1u);
-            else
-              issue_mmas<128>(tmem, d2, sfb2, sfa2, 1u);
-            commit_at(done2);
-          }
-          if (j + n == len) commit_at(full_acc_at);
+            issue_mmas<128>(tmem, d, sfb, sfa, j != 0 ? 1u : 0u);
+          commit_at(empty_at + 8 * st);
+          if (j + 1 == len) commit_at(full_acc_at);
         };
-        if (j == 0) {
+        if (j == 0) {   // the first scales while the accumulator is read out
           if (elect_one()) copies();
           __syncwarp();
           mbar_wait(acc_empty, (seg & 1) ^ 1, abort);
@@ -883,12 +864,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
           mmas();
         }
         __syncwarp();
-        if (resident) have |= (n == 2 ? 3u : 1u) << k;
-        j += n;
-        k += n;
-        st += n;
-        if (st >= C::kStages) {
-          st -= C::kStages;
+        if (resident) have |= 1u << k;
+        if (++st == C::kStages) {
+          st = 0;
           phase ^= 1;
         }
       }
