@@ -833,6 +833,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
         sslot = 0;
         sphase ^= 1;
       }
+      // Whole tiles whose activations' scales are all there, or all to be copied, go
+      // without a test between the instructions of a k-step (8192 tokens' first
+      // product 238 -> 230 us); halves and mixed ones with.
+      const uint32_t all = resident ? ((1u << len) - 1u) << k : 0u;
+      const int form = half >= 0 ? 0 : resident && (have & all) == all ? 1 : (have & all) == 0 ? 2 : 0;
       for (int j = 0; j < len; ++j, ++k) {
         if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(full_at + 8 * st, phase))) {
           mbar_wait(&full[st], phase, abort);
@@ -848,6 +853,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
             issue_mmas<kTileN>(tmem, d, sfb, sfa, j != 0 ? 1u : 0u);
           else
             issue_mmas<128>(tmem, d, sfb, sfa, j != 0 ? 1u : 0u);
+        };
+        auto commits = [&]() {
           commit_at(empty_at + 8 * st);
           if (j + 1 == len) commit_at(full_acc_at);
         };
@@ -858,18 +865,34 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
           abort = __any_sync(0xFFFFFFFFu, abort);
           if (abort) break;
           tc_fence_after();
-          if (elect_one()) mmas();
+          if (elect_one()) {
+            mmas();
+            commits();
+          }
+        } else if (form == 1) {
+          if (elect_one()) {
+            copy_scales(d, sfb, sfa, false, false);
+            issue_mmas<kTileN>(tmem, d, sfb, sfa, 1u);
+            commits();
+          }
+        } else if (form == 2) {
+          if (elect_one()) {
+            copy_scales(d, sfb, sfa, true, false);
+            issue_mmas<kTileN>(tmem, d, sfb, sfa, 1u);
+            commits();
+          }
         } else if (elect_one()) {
           copies();
           mmas();
+          commits();
         }
         __syncwarp();
-        if (resident) have |= 1u << k;
         if (++st == C::kStages) {
           st = 0;
           phase ^= 1;
         }
       }
+      have |= all;
       if (abort) break;
     }
     __syncwarp();
