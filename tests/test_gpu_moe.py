@@ -60,6 +60,19 @@ def test_route(capi, score, T, E, k, groups, keep, top, bias, bf16, renorm):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(96, 8), (96, 12), (72, 8), (160, 8), (160, 4), (192, 8), (192, 12), (384, 8),
+                                      (384, 4), (300, 3), (384, 1), (160, 1)])
+@pytest.mark.parametrize("bias,bf16,top", [(False, True, 1), (False, False, 1), (True, True, 2), (False, True, 2)])
+def test_route_groups_that_are_whole_lanes_or_not(capi, score, E, groups, bias, bf16, top):
+    x = logits_of(60, E, E + groups, bf16)
+    x[40:] = torch.round(x[40:])                     # ties of experts and of groups
+    x[:, 5::7] = -float("inf")
+    b = torch.randn(E, generator=torch.Generator().manual_seed(E)) * 0.1 if bias else None
+    keep = max(1, groups // 3)
+    check_route(capi, x, b, min(8, E // groups * keep), score, n_group=groups, topk_group=keep, group_top=top)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("bias", [False, True])
 def test_route_ties_go_to_the_lower_index(capi, score, bias):
     x = torch.zeros(40, 64)
