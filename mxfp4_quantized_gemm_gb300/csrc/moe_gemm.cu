@@ -11,19 +11,19 @@
 //           the second product.
 //
 // Few tokens: the weights of the experts they reach are nearly all the bytes
-// and HBM is the bound (64 x 8 of 128 experts, a network of 5120 x 1024: 152 us,
+// and HBM is the bound (64 x 8 of 128 experts, a network of 5120 x 1024: 151 us,
 // 0.87 of the measured rate over the whole call).  Many: the tensor pipe's four
-// MMAs and scale copies per 256-wide k-step, 790 cycles alone, 835 here (8192 x 8
-// of 64, gated: 252 us); the rows of the same call are bound by HBM's writes (671
-// MB in 188 us; nothing but writes goes at 3.85 TB/s).
+// MMAs and scale copies per 256-wide k-step, 381 ns alone, 393 here (8192 x 8 of
+// 64, gated: 228 us); the rows of the same call are bound by HBM's writes (671 MB
+// in 185 us; nothing but writes goes at 3.85 TB/s).
 // One kernel serves both, one CTA per SM: the ring, the
 // tile (128 activation rows x 256 weight rows) and the roles are those of
 // gemm.cu, and only the live rows of a row tile are loaded and stored.
 //
 // The number of tiles is known on the device only, so every CTA derives its
 // share from the plan (struct Walk): whole rounds of units of a few tiles of
-// one row tile, then what is left cut evenly along (tile, k-step) over all
-// CTAs.  A cut tile's parts go to memory in fp32; the CTA whose part arrives
+// one row tile, then single tiles, and what is left whole, in halves or cut
+// along (tile, k-step).  A cut tile's parts go to memory in fp32; the CTA whose part arrives
 // last (a counter per tile) adds them in CTA order, so the sum does not
 // depend on who is last, and no CTA ever waits for another.
 #include <cuda_bf16.h>
@@ -111,7 +111,8 @@ static_assert(sizeof(Segment) == 32, "two 16-byte words");
 // A CTA's share of the tiles, segment by segment.
 //  1. whole rounds of units: `unit` neighbouring tiles of one row tile, whose
 //     activations (and their scales in TMEM) serve them all (8192 x 8 of 64:
-//     units of four were 690 us, of eight 694, of one or two slower still);
+//     products 229 + 185 us by four, 229 + 188 by two, 231 + 193 by one, 231 + 189
+//     by eight);
 //  2. whole rounds of single tiles;
 //  3. the fewer than G tiles left: each on a CTA of its own, or as halves on
 //     two, or cut evenly along (tile, k-step) over all CTAs together with one
@@ -631,9 +632,9 @@ __device__ __forceinline__ void finish_cut(const MoeArgs& g, const Walk& walk, c
 // The scale copies and MMAs of a k-step, from the stage's descriptors.  What the
 // issuing warp does between them holds the tensor pipe up, so the stage's two
 // descriptors are formed once and the others are sums with constants: no
-// address in shared memory carries into the fields above it (8192 tokens' first
-// product 252 us; 278 with every descriptor formed from its address and the
-// barriers' addresses with them).
+// address in shared memory carries into the fields above it.  (8192 tokens' first
+// product: 278 us with every descriptor and barrier address formed on its own and
+// two k-steps' scales copied together against it, 236 so, a k-step at a time.)
 struct StageDescs {
   uint32_t tile, scales;   // low words at the stage's start; the high words are constants
   __device__ __forceinline__ explicit StageDescs(uint32_t stage)
@@ -835,7 +836,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
       }
       // Whole tiles whose activations' scales are all there, or all to be copied, go
       // without a test between the instructions of a k-step (8192 tokens' first
-      // product 238 -> 230 us); halves and mixed ones with.
+      // product 239 -> 228 us); halves and mixed ones with.
       const uint32_t all = resident ? ((1u << len) - 1u) << k : 0u;
       const int form = half >= 0 ? 0 : resident && (have & all) == all ? 1 : (have & all) == 0 ? 2 : 0;
       for (int j = 0; j < len; ++j, ++k) {
