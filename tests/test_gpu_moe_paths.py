@@ -67,6 +67,26 @@ def test_many_pairs_and_ids_that_are_not_aligned(capi):
     check_close(host_bits(a).reshape(T, k, N)[rows], acc, mag, n_acc(K), what="30000 x 5", K=K)
 
 
+@pytest.mark.parametrize("N", [1, 2, 3, 7, 31, 63, 127, 129, 191, 255, 257, 385, 1001])
+def test_rows_of_odd_widths(capi, N):
+    # rows that start at odd columns and end inside a word, many and few of them
+    check_rows(capi, 140, 1, 1, N, 192, np.zeros((140, 1), dtype=np.int32), np.arange(0, 140, 3), seed=N)
+    check_rows(capi, 60, 2, 3, N, 64, routing(60, 3, 2, N, 0.1)[0], np.arange(60), seed=N, bias=False)
+
+
+def test_rows_of_odd_widths_and_strides(capi):
+    # what lies between and behind the rows stays
+    w = Experts(capi, 2, 301, 256, 3, True)
+    x, ids = dev_bf16(synth.activations(150, 256, 3)), dev_i32(routing(150, 2, 1, 3)[0])
+    want = run_linear(capi, x, ids, w)
+    for ldo, at in ((301, 1), (302, 0), (303, 5), (304, 0), (305, 8), (320, 3)):
+        room = torch.full((150 * ldo + 16,), 7.0, dtype=BF, device="cuda")
+        run_linear(capi, x, ids, w, out=room[at:at + 150 * ldo].view(150, ldo))
+        got = room[at:at + 150 * ldo].view(150, ldo)
+        assert torch.equal(got[:, :301], want) and (got[:, 301:] == 7).all()
+        assert (room[:at] == 7).all() and (room[at + 150 * ldo:] == 7).all()
+
+
 @pytest.mark.parametrize("T", [3, 40, 200])
 def test_cut_tiles(capi, T):
     # one or two tiles of 56 k-steps: cut for several blocks
