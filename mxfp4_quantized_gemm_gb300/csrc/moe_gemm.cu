@@ -821,7 +821,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     uint32_t have = 0;
     int st = 0;
     uint32_t phase = 0;
-    for (int seg = 0; next_segment(); ++seg) {
+    for (int seg = 0; __all_sync(0xFFFFFFFFu, next_segment()); ++seg) {   // (a wait may end for one lane alone)
       const int len = s.len, half = s.half;
       int k = s.k0;
       if (s.rt != cur_rt) {
@@ -952,7 +952,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     walk.init(g, __ldcg(g.hdr));
     int pair_rt = -1, pair_of_row = -1;           // the row tile whose pairs this lane has: of row rl, or of row lane
     bool pair_few = false;                        // where the tile has few rows
-    for (int seg = 0; next_segment(); ++seg) {
+    for (int seg = 0; __all_sync(0xFFFFFFFFu, next_segment()); ++seg) {
       const int rows = s.info >> 16, expert = s.info & 0xFFFF;
       const bool whole = s.len == g.KT, few = whole && rows <= kFewRows;
       const int first_c8 = s.half > 0 ? 16 : 0;
@@ -975,7 +975,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
         sslot = 0;
         sphase ^= 1;
       }
-      const bool ok = mbar_wait(acc_full, seg & 1, abort);
+      mbar_wait(acc_full, seg & 1, abort);
+      const bool ok = !__any_sync(0xFFFFFFFFu, abort);
       tc_fence_after();
       uint32_t r[128];
       if (q * 32 < rows) {
