@@ -329,12 +329,13 @@ __global__ void __launch_bounds__(256, 4) moe_few_kernel(const __grid_constant__
   for (int t = t0; t < a.T; t += a.R) {
     if (t != t0) v = load_unit(a, t, kt, lane);
     // lane j: the row of pair j of the token, after the pairs before it of its
-    // expert.  `share` lanes count for each pair, every one a part of the ids.
+    // expert.  `share` lanes count for each pair, every one a part of the ids
+    // (none past the token's pairs: they would read on behind the last id).
     const int p0 = t * a.k;
     const int e = lane < a.k ? ids[p0 + lane] : -1;
     const bool on = static_cast<uint32_t>(e) < static_cast<uint32_t>(f.E);
     const int share = 32 / slots, pair = lane / share;
-    const int other = __shfl_sync(0xFFFFFFFFu, e, pair), before = p0 + pair;
+    const int other = __shfl_sync(0xFFFFFFFFu, e, pair), before = pair < a.k ? p0 + pair : 0;
     int n_before = 0;
     for (int c = 4 * (lane % share); c < before; c += 4 * share) {
       const int4 w = *reinterpret_cast<const int4*>(ids + c);

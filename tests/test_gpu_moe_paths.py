@@ -44,6 +44,13 @@ def test_pairs_around_the_one_kernel_plan(capi, T, k):
     check_rows(capi, T, k, 12, 96, 160, ids, np.arange(T), seed=T)
 
 
+@pytest.mark.parametrize("T,k", [(51, 5), (28, 9), (23, 11), (15, 17), (14, 18), (13, 19), (12, 21), (11, 23)])
+def test_few_pairs_whose_slots_fill_no_power_of_two(capi, T, k):
+    # the lanes that count past a token's last slot reach behind the last id here
+    ids = routing(T, 24, k, T, 0.1)[0]
+    check_rows(capi, T, k, 24, 40, 64, ids, np.arange(T), seed=k)
+
+
 def test_most_experts_and_slots(capi):
     ids = routing(40, 1024, 32, 1)[0]
     check_rows(capi, 40, 32, 1024, 40, 64, ids, np.arange(40), bias=False)
