@@ -269,8 +269,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-__device__ __forceinline__ void epi_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
 // Place of the part of cut tile `left` that CTA c leaves (each CTA's range cuts
 // at most two tiles).
 __device__ __forceinline__ int part_slot(const Walk& w, int KT, int left, int c) {
@@ -689,7 +687,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
   uint64_t* acc_empty = acc_full + 1;
   uint64_t* seg_full = acc_empty + 1;
   uint64_t* seg_empty = seg_full + kSegs;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_empty + kSegs);
+  uint64_t* epi_bar = seg_empty + kSegs;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
   volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint8_t* staging = smem + C::kRing + 512;
   uint8_t* segs = staging + 8 * kStageWarp;
@@ -704,6 +703,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, kEpiThreads / 32);
+    mbar_init(epi_bar, kEpiThreads / 32);
     for (int q = 0; q < kSegs; ++q) {
       mbar_init(&seg_full[q], 1);
       mbar_init(&seg_empty[q], kSegReaders);
@@ -821,6 +821,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     uint32_t have = 0;
     int st = 0;
     uint32_t phase = 0;
+    bool issued = false;
     for (int seg = 0; __all_sync(0xFFFFFFFFu, next_segment()); ++seg) {   // (a wait may end for one lane alone)
       const int len = s.len, half = s.half;
       int k = s.k0;
@@ -888,6 +889,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
           commits();
         }
         __syncwarp();
+        issued = true;
         if (++st == C::kStages) {
           st = 0;
           phase ^= 1;
@@ -897,6 +899,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
       if (abort) break;
     }
     __syncwarp();
+    if (abort && issued) {   // the MMAs in flight end before TMEM is given back
+      bool late = false;
+      const int last = st == 0 ? C::kStages - 1 : st - 1;
+      mbar_wait(&empty[last], st == 0 ? phase ^ 1 : phase, late);
+    }
    } else {
     // ---- warp 3: the segments of this CTA, ahead of the other roles.  The plan
     // is complete when this kernel starts (the kernel before it lets it start
@@ -947,6 +954,16 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     uint8_t* stage = staging + (warp - kFirstEpiWarp) * kStageWarp;
     const int ew = warp - kFirstEpiWarp;
     bool staged = false;                          // a warp's staging area may still be read by its warp
+    // Barrier of the epilogue warps.  A warp whose wait runs out goes no further
+    // through the segments, so the others' wait for it has a limit too (a hardware
+    // barrier's has none).
+    uint32_t epi_phase = 0;
+    auto epi_barrier = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(epi_bar);
+      mbar_wait(epi_bar, epi_phase, abort);
+      epi_phase ^= 1;
+    };
     // how the cut tiles are dealt out, for their sums
     Walk walk;
     walk.init(g, __ldcg(g.hdr));

@@ -76,6 +76,20 @@ def test_activations():
     assert abs(moe_ref.act("gelu", np.array([1.0]), np.array([1.0]))[0] - phi) < 1e-3
 
 
+def test_roles_of_the_products_wait_with_a_limit():
+    # a warp that gives up a wait leaves its role, and no hardware barrier ends
+    # without it: inside the roles there are bounded waits only
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "mxfp4_quantized_gemm_gb300", "csrc", "moe_gemm.cu")) as f:
+        source = re.sub(r"//[^\n]*", "", f.read())
+    start = source.index("if (warp < kFirstEpiWarp)")
+    roles = source[start:source.index("tmem_dealloc", start)]
+    assert not re.search(r"\bbar(rier)?\.(cta\.)?(sync|red)", source)
+    assert roles.count("__syncthreads") == 1           # behind all of them
+
+
 # --------------------------------------------------------------- refusals
 A = 1 << 20   # an aligned address that no refused call reads
 ROUTE = dict(logits=A, dtype=0, ld=64, bias=A, T=4, E=64, top_k=8, score=1, n_group=8, topk_group=4, group_top=2,
