@@ -303,15 +303,13 @@ __device__ __forceinline__ bool decide_in(const RouteArgs& a, int t, int lane, i
       if (g >= a.groups || !((kept >> g) & 1u)) key[j] = none;
     }
   }
-  // k rounds of the maximum over the warp and the lowest lane that has it, and
-  // one more to see how near the first one left out is
+  // k rounds of the maximum over the warp and the lowest lane that has it
   idx = -1;
   xsel = 0.f;
   ssel = 0.f;
-  uint64_t mine = none, after = none;              // lane r: the key of choice r; every lane: of the one left out
-  int iafter = -1;
+  uint64_t mine = none;                            // lane r: the key of choice r
 #pragma unroll 1
-  for (int r = 0; r <= a.k; ++r) {
+  for (int r = 0; r < a.k; ++r) {
     uint64_t best = key[0];
     int at = 0;
     float bs = rounded(s[0]);
@@ -327,11 +325,6 @@ __device__ __forceinline__ bool decide_in(const RouteArgs& a, int t, int lane, i
     const int who = __ffs(__ballot_sync(kAll, best == top)) - 1;
     const int i = __shfl_sync(kAll, lane * V + at, who);
     const float sv = __shfl_sync(kAll, bs, who);
-    if (r == a.k) {
-      after = top;
-      iafter = i;
-      break;
-    }
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if (lane == who && j == at) key[j] = none;
@@ -343,18 +336,25 @@ __device__ __forceinline__ bool decide_in(const RouteArgs& a, int t, int lane, i
   }
   if (idx >= 0) xsel = logit_at(a, t, idx);
   if (biased) {
-    uint64_t key2 = __shfl_down_sync(kAll, mine, 1);
-    int i2 = __shfl_down_sync(kAll, idx, 1);
-    if (lane == a.k - 1) {
-      key2 = after;
-      i2 = iafter;
-    }
-    if (lane < a.k && idx >= 0 && i2 >= 0) {
+    // neighbours among the chosen; the last of them against all that are left out
+    // (the highest of these may be equal to it, with the same inputs, and hide
+    // others that are near)
+    const float bsel = idx >= 0 ? __ldg(a.bias + idx) : 0.f;
+    const uint64_t key2 = __shfl_down_sync(kAll, mine, 1), last = __shfl_sync(kAll, mine, a.k - 1);
+    const float x2 = __shfl_down_sync(kAll, xsel, 1), b2 = __shfl_down_sync(kAll, bsel, 1);
+    const float xlast = __shfl_sync(kAll, xsel, a.k - 1), blast = __shfl_sync(kAll, bsel, a.k - 1);
+    auto close = [&](uint64_t k1, uint64_t k2) {
       F v1, v2;
-      from_key(mine, v1);
-      from_key(key2, v2);
-      const bool same = xsel == logit_at(a, t, i2) && __ldg(a.bias + idx) == __ldg(a.bias + i2);
-      near = near || (open(v1, v2, error) && !same);
+      from_key(k1, v1);
+      from_key(k2, v2);
+      return open(v1, v2, error);
+    };
+    if (lane < a.k - 1 && key2 != none) near = near || (close(mine, key2) && !(xsel == x2 && bsel == b2));
+    if (last != none) {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (key[j] != none && close(last, key[j]))
+          near = near || !(xlast == x[j] && blast == __ldg(a.bias + lane * V + j));
     }
   }
   return __any_sync(kAll, near);
@@ -601,19 +601,40 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&
     i2 = iafter;
     if (i2 >= 0) x2 = logit_at(a, t, i2);
   }
-  bool close = false;
+  bool close = false, alike = false;               // alike: near, but of the same inputs
   auto tolerance = [&](float c) { return kDropped * fabsf(c) + 0x1p-21f * unit; };
   if (lane < a.k && idx >= 0 && i2 >= 0) {
     if (biased) {
       const float c1 = from_key(mine), c2 = from_key(key2);
       const bool same = xsel == x2 && __ldg(a.bias + idx) == __ldg(a.bias + i2);
-      close = c1 - c2 <= tolerance(c1) + tolerance(c2) && !same;
+      close = c1 - c2 <= tolerance(c1) + tolerance(c2);
+      alike = close && same;
     } else {
-      close = mine == key2 && xsel != x2;
+      close = mine == key2;
+      alike = close && xsel == x2;
+    }
+    close = close && !alike;
+  }
+  near = near || __any_sync(kAll, close);
+  // Where the first one left out has the inputs of the last choice, one that is
+  // near may stand behind it: all that are left are looked at.  (Keys of 16-bit
+  // logits are exact.)
+  if (!near && !(a.bf16 && !biased) && __shfl_sync(kAll, alike, a.k - 1)) {
+    const uint32_t klast = __shfl_sync(kAll, mine, a.k - 1);
+    const float xlast = __shfl_sync(kAll, xsel, a.k - 1), c1 = from_key(klast);
+    const float blast = biased ? __ldg(a.bias + __shfl_sync(kAll, idx, a.k - 1)) : 0.f;
+#pragma unroll 1
+    for (int left = V; left > 0 && key[0] != 0; --left) {
+      const uint32_t k2 = key[0] & ~kPlace;
+      const int i = lane * V + static_cast<int>(kPlace - (key[0] & kPlace));
+      const float c2 = from_key(k2);
+      if (biased ? c1 - c2 <= tolerance(c1) + tolerance(c2) : k2 == klast)
+        near = near || logit_at(a, t, i) != xlast || (biased && __ldg(a.bias + i) != blast);
+#pragma unroll
+      for (int j = 0; j + 1 < V; ++j) key[j] = key[j + 1];
+      key[V - 1] = 0;
     }
   }
-  close = __any_sync(kAll, close);
-  near = near || close;
   ssel = idx >= 0 && !a.renorm ? score_of(sigmoid, xsel, m, sum) : 0.f;
   return __any_sync(kAll, near);
 }

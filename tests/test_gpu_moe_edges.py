@@ -1,0 +1,65 @@
+"""Mixture of experts on the GPU at inputs that lie on a border: experts that
+fp32 cannot tell apart beside equal ones."""
+
+import numpy as np
+import pytest
+import torch
+
+from moe_helpers import run_route
+from oracle import moe_ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def capi():
+    from mxfp4_quantized_gemm_gb300 import capi as c
+    return c
+
+
+def check_choice(capi, logits, bias, top_k, score, **kw):
+    """The kernel's ids are those of the 64-bit oracle."""
+    _, ids = run_route(capi, logits.cuda(), None if bias is None else bias.cuda(), top_k, score, **kw)
+    torch.cuda.synchronize()
+    assert capi.mxfp4_get_device_error() == capi.OK
+    _, want = moe_ref.route(logits.double().numpy(), None if bias is None else bias.double().numpy(), top_k,
+                            score == "softmax", **kw)
+    got = ids.cpu().numpy()
+    rows = np.unique(np.nonzero(got != want)[0])
+    assert not len(rows), f"{len(rows)} rows, first {rows[0]}: {got[rows[0]]} for {want[rows[0]]}"
+
+
+# numbers of experts for each number of logits a lane
+SIZES = [33, 64, 96, 128, 160, 192, 256, 384, 512, 1024]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", SIZES)
+@pytest.mark.parametrize("bias", [None, 0.0, 0.25])
+@pytest.mark.parametrize("base,ulps", [(1.0, 1), (2.0 ** -20, 1), (-3.0, 2)])
+def test_route_finds_a_higher_expert_behind_equal_ones(capi, score, E, bias, base, ulps):
+    # all logits equal but for 0 to 12 that are a step of fp32 higher or two (the
+    # scores of 2^-20 and its neighbour differ by 2^-45: more than pairs of fp32 tell)
+    g = np.random.default_rng(E)
+    x = np.full((40, E), base, dtype=np.float32)
+    up = np.float32(base)
+    for _ in range(ulps):
+        up = np.nextafter(up, np.float32(100.0))
+    higher = np.nextafter(up, np.float32(100.0))
+    for t in range(1, 40):
+        at = g.permutation(E)[:t % 13]
+        x[t, at] = np.where(g.random(len(at)) < 0.3, higher, up)
+    x[1, :], x[1, E - 1] = base, up                    # the last expert alone
+    b = None if bias is None else torch.full((E,), bias)
+    for k in (1, 8):
+        check_choice(capi, torch.from_numpy(x), b, k, score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", SIZES)
+def test_route_finds_a_higher_bias_behind_equal_ones(capi, score, E):
+    x, b = torch.ones(8, E), torch.zeros(E)
+    b[E - 2] = 1e-7 if score == "sigmoid" else 1e-9
+    x[4:, ::3] = -2.0
+    for k in (1, 5):
+        check_choice(capi, x, b, k, score)
