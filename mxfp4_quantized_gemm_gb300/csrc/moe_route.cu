@@ -192,6 +192,41 @@ __device__ __forceinline__ float logit_at(const RouteArgs& a, int t, int i) {
   return a.bf16 ? bf16_bits_to_float(static_cast<const uint16_t*>(a.x)[at]) : static_cast<const float*>(a.x)[at];
 }
 
+// Whether the groups of the mask have the same best logits (a.top of them),
+// where these alone decide (one bias for all their experts, or none): then they
+// are equal in any arithmetic, and their order is by the index.
+__device__ __noinline__ bool equal_groups(const RouteArgs& a, int t, int lane, uint32_t groups) {
+  const int size = a.E / a.groups;
+  uint32_t best0 = 0, next0 = 0, high = 0, low = 0;   // of the first group; of all biases and of their inverted keys
+  bool same = true;
+#pragma unroll 1
+  for (uint32_t m = groups; m != 0; m &= m - 1) {
+    const int g = __ffs(m) - 1;
+    uint32_t best = 0, next = 0;
+    auto meet = [&](uint32_t b, uint32_t n) {
+      next = max(max(next, n), min(best, b));
+      best = max(best, b);
+    };
+#pragma unroll 1
+    for (int i = g * size + lane; i < (g + 1) * size; i += 32) {
+      const float x = logit_at(a, t, i), b = a.bias != nullptr ? __ldg(a.bias + i) : 0.f;
+      if (!(x > -INFINITY && b > -INFINITY)) continue;
+      meet(key_of(x), 0u);
+      high = max(high, key_of(b));
+      low = max(low, ~key_of(b));
+    }
+    __syncwarp();
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) meet(__shfl_xor_sync(kAll, best, o), __shfl_xor_sync(kAll, next, o));
+    if (m == groups) {
+      best0 = best;
+      next0 = next;
+    }
+    same = same && best == best0 && (a.top == 1 || next == next0);
+  }
+  return same && warp_max(high) == ~warp_max(low);
+}
+
 // Decides row t in numbers F (Pair or double).  Lane l holds elements l * V ..
 // l * V + V - 1 of the row, so the lowest lane and place of equal values is the
 // lowest index.  At the end lane r < k holds the r-th choice: its index (-1:
@@ -279,23 +314,33 @@ __device__ __forceinline__ bool decide_in(const RouteArgs& a, int t, int lane, i
       }
     }
     if (group >= a.groups) gkey = none;            // (lanes past the last group)
+    const uint64_t mine = gkey;
     uint32_t kept = 0;
-    uint64_t last = none;
+    uint64_t last = none, out = none;              // the last group taken, the first left out
 #pragma unroll 1
     for (int r = 0; r <= a.keep; ++r) {
       const uint64_t top = warp_max(gkey);
       if (top == none) break;
       if (r == a.keep) {
-        F v1, v2;
-        from_key(last, v1);
-        from_key(top, v2);
-        near = (biased || by_score) && last != top && open(v1, v2, 2.f * error);
+        out = top;
         break;
       }
       const int g = __shfl_sync(kAll, group, __ffs(__ballot_sync(kAll, gkey == top)) - 1);
       last = top;
       kept |= 1u << g;
       if (group == g) gkey = none;
+    }
+    if (out != none && (biased || by_score)) {
+      auto close = [&](uint64_t k1, uint64_t k2) {
+        F v1, v2;
+        from_key(k1, v1);
+        from_key(k2, v2);
+        return open(v1, v2, 2.f * error);
+      };
+      if (close(last, out)) {
+        const bool in = mine != none && (((kept >> (group & 31)) & 1u) ? close(mine, out) : close(last, mine));
+        near = !equal_groups(a, t, lane, __reduce_or_sync(kAll, in ? 1u << (group & 31) : 0u));
+      }
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {

@@ -1,5 +1,5 @@
 """Mixture of experts on the GPU at inputs that lie on a border: experts that
-fp32 cannot tell apart beside equal ones."""
+fp32 cannot tell apart beside equal ones, scores that vanish."""
 
 import numpy as np
 import pytest
@@ -63,3 +63,23 @@ def test_route_finds_a_higher_bias_behind_equal_ones(capi, score, E):
     x[4:, ::3] = -2.0
     for k in (1, 5):
         check_choice(capi, x, b, k, score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(16, 4), (40, 4), (64, 8), (96, 32), (160, 8), (256, 8), (300, 3), (1024, 8)])
+@pytest.mark.parametrize("bias", [None, 0.0])
+def test_route_groups_whose_scores_vanish(capi, score, E, groups, bias):
+    # scores down to 1e-200: nothing in fp32, and still in order
+    gen = torch.Generator().manual_seed(E)
+    x = 60.0 * torch.randn(60, E, generator=gen)
+    if score == "sigmoid":
+        x = -90.0 - x.abs()
+    x[0] = -(400.0 / E) * torch.arange(E - 1, -1, -1.0)    # rising, the last group highest
+    x[1] = -(400.0 / E) * torch.randperm(E, generator=gen)
+    x[2] = -100.0                                       # all alike
+    x[3] = torch.round(x[3] / 40) * 40                  # few values
+    b = None if bias is None else torch.full((E,), bias)
+    for keep in (2, groups - 1):
+        k = min(32, E // groups * keep)
+        check_choice(capi, x, b, k, score, n_group=groups, topk_group=keep, group_top=2)
+        check_choice(capi, x, b, k, score, n_group=groups, topk_group=keep, group_top=1)
