@@ -25,6 +25,7 @@
 
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
 #include "gemm_common.cuh"
 #include "internal.h"
@@ -186,6 +187,12 @@ __device__ __forceinline__ bool open(Pair a, Pair b, float error) {
   return (a.h - b.h) + (a.l - b.l) <= error + 0x1p-44f * (fabsf(a.h) + fabsf(b.h));
 }
 __device__ __forceinline__ bool open(double, double, float) { return false; }
+// The key of a value that is `by` more than key k's (an infinite one stays).
+__device__ __forceinline__ uint64_t moved(uint64_t k, float by) {
+  Pair v;
+  from_key(k, v);
+  return key_of(isfinite(v.h) ? add(v, Pair{by, 0.f}) : Pair{v.h, 0.f});
+}
 
 __device__ __forceinline__ float logit_at(const RouteArgs& a, int t, int i) {
   const int64_t at = static_cast<int64_t>(t) * a.ld + i;
@@ -286,11 +293,15 @@ __device__ __forceinline__ bool decide_in(const RouteArgs& a, int t, int lane, i
       best = max(best, b);
     };
     auto compared = [&](int j) { return by_score && key[j] != none ? key_of(s[j]) : key[j]; };
+    float slack = 0.f;                             // how far the group's value can be off
     auto value = [&]() {                           // the key of the group's value
-      if (best == none || a.top == 1 || next == none) return best;
+      if (best == none) return best;
       F v1, v2;
       from_key(best, v1);
+      slack = error + 0x1p-44f * fabsf(rounded(v1));
+      if (a.top == 1 || next == none) return best;
       from_key(next, v2);
+      slack += error + 0x1p-44f * fabsf(rounded(v2));   // (the sum may be far smaller than either)
       return key_of(isinf(rounded(v1)) || isinf(rounded(v2)) ? v1 : add(v1, v2));
     };
     uint64_t gkey = none;
@@ -316,29 +327,21 @@ __device__ __forceinline__ bool decide_in(const RouteArgs& a, int t, int lane, i
     if (group >= a.groups) gkey = none;            // (lanes past the last group)
     const uint64_t mine = gkey;
     uint32_t kept = 0;
-    uint64_t last = none, out = none;              // the last group taken, the first left out
 #pragma unroll 1
-    for (int r = 0; r <= a.keep; ++r) {
+    for (int r = 0; r < a.keep; ++r) {
       const uint64_t top = warp_max(gkey);
       if (top == none) break;
-      if (r == a.keep) {
-        out = top;
-        break;
-      }
       const int g = __shfl_sync(kAll, group, __ffs(__ballot_sync(kAll, gkey == top)) - 1);
-      last = top;
       kept |= 1u << g;
       if (group == g) gkey = none;
     }
-    if (out != none && (biased || by_score)) {
-      auto close = [&](uint64_t k1, uint64_t k2) {
-        F v1, v2;
-        from_key(k1, v1);
-        from_key(k2, v2);
-        return open(v1, v2, 2.f * error);
-      };
-      if (close(last, out)) {
-        const bool in = mine != none && (((kept >> (group & 31)) & 1u) ? close(mine, out) : close(last, mine));
+    if (std::is_same_v<F, Pair> && (biased || by_score)) {
+      // the lowest that a group taken can be, the highest that one left out can be
+      const bool taken = mine != none && ((kept >> (group & 31)) & 1u), left = mine != none && !taken;
+      const uint64_t low = taken ? moved(mine, -slack) : ~0ull, high = left ? moved(mine, slack) : 0ull;
+      const uint64_t lowest = ~warp_max(~low), highest = warp_max(high);
+      if (highest >= lowest) {
+        const bool in = (taken && low <= highest) || (left && high >= lowest);
         near = !equal_groups(a, t, lane, __reduce_or_sync(kAll, in ? 1u << (group & 31) : 0u));
       }
     }
@@ -538,9 +541,14 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&
     auto value_of = [&](uint32_t k, float& err) {
       if (k == 0) return -INFINITY;
       const float c = from_key(k & ~kPlace);
-      const float v = by_score ? fast_score(c) : c;
-      err += biased ? kDropped * fabsf(c) + 0x1p-21f * unit
-                    : by_score ? 0x1p-21f * unit + 2.f * kDropped * fabsf(c) * v : kDropped * fabsf(c);
+      const float dropped = kDropped * fabsf(c);
+      if (!by_score) {
+        err += biased ? dropped + 0x1p-21f * unit : dropped;
+        return c;
+      }
+      // (of large logits the dropped bits are not small beside 1)
+      const float v = fast_score(c);
+      err += 0x1p-21f * unit + (dropped < 0.5f ? 2.f * dropped * v : fast_score(c + dropped) - v);
       return v;
     };
     auto set_group = [&](uint32_t best, uint32_t next) {
@@ -578,23 +586,24 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&
       }
     }
     if (group >= a.groups) gkey = 0;               // (lanes past the last group)
+    const uint32_t mine = gkey;
     uint32_t kept = 0;
-    float last = -INFINITY, last_err = 0.f;
-    for (int r = 0; r <= a.keep; ++r) {
+    for (int r = 0; r < a.keep; ++r) {
       const uint32_t top = warp_max(gkey);
       if (top == 0) break;
-      const int who = __ffs(__ballot_sync(kAll, gkey == top)) - 1;
-      const int g = __shfl_sync(kAll, group, who);
-      const float v = from_key(top), err = __shfl_sync(kAll, gerr, who);
-      if (r < a.keep) {
-        kept |= 1u << g;
-        last = v;
-        last_err = err;
-        if (group == g) gkey = 0;
-      } else if (last - v < last_err + err || (last == v && !exact)) {
-        near = true;
-      }
+      const int g = __shfl_sync(kAll, group, __ffs(__ballot_sync(kAll, gkey == top)) - 1);
+      kept |= 1u << g;
+      if (group == g) gkey = 0;
     }
+    // the lowest that a group taken can be, the highest that one left out can be:
+    // errors differ, and the sum of the best two may be far smaller than they
+    const bool taken = (kept >> (group & 31)) & 1u;
+    const float v = from_key(mine);
+    const bool finite = fabsf(v) < INFINITY;
+    const uint32_t low = mine != 0 && taken ? key_of(finite ? v - gerr : v) : kAll;
+    const uint32_t high = mine != 0 && !taken ? key_of(finite ? v + gerr : v) : 0u;
+    const uint32_t lowest = __reduce_min_sync(kAll, low), highest = warp_max(high);
+    near = highest > lowest || (highest == lowest && !exact);
     if (whole) {
       if (!((kept >> (group & 31)) & 1u) || group >= a.groups) key[0] = 0;   // what follows a first key of 0 is not met
     } else {

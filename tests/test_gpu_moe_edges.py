@@ -1,5 +1,6 @@
 """Mixture of experts on the GPU at inputs that lie on a border: experts that
-fp32 cannot tell apart beside equal ones, scores that vanish."""
+fp32 cannot tell apart beside equal ones, scores that vanish, groups whose
+values cancel."""
 
 import numpy as np
 import pytest
@@ -83,3 +84,31 @@ def test_route_groups_whose_scores_vanish(capi, score, E, groups, bias):
         k = min(32, E // groups * keep)
         check_choice(capi, x, b, k, score, n_group=groups, topk_group=keep, group_top=2)
         check_choice(capi, x, b, k, score, n_group=groups, topk_group=keep, group_top=1)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(64, 32), (96, 32), (128, 32), (320, 32), (512, 32), (1024, 32)])
+@pytest.mark.parametrize("large", [2.0 ** 14, 2.0 ** 18, 2.0 ** 40])
+def test_route_groups_whose_best_two_cancel(capi, score, E, groups, large):
+    # half of the groups: a bias of +large and one of -large, so that the sum is that of
+    # two scores with an error that the other groups' sums do not have
+    size = E // groups
+    g = np.random.default_rng(E)
+    x = torch.from_numpy(g.standard_normal((300, E)).astype(np.float32) * 3)
+    b = np.full(E, -np.inf, dtype=np.float32)
+    for n in range(groups):
+        b[n * size:n * size + 2] = (large, -large) if n % 2 else (0.0, 0.0)
+    if score == "softmax":
+        b[~np.isfinite(b)] = -4 * large                  # these count for the sum, no further
+    for keep in (1, 7, 16, 31):
+        check_choice(capi, x, torch.from_numpy(b), min(32, 2 * keep), score, n_group=groups, topk_group=keep,
+                     group_top=2)
+
+
+@pytest.mark.parametrize("E,groups", [(64, 8), (256, 8), (384, 8), (1024, 8)])
+@pytest.mark.parametrize("at", [2.0 ** 17, -2.0 ** 19, 2.0 ** 21])
+def test_route_groups_of_large_logits(capi, E, groups, at):
+    # what a key drops of such a logit is not small beside 1
+    x = at + 4.0 * torch.randn(100, E, generator=torch.Generator().manual_seed(E))
+    for keep in (1, 3):
+        check_choice(capi, x, None, 8, "softmax", n_group=groups, topk_group=keep, group_top=2)
