@@ -508,10 +508,16 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&
     }
     sum = warp_sum(sum);
   }
-  // Fast scores err by less than 2^-21 of the largest possible one, `unit`: the
-  // exponential of -v by at most (2 + 1.2 v) 2^-23 e^-v < 2^-22, which a sum or
-  // 1 + e^-v only divides; the division adds 2^-23.
+  // What fast scores are off by, of the largest possible one, `unit`.  The
+  // exponential of -v is good to (2 + 1.7 v) 2^-23 of it, its argument's rounding
+  // counted in.  Sigmoid: s (1 - s) times that, below 2^-23, the division's two
+  // units of 2^-23 and the sum's rounding: below 2^-21.  Softmax, in units of 2^-23 of `unit`: 2 by the
+  // exponential itself; by the sum, which is common to all scores, 9.3 (the mean of
+  // its terms' errors by their weight: at most that for E = 1024, where all terms
+  // but one have v near 5) and half of V + 4 (its additions); division and product
+  // 2.5: below 16 + V / 2.  Without a bias the common part moves no comparison.
   const float unit = sigmoid ? 1.f : sum > 0.f ? __fdividef(1.f, sum) : 0.f;
+  const float error = (sigmoid || !biased ? 0x1p-21f : (16.f + 0.5f * V) * 0x1p-23f) * unit;
   auto fast_score = [&](float v) {
     return sigmoid ? __fdividef(1.f, 1.f + __expf(-v)) : (v == m ? 1.f : __expf(v - m)) * unit;
   };
@@ -543,12 +549,12 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&
       const float c = from_key(k & ~kPlace);
       const float dropped = kDropped * fabsf(c);
       if (!by_score) {
-        err += biased ? dropped + 0x1p-21f * unit : dropped;
+        err += biased ? dropped + error : dropped;
         return c;
       }
       // (of large logits the dropped bits are not small beside 1)
       const float v = fast_score(c);
-      err += 0x1p-21f * unit + (dropped < 0.5f ? 2.f * dropped * v : fast_score(c + dropped) - v);
+      err += error + (dropped < 0.5f ? 2.f * dropped * v : fast_score(c + dropped) - v);
       return v;
     };
     auto set_group = [&](uint32_t best, uint32_t next) {
@@ -656,7 +662,7 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&
     if (i2 >= 0) x2 = logit_at(a, t, i2);
   }
   bool close = false, alike = false;               // alike: near, but of the same inputs
-  auto tolerance = [&](float c) { return kDropped * fabsf(c) + 0x1p-21f * unit; };
+  auto tolerance = [&](float c) { return kDropped * fabsf(c) + error; };
   if (lane < a.k && idx >= 0 && i2 >= 0) {
     if (biased) {
       const float c1 = from_key(mine), c2 = from_key(key2);

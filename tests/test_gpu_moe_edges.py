@@ -112,3 +112,15 @@ def test_route_groups_of_large_logits(capi, E, groups, at):
     x = at + 4.0 * torch.randn(100, E, generator=torch.Generator().manual_seed(E))
     for keep in (1, 3):
         check_choice(capi, x, None, 8, "softmax", n_group=groups, topk_group=keep, group_top=2)
+
+
+@pytest.mark.parametrize("E", [256, 1024])
+def test_route_softmax_scores_whose_sum_is_off(capi, E):
+    # biases that cancel the scores to 2^-25 of them: what is left is as small as the
+    # error of the sum of E exponentials, which is common to all scores
+    for v in np.linspace(5.5, 9.0, 500).astype(np.float32):
+        x = np.full((1, E), -v, dtype=np.float32)
+        x[0, 5] = 0.0
+        s = np.exp(x[0].astype(np.float64))
+        b = (-s / s.sum()).astype(np.float32)
+        check_choice(capi, torch.from_numpy(x), torch.from_numpy(b), 1, "softmax")
