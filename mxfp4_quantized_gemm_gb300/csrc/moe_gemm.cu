@@ -269,6 +269,8 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+__device__ __forceinline__ void epi_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
 // Place of the part of cut tile `left` that CTA c leaves (each CTA's range cuts
 // at most two tiles).
 __device__ __forceinline__ int part_slot(const Walk& w, int KT, int left, int c) {
@@ -346,7 +348,7 @@ __device__ __forceinline__ uint32_t quantize32_f32(const float (&v)[32], uint4& 
 // u clamped: SiLU and the clamped form with a1 = -alpha log2 e, the tanh form
 // of GELU since (1 + tanh v) / 2 = 1 / (1 + exp(-2 v)).  (As three branches,
 // unrolled over a row, the code outgrew the instruction cache: 16000 cycles a
-// tile instead of 2500.)  The clamps keep a NaN.
+// tile instead of 2500.)  The clamps keep a NaN. 
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -687,9 +689,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
   uint64_t* acc_empty = acc_full + 1;
   uint64_t* seg_full = acc_empty + 1;
   uint64_t* seg_empty = seg_full + kSegs;
-  uint64_t* epi_bar = seg_empty + kSegs;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(seg_empty + kSegs);
   volatile int* last_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* no_more = last_flag + 1;   // set by warp 3 behind its last record
   uint8_t* staging = smem + C::kRing + 512;
   uint8_t* segs = staging + 8 * kStageWarp;
 
@@ -703,7 +705,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, kEpiThreads / 32);
-    mbar_init(epi_bar, kEpiThreads / 32);
+    *no_more = 0;
     for (int q = 0; q < kSegs; ++q) {
       mbar_init(&seg_full[q], 1);
       mbar_init(&seg_empty[q], kSegReaders);
@@ -724,8 +726,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
   Segment s;
   int sslot = 0;
   uint32_t sphase = 0;
-  auto next_segment = [&]() -> bool {
-    if (!mbar_wait(&seg_full[sslot], sphase, abort)) return false;
+  auto read_segment = [&]() -> bool {
     const int4* p = reinterpret_cast<const int4*>(segs + sslot * kSegBytes);
     const int4 lo = p[0], hi = p[1];
     s.rt = lo.x;
@@ -736,6 +737,21 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     s.left = hi.y;
     s.info = hi.z;
     return s.rt >= 0;
+  };
+  auto next_segment = [&]() -> bool { return mbar_wait(&seg_full[sslot], sphase, abort) && read_segment(); };
+  // For the epilogue, whose warps share hardware barriers, which have no limit: they
+  // all go through every record that was handed out, also where a wait for an
+  // accumulator ran out, and leave together.  This wait ends because warp 3's do.
+  auto next_of_all = [&]() -> bool {
+    const uint32_t bar = smem_u32(&seg_full[sslot]);
+    while (!mbar_try_wait(bar, sphase)) {
+      if (*no_more == 0) continue;
+      __threadfence_block();
+      if (mbar_test_wait(bar, sphase)) break;
+      abort = true;
+      return false;
+    }
+    return read_segment();
   };
   auto done_segment = [&]() {
     mbar_arrive(&seg_empty[sslot]);
@@ -942,6 +958,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
         sphase ^= 1;
       }
     }
+    __threadfence_block();
+    if (lane == 0) *no_more = 1;
    }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
@@ -954,22 +972,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_gemm_kernel(const __grid_c
     uint8_t* stage = staging + (warp - kFirstEpiWarp) * kStageWarp;
     const int ew = warp - kFirstEpiWarp;
     bool staged = false;                          // a warp's staging area may still be read by its warp
-    // Barrier of the epilogue warps.  A warp whose wait runs out goes no further
-    // through the segments, so the others' wait for it has a limit too (a hardware
-    // barrier's has none).
-    uint32_t epi_phase = 0;
-    auto epi_barrier = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(epi_bar);
-      mbar_wait(epi_bar, epi_phase, abort);
-      epi_phase ^= 1;
-    };
     // how the cut tiles are dealt out, for their sums
     Walk walk;
     walk.init(g, __ldcg(g.hdr));
     int pair_rt = -1, pair_of_row = -1;           // the row tile whose pairs this lane has: of row rl, or of row lane
     bool pair_few = false;                        // where the tile has few rows
-    for (int seg = 0; __all_sync(0xFFFFFFFFu, next_segment()); ++seg) {
+    for (int seg = 0; __all_sync(0xFFFFFFFFu, next_of_all()); ++seg) {
       const int rows = s.info >> 16, expert = s.info & 0xFFFF;
       const bool whole = s.len == g.KT, few = whole && rows <= kFewRows;
       const int first_c8 = s.half > 0 ? 16 : 0;

@@ -76,18 +76,24 @@ def test_activations():
     assert abs(moe_ref.act("gelu", np.array([1.0]), np.array([1.0]))[0] - phi) < 1e-3
 
 
-def test_roles_of_the_products_wait_with_a_limit():
-    # a warp that gives up a wait leaves its role, and no hardware barrier ends
-    # without it: inside the roles there are bounded waits only
+def test_epilogue_warps_leave_together():
+    # a hardware barrier does not end without a warp that has left its role: the
+    # warps that share it leave by what they all see, not by a wait that one of them
+    # gave up, and no other role has such a barrier
     import os
     import re
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     with open(os.path.join(root, "mxfp4_quantized_gemm_gb300", "csrc", "moe_gemm.cu")) as f:
         source = re.sub(r"//[^\n]*", "", f.read())
     start = source.index("if (warp < kFirstEpiWarp)")
-    roles = source[start:source.index("tmem_dealloc", start)]
-    assert not re.search(r"\bbar(rier)?\.(cta\.)?(sync|red)", source)
-    assert roles.count("__syncthreads") == 1           # behind all of them
+    epilogue = source.index("setmaxnreg.inc", start)
+    end = source.index("__syncthreads", epilogue)
+    assert "epi_barrier" not in source[start:epilogue] and "__syncthreads" not in source[start:end]
+    role = source[epilogue:end]
+    assert "epi_barrier();" in role and "next_of_all()" in role
+    assert "next_segment()" not in role and not re.search(r"\b(break|return)\b", role)
+    wait = source[source.index("auto next_of_all"):start]
+    assert "mbar_wait(" not in wait and "clock64" not in wait and "no_more" in wait
 
 
 # --------------------------------------------------------------- refusals
