@@ -348,7 +348,9 @@ __device__ __forceinline__ uint32_t quantize32_f32(const float (&v)[32], uint4& 
 // u clamped: SiLU and the clamped form with a1 = -alpha log2 e, the tanh form
 // of GELU since (1 + tanh v) / 2 = 1 / (1 + exp(-2 v)).  (As three branches,
 // unrolled over a row, the code outgrew the instruction cache: 16000 cycles a
-// tile instead of 2500.)  The clamps keep a NaN. 
+// tile instead of 2500.)  The clamps keep a NaN.  a3 meets the gate before the
+// gate's square, which is infinite for gates beyond 2^64: 0 times that would be a
+// NaN in the forms without a cubic term.
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -367,7 +369,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 __device__ __forceinline__ float gated(const MoeArgs& g, float gate, float up) {
   gate = min_nan(gate, g.limit);
   up = max_nan(min_nan(up, g.limit), -g.limit);
-  const float z = gate * fmaf(g.a3, gate * gate, g.a1);
+  const float z = gate * fmaf(g.a3 * gate, gate, g.a1);
   return __fdividef(gate, 1.f + exp2_approx(z)) * (up + g.shift);
 }
 

@@ -6,8 +6,11 @@ import numpy as np
 import pytest
 import torch
 
-from moe_helpers import run_route
+from helpers import dev_bf16, host_bits, pack_weights
+from moe_helpers import Experts, dev_f32, dev_i32, routing, run_ffn, run_route
+from mxfp4_quantized_gemm_gb300 import synth
 from oracle import moe_ref
+from oracle import mxfp4_ref as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +127,57 @@ def test_route_softmax_scores_whose_sum_is_off(capi, E):
         s = np.exp(x[0].astype(np.float64))
         b = (-s / s.sum()).astype(np.float32)
         check_choice(capi, torch.from_numpy(x), torch.from_numpy(b), 1, "softmax")
+
+
+# ------------------------------------------------------------- large gates
+def powers_network(capi, K=64, I=64, N=40):
+    """Gates x[0], ups 1.5 x[32], results 32 h_0 + ...: every code is one power of two or 1.5."""
+    up, down = Experts(capi, 1, 2 * I, K, 0, False), Experts(capi, 1, N, I, 0, False)
+    up.codes[:], down.codes[:] = 0, 0x22                # (two codes a byte; 1.0 is 2, 1.5 is 3)
+    up.codes[0, 0::2, 0] = 0x02
+    up.codes[0, 1::2, 16] = 0x03
+    for w in (up, down):
+        w.scales[:] = 127
+        w.packed = pack_weights(capi, w.codes, w.scales, w.K)
+    return up, down
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "swiglu"])
+@pytest.mark.parametrize("T", [14, 70, 300])
+def test_ffn_gates_whose_square_is_infinite(capi, act, T):
+    up, down = powers_network(capi)
+    e = np.resize([3, 60, 63, 64, 66, 90, 110], T)
+    sign = np.where(np.arange(T) % 14 < 7, 1.0, -1.0)
+    x = np.zeros((T, 64), dtype=np.float32)
+    x[:, 0], x[:, 32] = sign * 2.0 ** e, 1.0
+    bits = synth.f32_to_bf16_bits(x)
+    ids, w = np.zeros((T, 1), dtype=np.int32), np.ones((T, 1), dtype=np.float32)
+    got = ref.bf16_bits_to_f64(host_bits(run_ffn(capi, dev_bf16(bits), dev_i32(ids), dev_f32(w), up, down, act)))
+    torch.cuda.synchronize()
+    assert capi.mxfp4_get_device_error() == capi.OK
+    # h is one value in all columns, far from the borders of its rounding
+    h = moe_ref.act(act, x[:, :1].astype(np.float64), np.full((T, 1), 1.5))
+    q = moe_ref.quantized(np.repeat(h, 64, axis=1), 64)
+    want = np.repeat(q.sum(1, keepdims=True), 40, axis=1)
+    assert np.isfinite(got).all()
+    far = np.abs(x[:, 0]) > 8                          # (at -8 the oracle's 1 + tanh has no digits left)
+    assert np.array_equal(got[far], want[far])
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 1e-12)[~far & (x[:, 0] > 0)].all()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "swiglu"])
+@pytest.mark.parametrize("T", [20, 200])
+def test_ffn_rows_that_are_not_finite_stay_alone(capi, act, T):
+    up, down = Experts(capi, 3, 2 * 70, 192, 1, True), Experts(capi, 3, 100, 70, 2, True)
+    ids, w = routing(T, 3, 2, 5)
+    x = synth.activations(T, 192, 3)
+    want = host_bits(run_ffn(capi, dev_bf16(x), dev_i32(ids), dev_f32(w), up, down, act))
+    bad = x.copy()
+    rows = [0, 7, T - 1]
+    bad[0, 3], bad[7, 100], bad[T - 1, 191] = 0x7F80, 0x7FC1, 0xFF80
+    got = host_bits(run_ffn(capi, dev_bf16(bad), dev_i32(ids), dev_f32(w), up, down, act))
+    torch.cuda.synchronize()
+    assert capi.mxfp4_get_device_error() == capi.OK
+    assert np.isnan(ref.bf16_bits_to_f64(got[rows])).all()
+    keep = np.setdiff1d(np.arange(T), rows)
+    assert np.array_equal(got[keep], want[keep])
