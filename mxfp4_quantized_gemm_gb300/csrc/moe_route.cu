@@ -457,11 +457,12 @@ __device__ __forceinline__ void load_bias(const RouteArgs& a, int lane, float (&
 
 // key_of(v) with the place j of V in its lowest bits, the lower place higher;
 // 0 for what is switched off.
-constexpr uint32_t place_mask(int V) {
-  uint32_t m = 1;
-  while (m < static_cast<uint32_t>(V)) m *= 2;
-  return m - 1;
+constexpr int place_bits(int V) {
+  int n = 0;
+  while ((1 << n) < V) ++n;
+  return n;
 }
+constexpr uint32_t place_mask(int V) { return (1u << place_bits(V)) - 1u; }
 template <int V>
 __device__ __forceinline__ uint32_t placed_key(float v, int j) {
   constexpr uint32_t kPlace = place_mask(V);
@@ -508,16 +509,20 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&
     }
     sum = warp_sum(sum);
   }
-  // What fast scores are off by, of the largest possible one, `unit`.  The
-  // exponential of -v is good to (2 + 1.7 v) 2^-23 of it, its argument's rounding
-  // counted in.  Sigmoid: s (1 - s) times that, below 2^-23, the division's two
-  // units of 2^-23 and the sum's rounding: below 2^-21.  Softmax, in units of 2^-23 of `unit`: 2 by the
-  // exponential itself; by the sum, which is common to all scores, 9.3 (the mean of
-  // its terms' errors by their weight: at most that for E = 1024, where all terms
-  // but one have v near 5) and half of V + 4 (its additions); division and product
-  // 2.5: below 16 + V / 2.  Without a bias the common part moves no comparison.
+  // What fast scores are off by, in units of 2^-23.  The exponential of -v is good to
+  // 2 + 1.7 v of it, its argument's rounding counted in.  Sigmoid: s (1 - s) times
+  // that, below 1, the division's 2 and the sum's rounding: below 4.  Softmax, each
+  // score: 2 of the largest possible one, `unit`, by the exponential and half of one by the
+  // product: below 3.  What all scores have in common, of each: by their sum the mean
+  // of its terms' errors by their weight (with n terms beside the largest at most that
+  // of n equal ones: 4.5 for n = 31, 1 more for twice as many) and half of V + 4 (its
+  // additions), by the division 2.  That moves the comparison of two near c by their
+  // scores' difference only, which is that of their biases.  (16384 tokens with a
+  // bias, of 256 / 64 experts: 21.5 / 11.8 us; 23.7 / 13.0 with the whole of `unit`
+  // in its place, 20.9 / 11.2 without, which is wrong.)
   const float unit = sigmoid ? 1.f : sum > 0.f ? __fdividef(1.f, sum) : 0.f;
-  const float error = (sigmoid || !biased ? 0x1p-21f : (16.f + 0.5f * V) * 0x1p-23f) * unit;
+  const float common = sigmoid || !biased ? 0.f : (8.5f + place_bits(V) + 0.5f * V) * 0x1p-23f;
+  const float error = (sigmoid ? 4.f : 3.f) * 0x1p-23f * unit;
   auto fast_score = [&](float v) {
     return sigmoid ? __fdividef(1.f, 1.f + __expf(-v)) : (v == m ? 1.f : __expf(v - m)) * unit;
   };
@@ -549,7 +554,7 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&
       const float c = from_key(k & ~kPlace);
       const float dropped = kDropped * fabsf(c);
       if (!by_score) {
-        err += biased ? dropped + error : dropped;
+        err += biased ? dropped + error + common * unit : dropped;
         return c;
       }
       // (of large logits the dropped bits are not small beside 1)
@@ -666,9 +671,9 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&
   if (lane < a.k && idx >= 0 && i2 >= 0) {
     if (biased) {
       const float c1 = from_key(mine), c2 = from_key(key2);
-      const bool same = xsel == x2 && __ldg(a.bias + idx) == __ldg(a.bias + i2);
-      close = c1 - c2 <= tolerance(c1) + tolerance(c2);
-      alike = close && same;
+      const float b1 = __ldg(a.bias + idx), b2 = __ldg(a.bias + i2);
+      close = c1 - c2 <= tolerance(c1) + tolerance(c2) + common * fabsf(b1 - b2);
+      alike = close && xsel == x2 && b1 == b2;
     } else {
       close = mine == key2;
       alike = close && xsel == x2;
@@ -687,9 +692,9 @@ __device__ __forceinline__ bool decide(const RouteArgs& a, int t, const float (&
     for (int left = V; left > 0 && key[0] != 0; --left) {
       const uint32_t k2 = key[0] & ~kPlace;
       const int i = lane * V + static_cast<int>(kPlace - (key[0] & kPlace));
-      const float c2 = from_key(k2);
-      if (biased ? c1 - c2 <= tolerance(c1) + tolerance(c2) : k2 == klast)
-        near = near || logit_at(a, t, i) != xlast || (biased && __ldg(a.bias + i) != blast);
+      const float c2 = from_key(k2), b2 = biased ? __ldg(a.bias + i) : 0.f;
+      if (biased ? c1 - c2 <= tolerance(c1) + tolerance(c2) + common * fabsf(blast - b2) : k2 == klast)
+        near = near || logit_at(a, t, i) != xlast || b2 != blast;
 #pragma unroll
       for (int j = 0; j + 1 < V; ++j) key[j] = key[j + 1];
       key[V - 1] = 0;
@@ -752,8 +757,10 @@ __device__ __forceinline__ void load_row(const RouteArgs& a, int t, int lane, fl
   for (int j = 0; j < V; ++j) x[j] = x[j] == x[j] ? x[j] : -INFINITY;
 }
 
+// (Blocks an SM for few logits a lane: what the usual path needs, so that the rows
+// that are decided again do not take them registers: 16384 x 64 12.2 us at 8.)
 template <int V>
-__global__ void __launch_bounds__(128, V <= 8 ? 8 : V <= 16 ? 5 : 2)
+__global__ void __launch_bounds__(128, V == 1 ? 12 : V == 2 ? 10 : V == 3 ? 9 : V <= 8 ? 8 : V <= 16 ? 5 : 2)
     moe_route_kernel(const __grid_constant__ RouteArgs a) {
   const int lane = threadIdx.x & 31;
   const int t = static_cast<int>(blockIdx.x) * 4 + (threadIdx.x >> 5);
