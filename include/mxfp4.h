@@ -589,7 +589,8 @@ MXFP4_API mxfp4_status mxfp4_moe_linear(const void* x_dev, int64_t ldx, const in
  *   residual_dev     bf16 [T][ldr >= N], or NULL; may be out_dev itself with
  *                    the same stride
  *   out_dev          bf16 [T][ldo >= N]; must not overlap x
- *   alpha, limit     of MXFP4_MOE_SWIGLU_CLAMP, else ignored
+ *   alpha, limit     of MXFP4_MOE_SWIGLU_CLAMP, else ignored: alpha finite, limit
+ *                    0 or more (infinite for none)
  * I is even.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE,
  * CUDA.
  */

@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
@@ -620,6 +621,8 @@ mxfp4_status mxfp4_moe_ffn(const void* x, int64_t ldx, const int32_t* ids, const
     return MXFP4_ERR_INVALID_ARG;
   if (I <= 0) return MXFP4_ERR_INVALID_ARG;
   if (act != MXFP4_MOE_SILU && act != MXFP4_MOE_GELU_TANH && act != MXFP4_MOE_SWIGLU_CLAMP) return MXFP4_ERR_INVALID_ARG;
+  // (a negative limit leaves no value; the columns that pad a tile are zeros because act of zeros is 0)
+  if (act == MXFP4_MOE_SWIGLU_CLAMP && (!(limit >= 0.f) || !std::isfinite(alpha))) return MXFP4_ERR_INVALID_ARG;
   mxfp4_status st = check_moe(T, top_k, E, K, N);
   if (st == MXFP4_OK) st = check_moe(T, top_k, E, K, 2 * static_cast<int64_t>(I));
   if (st != MXFP4_OK) return st;

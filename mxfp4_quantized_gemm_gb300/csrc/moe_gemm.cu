@@ -30,6 +30,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cstdint>
 
 #include "gemm_common.cuh"
@@ -1122,7 +1123,8 @@ cudaError_t launch_moe_gemm(const MoeGemmProblem& p, const MoePlan& plan, const 
   constexpr float kLog2e = 1.4426950408889634f;
   a.limit = p.act == MoeAct::kSwigluClamp ? p.limit : __builtin_huge_valf();
   a.shift = p.act == MoeAct::kSwigluClamp ? 1.f : 0.f;
-  a.a1 = -kLog2e * (p.act == MoeAct::kSwigluClamp ? p.alpha : p.act == MoeAct::kGeluTanh ? 1.5957691216057308f : 1.f);
+  const float by = p.act == MoeAct::kSwigluClamp ? p.alpha : p.act == MoeAct::kGeluTanh ? 1.5957691216057308f : 1.f;
+  a.a1 = fmaxf(-FLT_MAX, fminf(-kLog2e * by, FLT_MAX));   // (times a gate of 0 it is 0)
   a.a3 = p.act == MoeAct::kGeluTanh ? 0.044715f * a.a1 : 0.f;
   a.hdr = plan.hdr;
   a.tile = plan.tile;

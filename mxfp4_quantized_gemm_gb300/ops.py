@@ -37,6 +37,7 @@ and mixture-of-experts layers in MXFP4 (ids int32, negative for an empty slot):
 
 from __future__ import annotations
 
+import math
 from typing import Optional
 
 import torch
@@ -668,7 +669,8 @@ def _(x, ids, w_packed, bias, E, N):
     return x.new_empty(*x.shape[:-1], k, N)
 
 
-def _check_moe_ffn(x, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, residual, E, I, N, act) -> tuple[int, int]:
+def _check_moe_ffn(x, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, residual, E, I, N, act, alpha,
+                   limit) -> tuple[int, int]:
     where = "mxfp4::moe_ffn"
     bf = torch.bfloat16
     _check_args(where, x, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, residual,
@@ -676,6 +678,8 @@ def _check_moe_ffn(x, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, 
     K, k = _check_moe(where, x, ids, E)
     torch._check(weights.shape == ids.shape, lambda: f"{where}: weights {tuple(weights.shape)}, ids {tuple(ids.shape)}")
     torch._check(act in _MOE_ACTS, lambda: f"{where}: act {act!r} is none of {_MOE_ACTS}")
+    torch._check(act != "swiglu_clamp" or (math.isfinite(alpha) and limit >= 0),
+                 lambda: f"{where}: alpha = {alpha} must be finite, limit = {limit} not negative")
     torch._check(I > 0 and I % 2 == 0, lambda: f"{where}: I = {I} must be positive and even")
     _check_weights(where, w_gate_up, E, 2 * I, K)
     _check_weights(where, w_down, E, N, I)
@@ -694,8 +698,10 @@ def moe_ffn(x: Tensor, ids: Tensor, weights: Tensor, w_gate_up: Tensor, bias_gat
     """The experts' gated network of each token, weighted, summed and added to
     the residual: x [.., K], ids and weights [.., top_k], E packed matrices
     [2 I, K] (rows alternating gate and up: pack_gate_up) and [N, I] ->
-    [.., N] bf16.  act: silu, gelu_tanh or swiglu_clamp (of alpha and limit)."""
-    K, k = _check_moe_ffn(x, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, residual, E, I, N, act)
+    [.., N] bf16.  act: silu, gelu_tanh or swiglu_clamp (of alpha, finite, and
+    limit, not negative; the others ignore both)."""
+    K, k = _check_moe_ffn(x, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, residual, E, I, N, act, alpha,
+                          limit)
     c = _capi()
     out = torch.empty(*x.shape[:-1], N, dtype=torch.bfloat16, device=x.device)
     x2 = _rows(x, K)
@@ -715,5 +721,5 @@ def moe_ffn(x: Tensor, ids: Tensor, weights: Tensor, w_gate_up: Tensor, bias_gat
 
 @moe_ffn.register_fake
 def _(x, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, residual, E, I, N, act, alpha, limit):
-    _check_moe_ffn(x, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, residual, E, I, N, act)
+    _check_moe_ffn(x, ids, weights, w_gate_up, bias_gate_up, w_down, bias_down, residual, E, I, N, act, alpha, limit)
     return x.new_empty(*x.shape[:-1], N)

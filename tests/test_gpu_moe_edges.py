@@ -1,6 +1,7 @@
 """Mixture of experts on the GPU at inputs that lie on a border: experts that
 fp32 cannot tell apart beside equal ones, scores that vanish, groups whose
-values cancel."""
+values cancel, gates whose square is infinite, rows that are not finite, clamps
+at their limits."""
 
 import numpy as np
 import pytest
@@ -181,3 +182,24 @@ def test_ffn_rows_that_are_not_finite_stay_alone(capi, act, T):
     assert np.isnan(ref.bf16_bits_to_f64(got[rows])).all()
     keep = np.setdiff1d(np.arange(T), rows)
     assert np.array_equal(got[keep], want[keep])
+
+
+@pytest.mark.parametrize("alpha,limit", [(1.702, 0.0), (1.702, 0.5), (1.0, float("inf")), (0.0, 7.0), (3e38, 7.0)])
+def test_ffn_clamps_give_the_same_bits_for_few_and_many_rows(capi, alpha, limit):
+    # I = 70 ends inside a block of 32: what pads it has to be nothing
+    up, down = Experts(capi, 1, 2 * 70, 192, 1, True), Experts(capi, 1, 100, 70, 2, True)
+    x = dev_bf16(synth.activations(200, 192, 3))
+
+    def run(T):
+        ids, w = torch.zeros(T, 1, dtype=torch.int32, device="cuda"), torch.ones(T, 1, device="cuda")
+        out = torch.empty(T, 100, dtype=torch.bfloat16, device="cuda")
+        n = capi.mxfp4_moe_ffn_workspace_bytes(T, 1, 1, 192, 70, 100)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        capi.mxfp4_moe_ffn(x, 192, ids, w, up.packed, up.bias_dev, down.packed, down.bias_dev, None, 0, out, 100, T, 1, 1,
+                           192, 70, 100, capi.MOE_SWIGLU_CLAMP, alpha, limit, ws, n)
+        torch.cuda.synchronize()
+        return out
+
+    many, few = run(200), run(20)
+    assert many.isfinite().all() and torch.equal(many[:20], few)
+    assert capi.mxfp4_get_device_error() == capi.OK

@@ -164,6 +164,26 @@ def test_refusals_of_each(capi):
     assert status(capi, "mxfp4_moe_ffn", FFN, I=127) == shape
 
 
+def test_ffn_refuses_clamps_without_a_meaning(capi):
+    nan, inf = float("nan"), float("inf")
+    clamp = dict(FFN, act=2, workspace_bytes=0)         # (what is accepted goes as far as the workspace)
+    for change in (dict(limit=-1.0), dict(limit=nan), dict(limit=-inf), dict(alpha=nan), dict(alpha=inf)):
+        assert status(capi, "mxfp4_moe_ffn", clamp, **change) == capi.ERR_INVALID_ARG, change
+        for act in (0, 1):                              # they ignore both
+            assert status(capi, "mxfp4_moe_ffn", dict(clamp, act=act), **change) == capi.ERR_WORKSPACE, change
+    for change in (dict(), dict(limit=0.0), dict(limit=inf), dict(alpha=0.0), dict(alpha=-3e38)):
+        assert status(capi, "mxfp4_moe_ffn", clamp, **change) == capi.ERR_WORKSPACE, change
+    from mxfp4_quantized_gemm_gb300 import ops
+    ffn = dict(x=meta(7, 256), ids=meta(7, 2, dtype=torch.int32), weights=meta(7, 2, dtype=torch.float32),
+               w_gate_up=meta(ops._packed_weight_bytes(8, 192, 256), dtype=torch.uint8), bias_gate_up=None,
+               w_down=meta(ops._packed_weight_bytes(8, 300, 96), dtype=torch.uint8), bias_down=None, residual=None, E=8,
+               I=96, N=300, act="swiglu_clamp", alpha=1.702, limit=inf)
+    assert torch.ops.mxfp4.moe_ffn(**ffn).shape == (7, 300)
+    for change in (dict(limit=-1.0), dict(limit=nan), dict(alpha=inf)):
+        with pytest.raises(RuntimeError, match="mxfp4::moe_ffn"):
+            torch.ops.mxfp4.moe_ffn(**dict(ffn, **change))
+
+
 def test_workspace_queries(capi):
     lin, ffn = capi.mxfp4_moe_linear_workspace_bytes, capi.mxfp4_moe_ffn_workspace_bytes
     assert lin(0, 8, 64, 512, 256) == 0 and lin(4, 8, 64, 512, 255) == 0 and lin(4, 33, 64, 512, 256) == 0
