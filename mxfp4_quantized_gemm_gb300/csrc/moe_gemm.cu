@@ -50,8 +50,8 @@ constexpr int kUnit = 4;                           // tiles of one row tile that
 constexpr int kPartFloats = 128 * kTileN;          // one part of a cut tile
 constexpr int kMinSteps = 2;                       // k-steps a CTA takes at least where tiles are cut
 constexpr int kCutSteps = 12, kCutRows = 10;       // what cutting costs, in k-steps: 12 and one for 10 rows (see Walk)
-// Rows up to which a tile is finished row by row (16 alike; 48: 300 x 3 of 20 24.5
-// us in place of 23.0, 1024 x 8 of 64 163 in place of 152).
+// Rows up to which a tile is finished row by row (16 alike; 48: 300 x 3 of 20 24.1
+// us in place of 23.7, 1024 x 8 of 64 149.5 in place of 148.1).
 constexpr int kFewRows = 32;
 // Warp 0 brings the weights, warp 2 the activations, warp 1 issues the MMAs,
 // warp 3 finds the segments for all of them; warps 4..11 are the epilogue.  The
@@ -444,8 +444,9 @@ __device__ __forceinline__ void finish(const MoeArgs& g, const Segment& s, uint2
     // Rows that allow no wide access or end inside the tile: 8 rows at a time
     // through the warp's staging area, then a row at a time in aligned words of
     // two columns, which straddle the staged ones where the row starts at an odd
-    // column: 24.5 us for 1500 x 2 tokens of 1001 columns, of 1024 six less (whole
-    // lines).  Column by column it took 30, by 16 bytes a lane, put together from two pieces at a place that depends on the row, 25.5.
+    // column: 24.4 us for 1500 x 2 tokens of 1001 columns, of 1024 six less (whole
+    // lines).  Column by column it took 30, by 16 bytes a lane, put together from
+    // two pieces at a place that depends on the row, 25.5.
     const int count = g.N - n0 < 128 ? g.N - n0 : 128;
     for (int b = 0; b < 4; ++b) {
       if ((lane >> 3) == b) {
@@ -637,7 +638,8 @@ __device__ __forceinline__ void finish_cut(const MoeArgs& g, const Walk& walk, c
 // descriptors are formed once and the others are sums with constants: no
 // address in shared memory carries into the fields above it.  (8192 tokens' first
 // product: 278 us with every descriptor and barrier address formed on its own and
-// two k-steps' scales copied together against it, 236 so, a k-step at a time.)
+// two k-steps' scales copied together against it, 236 so, a k-step at a time, and
+// 228 without tests between the instructions.)
 struct StageDescs {
   uint32_t tile, scales;   // low words at the stage's start; the high words are constants
   __device__ __forceinline__ explicit StageDescs(uint32_t stage)

@@ -11,15 +11,16 @@
 // the place (so a compare-exchange is one maximum and one minimum); a choice
 // then is a maximum over the lanes' first keys (redux), and the lowest lane
 // that has it gives up its first key.  Instructions bound the kernel, not the
-// bytes (T * E logits): 1144 a token and 28.5 us for 16384 tokens of 256 experts
-// in 8 groups, 6.6 us for 8192 of 128 without groups, 4.7 us for 16 (2000 a
+// bytes (T * E logits): 1122 a token and 28.3 us for 16384 tokens of 256 experts
+// in 8 groups, 6.2 us for 8192 of 128 without groups, 4.8 us for 16 (2000 a
 // token and 62 us when the lanes searched their values in every round).
 //
 // The choice is exact: where two neighbours of the order up to place k + 1 (or
-// the last group taken and the first left out) lie nearer than the dropped
-// bits and the fp32 evaluation's error bound, the warp decides the row again
-// in pairs of fp32, and where that does not settle it either, in fp64.
-// Equal inputs are no such case: their order is by the index.
+// a group taken and one left out) lie nearer than the dropped bits and the fp32
+// evaluation's error bound, the warp decides the row again in pairs of fp32, and
+// where that does not settle it either, in fp64.  Equal inputs are no such case:
+// their order is by the index; but where the first one left out has the inputs of
+// the last choice, all that are left out are held against it.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
